@@ -541,6 +541,98 @@ int tpk_gdn_delta_rule_bwd(const tpk_plan* plan, const void* dev_image, const vo
                            float* dg, float* dbeta, int32_t H, int32_t dk, int32_t dv, float scale,
                            const void* state, size_t state_bytes, void* workspace, size_t ws_bytes, void* stream);
 
+/* ---- the operators around the token mixers --------------------------------
+ * No counterpart on the pages, which describe the packed row and its token
+ * mixers: these take a packed batch from token ids to hidden rows, around
+ * every mixer, and to its loss, and bring the gradients back.  They work row
+ * by row (F forwarded positions, or any other N rows).  Results do not depend
+ * on timing: sums run in a fixed order, without floating-point atomics. */
+#define TPK_BF16 0
+#define TPK_F32  1
+
+/* Embedding lookup with scaling:
+ *   out[f] = bf16(scale * table[tokens[f]])
+ * A position whose id is outside [0, V) (padding) gets a zero row.
+ *   table   [V, C] bf16 (table_type TPK_BF16) or fp32 (TPK_F32)
+ *   tokens  [N] int32;  out [N, C] bf16;  C % 8 == 0
+ * table and out are 16-byte aligned and do not overlap.  N = 0 does nothing.
+ * Errors: TPK_E_ARG on a NULL pointer, a bad size or type or misalignment. */
+int tpk_embed(const void* table, int32_t table_type, const int32_t* tokens, void* out, int64_t N, int64_t V,
+              int32_t C, float scale, void* stream);
+
+/* The table's gradient: dtable[v] = scale * sum of dout[f] over the positions
+ * with tokens[f] = v, summed in fp32 in a fixed order (the positions are
+ * sorted by id; the result is deterministic).  Every row of dtable is
+ * written, rows of ids that do not occur as zeros; ids outside [0, V) add to
+ * nothing.
+ *   dout [N, C] bf16;  dtable [V, C] bf16 or fp32 (table_type), overwritten
+ *   workspace: >= tpk_embed_bwd_workspace_bytes bytes, 256-byte aligned, need
+ *   not be cleared (the sorted positions, and one fp32 row per side of every
+ *   64 of them). */
+size_t tpk_embed_bwd_workspace_bytes(int64_t N, int64_t V, int32_t C);
+int tpk_embed_bwd(const int32_t* tokens, const void* dout, void* dtable, int32_t table_type, int64_t N, int64_t V,
+                  int32_t C, float scale, void* workspace, size_t ws_bytes, void* stream);
+
+/* The norms around a block, with its gate and the residual add.  Per row
+ * (RMS norms over C channels, rstd(a) = 1 / sqrt(mean a^2 + eps)):
+ *   u = y * rstd(y) * w_post                  norm after the block (w_post NULL: u = y)
+ *   r = res + scale * sigmoid(gate) * u       gate NULL: no gate
+ *   x = r * rstd(r) * w_pre                   norm before the next block
+ * Statistics are fp32 and x is formed from r before its rounding.
+ *   res, res_out, x [N, C] bf16;  y, gate [N, C] bf16 with row strides ld_y,
+ *   ld_gate (elements; may be column slices of a wider tensor);  w_post,
+ *   w_pre [C] fp32.  res_out receives r, and may be res itself.
+ *   y NULL: r = res (a norm before the first block); gate and w_post must be
+ *   NULL too and res_out is not written.
+ * Rows are 16-byte aligned, C % 8 == 0, C <= 16384 (TPK_E_UNSUPPORTED above). */
+int tpk_block_norm(const void* res, const void* y, int64_t ld_y, const void* gate, int64_t ld_gate,
+                   const float* w_post, const float* w_pre, void* res_out, void* x, int64_t N, int32_t C, float scale,
+                   float eps, void* stream);
+
+/* Gradients of tpk_block_norm for the gradients dres_out of r (NULL: none)
+ * and dx of x.  res, y, gate, w_post, w_pre, scale, eps as given to the
+ * forward (r is recomputed, so res must still hold the forward's input).
+ *   dres [N, C] bf16;  dy, dgate [N, C] bf16 with row strides ld_dy, ld_dgate
+ *   (given exactly where y and gate are);  dw_post, dw_pre [C] fp32,
+ *   overwritten (dw_post given exactly where w_post is).
+ *   workspace: >= tpk_block_norm_bwd_workspace_bytes bytes, 256-byte aligned,
+ *   need not be cleared (partial sums of dw_post and dw_pre). */
+size_t tpk_block_norm_bwd_workspace_bytes(int64_t N, int32_t C);
+int tpk_block_norm_bwd(const void* res, const void* y, int64_t ld_y, const void* gate, int64_t ld_gate,
+                       const float* w_post, const float* w_pre, const void* dres_out, const void* dx, void* dres,
+                       void* dy, int64_t ld_dy, void* dgate, int64_t ld_dgate, float* dw_post, float* dw_pre,
+                       int64_t N, int32_t C, float scale, float eps, void* workspace, size_t ws_bytes, void* stream);
+
+/* Softmax cross entropy over the vocabulary, fused with the output
+ * projection; the logits are never stored:
+ *   z[f, v] = scale * h[f] . w[v]             (scale: 1 / temperature)
+ *   lse[f]  = ln sum_v exp z[f, v]
+ *   loss[f] = lse[f] - z[f, target[f]]        (minus the target's log-probability)
+ * A position whose target is outside [0, V) carries no loss: loss and lse are
+ * zero and its row of h is not read into any product.
+ *   h [N, C] bf16, w [V, C] bf16, target [N] int32, loss, lse [N] fp32
+ *   C % 8 == 0; h, w 16-byte aligned; scale > 0 and finite
+ *   workspace: >= tpk_lm_loss_workspace_bytes(N, V, C, 0), 256-byte aligned,
+ *   need not be cleared.
+ *   dev_err: device int32 set to TPK_E_TIMEOUT if a wait gave up (may be NULL) */
+size_t tpk_lm_loss_workspace_bytes(int64_t N, int64_t V, int32_t C, int32_t backward);
+int tpk_lm_loss(const void* h, const void* w, const int32_t* target, float* loss, float* lse, int64_t N, int64_t V,
+                int32_t C, float scale, void* workspace, size_t ws_bytes, int32_t* dev_err, void* stream);
+
+/* Gradients of sum_f dloss[f] * loss[f]:
+ *   dz[f, v] = dloss[f] * scale * (exp(z[f, v] - lse[f]) - [v = target[f]])
+ *   dh[f] = sum_v dz[f, v] w[v],   dw[v] = sum_f dz[f, v] h[f]
+ * lse is the forward's.  The scores are computed again, one piece of the
+ * vocabulary at a time; dz enters its two products as bf16, sums are fp32 and
+ * deterministic.  dloss of a position without a target is not read.
+ *   dh [N, C] bf16, dw [V, C] bf16 (16-byte aligned), every row written
+ *   workspace: >= tpk_lm_loss_workspace_bytes(N, V, C, 1), 256-byte aligned,
+ *   need not be cleared (up to 4 GiB for dz, the gathered rows and dh's fp32
+ *   sums). */
+int tpk_lm_loss_bwd(const void* h, const void* w, const int32_t* target, const float* lse, const float* dloss,
+                    void* dh, void* dw, int64_t N, int64_t V, int32_t C, float scale, void* workspace,
+                    size_t ws_bytes, int32_t* dev_err, void* stream);
+
 /* Self-test of the device-side failure path (no counterpart on the pages):
  * launches one small kernel that waits, with the same bounded mbarrier wait
  * the attention kernels use, on a barrier nothing ever arrives at.  After

@@ -20,6 +20,7 @@ PREC_FAST, PREC_PRECISE = 0, 1
 PLACE_BFD = 0
 PLACE_NEXT_FIT = 1
 PLACE_GROUPS = 2
+BF16, F32 = 0, 1
 FIELD_DEPTH, FIELD_TOKEN_INDEX, FIELD_SUBTREE_END, FIELD_PARENT = 0, 1, 2, 3
 FIELD_FWD_RAW_BEGIN, FIELD_FWD_RAW = 4, 5
 FIELD_SEG_START, FIELD_SEG_LEN, FIELD_SEG_PARENT, FIELD_SEG_OFF = 6, 7, 8, 9
@@ -33,7 +34,11 @@ EXPORTS = [
     "tpk_tree_attn_bwd", "tpk_tree_attn_bwd_ex", "tpk_tree_attn_bwd_phase", "tpk_tree_attn_bwd_noalloc", "tpk_selftest_wait_timeout",
     "tpk_scatter_token_index", "tpk_gather_to_forwarded", "tpk_sum_to_forwarded", "tpk_gdn_conv",
     "tpk_gdn_workspace_bytes", "tpk_gdn_delta_rule", "tpk_gdn_conv_bwd_workspace_bytes", "tpk_gdn_conv_bwd",
-    "tpk_gdn_bwd_workspace_bytes", "tpk_gdn_delta_rule_bwd", "tpk_status_string",
+    "tpk_gdn_bwd_workspace_bytes", "tpk_gdn_delta_rule_bwd",
+    "tpk_embed", "tpk_embed_bwd_workspace_bytes", "tpk_embed_bwd",
+    "tpk_block_norm", "tpk_block_norm_bwd_workspace_bytes", "tpk_block_norm_bwd",
+    "tpk_lm_loss_workspace_bytes", "tpk_lm_loss", "tpk_lm_loss_bwd",
+    "tpk_status_string",
     "tpk_version",
 ]
 
@@ -112,6 +117,19 @@ def _sig(lib):
     lib.tpk_gdn_bwd_workspace_bytes.restype = SZ
     lib.tpk_gdn_delta_rule_bwd.argtypes = [P, P, P, P, P, I64, I64, P, P, P, P, P, P, I64, I64, P, P, I32, I32, I32,
                                            ctypes.c_float, P, SZ, P, SZ, P]
+    F = ctypes.c_float
+    lib.tpk_embed.argtypes = [P, I32, P, P, I64, I64, I32, F, P]
+    lib.tpk_embed_bwd_workspace_bytes.argtypes = [I64, I64, I32]
+    lib.tpk_embed_bwd_workspace_bytes.restype = SZ
+    lib.tpk_embed_bwd.argtypes = [P, P, P, I32, I64, I64, I32, F, P, SZ, P]
+    lib.tpk_block_norm.argtypes = [P, P, I64, P, I64, P, P, P, P, I64, I32, F, F, P]
+    lib.tpk_block_norm_bwd_workspace_bytes.argtypes = [I64, I32]
+    lib.tpk_block_norm_bwd_workspace_bytes.restype = SZ
+    lib.tpk_block_norm_bwd.argtypes = [P, P, I64, P, I64, P, P, P, P, P, P, I64, P, I64, P, P, I64, I32, F, F, P, SZ, P]
+    lib.tpk_lm_loss_workspace_bytes.argtypes = [I64, I64, I32, I32]
+    lib.tpk_lm_loss_workspace_bytes.restype = SZ
+    lib.tpk_lm_loss.argtypes = [P, P, P, P, P, I64, I64, I32, F, P, SZ, P, P]
+    lib.tpk_lm_loss_bwd.argtypes = [P, P, P, P, P, P, P, I64, I64, I32, F, P, SZ, P, P]
     lib.tpk_status_string.argtypes = [ctypes.c_int]
     lib.tpk_status_string.restype = ctypes.c_char_p
     lib.tpk_version.argtypes = []

@@ -1,0 +1,827 @@
+// Softmax cross entropy over a large vocabulary, fused with the output
+// projection and never keeping the logits, and its gradients.
+//
+//   z[f, v] = scale * h[f] . w[v],   lse[f] = ln sum_v exp z[f, v]
+//   loss[f] = lse[f] - z[f, target[f]]
+//   dz[f, v] = dloss[f] * scale * (exp(z[f, v] - lse[f]) - (v == target[f]))
+//   dh[f] = sum_v dz[f, v] w[v],     dw[v] = sum_f dz[f, v] h[f]
+// A position whose target lies outside [0, V) has no loss: its loss, lse and
+// dh are zero, its row of h reaches nothing (not even as 0 * NaN) and costs
+// no products, because the positions that have a target are first gathered
+// into consecutive rows.
+//
+// Everything is one matrix product with four epilogues (kFwd, kDz, kDh, kDw):
+//   kFwd  h w^T: each row's running (maximum, sum of exponentials) over a run
+//         of vocabulary tiles and the target's score; joined by a small kernel
+//   kDz   h w^T again for one piece of the vocabulary: dz in bf16
+//   kDh   dz w over the piece, accumulated over the pieces in fp32
+//   kDw   dz^T h: the piece's rows of dw
+// The vocabulary is cut into pieces so that dz of one piece fits the
+// workspace (kDzBytes).  dz enters its products as bf16 (as the score
+// gradients do in the attention backward): relative rounding 2^-9, the size
+// of the outputs' own.
+//
+// The product: 256 x 256 tiles on a pair of CTAs (tcgen05 cta_group::2, each
+// CTA holds 128 rows of A, 128 rows of B and its 128 rows of the result), 64
+// elements of K per stage, six stages filled by TMA, two accumulators of 256
+// TMEM columns so that a tile's epilogue runs under the next tile's products.
+// One CTA with a 128 x 256 tile would load 96 bytes of operands per cycle and
+// SM at full tensor rate; the pair loads 64.
+// Warps of a CTA: 0 TMA producer, 1 MMA issuer (of the pair's first CTA), 2
+// TMEM owner, 4-11 epilogue (two warpgroups, 128 columns each).  CTAs are
+// persistent and walk the tiles in panels of 8 columns of tiles, so the pairs
+// running together share rows of A and of B in L2.
+#include <cuda_bf16.h>
+
+#include "common.cuh"
+#include "pair.cuh"
+
+namespace tpk {
+namespace {
+
+constexpr int kStages = 6;
+constexpr int kTile = 256;            // rows and columns of a pair's tile
+constexpr int kHalf = 128;            // rows of A / of B a CTA holds
+constexpr int kBoxBytes = kHalf * 128;// one stage's operand: 128 x 64 bf16
+constexpr int kThreads = 384;
+constexpr int kEpiThreads = 256;
+constexpr int kPanel = 8;
+constexpr int kSplitPairs = 76;       // pairs a split over K aims to fill (two SMs each)
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kLn2 = 0.6931471805599453f;
+
+enum { kFwd = 0, kDz = 1, kDh = 2, kDw = 3 };
+
+struct LmParams {
+  const int32_t* count;     // device: gathered rows; nullptr: n_rows
+  int32_t n_rows;
+  int32_t V, C;
+  int64_t np;               // rows of the padded buffers
+  const int32_t* rows;      // gathered row -> position; nullptr: the same
+  const int32_t* target;
+  const float* lse;
+  const float* dloss;
+  float scale, scale_log2;
+  float2* part;             // kFwd: [2 * chunks][np]
+  float* zt;                // kFwd: [np] the target's score, log2 units
+  int32_t run;              // kFwd: vocabulary tiles per unit
+  int32_t v0, vcols, ld_dz; // the piece: first id, ids, row stride of dz
+  __nv_bfloat16* dz;
+  float* acc;               // kDh: fp32 tiles; kDw: fp32 tiles of a split over K
+  int32_t split_most;       // kDh
+  int32_t first, last;      // kDh: first / last piece
+  __nv_bfloat16* dh;
+  __nv_bfloat16* dw;
+  int32_t* err;
+};
+
+// Splits over K where the tiles alone do not fill the GPU.
+__device__ __forceinline__ int splits_for(int tiles, int most) {
+  const int s = tiles > 0 ? kSplitPairs / tiles : 1;
+  return s < 1 ? 1 : (s > most ? (most < 1 ? 1 : most) : s);
+}
+__device__ __forceinline__ int dw_splits(int tiles, int k_iters) { return splits_for(tiles, k_iters / 8); }
+
+struct LmSmem {
+  uint8_t a[kStages][kBoxBytes];
+  uint8_t b[kStages][kBoxBytes];
+  uint64_t full[kStages], empty[kStages];
+  uint64_t tm_full[2], tm_empty[2];
+  uint64_t drain;
+  uint32_t tmem_base;
+  int abort_flag;
+  uint32_t issued;   // stages the producer has filled
+};
+constexpr size_t kLmSmemBytes = sizeof(LmSmem) + 1024;
+static_assert(kLmSmemBytes <= 227 * 1024, "shared memory");
+
+// The tiles of one launch.  unit u covers n tiles [nt0, nt0 + n_run) of row
+// tile mt, and K iterations [k0, k0 + nk).
+struct Shape {
+  int mt, nt, units, splits, k_iters, run;
+};
+struct Unit {
+  int m, n0, n_run, k0, nk, split;
+};
+
+template <int kMode>
+__device__ __forceinline__ Shape shape_of(const LmParams& p, int count) {
+  Shape s;
+  const int row_tiles = (count + kTile - 1) / kTile;
+  s.splits = 1;
+  s.run = 1;
+  if constexpr (kMode == kFwd || kMode == kDz) {
+    s.mt = row_tiles;
+    const int vt = kMode == kFwd ? (p.V + kTile - 1) / kTile : (p.vcols + kTile - 1) / kTile;
+    s.run = kMode == kFwd ? p.run : 1;
+    s.nt = (vt + s.run - 1) / s.run;
+    s.k_iters = (p.C + 63) / 64;
+  } else if constexpr (kMode == kDh) {
+    s.mt = row_tiles;
+    s.nt = (p.C + kTile - 1) / kTile;
+    s.k_iters = (p.vcols + 63) / 64;
+    s.splits = splits_for(s.mt * s.nt, p.split_most);
+  } else {
+    s.mt = (p.vcols + kTile - 1) / kTile;
+    s.nt = (p.C + kTile - 1) / kTile;
+    s.k_iters = (count + 63) / 64;
+    s.splits = dw_splits(s.mt * s.nt, s.k_iters);
+  }
+  s.units = s.mt * s.nt * s.splits;
+  return s;
+}
+
+template <int kMode>
+__device__ __forceinline__ Unit unit_of(const LmParams& p, const Shape& s, int u) {
+  Unit w;
+  const int tiles = s.mt * s.nt;
+  w.split = u / tiles;
+  int t = u - w.split * tiles;
+  const int panel = t / (kPanel * s.mt);
+  t -= panel * kPanel * s.mt;
+  const int width = min(kPanel, s.nt - panel * kPanel);
+  w.m = t / width;
+  const int n = panel * kPanel + t % width;
+  w.n0 = n * s.run;
+  w.n_run = 1;
+  if constexpr (kMode == kFwd) w.n_run = min(s.run, (p.V + kTile - 1) / kTile - w.n0);
+  w.k0 = static_cast<int>(static_cast<int64_t>(s.k_iters) * w.split / s.splits);
+  w.nk = static_cast<int>(static_cast<int64_t>(s.k_iters) * (w.split + 1) / s.splits) - w.k0;
+  return w;
+}
+
+template <int kMode>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
+    lm_product_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ CUtensorMap tm_b,
+                      const LmParams p) {
+  extern __shared__ uint8_t smem_raw[];
+  LmSmem& S = *reinterpret_cast<LmSmem*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  constexpr bool kAmn = kMode == kDw;                      // A stored with M contiguous
+  constexpr bool kBmn = kMode == kDh || kMode == kDw;      // B stored with N contiguous
+  const int warp = threadIdx.x >> 5;
+  const uint32_t rank = ptx::cluster_rank();
+  const int pair = blockIdx.x >> 1, n_pairs = gridDim.x >> 1;
+  volatile int* abort_flag = &S.abort_flag;
+  const int count = p.count ? __ldg(p.count) : p.n_rows;
+  const Shape sh = shape_of<kMode>(p, count);
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < kStages; ++s) {
+      ptx::mbar_init(&S.full[s], 1);
+      ptx::mbar_init(&S.empty[s], 1);
+    }
+    for (int b = 0; b < 2; ++b) {
+      ptx::mbar_init(&S.tm_full[b], 1);
+      ptx::mbar_init(&S.tm_empty[b], 2 * kEpiThreads / 32);   // every epilogue warp of the pair
+    }
+    ptx::mbar_init(&S.drain, 1);
+    S.abort_flag = 0;
+    ptx::fence_mbar_init();
+  }
+  if (warp == 2) {
+    ptx::tmem_alloc_pair(&S.tmem_base, 512);
+    ptx::tmem_relinquish_pair();
+  }
+  ptx::tc_fence_before();
+  __syncthreads();
+  ptx::cluster_sync();   // the other CTA's barriers exist
+  ptx::tc_fence_after();
+  const uint32_t tmem = S.tmem_base;
+
+  if (warp == 0) {
+    // ------------------------------------------------------------ producer
+    if (ptx::elect_one()) {
+      ptx::prefetch_tensormap(&tm_a);
+      ptx::prefetch_tensormap(&tm_b);
+      uint32_t it = 0;
+      bool ok = true;
+      for (int u = pair; ok && u < sh.units; u += n_pairs) {
+        const Unit w = unit_of<kMode>(p, sh, u);
+        for (int j = 0; ok && j < w.n_run; ++j) {
+          const int m0 = w.m * kTile + static_cast<int>(rank) * kHalf;
+          const int n0 = (w.n0 + j) * kTile + static_cast<int>(rank) * kHalf;
+          for (int k = 0; k < w.nk; ++k, ++it) {
+            const int st = it % kStages;
+            if (it >= kStages && !ptx::mbar_wait(&S.empty[st], (it / kStages - 1) & 1, abort_flag, kWaitLimitNs)) {
+              ok = false;
+              break;
+            }
+            if (rank == 0) ptx::mbar_arrive_expect_tx(&S.full[st], 4 * kBoxBytes);
+            const uint32_t bar = ptx::cluster_addr(&S.full[st], 0);
+            const int kk = (w.k0 + k) * 64;
+            if constexpr (kAmn) {
+              ptx::tma_load_2d_pair(S.a[st], &tm_a, bar, m0, kk);
+              ptx::tma_load_2d_pair(S.a[st] + kBoxBytes / 2, &tm_a, bar, m0 + 64, kk);
+            } else {
+              ptx::tma_load_2d_pair(S.a[st], &tm_a, bar, kk, m0);
+            }
+            if constexpr (kBmn) {
+              const int y = kMode == kDh ? p.v0 + kk : kk;
+              ptx::tma_load_2d_pair(S.b[st], &tm_b, bar, n0, y);
+              ptx::tma_load_2d_pair(S.b[st] + kBoxBytes / 2, &tm_b, bar, n0 + 64, y);
+            } else {
+              ptx::tma_load_2d_pair(S.b[st], &tm_b, bar, kk, kMode == kDz ? p.v0 + n0 : n0);
+            }
+          }
+        }
+      }
+      S.issued = it;
+    }
+  } else if (warp == 1 && rank == 0) {
+    // ------------------------------------------------------------ MMA issuer
+    if (ptx::elect_one()) {
+      constexpr uint32_t idesc = ptx::idesc_bf16_f32(kTile, kTile, kAmn, kBmn);
+      // K step of 16 elements: 32 bytes along a K-major row, 16 rows of 128
+      // bytes of an MN-major box (its two 64-column boxes half a stage apart)
+      constexpr uint32_t kStepA = kAmn ? 2048 : 32, kStepB = kBmn ? 2048 : 32;
+      uint32_t it = 0, tile = 0;
+      bool ok = true;
+      for (int u = pair; ok && u < sh.units; u += n_pairs) {
+        const Unit w = unit_of<kMode>(p, sh, u);
+        if (w.nk == 0) continue;
+        for (int j = 0; ok && j < w.n_run; ++j, ++tile) {
+          const uint32_t buf = tile & 1;
+          if (tile >= 2 && !ptx::mbar_wait(&S.tm_empty[buf], (tile / 2 - 1) & 1, abort_flag, kWaitLimitNs)) {
+            ok = false;
+            break;
+          }
+          ptx::tc_fence_after();
+          for (int k = 0; k < w.nk; ++k, ++it) {
+            const int st = it % kStages;
+            if (!ptx::mbar_wait(&S.full[st], (it / kStages) & 1, abort_flag, kWaitLimitNs)) {
+              ok = false;
+              break;
+            }
+            ptx::tc_fence_after();
+            const uint64_t ad = ptx::sw128_desc(ptx::smem_addr(S.a[st]), kAmn ? kBoxBytes / 2 : 16, 1024);
+            const uint64_t bd = ptx::sw128_desc(ptx::smem_addr(S.b[st]), kBmn ? kBoxBytes / 2 : 16, 1024);
+#pragma unroll
+            for (int q = 0; q < 4; ++q)
+              ptx::mma_ss_pair(tmem + buf * kTile, ptx::desc_add(ad, q * kStepA), ptx::desc_add(bd, q * kStepB), idesc,
+                               (k > 0 || q > 0) ? 1u : 0u);
+            ptx::mma_commit_pair(&S.empty[st]);
+          }
+          if (ok) ptx::mma_commit_pair(&S.tm_full[buf]);
+        }
+      }
+      // every product issued above has completed before TMEM is released
+      ptx::mma_commit_pair(&S.drain);
+      ptx::mbar_drain(&S.drain, 0);
+    }
+  } else if (warp >= 4) {
+    // ------------------------------------------------------------ epilogue
+    const int wg = (warp - 4) >> 2;                     // column half
+    const int lane = threadIdx.x & 31;
+    const int r = static_cast<int>(rank) * kHalf + (warp & 3) * 32 + lane;   // row inside the tile
+    const uint32_t lane_off = static_cast<uint32_t>((warp & 3) * 32) << 16;
+    const uint32_t bar_empty[2] = {ptx::cluster_addr(&S.tm_empty[0], 0), ptx::cluster_addr(&S.tm_empty[1], 0)};
+    uint32_t tile = 0;
+    bool ok = true;
+    for (int u = pair; ok && u < sh.units; u += n_pairs) {
+      const Unit w = unit_of<kMode>(p, sh, u);
+      if (kMode == kDh && w.nk == 0) continue;
+      const int row = w.m * kTile + r;
+      const int64_t tile_id = static_cast<int64_t>(w.split) * sh.mt * sh.nt + w.m * sh.nt + w.n0;
+      // per-row inputs
+      int tgt = -1;
+      float m = -INFINITY, s = 0.f, coef = 0.f, lse2 = 0.f;
+      int64_t pos = row;
+      if (kMode != kDw && row < count) {
+        pos = p.rows ? __ldg(p.rows + row) : row;
+        if (kMode == kFwd || kMode == kDz) tgt = __ldg(p.target + pos);
+        if (kMode == kDz) {
+          coef = __ldg(p.dloss + pos) * p.scale;
+          lse2 = __ldg(p.lse + pos) * kLog2e;
+        }
+      }
+      for (int j = 0; j < w.n_run; ++j) {
+        const uint32_t buf = tile & 1;
+        const bool any = kMode != kDw || w.nk > 0;   // no rows at all: dw is zero
+        if (any) {
+          ok = ptx::mbar_wait(&S.tm_full[buf], (tile / 2) & 1, abort_flag, kWaitLimitNs);
+          ok = __all_sync(0xffffffffu, ok);
+          if (!ok) break;
+          ptx::tc_fence_after();
+          ++tile;
+        }
+        const int n0 = (w.n0 + j) * kTile + wg * kHalf;   // first column of this warpgroup
+#pragma unroll 1
+        for (int c = 0; c < 4; ++c) {
+          uint32_t raw[32];
+          if (any) {
+            ptx::tmem_ld32(tmem + lane_off + buf * kTile + wg * kHalf + c * 32, raw);
+            ptx::tmem_wait_ld();
+          } else {
+#pragma unroll
+            for (int e = 0; e < 32; ++e) raw[e] = 0;
+          }
+          if (any && c == 3) {
+            ptx::tc_fence_before();
+            __syncwarp();
+            if (lane == 0) ptx::mbar_arrive_cluster(bar_empty[buf]);
+          }
+          const int c0 = n0 + c * 32;
+          if constexpr (kMode == kFwd) {
+            float t[32];
+            float top = -INFINITY;
+#pragma unroll
+            for (int e = 0; e < 32; ++e) {
+              t[e] = __uint_as_float(raw[e]) * p.scale_log2;
+              if (c0 + e >= p.V) t[e] = -INFINITY;
+              top = fmaxf(top, t[e]);
+            }
+            if (static_cast<uint32_t>(tgt - c0) < 32u) {
+#pragma unroll
+              for (int e = 0; e < 32; ++e)
+                if (tgt - c0 == e && tgt < p.V) p.zt[row] = t[e];
+            }
+            const float mn = fmaxf(m, top);
+            const float ms = mn == -INFINITY ? 0.f : mn;
+            s *= ptx::ex2(m - ms);
+#pragma unroll
+            for (int e = 0; e < 32; ++e) s += ptx::ex2(t[e] - ms);
+            m = mn;
+          } else if constexpr (kMode == kDz) {
+            if (c0 < p.ld_dz) {
+              uint32_t o[16];
+#pragma unroll
+              for (int e = 0; e < 32; e += 2) {
+                float d[2];
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                  const float pr = ptx::ex2(fmaf(__uint_as_float(raw[e + i]), p.scale_log2, -lse2));
+                  const float g = pr - (p.v0 + c0 + e + i == tgt ? 1.f : 0.f);
+                  d[i] = row < count && c0 + e + i < p.vcols ? coef * g : 0.f;
+                }
+                o[e / 2] = ptx::pack_bf16x2(d[0], d[1]);
+              }
+              uint4* dst = reinterpret_cast<uint4*>(p.dz + static_cast<int64_t>(row) * p.ld_dz + c0);
+#pragma unroll
+              for (int q = 0; q < 4; ++q) dst[q] = make_uint4(o[4 * q], o[4 * q + 1], o[4 * q + 2], o[4 * q + 3]);
+            }
+          } else if constexpr (kMode == kDh) {
+            float* blk = p.acc + tile_id * (kTile * kTile) + r * kTile + wg * kHalf + c * 32;
+            const bool out = p.last && sh.splits == 1;
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+              float v[8];
+#pragma unroll
+              for (int e = 0; e < 8; ++e) v[e] = __uint_as_float(raw[8 * q + e]);
+              float4* ap = reinterpret_cast<float4*>(blk + 8 * q);
+              if (!p.first) {
+                const float4 x = ap[0], y = ap[1];
+                v[0] += x.x; v[1] += x.y; v[2] += x.z; v[3] += x.w;
+                v[4] += y.x; v[5] += y.y; v[6] += y.z; v[7] += y.w;
+              }
+              if (!out) {
+                ap[0] = make_float4(v[0], v[1], v[2], v[3]);
+                ap[1] = make_float4(v[4], v[5], v[6], v[7]);
+              } else if (row < count && c0 + 8 * q < p.C) {
+                *reinterpret_cast<uint4*>(p.dh + pos * p.C + c0 + 8 * q) =
+                    make_uint4(ptx::pack_bf16x2(v[0], v[1]), ptx::pack_bf16x2(v[2], v[3]),
+                               ptx::pack_bf16x2(v[4], v[5]), ptx::pack_bf16x2(v[6], v[7]));
+              }
+            }
+          } else {
+            if (sh.splits > 1) {
+              float4* ap = reinterpret_cast<float4*>(p.acc + tile_id * (kTile * kTile) + r * kTile + wg * kHalf + c * 32);
+#pragma unroll
+              for (int q = 0; q < 8; ++q)
+                ap[q] = make_float4(__uint_as_float(raw[4 * q]), __uint_as_float(raw[4 * q + 1]),
+                                    __uint_as_float(raw[4 * q + 2]), __uint_as_float(raw[4 * q + 3]));
+            } else if (row < p.vcols) {
+              __nv_bfloat16* dst = p.dw + (static_cast<int64_t>(p.v0) + row) * p.C + c0;
+#pragma unroll
+              for (int q = 0; q < 4; ++q)
+                if (c0 + 8 * q < p.C)
+                  *reinterpret_cast<uint4*>(dst + 8 * q) =
+                      make_uint4(ptx::pack_bf16x2(__uint_as_float(raw[8 * q]), __uint_as_float(raw[8 * q + 1])),
+                                 ptx::pack_bf16x2(__uint_as_float(raw[8 * q + 2]), __uint_as_float(raw[8 * q + 3])),
+                                 ptx::pack_bf16x2(__uint_as_float(raw[8 * q + 4]), __uint_as_float(raw[8 * q + 5])),
+                                 ptx::pack_bf16x2(__uint_as_float(raw[8 * q + 6]), __uint_as_float(raw[8 * q + 7])));
+            }
+          }
+        }
+      }
+      if (kMode == kFwd && ok && row < count)
+        p.part[(static_cast<int64_t>(w.n0 / sh.run) * 2 + wg) * p.np + row] = make_float2(m, s);
+    }
+  }
+  // Both CTAs leave together: nothing of the pair signals or reads a CTA that
+  // has gone.  After a timeout the stages' copies are waited for first.
+  __syncwarp();
+  __syncthreads();
+  ptx::cluster_sync();
+  if (S.abort_flag) {
+    if (threadIdx.x == 0) {
+      if (p.err) *p.err = TPK_E_TIMEOUT;
+      if (rank == 0)
+        for (uint32_t i = S.issued > kStages ? S.issued - kStages : 0; i < S.issued; ++i)
+          ptx::mbar_drain(&S.full[i % kStages], (i / kStages) & 1);
+    }
+  }
+  __syncwarp();
+  __syncthreads();
+  ptx::cluster_sync();
+  ptx::tc_fence_after();
+  if (warp == 2) ptx::tmem_dealloc_pair(tmem, 512);
+}
+
+// ---- gathering the positions that have a target ------------------------------
+// rows[0..count) = those positions, ascending; pos[f] = its row or -1.  One
+// CTA: a few microseconds per 10,000 positions, against milliseconds of
+// products for as many.
+constexpr int kIndexThreads = 1024;
+constexpr int kIndexPer = 4;
+
+__global__ void __launch_bounds__(kIndexThreads) lm_index_kernel(const int32_t* __restrict__ target, int N, int V,
+                                                                 int32_t* __restrict__ rows, int32_t* __restrict__ pos,
+                                                                 int32_t* __restrict__ count) {
+  __shared__ int sums[2][32];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  int base = 0, turn = 0;
+  for (int i0 = 0; i0 < N; i0 += kIndexThreads * kIndexPer, turn ^= 1) {
+    const int i = i0 + threadIdx.x * kIndexPer;
+    bool on[kIndexPer];
+    int n = 0;
+#pragma unroll
+    for (int e = 0; e < kIndexPer; ++e) {
+      const int t = i + e < N ? __ldg(target + i + e) : -1;
+      on[e] = t >= 0 && t < V;
+      n += on[e];
+    }
+    int inc = n;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int v = __shfl_up_sync(0xffffffffu, inc, o);
+      if (lane >= o) inc += v;
+    }
+    if (lane == 31) sums[turn][warp] = inc;
+    __syncthreads();
+    int ws = sums[turn][lane];
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int v = __shfl_up_sync(0xffffffffu, ws, o);
+      if (lane >= o) ws += v;
+    }
+    const int all = __shfl_sync(0xffffffffu, ws, 31);
+    const int before = warp > 0 ? __shfl_sync(0xffffffffu, ws, warp - 1) : 0;
+    int at = base + before + inc - n;
+#pragma unroll
+    for (int e = 0; e < kIndexPer; ++e)
+      if (i + e < N) {
+        pos[i + e] = on[e] ? at : -1;
+        if (on[e]) rows[at++] = i + e;
+      }
+    base += all;
+  }
+  if (threadIdx.x == 0) *count = base;
+}
+
+// hc[r] = h[rows[r]]; rows up to the next multiple of 256 are zero.
+__global__ void __launch_bounds__(256) lm_gather_kernel(const uint4* __restrict__ h, const int32_t* __restrict__ rows,
+                                                        const int32_t* __restrict__ count, int vecs,
+                                                        uint4* __restrict__ hc) {
+  const int lane = threadIdx.x & 31;
+  const int n = __ldg(count), padded = (n + kTile - 1) / kTile * kTile;
+  for (int64_t r = static_cast<int64_t>(blockIdx.x) * 8 + (threadIdx.x >> 5); r < padded;
+       r += static_cast<int64_t>(gridDim.x) * 8) {
+    const uint4* src = r < n ? h + static_cast<int64_t>(__ldg(rows + r)) * vecs : nullptr;
+    uint4* dst = hc + r * vecs;
+#pragma unroll 4
+    for (int c = lane; c < vecs; c += 32) dst[c] = src ? __ldg(src + c) : make_uint4(0, 0, 0, 0);
+  }
+}
+
+// loss and lse of every position: the slots' (maximum, sum) pairs joined, 32
+// rows per CTA, 8 warps over the slots.
+__global__ void __launch_bounds__(256) lm_join_kernel(const float2* __restrict__ part, const float* __restrict__ zt,
+                                                      const int32_t* __restrict__ pos,
+                                                      const int32_t* __restrict__ target, int N, int V, int slots,
+                                                      int64_t np, float* __restrict__ loss, float* __restrict__ lse) {
+  __shared__ float2 sm[8][32];
+  const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
+  const int i = blockIdx.x * 32 + lane;
+  int r = -1;
+  if (i < N) {
+    const int t = __ldg(target + i);
+    if (t >= 0 && t < V) r = pos ? __ldg(pos + i) : i;
+  }
+  float m = -INFINITY, s = 0.f;
+  if (r >= 0) {
+#pragma unroll 4
+    for (int k = w; k < slots; k += 8) {
+      const float2 x = __ldg(part + static_cast<int64_t>(k) * np + r);
+      const float mn = fmaxf(m, x.x);
+      const float ms = mn == -INFINITY ? 0.f : mn;
+      s = s * exp2f(m - ms) + x.y * exp2f(x.x - ms);
+      m = mn;
+    }
+  }
+  sm[w][lane] = make_float2(m, s);
+  __syncthreads();
+  if (w != 0 || i >= N) return;
+  if (r < 0) {
+    loss[i] = 0.f;
+    lse[i] = 0.f;
+    return;
+  }
+  for (int k = 1; k < 8; ++k) {
+    const float2 x = sm[k][lane];
+    const float mn = fmaxf(m, x.x);
+    const float ms = mn == -INFINITY ? 0.f : mn;
+    s = s * exp2f(m - ms) + x.y * exp2f(x.x - ms);
+    m = mn;
+  }
+  const float l2 = m + log2f(s);
+  lse[i] = l2 * kLn2;
+  loss[i] = (l2 - zt[r]) * kLn2;
+}
+
+// dh of every position that the product's last epilogue has not written:
+// zero without a target, the sum of the splits over K where there are any.
+__global__ void __launch_bounds__(256) lm_dh_kernel(const float* __restrict__ acc, const int32_t* __restrict__ pos,
+                                                    const int32_t* __restrict__ count, int N, int C, int split_most,
+                                                    uint4* __restrict__ dh) {
+  const int lane = threadIdx.x & 31;
+  const int mt = (__ldg(count) + kTile - 1) / kTile, nt = (C + kTile - 1) / kTile;
+  const int splits = splits_for(mt * nt, split_most);
+  const int vecs = C / 8;
+  for (int64_t i = static_cast<int64_t>(blockIdx.x) * 8 + (threadIdx.x >> 5); i < N;
+       i += static_cast<int64_t>(gridDim.x) * 8) {
+    const int r = __ldg(pos + i);
+    if (r < 0) {
+      for (int c = lane; c < vecs; c += 32) dh[i * vecs + c] = make_uint4(0, 0, 0, 0);
+      continue;
+    }
+    if (splits == 1) continue;
+    for (int c = lane; c < vecs; c += 32) {
+      const int col = c * 8;
+      float v[8] = {};
+      for (int s = 0; s < splits; ++s) {
+        const int64_t tile = (static_cast<int64_t>(s) * mt + r / kTile) * nt + col / kTile;
+        const float4* a = reinterpret_cast<const float4*>(acc + tile * (kTile * kTile) + (r % kTile) * kTile + col % kTile);
+        const float4 x = a[0], y = a[1];
+        v[0] += x.x; v[1] += x.y; v[2] += x.z; v[3] += x.w;
+        v[4] += y.x; v[5] += y.y; v[6] += y.z; v[7] += y.w;
+      }
+      dh[i * vecs + c] = make_uint4(ptx::pack_bf16x2(v[0], v[1]), ptx::pack_bf16x2(v[2], v[3]),
+                                    ptx::pack_bf16x2(v[4], v[5]), ptx::pack_bf16x2(v[6], v[7]));
+    }
+  }
+}
+
+// The piece's rows of dw where its product was split over K.
+__global__ void __launch_bounds__(256) lm_dw_kernel(const float* __restrict__ acc, const int32_t* __restrict__ count,
+                                                    int v0, int vcols, int C, uint4* __restrict__ dw) {
+  const int mt = (vcols + kTile - 1) / kTile, nt = (C + kTile - 1) / kTile;
+  const int splits = dw_splits(mt * nt, (__ldg(count) + 63) / 64);
+  if (splits == 1) return;
+  const int lane = threadIdx.x & 31;
+  const int vecs = C / 8;
+  for (int64_t r = static_cast<int64_t>(blockIdx.x) * 8 + (threadIdx.x >> 5); r < vcols;
+       r += static_cast<int64_t>(gridDim.x) * 8)
+    for (int c = lane; c < vecs; c += 32) {
+      const int col = c * 8;
+      float v[8] = {};
+      for (int s = 0; s < splits; ++s) {
+        const int64_t tile = (static_cast<int64_t>(s) * mt + r / kTile) * nt + col / kTile;
+        const float4* a = reinterpret_cast<const float4*>(acc + tile * (kTile * kTile) + (r % kTile) * kTile + col % kTile);
+        const float4 x = a[0], y = a[1];
+        v[0] += x.x; v[1] += x.y; v[2] += x.z; v[3] += x.w;
+        v[4] += y.x; v[5] += y.y; v[6] += y.z; v[7] += y.w;
+      }
+      dw[(v0 + r) * vecs + c] = make_uint4(ptx::pack_bf16x2(v[0], v[1]), ptx::pack_bf16x2(v[2], v[3]),
+                                           ptx::pack_bf16x2(v[4], v[5]), ptx::pack_bf16x2(v[6], v[7]));
+    }
+}
+
+// ---- host ------------------------------------------------------------------------
+constexpr int64_t kDzBytes = int64_t{4} << 30;   // dz of one piece
+constexpr int kDirectRows = kTile;               // forward: up to one row tile is not gathered
+
+int64_t up(int64_t n, int64_t k) { return (n + k - 1) / k * k; }
+
+struct LmShape {
+  int64_t np;        // N rounded up to whole tiles
+  int vt;            // vocabulary tiles
+  int run, chunks;   // forward: vocabulary tiles per unit, units per row tile
+  int64_t piece;     // backward: ids per piece (a multiple of 256)
+  int pieces;
+};
+LmShape lm_shape(int64_t N, int64_t V) {
+  LmShape s;
+  s.np = up(N, kTile);
+  s.vt = static_cast<int>((V + kTile - 1) / kTile);
+  // a unit of several vocabulary tiles keeps its rows' statistics in
+  // registers; short runs where there are few tiles to share out
+  const int64_t tiles = s.np / kTile * s.vt;
+  int64_t run = tiles / (kSplitPairs * 8);
+  run = run < 1 ? 1 : (run > 16 ? 16 : run);
+  s.run = static_cast<int>(run);
+  s.chunks = (s.vt + s.run - 1) / s.run;
+  int64_t most = kDzBytes / (s.np * 2) / kTile * kTile;
+  if (most < 4096) most = 4096;
+  s.pieces = static_cast<int>((V + most - 1) / most);
+  s.piece = up((V + s.pieces - 1) / s.pieces, kTile);
+  s.pieces = static_cast<int>((V + s.piece - 1) / s.piece);
+  return s;
+}
+
+struct Carve {
+  uint8_t* base;
+  size_t at = 0;
+  template <typename T>
+  T* take(int64_t n) {
+    T* p = reinterpret_cast<T*>(base + at);
+    at += static_cast<size_t>(up(n * static_cast<int64_t>(sizeof(T)), 1024));
+    return p;
+  }
+};
+
+struct LmWork {
+  int32_t *rows, *pos, *count;
+  __nv_bfloat16* hc;
+  float2* part;
+  float* zt;
+  __nv_bfloat16* dz;
+  float* acc_h;
+  float* acc_w;
+};
+size_t carve(uint8_t* base, int64_t N, int64_t V, int32_t C, bool backward, LmWork* w) {
+  const LmShape s = lm_shape(N, V);
+  Carve c{base};
+  LmWork o{};
+  if (backward || N > kDirectRows) {
+    o.rows = c.take<int32_t>(s.np);
+    o.pos = c.take<int32_t>(s.np);
+    o.count = c.take<int32_t>(1);
+    o.hc = c.take<__nv_bfloat16>(s.np * C);
+  }
+  if (!backward) {
+    o.part = c.take<float2>(2 * static_cast<int64_t>(s.chunks) * s.np);
+    o.zt = c.take<float>(s.np);
+  } else {
+    o.dz = c.take<__nv_bfloat16>(s.np * s.piece);
+    const int64_t nt = (C + kTile - 1) / kTile;
+    const int64_t th = s.np / kTile * nt;
+    // a split uses at most kSplitPairs tiles in all
+    o.acc_h = c.take<float>((th > kSplitPairs ? th : kSplitPairs) * kTile * kTile);
+    o.acc_w = c.take<float>(static_cast<int64_t>(kSplitPairs) * kTile * kTile);
+  }
+  if (w) *w = o;
+  return c.at;
+}
+
+bool sizes_ok(int64_t N, int64_t V, int32_t C) {
+  return N >= 0 && N < (int64_t{1} << 31) - kTile && V >= 1 && V < (int64_t{1} << 31) - 4096 && C >= 8 && C % 8 == 0 &&
+         C <= (1 << 20);
+}
+
+template <int kMode>
+int launch_product(const CUtensorMap& a, const CUtensorMap& b, const LmParams& p, int64_t most_units, cudaStream_t s) {
+  static PerContext<int> rec;
+  int st = set_smem_once(rec, lm_product_kernel<kMode>, kLmSmemBytes);
+  if (st != TPK_OK) return st;
+  int64_t pairs = num_sms() / 2;
+  if (pairs < 1) pairs = 1;
+  if (pairs > most_units) pairs = most_units;
+  lm_product_kernel<kMode><<<static_cast<unsigned>(2 * pairs), kThreads, kLmSmemBytes, s>>>(a, b, p);
+  return cuda_status(cudaGetLastError());
+}
+
+int64_t grid_for(int64_t warps) {
+  const int64_t blocks = (warps + 7) / 8, most = int64_t{num_sms()} * 16;
+  return blocks < most ? blocks : most;
+}
+
+// rows, pos, count and hc of the positions with a target
+int gather_rows(const void* h, const int32_t* target, int64_t N, int64_t V, int32_t C, const LmWork& w, cudaStream_t s) {
+  lm_index_kernel<<<1, kIndexThreads, 0, s>>>(target, static_cast<int>(N), static_cast<int>(V), w.rows, w.pos, w.count);
+  int st = cuda_status(cudaGetLastError());
+  if (st != TPK_OK) return st;
+  lm_gather_kernel<<<static_cast<unsigned>(grid_for(up(N, kTile))), 256, 0, s>>>(
+      static_cast<const uint4*>(h), w.rows, w.count, C / 8, reinterpret_cast<uint4*>(w.hc));
+  return cuda_status(cudaGetLastError());
+}
+
+bool aligned16(const void* p) { return reinterpret_cast<uintptr_t>(p) % 16 == 0; }
+
+}  // namespace
+}  // namespace tpk
+
+extern "C" size_t tpk_lm_loss_workspace_bytes(int64_t N, int64_t V, int32_t C, int32_t backward) {
+  using namespace tpk;
+  if (!sizes_ok(N, V, C) || N == 0) return 0;
+  return carve(nullptr, N, V, C, backward != 0, nullptr);
+}
+
+extern "C" int tpk_lm_loss(const void* h, const void* w, const int32_t* target, float* loss, float* lse, int64_t N,
+                           int64_t V, int32_t C, float scale, void* workspace, size_t ws_bytes, int32_t* dev_err,
+                           void* stream) {
+  using namespace tpk;
+  if (!sizes_ok(N, V, C) || !(scale > 0.f) || !(scale < INFINITY)) return TPK_E_ARG;
+  if (N == 0) return TPK_OK;
+  if (!h || !w || !target || !loss || !lse || !aligned16(h) || !aligned16(w)) return TPK_E_ARG;
+  LmWork k;
+  if (!workspace || reinterpret_cast<uintptr_t>(workspace) % 256 ||
+      ws_bytes < carve(static_cast<uint8_t*>(workspace), N, V, C, false, &k))
+    return TPK_E_WORKSPACE;
+  int st = check_device();
+  if (st != TPK_OK) return st;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  const LmShape sh = lm_shape(N, V);
+  if (k.hc) st = gather_rows(h, target, N, V, C, k, s);
+  CUtensorMap ma, mb;
+  if (st == TPK_OK) st = k.hc ? make_map_2d(&ma, k.hc, sh.np, C, C, kHalf) : make_map_2d(&ma, h, N, C, C, kHalf);
+  if (st == TPK_OK) st = make_map_2d(&mb, w, V, C, C, kHalf);
+  if (st != TPK_OK) return st;
+  LmParams p{};
+  p.count = k.count;
+  p.n_rows = static_cast<int32_t>(N);
+  p.V = static_cast<int32_t>(V);
+  p.C = C;
+  p.np = sh.np;
+  p.rows = k.rows;
+  p.target = target;
+  p.scale = scale;
+  p.scale_log2 = scale * kLog2e;
+  p.part = k.part;
+  p.zt = k.zt;
+  p.run = sh.run;
+  p.err = dev_err;
+  st = launch_product<kFwd>(ma, mb, p, sh.np / kTile * sh.chunks, s);
+  if (st != TPK_OK) return st;
+  lm_join_kernel<<<static_cast<unsigned>((N + 31) / 32), 256, 0, s>>>(k.part, k.zt, k.pos, target, static_cast<int>(N),
+                                                                      static_cast<int>(V), 2 * sh.chunks, sh.np, loss,
+                                                                      lse);
+  return cuda_status(cudaGetLastError());
+}
+
+extern "C" int tpk_lm_loss_bwd(const void* h, const void* w, const int32_t* target, const float* lse,
+                               const float* dloss, void* dh, void* dw, int64_t N, int64_t V, int32_t C, float scale,
+                               void* workspace, size_t ws_bytes, int32_t* dev_err, void* stream) {
+  using namespace tpk;
+  if (!sizes_ok(N, V, C) || !(scale > 0.f) || !(scale < INFINITY) || !dw || !aligned16(dw)) return TPK_E_ARG;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  if (N == 0) {
+    const int st = check_device();
+    return st != TPK_OK ? st : cuda_status(cudaMemsetAsync(dw, 0, static_cast<size_t>(V) * C * 2, s));
+  }
+  if (!h || !w || !target || !lse || !dloss || !dh || !aligned16(h) || !aligned16(w) || !aligned16(dh)) return TPK_E_ARG;
+  LmWork k;
+  if (!workspace || reinterpret_cast<uintptr_t>(workspace) % 256 ||
+      ws_bytes < carve(static_cast<uint8_t*>(workspace), N, V, C, true, &k))
+    return TPK_E_WORKSPACE;
+  int st = check_device();
+  if (st != TPK_OK) return st;
+  const LmShape sh = lm_shape(N, V);
+  st = gather_rows(h, target, N, V, C, k, s);
+  CUtensorMap hk, hm, wk, wm, zk, zm;   // h, w, dz: boxes of 128 rows (K-major) and of 64 (MN-major)
+  if (st == TPK_OK) st = make_map_2d(&hk, k.hc, sh.np, C, C, kHalf);
+  if (st == TPK_OK) st = make_map_2d(&hm, k.hc, sh.np, C, C, 64);
+  if (st == TPK_OK) st = make_map_2d(&wk, w, V, C, C, kHalf);
+  if (st == TPK_OK) st = make_map_2d(&wm, w, V, C, C, 64);
+  if (st == TPK_OK) st = make_map_2d(&zk, k.dz, sh.np, sh.piece, sh.piece, kHalf);
+  if (st == TPK_OK) st = make_map_2d(&zm, k.dz, sh.np, sh.piece, sh.piece, 64);
+  LmParams p{};
+  p.count = k.count;
+  p.n_rows = static_cast<int32_t>(N);
+  p.V = static_cast<int32_t>(V);
+  p.C = C;
+  p.np = sh.np;
+  p.rows = k.rows;
+  p.target = target;
+  p.lse = lse;
+  p.dloss = dloss;
+  p.scale = scale;
+  p.scale_log2 = scale * kLog2e;
+  p.ld_dz = static_cast<int32_t>(sh.piece);
+  p.dz = k.dz;
+  p.split_most = static_cast<int32_t>(((sh.piece < V ? sh.piece : V) + 63) / 64);
+  p.dh = static_cast<__nv_bfloat16*>(dh);
+  p.dw = static_cast<__nv_bfloat16*>(dw);
+  p.err = dev_err;
+  const int64_t ct = (C + kTile - 1) / kTile;
+  for (int i = 0; st == TPK_OK && i < sh.pieces; ++i) {
+    p.v0 = static_cast<int32_t>(i * sh.piece);
+    p.vcols = static_cast<int32_t>(V - p.v0 < sh.piece ? V - p.v0 : sh.piece);
+    p.first = i == 0;
+    p.last = i + 1 == sh.pieces;
+    const int64_t vt = (p.vcols + kTile - 1) / kTile;
+    st = launch_product<kDz>(hk, wk, p, sh.np / kTile * vt, s);
+    p.acc = k.acc_h;
+    if (st == TPK_OK) st = launch_product<kDh>(zk, wm, p, kSplitPairs > sh.np / kTile * ct ? kSplitPairs : sh.np / kTile * ct, s);
+    p.acc = k.acc_w;
+    if (st == TPK_OK) st = launch_product<kDw>(zm, hm, p, kSplitPairs > vt * ct ? kSplitPairs : vt * ct, s);
+    if (st == TPK_OK && 2 * vt * ct <= kSplitPairs) {
+      lm_dw_kernel<<<static_cast<unsigned>(grid_for(p.vcols)), 256, 0, s>>>(k.acc_w, k.count, p.v0, p.vcols, C,
+                                                                            static_cast<uint4*>(dw));
+      st = cuda_status(cudaGetLastError());
+    }
+  }
+  if (st != TPK_OK) return st;
+  lm_dh_kernel<<<static_cast<unsigned>(grid_for(N)), 256, 0, s>>>(k.acc_h, k.pos, k.count, static_cast<int>(N), C,
+                                                                  p.split_most, static_cast<uint4*>(dh));
+  return cuda_status(cudaGetLastError());
+}

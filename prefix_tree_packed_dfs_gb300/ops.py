@@ -605,3 +605,280 @@ def gdn_delta_rule_bwd(dplan, q, k, v, g, beta, dout, state, scale=None, dq=None
                                        _ptr(state), st_bytes, _ptr(workspace), ws_bytes, _stream()),
             "tpk_gdn_delta_rule_bwd")
     return dq, dk, dv, dg, dbeta
+
+
+# ---- the operators around the token mixers ----------------------------------
+
+_TABLE_TYPES = {torch.bfloat16: B.BF16, torch.float32: B.F32}
+
+
+def _same_device(ref, ref_name, *named):
+    """Every tensor (None skipped) a CUDA tensor on ref's device (checked after
+    the shapes, so a wrong shape is reported as such wherever the tensors live)."""
+    for t, n in ((ref, ref_name),) + named:
+        if t is None:
+            continue
+        if not t.is_cuda:
+            raise ValueError("%s must be a CUDA tensor (no CPU path exists)" % n)
+        if t.device != ref.device:
+            raise ValueError("%s is on %s, expected %s" % (n, t.device, ref.device))
+
+
+def _launch(ref, fn, what, *args):
+    """fn(*args, stream) on ref's device and that device's current stream."""
+    if ref.device.index == torch.cuda.current_device():
+        B.check(fn(*args, _stream()), what)
+    else:
+        with torch.cuda.device(ref.device):
+            B.check(fn(*args, _stream()), what)
+
+
+def _workspace(workspace, need, ref, what):
+    """The caller's workspace tensor, checked, or a new one on ref's device."""
+    if workspace is None:
+        return torch.empty(max(need, 256), dtype=torch.uint8, device=ref.device)
+    if not isinstance(workspace, torch.Tensor) or not workspace.is_contiguous():
+        raise ValueError("workspace must be a contiguous tensor")
+    if workspace.numel() * workspace.element_size() < need:
+        raise ValueError("workspace has %d bytes, %s needs %d"
+                         % (workspace.numel() * workspace.element_size(), what, need))
+    return workspace
+
+
+def _channels(C):
+    if C < 8 or C % 8:
+        raise ValueError("rows must have a multiple of 8 channels, got %d" % C)
+
+
+def embed(table, tokens, scale=1.0, out=None):
+    """Embedding lookup with scaling (``tpk_embed``): out[f] = scale *
+    table[tokens[f]] in bf16, a zero row where the id is outside the table.
+
+    table [V, C] bf16 or fp32, tokens [N] int32 (e.g. ``gather_to_forwarded``
+    of the raw token ids).  Returns out [N, C] bf16."""
+    lib = B.load()
+    if not isinstance(table, torch.Tensor) or table.dtype not in _TABLE_TYPES:
+        raise TypeError("table must be a bf16 or fp32 tensor")
+    _need(table, table.dtype, "table", 2, cuda=False)
+    _need(tokens, torch.int32, "tokens", 1, cuda=False)
+    V, C = table.shape
+    N = tokens.numel()
+    _channels(C)
+    if V < 1:
+        raise ValueError("table has no rows")
+    out = torch.empty((N, C), dtype=torch.bfloat16, device=table.device) if out is None else out
+    _need(out, torch.bfloat16, "out", 2, cuda=False)
+    _shape(out, (N, C), "out")
+    _same_device(table, "table", (tokens, "tokens"), (out, "out"))
+    _launch(table, lib.tpk_embed, "tpk_embed", _ptr(table), _TABLE_TYPES[table.dtype], _ptr(tokens), _ptr(out), N, V, C,
+            float(scale))
+    return out
+
+
+def embed_bwd(tokens, dout, vocab, scale=1.0, dtype=torch.float32, dtable=None, workspace=None):
+    """Gradient of ``embed``'s table (``tpk_embed_bwd``): dtable[v] = scale *
+    sum of dout[f] over tokens[f] = v, fp32 sums in a fixed order; ids that do
+    not occur get zero rows.
+
+    tokens [N] int32, dout [N, C] bf16 -> dtable [vocab, C] of ``dtype`` (fp32
+    or bf16; ignored if ``dtable`` is given)."""
+    lib = B.load()
+    _need(tokens, torch.int32, "tokens", 1, cuda=False)
+    _need(dout, torch.bfloat16, "dout", 2, cuda=False)
+    N, C = dout.shape
+    _channels(C)
+    V = int(vocab)
+    if V < 1:
+        raise ValueError("vocab must be positive")
+    if tokens.numel() != N:
+        raise ValueError("tokens has %d ids, dout %d rows" % (tokens.numel(), N))
+    dtype = dtype if dtable is None else dtable.dtype
+    if dtype not in _TABLE_TYPES:
+        raise TypeError("the table's gradient must be bf16 or fp32")
+    dtable = torch.empty((V, C), dtype=dtype, device=dout.device) if dtable is None else dtable
+    _need(dtable, dtype, "dtable", 2, cuda=False)
+    _shape(dtable, (V, C), "dtable")
+    need = int(lib.tpk_embed_bwd_workspace_bytes(N, V, C))
+    workspace = _workspace(workspace, need, dout, "the lookup's backward")
+    _same_device(dout, "dout", (tokens, "tokens"), (dtable, "dtable"), (workspace, "workspace"))
+    _launch(dout, lib.tpk_embed_bwd, "tpk_embed_bwd", _ptr(tokens), _ptr(dout), _ptr(dtable), _TABLE_TYPES[dtype], N, V,
+            C, float(scale), _ptr(workspace), workspace.numel() * workspace.element_size())
+    return dtable
+
+
+def _rows2(t, name, shape, strided=False):
+    """A 2-d bf16 tensor of ``shape``: contiguous, or with ``strided`` rows
+    that may lie apart (column slices), 16-byte aligned.  Returns the row
+    stride in elements."""
+    if not isinstance(t, torch.Tensor) or t.dtype != torch.bfloat16 or t.dim() != 2:
+        raise TypeError("%s must be a 2-d bf16 tensor" % name)
+    _shape(t, shape, name)
+    if not strided:
+        if not t.is_contiguous():
+            raise ValueError("%s must be contiguous" % name)
+        return shape[1]
+    if t.stride(1) != 1:
+        raise ValueError("%s: channels must be contiguous inside a row" % name)
+    if shape[0] <= 1:
+        return shape[1]
+    if t.stride(0) < shape[1] or t.stride(0) % 8:
+        raise ValueError("%s: rows must not overlap and must lie a multiple of 8 elements apart" % name)
+    return t.stride(0)
+
+
+def _norm_args(res, w_pre, y, w_post, gate):
+    """(N, C, ld_y, ld_gate), every input checked."""
+    if not isinstance(res, torch.Tensor) or res.dim() != 2:
+        raise TypeError("res must be a 2-d bf16 tensor")
+    N, C = res.shape
+    _channels(C)
+    _rows2(res, "res", (N, C))
+    if y is None and (gate is not None or w_post is not None):
+        raise ValueError("gate and w_post apply to y, which is missing")
+    ld_y = C if y is None else _rows2(y, "y", (N, C), strided=True)
+    ld_gate = C if gate is None else _rows2(gate, "gate", (N, C), strided=True)
+    for t, n in ((w_pre, "w_pre"), (w_post, "w_post")):
+        if t is not None or n == "w_pre":
+            _need(t, torch.float32, n, 1, cuda=False)
+            _shape(t, (C,), n)
+    return N, C, ld_y, ld_gate
+
+
+def block_norm(res, w_pre, y=None, w_post=None, gate=None, scale=1.0, eps=1e-6, res_out=None, out=None):
+    """The norms around a block with its gate and residual (``tpk_block_norm``):
+
+        r = res + scale * sigmoid(gate) * rmsnorm(y) * w_post
+        x = rmsnorm(r) * w_pre
+
+    res [N, C] bf16 (residual stream), y [N, C] bf16 (the block's output) and
+    gate [N, C] bf16, whose rows may be strided (column slices); w_pre, w_post
+    [C] fp32.  Without w_post y enters as it is, without gate the sigmoid is
+    1; without y (the norm before the first block) r is res.  Returns
+    (r, x), both [N, C] bf16; ``res_out`` may be ``res`` itself."""
+    lib = B.load()
+    N, C, ld_y, ld_gate = _norm_args(res, w_pre, y, w_post, gate)
+    if y is None:
+        if res_out is not None:
+            raise ValueError("without y nothing is added to res: res_out is not written")
+    else:
+        res_out = torch.empty_like(res) if res_out is None else res_out
+        _rows2(res_out, "res_out", (N, C))
+    out = torch.empty_like(res) if out is None else out
+    _rows2(out, "out", (N, C))
+    _same_device(res, "res", (w_pre, "w_pre"), (y, "y"), (w_post, "w_post"), (gate, "gate"), (res_out, "res_out"),
+                 (out, "out"))
+    _launch(res, lib.tpk_block_norm, "tpk_block_norm", _ptr(res), _ptr(y), ld_y, _ptr(gate), ld_gate, _ptr(w_post),
+            _ptr(w_pre), _ptr(res_out), _ptr(out), N, C, float(scale), float(eps))
+    return (res if y is None else res_out), out
+
+
+def block_norm_bwd(res, w_pre, dx, dres_out=None, y=None, w_post=None, gate=None, scale=1.0, eps=1e-6, dres=None,
+                   dy=None, dgate=None, dw_post=None, dw_pre=None, workspace=None):
+    """Gradients of ``block_norm`` (``tpk_block_norm_bwd``) for the gradients
+    dx of x and dres_out of r (None: none); the other inputs as given to the
+    forward.  dy and dgate may be column slices of a wider gradient.  Returns
+    (dres, dy, dgate, dw_post, dw_pre), None where the input was None."""
+    lib = B.load()
+    N, C, ld_y, ld_gate = _norm_args(res, w_pre, y, w_post, gate)
+    _rows2(dx, "dx", (N, C))
+    if dres_out is not None:
+        _rows2(dres_out, "dres_out", (N, C))
+    for t, n, ref in ((dy, "dy", y), (dgate, "dgate", gate), (dw_post, "dw_post", w_post)):
+        if t is not None and ref is None:
+            raise ValueError("%s is given, but not the input it is the gradient of" % n)
+    dres = torch.empty_like(res) if dres is None else dres
+    _rows2(dres, "dres", (N, C))
+    ld_dy = ld_dgate = C
+    if y is not None:
+        dy = torch.empty((N, C), dtype=torch.bfloat16, device=res.device) if dy is None else dy
+        ld_dy = _rows2(dy, "dy", (N, C), strided=True)
+    if gate is not None:
+        dgate = torch.empty((N, C), dtype=torch.bfloat16, device=res.device) if dgate is None else dgate
+        ld_dgate = _rows2(dgate, "dgate", (N, C), strided=True)
+    dw_pre = torch.empty_like(w_pre) if dw_pre is None else dw_pre
+    if w_post is not None:
+        dw_post = torch.empty_like(w_post) if dw_post is None else dw_post
+    for t, n in ((dw_pre, "dw_pre"), (dw_post, "dw_post")):
+        if t is not None:
+            _need(t, torch.float32, n, 1, cuda=False)
+            _shape(t, (C,), n)
+    need = int(lib.tpk_block_norm_bwd_workspace_bytes(N, C))
+    workspace = _workspace(workspace, need, res, "the norms' backward")
+    _same_device(res, "res", (w_pre, "w_pre"), (dx, "dx"), (dres_out, "dres_out"), (y, "y"), (w_post, "w_post"),
+                 (gate, "gate"), (dres, "dres"), (dy, "dy"), (dgate, "dgate"), (dw_post, "dw_post"), (dw_pre, "dw_pre"),
+                 (workspace, "workspace"))
+    _launch(res, lib.tpk_block_norm_bwd, "tpk_block_norm_bwd", _ptr(res), _ptr(y), ld_y, _ptr(gate), ld_gate,
+            _ptr(w_post), _ptr(w_pre), _ptr(dres_out), _ptr(dx), _ptr(dres), _ptr(dy), ld_dy, _ptr(dgate), ld_dgate,
+            _ptr(dw_post), _ptr(dw_pre), N, C, float(scale), float(eps), _ptr(workspace),
+            workspace.numel() * workspace.element_size())
+    return dres, dy, dgate, dw_post, dw_pre
+
+
+def _loss_args(h, w, target, scale):
+    """(N, V, C), the loss's inputs checked."""
+    _need(h, torch.bfloat16, "h", 2, cuda=False)
+    _need(w, torch.bfloat16, "w", 2, cuda=False)
+    _need(target, torch.int32, "target", 1, cuda=False)
+    N, C = h.shape
+    V = w.shape[0]
+    _channels(C)
+    _shape(w, (V, C), "w")
+    _shape(target, (N,), "target")
+    if V < 1:
+        raise ValueError("w has no rows")
+    if not (0.0 < float(scale) < math.inf):
+        raise ValueError("scale must be positive and finite")
+    return N, V, C
+
+
+def lm_loss(h, w, target, scale=1.0, loss=None, lse=None, workspace=None, dev_err=None):
+    """Softmax cross entropy over the vocabulary without the logits (``tpk_lm_loss``).
+
+    h [N, C] bf16 (hidden rows), w [V, C] bf16 (output projection), target [N]
+    int32; logits are ``scale * h @ w.T`` (scale = 1 / temperature).  Returns
+    (loss, lse), fp32 [N]: loss = lse - logit[target], both zero where the
+    target is outside [0, V) (a position without a prediction)."""
+    lib = B.load()
+    N, V, C = _loss_args(h, w, target, scale)
+    loss = torch.empty(N, dtype=torch.float32, device=h.device) if loss is None else loss
+    lse = torch.empty(N, dtype=torch.float32, device=h.device) if lse is None else lse
+    for t, n in ((loss, "loss"), (lse, "lse")):
+        _need(t, torch.float32, n, 1, cuda=False)
+        _shape(t, (N,), n)
+    if dev_err is not None:
+        _need(dev_err, torch.int32, "dev_err", cuda=False)
+    need = int(lib.tpk_lm_loss_workspace_bytes(N, V, C, 0))
+    workspace = _workspace(workspace, need, h, "the loss")
+    _same_device(h, "h", (w, "w"), (target, "target"), (loss, "loss"), (lse, "lse"), (workspace, "workspace"),
+                 (dev_err, "dev_err"))
+    _launch(h, lib.tpk_lm_loss, "tpk_lm_loss", _ptr(h), _ptr(w), _ptr(target), _ptr(loss), _ptr(lse), N, V, C,
+            float(scale), _ptr(workspace), workspace.numel() * workspace.element_size(), _ptr(dev_err))
+    return loss, lse
+
+
+def lm_loss_bwd(h, w, target, lse, dloss, scale=1.0, dh=None, dw=None, workspace=None, dev_err=None):
+    """Gradients of sum(dloss * loss) (``tpk_lm_loss_bwd``): h, w, target,
+    scale as given to ``lm_loss``, lse its result, dloss [N] fp32 the weight of
+    each position's loss (e.g. ``sum_to_forwarded`` of per-token weights).
+    Returns (dh [N, C] bf16, dw [V, C] bf16)."""
+    lib = B.load()
+    N, V, C = _loss_args(h, w, target, scale)
+    for t, n in ((lse, "lse"), (dloss, "dloss")):
+        _need(t, torch.float32, n, 1, cuda=False)
+        _shape(t, (N,), n)
+    dh = torch.empty_like(h) if dh is None else dh
+    dw = torch.empty_like(w) if dw is None else dw
+    _need(dh, torch.bfloat16, "dh", 2, cuda=False)
+    _shape(dh, (N, C), "dh")
+    _need(dw, torch.bfloat16, "dw", 2, cuda=False)
+    _shape(dw, (V, C), "dw")
+    if dev_err is not None:
+        _need(dev_err, torch.int32, "dev_err", cuda=False)
+    need = int(lib.tpk_lm_loss_workspace_bytes(N, V, C, 1))
+    workspace = _workspace(workspace, need, h, "the loss's backward")
+    _same_device(h, "h", (w, "w"), (target, "target"), (lse, "lse"), (dloss, "dloss"), (dh, "dh"), (dw, "dw"),
+                 (workspace, "workspace"), (dev_err, "dev_err"))
+    _launch(h, lib.tpk_lm_loss_bwd, "tpk_lm_loss_bwd", _ptr(h), _ptr(w), _ptr(target), _ptr(lse), _ptr(dloss), _ptr(dh),
+            _ptr(dw), N, V, C, float(scale), _ptr(workspace), workspace.numel() * workspace.element_size(),
+            _ptr(dev_err))
+    return dh, dw
