@@ -567,8 +567,8 @@ int tpk_embed(const void* table, int32_t table_type, const int32_t* tokens, void
  * nothing.
  *   dout [N, C] bf16;  dtable [V, C] bf16 or fp32 (table_type), overwritten
  *   workspace: >= tpk_embed_bwd_workspace_bytes bytes, 256-byte aligned, need
- *   not be cleared (the sorted positions, and one fp32 row per side of every
- *   64 of them). */
+ *   not be cleared (the sorted positions, and two fp32 rows for every 64 of
+ *   them, or every 16 below 16,384). */
 size_t tpk_embed_bwd_workspace_bytes(int64_t N, int64_t V, int32_t C);
 int tpk_embed_bwd(const int32_t* tokens, const void* dout, void* dtable, int32_t table_type, int64_t N, int64_t V,
                   int32_t C, float scale, void* workspace, size_t ws_bytes, void* stream);

@@ -17,7 +17,10 @@
 // kernel adds the groups in order (deterministic).
 #include <cuda_bf16.h>
 
+#include <type_traits>
+
 #include "common.cuh"
+#include "ptx.cuh"
 
 namespace tpk {
 namespace {
@@ -42,7 +45,58 @@ __device__ __forceinline__ void load8(const float* p, float (&f)[8]) {
   f[0] = a.x; f[1] = a.y; f[2] = a.z; f[3] = a.w;
   f[4] = b.x; f[5] = b.y; f[6] = b.z; f[7] = b.w;
 }
-__device__ __forceinline__ float sigmoid(float g) { return 1.f / (1.f + __expf(-g)); }
+// 1 / (1 + e^-g) from the hardware's 2^x and reciprocal (each within about
+// one ulp; e^-g = inf gives 0): relative error a few 2^-23 plus |g| 2^-24.
+__device__ __forceinline__ float sigmoid(float g) {
+  float r;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.f + ptx::ex2(g * -1.4426950408889634f)));
+  return r;
+}
+// 8 channels as four packed fp32 pairs: the backward does some 50 operations
+// per channel, and pairs halve the instructions (measured below).
+struct Oct {
+  uint64_t v[4];
+};
+__device__ __forceinline__ uint64_t pair_of(uint32_t u) {
+  return ptx::f2(__uint_as_float(u << 16), __uint_as_float(u & 0xFFFF0000u));
+}
+__device__ __forceinline__ Oct oct(uint4 u) { return {{pair_of(u.x), pair_of(u.y), pair_of(u.z), pair_of(u.w)}}; }
+__device__ __forceinline__ Oct load_oct(const float* p) {
+  const ulonglong2 a = __ldg(reinterpret_cast<const ulonglong2*>(p)), b = __ldg(reinterpret_cast<const ulonglong2*>(p) + 1);
+  return {{a.x, a.y, b.x, b.y}};
+}
+__device__ __forceinline__ uint32_t pack_pair(uint64_t v) {
+  float a, b;
+  ptx::unf2(v, a, b);
+  return pack2(a, b);
+}
+__device__ __forceinline__ uint4 pack_oct(const Oct& o) {
+  return make_uint4(pack_pair(o.v[0]), pack_pair(o.v[1]), pack_pair(o.v[2]), pack_pair(o.v[3]));
+}
+__device__ __forceinline__ uint64_t both(float a) { return ptx::f2(a, a); }
+__device__ __forceinline__ float add_pair(uint64_t v) {
+  float a, b;
+  ptx::unf2(v, a, b);
+  return a + b;
+}
+__device__ __forceinline__ uint64_t sigmoid2(uint64_t g) {
+  float a, b;
+  ptx::unf2(ptx::mul2(g, both(-1.4426950408889634f)), a, b);
+  ptx::unf2(ptx::add2(ptx::f2(ptx::ex2(a), ptx::ex2(b)), both(1.f)), a, b);
+  asm("rcp.approx.ftz.f32 %0, %0;" : "+f"(a));
+  asm("rcp.approx.ftz.f32 %0, %0;" : "+f"(b));
+  return ptx::f2(a, b);
+}
+
+// 16 bytes from global to this thread's own place in shared memory.
+__device__ __forceinline__ void copy16(uint4* dst, const uint4* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(ptx::smem_addr(dst)), "l"(src) : "memory");
+}
+__device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int kLeft>
+__device__ __forceinline__ void copy_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(kLeft) : "memory");
+}
 
 // Sum of NV values over the kT threads of a group; every thread gets it.  The
 // order is fixed.  r: NV * kT/32 shared floats that no other sum uses until
@@ -89,7 +143,7 @@ struct NormParams {
   uint4* dy;
   uint4* dgate;
   int64_t ld_dy, ld_dgate;
-  float* part;                // [groups][2][C]: dw_post, dw_pre
+  float* part;                // [CTAs][2][C]: dw_post, dw_pre
 };
 
 template <int kT>
@@ -170,177 +224,261 @@ __global__ void __launch_bounds__(kBlockThreads<kT>) block_norm_kernel(const Nor
 //   dres = dr;  d = scale * dr;  dgate = d * u * s * (1 - s), s = sigmoid(gate)
 //   du = d * s;  with yh = y * rstd(y), dm = du * w_post:
 //   dy = rstd(y) * (dm - yh * mean(dm * yh)),              dw_post = sum du * yh
-template <int kT>
-__global__ void __launch_bounds__(kBlockThreads<kT>) block_norm_bwd_kernel(const NormParams p) {
-  constexpr int kGroups = kBlockThreads<kT> / kT;
-  constexpr int kW = kT / 32;
+// A group walks rows a fixed stride apart.  A thread reads the same columns
+// of every row, so it copies its part of the row after next into its own
+// places in shared memory (asynchronously, no barrier) while the group works
+// on the current one: the three sums of a row each need a barrier, and
+// without the copies ahead nothing is in flight meanwhile.
+constexpr int kInputs = 5;   // y, res, gate, dx, dres_out
+
+template <int kT, int kV>
+struct BwdShape {
+  static constexpr int kGroups = kT < 256 ? 256 / kT : 1;
+  static constexpr int kBlock = kGroups * kT;
+  static constexpr int kMinBlocks = kBlock * kV <= 256 ? 3 : kBlock * kV <= 512 ? 2 : 1;
+  static constexpr int kAhead = kV <= 2 ? 2 : 1;   // rows copied ahead (as shared memory allows)
+  // the weights of a thread's columns stay in shared memory too: next to the
+  // rows they leave the L1 cache too small to hold them (re-read from L2 for
+  // every row otherwise); the widest rows have no room
+  static constexpr bool kHoldWeights = kV <= 2;
+  static constexpr size_t kRing = static_cast<size_t>(kAhead) * kInputs * kV * kBlock * 16;
+  static constexpr size_t kSmem = kRing + (kHoldWeights ? static_cast<size_t>(4) * kV * kBlock * 16 : 0);
+};
+
+template <int kT, int kV>
+__global__ void __launch_bounds__(BwdShape<kT, kV>::kBlock, BwdShape<kT, kV>::kMinBlocks)
+    block_norm_bwd_kernel(const NormParams p) {
+  using Shape = BwdShape<kT, kV>;
+  constexpr int kW = kT / 32, kBlock = Shape::kBlock, kGroups = Shape::kGroups, kAhead = Shape::kAhead;
+  extern __shared__ uint4 ring[];          // [kAhead][kInputs][kV][kBlock]
   __shared__ float red[kGroups][6 * kW];   // sums of y^2, of dm * yh, and of a row's pair, by turns of rows
   const int group = threadIdx.x / kT, t = threadIdx.x % kT;
   const int64_t groups = static_cast<int64_t>(gridDim.x) * kGroups;
-  const int64_t gid = static_cast<int64_t>(blockIdx.x) * kGroups + group;
   const int vecs = p.C / 8;
   const float inv_c = 1.f / static_cast<float>(p.C);
-  float acc_post[kVec][8] = {}, acc_pre[kVec][8] = {};
-  int turn = 0;
-  for (int64_t row = gid; row < p.N; row += groups, turn ^= 1) {
-    uint4 rr[kVec], yy[kVec], gg[kVec], dd[kVec], xx[kVec];
+  uint4* mine = ring + threadIdx.x;
+  auto place = [&](int stage, int input, int j) { return mine + ((stage * kInputs + input) * kV + j) * kBlock; };
+  auto fetch = [&](int64_t row, int stage) {
+    if (row < p.N) {
 #pragma unroll
-    for (int j = 0; j < kVec; ++j) {
-      const int c = t + j * kT;
-      rr[j] = yy[j] = gg[j] = dd[j] = xx[j] = make_uint4(0, 0, 0, 0);
-      if (c < vecs) {
-        if (p.y) yy[j] = p.y[row * p.ld_y + c];
-        rr[j] = p.res[row * vecs + c];
-        if (p.gate) gg[j] = p.gate[row * p.ld_gate + c];
-        xx[j] = p.dx[row * vecs + c];
-        if (p.dres_out) dd[j] = p.dres_out[row * vecs + c];
+      for (int j = 0; j < kV; ++j) {
+        const int c = t + j * kT;
+        if (c >= vecs) continue;
+        if (p.y) copy16(place(stage, 0, j), p.y + row * p.ld_y + c);
+        copy16(place(stage, 1, j), p.res + row * vecs + c);
+        if (p.gate) copy16(place(stage, 2, j), p.gate + row * p.ld_gate + c);
+        copy16(place(stage, 3, j), p.dx + row * vecs + c);
+        if (p.dres_out) copy16(place(stage, 4, j), p.dres_out + row * vecs + c);
       }
     }
+    copy_commit();
+  };
+  // [post 0, post 1, pre 0, pre 1][kV][kBlock] pieces of four weights
+  uint4* held = ring + Shape::kRing / 16 + threadIdx.x;
+  if constexpr (Shape::kHoldWeights) {
+#pragma unroll
+    for (int j = 0; j < kV; ++j) {
+      const int c = t + j * kT;
+      if (c >= vecs) continue;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const float* w = i < 2 ? p.w_post : p.w_pre;
+        if (w) held[(i * kV + j) * kBlock] = __ldg(reinterpret_cast<const uint4*>(w + c * 8) + (i & 1));
+      }
+    }
+  }
+  auto weights = [&](bool pre, int j) -> Oct {
+    if constexpr (Shape::kHoldWeights) {
+      const ulonglong2 a = ptx::lds128u(held + ((2 * pre) * kV + j) * kBlock);
+      const ulonglong2 b = ptx::lds128u(held + ((2 * pre + 1) * kV + j) * kBlock);
+      return {{a.x, a.y, b.x, b.y}};
+    } else {
+      return load_oct((pre ? p.w_pre : p.w_post) + (t + j * kT) * 8);
+    }
+  };
+  Oct acc_post[kV] = {}, acc_pre[kV] = {};
+  int stage = 0, turn = 0;
+  const int64_t first = static_cast<int64_t>(blockIdx.x) * kGroups + group;
+  for (int i = 0; i < kAhead; ++i) fetch(first + i * groups, i);
+  for (int64_t row = first; row < p.N; row += groups, stage = (stage + 1) % kAhead, turn ^= 1) {
+    copy_wait<kAhead - 1>();
     float rstd_y = 1.f;
     if (p.w_post) {
-      float ss[1] = {0.f};
+      uint64_t q = 0;
 #pragma unroll
-      for (int j = 0; j < kVec; ++j) {
-        float a[8];
-        unpack8(yy[j], a);
+      for (int j = 0; j < kV; ++j) {
+        if (t + j * kT >= vecs) continue;
+        const Oct y = oct(*place(stage, 0, j));
 #pragma unroll
-        for (int e = 0; e < 8; ++e) ss[0] = fmaf(a[e], a[e], ss[0]);
+        for (int e = 0; e < 4; ++e) q = ptx::fma2(y.v[e], y.v[e], q);
       }
+      float ss[1] = {add_pair(q)};
       group_sum<kT, 1>(ss, red[group], group, t);
       rstd_y = rsqrtf(ss[0] * inv_c + p.eps);
     }
-    float r[kVec][8];
-    float s2[2] = {0.f, 0.f};   // sum r^2, sum dn * r
+    Oct r[kV], sig[kV];
+    uint64_t q0 = 0, q1 = 0;   // sum r^2, sum dn * r
 #pragma unroll
-    for (int j = 0; j < kVec; ++j) {
+    for (int j = 0; j < kV; ++j) {
       const int c = t + j * kT;
-      unpack8(rr[j], r[j]);
       if (c >= vecs) continue;
-      float a[8], w[8];
+      r[j] = oct(*place(stage, 1, j));
       if (p.y) {
-        unpack8(yy[j], a);
+        Oct u = oct(*place(stage, 0, j));
         if (p.w_post) {
-          load8(p.w_post + c * 8, w);
+          const Oct w = weights(false, j);
 #pragma unroll
-          for (int e = 0; e < 8; ++e) a[e] = a[e] * rstd_y * w[e];
+          for (int e = 0; e < 4; ++e) u.v[e] = ptx::mul2(ptx::mul2(u.v[e], both(rstd_y)), w.v[e]);
         }
         if (p.gate) {
-          unpack8(gg[j], w);
+          const Oct g = oct(*place(stage, 2, j));
 #pragma unroll
-          for (int e = 0; e < 8; ++e) a[e] *= sigmoid(w[e]);
+          for (int e = 0; e < 4; ++e) {
+            sig[j].v[e] = sigmoid2(g.v[e]);
+            u.v[e] = ptx::mul2(u.v[e], sig[j].v[e]);
+          }
         }
 #pragma unroll
-        for (int e = 0; e < 8; ++e) r[j][e] = fmaf(p.scale, a[e], r[j][e]);
+        for (int e = 0; e < 4; ++e) r[j].v[e] = ptx::fma2(both(p.scale), u.v[e], r[j].v[e]);
       }
-      load8(p.w_pre + c * 8, w);
-      unpack8(xx[j], a);
+      const Oct w = weights(true, j), x = oct(*place(stage, 3, j));
 #pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        s2[0] = fmaf(r[j][e], r[j][e], s2[0]);
-        s2[1] = fmaf(a[e] * w[e], r[j][e], s2[1]);
+      for (int e = 0; e < 4; ++e) {
+        q0 = ptx::fma2(r[j].v[e], r[j].v[e], q0);
+        q1 = ptx::fma2(ptx::mul2(x.v[e], w.v[e]), r[j].v[e], q1);
       }
     }
+    float s2[2] = {add_pair(q0), add_pair(q1)};
     group_sum<kT, 2>(s2, red[group] + (2 + 2 * turn) * kW, group, t);
     const float rstd = rsqrtf(s2[0] * inv_c + p.eps);
     const float mean_r = s2[1] * inv_c * rstd;   // mean(dn * rh)
-    float dm[kVec][8];                           // dm = du * w_post (du without w_post)
-    float s1[1] = {0.f};
+    uint64_t q2 = 0;                             // sum dm * yh
 #pragma unroll
-    for (int j = 0; j < kVec; ++j) {
+    for (int j = 0; j < kV; ++j) {
       const int c = t + j * kT;
       if (c >= vecs) continue;
-      float w[8], x[8], d[8];
-      load8(p.w_pre + c * 8, w);
-      unpack8(xx[j], x);
-      unpack8(dd[j], d);
+      Oct d = {};
+      if (p.dres_out) d = oct(*place(stage, 4, j));
+      {
+        const Oct w = weights(true, j), x = oct(*place(stage, 3, j));
 #pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        const float rh = r[j][e] * rstd;
-        acc_pre[j][e] = fmaf(x[e], rh, acc_pre[j][e]);
-        d[e] += rstd * (x[e] * w[e] - rh * mean_r);
+        for (int e = 0; e < 4; ++e) {
+          const uint64_t rh = ptx::mul2(r[j].v[e], both(rstd));
+          acc_pre[j].v[e] = ptx::fma2(x.v[e], rh, acc_pre[j].v[e]);
+          const uint64_t m = ptx::fma2(rh, both(-mean_r), ptx::mul2(x.v[e], w.v[e]));
+          d.v[e] = ptx::fma2(m, both(rstd), d.v[e]);
+        }
       }
-      p.dres[row * vecs + c] = pack8(d);
+      p.dres[row * vecs + c] = pack_oct(d);
       if (!p.y) continue;
-      float a[8], u[8];
-      unpack8(yy[j], a);
-      if (p.w_post) load8(p.w_post + c * 8, w);
+      Oct yh = oct(*place(stage, 0, j));
+      Oct w = {};
+      if (p.w_post) w = weights(false, j);
 #pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        d[e] *= p.scale;
-        a[e] *= rstd_y;                          // yh (y itself without w_post)
-        u[e] = p.w_post ? a[e] * w[e] : a[e];
+      for (int e = 0; e < 4; ++e) {
+        d.v[e] = ptx::mul2(d.v[e], both(p.scale));
+        yh.v[e] = ptx::mul2(yh.v[e], both(rstd_y));   // y itself without w_post
       }
       if (p.gate) {
-        float g[8];
-        unpack8(gg[j], g);
+        Oct g;
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          const float s = sigmoid(g[e]);
-          g[e] = d[e] * u[e] * s * (1.f - s);
-          d[e] *= s;
+        for (int e = 0; e < 4; ++e) {
+          const uint64_t s = sig[j].v[e], u = p.w_post ? ptx::mul2(yh.v[e], w.v[e]) : yh.v[e];
+          d.v[e] = ptx::mul2(d.v[e], s);
+          g.v[e] = ptx::mul2(ptx::mul2(d.v[e], u), ptx::fma2(s, both(-1.f), both(1.f)));
         }
-        p.dgate[row * p.ld_dgate + c] = pack8(g);
+        p.dgate[row * p.ld_dgate + c] = pack_oct(g);
       }
+      // from here r holds dm = du * w_post (du without w_post)
 #pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        acc_post[j][e] = fmaf(d[e], a[e], acc_post[j][e]);
-        dm[j][e] = p.w_post ? d[e] * w[e] : d[e];
-        s1[0] = fmaf(dm[j][e], a[e], s1[0]);
+      for (int e = 0; e < 4; ++e) {
+        acc_post[j].v[e] = ptx::fma2(d.v[e], yh.v[e], acc_post[j].v[e]);
+        r[j].v[e] = p.w_post ? ptx::mul2(d.v[e], w.v[e]) : d.v[e];
+        q2 = ptx::fma2(r[j].v[e], yh.v[e], q2);
       }
     }
-    if (!p.y) continue;
-    float mean_y = 0.f;
-    if (p.w_post) {
-      group_sum<kT, 1>(s1, red[group] + kW, group, t);
-      mean_y = s1[0] * inv_c;
-    }
+    if (p.y) {
+      float mean_y = 0.f;
+      if (p.w_post) {
+        float s1[1] = {add_pair(q2)};
+        group_sum<kT, 1>(s1, red[group] + kW, group, t);
+        mean_y = s1[0] * inv_c;
+      }
 #pragma unroll
-    for (int j = 0; j < kVec; ++j) {
+      for (int j = 0; j < kV; ++j) {
+        const int c = t + j * kT;
+        if (c >= vecs) continue;
+        if (p.w_post) {
+          const Oct y = oct(*place(stage, 0, j));
+          const float k = -rstd_y * mean_y;
+#pragma unroll
+          for (int e = 0; e < 4; ++e) r[j].v[e] = ptx::mul2(ptx::fma2(y.v[e], both(k), r[j].v[e]), both(rstd_y));
+        }
+        p.dy[row * p.ld_dy + c] = pack_oct(r[j]);
+      }
+    }
+    fetch(row + kAhead * groups, stage);   // this thread has read its places of the stage
+  }
+  copy_wait<0>();
+  // one partial row per CTA: its groups' sums added in order
+  const int64_t width = 2 * static_cast<int64_t>(p.C);
+  float* part = p.part + blockIdx.x * width;
+  if constexpr (kGroups > 1) {
+    float* sums = reinterpret_cast<float*>(ring);   // [kGroups][2][kT * kV * 8]
+    constexpr int kRow = kT * kV * 8;
+    static_assert(static_cast<size_t>(kGroups) * 2 * kRow * 4 <= Shape::kRing, "sums fit the ring");
+    __syncthreads();
+#pragma unroll
+    for (int j = 0; j < kV; ++j)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const int at = (t + j * kT) * 8 + 2 * e;
+        *reinterpret_cast<uint64_t*>(sums + (group * 2) * kRow + at) = acc_post[j].v[e];
+        *reinterpret_cast<uint64_t*>(sums + (group * 2 + 1) * kRow + at) = acc_pre[j].v[e];
+      }
+    __syncthreads();
+    for (int i = threadIdx.x; i < 2 * p.C; i += kBlock) {
+      const int which = i >= p.C, c = i - which * p.C;
+      float s = 0.f;
+#pragma unroll
+      for (int g = 0; g < kGroups; ++g) s += sums[(g * 2 + which) * kRow + c];
+      part[i] = s;
+    }
+  } else {
+#pragma unroll
+    for (int j = 0; j < kV; ++j) {
       const int c = t + j * kT;
       if (c >= vecs) continue;
-      if (p.w_post) {
-        float a[8];
-        unpack8(yy[j], a);
-#pragma unroll
-        for (int e = 0; e < 8; ++e) dm[j][e] = rstd_y * (dm[j][e] - a[e] * rstd_y * mean_y);
-      }
-      p.dy[row * p.ld_dy + c] = pack8(dm[j]);
+      ulonglong2* d = reinterpret_cast<ulonglong2*>(part + c * 8);
+      d[0] = make_ulonglong2(acc_post[j].v[0], acc_post[j].v[1]);
+      d[1] = make_ulonglong2(acc_post[j].v[2], acc_post[j].v[3]);
+      d = reinterpret_cast<ulonglong2*>(part + p.C + c * 8);
+      d[0] = make_ulonglong2(acc_pre[j].v[0], acc_pre[j].v[1]);
+      d[1] = make_ulonglong2(acc_pre[j].v[2], acc_pre[j].v[3]);
     }
-  }
-#pragma unroll
-  for (int j = 0; j < kVec; ++j) {
-    const int c = t + j * kT;
-    if (c >= vecs) continue;
-    float4* d = reinterpret_cast<float4*>(p.part + (gid * 2) * p.C + c * 8);
-    d[0] = make_float4(acc_post[j][0], acc_post[j][1], acc_post[j][2], acc_post[j][3]);
-    d[1] = make_float4(acc_post[j][4], acc_post[j][5], acc_post[j][6], acc_post[j][7]);
-    d = reinterpret_cast<float4*>(p.part + (gid * 2 + 1) * p.C + c * 8);
-    d[0] = make_float4(acc_pre[j][0], acc_pre[j][1], acc_pre[j][2], acc_pre[j][3]);
-    d[1] = make_float4(acc_pre[j][4], acc_pre[j][5], acc_pre[j][6], acc_pre[j][7]);
   }
 }
 
-// dw[c] = sum over the groups' partials, 8 warps over the groups and 32
-// columns per block, combined in a fixed order.
-__global__ void __launch_bounds__(256) norm_dw_kernel(const float* __restrict__ part, int64_t groups, int C,
-                                                      float* __restrict__ dw_post, float* __restrict__ dw_pre) {
-  __shared__ float sm[8][32];
+// dw[c] = sum over the CTAs' partials: 32 columns per block, 32 warps over the
+// partials, combined in a fixed order.
+__global__ void __launch_bounds__(1024) norm_dw_kernel(const float* __restrict__ part, int parts, int C,
+                                                       float* __restrict__ dw_post, float* __restrict__ dw_pre) {
+  __shared__ float sm[32][33];
   const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
   const int c = blockIdx.x * 32 + lane;
   float* out = blockIdx.y ? dw_pre : dw_post;
   if (!out) return;
   float s = 0.f;
   if (c < C) {
-#pragma unroll 8
-    for (int64_t g = w; g < groups; g += 8) s += __ldg(part + (g * 2 + blockIdx.y) * C + c);
+#pragma unroll 4
+    for (int g = w; g < parts; g += 32) s += __ldg(part + (static_cast<int64_t>(g) * 2 + blockIdx.y) * C + c);
   }
   sm[w][lane] = s;
   __syncthreads();
-  if (w == 0 && c < C) {
+  s = sm[lane][w];   // column w of the block, partial sum `lane`
 #pragma unroll
-    for (int i = 1; i < 8; ++i) s += sm[i][lane];
-    out[c] = s;
-  }
+  for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+  if (lane == 0 && blockIdx.x * 32 + w < C) out[blockIdx.x * 32 + w] = s;
 }
 
 constexpr int kMaxC = 16384;
@@ -352,23 +490,26 @@ int threads_for(int C) {
   return t;
 }
 
-// Groups of the backward: enough CTAs to fill the SMs, no more than rows.
-template <int kT>
-int64_t bwd_blocks(int64_t N, int sms) {
-  constexpr int kGroups = kBlockThreads<kT> / kT;
-  const int64_t want = (N + kGroups - 1) / kGroups;
-  const int64_t most = int64_t{sms} * (kT >= 1024 ? 1 : 2);
-  return want < most ? want : most;
+// The backward's shapes by width: threads per row and 16-byte pieces per thread.
+template <typename F>
+auto bwd_shape(int C, F f) {
+  const int vecs = C / 8;
+  if (vecs <= 32) return f(BwdShape<32, 1>{}, std::integral_constant<int, 32>{}, std::integral_constant<int, 1>{});
+  if (vecs <= 64) return f(BwdShape<64, 1>{}, std::integral_constant<int, 64>{}, std::integral_constant<int, 1>{});
+  if (vecs <= 128) return f(BwdShape<128, 1>{}, std::integral_constant<int, 128>{}, std::integral_constant<int, 1>{});
+  if (vecs <= 256) return f(BwdShape<256, 1>{}, std::integral_constant<int, 256>{}, std::integral_constant<int, 1>{});
+  if (vecs <= 512) return f(BwdShape<256, 2>{}, std::integral_constant<int, 256>{}, std::integral_constant<int, 2>{});
+  if (vecs <= 1024) return f(BwdShape<512, 2>{}, std::integral_constant<int, 512>{}, std::integral_constant<int, 2>{});
+  return f(BwdShape<512, 4>{}, std::integral_constant<int, 512>{}, std::integral_constant<int, 4>{});
 }
-int64_t bwd_groups(int64_t N, int C, int sms) {
-  switch (threads_for(C)) {
-    case 32: return bwd_blocks<32>(N, sms) * 8;
-    case 64: return bwd_blocks<64>(N, sms) * 4;
-    case 128: return bwd_blocks<128>(N, sms) * 2;
-    case 256: return bwd_blocks<256>(N, sms);
-    case 512: return bwd_blocks<512>(N, sms);
-    default: return bwd_blocks<1024>(N, sms);
-  }
+
+// CTAs of the backward: as many as run together, no more than the rows need.
+template <typename Shape>
+int64_t bwd_blocks(int64_t N, int sms) {
+  const int64_t want = (N + Shape::kGroups - 1) / Shape::kGroups;
+  const int64_t fit = 228 * 1024 / static_cast<int64_t>(Shape::kSmem + 2048);   // 1 KB reserved per CTA, 1 KB static
+  const int64_t most = int64_t{sms} * (fit < Shape::kMinBlocks ? fit : Shape::kMinBlocks);
+  return want < most ? want : most;
 }
 
 template <int kT>
@@ -378,12 +519,6 @@ int launch_fwd(const NormParams& p, cudaStream_t s) {
   block_norm_kernel<kT><<<static_cast<unsigned>(blocks), kBlockThreads<kT>, 0, s>>>(p);
   return cuda_status(cudaGetLastError());
 }
-template <int kT>
-int launch_bwd(const NormParams& p, int sms, cudaStream_t s) {
-  block_norm_bwd_kernel<kT><<<static_cast<unsigned>(bwd_blocks<kT>(p.N, sms)), kBlockThreads<kT>, 0, s>>>(p);
-  return cuda_status(cudaGetLastError());
-}
-
 bool rows_ok(const void* p, int64_t ld, int32_t C) {
   return reinterpret_cast<uintptr_t>(p) % 16 == 0 && (!p || (ld >= C && ld % 8 == 0));
 }
@@ -438,12 +573,13 @@ extern "C" int tpk_block_norm(const void* res, const void* y, int64_t ld_y, cons
   }
 }
 
-// The partials of dw: the widest grid any device of this kind gets (the
-// groups actually launched are counted on the device at hand, never more).
+// The partials of dw, one per CTA of the widest grid any device gets.
 extern "C" size_t tpk_block_norm_bwd_workspace_bytes(int64_t N, int32_t C) {
   using namespace tpk;
   if (N < 0 || C < 8 || C % 8 || C > kMaxC) return 0;
-  return static_cast<size_t>(bwd_groups(N, C, kMaxSms)) * 2 * static_cast<size_t>(C) * 4;
+  return bwd_shape(C, [&](auto shape, auto, auto) {
+    return static_cast<size_t>(bwd_blocks<decltype(shape)>(N, kMaxSms)) * 2 * static_cast<size_t>(C) * 4;
+  });
 }
 
 extern "C" int tpk_block_norm_bwd(const void* res, const void* y, int64_t ld_y, const void* gate, int64_t ld_gate,
@@ -468,6 +604,7 @@ extern "C" int tpk_block_norm_bwd(const void* res, const void* y, int64_t ld_y, 
   if (st != TPK_OK) return st;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   const int sms = num_sms() < kMaxSms ? num_sms() : kMaxSms;
+  int64_t blocks = 0;
   if (N > 0) {
     NormParams p{};
     p.res = static_cast<const uint4*>(res);
@@ -489,18 +626,19 @@ extern "C" int tpk_block_norm_bwd(const void* res, const void* y, int64_t ld_y, 
     p.ld_dy = ld_dy / 8;
     p.ld_dgate = ld_dgate / 8;
     p.part = static_cast<float*>(workspace);
-    switch (threads_for(C)) {
-      case 32: st = launch_bwd<32>(p, sms, s); break;
-      case 64: st = launch_bwd<64>(p, sms, s); break;
-      case 128: st = launch_bwd<128>(p, sms, s); break;
-      case 256: st = launch_bwd<256>(p, sms, s); break;
-      case 512: st = launch_bwd<512>(p, sms, s); break;
-      default: st = launch_bwd<1024>(p, sms, s); break;
-    }
+    st = bwd_shape(C, [&](auto shape, auto kt, auto kv) {
+      using Shape = decltype(shape);
+      constexpr auto kern = block_norm_bwd_kernel<decltype(kt)::value, decltype(kv)::value>;
+      static PerContext<int> rec;
+      const int e = set_smem_once(rec, kern, Shape::kSmem);
+      if (e != TPK_OK) return e;
+      blocks = bwd_blocks<Shape>(N, sms);
+      kern<<<static_cast<unsigned>(blocks), Shape::kBlock, Shape::kSmem, s>>>(p);
+      return cuda_status(cudaGetLastError());
+    });
     if (st != TPK_OK) return st;
   }
-  const int64_t groups = N > 0 ? bwd_groups(N, C, sms) : 0;
-  norm_dw_kernel<<<dim3((C + 31) / 32, 2), 256, 0, s>>>(static_cast<const float*>(workspace), groups, C, dw_post,
-                                                       dw_pre);
+  norm_dw_kernel<<<dim3((C + 31) / 32, 2), 1024, 0, s>>>(static_cast<const float*>(workspace),
+                                                         static_cast<int>(blocks), C, dw_post, dw_pre);
   return cuda_status(cudaGetLastError());
 }

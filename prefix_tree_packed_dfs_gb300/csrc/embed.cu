@@ -7,8 +7,8 @@
 // Backward: dtable[v] = scale * sum of dout[f] over tokens[f] = v, fp32 sums
 // in ascending f (deterministic, no floating-point atomics).  The ids are
 // sorted with their positions (stable radix sort, hand-written below), the
-// sorted order is cut into pieces of kPiece positions, and a warp adds up the
-// rows of one piece for 256 columns.  A run of equal ids inside a piece is
+// sorted order is cut into pieces of 16 or 64 positions, and a warp adds up
+// the rows of one piece for 256 columns.  A run of equal ids inside a piece is
 // written straight to its row of dtable; a run that crosses pieces leaves one
 // fp32 partial per piece, and a second kernel adds those in order -- so a
 // frequent id (thousands of rows) is spread over as many warps as it has
@@ -79,82 +79,123 @@ __global__ void __launch_bounds__(kThreads) embed_kernel(const void* __restrict_
 }
 
 // ---- backward: stable radix sort of (id, position) ---------------------------
-// Tiles of `per` consecutive positions, one CTA each; a digit has 8 bits.
-// hist[pass][tile][digit] counts the tile's keys.  The first pass's counts
-// come from sort_hist_kernel; every scatter pass counts the next digit of the
-// tile each key lands in (integer atomics: the counts do not depend on their
-// order).  A scatter CTA adds up the counts of all tiles itself, which costs
-// tiles * 1 KB of L2 reads and saves a scan launch.
+// Tiles of kSortThreads * kRounds consecutive positions, one CTA each; a digit
+// has 8 bits.  A warp holds its contiguous run of the tile in registers, 32
+// keys per round, and ranks a key among the warp's earlier keys of the same
+// digit (__match_any_sync and a per-warp count per digit).
+// One tile (N <= 2048): one CTA runs every pass in shared memory.  More: the
+// first pass's counts hist[tile][digit] come from sort_hist_kernel; every
+// scatter pass counts the next digit of the tile each key lands in (integer
+// atomics: the counts do not depend on their order), and a scatter CTA adds
+// up the counts of all tiles itself, which costs tiles * 1 KB of L2 reads and
+// saves a scan launch.
 constexpr int kDigits = 256;
 constexpr int kSortThreads = 512;
 constexpr int kSortWarps = kSortThreads / 32;
-constexpr int kMinTile = 2048;
-constexpr int kMaxTiles = 512;
+constexpr int kFewRounds = 4, kManyRounds = 16;
+constexpr int64_t kFewTiles = 512;   // up to here tiles of kFewRounds
 
 __device__ __forceinline__ int key_of(int tok, int V) { return tok >= 0 && tok < V ? tok : V; }
 
-__global__ void __launch_bounds__(kSortThreads) sort_hist_kernel(const int32_t* __restrict__ tokens, int N, int V,
-                                                                 int per, int passes, int32_t* __restrict__ hist) {
-  __shared__ int h[kDigits];
-  const int tiles = gridDim.x, tile = blockIdx.x;
-  if (threadIdx.x < kDigits) h[threadIdx.x] = 0;
+// Inclusive scan of one value per thread over the first 256 threads (8 warps);
+// every thread of the CTA calls it.
+__device__ __forceinline__ int scan256(int v, int* warp_sums) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int u = __shfl_up_sync(0xffffffffu, v, o);
+    if (lane >= o) v += u;
+  }
+  if (warp < 8 && lane == 31) warp_sums[warp] = v;
   __syncthreads();
-  const int lo = tile * per, hi = min(N, lo + per);
-  for (int i = lo + threadIdx.x; i < hi; i += kSortThreads) atomicAdd(&h[key_of(__ldg(tokens + i), V) & (kDigits - 1)], 1);
-  __syncthreads();
-  if (threadIdx.x < kDigits) {
-    hist[tile * kDigits + threadIdx.x] = h[threadIdx.x];
-    for (int p = 1; p < passes; ++p) hist[(p * tiles + tile) * kDigits + threadIdx.x] = 0;
+  if (warp < 8)
+    for (int w = 0; w < warp; ++w) v += warp_sums[w];
+  return v;
+}
+
+// The warp's keys' ranks among its keys of the same digit; count[d] (the
+// warp's, zeroed) receives how many there are of each.
+template <int kRounds>
+__device__ __forceinline__ void rank_keys(const int (&key)[kRounds], int n, int shift, int* count, int (&rank)[kRounds]) {
+  const int lane = threadIdx.x & 31;
+#pragma unroll
+  for (int r = 0; r < kRounds; ++r) {
+    const bool in = r * 32 + lane < n;
+    const int d = in ? (key[r] >> shift) & (kDigits - 1) : kDigits;
+    const unsigned same = __match_any_sync(0xffffffffu, d);
+    const int before = in ? count[d] : 0;
+    rank[r] = before + __popc(same & ((1u << lane) - 1));
+    __syncwarp();
+    if (in && lane == __ffs(same) - 1) count[d] = before + __popc(same);
+    __syncwarp();
   }
 }
 
+template <int kRounds>
+__global__ void __launch_bounds__(kSortThreads) sort_hist_kernel(const int32_t* __restrict__ tokens, int N, int V,
+                                                                 int passes, int32_t* __restrict__ hist) {
+  __shared__ int h[kDigits];
+  const int tiles = gridDim.x, tile = blockIdx.x;
+  const int64_t lo = static_cast<int64_t>(tile) * (kSortThreads * kRounds);
+  int key[kRounds];
+#pragma unroll
+  for (int r = 0; r < kRounds; ++r) {
+    const int64_t i = lo + r * kSortThreads + threadIdx.x;
+    key[r] = i < N ? key_of(__ldg(tokens + i), V) : -1;
+  }
+  if (threadIdx.x < kDigits) {
+    h[threadIdx.x] = 0;
+    for (int p = 1; p < passes; ++p) hist[(static_cast<int64_t>(p) * tiles + tile) * kDigits + threadIdx.x] = 0;
+  }
+  __syncthreads();
+#pragma unroll
+  for (int r = 0; r < kRounds; ++r)
+    if (key[r] >= 0) atomicAdd(&h[key[r] & (kDigits - 1)], 1);
+  __syncthreads();
+  if (threadIdx.x < kDigits) hist[static_cast<int64_t>(tile) * kDigits + threadIdx.x] = h[threadIdx.x];
+}
+
 // One pass: keys_in (nullptr: the ids themselves, positions 0..N-1) sorted by
-// the 8 bits at `shift`.  per is a multiple of 32 * kSortWarps; a warp ranks
-// its own contiguous run of the tile, 32 keys at a time.
+// the 8 bits at `shift`.
+template <int kRounds>
 __global__ void __launch_bounds__(kSortThreads) sort_scatter_kernel(const int32_t* __restrict__ tokens,
                                                                     const int32_t* __restrict__ keys_in,
                                                                     const int32_t* __restrict__ pos_in, int N, int V,
-                                                                    int per, int shift, const int32_t* __restrict__ hist,
+                                                                    int shift, const int32_t* __restrict__ hist,
                                                                     int32_t* __restrict__ hist_next,
                                                                     int32_t* __restrict__ keys_out,
                                                                     int32_t* __restrict__ pos_out) {
   __shared__ int base[kSortWarps][kDigits];   // counts, then where each warp's keys of a digit go
-  __shared__ int scan[kDigits];
+  __shared__ int warp_sums[8];
+  constexpr int kPer = kSortThreads * kRounds, kRun = 32 * kRounds;
   const int tiles = gridDim.x, tile = blockIdx.x;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  for (int i = threadIdx.x; i < kSortWarps * kDigits; i += kSortThreads) (&base[0][0])[i] = 0;
-  __syncthreads();
-  const int run = per / kSortWarps;
-  const int lo = tile * per + warp * run, hi = min(N, min(tile * per + per, lo + run));
-  for (int i0 = lo; i0 < hi; i0 += 32) {
-    const int i = i0 + lane;
-    const int key = i < hi ? (keys_in ? __ldg(keys_in + i) : key_of(__ldg(tokens + i), V)) : 0;
-    const int d = i < hi ? (key >> shift) & (kDigits - 1) : kDigits;
-    const unsigned same = __match_any_sync(0xffffffffu, d);
-    if (i < hi && lane == __ffs(same) - 1) base[warp][d] += __popc(same);
-    __syncwarp();
+  const int64_t lo = static_cast<int64_t>(tile) * kPer + warp * kRun;
+  const int n = lo >= N ? 0 : static_cast<int>(N - lo < kRun ? N - lo : kRun);   // the warp's keys
+  int key[kRounds], pos[kRounds], rank[kRounds];
+#pragma unroll
+  for (int r = 0; r < kRounds; ++r) {
+    const int64_t i = lo + r * 32 + lane;
+    const bool in = r * 32 + lane < n;
+    key[r] = !in ? 0 : keys_in ? __ldg(keys_in + i) : key_of(__ldg(tokens + i), V);
+    pos[r] = !in ? 0 : pos_in ? __ldg(pos_in + i) : static_cast<int>(i);
   }
-  __syncthreads();
   int before = 0, total = 0;   // this digit's keys in earlier tiles, in all tiles
   if (threadIdx.x < kDigits) {
     const int32_t* hd = hist + threadIdx.x;
-#pragma unroll 8
+#pragma unroll 16
     for (int t = 0; t < tiles; ++t) {
-      const int c = __ldg(hd + t * kDigits);
+      const int c = __ldg(hd + static_cast<int64_t>(t) * kDigits);
       total += c;
       before += t < tile ? c : 0;
     }
-    scan[threadIdx.x] = total;
   }
+  for (int i = threadIdx.x; i < kSortWarps * kDigits; i += kSortThreads) (&base[0][0])[i] = 0;
   __syncthreads();
-  for (int o = 1; o < kDigits; o <<= 1) {
-    const int add = threadIdx.x < kDigits && threadIdx.x >= o ? scan[threadIdx.x - o] : 0;
-    __syncthreads();
-    if (threadIdx.x < kDigits) scan[threadIdx.x] += add;
-    __syncthreads();
-  }
+  rank_keys<kRounds>(key, n, shift, base[warp], rank);
+  int at = scan256(total, warp_sums) - total + before;   // its barrier also ends the ranking
   if (threadIdx.x < kDigits) {
-    int at = scan[threadIdx.x] - total + before;
+#pragma unroll
     for (int w = 0; w < kSortWarps; ++w) {
       const int c = base[w][threadIdx.x];
       base[w][threadIdx.x] = at;
@@ -162,29 +203,82 @@ __global__ void __launch_bounds__(kSortThreads) sort_scatter_kernel(const int32_
     }
   }
   __syncthreads();
-  for (int i0 = lo; i0 < hi; i0 += 32) {
-    const int i = i0 + lane;
-    const bool in = i < hi;
-    const int key = in ? (keys_in ? __ldg(keys_in + i) : key_of(__ldg(tokens + i), V)) : 0;
-    const int d = in ? (key >> shift) & (kDigits - 1) : kDigits;
-    const unsigned same = __match_any_sync(0xffffffffu, d);
-    int to = 0;
-    if (in) to = base[warp][d] + __popc(same & ((1u << lane) - 1));
-    __syncwarp();
-    if (in && lane == __ffs(same) - 1) base[warp][d] += __popc(same);
-    __syncwarp();
-    if (in) {
-      keys_out[to] = key;
-      pos_out[to] = pos_in ? __ldg(pos_in + i) : i;
-      if (hist_next) atomicAdd(hist_next + (to / per) * kDigits + ((key >> (shift + 8)) & (kDigits - 1)), 1);
+#pragma unroll
+  for (int r = 0; r < kRounds; ++r) {
+    if (r * 32 + lane >= n) continue;
+    const int to = base[warp][(key[r] >> shift) & (kDigits - 1)] + rank[r];
+    keys_out[to] = key[r];
+    pos_out[to] = pos[r];
+    if (hist_next)
+      atomicAdd(hist_next + static_cast<int64_t>(to / kPer) * kDigits + ((key[r] >> (shift + 8)) & (kDigits - 1)), 1);
+  }
+}
+
+// Every pass of a single tile, in shared memory.
+__global__ void __launch_bounds__(kSortThreads) sort_one_kernel(const int32_t* __restrict__ tokens, int N, int V,
+                                                                int passes, int32_t* __restrict__ keys_out,
+                                                                int32_t* __restrict__ pos_out) {
+  constexpr int kPer = kSortThreads * kFewRounds, kRun = 32 * kFewRounds;
+  __shared__ int base[kSortWarps][kDigits];
+  __shared__ int warp_sums[8];
+  __shared__ int sk[kPer], sp[kPer];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int lo = warp * kRun;
+  const int n = lo >= N ? 0 : min(N - lo, kRun);
+  int key[kFewRounds], pos[kFewRounds], rank[kFewRounds];
+#pragma unroll
+  for (int r = 0; r < kFewRounds; ++r) {
+    pos[r] = lo + r * 32 + lane;
+    key[r] = r * 32 + lane < n ? key_of(__ldg(tokens + pos[r]), V) : 0;
+  }
+  for (int p = 0; p < passes; ++p) {
+    for (int i = threadIdx.x; i < kSortWarps * kDigits; i += kSortThreads) (&base[0][0])[i] = 0;
+    __syncthreads();
+    rank_keys<kFewRounds>(key, n, 8 * p, base[warp], rank);
+    __syncthreads();
+    int total = 0;
+    if (threadIdx.x < kDigits)
+#pragma unroll
+      for (int w = 0; w < kSortWarps; ++w) total += base[w][threadIdx.x];
+    int at = scan256(total, warp_sums) - total;
+    if (threadIdx.x < kDigits) {
+#pragma unroll
+      for (int w = 0; w < kSortWarps; ++w) {
+        const int c = base[w][threadIdx.x];
+        base[w][threadIdx.x] = at;
+        at += c;
+      }
     }
+    __syncthreads();
+    const bool last = p + 1 == passes;
+#pragma unroll
+    for (int r = 0; r < kFewRounds; ++r) {
+      if (r * 32 + lane >= n) continue;
+      const int to = base[warp][(key[r] >> (8 * p)) & (kDigits - 1)] + rank[r];
+      (last ? keys_out : sk)[to] = key[r];
+      (last ? pos_out : sp)[to] = pos[r];
+    }
+    if (last) return;
+    __syncthreads();
+#pragma unroll
+    for (int r = 0; r < kFewRounds; ++r) {
+      const int i = lo + r * 32 + lane;
+      if (r * 32 + lane < n) {
+        key[r] = sk[i];
+        pos[r] = sp[i];
+      }
+    }
+    __syncthreads();
   }
 }
 
 // ---- backward: sums of runs ---------------------------------------------------
-constexpr int kPiece = 64;        // sorted positions per piece
 constexpr int kCols = 256;        // columns per warp (8 per lane)
-constexpr int kAhead = 8;         // rows in flight per warp
+constexpr int kBatch = 8;         // rows loaded together
+
+// Sorted positions per piece: long pieces leave fewer partials, short ones
+// give a small batch more warps (1,001 rows of 1,000: 16 beats 64).
+__host__ __device__ constexpr int piece_for(int64_t N) { return N >= 16384 ? 64 : 16; }
 
 template <bool kF32>
 __device__ __forceinline__ void store_row8(void* dst, int64_t at, const float (&a)[8], float s) {
@@ -219,7 +313,7 @@ __device__ __forceinline__ int lower_bound_warp(const int32_t* __restrict__ keys
 // Partials: part[(2 * piece + side) * C]: side 0 the piece's first run where
 // it began in an earlier piece, side 1 its last run where it goes on in a
 // later one (a piece that is all one run with both neighbours uses side 0).
-template <bool kF32>
+template <bool kF32, int kPiece>
 __global__ void __launch_bounds__(kThreads) embed_sum_kernel(const int32_t* __restrict__ keys,
                                                              const int32_t* __restrict__ pos,
                                                              const uint4* __restrict__ dout, int N, int V, int C,
@@ -241,114 +335,180 @@ __global__ void __launch_bounds__(kThreads) embed_sum_kernel(const int32_t* __re
     return;
   }
   const int64_t item = static_cast<int64_t>(blockIdx.x) * (kThreads / 32) + (threadIdx.x >> 5);
-  const int piece = static_cast<int>(item / parts);
+  const int64_t piece = item / parts;
   const int c = static_cast<int>(item % parts) * kCols + lane * 8;
-  const int lo = piece * kPiece;
+  const int64_t lo = piece * kPiece;
   if (lo >= N) return;
-  const int hi = min(N, lo + kPiece);
+  const int n = static_cast<int>(N - lo < kPiece ? N - lo : kPiece);
   const int vecs = C / 8;
   const bool col = c < C;
+  // the piece's ids and positions, one per lane and 32 of them
+  constexpr int kHeld = (kPiece + 31) / 32;
+  int hk[kHeld], hp[kHeld];
+#pragma unroll
+  for (int i = 0; i < kHeld; ++i) {
+    const int e = i * 32 + lane;
+    hk[i] = e < n ? __ldg(keys + lo + e) : -2;
+    hp[i] = e < n ? __ldg(pos + lo + e) : 0;
+  }
   const int prev = lo > 0 ? __ldg(keys + lo - 1) : -1;
-  const int next = hi < N ? __ldg(keys + hi) : -1;
-  float acc[8] = {};
-  int cur = __ldg(keys + lo);
-  bool joined = cur == prev;   // the current run began in an earlier piece
-  for (int b = lo; b < hi; b += kAhead) {
-    uint4 x[kAhead];
-    int k[kAhead];
+  const int next = lo + n < N ? __ldg(keys + lo + n) : -1;
+  uint4 x[2][kBatch];
+  auto fetch = [&](int b, uint4 (&to)[kBatch]) {
 #pragma unroll
-    for (int j = 0; j < kAhead; ++j) {
-      k[j] = b + j < hi ? __ldg(keys + b + j) : -2;
-      x[j] = make_uint4(0, 0, 0, 0);
-      if (b + j < hi && k[j] < V && col) x[j] = __ldg(dout + static_cast<int64_t>(__ldg(pos + b + j)) * vecs + c / 8);
+    for (int j = 0; j < kBatch; ++j) {
+      const int e = b + j;   // a constant once unrolled
+      const int k = __shfl_sync(0xffffffffu, hk[e / 32], e % 32), q = __shfl_sync(0xffffffffu, hp[e / 32], e % 32);
+      to[j] = make_uint4(0, 0, 0, 0);
+      if (k >= 0 && k < V && col) to[j] = __ldg(dout + static_cast<int64_t>(q) * vecs + c / 8);
     }
+  };
+  float acc[8] = {};
+  int cur = __shfl_sync(0xffffffffu, hk[0], 0);
+  bool joined = cur == prev;   // the current run began in an earlier piece
+  fetch(0, x[0]);
 #pragma unroll
-    for (int j = 0; j < kAhead; ++j) {
-      if (b + j >= hi) break;
-      if (k[j] != cur) {   // the run `cur` ends here
+  for (int b = 0; b < kPiece; b += kBatch) {
+    uint4(&now)[kBatch] = x[(b / kBatch) & 1];
+    if (b + kBatch < kPiece) fetch(b + kBatch, x[(b / kBatch + 1) & 1]);
+#pragma unroll
+    for (int j = 0; j < kBatch; ++j) {
+      const int e = b + j;
+      const int k = __shfl_sync(0xffffffffu, hk[e / 32], e % 32);
+      if (e < n && k != cur) {   // the run `cur` ends here
         if (col && cur < V) {
           if (joined)
-            store_row8<true>(part, (2ll * piece) * C + c, acc, 1.f);
+            store_row8<true>(part, (2 * piece) * C + c, acc, 1.f);
           else
             store_row8<kF32>(dtable, static_cast<int64_t>(cur) * C + c, acc, scale);
         }
 #pragma unroll
-        for (int e = 0; e < 8; ++e) acc[e] = 0.f;
-        cur = k[j];
+        for (int i = 0; i < 8; ++i) acc[i] = 0.f;
+        cur = k;
         joined = false;
       }
-      acc[0] += lo16(x[j].x); acc[1] += hi16(x[j].x);
-      acc[2] += lo16(x[j].y); acc[3] += hi16(x[j].y);
-      acc[4] += lo16(x[j].z); acc[5] += hi16(x[j].z);
-      acc[6] += lo16(x[j].w); acc[7] += hi16(x[j].w);
+      acc[0] += lo16(now[j].x); acc[1] += hi16(now[j].x);
+      acc[2] += lo16(now[j].y); acc[3] += hi16(now[j].y);
+      acc[4] += lo16(now[j].z); acc[5] += hi16(now[j].z);
+      acc[6] += lo16(now[j].w); acc[7] += hi16(now[j].w);
     }
   }
   if (col && cur < V) {
     if (joined)
-      store_row8<true>(part, (2ll * piece) * C + c, acc, 1.f);
+      store_row8<true>(part, (2 * piece) * C + c, acc, 1.f);
     else if (cur == next)
-      store_row8<true>(part, (2ll * piece + 1) * C + c, acc, 1.f);
+      store_row8<true>(part, (2 * piece + 1) * C + c, acc, 1.f);
     else
       store_row8<kF32>(dtable, static_cast<int64_t>(cur) * C + c, acc, scale);
   }
 }
 
-// A run that crosses pieces: its first piece's warp adds side 1 of that piece
-// and side 0 of the following ones, in order.
-template <bool kF32>
+// A run that crosses pieces: a warp of its first piece adds side 1 of that
+// piece and side 0 of the following ones, in order, for 128 columns.  A run
+// of thousands of positions is hundreds of dependent additions, so what
+// counts is the loads in flight: 16 at a time.
+template <bool kF32, int kPiece>
 __global__ void __launch_bounds__(kThreads) embed_join_kernel(const int32_t* __restrict__ keys, int N, int V, int C,
                                                               float scale, void* __restrict__ dtable,
                                                               const float* __restrict__ part) {
   const int lane = threadIdx.x & 31;
-  const int parts = (C + kCols - 1) / kCols;
+  const int parts = (C + 127) / 128;
   const int64_t item = static_cast<int64_t>(blockIdx.x) * (kThreads / 32) + (threadIdx.x >> 5);
-  const int piece = static_cast<int>(item / parts);
-  const int c = static_cast<int>(item % parts) * kCols + lane * 8;
-  const int pieces = (N + kPiece - 1) / kPiece;
-  if (piece >= pieces - 1) return;
-  const int hi = (piece + 1) * kPiece;
-  const int key = __ldg(keys + hi - 1);
-  if (key >= V || __ldg(keys + hi) != key) return;
-  const int lo = piece * kPiece;
-  // the run began before this piece: an earlier piece owns it
-  if (lo > 0 && __ldg(keys + lo) == key && __ldg(keys + lo - 1) == key) return;
+  const int64_t piece = item / parts;
+  const int c = static_cast<int>(item % parts) * 128 + lane * 4;
+  const int64_t lo = piece * kPiece, hi = lo + kPiece;
+  if (hi >= N) return;
+  const int key = __ldg(keys + hi - 1), next = __ldg(keys + hi);
+  const int begin = __ldg(keys + lo), prev = lo > 0 ? __ldg(keys + lo - 1) : -1;
+  if (key >= V || next != key) return;
+  if (begin == key && prev == key) return;   // the run began earlier: an earlier piece adds it up
   const int end = lower_bound_warp(keys, N, key + 1);   // one past the run
-  const int last = (end - 1) / kPiece;
+  const int64_t last = (end - 1) / kPiece;
   if (c >= C) return;
-  float acc[8];
-  {
-    const float4* s = reinterpret_cast<const float4*>(part + (2ll * piece + 1) * C + c);
-    const float4 a = s[0], b = s[1];
-    acc[0] = a.x; acc[1] = a.y; acc[2] = a.z; acc[3] = a.w;
-    acc[4] = b.x; acc[5] = b.y; acc[6] = b.z; acc[7] = b.w;
+  float4 acc = *reinterpret_cast<const float4*>(part + (2 * piece + 1) * C + c);
+  const float* from = part + c;
+  constexpr int kFlight = 16;
+  int64_t p = piece + 1;
+  for (; p + kFlight - 1 <= last; p += kFlight) {
+    float4 v[kFlight];
+#pragma unroll
+    for (int i = 0; i < kFlight; ++i) v[i] = __ldcg(reinterpret_cast<const float4*>(from + (2 * (p + i)) * C));
+#pragma unroll
+    for (int i = 0; i < kFlight; ++i) {
+      acc.x += v[i].x; acc.y += v[i].y; acc.z += v[i].z; acc.w += v[i].w;
+    }
   }
 #pragma unroll 4
-  for (int p = piece + 1; p <= last; ++p) {
-    const float4* s = reinterpret_cast<const float4*>(part + (2ll * p) * C + c);
-    const float4 a = s[0], b = s[1];
-    acc[0] += a.x; acc[1] += a.y; acc[2] += a.z; acc[3] += a.w;
-    acc[4] += b.x; acc[5] += b.y; acc[6] += b.z; acc[7] += b.w;
+  for (; p <= last; ++p) {
+    const float4 v = __ldcg(reinterpret_cast<const float4*>(from + (2 * p) * C));
+    acc.x += v.x; acc.y += v.y; acc.z += v.z; acc.w += v.w;
   }
-  store_row8<kF32>(dtable, static_cast<int64_t>(key) * C + c, acc, scale);
+  const int64_t at = static_cast<int64_t>(key) * C + c;
+  if constexpr (kF32)
+    *reinterpret_cast<float4*>(static_cast<float*>(dtable) + at) =
+        make_float4(acc.x * scale, acc.y * scale, acc.z * scale, acc.w * scale);
+  else
+    *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(dtable) + at) =
+        make_uint2(pack2(acc.x * scale, acc.y * scale), pack2(acc.z * scale, acc.w * scale));
 }
 
 // ---- host ------------------------------------------------------------------------
 struct SortShape {
-  int passes, per, tiles;
+  int passes, rounds;
+  int64_t tiles;
 };
 SortShape sort_shape(int64_t N, int64_t V) {
   SortShape s;
   s.passes = 1;
   while (s.passes < 4 && (V >> (8 * s.passes)) != 0) ++s.passes;   // keys 0..V
-  int64_t per = (N + kMaxTiles - 1) / kMaxTiles;
-  per = per < kMinTile ? kMinTile : per;
-  constexpr int64_t unit = 32 * kSortWarps;
-  s.per = static_cast<int>((per + unit - 1) / unit * unit);
-  s.tiles = static_cast<int>((N + s.per - 1) / s.per);
+  s.rounds = N <= kFewTiles * kSortThreads * kFewRounds ? kFewRounds : kManyRounds;
+  const int64_t per = int64_t{kSortThreads} * s.rounds;
+  s.tiles = (N + per - 1) / per;
   return s;
 }
 
 size_t up256(size_t n) { return (n + 255) / 256 * 256; }
+
+template <int kRounds>
+int sort_tiles(const int32_t* tokens, int n, int v, const SortShape& sh, int32_t* hist, int32_t* const (&buf)[4],
+               const int32_t** keys, const int32_t** pos, cudaStream_t s) {
+  const unsigned tiles = static_cast<unsigned>(sh.tiles);
+  sort_hist_kernel<kRounds><<<tiles, kSortThreads, 0, s>>>(tokens, n, v, sh.passes, hist);
+  int st = cuda_status(cudaGetLastError());
+  const int32_t *ki = nullptr, *pi = nullptr;
+  for (int p = 0; st == TPK_OK && p < sh.passes; ++p) {
+    int32_t* ko = buf[(p & 1) * 2];
+    int32_t* po = buf[(p & 1) * 2 + 1];
+    int32_t* h = hist + static_cast<int64_t>(p) * sh.tiles * kDigits;
+    sort_scatter_kernel<kRounds><<<tiles, kSortThreads, 0, s>>>(
+        tokens, ki, pi, n, v, 8 * p, h, p + 1 < sh.passes ? h + sh.tiles * kDigits : nullptr, ko, po);
+    st = cuda_status(cudaGetLastError());
+    ki = ko;
+    pi = po;
+  }
+  *keys = ki;
+  *pos = pi;
+  return st;
+}
+
+template <bool kF32, int kPiece>
+int sum_runs(const int32_t* keys, const int32_t* pos, const void* dout, int n, int v, int C, float scale, void* dtable,
+             float* part, cudaStream_t s) {
+  const int64_t pieces = (static_cast<int64_t>(n) + kPiece - 1) / kPiece;
+  const int64_t sum_blocks = (pieces * ((C + kCols - 1) / kCols) + kThreads / 32 - 1) / (kThreads / 32);
+  const int64_t join_blocks = (pieces * ((C + 127) / 128) + kThreads / 32 - 1) / (kThreads / 32);
+  int64_t zero_blocks = (static_cast<int64_t>(v) + kThreads / 32 - 1) / (kThreads / 32);
+  const int64_t most = int64_t{num_sms()} * 8;
+  if (zero_blocks > most) zero_blocks = most;
+  if (sum_blocks + zero_blocks > 0x7fffffff || join_blocks > 0x7fffffff) return TPK_E_ARG;
+  embed_sum_kernel<kF32, kPiece><<<static_cast<unsigned>(sum_blocks + zero_blocks), kThreads, 0, s>>>(
+      keys, pos, static_cast<const uint4*>(dout), n, v, C, scale, dtable, part, static_cast<int>(sum_blocks));
+  const int st = cuda_status(cudaGetLastError());
+  if (st != TPK_OK || pieces < 2) return st;
+  embed_join_kernel<kF32, kPiece><<<static_cast<unsigned>(join_blocks), kThreads, 0, s>>>(keys, n, v, C, scale, dtable,
+                                                                                          part);
+  return cuda_status(cudaGetLastError());
+}
 
 bool sizes_ok(int64_t N, int64_t V, int32_t C) {
   return N >= 0 && N < (int64_t{1} << 31) - 8192 && V >= 1 && V < (int64_t{1} << 31) - 1 && C >= 8 && C % 8 == 0 &&
@@ -391,7 +551,8 @@ extern "C" size_t tpk_embed_bwd_workspace_bytes(int64_t N, int64_t V, int32_t C)
   if (!sizes_ok(N, V, C)) return 0;
   const SortShape s = sort_shape(N, V);
   const size_t n = static_cast<size_t>(N);
-  const size_t pieces = (n + kPiece - 1) / kPiece;
+  const size_t piece = static_cast<size_t>(piece_for(N));
+  const size_t pieces = (n + piece - 1) / piece;
   return up256(static_cast<size_t>(s.passes) * s.tiles * kDigits * 4) + 4 * up256(n * 4) +
          up256(pieces * 2 * static_cast<size_t>(C) * 4);
 }
@@ -421,39 +582,19 @@ extern "C" int tpk_embed_bwd(const int32_t* tokens, const void* dout, void* dtab
     w += up256(static_cast<size_t>(N) * 4);
   }
   float* part = reinterpret_cast<float*>(w);
-  sort_hist_kernel<<<sh.tiles, kSortThreads, 0, s>>>(tokens, n, v, sh.per, sh.passes, hist);
-  st = cuda_status(cudaGetLastError());
-  const int32_t *ki = nullptr, *pi = nullptr;
-  for (int p = 0; st == TPK_OK && p < sh.passes; ++p) {
-    int32_t* ko = buf[(p & 1) * 2];
-    int32_t* po = buf[(p & 1) * 2 + 1];
-    int32_t* h = hist + static_cast<int64_t>(p) * sh.tiles * kDigits;
-    sort_scatter_kernel<<<sh.tiles, kSortThreads, 0, s>>>(tokens, ki, pi, n, v, sh.per, 8 * p, h,
-                                                          p + 1 < sh.passes ? h + sh.tiles * kDigits : nullptr, ko, po);
+  const int32_t *ki = buf[0], *pi = buf[1];
+  if (sh.tiles == 1) {
+    sort_one_kernel<<<1, kSortThreads, 0, s>>>(tokens, n, v, sh.passes, buf[0], buf[1]);
     st = cuda_status(cudaGetLastError());
-    ki = ko;
-    pi = po;
+  } else {
+    st = sh.rounds == kFewRounds ? sort_tiles<kFewRounds>(tokens, n, v, sh, hist, buf, &ki, &pi, s)
+                                 : sort_tiles<kManyRounds>(tokens, n, v, sh, hist, buf, &ki, &pi, s);
   }
   if (st != TPK_OK) return st;
-  const int64_t pieces = (N + kPiece - 1) / kPiece;
-  const int parts = (C + kCols - 1) / kCols;
-  const int64_t sum_blocks = (pieces * parts + kThreads / 32 - 1) / (kThreads / 32);
-  int64_t zero_blocks = (V + kThreads / 32 - 1) / (kThreads / 32);
-  const int64_t most = int64_t{num_sms()} * 8;
-  if (zero_blocks > most) zero_blocks = most;
-  if (sum_blocks + zero_blocks > 0x7fffffff) return TPK_E_ARG;
-  const unsigned grid = static_cast<unsigned>(sum_blocks + zero_blocks);
+  const bool few = piece_for(N) == 16;
   if (f32)
-    embed_sum_kernel<true><<<grid, kThreads, 0, s>>>(ki, pi, static_cast<const uint4*>(dout), n, v, C, scale, dtable,
-                                                     part, static_cast<int>(sum_blocks));
-  else
-    embed_sum_kernel<false><<<grid, kThreads, 0, s>>>(ki, pi, static_cast<const uint4*>(dout), n, v, C, scale, dtable,
-                                                      part, static_cast<int>(sum_blocks));
-  st = cuda_status(cudaGetLastError());
-  if (st != TPK_OK || pieces < 2) return st;
-  if (f32)
-    embed_join_kernel<true><<<static_cast<unsigned>(sum_blocks), kThreads, 0, s>>>(ki, n, v, C, scale, dtable, part);
-  else
-    embed_join_kernel<false><<<static_cast<unsigned>(sum_blocks), kThreads, 0, s>>>(ki, n, v, C, scale, dtable, part);
-  return cuda_status(cudaGetLastError());
+    return few ? sum_runs<true, 16>(ki, pi, dout, n, v, C, scale, dtable, part, s)
+               : sum_runs<true, 64>(ki, pi, dout, n, v, C, scale, dtable, part, s);
+  return few ? sum_runs<false, 16>(ki, pi, dout, n, v, C, scale, dtable, part, s)
+             : sum_runs<false, 64>(ki, pi, dout, n, v, C, scale, dtable, part, s);
 }

@@ -62,8 +62,8 @@ struct LmParams {
   const float* lse;
   const float* dloss;
   float scale, scale_log2;
-  float2* part;             // kFwd: [2 * chunks][np]
-  float* zt;                // kFwd: [np] the target's score, log2 units
+  float2* part;             // kFwd: [2 * chunks][np] (maximum score, sum of exponentials), scores unscaled
+  float* zt;                // kFwd: [np] the target's score, unscaled
   int32_t run;              // kFwd: vocabulary tiles per unit
   int32_t v0, vcols, ld_dz; // the piece: first id, ids, row stride of dz
   __nv_bfloat16* dz;
@@ -322,12 +322,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           }
           const int c0 = n0 + c * 32;
           if constexpr (kMode == kFwd) {
+            // unscaled scores and their maximum: the differences are exact to
+            // a rounding, which products with the scale would not leave them
             float t[32];
             float top = -INFINITY;
 #pragma unroll
             for (int e = 0; e < 32; ++e) {
-              t[e] = __uint_as_float(raw[e]) * p.scale_log2;
-              if (c0 + e >= p.V) t[e] = -INFINITY;
+              t[e] = c0 + e < p.V ? __uint_as_float(raw[e]) : -INFINITY;
               top = fmaxf(top, t[e]);
             }
             if (static_cast<uint32_t>(tgt - c0) < 32u) {
@@ -337,9 +338,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             }
             const float mn = fmaxf(m, top);
             const float ms = mn == -INFINITY ? 0.f : mn;
-            s *= ptx::ex2(m - ms);
+            float q[4] = {s * ptx::ex2((m - ms) * p.scale_log2), 0.f, 0.f, 0.f};
 #pragma unroll
-            for (int e = 0; e < 32; ++e) s += ptx::ex2(t[e] - ms);
+            for (int e = 0; e < 32; ++e) q[e & 3] += ptx::ex2((t[e] - ms) * p.scale_log2);
+            s = (q[0] + q[1]) + (q[2] + q[3]);
             m = mn;
           } else if constexpr (kMode == kDz) {
             if (c0 < p.ld_dz) {
@@ -432,7 +434,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 // CTA: a few microseconds per 10,000 positions, against milliseconds of
 // products for as many.
 constexpr int kIndexThreads = 1024;
-constexpr int kIndexPer = 4;
+constexpr int kIndexPer = 16;
 
 __global__ void __launch_bounds__(kIndexThreads) lm_index_kernel(const int32_t* __restrict__ target, int N, int V,
                                                                  int32_t* __restrict__ rows, int32_t* __restrict__ pos,
@@ -493,49 +495,139 @@ __global__ void __launch_bounds__(256) lm_gather_kernel(const uint4* __restrict_
   }
 }
 
-// loss and lse of every position: the slots' (maximum, sum) pairs joined, 32
-// rows per CTA, 8 warps over the slots.
+// (maximum, sum of exponentials of scale * (score - maximum)) of two sets of scores.
+__device__ __forceinline__ float2 merge(float2 a, float2 b, float scale_log2) {
+  const float m = fmaxf(a.x, b.x);
+  const float ms = m == -INFINITY ? 0.f : m;
+  return make_float2(m, a.y * exp2f((a.x - ms) * scale_log2) + b.y * exp2f((b.x - ms) * scale_log2));
+}
+
+// loss and lse of every position: the slots' pairs merged, kRows rows per CTA
+// and 256 / kRows threads over the slots of each.  Few rows have many slots
+// and few CTAs: 4 rows per CTA there, 32 (coalesced) otherwise.
+template <int kRows>
 __global__ void __launch_bounds__(256) lm_join_kernel(const float2* __restrict__ part, const float* __restrict__ zt,
                                                       const int32_t* __restrict__ pos,
                                                       const int32_t* __restrict__ target, int N, int V, int slots,
-                                                      int64_t np, float* __restrict__ loss, float* __restrict__ lse) {
-  __shared__ float2 sm[8][32];
-  const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
-  const int i = blockIdx.x * 32 + lane;
+                                                      int64_t np, float scale, float scale_log2,
+                                                      float* __restrict__ loss, float* __restrict__ lse) {
+  constexpr int kWays = 256 / kRows;
+  __shared__ float2 sm[kWays][kRows];
+  const int row = threadIdx.x % kRows, w = threadIdx.x / kRows;
+  const int i = blockIdx.x * kRows + row;
   int r = -1;
   if (i < N) {
     const int t = __ldg(target + i);
     if (t >= 0 && t < V) r = pos ? __ldg(pos + i) : i;
   }
-  float m = -INFINITY, s = 0.f;
+  float2 x = make_float2(-INFINITY, 0.f);
   if (r >= 0) {
 #pragma unroll 4
-    for (int k = w; k < slots; k += 8) {
-      const float2 x = __ldg(part + static_cast<int64_t>(k) * np + r);
-      const float mn = fmaxf(m, x.x);
+    for (int k = w; k < slots; k += kWays) x = merge(x, __ldg(part + static_cast<int64_t>(k) * np + r), scale_log2);
+  }
+  sm[w][row] = x;
+  __syncthreads();
+#pragma unroll
+  for (int o = kWays / 2; o > 0; o >>= 1) {
+    if (w < o) sm[w][row] = merge(sm[w][row], sm[w + o][row], scale_log2);
+    __syncthreads();
+  }
+  if (w != 0 || i >= N) return;
+  x = sm[0][row];
+  const float ln_s = logf(x.y);
+  lse[i] = r < 0 ? 0.f : fmaf(x.x, scale, ln_s);
+  loss[i] = r < 0 ? 0.f : fmaf(x.x - zt[r], scale, ln_s);
+}
+
+// ---- a few positions -----------------------------------------------------------
+// Up to kFewRows positions (the log-probability of sampled tokens): one read
+// of w, which is all the time there is; a tile of 256 rows of the tensor path
+// would be almost empty and its 256-column tiles too few to share out evenly.
+// A warp takes four rows of w at a time, 256 channels per step, and keeps the
+// running (maximum, sum) of its rows' scores; the CTA's eight warps merge
+// theirs into one slot.
+constexpr int kFewRows = 4;
+constexpr int kFewMost = 16384;      // fp32 values of h in shared memory
+constexpr int kFewBlocks = 608;      // slots
+constexpr int kFewV = 4;             // rows of w per warp and step
+
+template <int kN>
+__global__ void __launch_bounds__(256) lm_few_kernel(const uint4* __restrict__ h, const uint4* __restrict__ w,
+                                                     const int32_t* __restrict__ target, int N, int V, int C,
+                                                     int64_t np, float scale_log2, float2* __restrict__ part,
+                                                     float* __restrict__ zt) {
+  extern __shared__ float4 hs[];     // [kN][C / 8] pairs of float4
+  __shared__ float2 sm[8][kN];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int vecs = C / 8;
+  for (int i = threadIdx.x; i < kN * vecs; i += 256) {
+    const uint4 x = i / vecs < N ? __ldg(h + i) : make_uint4(0, 0, 0, 0);
+    hs[2 * i] = make_float4(__uint_as_float(x.x << 16), __uint_as_float(x.x & 0xFFFF0000u), __uint_as_float(x.y << 16),
+                            __uint_as_float(x.y & 0xFFFF0000u));
+    hs[2 * i + 1] = make_float4(__uint_as_float(x.z << 16), __uint_as_float(x.z & 0xFFFF0000u),
+                                __uint_as_float(x.w << 16), __uint_as_float(x.w & 0xFFFF0000u));
+  }
+  int tgt[kN];
+  float2 st[kN];
+#pragma unroll
+  for (int n = 0; n < kN; ++n) {
+    tgt[n] = n < N ? __ldg(target + n) : -1;
+    st[n] = make_float2(-INFINITY, 0.f);
+  }
+  __syncthreads();
+  const int64_t step = static_cast<int64_t>(gridDim.x) * 8 * kFewV;
+  for (int64_t v0 = (static_cast<int64_t>(blockIdx.x) * 8 + warp) * kFewV; v0 < V; v0 += step) {
+    uint64_t acc[kFewV][kN] = {};
+#pragma unroll 4
+    for (int c = lane; c < vecs; c += 32) {
+      uint4 x[kFewV];
+#pragma unroll
+      for (int i = 0; i < kFewV; ++i)
+        x[i] = v0 + i < V ? __ldg(w + (v0 + i) * vecs + c) : make_uint4(0, 0, 0, 0);
+#pragma unroll
+      for (int n = 0; n < kN; ++n) {
+        const ulonglong2 a = ptx::lds128u(hs + 2 * (n * vecs + c)), b = ptx::lds128u(hs + 2 * (n * vecs + c) + 1);
+#pragma unroll
+        for (int i = 0; i < kFewV; ++i) {
+          auto pair = [](uint32_t u) { return ptx::f2(__uint_as_float(u << 16), __uint_as_float(u & 0xFFFF0000u)); };
+          acc[i][n] = ptx::fma2(pair(x[i].x), a.x, acc[i][n]);
+          acc[i][n] = ptx::fma2(pair(x[i].y), a.y, acc[i][n]);
+          acc[i][n] = ptx::fma2(pair(x[i].z), b.x, acc[i][n]);
+          acc[i][n] = ptx::fma2(pair(x[i].w), b.y, acc[i][n]);
+        }
+      }
+    }
+#pragma unroll
+    for (int n = 0; n < kN; ++n) {
+      float z[kFewV], top = -INFINITY;
+#pragma unroll
+      for (int i = 0; i < kFewV; ++i) {
+        float lo, hi;
+        ptx::unf2(acc[i][n], lo, hi);
+        z[i] = lo + hi;
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) z[i] += __shfl_xor_sync(0xffffffffu, z[i], o);
+        if (v0 + i >= V) z[i] = -INFINITY;
+        if (lane == 0 && n < N && v0 + i < V && v0 + i == tgt[n]) zt[n] = z[i];
+        top = fmaxf(top, z[i]);
+      }
+      const float mn = fmaxf(st[n].x, top);
       const float ms = mn == -INFINITY ? 0.f : mn;
-      s = s * exp2f(m - ms) + x.y * exp2f(x.x - ms);
-      m = mn;
+      float s = st[n].y * ptx::ex2((st[n].x - ms) * scale_log2);
+#pragma unroll
+      for (int i = 0; i < kFewV; ++i) s += ptx::ex2((z[i] - ms) * scale_log2);
+      st[n] = make_float2(mn, s);
     }
   }
-  sm[w][lane] = make_float2(m, s);
+  if (lane == 0)
+#pragma unroll
+    for (int n = 0; n < kN; ++n) sm[warp][n] = st[n];
   __syncthreads();
-  if (w != 0 || i >= N) return;
-  if (r < 0) {
-    loss[i] = 0.f;
-    lse[i] = 0.f;
-    return;
+  if (threadIdx.x < N) {
+    float2 x = sm[0][threadIdx.x];
+    for (int k = 1; k < 8; ++k) x = merge(x, sm[k][threadIdx.x], scale_log2);
+    part[static_cast<int64_t>(blockIdx.x) * np + threadIdx.x] = x;
   }
-  for (int k = 1; k < 8; ++k) {
-    const float2 x = sm[k][lane];
-    const float mn = fmaxf(m, x.x);
-    const float ms = mn == -INFINITY ? 0.f : mn;
-    s = s * exp2f(m - ms) + x.y * exp2f(x.x - ms);
-    m = mn;
-  }
-  const float l2 = m + log2f(s);
-  lse[i] = l2 * kLn2;
-  loss[i] = (l2 - zt[r]) * kLn2;
 }
 
 // dh of every position that the product's last epilogue has not written:
@@ -628,6 +720,9 @@ LmShape lm_shape(int64_t N, int64_t V) {
   return s;
 }
 
+int few_rows(int64_t N) { return N == 3 ? 4 : static_cast<int>(N); }   // the kernel's kN
+bool use_few(int64_t N, int32_t C) { return N <= kFewRows && int64_t{few_rows(N)} * C <= kFewMost; }
+
 struct Carve {
   uint8_t* base;
   size_t at = 0;
@@ -659,7 +754,9 @@ size_t carve(uint8_t* base, int64_t N, int64_t V, int32_t C, bool backward, LmWo
     o.hc = c.take<__nv_bfloat16>(s.np * C);
   }
   if (!backward) {
-    o.part = c.take<float2>(2 * static_cast<int64_t>(s.chunks) * s.np);
+    int64_t slots = 2 * static_cast<int64_t>(s.chunks);
+    if (use_few(N, C) && slots < kFewBlocks) slots = kFewBlocks;
+    o.part = c.take<float2>(slots * s.np);
     o.zt = c.take<float>(s.np);
   } else {
     o.dz = c.take<__nv_bfloat16>(s.np * s.piece);
@@ -687,6 +784,18 @@ int launch_product(const CUtensorMap& a, const CUtensorMap& b, const LmParams& p
   if (pairs < 1) pairs = 1;
   if (pairs > most_units) pairs = most_units;
   lm_product_kernel<kMode><<<static_cast<unsigned>(2 * pairs), kThreads, kLmSmemBytes, s>>>(a, b, p);
+  return cuda_status(cudaGetLastError());
+}
+
+template <int kN>
+int launch_few(const void* h, const void* w, const int32_t* target, int64_t N, int64_t V, int32_t C, int64_t np,
+               float scale_log2, int blocks, const LmWork& k, cudaStream_t s) {
+  static PerContext<int> rec;
+  const int st = set_smem_once(rec, lm_few_kernel<kN>, sizeof(float) * kFewMost);
+  if (st != TPK_OK) return st;
+  lm_few_kernel<kN><<<blocks, 256, static_cast<size_t>(kN) * C * 4, s>>>(
+      static_cast<const uint4*>(h), static_cast<const uint4*>(w), target, static_cast<int>(N), static_cast<int>(V), C,
+      np, scale_log2, k.part, k.zt);
   return cuda_status(cudaGetLastError());
 }
 
@@ -732,29 +841,45 @@ extern "C" int tpk_lm_loss(const void* h, const void* w, const int32_t* target, 
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   const LmShape sh = lm_shape(N, V);
   if (k.hc) st = gather_rows(h, target, N, V, C, k, s);
-  CUtensorMap ma, mb;
-  if (st == TPK_OK) st = k.hc ? make_map_2d(&ma, k.hc, sh.np, C, C, kHalf) : make_map_2d(&ma, h, N, C, C, kHalf);
-  if (st == TPK_OK) st = make_map_2d(&mb, w, V, C, C, kHalf);
+  const float scale_log2 = scale * kLog2e;
+  int slots = 2 * sh.chunks;
+  if (use_few(N, C)) {
+    const int64_t want = (V + 8 * kFewV - 1) / (8 * kFewV);
+    int64_t blocks = int64_t{num_sms()} * 4;
+    blocks = blocks > kFewBlocks ? kFewBlocks : blocks;
+    slots = static_cast<int>(want < blocks ? want : blocks);
+    st = few_rows(N) == 1   ? launch_few<1>(h, w, target, N, V, C, sh.np, scale_log2, slots, k, s)
+         : few_rows(N) == 2 ? launch_few<2>(h, w, target, N, V, C, sh.np, scale_log2, slots, k, s)
+                  : launch_few<4>(h, w, target, N, V, C, sh.np, scale_log2, slots, k, s);
+  } else {
+    CUtensorMap ma, mb;
+    if (st == TPK_OK) st = k.hc ? make_map_2d(&ma, k.hc, sh.np, C, C, kHalf) : make_map_2d(&ma, h, N, C, C, kHalf);
+    if (st == TPK_OK) st = make_map_2d(&mb, w, V, C, C, kHalf);
+    if (st != TPK_OK) return st;
+    LmParams p{};
+    p.count = k.count;
+    p.n_rows = static_cast<int32_t>(N);
+    p.V = static_cast<int32_t>(V);
+    p.C = C;
+    p.np = sh.np;
+    p.rows = k.rows;
+    p.target = target;
+    p.scale = scale;
+    p.scale_log2 = scale_log2;
+    p.part = k.part;
+    p.zt = k.zt;
+    p.run = sh.run;
+    p.err = dev_err;
+    st = launch_product<kFwd>(ma, mb, p, sh.np / kTile * sh.chunks, s);
+  }
   if (st != TPK_OK) return st;
-  LmParams p{};
-  p.count = k.count;
-  p.n_rows = static_cast<int32_t>(N);
-  p.V = static_cast<int32_t>(V);
-  p.C = C;
-  p.np = sh.np;
-  p.rows = k.rows;
-  p.target = target;
-  p.scale = scale;
-  p.scale_log2 = scale * kLog2e;
-  p.part = k.part;
-  p.zt = k.zt;
-  p.run = sh.run;
-  p.err = dev_err;
-  st = launch_product<kFwd>(ma, mb, p, sh.np / kTile * sh.chunks, s);
-  if (st != TPK_OK) return st;
-  lm_join_kernel<<<static_cast<unsigned>((N + 31) / 32), 256, 0, s>>>(k.part, k.zt, k.pos, target, static_cast<int>(N),
-                                                                      static_cast<int>(V), 2 * sh.chunks, sh.np, loss,
-                                                                      lse);
+  const int n = static_cast<int>(N), v = static_cast<int>(V);
+  if (N <= 1024)
+    lm_join_kernel<4><<<(n + 3) / 4, 256, 0, s>>>(k.part, k.zt, k.pos, target, n, v, slots, sh.np, scale, scale_log2,
+                                                  loss, lse);
+  else
+    lm_join_kernel<32><<<(n + 31) / 32, 256, 0, s>>>(k.part, k.zt, k.pos, target, n, v, slots, sh.np, scale,
+                                                     scale_log2, loss, lse);
   return cuda_status(cudaGetLastError());
 }
 

@@ -608,29 +608,62 @@ def gdn_delta_rule_bwd(dplan, q, k, v, g, beta, dout, state, scale=None, dq=None
 
 
 # ---- the operators around the token mixers ----------------------------------
+#
+# One token's call is a few microseconds of GPU work, so these wrappers check
+# each tensor once (_arg) and hand plain addresses to ctypes.
 
 _TABLE_TYPES = {torch.bfloat16: B.BF16, torch.float32: B.F32}
 
 
-def _same_device(ref, ref_name, *named):
-    """Every tensor (None skipped) a CUDA tensor on ref's device (checked after
-    the shapes, so a wrong shape is reported as such wherever the tensors live)."""
-    for t, n in ((ref, ref_name),) + named:
+def _arg(t, dtype, shape, name):
+    """t's address, once it is a contiguous tensor of dtype and shape."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError("%s must be a torch.Tensor" % name)
+    if t.dtype is not dtype:
+        raise TypeError("%s must be %s, got %s" % (name, dtype, t.dtype))
+    if t.shape != shape:
+        raise ValueError("%s must have shape %s, got %s" % (name, tuple(shape), tuple(t.shape)))
+    if not t.is_contiguous():
+        raise ValueError("%s must be contiguous" % name)
+    return t.data_ptr()
+
+
+def _matrix(t, dtypes, name):
+    """The shape of the 2-d tensor t, of one of dtypes, with rows of 8k channels."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError("%s must be a torch.Tensor" % name)
+    if t.dtype not in dtypes or t.dim() != 2:
+        raise TypeError("%s must be a 2-d tensor of %s" % (name, " or ".join(str(d) for d in dtypes)))
+    n, c = t.shape
+    if c < 8 or c % 8:
+        raise ValueError("%s must have a multiple of 8 channels, got %d" % (name, c))
+    return n, c
+
+
+def _device(names, *tensors):
+    """The one CUDA device of all tensors (None skipped).  Checked after the
+    shapes, so a wrong shape is reported as such wherever the tensors live."""
+    dev = tensors[0].get_device()
+    for i, t in enumerate(tensors):
         if t is None:
             continue
-        if not t.is_cuda:
-            raise ValueError("%s must be a CUDA tensor (no CPU path exists)" % n)
-        if t.device != ref.device:
-            raise ValueError("%s is on %s, expected %s" % (n, t.device, ref.device))
+        d = t.get_device()
+        if d < 0:
+            raise ValueError("%s must be a CUDA tensor (no CPU path exists)" % names.split()[i])
+        if d != dev:
+            raise ValueError("%s is on %s, expected cuda:%d" % (names.split()[i], t.device, dev))
+    return dev
 
 
-def _launch(ref, fn, what, *args):
-    """fn(*args, stream) on ref's device and that device's current stream."""
-    if ref.device.index == torch.cuda.current_device():
-        B.check(fn(*args, _stream()), what)
+def _launch(dev, fn, *args):
+    """fn(*args, stream) on device dev and that device's current stream."""
+    if dev == torch._C._cuda_getDevice():
+        st = fn(*args, torch._C._cuda_getCurrentRawStream(dev))
     else:
-        with torch.cuda.device(ref.device):
-            B.check(fn(*args, _stream()), what)
+        with torch.cuda.device(dev):
+            st = fn(*args, torch._C._cuda_getCurrentRawStream(dev))
+    if st != B.TPK_OK:
+        B.check(st, fn.__name__)
 
 
 def _workspace(workspace, need, ref, what):
@@ -639,15 +672,16 @@ def _workspace(workspace, need, ref, what):
         return torch.empty(max(need, 256), dtype=torch.uint8, device=ref.device)
     if not isinstance(workspace, torch.Tensor) or not workspace.is_contiguous():
         raise ValueError("workspace must be a contiguous tensor")
-    if workspace.numel() * workspace.element_size() < need:
-        raise ValueError("workspace has %d bytes, %s needs %d"
-                         % (workspace.numel() * workspace.element_size(), what, need))
+    if workspace.nbytes < need:
+        raise ValueError("workspace has %d bytes, %s needs %d" % (workspace.nbytes, what, need))
     return workspace
 
 
-def _channels(C):
-    if C < 8 or C % 8:
-        raise ValueError("rows must have a multiple of 8 channels, got %d" % C)
+def _dev_err(t):
+    if t is None:
+        return None
+    _need(t, torch.int32, "dev_err", cuda=False)
+    return t.data_ptr()
 
 
 def embed(table, tokens, scale=1.0, out=None):
@@ -657,21 +691,16 @@ def embed(table, tokens, scale=1.0, out=None):
     table [V, C] bf16 or fp32, tokens [N] int32 (e.g. ``gather_to_forwarded``
     of the raw token ids).  Returns out [N, C] bf16."""
     lib = B.load()
-    if not isinstance(table, torch.Tensor) or table.dtype not in _TABLE_TYPES:
-        raise TypeError("table must be a bf16 or fp32 tensor")
-    _need(table, table.dtype, "table", 2, cuda=False)
-    _need(tokens, torch.int32, "tokens", 1, cuda=False)
-    V, C = table.shape
-    N = tokens.numel()
-    _channels(C)
+    V, C = _matrix(table, _TABLE_TYPES, "table")
     if V < 1:
         raise ValueError("table has no rows")
+    p_table = _arg(table, table.dtype, (V, C), "table")
+    N = tokens.numel() if isinstance(tokens, torch.Tensor) else 0
+    p_tok = _arg(tokens, torch.int32, (N,), "tokens")
     out = torch.empty((N, C), dtype=torch.bfloat16, device=table.device) if out is None else out
-    _need(out, torch.bfloat16, "out", 2, cuda=False)
-    _shape(out, (N, C), "out")
-    _same_device(table, "table", (tokens, "tokens"), (out, "out"))
-    _launch(table, lib.tpk_embed, "tpk_embed", _ptr(table), _TABLE_TYPES[table.dtype], _ptr(tokens), _ptr(out), N, V, C,
-            float(scale))
+    p_out = _arg(out, torch.bfloat16, (N, C), "out")
+    dev = _device("table tokens out", table, tokens, out)
+    _launch(dev, lib.tpk_embed, p_table, _TABLE_TYPES[table.dtype], p_tok, p_out, N, V, C, scale)
     return out
 
 
@@ -683,65 +712,54 @@ def embed_bwd(tokens, dout, vocab, scale=1.0, dtype=torch.float32, dtable=None, 
     tokens [N] int32, dout [N, C] bf16 -> dtable [vocab, C] of ``dtype`` (fp32
     or bf16; ignored if ``dtable`` is given)."""
     lib = B.load()
-    _need(tokens, torch.int32, "tokens", 1, cuda=False)
-    _need(dout, torch.bfloat16, "dout", 2, cuda=False)
-    N, C = dout.shape
-    _channels(C)
+    N, C = _matrix(dout, (torch.bfloat16,), "dout")
+    p_dout = _arg(dout, torch.bfloat16, (N, C), "dout")
+    p_tok = _arg(tokens, torch.int32, (N,), "tokens")
     V = int(vocab)
     if V < 1:
         raise ValueError("vocab must be positive")
-    if tokens.numel() != N:
-        raise ValueError("tokens has %d ids, dout %d rows" % (tokens.numel(), N))
     dtype = dtype if dtable is None else dtable.dtype
     if dtype not in _TABLE_TYPES:
         raise TypeError("the table's gradient must be bf16 or fp32")
     dtable = torch.empty((V, C), dtype=dtype, device=dout.device) if dtable is None else dtable
-    _need(dtable, dtype, "dtable", 2, cuda=False)
-    _shape(dtable, (V, C), "dtable")
-    need = int(lib.tpk_embed_bwd_workspace_bytes(N, V, C))
-    workspace = _workspace(workspace, need, dout, "the lookup's backward")
-    _same_device(dout, "dout", (tokens, "tokens"), (dtable, "dtable"), (workspace, "workspace"))
-    _launch(dout, lib.tpk_embed_bwd, "tpk_embed_bwd", _ptr(tokens), _ptr(dout), _ptr(dtable), _TABLE_TYPES[dtype], N, V,
-            C, float(scale), _ptr(workspace), workspace.numel() * workspace.element_size())
+    p_dt = _arg(dtable, dtype, (V, C), "dtable")
+    ws = _workspace(workspace, lib.tpk_embed_bwd_workspace_bytes(N, V, C), dout, "the lookup's backward")
+    dev = _device("dout tokens dtable workspace", dout, tokens, dtable, ws)
+    _launch(dev, lib.tpk_embed_bwd, p_tok, p_dout, p_dt, _TABLE_TYPES[dtype], N, V, C, scale, ws.data_ptr(), ws.nbytes)
     return dtable
 
 
-def _rows2(t, name, shape, strided=False):
-    """A 2-d bf16 tensor of ``shape``: contiguous, or with ``strided`` rows
-    that may lie apart (column slices), 16-byte aligned.  Returns the row
-    stride in elements."""
-    if not isinstance(t, torch.Tensor) or t.dtype != torch.bfloat16 or t.dim() != 2:
+def _rows2(t, name, shape):
+    """(address, row stride in elements) of a 2-d bf16 tensor whose rows may
+    lie apart (column slices), 16-byte aligned."""
+    if not isinstance(t, torch.Tensor) or t.dtype is not torch.bfloat16 or t.dim() != 2:
         raise TypeError("%s must be a 2-d bf16 tensor" % name)
-    _shape(t, shape, name)
-    if not strided:
-        if not t.is_contiguous():
-            raise ValueError("%s must be contiguous" % name)
-        return shape[1]
-    if t.stride(1) != 1:
+    if t.shape != shape:
+        raise ValueError("%s must have shape %s, got %s" % (name, tuple(shape), tuple(t.shape)))
+    ld, unit = t.stride()
+    if unit != 1:
         raise ValueError("%s: channels must be contiguous inside a row" % name)
     if shape[0] <= 1:
-        return shape[1]
-    if t.stride(0) < shape[1] or t.stride(0) % 8:
+        ld = shape[1]
+    elif ld < shape[1] or ld % 8:
         raise ValueError("%s: rows must not overlap and must lie a multiple of 8 elements apart" % name)
-    return t.stride(0)
+    return t.data_ptr(), ld
 
 
 def _norm_args(res, w_pre, y, w_post, gate):
-    """(N, C, ld_y, ld_gate), every input checked."""
-    if not isinstance(res, torch.Tensor) or res.dim() != 2:
-        raise TypeError("res must be a 2-d bf16 tensor")
-    N, C = res.shape
-    _channels(C)
-    _rows2(res, "res", (N, C))
-    if y is None and (gate is not None or w_post is not None):
-        raise ValueError("gate and w_post apply to y, which is missing")
-    ld_y = C if y is None else _rows2(y, "y", (N, C), strided=True)
-    ld_gate = C if gate is None else _rows2(gate, "gate", (N, C), strided=True)
-    for t, n in ((w_pre, "w_pre"), (w_post, "w_post")):
-        if t is not None or n == "w_pre":
-            _need(t, torch.float32, n, 1, cuda=False)
-            _shape(t, (C,), n)
-    return N, C, ld_y, ld_gate
+    """(shape, the inputs' addresses and row strides in the C call's order)."""
+    shape = _matrix(res, (torch.bfloat16,), "res")
+    C = shape[1]
+    p_res = _arg(res, torch.bfloat16, shape, "res")
+    if y is None:
+        if gate is not None or w_post is not None:
+            raise ValueError("gate and w_post apply to y, which is missing")
+        p_y, ld_y = None, C
+    else:
+        p_y, ld_y = _rows2(y, "y", shape)
+    p_gate, ld_gate = (None, C) if gate is None else _rows2(gate, "gate", shape)
+    p_post = None if w_post is None else _arg(w_post, torch.float32, (C,), "w_post")
+    return shape, (p_res, p_y, ld_y, p_gate, ld_gate, p_post, _arg(w_pre, torch.float32, (C,), "w_pre"))
 
 
 def block_norm(res, w_pre, y=None, w_post=None, gate=None, scale=1.0, eps=1e-6, res_out=None, out=None):
@@ -756,19 +774,17 @@ def block_norm(res, w_pre, y=None, w_post=None, gate=None, scale=1.0, eps=1e-6, 
     1; without y (the norm before the first block) r is res.  Returns
     (r, x), both [N, C] bf16; ``res_out`` may be ``res`` itself."""
     lib = B.load()
-    N, C, ld_y, ld_gate = _norm_args(res, w_pre, y, w_post, gate)
-    if y is None:
-        if res_out is not None:
-            raise ValueError("without y nothing is added to res: res_out is not written")
-    else:
+    shape, args = _norm_args(res, w_pre, y, w_post, gate)
+    p_ro = None
+    if y is not None:
         res_out = torch.empty_like(res) if res_out is None else res_out
-        _rows2(res_out, "res_out", (N, C))
+        p_ro = _arg(res_out, torch.bfloat16, shape, "res_out")
+    elif res_out is not None:
+        raise ValueError("without y nothing is added to res: res_out is not written")
     out = torch.empty_like(res) if out is None else out
-    _rows2(out, "out", (N, C))
-    _same_device(res, "res", (w_pre, "w_pre"), (y, "y"), (w_post, "w_post"), (gate, "gate"), (res_out, "res_out"),
-                 (out, "out"))
-    _launch(res, lib.tpk_block_norm, "tpk_block_norm", _ptr(res), _ptr(y), ld_y, _ptr(gate), ld_gate, _ptr(w_post),
-            _ptr(w_pre), _ptr(res_out), _ptr(out), N, C, float(scale), float(eps))
+    p_out = _arg(out, torch.bfloat16, shape, "out")
+    dev = _device("res w_pre y w_post gate res_out out", res, w_pre, y, w_post, gate, res_out, out)
+    _launch(dev, lib.tpk_block_norm, *args, p_ro, p_out, *shape, scale, eps)
     return (res if y is None else res_out), out
 
 
@@ -779,56 +795,46 @@ def block_norm_bwd(res, w_pre, dx, dres_out=None, y=None, w_post=None, gate=None
     forward.  dy and dgate may be column slices of a wider gradient.  Returns
     (dres, dy, dgate, dw_post, dw_pre), None where the input was None."""
     lib = B.load()
-    N, C, ld_y, ld_gate = _norm_args(res, w_pre, y, w_post, gate)
-    _rows2(dx, "dx", (N, C))
-    if dres_out is not None:
-        _rows2(dres_out, "dres_out", (N, C))
+    shape, args = _norm_args(res, w_pre, y, w_post, gate)
+    C = shape[1]
+    p_dx = _arg(dx, torch.bfloat16, shape, "dx")
+    p_dro = None if dres_out is None else _arg(dres_out, torch.bfloat16, shape, "dres_out")
     for t, n, ref in ((dy, "dy", y), (dgate, "dgate", gate), (dw_post, "dw_post", w_post)):
         if t is not None and ref is None:
             raise ValueError("%s is given, but not the input it is the gradient of" % n)
     dres = torch.empty_like(res) if dres is None else dres
-    _rows2(dres, "dres", (N, C))
+    p_dres = _arg(dres, torch.bfloat16, shape, "dres")
+    p_dy = p_dgate = p_dpost = None
     ld_dy = ld_dgate = C
     if y is not None:
-        dy = torch.empty((N, C), dtype=torch.bfloat16, device=res.device) if dy is None else dy
-        ld_dy = _rows2(dy, "dy", (N, C), strided=True)
+        dy = torch.empty(shape, dtype=torch.bfloat16, device=res.device) if dy is None else dy
+        p_dy, ld_dy = _rows2(dy, "dy", shape)
     if gate is not None:
-        dgate = torch.empty((N, C), dtype=torch.bfloat16, device=res.device) if dgate is None else dgate
-        ld_dgate = _rows2(dgate, "dgate", (N, C), strided=True)
-    dw_pre = torch.empty_like(w_pre) if dw_pre is None else dw_pre
+        dgate = torch.empty(shape, dtype=torch.bfloat16, device=res.device) if dgate is None else dgate
+        p_dgate, ld_dgate = _rows2(dgate, "dgate", shape)
     if w_post is not None:
         dw_post = torch.empty_like(w_post) if dw_post is None else dw_post
-    for t, n in ((dw_pre, "dw_pre"), (dw_post, "dw_post")):
-        if t is not None:
-            _need(t, torch.float32, n, 1, cuda=False)
-            _shape(t, (C,), n)
-    need = int(lib.tpk_block_norm_bwd_workspace_bytes(N, C))
-    workspace = _workspace(workspace, need, res, "the norms' backward")
-    _same_device(res, "res", (w_pre, "w_pre"), (dx, "dx"), (dres_out, "dres_out"), (y, "y"), (w_post, "w_post"),
-                 (gate, "gate"), (dres, "dres"), (dy, "dy"), (dgate, "dgate"), (dw_post, "dw_post"), (dw_pre, "dw_pre"),
-                 (workspace, "workspace"))
-    _launch(res, lib.tpk_block_norm_bwd, "tpk_block_norm_bwd", _ptr(res), _ptr(y), ld_y, _ptr(gate), ld_gate,
-            _ptr(w_post), _ptr(w_pre), _ptr(dres_out), _ptr(dx), _ptr(dres), _ptr(dy), ld_dy, _ptr(dgate), ld_dgate,
-            _ptr(dw_post), _ptr(dw_pre), N, C, float(scale), float(eps), _ptr(workspace),
-            workspace.numel() * workspace.element_size())
+        p_dpost = _arg(dw_post, torch.float32, (C,), "dw_post")
+    dw_pre = torch.empty_like(w_pre) if dw_pre is None else dw_pre
+    p_dpre = _arg(dw_pre, torch.float32, (C,), "dw_pre")
+    ws = _workspace(workspace, lib.tpk_block_norm_bwd_workspace_bytes(*shape), res, "the norms' backward")
+    dev = _device("res w_pre dx dres_out y w_post gate dres dy dgate dw_post dw_pre workspace", res, w_pre, dx, dres_out,
+                  y, w_post, gate, dres, dy, dgate, dw_post, dw_pre, ws)
+    _launch(dev, lib.tpk_block_norm_bwd, *args, p_dro, p_dx, p_dres, p_dy, ld_dy, p_dgate, ld_dgate, p_dpost, p_dpre,
+            *shape, scale, eps, ws.data_ptr(), ws.nbytes)
     return dres, dy, dgate, dw_post, dw_pre
 
 
 def _loss_args(h, w, target, scale):
-    """(N, V, C), the loss's inputs checked."""
-    _need(h, torch.bfloat16, "h", 2, cuda=False)
-    _need(w, torch.bfloat16, "w", 2, cuda=False)
-    _need(target, torch.int32, "target", 1, cuda=False)
-    N, C = h.shape
-    V = w.shape[0]
-    _channels(C)
-    _shape(w, (V, C), "w")
-    _shape(target, (N,), "target")
+    """(N, V, C, addresses of h, w, target), checked."""
+    N, C = _matrix(h, (torch.bfloat16,), "h")
+    V = _matrix(w, (torch.bfloat16,), "w")[0]
     if V < 1:
         raise ValueError("w has no rows")
-    if not (0.0 < float(scale) < math.inf):
+    if not 0.0 < scale < math.inf:
         raise ValueError("scale must be positive and finite")
-    return N, V, C
+    return N, V, C, (_arg(h, torch.bfloat16, (N, C), "h"), _arg(w, torch.bfloat16, (V, C), "w"),
+                     _arg(target, torch.int32, (N,), "target"))
 
 
 def lm_loss(h, w, target, scale=1.0, loss=None, lse=None, workspace=None, dev_err=None):
@@ -839,20 +845,14 @@ def lm_loss(h, w, target, scale=1.0, loss=None, lse=None, workspace=None, dev_er
     (loss, lse), fp32 [N]: loss = lse - logit[target], both zero where the
     target is outside [0, V) (a position without a prediction)."""
     lib = B.load()
-    N, V, C = _loss_args(h, w, target, scale)
+    N, V, C, args = _loss_args(h, w, target, scale)
     loss = torch.empty(N, dtype=torch.float32, device=h.device) if loss is None else loss
     lse = torch.empty(N, dtype=torch.float32, device=h.device) if lse is None else lse
-    for t, n in ((loss, "loss"), (lse, "lse")):
-        _need(t, torch.float32, n, 1, cuda=False)
-        _shape(t, (N,), n)
-    if dev_err is not None:
-        _need(dev_err, torch.int32, "dev_err", cuda=False)
-    need = int(lib.tpk_lm_loss_workspace_bytes(N, V, C, 0))
-    workspace = _workspace(workspace, need, h, "the loss")
-    _same_device(h, "h", (w, "w"), (target, "target"), (loss, "loss"), (lse, "lse"), (workspace, "workspace"),
-                 (dev_err, "dev_err"))
-    _launch(h, lib.tpk_lm_loss, "tpk_lm_loss", _ptr(h), _ptr(w), _ptr(target), _ptr(loss), _ptr(lse), N, V, C,
-            float(scale), _ptr(workspace), workspace.numel() * workspace.element_size(), _ptr(dev_err))
+    p_loss, p_lse = _arg(loss, torch.float32, (N,), "loss"), _arg(lse, torch.float32, (N,), "lse")
+    p_err = _dev_err(dev_err)
+    ws = _workspace(workspace, lib.tpk_lm_loss_workspace_bytes(N, V, C, 0), h, "the loss")
+    dev = _device("h w target loss lse workspace dev_err", h, w, target, loss, lse, ws, dev_err)
+    _launch(dev, lib.tpk_lm_loss, *args, p_loss, p_lse, N, V, C, scale, ws.data_ptr(), ws.nbytes, p_err)
     return loss, lse
 
 
@@ -862,23 +862,13 @@ def lm_loss_bwd(h, w, target, lse, dloss, scale=1.0, dh=None, dw=None, workspace
     each position's loss (e.g. ``sum_to_forwarded`` of per-token weights).
     Returns (dh [N, C] bf16, dw [V, C] bf16)."""
     lib = B.load()
-    N, V, C = _loss_args(h, w, target, scale)
-    for t, n in ((lse, "lse"), (dloss, "dloss")):
-        _need(t, torch.float32, n, 1, cuda=False)
-        _shape(t, (N,), n)
+    N, V, C, args = _loss_args(h, w, target, scale)
+    p_lse, p_dloss = _arg(lse, torch.float32, (N,), "lse"), _arg(dloss, torch.float32, (N,), "dloss")
     dh = torch.empty_like(h) if dh is None else dh
     dw = torch.empty_like(w) if dw is None else dw
-    _need(dh, torch.bfloat16, "dh", 2, cuda=False)
-    _shape(dh, (N, C), "dh")
-    _need(dw, torch.bfloat16, "dw", 2, cuda=False)
-    _shape(dw, (V, C), "dw")
-    if dev_err is not None:
-        _need(dev_err, torch.int32, "dev_err", cuda=False)
-    need = int(lib.tpk_lm_loss_workspace_bytes(N, V, C, 1))
-    workspace = _workspace(workspace, need, h, "the loss's backward")
-    _same_device(h, "h", (w, "w"), (target, "target"), (lse, "lse"), (dloss, "dloss"), (dh, "dh"), (dw, "dw"),
-                 (workspace, "workspace"), (dev_err, "dev_err"))
-    _launch(h, lib.tpk_lm_loss_bwd, "tpk_lm_loss_bwd", _ptr(h), _ptr(w), _ptr(target), _ptr(lse), _ptr(dloss), _ptr(dh),
-            _ptr(dw), N, V, C, float(scale), _ptr(workspace), workspace.numel() * workspace.element_size(),
-            _ptr(dev_err))
+    p_dh, p_dw = _arg(dh, torch.bfloat16, (N, C), "dh"), _arg(dw, torch.bfloat16, (V, C), "dw")
+    p_err = _dev_err(dev_err)
+    ws = _workspace(workspace, lib.tpk_lm_loss_workspace_bytes(N, V, C, 1), h, "the loss's backward")
+    dev = _device("h w target lse dloss dh dw workspace dev_err", h, w, target, lse, dloss, dh, dw, ws, dev_err)
+    _launch(dev, lib.tpk_lm_loss_bwd, *args, p_lse, p_dloss, p_dh, p_dw, N, V, C, scale, ws.data_ptr(), ws.nbytes, p_err)
     return dh, dw

@@ -107,6 +107,20 @@ def test_embed_bwd(ops, n, c, v, kind, dtype):
     assert torch.equal(got, ops.embed_bwd(t, dout, v, scale=0.7, dtype=dtype))   # deterministic
 
 
+@pytest.mark.parametrize("n,v", [(2048, 300), (2049, 300), (16383, 70), (16384, 5000), (1_048_576, 70000),
+                                 (1_048_577, 70000)])
+def test_embed_bwd_sizes_where_the_plan_changes(ops, n, v):
+    """One sort tile and two, both piece lengths, both tile lengths; fp64 sums on the GPU."""
+    tok, dout = torch.from_numpy(_tokens(n, v, 8, "zipf")).cuda(), _rnd(9, n, 8)
+    got = ops.embed_bwd(tok, dout, v)
+    at = torch.where((tok >= 0) & (tok < v), tok, v).long()
+    ref = torch.zeros(v + 1, 8, dtype=torch.float64, device="cuda").index_add_(0, at, dout.double())[:v]
+    mag = torch.zeros(v + 1, 8, dtype=torch.float64, device="cuda").index_add_(0, at, dout.double().abs())[:v]
+    # additions in a row: a piece's 64, then the pieces of the longest run
+    most = 64 + int(torch.bincount(at)[:v].max()) // 16 + 2
+    assert ((got.double() - ref).abs() <= most * U * mag).all()
+
+
 @pytest.mark.parametrize("n", [63, 64, 65, 128, 129, 5000])
 def test_embed_bwd_one_id(ops, n):
     """A single run over every piece, alone and beside one other id at either end."""
@@ -252,7 +266,10 @@ def test_block_norm_zero_rows_and_extremes(ops):
 # (N, V, C, share of positions with a target)
 LOSS = [(1, 1, 8, 1.0), (1, 32000, 64, 1.0), (3, 257, 8, 1.0), (255, 1000, 72, 0.5), (256, 256, 64, 1.0),
         (257, 5003, 128, 0.3), (700, 129, 1000, 0.9), (1030, 2049, 520, 0.02), (5, 4096, 2048, 0.8),
-        (2600, 300, 64, 0.7), (600, 7000, 264, 0.0)]
+        (2600, 300, 64, 0.7), (600, 7000, 264, 0.0),
+        # a few positions: one read of w (up to 16,384 values of h), and just above
+        (2, 5003, 4096, 1.0), (2, 3, 8, 1.0), (3, 1000, 2048, 0.7), (4, 77, 4096, 1.0), (4, 20011, 64, 0.5),
+        (2, 300, 8200, 1.0), (3, 100, 5464, 1.0), (1, 100, 16384, 1.0), (5, 1000, 64, 1.0)]
 
 
 def _loss_inputs(n, v, c, on, seed=31):
