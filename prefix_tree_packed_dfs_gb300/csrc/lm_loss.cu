@@ -23,12 +23,17 @@
 //
 // The product: 256 x 256 tiles on a pair of CTAs (tcgen05 cta_group::2, each
 // CTA holds 128 rows of A, 128 rows of B and its 128 rows of the result), 64
-// elements of K per stage, six stages filled by TMA, two accumulators of 256
-// TMEM columns so that a tile's epilogue runs under the next tile's products.
+// elements of K per stage, stages filled by TMA, two accumulators of 256 TMEM
+// columns so that a tile's epilogue runs under the next tile's products.
 // One CTA with a 128 x 256 tile would load 96 bytes of operands per cycle and
 // SM at full tensor rate; the pair loads 64.
 // Warps of a CTA: 0 TMA producer, 1 MMA issuer (of the pair's first CTA), 2
-// TMEM owner, 4-11 epilogue (two warpgroups, 128 columns each).  CTAs are
+// TMEM owner, 4-11 epilogue (two warpgroups, 128 columns each).  At widths
+// below about 1,000 the epilogue is what a tile waits for: its arithmetic is
+// on packed fp32 pairs, a chunk of 32 columns is read from TMEM while the one
+// before is worked on, and bf16 results (dz, dw) leave through shared memory
+// by TMA (stores of 64 bytes per row straight from the registers took 1.6x
+// the time).  CTAs are
 // persistent and walk the tiles in panels of 8 columns of tiles, so the pairs
 // running together share rows of A and of B in L2.
 #include <cuda_bf16.h>
@@ -39,7 +44,6 @@
 namespace tpk {
 namespace {
 
-constexpr int kStages = 6;
 constexpr int kTile = 256;            // rows and columns of a pair's tile
 constexpr int kHalf = 128;            // rows of A / of B a CTA holds
 constexpr int kBoxBytes = kHalf * 128;// one stage's operand: 128 x 64 bf16
@@ -82,9 +86,15 @@ __device__ __forceinline__ int splits_for(int tiles, int most) {
 }
 __device__ __forceinline__ int dw_splits(int tiles, int k_iters) { return splits_for(tiles, k_iters / 8); }
 
+// kDz and kDw give one stage's room to the tiles on their way out.
+template <int kMode>
 struct LmSmem {
+  static constexpr bool kOut = kMode == kDz || kMode == kDw;
+  static constexpr int kStages = kOut ? 5 : 6;
+  static constexpr int kOutBoxes = kOut ? 2 : 0;   // per warpgroup
   uint8_t a[kStages][kBoxBytes];
   uint8_t b[kStages][kBoxBytes];
+  uint8_t out[kOut ? 2 * kOutBoxes : 1][kOut ? kBoxBytes : 1024];
   uint64_t full[kStages], empty[kStages];
   uint64_t tm_full[2], tm_empty[2];
   uint64_t drain;
@@ -92,8 +102,9 @@ struct LmSmem {
   int abort_flag;
   uint32_t issued;   // stages the producer has filled
 };
-constexpr size_t kLmSmemBytes = sizeof(LmSmem) + 1024;
-static_assert(kLmSmemBytes <= 227 * 1024, "shared memory");
+template <int kMode>
+constexpr size_t kLmSmemBytes = sizeof(LmSmem<kMode>) + 1024;
+static_assert(kLmSmemBytes<kFwd> <= 227 * 1024 && kLmSmemBytes<kDz> <= 227 * 1024, "shared memory");
 
 // The tiles of one launch.  unit u covers n tiles [nt0, nt0 + n_run) of row
 // tile mt, and K iterations [k0, k0 + nk).
@@ -153,9 +164,11 @@ __device__ __forceinline__ Unit unit_of(const LmParams& p, const Shape& s, int u
 template <int kMode>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     lm_product_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ CUtensorMap tm_b,
-                      const LmParams p) {
+                      const __grid_constant__ CUtensorMap tm_out, const LmParams p) {
   extern __shared__ uint8_t smem_raw[];
-  LmSmem& S = *reinterpret_cast<LmSmem*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  using Smem = LmSmem<kMode>;
+  constexpr int kStages = Smem::kStages;
+  Smem& S = *reinterpret_cast<Smem*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   constexpr bool kAmn = kMode == kDw;                      // A stored with M contiguous
   constexpr bool kBmn = kMode == kDh || kMode == kDw;      // B stored with N contiguous
   const int warp = threadIdx.x >> 5;
@@ -272,10 +285,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     // ------------------------------------------------------------ epilogue
     const int wg = (warp - 4) >> 2;                     // column half
     const int lane = threadIdx.x & 31;
-    const int r = static_cast<int>(rank) * kHalf + (warp & 3) * 32 + lane;   // row inside the tile
+    const int rc = (warp & 3) * 32 + lane;              // row of this CTA's half tile
+    const int r = static_cast<int>(rank) * kHalf + rc;  // row of the tile
     const uint32_t lane_off = static_cast<uint32_t>((warp & 3) * 32) << 16;
     const uint32_t bar_empty[2] = {ptx::cluster_addr(&S.tm_empty[0], 0), ptx::cluster_addr(&S.tm_empty[1], 0)};
+    const uint64_t k2 = ptx::f2(p.scale_log2, p.scale_log2);
     uint32_t tile = 0;
+    int box = 0;   // kDz, kDw: the warpgroup's next box in shared memory
     bool ok = true;
     for (int u = pair; ok && u < sh.units; u += n_pairs) {
       const Unit w = unit_of<kMode>(p, sh, u);
@@ -292,6 +308,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         if (kMode == kDz) {
           coef = __ldg(p.dloss + pos) * p.scale;
           lse2 = __ldg(p.lse + pos) * kLog2e;
+          tgt -= p.v0;
         }
       }
       for (int j = 0; j < w.n_run; ++j) {
@@ -299,81 +316,135 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         const bool any = kMode != kDw || w.nk > 0;   // no rows at all: dw is zero
         if (any) {
           ok = ptx::mbar_wait(&S.tm_full[buf], (tile / 2) & 1, abort_flag, kWaitLimitNs);
-          ok = __all_sync(0xffffffffu, ok);
+          // a warpgroup with barriers of its own gives up as a whole
+          ok = Smem::kOut ? ptx::all_of_128(wg + 1, ok) : __all_sync(0xffffffffu, ok);
           if (!ok) break;
           ptx::tc_fence_after();
           ++tile;
         }
         const int n0 = (w.n0 + j) * kTile + wg * kHalf;   // first column of this warpgroup
-#pragma unroll 1
-        for (int c = 0; c < 4; ++c) {
-          uint32_t raw[32];
-          if (any) {
-            ptx::tmem_ld32(tmem + lane_off + buf * kTile + wg * kHalf + c * 32, raw);
-            ptx::tmem_wait_ld();
-          } else {
+        const uint32_t tm = tmem + lane_off + buf * kTile + wg * kHalf;
+        uint32_t raw[2][32];
+        if (any) {
+          ptx::tmem_ld32(tm, raw[0]);
+          ptx::tmem_wait_ld_of(raw[0]);
+        } else {
 #pragma unroll
-            for (int e = 0; e < 32; ++e) raw[e] = 0;
-          }
-          if (any && c == 3) {
-            ptx::tc_fence_before();
-            __syncwarp();
-            if (lane == 0) ptx::mbar_arrive_cluster(bar_empty[buf]);
-          }
+          for (int e = 0; e < 32; ++e) raw[0][e] = raw[1][e] = 0;
+        }
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          uint32_t(&x)[32] = raw[c & 1];
+          if (any && c < 3) ptx::tmem_ld32(tm + (c + 1) * 32, raw[(c + 1) & 1]);
           const int c0 = n0 + c * 32;
           if constexpr (kMode == kFwd) {
             // unscaled scores and their maximum: the differences are exact to
             // a rounding, which products with the scale would not leave them
-            float t[32];
-            float top = -INFINITY;
-#pragma unroll
-            for (int e = 0; e < 32; ++e) {
-              t[e] = c0 + e < p.V ? __uint_as_float(raw[e]) : -INFINITY;
-              top = fmaxf(top, t[e]);
-            }
-            if (static_cast<uint32_t>(tgt - c0) < 32u) {
+            if (c0 + 32 > p.V)
 #pragma unroll
               for (int e = 0; e < 32; ++e)
-                if (tgt - c0 == e && tgt < p.V) p.zt[row] = t[e];
-            }
-            const float mn = fmaxf(m, top);
-            const float ms = mn == -INFINITY ? 0.f : mn;
-            float q[4] = {s * ptx::ex2((m - ms) * p.scale_log2), 0.f, 0.f, 0.f};
+                if (c0 + e >= p.V) x[e] = 0xff800000u;   // -inf
+            if (static_cast<uint32_t>(tgt - c0) < 32u && tgt < p.V) {
 #pragma unroll
-            for (int e = 0; e < 32; ++e) q[e & 3] += ptx::ex2((t[e] - ms) * p.scale_log2);
-            s = (q[0] + q[1]) + (q[2] + q[3]);
+              for (int e = 0; e < 32; ++e)
+                if (tgt - c0 == e) p.zt[row] = __uint_as_float(x[e]);
+            }
+            float top[4] = {m, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+            for (int e = 0; e < 32; e += 2)
+              top[(e / 2) & 3] = ptx::max3(top[(e / 2) & 3], __uint_as_float(x[e]), __uint_as_float(x[e + 1]));
+            const float mn = ptx::max3(top[0], top[1], fmaxf(top[2], top[3]));
+            const float ms = mn == -INFINITY ? 0.f : mn;
+            const uint64_t neg = ptx::f2(-ms, -ms);
+            uint64_t q[2] = {ptx::f2(s * ptx::ex2((m - ms) * p.scale_log2), 0.f), 0};
+#pragma unroll
+            for (int e = 0; e < 32; e += 2) {
+              const uint64_t d = ptx::add2(ptx::f2(__uint_as_float(x[e]), __uint_as_float(x[e + 1])), neg);
+              float lo, hi;
+              ptx::unf2(ptx::mul2(d, k2), lo, hi);
+              q[(e / 2) & 1] = ptx::add2(q[(e / 2) & 1], ptx::f2(ptx::ex2(lo), ptx::ex2(hi)));
+            }
+            float lo, hi;
+            ptx::unf2(ptx::add2(q[0], q[1]), lo, hi);
+            s = lo + hi;
             m = mn;
-          } else if constexpr (kMode == kDz) {
-            if (c0 < p.ld_dz) {
-              uint32_t o[16];
+          } else if constexpr (kMode == kDz || kMode == kDw) {
+            uint32_t o[16];
+            if constexpr (kMode == kDz) {
+              const uint64_t minus = ptx::f2(-lse2, -lse2), c2 = ptx::f2(coef, coef);
+              float d[32];
 #pragma unroll
               for (int e = 0; e < 32; e += 2) {
-                float d[2];
-#pragma unroll
-                for (int i = 0; i < 2; ++i) {
-                  const float pr = ptx::ex2(fmaf(__uint_as_float(raw[e + i]), p.scale_log2, -lse2));
-                  const float g = pr - (p.v0 + c0 + e + i == tgt ? 1.f : 0.f);
-                  d[i] = row < count && c0 + e + i < p.vcols ? coef * g : 0.f;
-                }
-                o[e / 2] = ptx::pack_bf16x2(d[0], d[1]);
+                float lo, hi;
+                ptx::unf2(ptx::fma2(ptx::f2(__uint_as_float(x[e]), __uint_as_float(x[e + 1])), k2, minus), lo, hi);
+                d[e] = ptx::ex2(lo);
+                d[e + 1] = ptx::ex2(hi);
               }
-              uint4* dst = reinterpret_cast<uint4*>(p.dz + static_cast<int64_t>(row) * p.ld_dz + c0);
+              if (static_cast<uint32_t>(tgt - c0) < 32u) {
 #pragma unroll
-              for (int q = 0; q < 4; ++q) dst[q] = make_uint4(o[4 * q], o[4 * q + 1], o[4 * q + 2], o[4 * q + 3]);
+                for (int e = 0; e < 32; ++e)
+                  if (tgt - c0 == e) d[e] -= 1.f;
+              }
+              if (c0 + 32 > p.vcols)
+#pragma unroll
+                for (int e = 0; e < 32; ++e)
+                  if (c0 + e >= p.vcols) d[e] = 0.f;
+#pragma unroll
+              for (int e = 0; e < 32; e += 2) {
+                float lo, hi;
+                ptx::unf2(ptx::mul2(ptx::f2(d[e], d[e + 1]), c2), lo, hi);
+                o[e / 2] = ptx::pack_bf16x2(lo, hi);
+              }
+            } else {
+#pragma unroll
+              for (int e = 0; e < 32; e += 2)
+                o[e / 2] = ptx::pack_bf16x2(__uint_as_float(x[e]), __uint_as_float(x[e + 1]));
             }
-          } else if constexpr (kMode == kDh) {
+            if (kMode == kDz || sh.splits == 1) {
+              // out through shared memory: 64 columns per box, in the TMA's
+              // swizzle (16-byte piece i of row r at piece i ^ (r % 8))
+              uint8_t* stage = S.out[wg * Smem::kOutBoxes + box];
+              const bool leader = (threadIdx.x & 127) == 0;
+              if ((c & 1) == 0) {
+                if (leader) ptx::bulk_wait_read<Smem::kOutBoxes - 1>();   // this box's last store
+                asm volatile("bar.sync %0, 128;" ::"r"(wg + 1) : "memory");
+              }
+#pragma unroll
+              for (int q = 0; q < 4; ++q)
+                *reinterpret_cast<uint4*>(stage + rc * 128 + ((((c & 1) * 4 + q) ^ (rc & 7)) * 16)) =
+                    make_uint4(o[4 * q], o[4 * q + 1], o[4 * q + 2], o[4 * q + 3]);
+              if ((c & 1) == 1) {
+                ptx::fence_async_shared();
+                asm volatile("bar.sync %0, 128;" ::"r"(wg + 1) : "memory");
+                const int col = c0 - 32;
+                const int first_row = w.m * kTile + static_cast<int>(rank) * kHalf;
+                const bool inside = kMode == kDz ? col < p.ld_dz : col < p.C && first_row < p.vcols;
+                if (leader) {
+                  if (inside) ptx::tma_store_2d(&tm_out, stage, col, kMode == kDw ? p.v0 + first_row : first_row);
+                  ptx::bulk_commit();
+                }
+                box = (box + 1) % Smem::kOutBoxes;
+              }
+            } else {
+              float4* ap = reinterpret_cast<float4*>(p.acc + tile_id * (kTile * kTile) + r * kTile + wg * kHalf + c * 32);
+#pragma unroll
+              for (int q = 0; q < 8; ++q)
+                ap[q] = make_float4(__uint_as_float(x[4 * q]), __uint_as_float(x[4 * q + 1]),
+                                    __uint_as_float(x[4 * q + 2]), __uint_as_float(x[4 * q + 3]));
+            }
+          } else {
             float* blk = p.acc + tile_id * (kTile * kTile) + r * kTile + wg * kHalf + c * 32;
             const bool out = p.last && sh.splits == 1;
 #pragma unroll
             for (int q = 0; q < 4; ++q) {
               float v[8];
 #pragma unroll
-              for (int e = 0; e < 8; ++e) v[e] = __uint_as_float(raw[8 * q + e]);
+              for (int e = 0; e < 8; ++e) v[e] = __uint_as_float(x[8 * q + e]);
               float4* ap = reinterpret_cast<float4*>(blk + 8 * q);
               if (!p.first) {
-                const float4 x = ap[0], y = ap[1];
-                v[0] += x.x; v[1] += x.y; v[2] += x.z; v[3] += x.w;
-                v[4] += y.x; v[5] += y.y; v[6] += y.z; v[7] += y.w;
+                const float4 y = ap[0], z = ap[1];
+                v[0] += y.x; v[1] += y.y; v[2] += y.z; v[3] += y.w;
+                v[4] += z.x; v[5] += z.y; v[6] += z.z; v[7] += z.w;
               }
               if (!out) {
                 ap[0] = make_float4(v[0], v[1], v[2], v[3]);
@@ -384,23 +455,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                                ptx::pack_bf16x2(v[4], v[5]), ptx::pack_bf16x2(v[6], v[7]));
               }
             }
-          } else {
-            if (sh.splits > 1) {
-              float4* ap = reinterpret_cast<float4*>(p.acc + tile_id * (kTile * kTile) + r * kTile + wg * kHalf + c * 32);
-#pragma unroll
-              for (int q = 0; q < 8; ++q)
-                ap[q] = make_float4(__uint_as_float(raw[4 * q]), __uint_as_float(raw[4 * q + 1]),
-                                    __uint_as_float(raw[4 * q + 2]), __uint_as_float(raw[4 * q + 3]));
-            } else if (row < p.vcols) {
-              __nv_bfloat16* dst = p.dw + (static_cast<int64_t>(p.v0) + row) * p.C + c0;
-#pragma unroll
-              for (int q = 0; q < 4; ++q)
-                if (c0 + 8 * q < p.C)
-                  *reinterpret_cast<uint4*>(dst + 8 * q) =
-                      make_uint4(ptx::pack_bf16x2(__uint_as_float(raw[8 * q]), __uint_as_float(raw[8 * q + 1])),
-                                 ptx::pack_bf16x2(__uint_as_float(raw[8 * q + 2]), __uint_as_float(raw[8 * q + 3])),
-                                 ptx::pack_bf16x2(__uint_as_float(raw[8 * q + 4]), __uint_as_float(raw[8 * q + 5])),
-                                 ptx::pack_bf16x2(__uint_as_float(raw[8 * q + 6]), __uint_as_float(raw[8 * q + 7])));
+          }
+          if (any && c < 3) {
+            ptx::tmem_wait_ld_of(raw[(c + 1) & 1]);
+            if (c == 2) {   // the whole tile has been read
+              ptx::tc_fence_before();
+              __syncwarp();
+              if (lane == 0) ptx::mbar_arrive_cluster(bar_empty[buf]);
             }
           }
         }
@@ -408,6 +469,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       if (kMode == kFwd && ok && row < count)
         p.part[(static_cast<int64_t>(w.n0 / sh.run) * 2 + wg) * p.np + row] = make_float2(m, s);
     }
+    if (Smem::kOut) ptx::bulk_wait_all();   // (of the threads that stored)
   }
   // Both CTAs leave together: nothing of the pair signals or reads a CTA that
   // has gone.  After a timeout the stages' copies are waited for first.
@@ -434,48 +496,53 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 // CTA: a few microseconds per 10,000 positions, against milliseconds of
 // products for as many.
 constexpr int kIndexThreads = 1024;
-constexpr int kIndexPer = 16;
+constexpr int kIndexPer = 16;   // positions per thread and step, 1,024 apart
 
 __global__ void __launch_bounds__(kIndexThreads) lm_index_kernel(const int32_t* __restrict__ target, int N, int V,
                                                                  int32_t* __restrict__ rows, int32_t* __restrict__ pos,
                                                                  int32_t* __restrict__ count) {
-  __shared__ int sums[2][32];
+  __shared__ int cnt[kIndexPer * 32];    // positions with a target: [e][warp], then how many before each
+  __shared__ int sums[kIndexPer + 1];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  int base = 0, turn = 0;
-  for (int i0 = 0; i0 < N; i0 += kIndexThreads * kIndexPer, turn ^= 1) {
-    const int i = i0 + threadIdx.x * kIndexPer;
-    bool on[kIndexPer];
-    int n = 0;
+  int base = 0;
+  for (int64_t i0 = 0; i0 < N; i0 += kIndexThreads * kIndexPer) {
+    unsigned on[kIndexPer];   // the warp's ballots
 #pragma unroll
     for (int e = 0; e < kIndexPer; ++e) {
-      const int t = i + e < N ? __ldg(target + i + e) : -1;
-      on[e] = t >= 0 && t < V;
-      n += on[e];
+      const int64_t i = i0 + e * kIndexThreads + threadIdx.x;
+      const int t = i < N ? __ldg(target + i) : -1;
+      on[e] = __ballot_sync(0xffffffffu, t >= 0 && t < V);
     }
-    int inc = n;
+    if (lane == 0)
 #pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const int v = __shfl_up_sync(0xffffffffu, inc, o);
-      if (lane >= o) inc += v;
-    }
-    if (lane == 31) sums[turn][warp] = inc;
+      for (int e = 0; e < kIndexPer; ++e) cnt[e * 32 + warp] = __popc(on[e]);
     __syncthreads();
-    int ws = sums[turn][lane];
+    if (warp < kIndexPer) {
+      const int v = cnt[warp * 32 + lane];
+      int inc = v;
 #pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const int v = __shfl_up_sync(0xffffffffu, ws, o);
-      if (lane >= o) ws += v;
-    }
-    const int all = __shfl_sync(0xffffffffu, ws, 31);
-    const int before = warp > 0 ? __shfl_sync(0xffffffffu, ws, warp - 1) : 0;
-    int at = base + before + inc - n;
-#pragma unroll
-    for (int e = 0; e < kIndexPer; ++e)
-      if (i + e < N) {
-        pos[i + e] = on[e] ? at : -1;
-        if (on[e]) rows[at++] = i + e;
+      for (int o = 1; o < 32; o <<= 1) {
+        const int u = __shfl_up_sync(0xffffffffu, inc, o);
+        if (lane >= o) inc += u;
       }
-    base += all;
+      cnt[warp * 32 + lane] = inc - v;
+      if (lane == 31) sums[warp] = inc;
+    }
+    __syncthreads();
+    int before = base;
+#pragma unroll
+    for (int e = 0; e < kIndexPer; ++e) {
+      const int64_t i = i0 + e * kIndexThreads + threadIdx.x;
+      if (i < N) {
+        const bool has = on[e] >> lane & 1;
+        const int at = before + cnt[e * 32 + warp] + __popc(on[e] & ((1u << lane) - 1));
+        pos[i] = has ? at : -1;
+        if (has) rows[at] = static_cast<int>(i);
+      }
+      before += sums[e];
+    }
+    base = before;
+    __syncthreads();
   }
   if (threadIdx.x == 0) *count = base;
 }
@@ -630,6 +697,36 @@ __global__ void __launch_bounds__(256) lm_few_kernel(const uint4* __restrict__ h
   }
 }
 
+// 8 columns of row r of a product that was split over K: its splits' sums.
+__device__ __forceinline__ uint4 sum_splits(const float* __restrict__ acc, int64_t r, int col, int mt, int nt, int splits) {
+  const float* from = acc + ((r / kTile) * nt + col / kTile) * (kTile * kTile) + (r % kTile) * kTile + col % kTile;
+  const int64_t step = static_cast<int64_t>(mt) * nt * (kTile * kTile);
+  float v[8] = {};
+  int s = 0;
+  for (; s + 4 <= splits; s += 4) {
+    float4 x[4], y[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      x[i] = __ldcg(reinterpret_cast<const float4*>(from + (s + i) * step));
+      y[i] = __ldcg(reinterpret_cast<const float4*>(from + (s + i) * step) + 1);
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      v[0] += x[i].x; v[1] += x[i].y; v[2] += x[i].z; v[3] += x[i].w;
+      v[4] += y[i].x; v[5] += y[i].y; v[6] += y[i].z; v[7] += y[i].w;
+    }
+  }
+  for (; s < splits; ++s) {
+    const float4 x = __ldcg(reinterpret_cast<const float4*>(from + s * step));
+    const float4 y = __ldcg(reinterpret_cast<const float4*>(from + s * step) + 1);
+    v[0] += x.x; v[1] += x.y; v[2] += x.z; v[3] += x.w;
+    v[4] += y.x; v[5] += y.y; v[6] += y.z; v[7] += y.w;
+  }
+  return make_uint4(ptx::pack_bf16x2(v[0], v[1]), ptx::pack_bf16x2(v[2], v[3]), ptx::pack_bf16x2(v[4], v[5]),
+                    ptx::pack_bf16x2(v[6], v[7]));
+}
+
+// A warp's share of a row: one 16-byte piece per lane; item = (row, 32 pieces).
 // dh of every position that the product's last epilogue has not written:
 // zero without a target, the sum of the splits over K where there are any.
 __global__ void __launch_bounds__(256) lm_dh_kernel(const float* __restrict__ acc, const int32_t* __restrict__ pos,
@@ -638,28 +735,14 @@ __global__ void __launch_bounds__(256) lm_dh_kernel(const float* __restrict__ ac
   const int lane = threadIdx.x & 31;
   const int mt = (__ldg(count) + kTile - 1) / kTile, nt = (C + kTile - 1) / kTile;
   const int splits = splits_for(mt * nt, split_most);
-  const int vecs = C / 8;
-  for (int64_t i = static_cast<int64_t>(blockIdx.x) * 8 + (threadIdx.x >> 5); i < N;
-       i += static_cast<int64_t>(gridDim.x) * 8) {
+  const int vecs = C / 8, parts = (vecs + 31) / 32;
+  for (int64_t it = static_cast<int64_t>(blockIdx.x) * 8 + (threadIdx.x >> 5); it < static_cast<int64_t>(N) * parts;
+       it += static_cast<int64_t>(gridDim.x) * 8) {
+    const int64_t i = it / parts;
+    const int c = static_cast<int>(it % parts) * 32 + lane;
     const int r = __ldg(pos + i);
-    if (r < 0) {
-      for (int c = lane; c < vecs; c += 32) dh[i * vecs + c] = make_uint4(0, 0, 0, 0);
-      continue;
-    }
-    if (splits == 1) continue;
-    for (int c = lane; c < vecs; c += 32) {
-      const int col = c * 8;
-      float v[8] = {};
-      for (int s = 0; s < splits; ++s) {
-        const int64_t tile = (static_cast<int64_t>(s) * mt + r / kTile) * nt + col / kTile;
-        const float4* a = reinterpret_cast<const float4*>(acc + tile * (kTile * kTile) + (r % kTile) * kTile + col % kTile);
-        const float4 x = a[0], y = a[1];
-        v[0] += x.x; v[1] += x.y; v[2] += x.z; v[3] += x.w;
-        v[4] += y.x; v[5] += y.y; v[6] += y.z; v[7] += y.w;
-      }
-      dh[i * vecs + c] = make_uint4(ptx::pack_bf16x2(v[0], v[1]), ptx::pack_bf16x2(v[2], v[3]),
-                                    ptx::pack_bf16x2(v[4], v[5]), ptx::pack_bf16x2(v[6], v[7]));
-    }
+    if (c >= vecs || (r >= 0 && splits == 1)) continue;
+    dh[i * vecs + c] = r < 0 ? make_uint4(0, 0, 0, 0) : sum_splits(acc, r, c * 8, mt, nt, splits);
   }
 }
 
@@ -670,22 +753,13 @@ __global__ void __launch_bounds__(256) lm_dw_kernel(const float* __restrict__ ac
   const int splits = dw_splits(mt * nt, (__ldg(count) + 63) / 64);
   if (splits == 1) return;
   const int lane = threadIdx.x & 31;
-  const int vecs = C / 8;
-  for (int64_t r = static_cast<int64_t>(blockIdx.x) * 8 + (threadIdx.x >> 5); r < vcols;
-       r += static_cast<int64_t>(gridDim.x) * 8)
-    for (int c = lane; c < vecs; c += 32) {
-      const int col = c * 8;
-      float v[8] = {};
-      for (int s = 0; s < splits; ++s) {
-        const int64_t tile = (static_cast<int64_t>(s) * mt + r / kTile) * nt + col / kTile;
-        const float4* a = reinterpret_cast<const float4*>(acc + tile * (kTile * kTile) + (r % kTile) * kTile + col % kTile);
-        const float4 x = a[0], y = a[1];
-        v[0] += x.x; v[1] += x.y; v[2] += x.z; v[3] += x.w;
-        v[4] += y.x; v[5] += y.y; v[6] += y.z; v[7] += y.w;
-      }
-      dw[(v0 + r) * vecs + c] = make_uint4(ptx::pack_bf16x2(v[0], v[1]), ptx::pack_bf16x2(v[2], v[3]),
-                                           ptx::pack_bf16x2(v[4], v[5]), ptx::pack_bf16x2(v[6], v[7]));
-    }
+  const int vecs = C / 8, parts = (vecs + 31) / 32;
+  for (int64_t it = static_cast<int64_t>(blockIdx.x) * 8 + (threadIdx.x >> 5); it < static_cast<int64_t>(vcols) * parts;
+       it += static_cast<int64_t>(gridDim.x) * 8) {
+    const int64_t r = it / parts;
+    const int c = static_cast<int>(it % parts) * 32 + lane;
+    if (c < vecs) dw[(v0 + r) * vecs + c] = sum_splits(acc, r, c * 8, mt, nt, splits);
+  }
 }
 
 // ---- host ------------------------------------------------------------------------
@@ -776,14 +850,15 @@ bool sizes_ok(int64_t N, int64_t V, int32_t C) {
 }
 
 template <int kMode>
-int launch_product(const CUtensorMap& a, const CUtensorMap& b, const LmParams& p, int64_t most_units, cudaStream_t s) {
+int launch_product(const CUtensorMap& a, const CUtensorMap& b, const CUtensorMap& out, const LmParams& p,
+                   int64_t most_units, cudaStream_t s) {
   static PerContext<int> rec;
-  int st = set_smem_once(rec, lm_product_kernel<kMode>, kLmSmemBytes);
+  int st = set_smem_once(rec, lm_product_kernel<kMode>, kLmSmemBytes<kMode>);
   if (st != TPK_OK) return st;
   int64_t pairs = num_sms() / 2;
   if (pairs < 1) pairs = 1;
   if (pairs > most_units) pairs = most_units;
-  lm_product_kernel<kMode><<<static_cast<unsigned>(2 * pairs), kThreads, kLmSmemBytes, s>>>(a, b, p);
+  lm_product_kernel<kMode><<<static_cast<unsigned>(2 * pairs), kThreads, kLmSmemBytes<kMode>, s>>>(a, b, out, p);
   return cuda_status(cudaGetLastError());
 }
 
@@ -870,7 +945,7 @@ extern "C" int tpk_lm_loss(const void* h, const void* w, const int32_t* target, 
     p.zt = k.zt;
     p.run = sh.run;
     p.err = dev_err;
-    st = launch_product<kFwd>(ma, mb, p, sh.np / kTile * sh.chunks, s);
+    st = launch_product<kFwd>(ma, mb, ma, p, sh.np / kTile * sh.chunks, s);
   }
   if (st != TPK_OK) return st;
   const int n = static_cast<int>(N), v = static_cast<int>(V);
@@ -902,12 +977,14 @@ extern "C" int tpk_lm_loss_bwd(const void* h, const void* w, const int32_t* targ
   if (st != TPK_OK) return st;
   const LmShape sh = lm_shape(N, V);
   st = gather_rows(h, target, N, V, C, k, s);
-  CUtensorMap hk, hm, wk, wm, zk, zm;   // h, w, dz: boxes of 128 rows (K-major) and of 64 (MN-major)
+  // h, w, dz: boxes of 128 rows (K-major operands, dz's and dw's way out) and of 64 (MN-major)
+  CUtensorMap hk, hm, wk, wm, zk, zm, dwk;
   if (st == TPK_OK) st = make_map_2d(&hk, k.hc, sh.np, C, C, kHalf);
   if (st == TPK_OK) st = make_map_2d(&hm, k.hc, sh.np, C, C, 64);
   if (st == TPK_OK) st = make_map_2d(&wk, w, V, C, C, kHalf);
   if (st == TPK_OK) st = make_map_2d(&wm, w, V, C, C, 64);
   if (st == TPK_OK) st = make_map_2d(&zk, k.dz, sh.np, sh.piece, sh.piece, kHalf);
+  if (st == TPK_OK) st = make_map_2d(&dwk, dw, V, C, C, kHalf);
   if (st == TPK_OK) st = make_map_2d(&zm, k.dz, sh.np, sh.piece, sh.piece, 64);
   LmParams p{};
   p.count = k.count;
@@ -934,19 +1011,19 @@ extern "C" int tpk_lm_loss_bwd(const void* h, const void* w, const int32_t* targ
     p.first = i == 0;
     p.last = i + 1 == sh.pieces;
     const int64_t vt = (p.vcols + kTile - 1) / kTile;
-    st = launch_product<kDz>(hk, wk, p, sh.np / kTile * vt, s);
+    st = launch_product<kDz>(hk, wk, zk, p, sh.np / kTile * vt, s);
     p.acc = k.acc_h;
-    if (st == TPK_OK) st = launch_product<kDh>(zk, wm, p, kSplitPairs > sh.np / kTile * ct ? kSplitPairs : sh.np / kTile * ct, s);
+    if (st == TPK_OK) st = launch_product<kDh>(zk, wm, zk, p, kSplitPairs > sh.np / kTile * ct ? kSplitPairs : sh.np / kTile * ct, s);
     p.acc = k.acc_w;
-    if (st == TPK_OK) st = launch_product<kDw>(zm, hm, p, kSplitPairs > vt * ct ? kSplitPairs : vt * ct, s);
-    if (st == TPK_OK && 2 * vt * ct <= kSplitPairs) {
-      lm_dw_kernel<<<static_cast<unsigned>(grid_for(p.vcols)), 256, 0, s>>>(k.acc_w, k.count, p.v0, p.vcols, C,
+    if (st == TPK_OK) st = launch_product<kDw>(zm, hm, dwk, p, kSplitPairs > vt * ct ? kSplitPairs : vt * ct, s);
+    if (st == TPK_OK && 2 * vt * ct <= kSplitPairs) {   // few enough tiles for a split
+      lm_dw_kernel<<<static_cast<unsigned>(grid_for(p.vcols * ((C / 8 + 31) / 32))), 256, 0, s>>>(k.acc_w, k.count, p.v0, p.vcols, C,
                                                                             static_cast<uint4*>(dw));
       st = cuda_status(cudaGetLastError());
     }
   }
   if (st != TPK_OK) return st;
-  lm_dh_kernel<<<static_cast<unsigned>(grid_for(N)), 256, 0, s>>>(k.acc_h, k.pos, k.count, static_cast<int>(N), C,
+  lm_dh_kernel<<<static_cast<unsigned>(grid_for(N * ((C / 8 + 31) / 32))), 256, 0, s>>>(k.acc_h, k.pos, k.count, static_cast<int>(N), C,
                                                                   p.split_most, static_cast<uint4*>(dh));
   return cuda_status(cudaGetLastError());
 }
