@@ -24,8 +24,11 @@ __device__ __forceinline__ uint32_t cluster_addr(const void* p, uint32_t rank) {
   asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(smem_addr(p)), "r"(rank));
   return r;
 }
+// Arrival on a barrier of either CTA.  It hands over TMEM columns, which the
+// tcgen05 fences order; the form that also releases memory to the cluster
+// waits for the warp's earlier global stores.
 __device__ __forceinline__ void mbar_arrive_cluster(uint32_t bar) {
-  asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
+  asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
 }
 // 2-d tile into this CTA's shared memory; the bytes are counted on `bar`, a
 // barrier of either CTA of the pair (address from cluster_addr).
