@@ -642,19 +642,27 @@ __global__ void __launch_bounds__(256) lm_join_kernel(const float2* __restrict__
 // Up to kFewRows positions (the log-probability of sampled tokens): one read
 // of w, which is all the time there is; a tile of 256 rows of the tensor path
 // would be almost empty and its 256-column tiles too few to share out evenly.
-// A warp takes four rows of w at a time, 256 channels per step, and keeps the
-// running (maximum, sum) of its rows' scores; the CTA's eight warps merge
-// theirs into one slot.
+// A warp takes a few rows of w at a time and keeps the running (maximum, sum)
+// of its rows' scores; the CTA's eight warps merge theirs into one slot.
 constexpr int kFewRows = 4;
 constexpr int kFewMost = 16384;      // fp32 values of h in shared memory
 constexpr int kFewBlocks = 608;      // slots
-constexpr int kFewV = 4;             // rows of w per warp and step
+// Rows of w per warp and step, steps of 256 channels loaded together, CTAs per
+// SM.  One position: 27.8 us at 32,000 ids of width 2,048 against 30.9 with
+// four rows and four steps; with more positions the sums take the registers.
+template <int kN>
+struct Few {
+  static constexpr int kV = kN == 1 ? 2 : 4;
+  static constexpr int kUnroll = kN == 1 ? 8 : 2;
+  static constexpr int kPerSm = kN == 1 ? 4 : kN == 2 ? 3 : 2;
+};
 
 template <int kN>
-__global__ void __launch_bounds__(256) lm_few_kernel(const uint4* __restrict__ h, const uint4* __restrict__ w,
+__global__ void __launch_bounds__(256, Few<kN>::kPerSm) lm_few_kernel(const uint4* __restrict__ h, const uint4* __restrict__ w,
                                                      const int32_t* __restrict__ target, int N, int V, int C,
                                                      int64_t np, float scale_log2, float2* __restrict__ part,
                                                      float* __restrict__ zt) {
+  constexpr int kFewV = Few<kN>::kV;
   extern __shared__ float4 hs[];     // [kN][C / 8] pairs of float4
   __shared__ float2 sm[8][kN];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -677,7 +685,7 @@ __global__ void __launch_bounds__(256) lm_few_kernel(const uint4* __restrict__ h
   const int64_t step = static_cast<int64_t>(gridDim.x) * 8 * kFewV;
   for (int64_t v0 = (static_cast<int64_t>(blockIdx.x) * 8 + warp) * kFewV; v0 < V; v0 += step) {
     uint64_t acc[kFewV][kN] = {};
-#pragma unroll 4
+#pragma unroll Few<kN>::kUnroll
     for (int c = lane; c < vecs; c += 32) {
       uint4 x[kFewV];
 #pragma unroll
@@ -909,11 +917,16 @@ int launch_product(const CUtensorMap& a, const CUtensorMap& b, const CUtensorMap
 
 template <int kN>
 int launch_few(const void* h, const void* w, const int32_t* target, int64_t N, int64_t V, int32_t C, int64_t np,
-               float scale_log2, int blocks, const LmWork& k, cudaStream_t s) {
+               float scale_log2, int* slots, const LmWork& k, cudaStream_t s) {
   static PerContext<int> rec;
   const int st = set_smem_once(rec, lm_few_kernel<kN>, sizeof(float) * kFewMost);
   if (st != TPK_OK) return st;
-  lm_few_kernel<kN><<<blocks, 256, static_cast<size_t>(kN) * C * 4, s>>>(
+  const int64_t want = (V + 8 * Few<kN>::kV - 1) / (8 * Few<kN>::kV);
+  int64_t blocks = int64_t{num_sms()} * Few<kN>::kPerSm;
+  blocks = blocks > kFewBlocks ? kFewBlocks : blocks;
+  blocks = want < blocks ? want : blocks;
+  *slots = static_cast<int>(blocks);
+  lm_few_kernel<kN><<<static_cast<unsigned>(blocks), 256, static_cast<size_t>(kN) * C * 4, s>>>(
       static_cast<const uint4*>(h), static_cast<const uint4*>(w), target, static_cast<int>(N), static_cast<int>(V), C,
       np, scale_log2, k.part, k.zt);
   return cuda_status(cudaGetLastError());
@@ -964,13 +977,9 @@ extern "C" int tpk_lm_loss(const void* h, const void* w, const int32_t* target, 
   const float scale_log2 = scale * kLog2e;
   int slots = 2 * sh.chunks;
   if (use_few(N, C)) {
-    const int64_t want = (V + 8 * kFewV - 1) / (8 * kFewV);
-    int64_t blocks = int64_t{num_sms()} * 4;
-    blocks = blocks > kFewBlocks ? kFewBlocks : blocks;
-    slots = static_cast<int>(want < blocks ? want : blocks);
-    st = few_rows(N) == 1   ? launch_few<1>(h, w, target, N, V, C, sh.np, scale_log2, slots, k, s)
-         : few_rows(N) == 2 ? launch_few<2>(h, w, target, N, V, C, sh.np, scale_log2, slots, k, s)
-                  : launch_few<4>(h, w, target, N, V, C, sh.np, scale_log2, slots, k, s);
+    st = few_rows(N) == 1   ? launch_few<1>(h, w, target, N, V, C, sh.np, scale_log2, &slots, k, s)
+         : few_rows(N) == 2 ? launch_few<2>(h, w, target, N, V, C, sh.np, scale_log2, &slots, k, s)
+                            : launch_few<4>(h, w, target, N, V, C, sh.np, scale_log2, &slots, k, s);
   } else {
     CUtensorMap ma, mb;
     if (st == TPK_OK) st = k.hc ? make_map_2d(&ma, k.hc, sh.np, C, C, kHalf) : make_map_2d(&ma, h, N, C, C, kHalf);

@@ -700,7 +700,7 @@ def embed(table, tokens, scale=1.0, out=None):
     out = torch.empty((N, C), dtype=torch.bfloat16, device=table.device) if out is None else out
     p_out = _arg(out, torch.bfloat16, (N, C), "out")
     dev = _device("table tokens out", table, tokens, out)
-    _launch(dev, lib.tpk_embed, p_table, _TABLE_TYPES[table.dtype], p_tok, p_out, N, V, C, scale)
+    _launch(dev, lib.tpk_embed, p_table, _TABLE_TYPES[table.dtype], p_tok, p_out, N, V, C, float(scale))
     return out
 
 
@@ -725,7 +725,7 @@ def embed_bwd(tokens, dout, vocab, scale=1.0, dtype=torch.float32, dtable=None, 
     p_dt = _arg(dtable, dtype, (V, C), "dtable")
     ws = _workspace(workspace, lib.tpk_embed_bwd_workspace_bytes(N, V, C), dout, "the lookup's backward")
     dev = _device("dout tokens dtable workspace", dout, tokens, dtable, ws)
-    _launch(dev, lib.tpk_embed_bwd, p_tok, p_dout, p_dt, _TABLE_TYPES[dtype], N, V, C, scale, ws.data_ptr(), ws.nbytes)
+    _launch(dev, lib.tpk_embed_bwd, p_tok, p_dout, p_dt, _TABLE_TYPES[dtype], N, V, C, float(scale), ws.data_ptr(), ws.nbytes)
     return dtable
 
 
@@ -784,7 +784,7 @@ def block_norm(res, w_pre, y=None, w_post=None, gate=None, scale=1.0, eps=1e-6, 
     out = torch.empty_like(res) if out is None else out
     p_out = _arg(out, torch.bfloat16, shape, "out")
     dev = _device("res w_pre y w_post gate res_out out", res, w_pre, y, w_post, gate, res_out, out)
-    _launch(dev, lib.tpk_block_norm, *args, p_ro, p_out, *shape, scale, eps)
+    _launch(dev, lib.tpk_block_norm, *args, p_ro, p_out, *shape, float(scale), float(eps))
     return (res if y is None else res_out), out
 
 
@@ -821,7 +821,7 @@ def block_norm_bwd(res, w_pre, dx, dres_out=None, y=None, w_post=None, gate=None
     dev = _device("res w_pre dx dres_out y w_post gate dres dy dgate dw_post dw_pre workspace", res, w_pre, dx, dres_out,
                   y, w_post, gate, dres, dy, dgate, dw_post, dw_pre, ws)
     _launch(dev, lib.tpk_block_norm_bwd, *args, p_dro, p_dx, p_dres, p_dy, ld_dy, p_dgate, ld_dgate, p_dpost, p_dpre,
-            *shape, scale, eps, ws.data_ptr(), ws.nbytes)
+            *shape, float(scale), float(eps), ws.data_ptr(), ws.nbytes)
     return dres, dy, dgate, dw_post, dw_pre
 
 
@@ -852,7 +852,7 @@ def lm_loss(h, w, target, scale=1.0, loss=None, lse=None, workspace=None, dev_er
     p_err = _dev_err(dev_err)
     ws = _workspace(workspace, lib.tpk_lm_loss_workspace_bytes(N, V, C, 0), h, "the loss")
     dev = _device("h w target loss lse workspace dev_err", h, w, target, loss, lse, ws, dev_err)
-    _launch(dev, lib.tpk_lm_loss, *args, p_loss, p_lse, N, V, C, scale, ws.data_ptr(), ws.nbytes, p_err)
+    _launch(dev, lib.tpk_lm_loss, *args, p_loss, p_lse, N, V, C, float(scale), ws.data_ptr(), ws.nbytes, p_err)
     return loss, lse
 
 
@@ -870,5 +870,5 @@ def lm_loss_bwd(h, w, target, lse, dloss, scale=1.0, dh=None, dw=None, workspace
     p_err = _dev_err(dev_err)
     ws = _workspace(workspace, lib.tpk_lm_loss_workspace_bytes(N, V, C, 1), h, "the loss's backward")
     dev = _device("h w target lse dloss dh dw workspace dev_err", h, w, target, lse, dloss, dh, dw, ws, dev_err)
-    _launch(dev, lib.tpk_lm_loss_bwd, *args, p_lse, p_dloss, p_dh, p_dw, N, V, C, scale, ws.data_ptr(), ws.nbytes, p_err)
+    _launch(dev, lib.tpk_lm_loss_bwd, *args, p_lse, p_dloss, p_dh, p_dw, N, V, C, float(scale), ws.data_ptr(), ws.nbytes, p_err)
     return dh, dw
