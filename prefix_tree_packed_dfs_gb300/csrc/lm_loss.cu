@@ -27,6 +27,13 @@
 // columns so that a tile's epilogue runs under the next tile's products.
 // One CTA with a 128 x 256 tile would load 96 bytes of operands per cycle and
 // SM at full tensor rate; the pair loads 64.
+// The tensor core adds to its fp32 accumulator with truncation, a bias towards
+// zero of half a unit per step of 16 that grows with the width (measured: a
+// score of 6 at width 4,096 came out 2.5e-5 low).  The forward's fp32 results
+// show it, so there a tile's products stop after every 512 elements of K
+// (kChunk stages) and the epilogue adds the chunks up in registers with
+// rounding to nearest.  dz, dh and dw are rounded to bf16, a hundred times
+// coarser, and accumulate over all of K.
 // Warps of a CTA: 0 TMA producer, 1 MMA issuer (of the pair's first CTA), 2
 // TMEM owner, 4-11 epilogue (two warpgroups, 128 columns each).  At widths
 // below about 1,000 the epilogue is what a tile waits for: its arithmetic is
@@ -53,6 +60,13 @@ constexpr int kPanel = 8;
 constexpr int kSplitPairs = 76;       // pairs a split over K aims to fill (two SMs each)
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
+
+constexpr int kChunk = 8;             // stages of 64 elements per accumulation of the forward
+// The forward's epilogue holds 128 columns of a row per thread: the other
+// warps give registers to its two warpgroups.
+constexpr uint32_t kRegsCtl = 56;
+constexpr uint32_t kRegsEpi = 216;
+constexpr int kRegsNeeded = 128 * kRegsCtl + 256 * kRegsEpi;
 
 enum { kFwd = 0, kDz = 1, kDh = 2, kDw = 3 };
 
@@ -232,7 +246,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   ptx::cluster_sync();   // the other CTA's barriers exist
   ptx::tc_fence_after();
   const uint32_t tmem = S.tmem_base;
-
+  if (warp < 4) {
+  if constexpr (kMode == kFwd) ptx::regs_dec<kRegsCtl>();
   if (warp == 0) {
     // ------------------------------------------------------------ producer
     if (ptx::elect_one()) {
@@ -284,14 +299,17 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       for (int u = pair; ok && u < sh.units; u += n_pairs) {
         const Unit w = unit_of<kMode>(p, sh, u);
         if (w.nk == 0) continue;
-        for (int j = 0; ok && j < w.n_run; ++j, ++tile) {
+        const int per = kMode == kFwd ? kChunk : w.nk;   // stages per accumulation
+        const int chunks = (w.nk + per - 1) / per;
+        for (int j = 0; ok && j < w.n_run * chunks; ++j, ++tile) {
           const uint32_t buf = tile & 1;
           if (tile >= 2 && !ptx::mbar_wait(&S.tm_empty[buf], (tile / 2 - 1) & 1, abort_flag, kWaitLimitNs)) {
             ok = false;
             break;
           }
           ptx::tc_fence_after();
-          for (int k = 0; k < w.nk; ++k, ++it) {
+          const int nk = min(per, w.nk - j % chunks * per);
+          for (int k = 0; k < nk; ++k, ++it) {
             const int st = it % kStages;
             if (!ptx::mbar_wait(&S.full[st], (it / kStages) & 1, abort_flag, kWaitLimitNs)) {
               ok = false;
@@ -313,8 +331,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       ptx::mma_commit_pair(&S.drain);
       ptx::mbar_drain(&S.drain, 0);
     }
-  } else if (warp >= 4) {
+  }
+  } else {
     // ------------------------------------------------------------ epilogue
+    if constexpr (kMode == kFwd) ptx::regs_inc<kRegsEpi>();
     const int wg = (warp - 4) >> 2;                     // column half
     const int lane = threadIdx.x & 31;
     const int rc = (warp & 3) * 32 + lane;              // row of this CTA's half tile
@@ -344,6 +364,77 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         }
       }
       for (int j = 0; j < w.n_run; ++j) {
+        if constexpr (kMode == kFwd) {
+          // the row's 128 columns as packed pairs, chunks of K added up
+          uint64_t z[kHalf / 2];
+          auto chunk = [&](bool first) {
+            const uint32_t buf = tile & 1;
+            if (!__all_sync(0xffffffffu, ptx::mbar_wait(&S.tm_full[buf], (tile / 2) & 1, abort_flag, kWaitLimitNs)))
+              return false;
+            ptx::tc_fence_after();
+            ++tile;
+            const uint32_t tm = tmem + lane_off + buf * kTile + wg * kHalf;
+#pragma unroll
+            for (int c = 0; c < 4; ++c) {
+              uint32_t x[32];
+              ptx::tmem_ld32(tm + c * 32, x);
+              ptx::tmem_wait_ld_of(x);
+#pragma unroll
+              for (int e = 0; e < 16; ++e) {
+                const uint64_t v = ptx::f2(__uint_as_float(x[2 * e]), __uint_as_float(x[2 * e + 1]));
+                z[c * 16 + e] = first ? v : ptx::add2(z[c * 16 + e], v);
+              }
+            }
+            ptx::tc_fence_before();
+            __syncwarp();
+            if (lane == 0) ptx::mbar_arrive_cluster(bar_empty[buf]);
+            return true;
+          };
+          ok = chunk(true);
+#pragma unroll 1
+          for (int k = kChunk; ok && k < w.nk; k += kChunk) ok = chunk(false);
+          if (!ok) break;
+          // unscaled scores and their maximum: the differences are exact to a
+          // rounding, which products with the scale would not leave them
+          const int c0 = (w.n0 + j) * kTile + wg * kHalf;
+          if (c0 + kHalf > p.V)
+#pragma unroll
+            for (int e = 0; e < kHalf / 2; ++e) {
+              float lo, hi;
+              ptx::unf2(z[e], lo, hi);
+              z[e] = ptx::f2(c0 + 2 * e < p.V ? lo : -INFINITY, c0 + 2 * e + 1 < p.V ? hi : -INFINITY);
+            }
+          if (static_cast<uint32_t>(tgt - c0) < static_cast<uint32_t>(kHalf) && tgt < p.V) {
+#pragma unroll
+            for (int e = 0; e < kHalf / 2; ++e) {
+              float lo, hi;
+              ptx::unf2(z[e], lo, hi);
+              if (tgt - c0 == 2 * e) p.zt[row] = lo;
+              if (tgt - c0 == 2 * e + 1) p.zt[row] = hi;
+            }
+          }
+          float top[4] = {m, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+          for (int e = 0; e < kHalf / 2; ++e) {
+            float lo, hi;
+            ptx::unf2(z[e], lo, hi);
+            top[e & 3] = ptx::max3(top[e & 3], lo, hi);
+          }
+          const float mn = ptx::max3(top[0], top[1], fmaxf(top[2], top[3]));
+          const float ms = mn == -INFINITY ? 0.f : mn;
+          const uint64_t neg = ptx::f2(-ms, -ms);
+          uint64_t q[4] = {ptx::f2(s * ptx::ex2((m - ms) * p.scale_log2), 0.f), 0, 0, 0};
+#pragma unroll
+          for (int e = 0; e < kHalf / 2; ++e) {
+            float lo, hi;
+            ptx::unf2(ptx::mul2(ptx::add2(z[e], neg), k2), lo, hi);
+            q[e & 3] = ptx::add2(q[e & 3], ptx::f2(ptx::ex2(lo), ptx::ex2(hi)));
+          }
+          float lo, hi;
+          ptx::unf2(ptx::add2(ptx::add2(q[0], q[1]), ptx::add2(q[2], q[3])), lo, hi);
+          s = lo + hi;
+          m = mn;
+        } else {
         const uint32_t buf = tile & 1;
         const bool any = kMode != kDw || w.nk > 0;   // no rows at all: dw is zero
         if (any) {
@@ -369,38 +460,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           uint32_t(&x)[32] = raw[c & 1];
           if (any && c < 3) ptx::tmem_ld32(tm + (c + 1) * 32, raw[(c + 1) & 1]);
           const int c0 = n0 + c * 32;
-          if constexpr (kMode == kFwd) {
-            // unscaled scores and their maximum: the differences are exact to
-            // a rounding, which products with the scale would not leave them
-            if (c0 + 32 > p.V)
-#pragma unroll
-              for (int e = 0; e < 32; ++e)
-                if (c0 + e >= p.V) x[e] = 0xff800000u;   // -inf
-            if (static_cast<uint32_t>(tgt - c0) < 32u && tgt < p.V) {
-#pragma unroll
-              for (int e = 0; e < 32; ++e)
-                if (tgt - c0 == e) p.zt[row] = __uint_as_float(x[e]);
-            }
-            float top[4] = {m, -INFINITY, -INFINITY, -INFINITY};
-#pragma unroll
-            for (int e = 0; e < 32; e += 2)
-              top[(e / 2) & 3] = ptx::max3(top[(e / 2) & 3], __uint_as_float(x[e]), __uint_as_float(x[e + 1]));
-            const float mn = ptx::max3(top[0], top[1], fmaxf(top[2], top[3]));
-            const float ms = mn == -INFINITY ? 0.f : mn;
-            const uint64_t neg = ptx::f2(-ms, -ms);
-            uint64_t q[2] = {ptx::f2(s * ptx::ex2((m - ms) * p.scale_log2), 0.f), 0};
-#pragma unroll
-            for (int e = 0; e < 32; e += 2) {
-              const uint64_t d = ptx::add2(ptx::f2(__uint_as_float(x[e]), __uint_as_float(x[e + 1])), neg);
-              float lo, hi;
-              ptx::unf2(ptx::mul2(d, k2), lo, hi);
-              q[(e / 2) & 1] = ptx::add2(q[(e / 2) & 1], ptx::f2(ptx::ex2(lo), ptx::ex2(hi)));
-            }
-            float lo, hi;
-            ptx::unf2(ptx::add2(q[0], q[1]), lo, hi);
-            s = lo + hi;
-            m = mn;
-          } else if constexpr (kMode == kDz || kMode == kDw) {
+          if constexpr (kMode == kDz || kMode == kDw) {
             uint32_t o[16];
             if constexpr (kMode == kDz) {
               const uint64_t minus = ptx::f2(-lse2, -lse2), c2 = ptx::f2(coef, coef);
@@ -496,6 +556,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
               if (lane == 0) ptx::mbar_arrive_cluster(bar_empty[buf]);
             }
           }
+        }
         }
       }
       if (kMode == kFwd && ok && row < count)
@@ -906,7 +967,15 @@ template <int kMode>
 int launch_product(const CUtensorMap& a, const CUtensorMap& b, const CUtensorMap& out, const LmParams& p,
                    int64_t most_units, cudaStream_t s) {
   static PerContext<int> rec;
-  int st = set_smem_once(rec, lm_product_kernel<kMode>, kLmSmemBytes<kMode>);
+  int unused = 0;
+  const int st = rec.get(&unused, [](int*) {
+    cudaFuncAttributes fa;
+    if (cudaFuncGetAttributes(&fa, lm_product_kernel<kMode>) != cudaSuccess) return TPK_E_CUDA;
+    // setmaxnreg waits for registers the CTA was not launched with
+    if (kMode == kFwd && fa.numRegs * kThreads < kRegsNeeded) return TPK_E_UNSUPPORTED;
+    return cuda_status(cudaFuncSetAttribute(lm_product_kernel<kMode>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                            static_cast<int>(kLmSmemBytes<kMode>)));
+  });
   if (st != TPK_OK) return st;
   int64_t pairs = num_sms() / 2;
   if (pairs < 1) pairs = 1;

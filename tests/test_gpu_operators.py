@@ -327,6 +327,19 @@ def test_lm_loss_and_gradients(ops, n, v, c, on, scale):
     assert torch.equal(again[0], dh) and torch.equal(again[1], dw)              # deterministic
 
 
+def test_lm_loss_scores_do_not_drift_with_the_width(ops):
+    """Products of one sign, 16,384 channels: an accumulator that is truncated
+    1,024 times drifts by up to 1024 * 2^-23.  A score is added up in chunks of
+    512 channels: at most 32 truncations of one unit (2^-23) each, then 32
+    roundings (2^-24) of the running sum; lse adds the logarithm and its own
+    roundings of |lse| (2^-22)."""
+    n, c = 300, 16384
+    h, w = _rnd(55, n, c).abs(), _rnd(56, 3, c, std=0.01).abs()
+    lse = ops.lm_loss(h, w, torch.zeros(n, dtype=torch.int32, device="cuda"))[1].double()
+    ref = torch.logsumexp(h.double() @ w.double().T, 1)
+    assert ((lse - ref).abs() <= (32 * 2.0 ** -23 + 32 * 2.0 ** -24 + 2.0 ** -22) * ref).all()
+
+
 def test_lm_loss_pieces(ops):
     """More than one piece of the vocabulary: dz would take more than 4 GiB.
     Sampled rows of dh and dw against fp64."""
