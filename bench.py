@@ -113,6 +113,9 @@ def _args():
     ap.add_argument("--layout", action="store_true",
                     help="raw order <-> packed layout kernels (materialisation gather, sum of raw-order rows) "
                          "on --workload; one line")
+    ap.add_argument("--operators", action="store_true",
+                    help="embedding, block norms and vocabulary loss, forward and backward, on --workload's packed "
+                         "positions (width Hq * head_dim, 32,000 ids); one line")
     ap.add_argument("--sweep", action="store_true",
                     help="packing-ratio sweep (32,768-token rows): forward time against forwarded and raw "
                          "tokens, tree layout vs sequence packing of the same raw tokens; one line per point")
@@ -919,6 +922,71 @@ def run_layout(a):
                       "l2": "flushed (256 MiB write) before every timed launch"}), flush=True)
 
 
+def run_operators(a):
+    """The operators around the token mixers on one workload's packed
+    positions: width Hq * head_dim, the workloads' 32,000 token ids, targets
+    the next packed token of every position that has one.  L2 flushed before
+    every timed call; one JSON line."""
+    import torch
+    import workloads
+    from prefix_tree_packed_dfs_gb300 import ops
+    from workloads import rng as wrng
+    peaks = _peaks()
+    flush = torch.empty(256 << 20, dtype=torch.uint8, device="cuda")
+    w = workloads.get(a.workload)
+    plan = ops.Plan.from_sequences(w.sequences, group_ids=w.group_ids, row_capacity=w.row_capacity,
+                                   min_shared=w.min_shared)
+    dp = plan.to_device()
+    F, C, V = plan.info["n_fwd"], w.n_heads_q * w.head_dim, workloads.VOCAB
+    nxt = np.concatenate([np.append(s[1:], -1) for s in w.sequences]).astype(np.int32)
+    tok = ops.gather_to_forwarded(dp, torch.from_numpy(np.concatenate(w.sequences).astype(np.int32)).cuda())
+    target = ops.gather_to_forwarded(dp, torch.from_numpy(nxt).cuda())
+    seed = w.seed_base + 70
+    table = wrng.normal_bf16(seed, (V, C), "cuda")
+    rows = [wrng.normal_bf16(seed + 1 + i, (F, C), "cuda") for i in range(5)]
+    res, y, gate, dx, dr = rows
+    wn = torch.ones(C, device="cuda")
+    dloss = torch.full((F,), 1.0 / F, device="cuda")
+    h = rows[0]
+    loss, lse = ops.lm_loss(h, table, target, scale=C ** -0.5)
+    n_on = int((target >= 0).sum())
+
+    def timed(fn):
+        for _ in range(a.warmup):
+            fn()
+        times = []
+        for _ in range(max(a.steps, 3)):
+            flush.fill_(1)
+            e0, e1 = torch.cuda.Event(enable_timing=True), torch.cuda.Event(enable_timing=True)
+            e0.record()
+            fn()
+            e1.record()
+            torch.cuda.synchronize()
+            times.append(e0.elapsed_time(e1))
+        return statistics.median(times)
+
+    out = {}
+    for name, fn, nbytes, flops in (
+            ("embed", lambda: ops.embed(table, tok), (min(F, V) + F) * C * 2 + 4 * F, 0),
+            ("embed_bwd", lambda: ops.embed_bwd(tok, dx, V), F * C * 2 + 4 * F + V * C * 4, 0),
+            ("block_norm", lambda: ops.block_norm(res, wn, y=y, w_post=wn, gate=gate), 10 * F * C, 0),
+            ("block_norm_bwd", lambda: ops.block_norm_bwd(res, wn, dx, dres_out=dr, y=y, w_post=wn, gate=gate),
+             16 * F * C, 0),
+            ("lm_loss", lambda: ops.lm_loss(h, table, target, scale=C ** -0.5), (F + V) * C * 2, 2 * n_on * V * C),
+            ("lm_loss_bwd", lambda: ops.lm_loss_bwd(h, table, target, lse, dloss, scale=C ** -0.5),
+             2 * (F + V) * C * 2, 6 * n_on * V * C)):
+        ms = timed(fn)
+        out[name] = {"ms": ms, "algorithmic_bytes": nbytes, "gbs": nbytes / ms / 1e6,
+                     "frac_of_copy_peak": nbytes / ms / 1e6 / peaks["hbm_gbs"]}
+        if flops:   # the backward's count holds the recomputed scores
+            out[name].update(tflops=flops / ms / 1e9, frac_of_sustained=flops / ms / 1e9 / peaks["bf16_tflops_sustained"])
+    print(json.dumps({"mode": "operators", "workload": a.workload, "positions": F, "with_target": n_on, "width": C,
+                      "vocabulary": V, "operators": out, "peak_gbs": peaks["hbm_gbs"],
+                      "peak_tflops_sustained": peaks["bf16_tflops_sustained"],
+                      "peak_kind": "copy bandwidth and bf16 products (%s)" % peaks["source"],
+                      "l2": "flushed (256 MiB write) before every timed call"}), flush=True)
+
+
 def _time_library_planner(ops, w):
     """(first build ms, median of three further builds ms, last plan).  Each
     plan is destroyed before the next build, as a loop that plans one batch
@@ -995,6 +1063,8 @@ def main():
         run_sweep(a)
     elif a.layout:
         run_layout(a)
+    elif a.operators:
+        run_operators(a)
     elif a.gdn:
         import torch
         print(json.dumps({"mode": "gdn", **run_gdn(_peaks(), 0, max(a.warmup, 1), names=(a.workload,))}), flush=True)

@@ -15,27 +15,21 @@
 // The weights' gradients are column sums: every group of threads keeps its
 // own columns' sums over the rows it walks and writes them once, and a second
 // kernel adds the groups in order (deterministic).
-#include <cuda_bf16.h>
-
 #include <type_traits>
 
-#include "common.cuh"
 #include "ptx.cuh"
+#include "rowwise.cuh"
 
 namespace tpk {
 namespace {
 
 constexpr int kVec = 2;   // 16-byte pieces (8 channels) per thread: kT * 16 >= C
 
-__device__ __forceinline__ uint32_t pack2(float a, float b) {
-  const __nv_bfloat162 v = __floats2bfloat162_rn(a, b);
-  return *reinterpret_cast<const uint32_t*>(&v);
-}
 __device__ __forceinline__ void unpack8(uint4 u, float (&f)[8]) {
-  f[0] = __uint_as_float(u.x << 16); f[1] = __uint_as_float(u.x & 0xFFFF0000u);
-  f[2] = __uint_as_float(u.y << 16); f[3] = __uint_as_float(u.y & 0xFFFF0000u);
-  f[4] = __uint_as_float(u.z << 16); f[5] = __uint_as_float(u.z & 0xFFFF0000u);
-  f[6] = __uint_as_float(u.w << 16); f[7] = __uint_as_float(u.w & 0xFFFF0000u);
+  f[0] = lo16(u.x); f[1] = hi16(u.x);
+  f[2] = lo16(u.y); f[3] = hi16(u.y);
+  f[4] = lo16(u.z); f[5] = hi16(u.z);
+  f[6] = lo16(u.w); f[7] = hi16(u.w);
 }
 __device__ __forceinline__ uint4 pack8(const float (&f)[8]) {
   return make_uint4(pack2(f[0], f[1]), pack2(f[2], f[3]), pack2(f[4], f[5]), pack2(f[6], f[7]));
@@ -58,7 +52,7 @@ struct Oct {
   uint64_t v[4];
 };
 __device__ __forceinline__ uint64_t pair_of(uint32_t u) {
-  return ptx::f2(__uint_as_float(u << 16), __uint_as_float(u & 0xFFFF0000u));
+  return ptx::f2(lo16(u), hi16(u));
 }
 __device__ __forceinline__ Oct oct(uint4 u) { return {{pair_of(u.x), pair_of(u.y), pair_of(u.z), pair_of(u.w)}}; }
 __device__ __forceinline__ Oct load_oct(const float* p) {

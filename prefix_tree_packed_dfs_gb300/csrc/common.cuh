@@ -64,23 +64,6 @@ inline int make_map_bf16(CUtensorMap* map, const void* base, int64_t rows, int h
   return r == CUDA_SUCCESS ? TPK_OK : TPK_E_CUDA;
 }
 
-// Tensor map over a row-major bf16 matrix [rows, cols] with row stride ld
-// (elements), 128-byte swizzle, box of 64 columns (128 bytes) x box_rows rows.
-// Elements outside the matrix read as zero.
-inline int make_map_2d(CUtensorMap* map, const void* base, int64_t rows, int64_t cols, int64_t ld, int box_rows) {
-  auto fn = encode_fn();
-  if (!fn) return TPK_E_CUDA;
-  if (reinterpret_cast<uintptr_t>(base) % 16 || ld % 8) return TPK_E_ARG;
-  cuuint64_t dims[2] = {static_cast<cuuint64_t>(cols), static_cast<cuuint64_t>(rows)};
-  cuuint64_t strides[1] = {static_cast<cuuint64_t>(ld) * 2};
-  cuuint32_t box[2] = {64, static_cast<cuuint32_t>(box_rows)};
-  cuuint32_t estride[2] = {1, 1};
-  CUresult r = fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(base), dims, strides, box, estride,
-                  CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-                  CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
-  return r == CUDA_SUCCESS ? TPK_OK : TPK_E_CUDA;
-}
-
 // Unique id of the CUDA context the calling thread's runtime calls act on
 // (the device's primary context unless the caller made another one current).
 // Ids are never reused within a process, so a context created after
@@ -149,10 +132,6 @@ int set_smem_once(PerContext<int>& rec, Kern kern, size_t bytes) {
                : TPK_E_CUDA;
   });
 }
-
-// Most SMs of any part this library runs on (workspace sizes that must not
-// depend on the current device count on it).
-constexpr int kMaxSms = 256;
 
 inline int num_sms() {
   int dev = 0, n = 0;

@@ -15,21 +15,12 @@
 // pieces.  Rows of ids that do not occur are zeroed by other blocks of the
 // same launch, which look the id up in the sorted order (32-way search, so
 // the table is written once instead of cleared and written again).
-#include <cuda_bf16.h>
-
-#include "common.cuh"
+#include "rowwise.cuh"
 
 namespace tpk {
 namespace {
 
 constexpr int kThreads = 256;
-
-__device__ __forceinline__ uint32_t pack2(float a, float b) {
-  const __nv_bfloat162 v = __floats2bfloat162_rn(a, b);
-  return *reinterpret_cast<const uint32_t*>(&v);
-}
-__device__ __forceinline__ float lo16(uint32_t u) { return __uint_as_float(u << 16); }
-__device__ __forceinline__ float hi16(uint32_t u) { return __uint_as_float(u & 0xFFFF0000u); }
 
 __device__ __forceinline__ uint4 scale8(uint4 x, float s) {
   return make_uint4(pack2(lo16(x.x) * s, hi16(x.x) * s), pack2(lo16(x.y) * s, hi16(x.y) * s),

@@ -43,10 +43,8 @@
 // the time).  CTAs are
 // persistent and walk the tiles in panels of 8 columns of tiles, so the pairs
 // running together share rows of A and of B in L2.
-#include <cuda_bf16.h>
-
-#include "common.cuh"
 #include "pair.cuh"
+#include "rowwise.cuh"
 
 namespace tpk {
 namespace {
@@ -730,10 +728,10 @@ __global__ void __launch_bounds__(256, Few<kN>::kPerSm) lm_few_kernel(const uint
   const int vecs = C / 8;
   for (int i = threadIdx.x; i < kN * vecs; i += 256) {
     const uint4 x = i / vecs < N ? __ldg(h + i) : make_uint4(0, 0, 0, 0);
-    hs[2 * i] = make_float4(__uint_as_float(x.x << 16), __uint_as_float(x.x & 0xFFFF0000u), __uint_as_float(x.y << 16),
-                            __uint_as_float(x.y & 0xFFFF0000u));
-    hs[2 * i + 1] = make_float4(__uint_as_float(x.z << 16), __uint_as_float(x.z & 0xFFFF0000u),
-                                __uint_as_float(x.w << 16), __uint_as_float(x.w & 0xFFFF0000u));
+    hs[2 * i] = make_float4(lo16(x.x), hi16(x.x), lo16(x.y),
+                            hi16(x.y));
+    hs[2 * i + 1] = make_float4(lo16(x.z), hi16(x.z),
+                                lo16(x.w), hi16(x.w));
   }
   int tgt[kN];
   float2 st[kN];
@@ -757,7 +755,7 @@ __global__ void __launch_bounds__(256, Few<kN>::kPerSm) lm_few_kernel(const uint
         const ulonglong2 a = ptx::lds128u(hs + 2 * (n * vecs + c)), b = ptx::lds128u(hs + 2 * (n * vecs + c) + 1);
 #pragma unroll
         for (int i = 0; i < kFewV; ++i) {
-          auto pair = [](uint32_t u) { return ptx::f2(__uint_as_float(u << 16), __uint_as_float(u & 0xFFFF0000u)); };
+          auto pair = [](uint32_t u) { return ptx::f2(lo16(u), hi16(u)); };
           acc[i][n] = ptx::fma2(pair(x[i].x), a.x, acc[i][n]);
           acc[i][n] = ptx::fma2(pair(x[i].y), a.y, acc[i][n]);
           acc[i][n] = ptx::fma2(pair(x[i].z), b.x, acc[i][n]);
@@ -1015,8 +1013,6 @@ int gather_rows(const void* h, const int32_t* target, int64_t N, int64_t V, int3
       static_cast<const uint4*>(h), w.rows, w.count, C / 8, reinterpret_cast<uint4*>(w.hc));
   return cuda_status(cudaGetLastError());
 }
-
-bool aligned16(const void* p) { return reinterpret_cast<uintptr_t>(p) % 16 == 0; }
 
 }  // namespace
 }  // namespace tpk
