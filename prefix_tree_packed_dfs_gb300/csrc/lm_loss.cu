@@ -403,13 +403,18 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
               z[e] = ptx::f2(c0 + 2 * e < p.V ? lo : -INFINITY, c0 + 2 * e + 1 < p.V ? hi : -INFINITY);
             }
           if (static_cast<uint32_t>(tgt - c0) < static_cast<uint32_t>(kHalf) && tgt < p.V) {
+            // the target's score, halving the columns by the bits of its place
+            uint64_t y[kHalf / 4];
+            const int at = tgt - c0;
 #pragma unroll
-            for (int e = 0; e < kHalf / 2; ++e) {
-              float lo, hi;
-              ptx::unf2(z[e], lo, hi);
-              if (tgt - c0 == 2 * e) p.zt[row] = lo;
-              if (tgt - c0 == 2 * e + 1) p.zt[row] = hi;
-            }
+            for (int e = 0; e < 32; ++e) y[e] = at & 64 ? z[32 + e] : z[e];
+#pragma unroll
+            for (int half = 16; half > 0; half >>= 1)
+#pragma unroll
+              for (int e = 0; e < half; ++e) y[e] = at & (2 * half) ? y[half + e] : y[e];
+            float lo, hi;
+            ptx::unf2(y[0], lo, hi);
+            p.zt[row] = at & 1 ? hi : lo;
           }
           float top[4] = {m, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
@@ -583,74 +588,104 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 }
 
 // ---- gathering the positions that have a target ------------------------------
-// rows[0..count) = those positions, ascending; pos[f] = its row or -1.  One
-// CTA: a few microseconds per 10,000 positions, against milliseconds of
-// products for as many.
-constexpr int kIndexThreads = 1024;
-constexpr int kIndexPer = 16;   // positions per thread and step, 1,024 apart
+// rows[0..count) = those positions, ascending; pos[f] = its row or -1; hc[r] =
+// h[rows[r]], rows up to the next multiple of 256 zero.  One launch: a CTA
+// takes a run of positions and counts the targets before it itself (every CTA
+// reads all of target, a few bytes per position against a row's thousands).
+constexpr int kRowsThreads = 512;
+constexpr int kRowsBlocks = 304;
+constexpr int kRowsLeast = 16;   // positions per CTA
 
-__global__ void __launch_bounds__(kIndexThreads) lm_index_kernel(const int32_t* __restrict__ target, int N, int V,
-                                                                 int32_t* __restrict__ rows, int32_t* __restrict__ pos,
-                                                                 int32_t* __restrict__ count) {
-  __shared__ int cnt[kIndexPer * 32];    // positions with a target: [e][warp], then how many before each
-  __shared__ int sums[kIndexPer + 1];
+__global__ void __launch_bounds__(kRowsThreads) lm_rows_kernel(const int32_t* __restrict__ target, int N, int V,
+                                                               const uint4* __restrict__ h, int vecs, int ld,
+                                                               int per, int32_t* __restrict__ rows,
+                                                               int32_t* __restrict__ pos, int32_t* __restrict__ count,
+                                                               uint4* __restrict__ hc) {
+  constexpr int kWarps = kRowsThreads / 32;
+  __shared__ int sums[2][kWarps];
+  __shared__ int list[kRowsThreads];   // positions with a target of the 512 at hand
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  int base = 0;
-  for (int64_t i0 = 0; i0 < N; i0 += kIndexThreads * kIndexPer) {
-    unsigned on[kIndexPer];   // the warp's ballots
-#pragma unroll
-    for (int e = 0; e < kIndexPer; ++e) {
-      const int64_t i = i0 + e * kIndexThreads + threadIdx.x;
-      const int t = i < N ? __ldg(target + i) : -1;
-      on[e] = __ballot_sync(0xffffffffu, t >= 0 && t < V);
+  const int64_t lo = static_cast<int64_t>(blockIdx.x) * per;
+  const int64_t hi = lo + per < N ? lo + per : N;
+  int before = 0, all = 0;
+  auto add = [&](int64_t i, int t) {
+    const int on = t >= 0 && t < V;
+    all += on;
+    before += i < lo ? on : 0;
+  };
+  int64_t i0 = 0;
+  if (reinterpret_cast<uintptr_t>(target) % 16 == 0) {
+    const int64_t quads = N / 4;
+#pragma unroll 4
+    for (int64_t q = threadIdx.x; q < quads; q += kRowsThreads) {
+      const int4 t = __ldg(reinterpret_cast<const int4*>(target) + q);
+      add(4 * q, t.x);
+      add(4 * q + 1, t.y);
+      add(4 * q + 2, t.z);
+      add(4 * q + 3, t.w);
     }
-    if (lane == 0)
-#pragma unroll
-      for (int e = 0; e < kIndexPer; ++e) cnt[e * 32 + warp] = __popc(on[e]);
-    __syncthreads();
-    if (warp < kIndexPer) {
-      const int v = cnt[warp * 32 + lane];
-      int inc = v;
-#pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const int u = __shfl_up_sync(0xffffffffu, inc, o);
-        if (lane >= o) inc += u;
-      }
-      cnt[warp * 32 + lane] = inc - v;
-      if (lane == 31) sums[warp] = inc;
-    }
-    __syncthreads();
-    int before = base;
-#pragma unroll
-    for (int e = 0; e < kIndexPer; ++e) {
-      const int64_t i = i0 + e * kIndexThreads + threadIdx.x;
-      if (i < N) {
-        const bool has = on[e] >> lane & 1;
-        const int at = before + cnt[e * 32 + warp] + __popc(on[e] & ((1u << lane) - 1));
-        pos[i] = has ? at : -1;
-        if (has) rows[at] = static_cast<int>(i);
-      }
-      before += sums[e];
-    }
-    base = before;
-    __syncthreads();
+    i0 = 4 * quads;
   }
-  if (threadIdx.x == 0) *count = base;
+#pragma unroll 8
+  for (int64_t i = i0 + threadIdx.x; i < N; i += kRowsThreads) add(i, __ldg(target + i));
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) {
+    before += __shfl_xor_sync(0xffffffffu, before, o);
+    all += __shfl_xor_sync(0xffffffffu, all, o);
+  }
+  if (lane == 0) {
+    sums[0][warp] = before;
+    sums[1][warp] = all;
+  }
+  __syncthreads();
+  before = all = 0;
+#pragma unroll
+  for (int w = 0; w < kWarps; ++w) {
+    before += sums[0][w];
+    all += sums[1][w];
+  }
+  if (blockIdx.x == 0 && threadIdx.x == 0) *count = all;
+  for (int64_t at = lo; at < hi; at += kRowsThreads) {
+    __syncthreads();   // sums and list of the step before have been read
+    const int64_t i = at + threadIdx.x;
+    const int t = i < hi ? __ldg(target + i) : -1;
+    const bool on = t >= 0 && t < V;
+    const unsigned mask = __ballot_sync(0xffffffffu, on);
+    if (lane == 0) sums[0][warp] = __popc(mask);
+    __syncthreads();
+    int mine = __popc(mask & ((1u << lane) - 1)), n = 0;
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) {
+      mine += w < warp ? sums[0][w] : 0;
+      n += sums[0][w];
+    }
+    if (i < hi) pos[i] = on ? before + mine : -1;
+    if (on) {
+      rows[before + mine] = static_cast<int>(i);
+      list[mine] = static_cast<int>(i);
+    }
+    __syncthreads();
+    for (int k = warp; k < n; k += kWarps) {
+      const uint4* src = h + static_cast<int64_t>(list[k]) * vecs;
+      uint4* dst = hc + static_cast<int64_t>(before + k) * ld;
+#pragma unroll 4
+      for (int c = lane; c < vecs; c += 32) dst[c] = __ldg(src + c);
+    }
+    before += n;
+  }
+  const int padded = (all + kTile - 1) / kTile * kTile;
+  for (int r = all + static_cast<int>(blockIdx.x) * kWarps + warp; r < padded; r += static_cast<int>(gridDim.x) * kWarps)
+    for (int c = lane; c < vecs; c += 32) hc[static_cast<int64_t>(r) * ld + c] = make_uint4(0, 0, 0, 0);
 }
 
-// hc[r] = h[rows[r]]; rows up to the next multiple of 256 are zero.
-__global__ void __launch_bounds__(256) lm_gather_kernel(const uint4* __restrict__ h, const int32_t* __restrict__ rows,
-                                                        const int32_t* __restrict__ count, int vecs,
-                                                        uint4* __restrict__ hc) {
+// w with rows 128 bytes aligned.
+__global__ void __launch_bounds__(256) lm_align_kernel(const uint4* __restrict__ w, int V, int vecs, int ld,
+                                                       uint4* __restrict__ wc) {
   const int lane = threadIdx.x & 31;
-  const int n = __ldg(count), padded = (n + kTile - 1) / kTile * kTile;
-  for (int64_t r = static_cast<int64_t>(blockIdx.x) * 8 + (threadIdx.x >> 5); r < padded;
-       r += static_cast<int64_t>(gridDim.x) * 8) {
-    const uint4* src = r < n ? h + static_cast<int64_t>(__ldg(rows + r)) * vecs : nullptr;
-    uint4* dst = hc + r * vecs;
+  for (int64_t r = static_cast<int64_t>(blockIdx.x) * 8 + (threadIdx.x >> 5); r < V;
+       r += static_cast<int64_t>(gridDim.x) * 8)
 #pragma unroll 4
-    for (int c = lane; c < vecs; c += 32) dst[c] = src ? __ldg(src + c) : make_uint4(0, 0, 0, 0);
-  }
+    for (int c = lane; c < vecs; c += 32) wc[r * ld + c] = __ldg(w + r * vecs + c);
 }
 
 // (maximum, sum of exponentials of scale * (score - maximum)) of two sets of scores.
@@ -835,13 +870,19 @@ __global__ void __launch_bounds__(256) lm_dh_kernel(const float* __restrict__ ac
   const int mt = (__ldg(count) + kTile - 1) / kTile, nt = (C + kTile - 1) / kTile;
   const int splits = splits_for(static_cast<int64_t>(mt) * nt, split_most);
   const int vecs = C / 8, parts = (vecs + 31) / 32;
-  for (int64_t it = static_cast<int64_t>(blockIdx.x) * 8 + (threadIdx.x >> 5); it < static_cast<int64_t>(N) * parts;
-       it += static_cast<int64_t>(gridDim.x) * 8) {
+  const int64_t first = static_cast<int64_t>(blockIdx.x) * 8 + (threadIdx.x >> 5);
+  const int64_t step = static_cast<int64_t>(gridDim.x) * 8;
+  if (splits == 1) {   // rows without a target alone
+    for (int64_t i = first; i < N; i += step)
+      if (__ldg(pos + i) < 0)
+        for (int c = lane; c < vecs; c += 32) dh[i * vecs + c] = make_uint4(0, 0, 0, 0);
+    return;
+  }
+  for (int64_t it = first; it < static_cast<int64_t>(N) * parts; it += step) {
     const int64_t i = it / parts;
     const int c = static_cast<int>(it % parts) * 32 + lane;
     const int r = __ldg(pos + i);
-    if (c >= vecs || (r >= 0 && splits == 1)) continue;
-    dh[i * vecs + c] = r < 0 ? make_uint4(0, 0, 0, 0) : sum_splits(acc, r, c * 8, mt, nt, splits);
+    if (c < vecs) dh[i * vecs + c] = r < 0 ? make_uint4(0, 0, 0, 0) : sum_splits(acc, r, c * 8, mt, nt, splits);
   }
 }
 
@@ -863,9 +904,23 @@ __global__ void __launch_bounds__(256) lm_dw_kernel(const float* __restrict__ ac
 
 // ---- host ------------------------------------------------------------------------
 constexpr int64_t kDzBytes = int64_t{4} << 30;   // dz of one piece
-constexpr int kDirectRows = kTile;               // forward: up to one row tile is not gathered
 
 int64_t up(int64_t n, int64_t k) { return (n + k - 1) / k * k; }
+
+// The forward takes h as it is, rows without a target included, where
+// gathering costs more than it can save: one tile of rows, or a product of
+// about 15 us (the gather takes 8).  The backward always gathers: rows
+// without a target must not reach dw.
+bool use_direct(int64_t N, int64_t V, int32_t C) {
+  return N <= kTile || static_cast<double>(N) * static_cast<double>(V) * C <= 1.2e10;
+}
+
+// Rows of h and w that do not start on 64 bytes cost the TMA loads a second
+// line each: 1.2 to 1.35x the product's time at widths of 552 and 1,000.
+// Gathered rows are laid out aligned; w is copied so where there are enough
+// rows to pay for reading and writing it once.
+int32_t row_stride(int32_t C) { return C % 32 ? (C + 63) / 64 * 64 : C; }
+bool align_w(int64_t N, int32_t C, bool backward) { return C % 32 && N >= (backward ? 2048 : 4096); }
 
 struct LmShape {
   int64_t np;        // N rounded up to whole tiles
@@ -918,7 +973,8 @@ struct Carve {
 
 struct LmWork {
   int32_t *rows, *pos, *count;
-  __nv_bfloat16* hc;
+  __nv_bfloat16* hc;    // gathered rows of h, row_stride apart; nullptr: none
+  __nv_bfloat16* wc;    // aligned copy of w; nullptr: none
   float2* part;
   float* zt;
   __nv_bfloat16* dz;
@@ -929,11 +985,12 @@ size_t carve(uint8_t* base, int64_t N, int64_t V, int32_t C, bool backward, LmWo
   const LmShape s = lm_shape(N, V);
   Carve c{base};
   LmWork o{};
-  if (backward || N > kDirectRows) {
+  if (backward || !use_direct(N, V, C)) {
     o.rows = c.take<int32_t>(s.np);
     o.pos = c.take<int32_t>(s.np);
     o.count = c.take<int32_t>(1);
-    o.hc = c.take<__nv_bfloat16>(s.np * C);
+    o.hc = c.take<__nv_bfloat16>(s.np * row_stride(C));
+    if (align_w(N, C, backward)) o.wc = c.take<__nv_bfloat16>(V * row_stride(C));
   }
   if (!backward) {
     int64_t slots = 2 * static_cast<int64_t>(s.chunks);
@@ -1004,13 +1061,19 @@ int64_t grid_for(int64_t warps) {
   return blocks < most ? blocks : most;
 }
 
-// rows, pos, count and hc of the positions with a target
-int gather_rows(const void* h, const int32_t* target, int64_t N, int64_t V, int32_t C, const LmWork& w, cudaStream_t s) {
-  lm_index_kernel<<<1, kIndexThreads, 0, s>>>(target, static_cast<int>(N), static_cast<int>(V), w.rows, w.pos, w.count);
-  int st = cuda_status(cudaGetLastError());
-  if (st != TPK_OK) return st;
-  lm_gather_kernel<<<static_cast<unsigned>(grid_for(up(N, kTile))), 256, 0, s>>>(
-      static_cast<const uint4*>(h), w.rows, w.count, C / 8, reinterpret_cast<uint4*>(w.hc));
+// rows, pos, count and hc of the positions with a target, and w's aligned copy
+int gather_rows(const void* h, const void* wt, const int32_t* target, int64_t N, int64_t V, int32_t C, const LmWork& w,
+                cudaStream_t s) {
+  int64_t per = (N + kRowsBlocks - 1) / kRowsBlocks;
+  per = per < kRowsLeast ? kRowsLeast : per;
+  const int ld = row_stride(C) / 8;
+  lm_rows_kernel<<<static_cast<unsigned>((N + per - 1) / per), kRowsThreads, 0, s>>>(
+      target, static_cast<int>(N), static_cast<int>(V), static_cast<const uint4*>(h), C / 8, ld, static_cast<int>(per),
+      w.rows, w.pos, w.count, reinterpret_cast<uint4*>(w.hc));
+  const int st = cuda_status(cudaGetLastError());
+  if (st != TPK_OK || !w.wc) return st;
+  lm_align_kernel<<<static_cast<unsigned>(grid_for(V)), 256, 0, s>>>(static_cast<const uint4*>(wt), static_cast<int>(V),
+                                                                     C / 8, ld, reinterpret_cast<uint4*>(w.wc));
   return cuda_status(cudaGetLastError());
 }
 
@@ -1038,7 +1101,8 @@ extern "C" int tpk_lm_loss(const void* h, const void* w, const int32_t* target, 
   if (st != TPK_OK) return st;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   const LmShape sh = lm_shape(N, V);
-  if (k.hc) st = gather_rows(h, target, N, V, C, k, s);
+  if (k.hc) st = gather_rows(h, w, target, N, V, C, k, s);
+  const int32_t ld = row_stride(C);
   const float scale_log2 = scale * kLog2e;
   int slots = 2 * sh.chunks;
   if (use_few(N, C)) {
@@ -1047,8 +1111,8 @@ extern "C" int tpk_lm_loss(const void* h, const void* w, const int32_t* target, 
                             : launch_few<4>(h, w, target, N, V, C, sh.np, scale_log2, &slots, k, s);
   } else {
     CUtensorMap ma, mb;
-    if (st == TPK_OK) st = k.hc ? make_map_2d(&ma, k.hc, sh.np, C, C, kHalf) : make_map_2d(&ma, h, N, C, C, kHalf);
-    if (st == TPK_OK) st = make_map_2d(&mb, w, V, C, C, kHalf);
+    if (st == TPK_OK) st = k.hc ? make_map_2d(&ma, k.hc, sh.np, C, ld, kHalf) : make_map_2d(&ma, h, N, C, C, kHalf);
+    if (st == TPK_OK) st = k.wc ? make_map_2d(&mb, k.wc, V, C, ld, kHalf) : make_map_2d(&mb, w, V, C, C, kHalf);
     if (st != TPK_OK) return st;
     LmParams p{};
     p.count = k.count;
@@ -1095,13 +1159,15 @@ extern "C" int tpk_lm_loss_bwd(const void* h, const void* w, const int32_t* targ
   int st = check_device();
   if (st != TPK_OK) return st;
   const LmShape sh = lm_shape(N, V);
-  st = gather_rows(h, target, N, V, C, k, s);
+  st = gather_rows(h, w, target, N, V, C, k, s);
+  const int32_t ld = row_stride(C), ldw = k.wc ? ld : C;
+  const void* wt = k.wc ? k.wc : w;
   // h, w, dz: boxes of 128 rows (K-major operands, dz's and dw's way out) and of 64 (MN-major)
   CUtensorMap hk, hm, wk, wm, zk, zm, dwk;
-  if (st == TPK_OK) st = make_map_2d(&hk, k.hc, sh.np, C, C, kHalf);
-  if (st == TPK_OK) st = make_map_2d(&hm, k.hc, sh.np, C, C, 64);
-  if (st == TPK_OK) st = make_map_2d(&wk, w, V, C, C, kHalf);
-  if (st == TPK_OK) st = make_map_2d(&wm, w, V, C, C, 64);
+  if (st == TPK_OK) st = make_map_2d(&hk, k.hc, sh.np, C, ld, kHalf);
+  if (st == TPK_OK) st = make_map_2d(&hm, k.hc, sh.np, C, ld, 64);
+  if (st == TPK_OK) st = make_map_2d(&wk, wt, V, C, ldw, kHalf);
+  if (st == TPK_OK) st = make_map_2d(&wm, wt, V, C, ldw, 64);
   if (st == TPK_OK) st = make_map_2d(&zk, k.dz, sh.np, sh.piece, sh.piece, kHalf);
   if (st == TPK_OK) st = make_map_2d(&dwk, dw, V, C, C, kHalf);
   if (st == TPK_OK) st = make_map_2d(&zm, k.dz, sh.np, sh.piece, sh.piece, 64);
