@@ -546,7 +546,9 @@ int tpk_gdn_delta_rule_bwd(const tpk_plan* plan, const void* dev_image, const vo
  * mixers: these take a packed batch from token ids to hidden rows, around
  * every mixer, and to its loss, and bring the gradients back.  They work row
  * by row (F forwarded positions, or any other N rows).  Results do not depend
- * on timing: sums run in a fixed order, without floating-point atomics. */
+ * on timing: sums run in a fixed order, without floating-point atomics.
+ * Workspaces and outputs belong to one call at a time: calls, or replays of
+ * captured graphs, that may overlap on the GPU need their own. */
 #define TPK_BF16 0
 #define TPK_F32  1
 
@@ -581,7 +583,7 @@ int tpk_embed_bwd(const int32_t* tokens, const void* dout, void* dtable, int32_t
  * Statistics are fp32 and x is formed from r before its rounding.
  *   res, res_out, x [N, C] bf16;  y, gate [N, C] bf16 with row strides ld_y,
  *   ld_gate (elements; may be column slices of a wider tensor);  w_post,
- *   w_pre [C] fp32.  res_out receives r, and may be res itself.
+ *   w_pre [C] fp32, 16-byte aligned.  res_out receives r, and may be res itself.
  *   y NULL: r = res (a norm before the first block); gate and w_post must be
  *   NULL too and res_out is not written.
  * Rows are 16-byte aligned, C % 8 == 0, C <= 16384 (TPK_E_UNSUPPORTED above). */
@@ -627,8 +629,8 @@ int tpk_lm_loss(const void* h, const void* w, const int32_t* target, float* loss
  * deterministic.  dloss of a position without a target is not read.
  *   dh [N, C] bf16, dw [V, C] bf16 (16-byte aligned), every row written
  *   workspace: >= tpk_lm_loss_workspace_bytes(N, V, C, 1), 256-byte aligned,
- *   need not be cleared (up to 4 GiB for dz, the gathered rows and dh's fp32
- *   sums). */
+ *   need not be cleared (dz of one piece: up to 4 GiB, or 4,096 ids; the gathered
+ *   rows; dh's fp32 sums). */
 int tpk_lm_loss_bwd(const void* h, const void* w, const int32_t* target, const float* lse, const float* dloss,
                     void* dh, void* dw, int64_t N, int64_t V, int32_t C, float scale, void* workspace,
                     size_t ws_bytes, int32_t* dev_err, void* stream);

@@ -39,10 +39,13 @@
 // below about 1,000 the epilogue is what a tile waits for: its arithmetic is
 // on packed fp32 pairs, a chunk of 32 columns is read from TMEM while the one
 // before is worked on, and bf16 results (dz, dw) leave through shared memory
-// by TMA (stores of 64 bytes per row straight from the registers took 1.6x
-// the time).  CTAs are
+// by TMA (stores of 64 bytes per row straight from the registers took 1.5x the
+// time: dz of 9,441 rows, width 552, 61,282 ids 855 us against 579).  CTAs are
 // persistent and walk the tiles in panels of 8 columns of tiles, so the pairs
 // running together share rows of A and of B in L2.
+// What bounds it: the tensor pipe, busy 98% of the forward's cycles and 93-95%
+// of the others' (8,192 rows, width 2,048, 32,000 ids: forward 520 us, 2,065
+// TFLOP/s; dz 560, dh 574, dw 572 us); in long runs the power limit.
 #include "pair.cuh"
 #include "rowwise.cuh"
 
@@ -57,7 +60,6 @@ constexpr int kEpiThreads = 256;
 constexpr int kPanel = 8;
 constexpr int kSplitPairs = 76;       // pairs a split over K aims to fill (two SMs each)
 constexpr float kLog2e = 1.4426950408889634f;
-constexpr float kLn2 = 0.6931471805599453f;
 
 constexpr int kChunk = 8;             // stages of 64 elements per accumulation of the forward
 // The forward's epilogue holds 128 columns of a row per thread: the other
@@ -150,8 +152,8 @@ template <int kMode>
 constexpr size_t kLmSmemBytes = sizeof(LmSmem<kMode>) + 1024;
 static_assert(kLmSmemBytes<kFwd> <= 227 * 1024 && kLmSmemBytes<kDz> <= 227 * 1024, "shared memory");
 
-// The tiles of one launch.  unit u covers n tiles [nt0, nt0 + n_run) of row
-// tile mt, and K iterations [k0, k0 + nk).
+// The tiles of one launch.  Unit u covers the column tiles [n0, n0 + n_run) of
+// row tile m, and the stages [k0, k0 + nk) of K.
 struct Shape {
   int mt, nt, units, splits, k_iters, run;
 };
@@ -355,6 +357,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       if (kMode != kDw && row < count) {
         pos = p.rows ? __ldg(p.rows + row) : row;
         if (kMode == kFwd || kMode == kDz) tgt = __ldg(p.target + pos);
+        if (tgt < 0 || tgt >= p.V) tgt = -1;
         if (kMode == kDz) {
           coef = __ldg(p.dloss + pos) * p.scale;
           lse2 = __ldg(p.lse + pos) * kLog2e;
@@ -402,7 +405,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
               ptx::unf2(z[e], lo, hi);
               z[e] = ptx::f2(c0 + 2 * e < p.V ? lo : -INFINITY, c0 + 2 * e + 1 < p.V ? hi : -INFINITY);
             }
-          if (static_cast<uint32_t>(tgt - c0) < static_cast<uint32_t>(kHalf) && tgt < p.V) {
+          if (static_cast<uint32_t>(tgt - c0) < static_cast<uint32_t>(kHalf)) {
             // the target's score, halving the columns by the bits of its place
             uint64_t y[kHalf / 4];
             const int at = tgt - c0;
@@ -752,10 +755,9 @@ struct Few {
 };
 
 template <int kN>
-__global__ void __launch_bounds__(256, Few<kN>::kPerSm) lm_few_kernel(const uint4* __restrict__ h, const uint4* __restrict__ w,
-                                                     const int32_t* __restrict__ target, int N, int V, int C,
-                                                     int64_t np, float scale_log2, float2* __restrict__ part,
-                                                     float* __restrict__ zt) {
+__global__ void __launch_bounds__(256, Few<kN>::kPerSm)
+    lm_few_kernel(const uint4* __restrict__ h, const uint4* __restrict__ w, const int32_t* __restrict__ target, int N,
+                  int V, int C, int64_t np, float scale_log2, float2* __restrict__ part, float* __restrict__ zt) {
   constexpr int kFewV = Few<kN>::kV;
   extern __shared__ float4 hs[];     // [kN][C / 8] pairs of float4
   __shared__ float2 sm[8][kN];
@@ -763,10 +765,8 @@ __global__ void __launch_bounds__(256, Few<kN>::kPerSm) lm_few_kernel(const uint
   const int vecs = C / 8;
   for (int i = threadIdx.x; i < kN * vecs; i += 256) {
     const uint4 x = i / vecs < N ? __ldg(h + i) : make_uint4(0, 0, 0, 0);
-    hs[2 * i] = make_float4(lo16(x.x), hi16(x.x), lo16(x.y),
-                            hi16(x.y));
-    hs[2 * i + 1] = make_float4(lo16(x.z), hi16(x.z),
-                                lo16(x.w), hi16(x.w));
+    hs[2 * i] = make_float4(lo16(x.x), hi16(x.x), lo16(x.y), hi16(x.y));
+    hs[2 * i + 1] = make_float4(lo16(x.z), hi16(x.z), lo16(x.w), hi16(x.w));
   }
   int tgt[kN];
   float2 st[kN];
@@ -1001,7 +1001,7 @@ size_t carve(uint8_t* base, int64_t N, int64_t V, int32_t C, bool backward, LmWo
     o.dz = c.take<__nv_bfloat16>(s.np * s.piece);
     const int64_t nt = (C + kTile - 1) / kTile;
     const int64_t th = s.np / kTile * nt, sh = split_tiles(th);
-    o.acc_h = c.take<float>((th > sh ? th : sh) * kTile * kTile);
+    o.acc_h = c.take<float>((s.pieces > 1 && th > sh ? th : sh) * kTile * kTile);   // one piece: splits alone
     // dw: the tiles of a full piece and of the last one are known here
     const int most = split_limit(static_cast<int>(s.np / 64));
     const int64_t full = s.piece / kTile * nt, rest = ((V - (s.pieces - 1) * s.piece) + kTile - 1) / kTile * nt;

@@ -559,3 +559,101 @@ def test_training_step_over_a_packed_tree(ops):
     # is the loss of the raw tokens
     raw_loss, total = loss[dp.token_index.long()].double(), (loss.double() * dl.double()).sum()
     assert torch.isclose((raw_loss * weight[0].double()).sum(), total, rtol=1e-5, atol=1e-4)
+
+
+# ---- nothing but the outputs is written, nothing but the inputs is read ----------------------
+
+def _inside(rows, cols, dtype, fill):
+    """(view of rows x cols, whole buffer): five guard rows of ``fill`` on either side."""
+    buf = torch.full((rows + 10, cols), fill, dtype=dtype, device="cuda")
+    return buf[5:5 + rows], buf
+
+
+def _guards_whole(buf, rows, fill):
+    return bool((buf[:5] == fill).all()) and bool((buf[5 + rows:] == fill).all())
+
+
+def _dirty(need):
+    """A workspace of exactly ``need`` bytes of 0xFF (NaN, -1), and what lies behind it."""
+    buf = torch.full((need + 4096,), 255, dtype=torch.uint8, device="cuda")
+    return buf[:need], buf[need:]
+
+
+@pytest.mark.parametrize("n,v,c", [(3, 300, 64), (700, 1000, 72), (257, 513, 264), (2100, 333, 520), (4100, 900, 40)])
+def test_outputs_and_workspaces_keep_to_their_bounds(ops, n, v, c):
+    from prefix_tree_packed_dfs_gb300 import binding
+    lib = binding.load()
+    tok = torch.from_numpy(_tokens(n, v, 101, "zipf")).cuda()
+    table, y, gate = _rnd(102, v, c), _rnd(103, n, c), _rnd(104, n, c)
+    w = 1 + _rnd(105, c, std=0.1, dtype=torch.float32)
+    dl = _rnd(106, n, dtype=torch.float32)
+
+    def both(fn, shapes, need):
+        """fn into guarded outputs with a dirty workspace of the least size, and plainly."""
+        outs = [_inside(r, k, t, 3.0) for r, k, t in shapes]
+        ws, behind = _dirty(need)
+        fn([o[0] for o in outs], ws if need else None)
+        plain = [torch.empty(r, k, dtype=t, device="cuda") for r, k, t in shapes]
+        fn(plain, None)
+        for (o, buf), p, (r, _, _) in zip(outs, plain, shapes):
+            assert _guards_whole(buf, r, 3.0) and torch.equal(o, p)
+        assert (behind == 255).all()
+        return plain
+
+    bf, f32 = torch.bfloat16, torch.float32
+    (emb,) = both(lambda o, ws: ops.embed(table, tok, out=o[0]), [(n, c, bf)], 0)
+    both(lambda o, ws: ops.embed_bwd(tok, y, v, dtable=o[0], workspace=ws), [(v, c, f32)],
+         lib.tpk_embed_bwd_workspace_bytes(n, v, c))
+    r, x = both(lambda o, ws: ops.block_norm(emb, w, y=y, w_post=w, gate=gate, res_out=o[0], out=o[1]),
+                [(n, c, bf), (n, c, bf)], 0)
+    both(lambda o, ws: ops.block_norm_bwd(emb, w, x, dres_out=r, y=y, w_post=w, gate=gate, dres=o[0], dy=o[1],
+                                          dgate=o[2], dw_post=o[3].view(c), dw_pre=o[4].view(c), workspace=ws),
+         [(n, c, bf), (n, c, bf), (n, c, bf), (1, c, f32), (1, c, f32)], lib.tpk_block_norm_bwd_workspace_bytes(n, c))
+    loss, lse = both(lambda o, ws: ops.lm_loss(x, table, tok, loss=o[0].view(n), lse=o[1].view(n), workspace=ws),
+                     [(n, 1, f32), (n, 1, f32)], lib.tpk_lm_loss_workspace_bytes(n, v, c, 0))
+    both(lambda o, ws: ops.lm_loss_bwd(x, table, tok, lse.view(n), dl, dh=o[0], dw=o[1], workspace=ws),
+         [(n, c, bf), (v, c, bf)], lib.tpk_lm_loss_workspace_bytes(n, v, c, 1))
+
+
+def test_ids_and_weights_of_one_element_alignment(ops):
+    """Ids, targets, lse and loss weights need no more than their own alignment."""
+    n, v, c = 1500, 700, 64
+    whole = torch.from_numpy(_tokens(n + 1, v, 111, "uniform")).cuda()
+    tok = whole[1:]
+    assert tok.data_ptr() % 16
+    table, h = _rnd(112, v, c), _rnd(113, n, c)
+    assert torch.equal(ops.embed(table, tok), ops.embed(table, tok.clone()))
+    assert torch.equal(ops.embed_bwd(tok, h, v), ops.embed_bwd(tok.clone(), h, v))
+    a, b = ops.lm_loss(h, table, tok), ops.lm_loss(h, table, tok.clone())
+    assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
+    dl = _rnd(114, n + 1, dtype=torch.float32)[1:]
+    lse = torch.cat([a[1][:1], a[1]])[1:]
+    p, q = ops.lm_loss_bwd(h, table, tok, lse, dl), ops.lm_loss_bwd(h, table, tok.clone(), a[1], dl.clone())
+    assert torch.equal(p[0], q[0]) and torch.equal(p[1], q[1])
+    # the norms' weights are read 16 bytes at a time: other addresses are refused
+    from prefix_tree_packed_dfs_gb300.binding import TpkError
+    with pytest.raises(TpkError):
+        ops.block_norm(h, torch.ones(c + 1, device="cuda")[1:])
+
+
+def test_the_same_position_sets_in_any_company(ops):
+    """A position's loss and gradient do not depend on how many others have no
+    target: the same rows alone, and scattered among rows without one."""
+    n, v, c = 900, 1200, 128
+    h, w = _rnd(121, n, c), _rnd(122, v, c, std=0.2)
+    t = torch.from_numpy((np.random.default_rng(123).integers(0, v, n)).astype(np.int32)).cuda()
+    dl = _rnd(124, n, dtype=torch.float32)
+    loss, lse = ops.lm_loss(h, w, t)
+    dh, dw = ops.lm_loss_bwd(h, w, t, lse, dl)
+    at = torch.sort(torch.randperm(5 * n, generator=torch.Generator().manual_seed(125))[:n]).values.cuda()
+    hs = torch.full((5 * n, c), float("nan"), dtype=torch.bfloat16, device="cuda")
+    ts = torch.full((5 * n,), -7, dtype=torch.int32, device="cuda")
+    ds = torch.full((5 * n,), float("inf"), device="cuda")
+    hs[at], ts[at], ds[at] = h, t, dl
+    loss2, lse2 = ops.lm_loss(hs, w, ts)
+    dh2, dw2 = ops.lm_loss_bwd(hs, w, ts, lse2, ds)
+    assert torch.equal(loss2[at], loss) and torch.equal(lse2[at], lse)
+    assert torch.equal(dh2[at], dh) and torch.equal(dw2, dw)
+    rest = torch.ones(5 * n, dtype=torch.bool, device="cuda")
+    rest[at] = False
+    assert not loss2[rest].any() and not lse2[rest].any() and not dh2[rest].any()
