@@ -11,10 +11,17 @@
 // element).  The backward recomputes r from the same inputs instead of
 // reading a saved one (the same bytes, and no rounding in between), so it
 // reads res, y, gate, dr, dx and writes dres, dy, dgate (16 bytes per
-// element).  A row stays in the registers of kT threads, 16 channels each.
-// The weights' gradients are column sums: every group of threads keeps its
-// own columns' sums over the rows it walks and writes them once, and a second
-// kernel adds the groups in order (deterministic).
+// element).  In the forward a row stays in the registers of kT threads, 16
+// channels each; in the backward it is copied ahead into shared memory.
+// The weights' gradients are column sums: every CTA keeps its threads'
+// columns' sums over the rows it walks and writes them once, and a second
+// kernel adds the CTAs' in order (deterministic).
+// Measured on GB300: forward 96,888 x 2,048 283 us, 7.0 TB/s (the copy peak);
+// backward 32,768 x 4,096 340 us, 6.3 TB/s (0.93 of it), 79% of the DRAM
+// cycles.  What took the backward there from 614 us: rows copied ahead 417,
+// then the weights in shared memory instead of L1 340 (packed arithmetic
+// alone changed nothing, but its registers are fewer).  One 16-byte piece per
+// thread and 512 threads per row instead of two and 256: 449.
 #include <type_traits>
 
 #include "ptx.cuh"
