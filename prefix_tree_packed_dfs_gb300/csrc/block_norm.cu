@@ -63,7 +63,8 @@ __device__ __forceinline__ uint64_t pair_of(uint32_t u) {
 }
 __device__ __forceinline__ Oct oct(uint4 u) { return {{pair_of(u.x), pair_of(u.y), pair_of(u.z), pair_of(u.w)}}; }
 __device__ __forceinline__ Oct load_oct(const float* p) {
-  const ulonglong2 a = __ldg(reinterpret_cast<const ulonglong2*>(p)), b = __ldg(reinterpret_cast<const ulonglong2*>(p) + 1);
+  const ulonglong2* q = reinterpret_cast<const ulonglong2*>(p);
+  const ulonglong2 a = __ldg(q), b = __ldg(q + 1);
   return {{a.x, a.y, b.x, b.y}};
 }
 __device__ __forceinline__ uint32_t pack_pair(uint64_t v) {
@@ -631,7 +632,7 @@ extern "C" int tpk_block_norm_bwd(const void* res, const void* y, int64_t ld_y, 
       using Shape = decltype(shape);
       constexpr auto kern = block_norm_bwd_kernel<decltype(kt)::value, decltype(kv)::value>;
       static PerContext<int> rec;
-      const int e = set_smem_once(rec, kern, Shape::kSmem);
+      const int e = guarded([&] { return set_smem_once(rec, kern, Shape::kSmem); });
       if (e != TPK_OK) return e;
       blocks = bwd_blocks<Shape>(N, sms);
       kern<<<static_cast<unsigned>(blocks), Shape::kBlock, Shape::kSmem, s>>>(p);

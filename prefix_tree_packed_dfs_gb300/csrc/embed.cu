@@ -113,7 +113,8 @@ __device__ __forceinline__ int scan256(int v, int* warp_sums) {
 // The warp's keys' ranks among its keys of the same digit; count[d] (the
 // warp's, zeroed) receives how many there are of each.
 template <int kRounds>
-__device__ __forceinline__ void rank_keys(const int (&key)[kRounds], int n, int shift, int* count, int (&rank)[kRounds]) {
+__device__ __forceinline__ void rank_keys(const int (&key)[kRounds], int n, int shift, int* count,
+                                          int (&rank)[kRounds]) {
   const int lane = threadIdx.x & 31;
 #pragma unroll
   for (int r = 0; r < kRounds; ++r) {

@@ -441,128 +441,129 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           s = lo + hi;
           m = mn;
         } else {
-        const uint32_t buf = tile & 1;
-        const bool any = kMode != kDw || w.nk > 0;   // no rows at all: dw is zero
-        if (any) {
-          ok = ptx::mbar_wait(&S.tm_full[buf], (tile / 2) & 1, abort_flag, kWaitLimitNs);
-          // a warpgroup with barriers of its own gives up as a whole
-          ok = Smem::kOut ? ptx::all_of_128(wg + 1, ok) : __all_sync(0xffffffffu, ok);
-          if (!ok) break;
-          ptx::tc_fence_after();
-          ++tile;
-        }
-        const int n0 = (w.n0 + j) * kTile + wg * kHalf;   // first column of this warpgroup
-        const uint32_t tm = tmem + lane_off + buf * kTile + wg * kHalf;
-        uint32_t raw[2][32];
-        if (any) {
-          ptx::tmem_ld32(tm, raw[0]);
-          ptx::tmem_wait_ld_of(raw[0]);
-        } else {
-#pragma unroll
-          for (int e = 0; e < 32; ++e) raw[0][e] = raw[1][e] = 0;
-        }
-#pragma unroll
-        for (int c = 0; c < 4; ++c) {
-          uint32_t(&x)[32] = raw[c & 1];
-          if (any && c < 3) ptx::tmem_ld32(tm + (c + 1) * 32, raw[(c + 1) & 1]);
-          const int c0 = n0 + c * 32;
-          if constexpr (kMode == kDz || kMode == kDw) {
-            uint32_t o[16];
-            if constexpr (kMode == kDz) {
-              const uint64_t minus = ptx::f2(-lse2, -lse2), c2 = ptx::f2(coef, coef);
-              float d[32];
-#pragma unroll
-              for (int e = 0; e < 32; e += 2) {
-                float lo, hi;
-                ptx::unf2(ptx::fma2(ptx::f2(__uint_as_float(x[e]), __uint_as_float(x[e + 1])), k2, minus), lo, hi);
-                d[e] = ptx::ex2(lo);
-                d[e + 1] = ptx::ex2(hi);
-              }
-              if (static_cast<uint32_t>(tgt - c0) < 32u) {
-#pragma unroll
-                for (int e = 0; e < 32; ++e)
-                  if (tgt - c0 == e) d[e] -= 1.f;
-              }
-              if (c0 + 32 > p.vcols)
-#pragma unroll
-                for (int e = 0; e < 32; ++e)
-                  if (c0 + e >= p.vcols) d[e] = 0.f;
-#pragma unroll
-              for (int e = 0; e < 32; e += 2) {
-                float lo, hi;
-                ptx::unf2(ptx::mul2(ptx::f2(d[e], d[e + 1]), c2), lo, hi);
-                o[e / 2] = ptx::pack_bf16x2(lo, hi);
-              }
-            } else {
-#pragma unroll
-              for (int e = 0; e < 32; e += 2)
-                o[e / 2] = ptx::pack_bf16x2(__uint_as_float(x[e]), __uint_as_float(x[e + 1]));
-            }
-            if (kMode == kDz || sh.splits == 1) {
-              // out through shared memory: 64 columns per box, in the TMA's
-              // swizzle (16-byte piece i of row r at piece i ^ (r % 8))
-              uint8_t* stage = S.out[wg * Smem::kOutBoxes + box];
-              const bool leader = (threadIdx.x & 127) == 0;
-              if ((c & 1) == 0) {
-                if (leader) ptx::bulk_wait_read<Smem::kOutBoxes - 1>();   // this box's last store
-                asm volatile("bar.sync %0, 128;" ::"r"(wg + 1) : "memory");
-              }
-#pragma unroll
-              for (int q = 0; q < 4; ++q)
-                *reinterpret_cast<uint4*>(stage + rc * 128 + ((((c & 1) * 4 + q) ^ (rc & 7)) * 16)) =
-                    make_uint4(o[4 * q], o[4 * q + 1], o[4 * q + 2], o[4 * q + 3]);
-              if ((c & 1) == 1) {
-                ptx::fence_async_shared();
-                asm volatile("bar.sync %0, 128;" ::"r"(wg + 1) : "memory");
-                const int col = c0 - 32;
-                const int first_row = w.m * kTile + static_cast<int>(rank) * kHalf;
-                const bool inside = kMode == kDz ? col < p.ld_dz : col < p.C && first_row < p.vcols;
-                if (leader) {
-                  if (inside) ptx::tma_store_2d(&tm_out, stage, col, kMode == kDw ? p.v0 + first_row : first_row);
-                  ptx::bulk_commit();
-                }
-                box = (box + 1) % Smem::kOutBoxes;
-              }
-            } else {
-              float4* ap = reinterpret_cast<float4*>(p.acc + tile_id * (kTile * kTile) + r * kTile + wg * kHalf + c * 32);
-#pragma unroll
-              for (int q = 0; q < 8; ++q)
-                ap[q] = make_float4(__uint_as_float(x[4 * q]), __uint_as_float(x[4 * q + 1]),
-                                    __uint_as_float(x[4 * q + 2]), __uint_as_float(x[4 * q + 3]));
-            }
+          const uint32_t buf = tile & 1;
+          const bool any = kMode != kDw || w.nk > 0;   // no rows at all: dw is zero
+          if (any) {
+            ok = ptx::mbar_wait(&S.tm_full[buf], (tile / 2) & 1, abort_flag, kWaitLimitNs);
+            // a warpgroup with barriers of its own gives up as a whole
+            ok = Smem::kOut ? ptx::all_of_128(wg + 1, ok) : __all_sync(0xffffffffu, ok);
+            if (!ok) break;
+            ptx::tc_fence_after();
+            ++tile;
+          }
+          const int n0 = (w.n0 + j) * kTile + wg * kHalf;   // first column of this warpgroup
+          const uint32_t tm = tmem + lane_off + buf * kTile + wg * kHalf;
+          uint32_t raw[2][32];
+          if (any) {
+            ptx::tmem_ld32(tm, raw[0]);
+            ptx::tmem_wait_ld_of(raw[0]);
           } else {
-            float* blk = p.acc + tile_id * (kTile * kTile) + r * kTile + wg * kHalf + c * 32;
-            const bool out = p.last && sh.splits == 1;
 #pragma unroll
-            for (int q = 0; q < 4; ++q) {
-              float v[8];
+            for (int e = 0; e < 32; ++e) raw[0][e] = raw[1][e] = 0;
+          }
 #pragma unroll
-              for (int e = 0; e < 8; ++e) v[e] = __uint_as_float(x[8 * q + e]);
-              float4* ap = reinterpret_cast<float4*>(blk + 8 * q);
-              if (!p.first) {
-                const float4 y = ap[0], z = ap[1];
-                v[0] += y.x; v[1] += y.y; v[2] += y.z; v[3] += y.w;
-                v[4] += z.x; v[5] += z.y; v[6] += z.z; v[7] += z.w;
+          for (int c = 0; c < 4; ++c) {
+            uint32_t(&x)[32] = raw[c & 1];
+            if (any && c < 3) ptx::tmem_ld32(tm + (c + 1) * 32, raw[(c + 1) & 1]);
+            const int c0 = n0 + c * 32;
+            if constexpr (kMode == kDz || kMode == kDw) {
+              uint32_t o[16];
+              if constexpr (kMode == kDz) {
+                const uint64_t minus = ptx::f2(-lse2, -lse2), c2 = ptx::f2(coef, coef);
+                float d[32];
+#pragma unroll
+                for (int e = 0; e < 32; e += 2) {
+                  float lo, hi;
+                  ptx::unf2(ptx::fma2(ptx::f2(__uint_as_float(x[e]), __uint_as_float(x[e + 1])), k2, minus), lo, hi);
+                  d[e] = ptx::ex2(lo);
+                  d[e + 1] = ptx::ex2(hi);
+                }
+                if (static_cast<uint32_t>(tgt - c0) < 32u) {
+#pragma unroll
+                  for (int e = 0; e < 32; ++e)
+                    if (tgt - c0 == e) d[e] -= 1.f;
+                }
+                if (c0 + 32 > p.vcols)
+#pragma unroll
+                  for (int e = 0; e < 32; ++e)
+                    if (c0 + e >= p.vcols) d[e] = 0.f;
+#pragma unroll
+                for (int e = 0; e < 32; e += 2) {
+                  float lo, hi;
+                  ptx::unf2(ptx::mul2(ptx::f2(d[e], d[e + 1]), c2), lo, hi);
+                  o[e / 2] = ptx::pack_bf16x2(lo, hi);
+                }
+              } else {
+#pragma unroll
+                for (int e = 0; e < 32; e += 2)
+                  o[e / 2] = ptx::pack_bf16x2(__uint_as_float(x[e]), __uint_as_float(x[e + 1]));
               }
-              if (!out) {
-                ap[0] = make_float4(v[0], v[1], v[2], v[3]);
-                ap[1] = make_float4(v[4], v[5], v[6], v[7]);
-              } else if (row < count && c0 + 8 * q < p.C) {
-                *reinterpret_cast<uint4*>(p.dh + pos * p.C + c0 + 8 * q) =
-                    make_uint4(ptx::pack_bf16x2(v[0], v[1]), ptx::pack_bf16x2(v[2], v[3]),
-                               ptx::pack_bf16x2(v[4], v[5]), ptx::pack_bf16x2(v[6], v[7]));
+              if (kMode == kDz || sh.splits == 1) {
+                // out through shared memory: 64 columns per box, in the TMA's
+                // swizzle (16-byte piece i of row r at piece i ^ (r % 8))
+                uint8_t* stage = S.out[wg * Smem::kOutBoxes + box];
+                const bool leader = (threadIdx.x & 127) == 0;
+                if ((c & 1) == 0) {
+                  if (leader) ptx::bulk_wait_read<Smem::kOutBoxes - 1>();   // this box's last store
+                  asm volatile("bar.sync %0, 128;" ::"r"(wg + 1) : "memory");
+                }
+#pragma unroll
+                for (int q = 0; q < 4; ++q)
+                  *reinterpret_cast<uint4*>(stage + rc * 128 + ((((c & 1) * 4 + q) ^ (rc & 7)) * 16)) =
+                      make_uint4(o[4 * q], o[4 * q + 1], o[4 * q + 2], o[4 * q + 3]);
+                if ((c & 1) == 1) {
+                  ptx::fence_async_shared();
+                  asm volatile("bar.sync %0, 128;" ::"r"(wg + 1) : "memory");
+                  const int col = c0 - 32;
+                  const int first_row = w.m * kTile + static_cast<int>(rank) * kHalf;
+                  const bool inside = kMode == kDz ? col < p.ld_dz : col < p.C && first_row < p.vcols;
+                  if (leader) {
+                    if (inside) ptx::tma_store_2d(&tm_out, stage, col, kMode == kDw ? p.v0 + first_row : first_row);
+                    ptx::bulk_commit();
+                  }
+                  box = (box + 1) % Smem::kOutBoxes;
+                }
+              } else {
+                float* blk = p.acc + tile_id * (kTile * kTile) + r * kTile + wg * kHalf + c * 32;
+                float4* ap = reinterpret_cast<float4*>(blk);
+#pragma unroll
+                for (int q = 0; q < 8; ++q)
+                  ap[q] = make_float4(__uint_as_float(x[4 * q]), __uint_as_float(x[4 * q + 1]),
+                                      __uint_as_float(x[4 * q + 2]), __uint_as_float(x[4 * q + 3]));
+              }
+            } else {
+              float* blk = p.acc + tile_id * (kTile * kTile) + r * kTile + wg * kHalf + c * 32;
+              const bool out = p.last && sh.splits == 1;
+#pragma unroll
+              for (int q = 0; q < 4; ++q) {
+                float v[8];
+#pragma unroll
+                for (int e = 0; e < 8; ++e) v[e] = __uint_as_float(x[8 * q + e]);
+                float4* ap = reinterpret_cast<float4*>(blk + 8 * q);
+                if (!p.first) {
+                  const float4 y = ap[0], z = ap[1];
+                  v[0] += y.x; v[1] += y.y; v[2] += y.z; v[3] += y.w;
+                  v[4] += z.x; v[5] += z.y; v[6] += z.z; v[7] += z.w;
+                }
+                if (!out) {
+                  ap[0] = make_float4(v[0], v[1], v[2], v[3]);
+                  ap[1] = make_float4(v[4], v[5], v[6], v[7]);
+                } else if (row < count && c0 + 8 * q < p.C) {
+                  *reinterpret_cast<uint4*>(p.dh + pos * p.C + c0 + 8 * q) =
+                      make_uint4(ptx::pack_bf16x2(v[0], v[1]), ptx::pack_bf16x2(v[2], v[3]),
+                                 ptx::pack_bf16x2(v[4], v[5]), ptx::pack_bf16x2(v[6], v[7]));
+                }
+              }
+            }
+            if (any && c < 3) {
+              ptx::tmem_wait_ld_of(raw[(c + 1) & 1]);
+              if (c == 2) {   // the whole tile has been read
+                ptx::tc_fence_before();
+                __syncwarp();
+                if (lane == 0) ptx::mbar_arrive_cluster(bar_empty[buf]);
               }
             }
           }
-          if (any && c < 3) {
-            ptx::tmem_wait_ld_of(raw[(c + 1) & 1]);
-            if (c == 2) {   // the whole tile has been read
-              ptx::tc_fence_before();
-              __syncwarp();
-              if (lane == 0) ptx::mbar_arrive_cluster(bar_empty[buf]);
-            }
-          }
-        }
         }
       }
       if (kMode == kFwd && ok && row < count)
@@ -677,7 +678,8 @@ __global__ void __launch_bounds__(kRowsThreads) lm_rows_kernel(const int32_t* __
     before += n;
   }
   const int padded = (all + kTile - 1) / kTile * kTile;
-  for (int r = all + static_cast<int>(blockIdx.x) * kWarps + warp; r < padded; r += static_cast<int>(gridDim.x) * kWarps)
+  const int step = static_cast<int>(gridDim.x) * kWarps;
+  for (int r = all + static_cast<int>(blockIdx.x) * kWarps + warp; r < padded; r += step)
     for (int c = lane; c < vecs; c += 32) hc[static_cast<int64_t>(r) * ld + c] = make_uint4(0, 0, 0, 0);
 }
 
@@ -832,7 +834,8 @@ __global__ void __launch_bounds__(256, Few<kN>::kPerSm)
 }
 
 // 8 columns of row r of a product that was split over K: its splits' sums.
-__device__ __forceinline__ uint4 sum_splits(const float* __restrict__ acc, int64_t r, int col, int mt, int nt, int splits) {
+__device__ __forceinline__ uint4 sum_splits(const float* __restrict__ acc, int64_t r, int col, int mt, int nt,
+                                            int splits) {
   const float* from = acc + ((r / kTile) * nt + col / kTile) * (kTile * kTile) + (r % kTile) * kTile + col % kTile;
   const int64_t step = static_cast<int64_t>(mt) * nt * (kTile * kTile);
   float v[8] = {};
@@ -1023,14 +1026,14 @@ int launch_product(const CUtensorMap& a, const CUtensorMap& b, const CUtensorMap
                    int64_t most_units, cudaStream_t s) {
   static PerContext<int> rec;
   int unused = 0;
-  const int st = rec.get(&unused, [](int*) {
+  const int st = guarded([&] { return rec.get(&unused, [](int*) {
     cudaFuncAttributes fa;
     if (cudaFuncGetAttributes(&fa, lm_product_kernel<kMode>) != cudaSuccess) return TPK_E_CUDA;
     // setmaxnreg waits for registers the CTA was not launched with
     if (kMode == kFwd && fa.numRegs * kThreads < kRegsNeeded) return TPK_E_UNSUPPORTED;
     return cuda_status(cudaFuncSetAttribute(lm_product_kernel<kMode>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                             static_cast<int>(kLmSmemBytes<kMode>)));
-  });
+  }); });
   if (st != TPK_OK) return st;
   int64_t pairs = num_sms() / 2;
   if (pairs < 1) pairs = 1;
@@ -1043,7 +1046,7 @@ template <int kN>
 int launch_few(const void* h, const void* w, const int32_t* target, int64_t N, int64_t V, int32_t C, int64_t np,
                float scale_log2, int* slots, const LmWork& k, cudaStream_t s) {
   static PerContext<int> rec;
-  const int st = set_smem_once(rec, lm_few_kernel<kN>, sizeof(float) * kFewMost);
+  const int st = guarded([&] { return set_smem_once(rec, lm_few_kernel<kN>, sizeof(float) * kFewMost); });
   if (st != TPK_OK) return st;
   const int64_t want = (V + 8 * Few<kN>::kV - 1) / (8 * Few<kN>::kV);
   int64_t blocks = int64_t{num_sms()} * Few<kN>::kPerSm;
@@ -1151,7 +1154,8 @@ extern "C" int tpk_lm_loss_bwd(const void* h, const void* w, const int32_t* targ
     const int st = check_device();
     return st != TPK_OK ? st : cuda_status(cudaMemsetAsync(dw, 0, static_cast<size_t>(V) * C * 2, s));
   }
-  if (!h || !w || !target || !lse || !dloss || !dh || !aligned16(h) || !aligned16(w) || !aligned16(dh)) return TPK_E_ARG;
+  if (!h || !w || !target || !lse || !dloss || !dh) return TPK_E_ARG;
+  if (!aligned16(h) || !aligned16(w) || !aligned16(dh)) return TPK_E_ARG;
   LmWork k;
   if (!workspace || reinterpret_cast<uintptr_t>(workspace) % 256 ||
       ws_bytes < carve(static_cast<uint8_t*>(workspace), N, V, C, true, &k))
@@ -1202,13 +1206,14 @@ extern "C" int tpk_lm_loss_bwd(const void* h, const void* w, const int32_t* targ
     p.acc = k.acc_w;
     if (st == TPK_OK) st = launch_product<kDw>(zm, hm, dwk, p, INT64_MAX, s);
     if (st == TPK_OK && splits_for(vt * ct, split_limit(static_cast<int>(sh.np / 64))) > 1) {
-      lm_dw_kernel<<<static_cast<unsigned>(grid_for(p.vcols * ((C / 8 + 31) / 32))), 256, 0, s>>>(k.acc_w, k.count, p.v0, p.vcols, C,
-                                                                            static_cast<uint4*>(dw));
+      const int64_t warps = int64_t{p.vcols} * ((C / 8 + 31) / 32);
+      lm_dw_kernel<<<static_cast<unsigned>(grid_for(warps)), 256, 0, s>>>(k.acc_w, k.count, p.v0, p.vcols, C,
+                                                                          static_cast<uint4*>(dw));
       st = cuda_status(cudaGetLastError());
     }
   }
   if (st != TPK_OK) return st;
-  lm_dh_kernel<<<static_cast<unsigned>(grid_for(N * ((C / 8 + 31) / 32))), 256, 0, s>>>(k.acc_h, k.pos, k.count, static_cast<int>(N), C,
-                                                                  p.split_most, static_cast<uint4*>(dh));
+  lm_dh_kernel<<<static_cast<unsigned>(grid_for(N * ((C / 8 + 31) / 32))), 256, 0, s>>>(
+      k.acc_h, k.pos, k.count, static_cast<int>(N), C, p.split_most, static_cast<uint4*>(dh));
   return cuda_status(cudaGetLastError());
 }

@@ -15,6 +15,17 @@ constexpr int kMaxSms = 256;
 
 inline bool aligned16(const void* p) { return reinterpret_cast<uintptr_t>(p) % 16 == 0; }
 
+// body() -> status, for the C entry points: nothing thrown on the host (out of
+// memory, a mutex) leaves the library.
+template <typename Body>
+int guarded(Body body) {
+  try {
+    return body();
+  } catch (...) {
+    return TPK_E_HOST;
+  }
+}
+
 // Tensor map over a row-major bf16 matrix [rows, cols] with row stride ld
 // (elements), 128-byte swizzle, box of 64 columns (128 bytes) x box_rows rows.
 // Elements outside the matrix read as zero and are not written.

@@ -725,7 +725,8 @@ def embed_bwd(tokens, dout, vocab, scale=1.0, dtype=torch.float32, dtable=None, 
     p_dt = _arg(dtable, dtype, (V, C), "dtable")
     ws = _workspace(workspace, lib.tpk_embed_bwd_workspace_bytes(N, V, C), dout, "the lookup's backward")
     dev = _device("dout tokens dtable workspace", dout, tokens, dtable, ws)
-    _launch(dev, lib.tpk_embed_bwd, p_tok, p_dout, p_dt, _TABLE_TYPES[dtype], N, V, C, float(scale), ws.data_ptr(), ws.nbytes)
+    _launch(dev, lib.tpk_embed_bwd, p_tok, p_dout, p_dt, _TABLE_TYPES[dtype], N, V, C, float(scale), ws.data_ptr(),
+            ws.nbytes)
     return dtable
 
 
@@ -818,8 +819,8 @@ def block_norm_bwd(res, w_pre, dx, dres_out=None, y=None, w_post=None, gate=None
     dw_pre = torch.empty_like(w_pre) if dw_pre is None else dw_pre
     p_dpre = _arg(dw_pre, torch.float32, (C,), "dw_pre")
     ws = _workspace(workspace, lib.tpk_block_norm_bwd_workspace_bytes(*shape), res, "the norms' backward")
-    dev = _device("res w_pre dx dres_out y w_post gate dres dy dgate dw_post dw_pre workspace", res, w_pre, dx, dres_out,
-                  y, w_post, gate, dres, dy, dgate, dw_post, dw_pre, ws)
+    dev = _device("res w_pre dx dres_out y w_post gate dres dy dgate dw_post dw_pre workspace", res, w_pre, dx,
+                  dres_out, y, w_post, gate, dres, dy, dgate, dw_post, dw_pre, ws)
     _launch(dev, lib.tpk_block_norm_bwd, *args, p_dro, p_dx, p_dres, p_dy, ld_dy, p_dgate, ld_dgate, p_dpost, p_dpre,
             *shape, float(scale), float(eps), ws.data_ptr(), ws.nbytes)
     return dres, dy, dgate, dw_post, dw_pre
@@ -870,5 +871,6 @@ def lm_loss_bwd(h, w, target, lse, dloss, scale=1.0, dh=None, dw=None, workspace
     p_err = _dev_err(dev_err)
     ws = _workspace(workspace, lib.tpk_lm_loss_workspace_bytes(N, V, C, 1), h, "the loss's backward")
     dev = _device("h w target lse dloss dh dw workspace dev_err", h, w, target, lse, dloss, dh, dw, ws, dev_err)
-    _launch(dev, lib.tpk_lm_loss_bwd, *args, p_lse, p_dloss, p_dh, p_dw, N, V, C, float(scale), ws.data_ptr(), ws.nbytes, p_err)
+    _launch(dev, lib.tpk_lm_loss_bwd, *args, p_lse, p_dloss, p_dh, p_dw, N, V, C, float(scale), ws.data_ptr(),
+            ws.nbytes, p_err)
     return dh, dw
