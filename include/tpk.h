@@ -611,7 +611,7 @@ int tpk_block_norm_bwd(const void* res, const void* y, int64_t ld_y, const void*
  *   lse[f]  = ln sum_v exp z[f, v]
  *   loss[f] = lse[f] - z[f, target[f]]        (minus the target's log-probability)
  * A position whose target is outside [0, V) carries no loss: loss and lse are
- * zero and its row of h is not read into any product.
+ * zero, and what its row of h holds (NaN, say) reaches no result.
  *   h [N, C] bf16, w [V, C] bf16, target [N] int32, loss, lse [N] fp32
  *   C % 8 == 0; h, w 16-byte aligned; scale > 0 and finite
  *   workspace: >= tpk_lm_loss_workspace_bytes(N, V, C, 0), 256-byte aligned,

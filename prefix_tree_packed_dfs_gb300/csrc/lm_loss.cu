@@ -18,8 +18,8 @@
 //   kDw   dz^T h: the piece's rows of dw
 // The vocabulary is cut into pieces so that dz of one piece fits the
 // workspace (kDzBytes).  dz enters its products as bf16 (as the score
-// gradients do in the attention backward): relative rounding 2^-9, the size
-// of the outputs' own.
+// gradients do in the attention backward): a relative rounding of 2^-8 at
+// most, the size of the outputs' own.
 //
 // The product: 256 x 256 tiles on a pair of CTAs (tcgen05 cta_group::2, each
 // CTA holds 128 rows of A, 128 rows of B and its 128 rows of the result), 64
