@@ -585,7 +585,8 @@ def _dirty(need):
     return buf[:need], buf[need:]
 
 
-@pytest.mark.parametrize("n,v,c", [(3, 300, 64), (700, 1000, 72), (257, 513, 264), (2100, 333, 520), (4100, 900, 40)])
+@pytest.mark.parametrize("n,v,c", [(3, 300, 64), (700, 1000, 72), (257, 513, 264), (2100, 333, 520), (4100, 900, 40),
+                                   (5000, 9000, 264)])
 def test_outputs_and_workspaces_keep_to_their_bounds(ops, n, v, c):
     from prefix_tree_packed_dfs_gb300 import binding
     lib = binding.load()
@@ -663,3 +664,83 @@ def test_the_same_position_sets_in_any_company(ops):
     rest = torch.ones(5 * n, dtype=torch.bool, device="cuda")
     rest[at] = False
     assert not loss2[rest].any() and not lse2[rest].any() and not dh2[rest].any()
+
+
+def test_lm_loss_long_batch(ops):
+    """600,000 positions of width 3,600: more than 2^31 elements of h, of dh and
+    of a piece's dz, two pieces, rows that are copied to be aligned.  Sampled
+    rows of dh and dw against fp64 (dw by the lse under test, sampled too)."""
+    n, v, c = 600_000, 8000, 3600
+    w = _rnd(131, v, c, std=0.03)
+    h = torch.empty(n, c, dtype=torch.bfloat16, device="cuda")
+    gen = torch.Generator(device="cuda").manual_seed(132)
+    for part in h.split(50_000):
+        part.copy_(torch.randn(part.shape, generator=gen, device="cuda"))
+    g = np.random.default_rng(133)
+    t = g.integers(0, v, n).astype(np.int32)
+    t[g.random(n) < 0.1] = -1
+    tt = torch.from_numpy(t).cuda()
+    dl = _rnd(134, n, dtype=torch.float32)
+    loss, lse = ops.lm_loss(h, w, tt)
+    dh, dw = ops.lm_loss_bwd(h, w, tt, lse, dl)
+    rows = np.concatenate([g.integers(0, n, 24), [0, 1, n - 2, n - 1]])
+    cols = np.concatenate([g.integers(0, v, 8), [0, 4095, 4096, v - 1]])
+    on = tt[rows] >= 0
+    z = h[rows].double() @ w.double().T
+    r_lse = torch.where(on, torch.logsumexp(z, 1), 0.0)
+    # a score: 32 truncations (2^-23) per chunk of 512 channels and 8 roundings
+    # of the sum, of sum|h w| = 3600 * 0.03 * 2 / pi = 69; the softmax sum 2^-14
+    assert (lse[rows].double() - r_lse).abs().max() <= (32 * 2.0 ** -23 + 8 * 2.0 ** -24) * 80 + 2.0 ** -14
+    d = torch.softmax(z, 1)
+    d.scatter_add_(1, tt[rows].long().clamp(min=0)[:, None],
+                   -torch.ones(len(rows), 1, dtype=torch.float64, device="cuda"))
+    ref = (d * torch.where(on, dl[rows].double(), 0.0)[:, None]) @ w.double()
+    assert (dh[rows].double() - ref).norm() <= 3.2e-3 * ref.norm()
+    for i in np.flatnonzero(t < 0)[[0, -1]]:
+        assert not dh[i].any()
+    ref = torch.zeros(len(cols), c, dtype=torch.float64, device="cuda")
+    wc, ids = w[cols].double(), torch.from_numpy(cols).cuda()
+    for lo in range(0, n, 50_000):
+        at = slice(lo, min(n, lo + 50_000))
+        hd = h[at].double()
+        p = torch.exp(hd @ wc.T - lse[at].double()[:, None]) - (tt[at, None] == ids[None]).double()
+        ref += (p * torch.where(tt[at] >= 0, dl[at].double(), 0.0)[:, None]).T @ hd
+    assert (dw[cols].double() - ref).norm() <= 3.2e-3 * ref.norm()
+
+
+def test_calls_from_two_host_threads(ops):
+    """Two threads, a stream each, first calls of some shapes included."""
+    import threading
+    states = [_state(141), _state(142, n=333, c=200, v=1111)]
+    want = []
+    out, errs = [None, None], []
+
+    def work(i):
+        try:
+            st = torch.cuda.Stream()
+            with torch.cuda.stream(st):
+                for _ in range(4):
+                    s = states[i]
+                    r = {}
+                    r["emb"] = ops.embed(s["table"], s["tok"])
+                    r["r"], r["x"] = ops.block_norm(r["emb"], s["w"], y=s["y"], w_post=s["w"], gate=s["gate"])
+                    r["loss"], r["lse"] = ops.lm_loss(r["x"], s["table"], s["tok"])
+                    r["dh"], r["dw"] = ops.lm_loss_bwd(r["x"], s["table"], s["tok"], r["lse"], s["dl"])
+                    r["dt"] = ops.embed_bwd(s["tok"], r["dh"], s["table"].shape[0])
+                    out[i] = r
+            st.synchronize()
+        except Exception as e:      # reported by the test's own thread
+            errs.append(e)
+
+    torch.cuda.synchronize()
+    threads = [threading.Thread(target=work, args=(i,)) for i in range(2)]
+    for th in threads:
+        th.start()
+    for th in threads:
+        th.join()
+    assert not errs, errs
+    both, out = out, [None, None]
+    for i in range(2):
+        work(i)
+        want.append(out[i])
+        _same(both[i], want[i])
