@@ -628,6 +628,14 @@ def _arg(t, dtype, shape, name):
     return t.data_ptr()
 
 
+def _out(t, dtype, shape, name, ref):
+    """(tensor, address) of an output: the caller's, checked, or a new one."""
+    if t is None:
+        t = torch.empty(shape, dtype=dtype, device=ref.device)
+        return t, t.data_ptr()
+    return t, _arg(t, dtype, shape, name)
+
+
 def _matrix(t, dtypes, name):
     """The shape of the 2-d tensor t, of one of dtypes, with rows of 8k channels."""
     if not isinstance(t, torch.Tensor):
@@ -641,8 +649,8 @@ def _matrix(t, dtypes, name):
 
 
 def _device(names, *tensors):
-    """The one CUDA device of all tensors (None skipped).  Checked after the
-    shapes, so a wrong shape is reported as such wherever the tensors live."""
+    """The one CUDA device of the caller's tensors (None skipped).  Checked after
+    the shapes, so a wrong shape is reported as such wherever the tensors live."""
     dev = tensors[0].get_device()
     for i, t in enumerate(tensors):
         if t is None:
@@ -697,9 +705,9 @@ def embed(table, tokens, scale=1.0, out=None):
     p_table = _arg(table, table.dtype, (V, C), "table")
     N = tokens.numel() if isinstance(tokens, torch.Tensor) else 0
     p_tok = _arg(tokens, torch.int32, (N,), "tokens")
-    out = torch.empty((N, C), dtype=torch.bfloat16, device=table.device) if out is None else out
-    p_out = _arg(out, torch.bfloat16, (N, C), "out")
-    dev = _device("table tokens out", table, tokens, out)
+    given = out
+    out, p_out = _out(out, torch.bfloat16, (N, C), "out", table)
+    dev = _device("table tokens out", table, tokens, given)
     _launch(dev, lib.tpk_embed, p_table, _TABLE_TYPES[table.dtype], p_tok, p_out, N, V, C, float(scale))
     return out
 
@@ -721,10 +729,10 @@ def embed_bwd(tokens, dout, vocab, scale=1.0, dtype=torch.float32, dtable=None, 
     dtype = dtype if dtable is None else dtable.dtype
     if dtype not in _TABLE_TYPES:
         raise TypeError("the table's gradient must be bf16 or fp32")
-    dtable = torch.empty((V, C), dtype=dtype, device=dout.device) if dtable is None else dtable
-    p_dt = _arg(dtable, dtype, (V, C), "dtable")
+    given = dtable, workspace
+    dtable, p_dt = _out(dtable, dtype, (V, C), "dtable", dout)
     ws = _workspace(workspace, lib.tpk_embed_bwd_workspace_bytes(N, V, C), dout, "the lookup's backward")
-    dev = _device("dout tokens dtable workspace", dout, tokens, dtable, ws)
+    dev = _device("dout tokens dtable workspace", dout, tokens, *given)
     _launch(dev, lib.tpk_embed_bwd, p_tok, p_dout, p_dt, _TABLE_TYPES[dtype], N, V, C, float(scale), ws.data_ptr(),
             ws.nbytes)
     return dtable
@@ -776,15 +784,12 @@ def block_norm(res, w_pre, y=None, w_post=None, gate=None, scale=1.0, eps=1e-6, 
     (r, x), both [N, C] bf16; ``res_out`` may be ``res`` itself."""
     lib = B.load()
     shape, args = _norm_args(res, w_pre, y, w_post, gate)
-    p_ro = None
-    if y is not None:
-        res_out = torch.empty_like(res) if res_out is None else res_out
-        p_ro = _arg(res_out, torch.bfloat16, shape, "res_out")
-    elif res_out is not None:
+    if y is None and res_out is not None:
         raise ValueError("without y nothing is added to res: res_out is not written")
-    out = torch.empty_like(res) if out is None else out
-    p_out = _arg(out, torch.bfloat16, shape, "out")
-    dev = _device("res w_pre y w_post gate res_out out", res, w_pre, y, w_post, gate, res_out, out)
+    given = res_out, out
+    res_out, p_ro = (None, None) if y is None else _out(res_out, torch.bfloat16, shape, "res_out", res)
+    out, p_out = _out(out, torch.bfloat16, shape, "out", res)
+    dev = _device("res w_pre y w_post gate res_out out", res, w_pre, y, w_post, gate, *given)
     _launch(dev, lib.tpk_block_norm, *args, p_ro, p_out, *shape, float(scale), float(eps))
     return (res if y is None else res_out), out
 
@@ -803,24 +808,25 @@ def block_norm_bwd(res, w_pre, dx, dres_out=None, y=None, w_post=None, gate=None
     for t, n, ref in ((dy, "dy", y), (dgate, "dgate", gate), (dw_post, "dw_post", w_post)):
         if t is not None and ref is None:
             raise ValueError("%s is given, but not the input it is the gradient of" % n)
-    dres = torch.empty_like(res) if dres is None else dres
-    p_dres = _arg(dres, torch.bfloat16, shape, "dres")
+    given = dres, dy, dgate, dw_post, dw_pre, workspace
+    bf16 = torch.bfloat16
+    dres, p_dres = _out(dres, bf16, shape, "dres", res)
     p_dy = p_dgate = p_dpost = None
     ld_dy = ld_dgate = C
-    if y is not None:
-        dy = torch.empty(shape, dtype=torch.bfloat16, device=res.device) if dy is None else dy
+    if dy is not None:
         p_dy, ld_dy = _rows2(dy, "dy", shape)
-    if gate is not None:
-        dgate = torch.empty(shape, dtype=torch.bfloat16, device=res.device) if dgate is None else dgate
+    elif y is not None:
+        dy, p_dy = _out(None, bf16, shape, "dy", res)
+    if dgate is not None:
         p_dgate, ld_dgate = _rows2(dgate, "dgate", shape)
+    elif gate is not None:
+        dgate, p_dgate = _out(None, bf16, shape, "dgate", res)
     if w_post is not None:
-        dw_post = torch.empty_like(w_post) if dw_post is None else dw_post
-        p_dpost = _arg(dw_post, torch.float32, (C,), "dw_post")
-    dw_pre = torch.empty_like(w_pre) if dw_pre is None else dw_pre
-    p_dpre = _arg(dw_pre, torch.float32, (C,), "dw_pre")
+        dw_post, p_dpost = _out(dw_post, torch.float32, (C,), "dw_post", res)
+    dw_pre, p_dpre = _out(dw_pre, torch.float32, (C,), "dw_pre", res)
     ws = _workspace(workspace, lib.tpk_block_norm_bwd_workspace_bytes(*shape), res, "the norms' backward")
     dev = _device("res w_pre dx dres_out y w_post gate dres dy dgate dw_post dw_pre workspace", res, w_pre, dx,
-                  dres_out, y, w_post, gate, dres, dy, dgate, dw_post, dw_pre, ws)
+                  dres_out, y, w_post, gate, *given)
     _launch(dev, lib.tpk_block_norm_bwd, *args, p_dro, p_dx, p_dres, p_dy, ld_dy, p_dgate, ld_dgate, p_dpost, p_dpre,
             *shape, float(scale), float(eps), ws.data_ptr(), ws.nbytes)
     return dres, dy, dgate, dw_post, dw_pre
@@ -847,12 +853,12 @@ def lm_loss(h, w, target, scale=1.0, loss=None, lse=None, workspace=None, dev_er
     target is outside [0, V) (a position without a prediction)."""
     lib = B.load()
     N, V, C, args = _loss_args(h, w, target, scale)
-    loss = torch.empty(N, dtype=torch.float32, device=h.device) if loss is None else loss
-    lse = torch.empty(N, dtype=torch.float32, device=h.device) if lse is None else lse
-    p_loss, p_lse = _arg(loss, torch.float32, (N,), "loss"), _arg(lse, torch.float32, (N,), "lse")
+    given = loss, lse, workspace, dev_err
+    loss, p_loss = _out(loss, torch.float32, (N,), "loss", h)
+    lse, p_lse = _out(lse, torch.float32, (N,), "lse", h)
     p_err = _dev_err(dev_err)
     ws = _workspace(workspace, lib.tpk_lm_loss_workspace_bytes(N, V, C, 0), h, "the loss")
-    dev = _device("h w target loss lse workspace dev_err", h, w, target, loss, lse, ws, dev_err)
+    dev = _device("h w target loss lse workspace dev_err", h, w, target, *given)
     _launch(dev, lib.tpk_lm_loss, *args, p_loss, p_lse, N, V, C, float(scale), ws.data_ptr(), ws.nbytes, p_err)
     return loss, lse
 
@@ -865,12 +871,12 @@ def lm_loss_bwd(h, w, target, lse, dloss, scale=1.0, dh=None, dw=None, workspace
     lib = B.load()
     N, V, C, args = _loss_args(h, w, target, scale)
     p_lse, p_dloss = _arg(lse, torch.float32, (N,), "lse"), _arg(dloss, torch.float32, (N,), "dloss")
-    dh = torch.empty_like(h) if dh is None else dh
-    dw = torch.empty_like(w) if dw is None else dw
-    p_dh, p_dw = _arg(dh, torch.bfloat16, (N, C), "dh"), _arg(dw, torch.bfloat16, (V, C), "dw")
+    given = dh, dw, workspace, dev_err
+    dh, p_dh = _out(dh, torch.bfloat16, (N, C), "dh", h)
+    dw, p_dw = _out(dw, torch.bfloat16, (V, C), "dw", h)
     p_err = _dev_err(dev_err)
     ws = _workspace(workspace, lib.tpk_lm_loss_workspace_bytes(N, V, C, 1), h, "the loss's backward")
-    dev = _device("h w target lse dloss dh dw workspace dev_err", h, w, target, lse, dloss, dh, dw, ws, dev_err)
+    dev = _device("h w target lse dloss dh dw workspace dev_err", h, w, target, lse, dloss, *given)
     _launch(dev, lib.tpk_lm_loss_bwd, *args, p_lse, p_dloss, p_dh, p_dw, N, V, C, float(scale), ws.data_ptr(),
             ws.nbytes, p_err)
     return dh, dw
