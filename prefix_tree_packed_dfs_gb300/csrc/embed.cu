@@ -12,13 +12,16 @@
 // written straight to its row of dtable; a run that crosses pieces leaves one
 // fp32 partial per piece, and a second kernel adds those in order -- so a
 // frequent id (thousands of rows) is spread over as many warps as it has
-// pieces.  Rows of ids that do not occur are zeroed by other blocks of the
-// same launch, which look the id up in the sorted order (32-way search, so
-// the table is written once instead of cleared and written again).
+// pieces.  Rows of ids that do not occur are zeroed: the highest ids by other
+// CTAs of the sort's launches, which leave the memory idle, the rest by other
+// CTAs of the sums' launch, which look the id up in the sorted order (32-way
+// search, so those rows are written once).
 // Measured on GB300, 96,888 rows of 2,048, 32,000 ids: lookup from an fp32
 // table 106 us (6.2 TB/s of the least bytes), from a bf16 one 80 us (6.6);
-// gradient 150 us: sort 25, sums 108 (6.1 TB/s: HBM-bound), join 17.  1,001
-// rows of 1,000: 11.5 us, four launches.
+// gradient 141 us, of which the sums are HBM-bound.  Rows cleared under the
+// sort, 48 MB per launch: 143 -> 141 us here, 60 -> 55 for 30,000 rows of
+// 1,024 into 30,000 (24 MB 56, 80 MB 61: then the sort waits for the memory).
+// 1,001 rows of 1,000: 11 us, three launches.
 #include <type_traits>
 
 #include "rowwise.cuh"
@@ -92,6 +95,20 @@ constexpr int kSortWarps = kSortThreads / 32;
 constexpr int kFewRounds = 4, kManyRounds = 16;
 constexpr int64_t kFewTiles = 512;   // up to here tiles of kFewRounds
 
+// The sort leaves the memory idle, so its launches carry CTAs that clear rows
+// of dtable meanwhile: the highest ids, kClear bytes per launch (what the
+// memory writes in a pass's time); rows whose ids do occur are written later.
+constexpr int64_t kClear = int64_t{48} << 20;
+struct Clear {
+  uint4* at;     // the launch's rows, 16-byte pieces
+  int64_t n;
+};
+__device__ __forceinline__ void clear_rows(const Clear& z, int block, int blocks) {
+  for (int64_t i = static_cast<int64_t>(block) * kSortThreads + threadIdx.x; i < z.n;
+       i += static_cast<int64_t>(blocks) * kSortThreads)
+    z.at[i] = make_uint4(0, 0, 0, 0);
+}
+
 __device__ __forceinline__ int key_of(int tok, int V) { return tok >= 0 && tok < V ? tok : V; }
 
 // Inclusive scan of one value per thread over the first 256 threads (8 warps);
@@ -162,11 +179,13 @@ __global__ void __launch_bounds__(kSortThreads) sort_scatter_kernel(const int32_
                                                                     int shift, const int32_t* __restrict__ hist,
                                                                     int32_t* __restrict__ hist_next,
                                                                     int32_t* __restrict__ keys_out,
-                                                                    int32_t* __restrict__ pos_out) {
+                                                                    int32_t* __restrict__ pos_out, int tiles,
+                                                                    Clear clear) {
+  if (static_cast<int>(blockIdx.x) >= tiles) return clear_rows(clear, blockIdx.x - tiles, gridDim.x - tiles);
   __shared__ int base[kSortWarps][kDigits];   // counts, then where each warp's keys of a digit go
   __shared__ int warp_sums[8];
   constexpr int kPer = kSortThreads * kRounds, kRun = 32 * kRounds;
-  const int tiles = gridDim.x, tile = blockIdx.x;
+  const int tile = blockIdx.x;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int64_t lo = static_cast<int64_t>(tile) * kPer + warp * kRun;
   const int n = lo >= N ? 0 : static_cast<int>(N - lo < kRun ? N - lo : kRun);   // the warp's keys
@@ -215,7 +234,8 @@ __global__ void __launch_bounds__(kSortThreads) sort_scatter_kernel(const int32_
 // Every pass of a single tile, in shared memory.
 __global__ void __launch_bounds__(kSortThreads) sort_one_kernel(const int32_t* __restrict__ tokens, int N, int V,
                                                                 int passes, int32_t* __restrict__ keys_out,
-                                                                int32_t* __restrict__ pos_out) {
+                                                                int32_t* __restrict__ pos_out, Clear clear) {
+  if (blockIdx.x > 0) return clear_rows(clear, blockIdx.x - 1, gridDim.x - 1);
   constexpr int kPer = kSortThreads * kFewRounds, kRun = 32 * kFewRounds;
   __shared__ int base[kSortWarps][kDigits];
   __shared__ int warp_sums[8];
@@ -316,14 +336,14 @@ __global__ void __launch_bounds__(kThreads) embed_sum_kernel(const int32_t* __re
                                                              const int32_t* __restrict__ pos,
                                                              const uint4* __restrict__ dout, int N, int V, int C,
                                                              float scale, void* __restrict__ dtable,
-                                                             float* __restrict__ part, int sum_blocks) {
+                                                             float* __restrict__ part, int sum_blocks, int cleared) {
   const int lane = threadIdx.x & 31;
   const int parts = (C + kCols - 1) / kCols;
   if (static_cast<int>(blockIdx.x) >= sum_blocks) {
-    // rows of ids that do not occur
+    // rows of ids that do not occur, up to those cleared under the sort
     const int64_t warps = static_cast<int64_t>(gridDim.x - sum_blocks) * (kThreads / 32);
-    for (int64_t v = static_cast<int64_t>(blockIdx.x - sum_blocks) * (kThreads / 32) + (threadIdx.x >> 5); v < V;
-         v += warps) {
+    for (int64_t v = static_cast<int64_t>(blockIdx.x - sum_blocks) * (kThreads / 32) + (threadIdx.x >> 5);
+         v < cleared; v += warps) {
       const int i = lower_bound_warp(keys, N, static_cast<int>(v));
       if (i < N && __ldg(keys + i) == v) continue;
       const int n16 = C * (kF32 ? 4 : 2) / 16;
@@ -480,9 +500,26 @@ SortShape sort_shape(int64_t N, int64_t V) {
 
 size_t up256(size_t n) { return (n + 255) / 256 * 256; }
 
+// The rows of dtable still to be cleared, [0, rows): the sort's launches take
+// from the end.
+struct Clearing {
+  uint8_t* dtable;
+  int64_t rows, row_bytes;
+  Clear next() {
+    int64_t n = kClear / row_bytes;
+    n = n < rows ? n : rows;
+    rows -= n;
+    return {reinterpret_cast<uint4*>(dtable + rows * row_bytes), n * row_bytes / 16};
+  }
+};
+unsigned clear_blocks(const Clear& c) {
+  const int64_t want = (c.n + 4 * kSortThreads - 1) / (4 * kSortThreads), most = int64_t{num_sms()} * 2;
+  return static_cast<unsigned>(want < most ? want : most);
+}
+
 template <int kRounds>
 int sort_tiles(const int32_t* tokens, int n, int v, const SortShape& sh, int32_t* hist, int32_t* const (&buf)[4],
-               const int32_t** keys, const int32_t** pos, cudaStream_t s) {
+               Clearing* z, const int32_t** keys, const int32_t** pos, cudaStream_t s) {
   const unsigned tiles = static_cast<unsigned>(sh.tiles);
   sort_hist_kernel<kRounds><<<tiles, kSortThreads, 0, s>>>(tokens, n, v, sh.passes, hist);
   int st = cuda_status(cudaGetLastError());
@@ -491,8 +528,10 @@ int sort_tiles(const int32_t* tokens, int n, int v, const SortShape& sh, int32_t
     int32_t* ko = buf[(p & 1) * 2];
     int32_t* po = buf[(p & 1) * 2 + 1];
     int32_t* h = hist + static_cast<int64_t>(p) * sh.tiles * kDigits;
-    sort_scatter_kernel<kRounds><<<tiles, kSortThreads, 0, s>>>(
-        tokens, ki, pi, n, v, 8 * p, h, p + 1 < sh.passes ? h + sh.tiles * kDigits : nullptr, ko, po);
+    const Clear c = z->next();
+    sort_scatter_kernel<kRounds><<<tiles + clear_blocks(c), kSortThreads, 0, s>>>(
+        tokens, ki, pi, n, v, 8 * p, h, p + 1 < sh.passes ? h + sh.tiles * kDigits : nullptr, ko, po,
+        static_cast<int>(tiles), c);
     st = cuda_status(cudaGetLastError());
     ki = ko;
     pi = po;
@@ -504,16 +543,17 @@ int sort_tiles(const int32_t* tokens, int n, int v, const SortShape& sh, int32_t
 
 template <bool kF32, int kPiece>
 int sum_runs(const int32_t* keys, const int32_t* pos, const void* dout, int n, int v, int C, float scale, void* dtable,
-             float* part, cudaStream_t s) {
+             float* part, int cleared, cudaStream_t s) {
   const int64_t pieces = (static_cast<int64_t>(n) + kPiece - 1) / kPiece;
   const int64_t sum_blocks = (pieces * ((C + kCols - 1) / kCols) + kThreads / 32 - 1) / (kThreads / 32);
   const int64_t join_blocks = (pieces * ((C + 127) / 128) + kThreads / 32 - 1) / (kThreads / 32);
-  int64_t zero_blocks = (static_cast<int64_t>(v) + kThreads / 32 - 1) / (kThreads / 32);
+  int64_t zero_blocks = (static_cast<int64_t>(cleared) + kThreads / 32 - 1) / (kThreads / 32);
   const int64_t most = int64_t{num_sms()} * 8;
   if (zero_blocks > most) zero_blocks = most;
   if (sum_blocks + zero_blocks > 0x7fffffff || join_blocks > 0x7fffffff) return TPK_E_ARG;
   embed_sum_kernel<kF32, kPiece><<<static_cast<unsigned>(sum_blocks + zero_blocks), kThreads, 0, s>>>(
-      keys, pos, static_cast<const uint4*>(dout), n, v, C, scale, dtable, part, static_cast<int>(sum_blocks));
+      keys, pos, static_cast<const uint4*>(dout), n, v, C, scale, dtable, part, static_cast<int>(sum_blocks),
+      cleared);
   const int st = cuda_status(cudaGetLastError());
   if (st != TPK_OK || pieces < 2) return st;
   embed_join_kernel<kF32, kPiece><<<static_cast<unsigned>(join_blocks), kThreads, 0, s>>>(keys, n, v, C, scale, dtable,
@@ -594,18 +634,21 @@ extern "C" int tpk_embed_bwd(const int32_t* tokens, const void* dout, void* dtab
   }
   float* part = reinterpret_cast<float*>(w);
   const int32_t *ki = buf[0], *pi = buf[1];
+  Clearing z{static_cast<uint8_t*>(dtable), V, int64_t{C} * (f32 ? 4 : 2)};
   if (sh.tiles == 1) {
-    sort_one_kernel<<<1, kSortThreads, 0, s>>>(tokens, n, v, sh.passes, buf[0], buf[1]);
+    const Clear c = z.next();
+    sort_one_kernel<<<1 + clear_blocks(c), kSortThreads, 0, s>>>(tokens, n, v, sh.passes, buf[0], buf[1], c);
     st = cuda_status(cudaGetLastError());
   } else {
-    st = sh.rounds == kFewRounds ? sort_tiles<kFewRounds>(tokens, n, v, sh, hist, buf, &ki, &pi, s)
-                                 : sort_tiles<kManyRounds>(tokens, n, v, sh, hist, buf, &ki, &pi, s);
+    st = sh.rounds == kFewRounds ? sort_tiles<kFewRounds>(tokens, n, v, sh, hist, buf, &z, &ki, &pi, s)
+                                 : sort_tiles<kManyRounds>(tokens, n, v, sh, hist, buf, &z, &ki, &pi, s);
   }
   if (st != TPK_OK) return st;
   const bool few = piece_for(N) == 16;
+  const int left = static_cast<int>(z.rows);
   if (f32)
-    return few ? sum_runs<true, 16>(ki, pi, dout, n, v, C, scale, dtable, part, s)
-               : sum_runs<true, 64>(ki, pi, dout, n, v, C, scale, dtable, part, s);
-  return few ? sum_runs<false, 16>(ki, pi, dout, n, v, C, scale, dtable, part, s)
-             : sum_runs<false, 64>(ki, pi, dout, n, v, C, scale, dtable, part, s);
+    return few ? sum_runs<true, 16>(ki, pi, dout, n, v, C, scale, dtable, part, left, s)
+               : sum_runs<true, 64>(ki, pi, dout, n, v, C, scale, dtable, part, left, s);
+  return few ? sum_runs<false, 16>(ki, pi, dout, n, v, C, scale, dtable, part, left, s)
+             : sum_runs<false, 64>(ki, pi, dout, n, v, C, scale, dtable, part, left, s);
 }
