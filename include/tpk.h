@@ -624,8 +624,10 @@ int tpk_lm_loss(const void* h, const void* w, const int32_t* target, float* loss
 /* Gradients of sum_f dloss[f] * loss[f]:
  *   dz[f, v] = dloss[f] * scale * (exp(z[f, v] - lse[f]) - [v = target[f]])
  *   dh[f] = sum_v dz[f, v] w[v],   dw[v] = sum_f dz[f, v] h[f]
- * lse is the forward's.  The scores are computed again, one piece of the
- * vocabulary at a time; dz enters its two products as bf16, sums are fp32 and
+ * lse is the forward's, of a call with the same N: near exp(z - lse) = 1 the
+ * difference from 1 is right only for the scores that lse was formed from.
+ * They are computed again, one piece of the vocabulary at a time; dz enters
+ * its two products as bf16, sums are fp32 and
  * deterministic.  dloss of a position without a target is not read.
  *   dh [N, C] bf16, dw [V, C] bf16 (16-byte aligned), every row written
  *   workspace: >= tpk_lm_loss_workspace_bytes(N, V, C, 1), 256-byte aligned,

@@ -19,7 +19,11 @@
 // The vocabulary is cut into pieces so that dz of one piece fits the
 // workspace (kDzBytes).  dz enters its products as bf16 (as the score
 // gradients do in the attention backward): a relative rounding of 2^-8 at
-// most, the size of the outputs' own.
+// most, the size of the outputs' own.  At a target of probability near 1 the
+// element is the small difference exp(z - lse) - 1, which carries any error of
+// z against lse whole; so kDz computes the very scores of kFwd (the same
+// chunks of K in the same order), and z - lse is formed before anything is
+// rounded: what is left is the rounding of lse itself, |lse| 2^-24.
 //
 // The product: 256 x 256 tiles on a pair of CTAs (tcgen05 cta_group::2, each
 // CTA holds 128 rows of A, 128 rows of B and its 128 rows of the result), 64
@@ -28,12 +32,10 @@
 // One CTA with a 128 x 256 tile would load 96 bytes of operands per cycle and
 // SM at full tensor rate; the pair loads 64.
 // The tensor core adds to its fp32 accumulator with truncation, a bias towards
-// zero of half a unit per step of 16 that grows with the width (measured: a
-// score of 6 at width 4,096 came out 2.5e-5 low).  The forward's fp32 results
-// show it, so there a tile's products stop after every 512 elements of K
-// (kChunk stages) and the epilogue adds the chunks up in registers with
-// rounding to nearest.  dz, dh and dw are rounded to bf16, a hundred times
-// coarser, and accumulate over all of K.
+// zero that grows with the number of steps of 16 (measured: a score of 6 at
+// width 4,096 came out 2.5e-5 low).  The scores show it, so their accumulation
+// stops after every 512 elements (kChunkOf stages) and the epilogue adds the
+// chunks up in registers with rounding to nearest.
 // Warps of a CTA: 0 TMA producer, 1 MMA issuer (of the pair's first CTA), 2
 // TMEM owner, 4-11 epilogue (two warpgroups, 128 columns each).  At widths
 // below about 1,000 the epilogue is what a tile waits for: its arithmetic is
@@ -46,6 +48,8 @@
 // What bounds it: the tensor pipe, busy 98% of the forward's cycles and 93-95%
 // of the others' (8,192 rows, width 2,048, 32,000 ids: forward 520 us, 2,065
 // TFLOP/s; dz 560, dh 574, dw 572 us); in long runs the power limit.
+#include <type_traits>
+
 #include "pair.cuh"
 #include "rowwise.cuh"
 
@@ -61,14 +65,16 @@ constexpr int kPanel = 8;
 constexpr int kSplitPairs = 76;       // pairs a split over K aims to fill (two SMs each)
 constexpr float kLog2e = 1.4426950408889634f;
 
-constexpr int kChunk = 8;             // stages of 64 elements per accumulation of the forward
-// The forward's epilogue holds 128 columns of a row per thread: the other
-// warps give registers to its two warpgroups.
+enum { kFwd = 0, kDz = 1, kDh = 2, kDw = 3 };
+
+// Stages of 64 elements per accumulation: the gradients' are all of K.
+template <int kMode>
+constexpr int kChunkOf = kMode == kFwd || kMode == kDz ? 8 : 1 << 25;
+// The epilogue holds 128 columns of a row per thread: the other warps give
+// registers to its two warpgroups.
 constexpr uint32_t kRegsCtl = 56;
 constexpr uint32_t kRegsEpi = 216;
 constexpr int kRegsNeeded = 128 * kRegsCtl + 256 * kRegsEpi;
-
-enum { kFwd = 0, kDz = 1, kDh = 2, kDw = 3 };
 
 struct LmParams {
   const int32_t* count;     // device: gathered rows; nullptr: n_rows
@@ -84,12 +90,11 @@ struct LmParams {
   float* zt;                // kFwd: [np] the target's score, unscaled
   int32_t run;              // kFwd: vocabulary tiles per unit
   int32_t v0, vcols, ld_dz; // the piece: first id, ids, row stride of dz
-  __nv_bfloat16* dz;
   float* acc;               // kDh: fp32 tiles; kDw: fp32 tiles of a split over K
   int32_t split_most;       // kDh
   int32_t first, last;      // kDh: first / last piece
   __nv_bfloat16* dh;
-  __nv_bfloat16* dw;
+  __nv_bfloat16* dw;        // kDw without any rows (else through the tensor map)
   int32_t* err;
 };
 
@@ -207,7 +212,13 @@ __device__ __forceinline__ Unit unit_of(const LmParams& p, const Shape& s, int u
   return w;
 }
 
-template <int kMode>
+// Columns 2 e and 2 e + 1 of 32 read from TMEM.
+__device__ __forceinline__ uint64_t pair_at(const uint32_t (&x)[32], int e) {
+  return ptx::f2(__uint_as_float(x[2 * e]), __uint_as_float(x[2 * e + 1]));
+}
+
+// kOne: every tile is a single accumulation, which then need not be held whole.
+template <int kMode, bool kOne>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     lm_product_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ CUtensorMap tm_b,
                       const __grid_constant__ CUtensorMap tm_out, const LmParams p) {
@@ -247,7 +258,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   ptx::tc_fence_after();
   const uint32_t tmem = S.tmem_base;
   if (warp < 4) {
-  if constexpr (kMode == kFwd) ptx::regs_dec<kRegsCtl>();
+  if constexpr (!kOne) ptx::regs_dec<kRegsCtl>();
   if (warp == 0) {
     // ------------------------------------------------------------ producer
     if (ptx::elect_one()) {
@@ -299,7 +310,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       for (int u = pair; ok && u < sh.units; u += n_pairs) {
         const Unit w = unit_of<kMode>(p, sh, u);
         if (w.nk == 0) continue;
-        const int per = kMode == kFwd ? kChunk : w.nk;   // stages per accumulation
+        constexpr int per = kChunkOf<kMode>;
         const int chunks = (w.nk + per - 1) / per;
         for (int j = 0; ok && j < w.n_run * chunks; ++j, ++tile) {
           const uint32_t buf = tile & 1;
@@ -334,25 +345,36 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   }
   } else {
     // ------------------------------------------------------------ epilogue
-    if constexpr (kMode == kFwd) ptx::regs_inc<kRegsEpi>();
+    if constexpr (!kOne) ptx::regs_inc<kRegsEpi>();
     const int wg = (warp - 4) >> 2;                     // column half
     const int lane = threadIdx.x & 31;
     const int rc = (warp & 3) * 32 + lane;              // row of this CTA's half tile
     const int r = static_cast<int>(rank) * kHalf + rc;  // row of the tile
     const uint32_t lane_off = static_cast<uint32_t>((warp & 3) * 32) << 16;
     const uint32_t bar_empty[2] = {ptx::cluster_addr(&S.tm_empty[0], 0), ptx::cluster_addr(&S.tm_empty[1], 0)};
-    const uint64_t k2 = ptx::f2(p.scale_log2, p.scale_log2);
+    // the exponent of 2 of a score (kFwd), of z - lse (kDz)
+    const float to_2 = kMode == kFwd ? p.scale_log2 : kLog2e;
+    const uint64_t k2 = ptx::f2(to_2, to_2), kz = ptx::f2(p.scale, p.scale);
     uint32_t tile = 0;
     int box = 0;   // kDz, kDw: the warpgroup's next box in shared memory
     bool ok = true;
     for (int u = pair; ok && u < sh.units; u += n_pairs) {
       const Unit w = unit_of<kMode>(p, sh, u);
-      if (kMode == kDh && w.nk == 0) continue;
+      if (w.nk == 0) {
+        // no ids left for this split (kDh); no rows at all: dw is zero
+        if (kMode == kDw) {
+          const int at = w.m * kTile + r, c0 = w.n0 * kTile + wg * kHalf;
+          if (at < p.vcols)
+            for (int c = c0; c < min(c0 + kHalf, p.C); c += 8)
+              *reinterpret_cast<uint4*>(p.dw + static_cast<int64_t>(p.v0 + at) * p.C + c) = make_uint4(0, 0, 0, 0);
+        }
+        continue;
+      }
       const int row = w.m * kTile + r;
       const int64_t tile_id = static_cast<int64_t>(w.split) * sh.mt * sh.nt + w.m * sh.nt + w.n0;
       // per-row inputs
       int tgt = -1;
-      float m = -INFINITY, s = 0.f, coef = 0.f, lse2 = 0.f;
+      float m = -INFINITY, s = 0.f, coef = 0.f, lse = 0.f;
       int64_t pos = row;
       if (kMode != kDw && row < count) {
         pos = p.rows ? __ldg(p.rows + row) : row;
@@ -360,41 +382,56 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         if (tgt < 0 || tgt >= p.V) tgt = -1;
         if (kMode == kDz) {
           coef = __ldg(p.dloss + pos) * p.scale;
-          lse2 = __ldg(p.lse + pos) * kLog2e;
+          lse = __ldg(p.lse + pos);
           tgt -= p.v0;
         }
       }
       for (int j = 0; j < w.n_run; ++j) {
-        if constexpr (kMode == kFwd) {
-          // the row's 128 columns as packed pairs, chunks of K added up
-          uint64_t z[kHalf / 2];
-          auto chunk = [&](bool first) {
-            const uint32_t buf = tile & 1;
-            if (!__all_sync(0xffffffffu, ptx::mbar_wait(&S.tm_full[buf], (tile / 2) & 1, abort_flag, kWaitLimitNs)))
-              return false;
-            ptx::tc_fence_after();
-            ++tile;
-            const uint32_t tm = tmem + lane_off + buf * kTile + wg * kHalf;
+        // the row's 128 columns as packed pairs, chunks of K added up
+        uint64_t z[kHalf / 2];
+        auto chunk = [&](auto first) {
+          const uint32_t buf = tile & 1;
+          if (!__all_sync(0xffffffffu, ptx::mbar_wait(&S.tm_full[buf], (tile / 2) & 1, abort_flag, kWaitLimitNs)))
+            return false;
+          ptx::tc_fence_after();
+          ++tile;
+          const uint32_t tm = tmem + lane_off + buf * kTile + wg * kHalf;
+          if constexpr (decltype(first)::value) {   // every read in flight at once
+            uint32_t x[4][32];
+#pragma unroll
+            for (int c = 0; c < 4; ++c) ptx::tmem_ld32(tm + c * 32, x[c]);
+#pragma unroll
+            for (int c = 0; c < 4; ++c) {
+              ptx::tmem_wait_ld_of(x[c]);
+#pragma unroll
+              for (int e = 0; e < 16; ++e) z[c * 16 + e] = pair_at(x[c], e);
+            }
+          } else {
 #pragma unroll
             for (int c = 0; c < 4; ++c) {
               uint32_t x[32];
               ptx::tmem_ld32(tm + c * 32, x);
               ptx::tmem_wait_ld_of(x);
 #pragma unroll
-              for (int e = 0; e < 16; ++e) {
-                const uint64_t v = ptx::f2(__uint_as_float(x[2 * e]), __uint_as_float(x[2 * e + 1]));
-                z[c * 16 + e] = first ? v : ptx::add2(z[c * 16 + e], v);
-              }
+              for (int e = 0; e < 16; ++e) z[c * 16 + e] = ptx::add2(z[c * 16 + e], pair_at(x, e));
             }
-            ptx::tc_fence_before();
-            __syncwarp();
-            if (lane == 0) ptx::mbar_arrive_cluster(bar_empty[buf]);
-            return true;
-          };
-          ok = chunk(true);
+          }
+          ptx::tc_fence_before();
+          __syncwarp();
+          if (lane == 0) ptx::mbar_arrive_cluster(bar_empty[buf]);
+          return true;
+        };
+        if constexpr (!kOne) {
+          ok = chunk(std::true_type{});
 #pragma unroll 1
-          for (int k = kChunk; ok && k < w.nk; k += kChunk) ok = chunk(false);
-          if (!ok) break;
+          for (int k = kChunkOf<kMode>; ok && k < w.nk; k += kChunkOf<kMode>) ok = chunk(std::false_type{});
+        } else {
+          ok = ptx::mbar_wait(&S.tm_full[tile & 1], (tile / 2) & 1, abort_flag, kWaitLimitNs);
+        }
+        // a warpgroup with barriers of its own gives up as a whole
+        if (Smem::kOut) ok = ptx::all_of_128(wg + 1, ok);
+        if (!ok) break;
+        if constexpr (kMode == kFwd) {
           // unscaled scores and their maximum: the differences are exact to a
           // rounding, which products with the scale would not leave them
           const int c0 = (w.n0 + j) * kTile + wg * kHalf;
@@ -441,40 +478,21 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           s = lo + hi;
           m = mn;
         } else {
-          const uint32_t buf = tile & 1;
-          const bool any = kMode != kDw || w.nk > 0;   // no rows at all: dw is zero
-          if (any) {
-            ok = ptx::mbar_wait(&S.tm_full[buf], (tile / 2) & 1, abort_flag, kWaitLimitNs);
-            // a warpgroup with barriers of its own gives up as a whole
-            ok = Smem::kOut ? ptx::all_of_128(wg + 1, ok) : __all_sync(0xffffffffu, ok);
-            if (!ok) break;
-            ptx::tc_fence_after();
-            ++tile;
-          }
           const int n0 = (w.n0 + j) * kTile + wg * kHalf;   // first column of this warpgroup
-          const uint32_t tm = tmem + lane_off + buf * kTile + wg * kHalf;
-          uint32_t raw[2][32];
-          if (any) {
-            ptx::tmem_ld32(tm, raw[0]);
-            ptx::tmem_wait_ld_of(raw[0]);
-          } else {
-#pragma unroll
-            for (int e = 0; e < 32; ++e) raw[0][e] = raw[1][e] = 0;
-          }
-#pragma unroll
-          for (int c = 0; c < 4; ++c) {
-            uint32_t(&x)[32] = raw[c & 1];
-            if (any && c < 3) ptx::tmem_ld32(tm + (c + 1) * 32, raw[(c + 1) & 1]);
+          // columns 32 c .. 32 c + 31 on their way out
+          auto emit = [&](int c, const uint64_t(&x)[16]) {
             const int c0 = n0 + c * 32;
             if constexpr (kMode == kDz || kMode == kDw) {
               uint32_t o[16];
               if constexpr (kMode == kDz) {
-                const uint64_t minus = ptx::f2(-lse2, -lse2), c2 = ptx::f2(coef, coef);
+                // z - lse, then the exponent of 2: with lse scaled first, the small
+                // difference of a p near 1 would carry that rounding too
+                const uint64_t minus = ptx::f2(-lse, -lse), c2 = ptx::f2(coef, coef);
                 float d[32];
 #pragma unroll
                 for (int e = 0; e < 32; e += 2) {
                   float lo, hi;
-                  ptx::unf2(ptx::fma2(ptx::f2(__uint_as_float(x[e]), __uint_as_float(x[e + 1])), k2, minus), lo, hi);
+                  ptx::unf2(ptx::mul2(ptx::fma2(x[e / 2], kz, minus), k2), lo, hi);
                   d[e] = ptx::ex2(lo);
                   d[e + 1] = ptx::ex2(hi);
                 }
@@ -495,8 +513,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                 }
               } else {
 #pragma unroll
-                for (int e = 0; e < 32; e += 2)
-                  o[e / 2] = ptx::pack_bf16x2(__uint_as_float(x[e]), __uint_as_float(x[e + 1]));
+                for (int e = 0; e < 16; ++e) {
+                  float lo, hi;
+                  ptx::unf2(x[e], lo, hi);
+                  o[e] = ptx::pack_bf16x2(lo, hi);
+                }
               }
               if (kMode == kDz || sh.splits == 1) {
                 // out through shared memory: 64 columns per box, in the TMA's
@@ -525,43 +546,69 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                 }
               } else {
                 float* blk = p.acc + tile_id * (kTile * kTile) + r * kTile + wg * kHalf + c * 32;
-                float4* ap = reinterpret_cast<float4*>(blk);
+                ulonglong2* ap = reinterpret_cast<ulonglong2*>(blk);
 #pragma unroll
-                for (int q = 0; q < 8; ++q)
-                  ap[q] = make_float4(__uint_as_float(x[4 * q]), __uint_as_float(x[4 * q + 1]),
-                                      __uint_as_float(x[4 * q + 2]), __uint_as_float(x[4 * q + 3]));
+                for (int q = 0; q < 8; ++q) ap[q] = make_ulonglong2(x[2 * q], x[2 * q + 1]);
               }
             } else {
               float* blk = p.acc + tile_id * (kTile * kTile) + r * kTile + wg * kHalf + c * 32;
               const bool out = p.last && sh.splits == 1;
 #pragma unroll
               for (int q = 0; q < 4; ++q) {
-                float v[8];
-#pragma unroll
-                for (int e = 0; e < 8; ++e) v[e] = __uint_as_float(x[8 * q + e]);
-                float4* ap = reinterpret_cast<float4*>(blk + 8 * q);
+                uint64_t v[4] = {x[4 * q], x[4 * q + 1], x[4 * q + 2], x[4 * q + 3]};
+                ulonglong2* ap = reinterpret_cast<ulonglong2*>(blk + 8 * q);
                 if (!p.first) {
-                  const float4 y = ap[0], z = ap[1];
-                  v[0] += y.x; v[1] += y.y; v[2] += y.z; v[3] += y.w;
-                  v[4] += z.x; v[5] += z.y; v[6] += z.z; v[7] += z.w;
+                  const ulonglong2 y0 = ap[0], y1 = ap[1];
+                  v[0] = ptx::add2(v[0], y0.x);
+                  v[1] = ptx::add2(v[1], y0.y);
+                  v[2] = ptx::add2(v[2], y1.x);
+                  v[3] = ptx::add2(v[3], y1.y);
                 }
                 if (!out) {
-                  ap[0] = make_float4(v[0], v[1], v[2], v[3]);
-                  ap[1] = make_float4(v[4], v[5], v[6], v[7]);
+                  ap[0] = make_ulonglong2(v[0], v[1]);
+                  ap[1] = make_ulonglong2(v[2], v[3]);
                 } else if (row < count && c0 + 8 * q < p.C) {
-                  *reinterpret_cast<uint4*>(p.dh + pos * p.C + c0 + 8 * q) =
-                      make_uint4(ptx::pack_bf16x2(v[0], v[1]), ptx::pack_bf16x2(v[2], v[3]),
-                                 ptx::pack_bf16x2(v[4], v[5]), ptx::pack_bf16x2(v[6], v[7]));
+                  uint32_t o[4];
+#pragma unroll
+                  for (int e = 0; e < 4; ++e) {
+                    float lo, hi;
+                    ptx::unf2(v[e], lo, hi);
+                    o[e] = ptx::pack_bf16x2(lo, hi);
+                  }
+                  *reinterpret_cast<uint4*>(p.dh + pos * p.C + c0 + 8 * q) = make_uint4(o[0], o[1], o[2], o[3]);
                 }
               }
             }
-            if (any && c < 3) {
-              ptx::tmem_wait_ld_of(raw[(c + 1) & 1]);
+          };
+          uint64_t x[16];
+          if constexpr (kOne) {
+            // 32 columns are read from TMEM while those before go out
+            const uint32_t buf = tile & 1;
+            const uint32_t tm = tmem + lane_off + buf * kTile + wg * kHalf;
+            ptx::tc_fence_after();
+            ++tile;
+            uint32_t raw[2][32];
+            ptx::tmem_ld32(tm, raw[0]);
+            ptx::tmem_wait_ld_of(raw[0]);
+#pragma unroll
+            for (int c = 0; c < 4; ++c) {
+              if (c < 3) ptx::tmem_ld32(tm + (c + 1) * 32, raw[(c + 1) & 1]);
+#pragma unroll
+              for (int e = 0; e < 16; ++e) x[e] = pair_at(raw[c & 1], e);
+              emit(c, x);
+              if (c < 3) ptx::tmem_wait_ld_of(raw[(c + 1) & 1]);
               if (c == 2) {   // the whole tile has been read
                 ptx::tc_fence_before();
                 __syncwarp();
                 if (lane == 0) ptx::mbar_arrive_cluster(bar_empty[buf]);
               }
+            }
+          } else {
+#pragma unroll
+            for (int c = 0; c < 4; ++c) {
+#pragma unroll
+              for (int e = 0; e < 16; ++e) x[e] = z[c * 16 + e];
+              emit(c, x);
             }
           }
         }
@@ -756,6 +803,28 @@ struct Few {
   static constexpr int kPerSm = kN == 1 ? 4 : kN == 2 ? 3 : 2;
 };
 
+// A score, 8 channels at a time per lane, then the warp's sum: one order for
+// the forward's scores and the backward's targets.
+__device__ __forceinline__ uint64_t dot8(uint4 w, ulonglong2 a, ulonglong2 b, uint64_t acc) {
+  auto pair = [](uint32_t u) { return ptx::f2(lo16(u), hi16(u)); };
+  acc = ptx::fma2(pair(w.x), a.x, acc);
+  acc = ptx::fma2(pair(w.y), a.y, acc);
+  acc = ptx::fma2(pair(w.z), b.x, acc);
+  return ptx::fma2(pair(w.w), b.y, acc);
+}
+__device__ __forceinline__ uint64_t dot8(uint4 w, uint4 h, uint64_t acc) {
+  auto pair = [](uint32_t u) { return ptx::f2(lo16(u), hi16(u)); };
+  return dot8(w, make_ulonglong2(pair(h.x), pair(h.y)), make_ulonglong2(pair(h.z), pair(h.w)), acc);
+}
+__device__ __forceinline__ float dot_sum(uint64_t acc) {
+  float lo, hi;
+  ptx::unf2(acc, lo, hi);
+  float z = lo + hi;
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) z += __shfl_xor_sync(0xffffffffu, z, o);
+  return z;
+}
+
 template <int kN>
 __global__ void __launch_bounds__(256, Few<kN>::kPerSm)
     lm_few_kernel(const uint4* __restrict__ h, const uint4* __restrict__ w, const int32_t* __restrict__ target, int N,
@@ -791,13 +860,7 @@ __global__ void __launch_bounds__(256, Few<kN>::kPerSm)
       for (int n = 0; n < kN; ++n) {
         const ulonglong2 a = ptx::lds128u(hs + 2 * (n * vecs + c)), b = ptx::lds128u(hs + 2 * (n * vecs + c) + 1);
 #pragma unroll
-        for (int i = 0; i < kFewV; ++i) {
-          auto pair = [](uint32_t u) { return ptx::f2(lo16(u), hi16(u)); };
-          acc[i][n] = ptx::fma2(pair(x[i].x), a.x, acc[i][n]);
-          acc[i][n] = ptx::fma2(pair(x[i].y), a.y, acc[i][n]);
-          acc[i][n] = ptx::fma2(pair(x[i].z), b.x, acc[i][n]);
-          acc[i][n] = ptx::fma2(pair(x[i].w), b.y, acc[i][n]);
-        }
+        for (int i = 0; i < kFewV; ++i) acc[i][n] = dot8(x[i], a, b, acc[i][n]);
       }
     }
 #pragma unroll
@@ -805,11 +868,7 @@ __global__ void __launch_bounds__(256, Few<kN>::kPerSm)
       float z[kFewV], top = -INFINITY;
 #pragma unroll
       for (int i = 0; i < kFewV; ++i) {
-        float lo, hi;
-        ptx::unf2(acc[i][n], lo, hi);
-        z[i] = lo + hi;
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1) z[i] += __shfl_xor_sync(0xffffffffu, z[i], o);
+        z[i] = dot_sum(acc[i][n]);
         if (v0 + i >= V) z[i] = -INFINITY;
         if (lane == 0 && n < N && v0 + i < V && v0 + i == tgt[n]) zt[n] = z[i];
         top = fmaxf(top, z[i]);
@@ -831,6 +890,25 @@ __global__ void __launch_bounds__(256, Few<kN>::kPerSm)
     for (int k = 1; k < 8; ++k) x = merge(x, sm[k][threadIdx.x], scale_log2);
     part[static_cast<int64_t>(blockIdx.x) * np + threadIdx.x] = x;
   }
+}
+
+// dz of a few positions at their targets, for the scores that lm_few_kernel
+// computes: those of the tensor core are truncated, by more than exp(z - lse) - 1
+// may be off where the target's probability is near 1.  A warp per position.
+__global__ void lm_few_target_kernel(const uint4* __restrict__ h, const uint4* __restrict__ w,
+                                     const int32_t* __restrict__ target, const int32_t* __restrict__ pos,
+                                     const float* __restrict__ lse, const float* __restrict__ dloss, int v0, int vcols,
+                                     int vecs, float scale, int ld_dz, __nv_bfloat16* __restrict__ dz) {
+  const int lane = threadIdx.x & 31, f = threadIdx.x >> 5;
+  const int r = __ldg(pos + f);
+  const int64_t t = __ldg(target + f);
+  if (r < 0 || t < v0 || t >= int64_t{v0} + vcols) return;
+  uint64_t acc = 0;
+  for (int c = lane; c < vecs; c += 32) acc = dot8(__ldg(w + t * vecs + c), __ldg(h + f * vecs + c), acc);
+  const float z = dot_sum(acc);
+  if (lane == 0)
+    dz[static_cast<int64_t>(r) * ld_dz + (t - v0)] =
+        __float2bfloat16_rn(__ldg(dloss + f) * scale * expm1f(fmaf(z, scale, -__ldg(lse + f))));
 }
 
 // 8 columns of row r of a product that was split over K: its splits' sums.
@@ -1021,24 +1099,25 @@ bool sizes_ok(int64_t N, int64_t V, int32_t C) {
          C <= (1 << 20);
 }
 
-template <int kMode>
+template <int kMode, bool kOne = false>
 int launch_product(const CUtensorMap& a, const CUtensorMap& b, const CUtensorMap& out, const LmParams& p,
                    int64_t most_units, cudaStream_t s) {
+  constexpr auto kern = lm_product_kernel<kMode, kOne>;
   static PerContext<int> rec;
   int unused = 0;
   const int st = guarded([&] { return rec.get(&unused, [](int*) {
     cudaFuncAttributes fa;
-    if (cudaFuncGetAttributes(&fa, lm_product_kernel<kMode>) != cudaSuccess) return TPK_E_CUDA;
+    if (cudaFuncGetAttributes(&fa, kern) != cudaSuccess) return TPK_E_CUDA;
     // setmaxnreg waits for registers the CTA was not launched with
-    if (kMode == kFwd && fa.numRegs * kThreads < kRegsNeeded) return TPK_E_UNSUPPORTED;
-    return cuda_status(cudaFuncSetAttribute(lm_product_kernel<kMode>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+    if (!kOne && fa.numRegs * kThreads < kRegsNeeded) return TPK_E_UNSUPPORTED;
+    return cuda_status(cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                             static_cast<int>(kLmSmemBytes<kMode>)));
   }); });
   if (st != TPK_OK) return st;
   int64_t pairs = num_sms() / 2;
   if (pairs < 1) pairs = 1;
   if (pairs > most_units) pairs = most_units;
-  lm_product_kernel<kMode><<<static_cast<unsigned>(2 * pairs), kThreads, kLmSmemBytes<kMode>, s>>>(a, b, out, p);
+  kern<<<static_cast<unsigned>(2 * pairs), kThreads, kLmSmemBytes<kMode>, s>>>(a, b, out, p);
   return cuda_status(cudaGetLastError());
 }
 
@@ -1188,7 +1267,6 @@ extern "C" int tpk_lm_loss_bwd(const void* h, const void* w, const int32_t* targ
   p.scale = scale;
   p.scale_log2 = scale * kLog2e;
   p.ld_dz = static_cast<int32_t>(sh.piece);
-  p.dz = k.dz;
   p.split_most = split_limit(static_cast<int>(((sh.piece < V ? sh.piece : V) + 63) / 64));
   p.dh = static_cast<__nv_bfloat16*>(dh);
   p.dw = static_cast<__nv_bfloat16*>(dw);
@@ -1200,7 +1278,15 @@ extern "C" int tpk_lm_loss_bwd(const void* h, const void* w, const int32_t* targ
     p.first = i == 0;
     p.last = i + 1 == sh.pieces;
     const int64_t vt = (p.vcols + kTile - 1) / kTile;
-    st = launch_product<kDz>(hk, wk, zk, p, sh.np / kTile * vt, s);
+    const int64_t dz_units = sh.np / kTile * vt;
+    st = C <= 64 * kChunkOf<kDz> ? launch_product<kDz, true>(hk, wk, zk, p, dz_units, s)
+                                 : launch_product<kDz>(hk, wk, zk, p, dz_units, s);
+    if (st == TPK_OK && use_few(N, C)) {
+      lm_few_target_kernel<<<1, static_cast<unsigned>(32 * N), 0, s>>>(
+          static_cast<const uint4*>(h), static_cast<const uint4*>(w), target, k.pos, lse, dloss, p.v0, p.vcols, C / 8,
+          scale, p.ld_dz, k.dz);
+      st = cuda_status(cudaGetLastError());
+    }
     p.acc = k.acc_h;
     if (st == TPK_OK) st = launch_product<kDh>(zk, wm, zk, p, INT64_MAX, s);
     p.acc = k.acc_w;

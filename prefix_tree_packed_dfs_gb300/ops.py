@@ -865,8 +865,9 @@ def lm_loss(h, w, target, scale=1.0, loss=None, lse=None, workspace=None, dev_er
 
 def lm_loss_bwd(h, w, target, lse, dloss, scale=1.0, dh=None, dw=None, workspace=None, dev_err=None):
     """Gradients of sum(dloss * loss) (``tpk_lm_loss_bwd``): h, w, target,
-    scale as given to ``lm_loss``, lse its result, dloss [N] fp32 the weight of
-    each position's loss (e.g. ``sum_to_forwarded`` of per-token weights).
+    scale as given to ``lm_loss``, lse its result for these rows in one call (it
+    has to fit the scores, which are computed again), dloss [N] fp32 the weight
+    of each position's loss (e.g. ``sum_to_forwarded`` of per-token weights).
     Returns (dh [N, C] bf16, dw [V, C] bf16)."""
     lib = B.load()
     N, V, C, args = _loss_args(h, w, target, scale)
