@@ -60,3 +60,61 @@ def test_lm_loss_gradient_of_confident_targets(ops, n, c):
     tol = most * dl.double().abs() * (4 * BF * -torch.expm1(-r_loss) + (lse.double().abs() + 24) * U)
     worst = int((off - tol).argmax())
     assert (off <= tol).all(), (worst, float(off[worst]), float(tol[worst]), float(ref[worst].norm()))
+
+
+def _relative_mean(got, ref):
+    return float(((got.double() - ref) / ref).mean())
+
+
+# A long sum of one sign: an accumulation of n truncations, each below one unit
+# (2 u) of the running value, is low by at most n u of its result (half of them
+# at full magnitude).  The accumulations are of 2,048 elements, 128 instructions
+# of 16 products with two truncations each, added up with rounding to nearest.
+# What else is not zero in the mean is small: the exponentials (2^-22) and lse
+# (|lse| u).  The bf16 roundings of the results are: their mean over the M
+# elements looked at is within 4 b / (2 sqrt M).
+STEPS = 256
+
+
+def test_lm_loss_dw_of_a_long_batch_of_one_sign(ops):
+    """200,000 positions, all of one target: dw of the other ids is a sum of
+    200,000 positive terms (320 tiles of dw: no split over the positions)."""
+    n, v, c = 200_000, 8192, 2560
+    scale = torch.rand(c, generator=torch.Generator(device="cuda").manual_seed(211), device="cuda") * 1.5 + 0.5
+    h = torch.empty(n, c, dtype=torch.bfloat16, device="cuda")
+    for i, part in enumerate(h.split(50_000)):
+        part.copy_(_rnd(212 + i, *part.shape, dtype=torch.float32).abs() * scale)
+    w = _rnd(216, v, c, std=0.01)
+    tt = torch.zeros(n, dtype=torch.int32, device="cuda")
+    dl = torch.full((n,), 2.0 ** -10, device="cuda")
+    _, lse = ops.lm_loss(h, w, tt)
+    _, dw = ops.lm_loss_bwd(h, w, tt, lse, dl)
+    ids = torch.arange(1, v, 509, device="cuda")
+    ref = torch.zeros(len(ids), c, dtype=torch.float64, device="cuda")
+    for lo in range(0, n, 50_000):
+        hd = h[lo:lo + 50_000].double()
+        ref += torch.exp(hd @ w[ids].double().T - lse[lo:lo + 50_000].double()[:, None]).T @ hd * 2.0 ** -10
+    tol = STEPS * U + 2.0 ** -22 + float(lse.abs().max()) * U + 2 * BF / ref.numel() ** 0.5
+    assert abs(_relative_mean(dw[ids], ref)) <= tol
+
+
+def test_lm_loss_dh_of_a_large_vocabulary_of_one_sign(ops):
+    """262,144 ids with positive rows and a target whose row is zero: dh is a
+    sum of 262,144 positive terms (320 tiles of dh: no split over the ids)."""
+    n, v, c = 8192, 262_144, 2560
+    scale = torch.rand(c, generator=torch.Generator(device="cuda").manual_seed(221), device="cuda") * 1.5 + 0.5
+    w = torch.empty(v, c, dtype=torch.bfloat16, device="cuda")
+    for i, part in enumerate(w.split(65_536)):
+        part.copy_(_rnd(222 + i, *part.shape, dtype=torch.float32).abs() * scale)
+    w[7] = 0
+    h = _rnd(226, n, c, std=0.01)
+    tt = torch.full((n,), 7, dtype=torch.int32, device="cuda")
+    _, lse = ops.lm_loss(h, w, tt)
+    dh, _ = ops.lm_loss_bwd(h, w, tt, lse, torch.ones(n, device="cuda"))
+    rows = torch.arange(3, n, 257, device="cuda")
+    ref = torch.zeros(len(rows), c, dtype=torch.float64, device="cuda")
+    for lo in range(0, v, 65_536):
+        wd = w[lo:lo + 65_536].double()
+        ref += torch.exp(h[rows].double() @ wd.T - lse[rows].double()[:, None]) @ wd
+    tol = STEPS * U + 2.0 ** -22 + float(lse.abs().max()) * U + 2 * BF / ref.numel() ** 0.5
+    assert abs(_relative_mean(dh[rows], ref)) <= tol
