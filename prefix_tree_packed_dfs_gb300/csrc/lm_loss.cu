@@ -468,7 +468,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           const float mn = ptx::max3(top[0], top[1], fmaxf(top[2], top[3]));
           const float ms = mn == -INFINITY ? 0.f : mn;
           const uint64_t neg = ptx::f2(-ms, -ms);
-          uint64_t q[4] = {ptx::f2(s * ptx::ex2((m - ms) * p.scale_log2), 0.f), 0, 0, 0};
+          uint64_t q[4] = {};
 #pragma unroll
           for (int e = 0; e < kHalf / 2; ++e) {
             float lo, hi;
@@ -477,7 +477,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           }
           float lo, hi;
           ptx::unf2(ptx::add2(ptx::add2(q[0], q[1]), ptx::add2(q[2], q[3])), lo, hi);
-          s = lo + hi;
+          // the tile's sum first: many small terms added one by one onto the
+          // large term of an earlier tile would round away
+          s = fmaf(s, ptx::ex2((m - ms) * p.scale_log2), lo + hi);
           m = mn;
         } else {
           const int n0 = (w.n0 + j) * kTile + wg * kHalf;   // first column of this warpgroup

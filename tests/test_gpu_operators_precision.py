@@ -118,3 +118,23 @@ def test_lm_loss_dh_of_a_large_vocabulary_of_one_sign(ops):
         ref += torch.exp(h[rows].double() @ wd.T - lse[rows].double()[:, None]) @ wd
     tol = STEPS * U + 2.0 ** -22 + float(lse.abs().max()) * U + 2 * BF / ref.numel() ** 0.5
     assert abs(_relative_mean(dh[rows], ref)) <= tol
+
+
+def test_lm_loss_of_many_small_probabilities(ops):
+    """A target with score 17 against 31,999 ids with score 0: each adds e^-17,
+    less than half a step of the sum that already holds the target's 1.  The
+    loss may miss what is added onto that 1 element by element: the 15 other
+    columns of the target's own accumulator in its tile, then an addition per
+    tile of its run (16 at most), per slot (2 * 16) and in the joining tree
+    (5), each off by u, 2^-22 of the exponentials and two roundings of the
+    small loss itself."""
+    n, v, c = 96_888, 32_000, 8
+    h = torch.zeros(n, c, dtype=torch.bfloat16, device="cuda")
+    h[:, 0] = 17.0
+    w = torch.zeros(v, c, dtype=torch.bfloat16, device="cuda")
+    ref = float(np.log1p((v - 1) * np.exp(-17.0)))
+    for target in (0, 64, 16_000):
+        w.zero_()
+        w[target, 0] = 1.0
+        loss, _ = ops.lm_loss(h, w, torch.full((n,), target, dtype=torch.int32, device="cuda"))
+        assert float((loss.double() - ref).abs().max()) <= (15 + 16 + 32 + 5) * U + ref * (2.0 ** -22 + 2 * U)
