@@ -81,10 +81,17 @@ __device__ __forceinline__ float add_pair(uint64_t v) {
   ptx::unf2(v, a, b);
   return a + b;
 }
-__device__ __forceinline__ uint64_t sigmoid2(uint64_t g) {
+// e^-g of a gate, finite; sigmoid(g) = 1 / (1 + e^-g) of it, and 1 - sigmoid(g)
+// as their product: from sigmoid(g) itself it would cancel where that is near 1.
+// (Where e^-g would be infinite the sigmoid comes out as zero, and the product too.)
+__device__ __forceinline__ uint64_t exp_minus2(uint64_t g) {
   float a, b;
   ptx::unf2(ptx::mul2(g, both(-1.4426950408889634f)), a, b);
-  ptx::unf2(ptx::add2(ptx::f2(ptx::ex2(a), ptx::ex2(b)), both(1.f)), a, b);
+  return ptx::f2(fminf(ptx::ex2(a), 3.4e38f), fminf(ptx::ex2(b), 3.4e38f));
+}
+__device__ __forceinline__ uint64_t sigmoid2(uint64_t exp_minus) {
+  float a, b;
+  ptx::unf2(ptx::add2(exp_minus, both(1.f)), a, b);
   asm("rcp.approx.ftz.f32 %0, %0;" : "+f"(a));
   asm("rcp.approx.ftz.f32 %0, %0;" : "+f"(b));
   return ptx::f2(a, b);
@@ -318,7 +325,7 @@ __global__ void __launch_bounds__(BwdShape<kT, kV>::kBlock, BwdShape<kT, kV>::kM
       group_sum<kT, 1>(ss, red[group], group, t);
       rstd_y = rsqrtf(ss[0] * inv_c + p.eps);
     }
-    Oct r[kV], sig[kV];
+    Oct r[kV], ex[kV];
     uint64_t q0 = 0, q1 = 0;   // sum r^2, sum dn * r
 #pragma unroll
     for (int j = 0; j < kV; ++j) {
@@ -336,8 +343,8 @@ __global__ void __launch_bounds__(BwdShape<kT, kV>::kBlock, BwdShape<kT, kV>::kM
           const Oct g = oct(*place(stage, 2, j));
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
-            sig[j].v[e] = sigmoid2(g.v[e]);
-            u.v[e] = ptx::mul2(u.v[e], sig[j].v[e]);
+            ex[j].v[e] = exp_minus2(g.v[e]);
+            u.v[e] = ptx::mul2(u.v[e], sigmoid2(ex[j].v[e]));
           }
         }
 #pragma unroll
@@ -385,9 +392,9 @@ __global__ void __launch_bounds__(BwdShape<kT, kV>::kBlock, BwdShape<kT, kV>::kM
         Oct g;
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-          const uint64_t s = sig[j].v[e], u = p.w_post ? ptx::mul2(yh.v[e], w.v[e]) : yh.v[e];
+          const uint64_t s = sigmoid2(ex[j].v[e]), u = p.w_post ? ptx::mul2(yh.v[e], w.v[e]) : yh.v[e];
           d.v[e] = ptx::mul2(d.v[e], s);
-          g.v[e] = ptx::mul2(ptx::mul2(d.v[e], u), ptx::fma2(s, both(-1.f), both(1.f)));
+          g.v[e] = ptx::mul2(ptx::mul2(d.v[e], u), ptx::mul2(ex[j].v[e], s));
         }
         p.dgate[row * p.ld_dgate + c] = pack_oct(g);
       }

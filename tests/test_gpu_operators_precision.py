@@ -138,3 +138,29 @@ def test_lm_loss_of_many_small_probabilities(ops):
         w[target, 0] = 1.0
         loss, _ = ops.lm_loss(h, w, torch.full((n,), target, dtype=torch.int32, device="cuda"))
         assert float((loss.double() - ref).abs().max()) <= (15 + 16 + 32 + 5) * U + ref * (2.0 ** -22 + 2 * U)
+
+
+@pytest.mark.parametrize("post", [True, False])
+@pytest.mark.parametrize("c", [64, 520, 2048, 16384])
+def test_block_norm_gradient_of_saturated_gates(ops, post, c):
+    """dgate = d u s (1 - s), s = sigmoid(gate): relative at both ends, where
+    s or 1 - s is e^-|gate|.  s, 1 - s, u and d are within 2^-16 of their terms'
+    magnitudes each (a row's statistics 64 u, 2^x of |gate| <= 80 another 80 u),
+    their product within 2^-15 and a bf16 rounding b.  At |gate| = 80 some
+    products lie below the least normal number 2^-126: there fp32 and bf16 have
+    fewer bits or flush to zero, both off by less than 2^-126."""
+    n = 34
+    gates = torch.tensor([12.0, -12.0, 20.0, -20.0, 9.0, -9.0, 40.0, -40.0, 80.0, -80.0, 0.0, 3.0, -3.0, 16.0, 17.5,
+                          30.0, -30.0], device="cuda")
+    gate = gates.repeat(2)[:, None].expand(n, c).contiguous().bfloat16()
+    res, y, dr = _rnd(231, n, c), _rnd(232, n, c), _rnd(233, n, c)
+    one = torch.ones(c, device="cuda")
+    wp = 1 + _rnd(234, c, std=0.1, dtype=torch.float32) if post else None
+    # no gradient through the second norm: d = scale * dres_out alone
+    got = ops.block_norm_bwd(res, one, torch.zeros_like(res), dres_out=dr, y=y, w_post=wp, gate=gate, scale=0.5)[2]
+    u = y.double()
+    if post:
+        u = u / (u.square().mean(1, keepdim=True) + 1e-6).sqrt() * wp.double()
+    g = gate.double()
+    ref = 0.5 * dr.double() * u * torch.sigmoid(g) * torch.sigmoid(-g)
+    assert ((got.double() - ref).abs() <= (BF + 2.0 ** -15) * ref.abs() + 2.0 ** -126).all()
