@@ -1098,8 +1098,9 @@ size_t carve(uint8_t* base, int64_t N, int64_t V, int32_t C, bool backward, LmWo
   return c.at;
 }
 
+// (the row counters of the kernels' last strides stay below 2^31)
 bool sizes_ok(int64_t N, int64_t V, int32_t C) {
-  return N >= 0 && N < (int64_t{1} << 31) - kTile && V >= 1 && V < (int64_t{1} << 31) - 4096 && C >= 8 && C % 8 == 0 &&
+  return N >= 0 && N < (int64_t{1} << 31) - 8192 && V >= 1 && V < (int64_t{1} << 31) - 4096 && C >= 8 && C % 8 == 0 &&
          C <= (1 << 20);
 }
 
