@@ -62,6 +62,29 @@ def test_lm_loss_gradient_of_confident_targets(ops, n, c):
     assert (off <= tol).all(), (worst, float(off[worst]), float(tol[worst]), float(ref[worst].norm()))
 
 
+@pytest.mark.parametrize("n,v,c", [(700, 129, 1000), (257, 513, 4096), (3000, 1200, 1000), (5, 4096, 2048),
+                                   (2, 5003, 4096), (4, 77, 4096), (1, 100, 16384), (300, 40, 16384)])
+@pytest.mark.parametrize("scale", [1.0, 0.7])
+def test_lm_loss_gradients_in_the_two_norm_at_wide_rows(ops, n, v, c, scale):
+    """dz and the result each round by b at most, b / sqrt 3 in the root mean
+    square: b sqrt(2/3) = 3.2e-3.  With a handful of positions the targets'
+    elements carry dw, each a single rounding of dz: b + b / sqrt 3.  Scores
+    (standard deviation 2) are within 1e-5: a hundredth of that."""
+    h, w = _rnd(241, n, c), _rnd(242, v, c, std=2.0 / c ** 0.5)
+    tt = torch.from_numpy(np.random.default_rng(243).integers(0, v, n).astype(np.int32)).cuda()
+    dl = _rnd(244, n, dtype=torch.float32)
+    _, lse = ops.lm_loss(h, w, tt, scale=scale)
+    dh, dw = ops.lm_loss_bwd(h, w, tt, lse, dl, scale=scale)
+    sc = float(np.float32(scale))
+    hd, wd = h.double(), w.double()
+    p = torch.softmax(sc * (hd @ wd.T), 1)
+    p[torch.arange(n, device="cuda"), tt.long()] -= 1
+    dz = p * (dl.double() * sc)[:, None]
+    most = BF * (2 / 3) ** 0.5 if n >= 16 else BF * (1 + 3 ** -0.5)
+    for got, ref in ((dh, dz @ wd), (dw, dz.T @ hd)):
+        assert float((got.double() - ref).norm() / ref.norm()) <= 1.01 * most
+
+
 def _relative_mean(got, ref):
     return float(((got.double() - ref) / ref).mean())
 
