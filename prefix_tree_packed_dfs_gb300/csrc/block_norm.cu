@@ -85,9 +85,14 @@ __device__ __forceinline__ float add_pair(uint64_t v) {
 // as their product: from sigmoid(g) itself it would cancel where that is near 1.
 // (Where e^-g would be infinite the sigmoid comes out as zero, and the product too.)
 __device__ __forceinline__ uint64_t exp_minus2(uint64_t g) {
+  auto finite = [](float e) {   // NaN stays NaN
+    float r;
+    asm("min.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(e), "f"(3.4e38f));
+    return r;
+  };
   float a, b;
   ptx::unf2(ptx::mul2(g, both(-1.4426950408889634f)), a, b);
-  return ptx::f2(fminf(ptx::ex2(a), 3.4e38f), fminf(ptx::ex2(b), 3.4e38f));
+  return ptx::f2(finite(ptx::ex2(a)), finite(ptx::ex2(b)));
 }
 __device__ __forceinline__ uint64_t sigmoid2(uint64_t exp_minus) {
   float a, b;

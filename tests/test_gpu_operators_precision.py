@@ -187,3 +187,21 @@ def test_block_norm_gradient_of_saturated_gates(ops, post, c):
     g = gate.double()
     ref = 0.5 * dr.double() * u * torch.sigmoid(g) * torch.sigmoid(-g)
     assert ((got.double() - ref).abs() <= (BF + 2.0 ** -15) * ref.abs() + 2.0 ** -126).all()
+
+
+@pytest.mark.parametrize("post", [True, False])
+def test_block_norm_gradient_of_gates_that_are_no_numbers(ops, post):
+    """A NaN gate makes its whole row NaN, as r there is NaN, and no other row;
+    infinite gates are an open and a closed one."""
+    n, c = 9, 264
+    res, y, dr, dx = (_rnd(s, n, c) for s in (251, 252, 253, 254))
+    one = torch.ones(c, device="cuda")
+    wp = one if post else None
+    gate = torch.zeros(n, c, dtype=torch.bfloat16, device="cuda")
+    gate[3, 5] = float("nan")
+    gate[6], gate[7] = float("inf"), float("-inf")
+    dres, dy, dgate = ops.block_norm_bwd(res, one, dx, dres_out=dr, y=y, w_post=wp, gate=gate)[:3]
+    for t in (dres, dy):
+        assert torch.isnan(t[3]).all() and torch.isfinite(t[:3]).all() and torch.isfinite(t[4:]).all()
+    assert torch.isnan(dgate[3]).all()
+    assert not dgate[6:8].any() and not dy[7].any() and dy[6].any()
