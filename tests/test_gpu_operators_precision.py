@@ -85,6 +85,32 @@ def test_lm_loss_gradients_in_the_two_norm_at_wide_rows(ops, n, v, c, scale):
         assert float((got.double() - ref).norm() / ref.norm()) <= 1.01 * most
 
 
+def test_lm_loss_gradient_of_few_positions_in_the_second_piece(ops):
+    """9,000,000 ids: more than the 8,388,608 of one piece of dz.  A target of
+    probability 1 - p = 1e-4 in either piece, and next to the border."""
+    n, v, c = 4, 9_000_000, 8
+    w = _rnd(261, v, c, std=0.1)
+    tt = torch.tensor([5, 8_388_607, 8_388_608, v - 1], dtype=torch.int32, device="cuda")
+    w[tt.long()] = torch.eye(8, device="cuda").bfloat16()[:4] * 8
+    h = torch.zeros(n, c, dtype=torch.bfloat16, device="cuda")
+    h[torch.arange(4), torch.arange(4)] = 3.25                       # score 26; ln(9e6) = 16
+    dl = torch.ones(n, device="cuda")
+    _, lse = ops.lm_loss(h, w, tt)
+    dh, dw = ops.lm_loss_bwd(h, w, tt, lse, dl)
+    logp = torch.log_softmax(h.double() @ w.double().T, 1)
+    at = torch.arange(n, device="cuda")
+    miss = -torch.expm1(logp[at, tt.long()])
+    assert 1e-5 < float(miss.min()) and float(miss.max()) < 1e-3
+    p = logp.exp()
+    p[at, tt.long()] = -miss
+    # the bound of the confident targets above; |w| of the targets is 8
+    tol = 8 * (4 * BF * miss + (lse.double().abs() + 24) * U)
+    assert ((dh.double() - p @ w.double()).norm(dim=1) <= tol).all()
+    # dw of a target: dz h, another rounding, and what the other positions add
+    ref = p[:, tt.long()].T @ h.double()
+    assert ((dw[tt.long()].double() - ref).norm(dim=1) <= 3.25 * (4 * BF * miss + (lse.double().abs() + 24) * U)).all()
+
+
 def _relative_mean(got, ref):
     return float(((got.double() - ref) / ref).mean())
 
