@@ -17,11 +17,13 @@
 // columns' sums over the rows it walks and writes them once, and a second
 // kernel adds the CTAs' in order (deterministic).
 // Measured on GB300: forward 96,888 x 2,048 283 us, 7.0 TB/s (the copy peak);
-// backward 32,768 x 4,096 340 us, 6.3 TB/s (0.93 of it), 79% of the DRAM
+// backward 32,768 x 4,096 351 us, 6.1 TB/s (0.90 of it), 77% of the DRAM
 // cycles.  What took the backward there from 614 us: rows copied ahead 417,
 // then the weights in shared memory instead of L1 340 (packed arithmetic
 // alone changed nothing, but its registers are fewer).  One 16-byte piece per
-// thread and 512 threads per row instead of two and 256: 449.
+// thread and 512 threads per row instead of two and 256: 449.  Keeping e^-gate
+// for an exact 1 - sigmoid costs 3%; the gate read a second time for it 5%, the
+// smaller of sigmoid and its complement kept with a sign 7%.
 #include <type_traits>
 
 #include "ptx.cuh"
@@ -54,7 +56,7 @@ __device__ __forceinline__ float sigmoid(float g) {
   return r;
 }
 // 8 channels as four packed fp32 pairs: the backward does some 50 operations
-// per channel, and pairs halve the instructions (measured below).
+// per channel, and a pair takes one instruction and fewer registers.
 struct Oct {
   uint64_t v[4];
 };

@@ -6,9 +6,10 @@
 //   dz[f, v] = dloss[f] * scale * (exp(z[f, v] - lse[f]) - (v == target[f]))
 //   dh[f] = sum_v dz[f, v] w[v],     dw[v] = sum_f dz[f, v] h[f]
 // A position whose target lies outside [0, V) has no loss: its loss, lse and
-// dh are zero, its row of h reaches nothing (not even as 0 * NaN) and costs
-// no products, because the positions that have a target are first gathered
-// into consecutive rows.
+// dh are zero and its row of h reaches nothing (not even as 0 * NaN).  The
+// positions that have a target are first gathered into consecutive rows, so
+// the others cost no products either; forwards too small for that to pay
+// (use_direct, use_few) compute them and drop them.
 //
 // Everything is one matrix product with four epilogues (kFwd, kDz, kDh, kDw):
 //   kFwd  h w^T: each row's running (maximum, sum of exponentials) over a run
@@ -36,8 +37,8 @@
 // width 4,096 came out 2.5e-5 low; a gradient summed over 200,000 terms of one
 // sign 1.2e-3).  So an accumulation stops after kChunkOf stages and the epilogue
 // adds the chunks up in registers with rounding to nearest: 512 elements for
-// the scores, 2,048 for dh and dw, whose results are rounded to bf16 (1.3e-5
-// there; with 512 the products took 2% longer).
+// the scores, 2,048 for dh and dw, whose results are rounded to bf16 (there
+// 1e-5 is left; with 512 the products took 1 to 2% longer).
 // Warps of a CTA: 0 TMA producer, 1 MMA issuer (of the pair's first CTA), 2
 // TMEM owner, 4-11 epilogue (two warpgroups, 128 columns each).  At widths
 // below about 1,000 the epilogue is what a tile waits for: its arithmetic is
@@ -47,9 +48,9 @@
 // time: dz of 9,441 rows, width 552, 61,282 ids 855 us against 579).  CTAs are
 // persistent and walk the tiles in panels of 8 columns of tiles, so the pairs
 // running together share rows of A and of B in L2.
-// What bounds it: the tensor pipe, busy 98% of the forward's cycles and 93-95%
-// of the others' (8,192 rows, width 2,048, 32,000 ids: forward 520 us, 2,065
-// TFLOP/s; dz 560, dh 574, dw 572 us); in long runs the power limit.
+// What bounds it: the tensor pipe, busy 98% of the forward's cycles and 90-94%
+// of the others' (8,192 rows, width 2,048, 32,000 ids: forward 516 us, 2,080
+// TFLOP/s; dz 564, dh 584, dw 572 us); in long runs the power limit.
 #include <type_traits>
 
 #include "pair.cuh"
@@ -103,8 +104,8 @@ struct LmParams {
 // Splits over K where the tiles alone do not fill the GPU: one round of units
 // for a few tiles; otherwise, below four rounds, the split into up to 8 that
 // makes the rounds shortest, where it saves a tenth or more (111 tiles in two
-// rounds of one against three rounds of a half: 600 -> 440 us at 9,441 rows,
-// width 552, 61,282 ids).  `most`: splits with 8 or more stages of K each.
+// rounds of one against three rounds of a half: 559 -> 471 us, the splits' sum
+// included, for dh of 9,441 rows, width 552, 61,282 ids).  `most`: splits with 8 or more stages of K each.
 constexpr int kSplitRounds = 4, kSplitMost = 8;
 __host__ __device__ inline int splits_for(int64_t tiles, int most) {
   if (tiles <= 0 || tiles > kSplitRounds * kSplitPairs || most <= 1) return 1;

@@ -850,7 +850,8 @@ def lm_loss(h, w, target, scale=1.0, loss=None, lse=None, workspace=None, dev_er
     h [N, C] bf16 (hidden rows), w [V, C] bf16 (output projection), target [N]
     int32; logits are ``scale * h @ w.T`` (scale = 1 / temperature).  Returns
     (loss, lse), fp32 [N]: loss = lse - logit[target], both zero where the
-    target is outside [0, V) (a position without a prediction)."""
+    target is outside [0, V) (a position without a prediction).  A device wait
+    that gives up is reported in ``dev_err`` (int32) alone."""
     lib = B.load()
     N, V, C, args = _loss_args(h, w, target, scale)
     given = loss, lse, workspace, dev_err
