@@ -201,11 +201,8 @@ def _run_own(s):
     if op == "linear":
         return ops.linear(s["x"], s["w"], bias=s["bias"], act=case["act"], residual=s["res"])
     if op == "linear_step":
-        if case["act"] == "none":
-            pre, y = None, ops.linear(s["x"], s["w"], bias=s["bias"], residual=s["res"])
-        else:
-            y, pre = ops.linear(s["x"], s["w"], bias=s["bias"], act=case["act"], residual=s["res"], save_pre=True)
-        dx, dw, db = ops.linear_bwd(s["x"], s["w"], s["dy"], act=case["act"], pre=pre, bias=case["bias"])
+        y = ops.linear(s["x"], s["w"], bias=s["bias"], act=case["act"], residual=s["res"])
+        dx, dw, db = ops.linear_bwd(s["x"], s["w"], s["dy"], bias=s["bias"], act=case["act"])
         return [t for t in (y, dx, dw, db) if t is not None]
     if op == "ffn":
         return ops.gated_ffn(s["x"], s["w_in"], s["w_out"], act=case["act"], residual=s["res"])
