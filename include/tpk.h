@@ -266,6 +266,35 @@ int tpk_rope_by_depth(const void* q_in, const void* k_in, void* q_out, void* k_o
                       const int32_t* depth, int64_t F, int32_t Hq, int32_t Hkv, int32_t d,
                       double base, int32_t inverse, void* stream);
 
+/* RoPE at depth positions in its other forms: pairs of either layout, in a part
+ * of the head, with any angle per position and pair (contexts stretched by
+ * scaled frequencies) and rows that lie apart (column slices of a fused
+ * projection).  Per position f, head and pair i < rot / 2:
+ *   (a, b) -> factor * (a cos t - b sin t, a sin t + b cos t),  t = depth[f] * freqs[i]
+ *   half layout (interleaved = 0): a, b = channels i and i + rot/2
+ *   interleaved (1):               a, b = channels 2i and 2i + 1
+ * Channels from rot on are copied.  inverse != 0: by -t, with the same factor:
+ * the transpose, which takes gradients with respect to the outputs to those with
+ * respect to the inputs.
+ *   q_in, q_out [F, Hq, d], k_in, k_out [F, Hkv, d] bf16, heads contiguous in a
+ *   row, row strides ld_* in elements (multiples of 8); out == in (same stride)
+ *   rotates in place; no other overlap; a NULL pair skips that tensor.
+ *   depth: device int32 [F], any value.  opts, with freqs [rot / 2], is host
+ *   memory and read before the call returns.
+ *   16 <= rot <= min(d, 256), rot % 16 == 0;  d % 8 == 0, d <= 512.
+ * fp32 arithmetic; the angle's place in its turn is exact to depth * 2^-53 turns.
+ * tpk_tree_attn_bwd_ex's rope_base undoes tpk_rope_by_depth's form alone: with
+ * this one take dq, dk of the rotated inputs and rotate them back here. */
+typedef struct {
+    int32_t rot;            /* channels of the head that are rotated */
+    int32_t interleaved;    /* 0 or 1 */
+    double factor;          /* on cos and sin (1: a rotation) */
+    const double* freqs;    /* radians per position of each pair */
+} tpk_rope_opts;
+int tpk_rope_by_depth_ex(const void* q_in, int64_t ld_q, const void* k_in, int64_t ld_k, void* q_out, int64_t ld_qo,
+                         void* k_out, int64_t ld_ko, const int32_t* depth, int64_t F, int32_t Hq, int32_t Hkv,
+                         int32_t d, const tpk_rope_opts* opts, int32_t inverse, void* stream);
+
 /* Options of the attention calls (tpk_tree_attn_fwd_ex, tpk_tree_attn_bwd_ex).
  * No counterpart on the pages: they choose the arithmetic, not the result.
  *   precision  TPK_PREC_FAST: the probabilities P (forward and backward) and
@@ -636,6 +665,107 @@ int tpk_lm_loss(const void* h, const void* w, const int32_t* target, float* loss
 int tpk_lm_loss_bwd(const void* h, const void* w, const int32_t* target, const float* lse, const float* dloss,
                     void* dh, void* dw, int64_t N, int64_t V, int32_t C, float scale, void* workspace,
                     size_t ws_bytes, int32_t* dev_err, void* stream);
+
+/* ---- projections and the feed-forward block --------------------------------
+ * No counterpart on the pages, as above: the matrix products of a layer around
+ * its token mixer.  bf16 rows and weights, fp32 sums and biases; each result is
+ * rounded once.  Rows of x, y, residual and the gradients may lie apart (row
+ * strides ld_*, in elements: multiples of 8, not below the width; column slices
+ * of a fused projection), weights are contiguous.  Widths are multiples of 8,
+ * pointers 16-byte aligned.  Sums run in a fixed order: results do not depend on
+ * timing.  Workspaces need not be cleared, are 256-byte aligned, and belong to
+ * one call (or captured graph) at a time.
+ * Errors: TPK_E_ARG for a bad pointer, size, stride or activation,
+ * TPK_E_UNSUPPORTED for a width of a sum above 32,768, TPK_E_OVERFLOW for more
+ * than 2^27 tiles of 256 x 256, TPK_E_WORKSPACE; dev_err (device int32, may be
+ * NULL) becomes TPK_E_TIMEOUT if a device wait gave up. */
+#define TPK_ACT_NONE      0
+#define TPK_ACT_SILU      1  /* z / (1 + exp(-z)) */
+#define TPK_ACT_GELU      2  /* z Phi(z), Phi within 1.5e-7 */
+#define TPK_ACT_GELU_TANH 3  /* 0.5 z (1 + tanh(sqrt(2/pi) (z + 0.044715 z^3))) */
+
+/* Matrix product with bias, activation and residual:
+ *   y[n, o] = act( sum_c x[n, c] w[o, c] + bias[o] ) + residual[n, o]
+ *   x [N, C], w [O, C], residual, y [N, O] bf16;  bias [O] fp32
+ * bias and residual may be NULL; y may be residual itself (same stride), else
+ * outputs overlap no input.  C <= 32,768, O <= 2^20.  N = 0 does nothing.
+ * workspace: tpk_linear_workspace_bytes(N, C, O, act, 0) bytes, may be 0. */
+size_t tpk_linear_workspace_bytes(int64_t N, int32_t C, int32_t O, int32_t act, int32_t backward);
+int tpk_linear(const void* x, int64_t ld_x, const void* w, const float* bias, int32_t act, const void* residual,
+               int64_t ld_res, void* y, int64_t ld_y, int64_t N, int32_t C, int32_t O, void* workspace,
+               size_t ws_bytes, int32_t* dev_err, void* stream);
+
+/* Gradients of tpk_linear for the gradient dy of y (the residual's is dy):
+ *   z = x w^T + bias, formed again where there is an activation
+ *   dz = dy act'(z) (as bf16 in its products),  dx = dz w,  dw = dz^T x,
+ *   db[o] = sum_n dz[n, o] (fp32, of the unrounded dz)
+ *   dy [N, O], dx [N, C], dw [O, C] bf16, db [O] fp32 or NULL; every row of dw
+ *   and db is written (zeros for N = 0).  x, w, bias, act as in the forward.
+ *   workspace: tpk_linear_workspace_bytes(N, C, O, act, 1) bytes (dz, its sums,
+ *   partial tiles). */
+int tpk_linear_bwd(const void* x, int64_t ld_x, const void* w, const float* bias, int32_t act, const void* dy,
+                   int64_t ld_dy, void* dx, int64_t ld_dx, void* dw, float* db, int64_t N, int32_t C, int32_t O,
+                   void* workspace, size_t ws_bytes, int32_t* dev_err, void* stream);
+
+/* Gated feed-forward block:
+ *   g = x w_in[0:I]^T,  u = x w_in[I:2I]^T,  a = act(g) * u,  y = a w_out^T + residual
+ *   x [N, C], w_in [2 I, C], w_out [O, I], residual, y [N, O] bf16
+ *   pre [N, 2 I] (g | u) and a [N, I] bf16, contiguous: kept for the backward;
+ *   pre NULL: not written; a NULL: in the workspace.
+ * residual may be NULL; y may be residual itself.  C, I, O <= 32,768.
+ *   workspace: tpk_gated_ffn_workspace_bytes(N, C, I, O, 0) bytes (less is
+ *   needed where a is given). */
+size_t tpk_gated_ffn_workspace_bytes(int64_t N, int32_t C, int32_t I, int32_t O, int32_t backward);
+int tpk_gated_ffn(const void* x, int64_t ld_x, const void* w_in, const void* w_out, int32_t act, const void* residual,
+                  int64_t ld_res, void* pre, void* a, void* y, int64_t ld_y, int64_t N, int32_t C, int32_t I,
+                  int32_t O, void* workspace, size_t ws_bytes, int32_t* dev_err, void* stream);
+
+/* Gradients of tpk_gated_ffn for the gradient dy of y (the residual's is dy):
+ *   da = dy w_out,  dg = da u act'(g),  du = da act(g)
+ *   dx = dg w_in[0:I] + du w_in[I:2I],  dw_in = (dg | du)^T x,  dw_out = dy^T a
+ *   pre and a: the forward's, read only.  dx [N, C], dw_in [2 I, C], dw_out
+ *   [O, I] bf16, every row of the weights' gradients written (zeros for N = 0).
+ *   workspace: tpk_gated_ffn_workspace_bytes(N, C, I, O, 1) bytes (dg | du,
+ *   partial tiles). */
+int tpk_gated_ffn_bwd(const void* x, int64_t ld_x, const void* w_in, const void* w_out, int32_t act, const void* dy,
+                      int64_t ld_dy, const void* pre, const void* a, void* dx, int64_t ld_dx, void* dw_in,
+                      void* dw_out, int64_t N, int32_t C, int32_t I, int32_t O, void* workspace, size_t ws_bytes,
+                      int32_t* dev_err, void* stream);
+
+/* Clipped policy objective with a KL term over a packed batch, and its gradient
+ * with respect to tpk_lm_loss's loss: what stands between a batch's
+ * log-probabilities and the dloss of tpk_lm_loss_bwd.  Per raw token r with
+ * weight[r] != 0, at position f = token_index[r]:
+ *   logp = -loss[f],  d = logp - old_logp[r]
+ *   ratio = exp(d); with seq_offsets: exp(mean of d over the sequence's tokens
+ *           of nonzero weight)
+ *   s = min(ratio A, clamp(ratio, 1 - clip_low, 1 + clip_high) A),  A = advantage[r]
+ *   dual_clip c > 1 (0: off): s = max(s, c A) where A < 0
+ *   kl = exp(t) - t - 1,  t = ref_logp[r] - logp     (ref_logp NULL: 0)
+ *   objective = sum_r weight[r] (kl_coef kl - s)
+ *   dloss[f]  = d objective / d loss[f], summed over the raw tokens of f
+ * A token whose s is held by a border passes no gradient of its ratio.  Of a
+ * token of weight 0 nothing else is read.  Shared positions take the shares of
+ * all their raw tokens.
+ *   loss, dloss [F] fp32;  old_logp, ref_logp, advantage, weight [R] fp32
+ *   token_index, fwd_raw_begin, fwd_raw: the plan image's (TPK_FIELD_*)
+ *   seq_offsets: device int32 [n_seqs + 1], ascending, 0 first and R last, or
+ *   NULL with n_seqs = 0.
+ *   stats [5] fp32: the objective; sums of weight times kl, times 1 where s is
+ *   held by a border, times ratio; the sum of weights (fp64 sums, fixed order).
+ *   workspace: tpk_policy_loss_workspace_bytes bytes, 256-byte aligned, need not
+ *   be cleared (a share per raw token, partial sums); one call at a time.
+ * R = 0 writes zero stats.  Errors: TPK_E_ARG, TPK_E_WORKSPACE. */
+typedef struct {
+    double clip_low, clip_high;   /* 0 <= clip_low <= 1, clip_high >= 0 */
+    double dual_clip;             /* 0, or > 1 */
+    double kl_coef;               /* >= 0 */
+} tpk_policy_opts;
+size_t tpk_policy_loss_workspace_bytes(int64_t R, int32_t n_seqs);
+int tpk_policy_loss(const float* loss, const float* old_logp, const float* ref_logp, const float* advantage,
+                    const float* weight, const int32_t* token_index, const int32_t* fwd_raw_begin,
+                    const int32_t* fwd_raw, const int32_t* seq_offsets, int32_t n_seqs, const tpk_policy_opts* opts,
+                    float* stats, float* dloss, int64_t R, int64_t F, void* workspace, size_t ws_bytes, void* stream);
 
 /* Self-test of the device-side failure path (no counterpart on the pages):
  * launches one small kernel that waits, with the same bounded mbarrier wait

@@ -21,6 +21,7 @@ PLACE_BFD = 0
 PLACE_NEXT_FIT = 1
 PLACE_GROUPS = 2
 BF16, F32 = 0, 1
+ACT_NONE, ACT_SILU, ACT_GELU, ACT_GELU_TANH = 0, 1, 2, 3
 FIELD_DEPTH, FIELD_TOKEN_INDEX, FIELD_SUBTREE_END, FIELD_PARENT = 0, 1, 2, 3
 FIELD_FWD_RAW_BEGIN, FIELD_FWD_RAW = 4, 5
 FIELD_SEG_START, FIELD_SEG_LEN, FIELD_SEG_PARENT, FIELD_SEG_OFF = 6, 7, 8, 9
@@ -38,6 +39,9 @@ EXPORTS = [
     "tpk_embed", "tpk_embed_bwd_workspace_bytes", "tpk_embed_bwd",
     "tpk_block_norm", "tpk_block_norm_bwd_workspace_bytes", "tpk_block_norm_bwd",
     "tpk_lm_loss_workspace_bytes", "tpk_lm_loss", "tpk_lm_loss_bwd",
+    "tpk_rope_by_depth_ex", "tpk_linear_workspace_bytes", "tpk_linear", "tpk_linear_bwd",
+    "tpk_gated_ffn_workspace_bytes", "tpk_gated_ffn", "tpk_gated_ffn_bwd",
+    "tpk_policy_loss_workspace_bytes", "tpk_policy_loss",
     "tpk_status_string",
     "tpk_version",
 ]
@@ -57,6 +61,18 @@ class AttnOpts(ctypes.Structure):
     """tpk_attn_opts: precision, inverse RoPE base (backward), O's rounding residual."""
     _fields_ = [("precision", ctypes.c_int32), ("reserved", ctypes.c_int32), ("rope_base", ctypes.c_double),
                 ("o_lo", ctypes.c_void_p)]
+
+
+class RopeOpts(ctypes.Structure):
+    """tpk_rope_opts: rotated channels, pairing, factor, host array of radians per position."""
+    _fields_ = [("rot", ctypes.c_int32), ("interleaved", ctypes.c_int32), ("factor", ctypes.c_double),
+                ("freqs", ctypes.c_void_p)]
+
+
+class PolicyOpts(ctypes.Structure):
+    """tpk_policy_opts: the clip's borders and the KL term's coefficient."""
+    _fields_ = [("clip_low", ctypes.c_double), ("clip_high", ctypes.c_double), ("dual_clip", ctypes.c_double),
+                ("kl_coef", ctypes.c_double)]
 
 
 class PlanInfo(ctypes.Structure):
@@ -130,6 +146,19 @@ def _sig(lib):
     lib.tpk_lm_loss_workspace_bytes.restype = SZ
     lib.tpk_lm_loss.argtypes = [P, P, P, P, P, I64, I64, I32, F, P, SZ, P, P]
     lib.tpk_lm_loss_bwd.argtypes = [P, P, P, P, P, P, P, I64, I64, I32, F, P, SZ, P, P]
+    lib.tpk_rope_by_depth_ex.argtypes = [P, I64, P, I64, P, I64, P, I64, P, I64, I32, I32, I32,
+                                         ctypes.POINTER(RopeOpts), I32, P]
+    lib.tpk_linear_workspace_bytes.argtypes = [I64, I32, I32, I32, I32]
+    lib.tpk_linear_workspace_bytes.restype = SZ
+    lib.tpk_linear.argtypes = [P, I64, P, P, I32, P, I64, P, I64, I64, I32, I32, P, SZ, P, P]
+    lib.tpk_linear_bwd.argtypes = [P, I64, P, P, I32, P, I64, P, I64, P, P, I64, I32, I32, P, SZ, P, P]
+    lib.tpk_gated_ffn_workspace_bytes.argtypes = [I64, I32, I32, I32, I32]
+    lib.tpk_gated_ffn_workspace_bytes.restype = SZ
+    lib.tpk_gated_ffn.argtypes = [P, I64, P, P, I32, P, I64, P, P, P, I64, I64, I32, I32, I32, P, SZ, P, P]
+    lib.tpk_gated_ffn_bwd.argtypes = [P, I64, P, P, I32, P, I64, P, P, P, I64, P, P, I64, I32, I32, I32, P, SZ, P, P]
+    lib.tpk_policy_loss_workspace_bytes.argtypes = [I64, I32]
+    lib.tpk_policy_loss_workspace_bytes.restype = SZ
+    lib.tpk_policy_loss.argtypes = [P] * 9 + [I32, ctypes.POINTER(PolicyOpts), P, P, I64, I64, P, SZ, P]
     lib.tpk_status_string.argtypes = [ctypes.c_int]
     lib.tpk_status_string.restype = ctypes.c_char_p
     lib.tpk_version.argtypes = []

@@ -1,0 +1,275 @@
+// A few rows times a weight matrix: one read of the weights is all the time
+// there is.  The operands change places: 128 rows of the weights are the MMA's
+// M, the tokens (16, 32 or 64, padded by the TMA with zeros) its N.  A tile's K
+// is shared out over a cluster of up to 8 CTAs, so that a few dozen tiles keep
+// every SM loading; each CTA streams its share through a ring of TMA stages,
+// and the partial sums meet through distributed shared memory, added in the
+// order of the ranks.  For the gated form a tile holds 64 rows of the gate's
+// weights and the 64 of the up projection's for the same channels.
+#include "few.cuh"
+
+namespace tpk {
+namespace product {
+namespace {
+
+constexpr int kFewThreads = 128;
+constexpr int kFewCluster = 8;
+
+template <int kTok>
+struct FewSmem {
+  static constexpr int kStages = kTok == 16 ? 6 : kTok == 32 ? 5 : 4;   // two CTAs per SM
+  uint8_t a[kStages][kBoxBytes];
+  uint8_t b[kStages][kTok * 128];
+  uint64_t full[kStages], empty[kStages];
+  uint64_t done;
+  uint32_t tmem_base;
+  int abort_flag;
+};
+template <int kTok>
+constexpr size_t kFewBytes = sizeof(FewSmem<kTok>) + 1024;
+
+struct FewParams {
+  int32_t N, O, k_iters;     // tokens, results per token (of one of the two, gated), stages of K
+  int32_t act;
+  const float* bias;
+  const __nv_bfloat16* residual;
+  int64_t ld_res;
+  __nv_bfloat16* y;
+  int64_t ld_y;
+  __nv_bfloat16* pre;        // gated: nullptr, or [N, 2 O]
+  int32_t* err;
+};
+
+struct FewMaps {
+  CUtensorMap w, w2, x;
+};
+
+template <int kTok, bool kGated>
+__global__ void __launch_bounds__(kFewThreads) few_kernel(const __grid_constant__ FewMaps maps, const FewParams p) {
+  extern __shared__ uint8_t smem_raw[];
+  using Sm = FewSmem<kTok>;
+  constexpr int kS = Sm::kStages;
+  Sm& S = *reinterpret_cast<Sm*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  float* red = reinterpret_cast<float*>(S.a[0]);   // [kTok][128], once the stages have been read
+  static_assert(kTok * 512 <= kS * kBoxBytes, "partial sums");
+  constexpr int kCols = kTok < 32 ? 32 : kTok;     // TMEM columns
+  const int warp = threadIdx.x >> 5;
+  uint32_t rank, ranks;
+  asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(rank));
+  asm volatile("mov.u32 %0, %%cluster_nctarank;" : "=r"(ranks));
+  const int tile = blockIdx.x / ranks;
+  const int k0 = static_cast<int>(static_cast<int64_t>(p.k_iters) * rank / ranks);
+  const int nk = static_cast<int>(static_cast<int64_t>(p.k_iters) * (rank + 1) / ranks) - k0;
+  volatile int* abort_flag = &S.abort_flag;
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < kS; ++s) {
+      ptx::mbar_init(&S.full[s], 1);
+      ptx::mbar_init(&S.empty[s], 1);
+    }
+    ptx::mbar_init(&S.done, 1);
+    S.abort_flag = 0;
+    ptx::fence_mbar_init();
+  }
+  if (warp == 2) {
+    ptx::tmem_alloc(&S.tmem_base, kCols);
+    ptx::tmem_relinquish();
+  }
+  ptx::tc_fence_before();
+  __syncthreads();
+  ptx::tc_fence_after();
+  const uint32_t tmem = S.tmem_base;
+  if (kGated) ptx::dependents_launch();
+  if (warp == 0) {
+    if (ptx::elect_one()) {
+      auto weights = [&](int st, int k) {
+        ptx::mbar_arrive_expect_tx(&S.full[st], kBoxBytes + kTok * 128);
+        if (kGated) {
+          ptx::tma_load_2d(S.a[st], &maps.w, &S.full[st], (k0 + k) * 64, tile * 64);
+          ptx::tma_load_2d(S.a[st] + kBoxBytes / 2, &maps.w2, &S.full[st], (k0 + k) * 64, tile * 64);
+        } else {
+          ptx::tma_load_2d(S.a[st], &maps.w, &S.full[st], (k0 + k) * 64, tile * 128);
+        }
+      };
+      // the weights wait for no earlier kernel
+      const int first = nk < kS ? nk : kS;
+      for (int k = 0; k < first; ++k) weights(k, k);
+      ptx::dependency_wait();
+      for (int k = 0; k < first; ++k) ptx::tma_load_2d(S.b[k], &maps.x, &S.full[k], (k0 + k) * 64, 0);
+      int issued = first;
+      for (int k = kS; k < nk; ++k, ++issued) {
+        const int st = k % kS;
+        if (!ptx::mbar_wait(&S.empty[st], (k / kS - 1) & 1, abort_flag, kWaitLimitNs)) break;
+        weights(st, k);
+        ptx::tma_load_2d(S.b[st], &maps.x, &S.full[st], (k0 + k) * 64, 0);
+      }
+      // nothing is left in flight, whatever became of the products
+      for (int k = issued > kS ? issued - kS : 0; k < issued; ++k) ptx::mbar_drain(&S.full[k % kS], (k / kS) & 1);
+    }
+  } else if (warp == 1) {
+    if (ptx::elect_one()) {
+      constexpr uint32_t idesc = ptx::idesc_bf16_f32(128, kTok, false, false);
+      for (int k = 0; k < nk; ++k) {
+        const int st = k % kS;
+        if (!ptx::mbar_wait(&S.full[st], (k / kS) & 1, abort_flag, kWaitLimitNs)) break;
+        ptx::tc_fence_after();
+        const uint64_t ad = ptx::sw128_desc(ptx::smem_addr(S.a[st]), 16, 1024);
+        const uint64_t bd = ptx::sw128_desc(ptx::smem_addr(S.b[st]), 16, 1024);
+#pragma unroll
+        for (int q = 0; q < 4; ++q)
+          ptx::mma_ss(tmem, ptx::desc_add(ad, q * 32), ptx::desc_add(bd, q * 32), idesc, (k > 0 || q > 0) ? 1u : 0u);
+        ptx::mma_commit(&S.empty[st]);
+      }
+      ptx::mma_commit(&S.done);
+    }
+  }
+  __syncwarp();
+  ptx::dependency_wait();
+  const bool ok = ptx::mbar_drain(&S.done, 0);   // every product issued has been done
+  ptx::tc_fence_after();
+  // every thread's row of the accumulator (a result's channel) to shared memory, channels side by side
+  __syncthreads();   // the producer's last loads have landed: the stages are free
+  if (ok) {
+#pragma unroll
+    for (int c = 0; c < kTok; c += 16) {
+      uint32_t r[16];
+      ptx::tmem_ld16(tmem + (static_cast<uint32_t>(warp * 32) << 16) + c, r);
+      ptx::tmem_wait_ld();
+#pragma unroll
+      for (int e = 0; e < 16; ++e) red[(c + e) * 128 + threadIdx.x] = __uint_as_float(r[e]);
+    }
+  }
+  ptx::tc_fence_before();
+  __syncthreads();
+  ptx::cluster_sync();   // every CTA's partial sums are there
+  if (warp == 2) {
+    ptx::tc_fence_after();
+    ptx::tmem_dealloc(tmem, kCols);
+  }
+  if ((!ok || S.abort_flag) && threadIdx.x == 0 && p.err) *p.err = TPK_E_TIMEOUT;
+
+  // this CTA's share of the channels, four at a time
+  constexpr int kWide = kGated ? 64 : 128;
+  const int quads = kWide / 4 / static_cast<int>(ranks);
+  for (int i = threadIdx.x; i < p.N * quads; i += kFewThreads) {
+    const int t = i / quads, at = (static_cast<int>(rank) * quads + i % quads) * 4;
+    const int o = tile * kWide + at;
+    if (o >= p.O) continue;
+    float4 v = make_float4(0.f, 0.f, 0.f, 0.f), u = v;
+    for (uint32_t k = 0; k < ranks; ++k) {
+      const float4 d = ptx::lds128_cluster(red + t * 128 + at, k);
+      v.x += d.x; v.y += d.y; v.z += d.z; v.w += d.w;
+      if (kGated) {
+        const float4 e = ptx::lds128_cluster(red + t * 128 + 64 + at, k);
+        u.x += e.x; u.y += e.y; u.z += e.z; u.w += e.w;
+      }
+    }
+    if (kGated) {
+      if (p.pre) {
+        __nv_bfloat16* g = p.pre + static_cast<int64_t>(t) * 2 * p.O + o;
+        *reinterpret_cast<uint2*>(g) = make_uint2(pack2(v.x, v.y), pack2(v.z, v.w));
+        *reinterpret_cast<uint2*>(g + p.O) = make_uint2(pack2(u.x, u.y), pack2(u.z, u.w));
+      }
+    } else if (p.bias) {
+      const float4 b = __ldg(reinterpret_cast<const float4*>(p.bias + o));
+      v.x += b.x; v.y += b.y; v.z += b.z; v.w += b.w;
+    }
+    with_act(p.act, [&](auto k) {
+      constexpr int kAct = decltype(k)::value;
+      v = make_float4(act_of<kAct>(v.x), act_of<kAct>(v.y), act_of<kAct>(v.z), act_of<kAct>(v.w));
+    });
+    if (kGated) {
+      v.x *= u.x; v.y *= u.y; v.z *= u.z; v.w *= u.w;
+    } else if (p.residual) {
+      const uint2 q = *reinterpret_cast<const uint2*>(p.residual + t * p.ld_res + o);
+      v.x += lo16(q.x); v.y += hi16(q.x); v.z += lo16(q.y); v.w += hi16(q.y);
+    }
+    *reinterpret_cast<uint2*>(p.y + t * p.ld_y + o) = make_uint2(pack2(v.x, v.y), pack2(v.z, v.w));
+  }
+  ptx::cluster_sync();   // nobody reads a CTA that has gone
+}
+
+// CTAs that share a tile's K: as many as keep two CTAs per SM busy, each with
+// two stages or more.
+int few_ranks(int64_t tiles, int k_iters) {
+  int s = kFewCluster;
+  while (s > 1 && (tiles * s > 2 * num_sms() || k_iters < 2 * s)) s /= 2;
+  return s;
+}
+
+template <int kTok, bool kGated>
+int few_launch(const FewMaps& m, const FewParams& p, bool after, cudaStream_t s) {
+  constexpr auto kern = few_kernel<kTok, kGated>;
+  static PerContext<int> rec;
+  const int st = guarded([&] { return set_smem_once(rec, kern, kFewBytes<kTok>); });
+  if (st != TPK_OK) return st;
+  const int64_t tiles = (p.O + (kGated ? 63 : 127)) / (kGated ? 64 : 128);
+  const int ranks = few_ranks(tiles, p.k_iters);
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(static_cast<unsigned>(tiles * ranks));
+  cfg.blockDim = dim3(kFewThreads);
+  cfg.dynamicSmemBytes = kFewBytes<kTok>;
+  cfg.stream = s;
+  cudaLaunchAttribute at[2];
+  at[0].id = cudaLaunchAttributeClusterDimension;
+  at[0].val.clusterDim.x = static_cast<unsigned>(ranks);
+  at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
+  at[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[1].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = after ? 2 : 1;
+  return cuda_status(cudaLaunchKernelEx(&cfg, kern, m, p));
+}
+
+template <bool kGated>
+int few_dispatch(const Mat& x, FewMaps& m, const FewParams& p, bool after, cudaStream_t s) {
+  const int tok = p.N <= 16 ? 16 : p.N <= 32 ? 32 : 64;
+  const int st = map_of(&m.x, x, tok);
+  if (st != TPK_OK) return st;
+  return tok == 16   ? few_launch<16, kGated>(m, p, after, s)
+         : tok == 32 ? few_launch<32, kGated>(m, p, after, s)
+                     : few_launch<64, kGated>(m, p, after, s);
+}
+
+}  // namespace
+
+int few_linear(const Mat& x, const Mat& w, const float* bias, int act, const Mat& residual, const Mat& y, bool after,
+               int32_t* err, cudaStream_t s) {
+  FewMaps m;
+  int st = map_of(&m.w, w, 128);
+  if (st != TPK_OK) return st;
+  m.w2 = m.w;
+  FewParams p{};
+  p.N = static_cast<int32_t>(x.rows);
+  p.O = static_cast<int32_t>(w.rows);
+  p.k_iters = static_cast<int32_t>((w.cols + 63) / 64);
+  p.act = act;
+  p.bias = bias;
+  p.residual = static_cast<const __nv_bfloat16*>(residual.p);
+  p.ld_res = residual.ld;
+  p.y = static_cast<__nv_bfloat16*>(const_cast<void*>(y.p));
+  p.ld_y = y.ld;
+  p.err = err;
+  return few_dispatch<false>(x, m, p, after, s);
+}
+
+int few_gate(const Mat& x, const Mat& w_gate, const Mat& w_up, int act, const Mat& a, __nv_bfloat16* pre, int32_t* err,
+             cudaStream_t s) {
+  FewMaps m;
+  int st = map_of(&m.w, w_gate, 64);
+  if (st == TPK_OK) st = map_of(&m.w2, w_up, 64);
+  if (st != TPK_OK) return st;
+  FewParams p{};
+  p.N = static_cast<int32_t>(x.rows);
+  p.O = static_cast<int32_t>(w_gate.rows);
+  p.k_iters = static_cast<int32_t>((w_gate.cols + 63) / 64);
+  p.act = act;
+  p.y = static_cast<__nv_bfloat16*>(const_cast<void*>(a.p));
+  p.ld_y = a.ld;
+  p.pre = pre;
+  p.err = err;
+  return few_dispatch<true>(x, m, p, false, s);
+}
+
+}  // namespace product
+}  // namespace tpk

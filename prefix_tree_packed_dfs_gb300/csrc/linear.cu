@@ -1,0 +1,311 @@
+// Projections: y = act(x w^T + bias) + residual, and the gradients
+//   dz = dy act'(z), z = x w^T + bias,   dx = dz w,   dw = dz^T x,   db = sum of dz's rows.
+// The products and their epilogues are product.cuh's; few rows go to few.cu.
+// With an activation the backward forms z again: one more product, and nothing
+// the width of z is kept from the forward (z kept in bf16 would put its rounding
+// into db, an fp32 sum).  dz is rounded to bf16 for its two products, as every
+// operand of the tensor cores is; db sums it before that rounding.
+#include "few.cuh"
+
+namespace tpk {
+namespace product {
+namespace {
+
+constexpr int kSumThreads = 256;   // 32 lanes of 8 columns x 8 rows at a time
+constexpr int kSumCols = 256;
+constexpr int kSumMost = 64;       // partial rows left for the last pass
+
+template <typename T>
+struct Eight;
+template <>
+struct Eight<__nv_bfloat16> {
+  static __device__ __forceinline__ void add(const __nv_bfloat16* p, float (&v)[8]) {
+    const uint4 q = __ldg(reinterpret_cast<const uint4*>(p));
+    v[0] += lo16(q.x); v[1] += hi16(q.x); v[2] += lo16(q.y); v[3] += hi16(q.y);
+    v[4] += lo16(q.z); v[5] += hi16(q.z); v[6] += lo16(q.w); v[7] += hi16(q.w);
+  }
+};
+template <>
+struct Eight<float> {
+  static __device__ __forceinline__ void add(const float* p, float (&v)[8]) {
+    const float4 a = __ldg(reinterpret_cast<const float4*>(p)), b = __ldg(reinterpret_cast<const float4*>(p) + 1);
+    v[0] += a.x; v[1] += a.y; v[2] += a.z; v[3] += a.w;
+    v[4] += b.x; v[5] += b.y; v[6] += b.z; v[7] += b.w;
+  }
+};
+
+// out[b][c] = sum of the rows b * per .. of m: a CTA takes 256 columns of `per` rows.
+template <typename T>
+__global__ void __launch_bounds__(kSumThreads) column_sum_kernel(const T* __restrict__ m, int64_t rows, int cols,
+                                                                 int64_t ld, int64_t per, float* __restrict__ out) {
+  __shared__ float4 part[8][32][2];
+  const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
+  const int c = blockIdx.x * kSumCols + lane * 8;
+  const int64_t lo = static_cast<int64_t>(blockIdx.y) * per, hi = lo + per < rows ? lo + per : rows;
+  float v[8] = {};
+  if (c < cols) {
+#pragma unroll 8
+    for (int64_t r = lo + w; r < hi; r += 8) Eight<T>::add(m + r * ld + c, v);
+  }
+  part[w][lane][0] = make_float4(v[0], v[1], v[2], v[3]);
+  part[w][lane][1] = make_float4(v[4], v[5], v[6], v[7]);
+  __syncthreads();
+  if (w >= 2 || c >= cols) return;
+  float4 s = part[0][lane][w];
+#pragma unroll
+  for (int i = 1; i < 8; ++i) {
+    const float4 x = part[i][lane][w];
+    s.x += x.x; s.y += x.y; s.z += x.z; s.w += x.w;
+  }
+  *reinterpret_cast<float4*>(out + static_cast<int64_t>(blockIdx.y) * cols + c + w * 4) = s;
+}
+
+// Row blocks of the first pass: enough CTAs for two per SM, 32 rows each or more.
+int64_t sum_rows(int64_t rows, int64_t cols) {
+  const int64_t across = (cols + kSumCols - 1) / kSumCols;
+  int64_t blocks = (2 * kMaxSms + across - 1) / across;
+  blocks = blocks < 1 ? 1 : blocks > kSumMost ? kSumMost : blocks;
+  const int64_t per = (rows + blocks - 1) / blocks;
+  return per < 32 ? 32 : per;
+}
+int64_t sum_blocks(int64_t rows, int64_t cols) {
+  const int64_t per = sum_rows(rows, cols);
+  return (rows + per - 1) / per;
+}
+
+template <typename T>
+int column_sums(const T* m, int64_t rows, int64_t cols, int64_t ld, float* part, float* out, cudaStream_t s) {
+  const unsigned across = static_cast<unsigned>((cols + kSumCols - 1) / kSumCols);
+  const int64_t per = sum_rows(rows, cols), blocks = sum_blocks(rows, cols);
+  float* to = blocks == 1 ? out : part;
+  column_sum_kernel<T><<<dim3(across, static_cast<unsigned>(blocks)), kSumThreads, 0, s>>>(
+      m, rows, static_cast<int>(cols), ld, per, to);
+  if (blocks > 1)
+    column_sum_kernel<float><<<dim3(across, 1), kSumThreads, 0, s>>>(part, blocks, static_cast<int>(cols), cols, blocks,
+                                                                     out);
+  return cuda_status(cudaGetLastError());
+}
+
+// The sum of a split product's partial tiles, 8 columns per thread, and kLin's
+// epilogue.
+__global__ void __launch_bounds__(256) join_kernel(const float* __restrict__ acc, int M, int N, int splits,
+                                                   const float* __restrict__ bias, int act,
+                                                   const __nv_bfloat16* residual, int64_t ld_res,
+                                                   __nv_bfloat16* out, int64_t ld_out) {
+  const int nt = (N + kTile - 1) / kTile;
+  const int64_t step = static_cast<int64_t>((M + kTile - 1) / kTile) * nt * (kTile * kTile);
+  const int vecs = N / 8;
+  const int64_t items = static_cast<int64_t>(M) * vecs;
+  for (int64_t it = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x; it < items;
+       it += static_cast<int64_t>(gridDim.x) * 256) {
+    const int64_t r = it / vecs;
+    const int col = static_cast<int>(it - r * vecs) * 8;
+    const float* from = acc + ((r / kTile) * nt + col / kTile) * (kTile * kTile) + (r % kTile) * kTile + col % kTile;
+    float v[8] = {};
+#pragma unroll 4
+    for (int s = 0; s < splits; ++s) {
+      const float4 x = __ldcg(reinterpret_cast<const float4*>(from + s * step));
+      const float4 y = __ldcg(reinterpret_cast<const float4*>(from + s * step) + 1);
+      v[0] += x.x; v[1] += x.y; v[2] += x.z; v[3] += x.w;
+      v[4] += y.x; v[5] += y.y; v[6] += y.z; v[7] += y.w;
+    }
+    if (bias) {
+      const float4 x = __ldg(reinterpret_cast<const float4*>(bias + col));
+      const float4 y = __ldg(reinterpret_cast<const float4*>(bias + col) + 1);
+      v[0] += x.x; v[1] += x.y; v[2] += x.z; v[3] += x.w;
+      v[4] += y.x; v[5] += y.y; v[6] += y.z; v[7] += y.w;
+    }
+    if (act != TPK_ACT_NONE)
+      with_act(act, [&](auto t) {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) v[e] = act_of<decltype(t)::value>(v[e]);
+      });
+    if (residual) {
+      const uint4 q = *reinterpret_cast<const uint4*>(residual + r * ld_res + col);
+      v[0] += lo16(q.x); v[1] += hi16(q.x); v[2] += lo16(q.y); v[3] += hi16(q.y);
+      v[4] += lo16(q.z); v[5] += hi16(q.z); v[6] += lo16(q.w); v[7] += hi16(q.w);
+    }
+    *reinterpret_cast<uint4*>(out + r * ld_out + col) =
+        make_uint4(pack2(v[0], v[1]), pack2(v[2], v[3]), pack2(v[4], v[5]), pack2(v[6], v[7]));
+  }
+}
+
+int join(const float* acc, int64_t M, int64_t N, int splits, const float* bias, int act, const Mat& residual,
+         const Mat& out, cudaStream_t s) {
+  const int64_t blocks = (M * (N / 8) + 255) / 256, most = int64_t{num_sms()} * 16;
+  join_kernel<<<static_cast<unsigned>(blocks < most ? blocks : most), 256, 0, s>>>(
+      acc, static_cast<int>(M), static_cast<int>(N), splits, bias, act,
+      static_cast<const __nv_bfloat16*>(residual.p), residual.ld, static_cast<__nv_bfloat16*>(const_cast<void*>(out.p)),
+      out.ld);
+  return cuda_status(cudaGetLastError());
+}
+
+Params params(int64_t M, int64_t N, int64_t K, bool split, float* acc, int32_t* err) {
+  Params p{};
+  p.M = static_cast<int32_t>(M);
+  p.N = static_cast<int32_t>(N);
+  p.K = static_cast<int32_t>(K);
+  p.splits = split ? splits_for(tiles_of(M, N), (K + 63) / 64) : 1;
+  p.acc = acc;
+  p.err = err;
+  return p;
+}
+
+struct LinearWork {
+  __nv_bfloat16* dz = nullptr;
+  float *sums = nullptr, *part = nullptr, *acc = nullptr;
+};
+size_t carve(uint8_t* base, int64_t N, int64_t C, int64_t O, int32_t act, bool backward, LinearWork* w) {
+  LinearWork o;
+  size_t at = 0;
+  auto take = [&](size_t bytes) {
+    uint8_t* p = base + at;
+    at += (bytes + 1023) / 1024 * 1024;
+    return p;
+  };
+  if (!backward) {
+    if (N > kFewRows) o.acc = reinterpret_cast<float*>(take(acc_bytes(N, O, C)));
+  } else {
+    if (act != TPK_ACT_NONE) {
+      o.dz = reinterpret_cast<__nv_bfloat16*>(take(static_cast<size_t>(N) * O * 2));
+      o.sums = reinterpret_cast<float*>(take(static_cast<size_t>((N + 31) / 32) * O * 4));
+    }
+    o.part = reinterpret_cast<float*>(take(static_cast<size_t>(kSumMost) * O * 4));
+    const size_t x = acc_bytes(N, C, O), y = acc_bytes(O, C, N);
+    o.acc = reinterpret_cast<float*>(take(x > y ? x : y));
+  }
+  if (w) *w = o;
+  return at;
+}
+
+bool sizes_ok(int64_t N, int64_t C, int64_t O) {
+  return N >= 0 && N < (int64_t{1} << 31) - 8192 && C >= 8 && C % 8 == 0 && O >= 8 && O % 8 == 0 && O <= (1 << 20);
+}
+// tiles of every product are counted in 32 bits
+bool tiles_ok(int64_t N, int64_t C, int64_t O) { return tiles_of(N, C > O ? C : O) < (int64_t{1} << 27); }
+bool act_ok(int32_t act) { return act >= TPK_ACT_NONE && act <= TPK_ACT_GELU_TANH; }
+bool ld_ok(int64_t ld, int64_t cols) { return ld >= cols && ld % 8 == 0; }
+
+}  // namespace
+
+int linear_product(const Mat& x, const Mat& w, const float* bias, int act, const Mat& residual, const Mat& y,
+                   float* acc, int32_t* err, cudaStream_t s) {
+  if (x.rows <= kFewRows) return few_linear(x, w, bias, act, residual, y, false, err, s);
+  Maps m;
+  int st = map_of(&m.a, x, kHalf);
+  if (st == TPK_OK) st = map_of(&m.b, w, kHalf);
+  if (st == TPK_OK) st = map_of(&m.out, y, kHalf);
+  if (st == TPK_OK && residual.p) st = map_of(&m.in, residual, kHalf);
+  if (st != TPK_OK) return st;
+  Params p = params(x.rows, w.rows, x.cols, true, acc, err);
+  p.bias = bias;
+  p.act = act;
+  p.has_in = residual.p != nullptr;
+  st = launch<kLin, true>(m, p, s);
+  if (st == TPK_OK && p.splits > 1) st = join(acc, p.M, p.N, p.splits, bias, act, residual, y, s);
+  return st;
+}
+
+int input_product(const Mat& dz, const Mat& w, const Mat& dx, float* acc, int32_t* err, cudaStream_t s) {
+  Maps m;
+  int st = map_of(&m.a, dz, kHalf);
+  if (st == TPK_OK) st = map_of(&m.b, w, 64);
+  if (st == TPK_OK) st = map_of(&m.out, dx, kHalf);
+  if (st != TPK_OK) return st;
+  const Params p = params(dz.rows, w.cols, dz.cols, true, acc, err);
+  const int64_t each = (dz.cols + 63) / 64 / p.splits + 1;   // stages of a unit, at most
+  st = each <= kChunk ? launch<kDx, true>(m, p, s) : launch<kDx, false>(m, p, s);
+  if (st == TPK_OK && p.splits > 1) st = join(acc, p.M, p.N, p.splits, nullptr, TPK_ACT_NONE, Mat{}, dx, s);
+  return st;
+}
+
+int weight_product(const Mat& dz, const Mat& x, const Mat& dw, float* acc, int32_t* err, cudaStream_t s) {
+  Maps m;
+  int st = map_of(&m.a, dz, 64);
+  if (st == TPK_OK) st = map_of(&m.b, x, 64);
+  if (st == TPK_OK) st = map_of(&m.out, dw, kHalf);
+  if (st != TPK_OK) return st;
+  const Params p = params(dz.cols, x.cols, dz.rows, true, acc, err);
+  const int64_t each = (dz.rows + 63) / 64 / p.splits + 1;
+  st = each <= kChunk ? launch<kDw, true>(m, p, s) : launch<kDw, false>(m, p, s);
+  if (st == TPK_OK && p.splits > 1) st = join(acc, p.M, p.N, p.splits, nullptr, TPK_ACT_NONE, Mat{}, dw, s);
+  return st;
+}
+
+}  // namespace product
+}  // namespace tpk
+
+extern "C" size_t tpk_linear_workspace_bytes(int64_t N, int32_t C, int32_t O, int32_t act, int32_t backward) {
+  using namespace tpk::product;
+  if (!sizes_ok(N, C, O) || !tiles_ok(N, C, O) || N == 0) return 0;
+  return carve(nullptr, N, C, O, act, backward != 0, nullptr);
+}
+
+extern "C" int tpk_linear(const void* x, int64_t ld_x, const void* w, const float* bias, int32_t act,
+                          const void* residual, int64_t ld_res, void* y, int64_t ld_y, int64_t N, int32_t C, int32_t O,
+                          void* workspace, size_t ws_bytes, int32_t* dev_err, void* stream) {
+  using namespace tpk;
+  using namespace tpk::product;
+  if (!sizes_ok(N, C, O) || !act_ok(act) || !ld_ok(ld_x, C) || !ld_ok(ld_y, O)) return TPK_E_ARG;
+  if (residual && !ld_ok(ld_res, O)) return TPK_E_ARG;
+  if (C > kMostK) return TPK_E_UNSUPPORTED;
+  if (!tiles_ok(N, C, O)) return TPK_E_OVERFLOW;
+  if (N == 0) return TPK_OK;
+  if (!x || !w || !y || !aligned16(x) || !aligned16(w) || !aligned16(y) || !aligned16(residual) || !aligned16(bias))
+    return TPK_E_ARG;
+  LinearWork k;
+  const size_t need = carve(static_cast<uint8_t*>(workspace), N, C, O, act, false, &k);
+  if (need && (!workspace || reinterpret_cast<uintptr_t>(workspace) % 256 || ws_bytes < need)) return TPK_E_WORKSPACE;
+  const int st = check_device();
+  if (st != TPK_OK) return st;
+  return linear_product(Mat{x, N, C, ld_x}, Mat{w, O, C, C}, bias, act, Mat{residual, N, O, ld_res}, Mat{y, N, O, ld_y},
+                        k.acc, dev_err, static_cast<cudaStream_t>(stream));
+}
+
+extern "C" int tpk_linear_bwd(const void* x, int64_t ld_x, const void* w, const float* bias, int32_t act,
+                              const void* dy, int64_t ld_dy, void* dx, int64_t ld_dx, void* dw, float* db, int64_t N,
+                              int32_t C, int32_t O, void* workspace, size_t ws_bytes, int32_t* dev_err, void* stream) {
+  using namespace tpk;
+  using namespace tpk::product;
+  if (!sizes_ok(N, C, O) || !act_ok(act) || !ld_ok(ld_x, C) || !ld_ok(ld_dy, O) || !ld_ok(ld_dx, C)) return TPK_E_ARG;
+  if (C > kMostK) return TPK_E_UNSUPPORTED;
+  if (!tiles_ok(N, C, O)) return TPK_E_OVERFLOW;
+  if (!dw || !aligned16(dw) || !aligned16(db)) return TPK_E_ARG;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  int st;
+  if (N == 0) {
+    st = check_device();
+    if (st == TPK_OK) st = cuda_status(cudaMemsetAsync(dw, 0, static_cast<size_t>(O) * C * 2, s));
+    if (st == TPK_OK && db) st = cuda_status(cudaMemsetAsync(db, 0, static_cast<size_t>(O) * 4, s));
+    return st;
+  }
+  if (!x || !w || !dy || !dx || !aligned16(x) || !aligned16(w) || !aligned16(dy) || !aligned16(dx) || !aligned16(bias))
+    return TPK_E_ARG;
+  LinearWork k;
+  if (!workspace || reinterpret_cast<uintptr_t>(workspace) % 256 ||
+      ws_bytes < carve(static_cast<uint8_t*>(workspace), N, C, O, act, true, &k))
+    return TPK_E_WORKSPACE;
+  st = check_device();
+  if (st != TPK_OK) return st;
+  const Mat mx{x, N, C, ld_x}, mw{w, O, C, C};
+  Mat dz{dy, N, O, ld_dy};
+  if (act != TPK_ACT_NONE) {
+    Maps m;
+    st = map_of(&m.a, mx, kHalf);
+    if (st == TPK_OK) st = map_of(&m.b, mw, kHalf);
+    if (st == TPK_OK) st = map_of(&m.in, dz, kHalf);
+    dz = Mat{k.dz, N, O, O};
+    if (st == TPK_OK) st = map_of(&m.out, dz, kHalf);
+    Params p = params(N, O, C, false, nullptr, dev_err);
+    p.bias = bias;
+    p.act = act;
+    p.colsum = db ? k.sums : nullptr;
+    if (st == TPK_OK) st = launch<kDz, true>(m, p, s);
+    if (st == TPK_OK && db) st = column_sums(k.sums, (N + 31) / 32, O, O, k.part, db, s);
+  } else if (db) {
+    st = column_sums(static_cast<const __nv_bfloat16*>(dy), N, O, ld_dy, k.part, db, s);
+  }
+  if (st == TPK_OK) st = input_product(dz, mw, Mat{dx, N, C, ld_dx}, k.acc, dev_err, s);
+  if (st == TPK_OK) st = weight_product(dz, mx, Mat{dw, O, C, C}, k.acc, dev_err, s);
+  return st;
+}

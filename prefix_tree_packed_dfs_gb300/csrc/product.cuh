@@ -1,0 +1,712 @@
+// The matrix products of the projections and the feed-forward block, with
+// their epilogues (linear.cu, ffn.cu).  A product is  D[m, n] = sum_k A B  over
+// bf16 operands, fp32 sums:
+//   kLin      x w^T              act(z + bias) + residual
+//   kDz       x w^T              dz = dy act'(z + bias), its column sums
+//   kDx       dz w               stored
+//   kDw       dz^T x             stored
+//   kGate     x (w_gate | w_up)^T   a = act(g) u (and g, u kept)
+//   kGateBwd  dy w_out              dg = da u act'(g), du = da act(g)
+// kLin, kDx and kDw may be split over K where their tiles alone do not fill
+// the GPU: fp32 partial tiles, summed in a fixed order by linear.cu's
+// join_kernel, which then does the epilogue.
+//
+// 256 x 256 tiles on a pair of CTAs (tcgen05 cta_group::2): each CTA holds 128
+// rows of A, 128 of B and its 128 rows of the result.  64 elements of K per
+// stage, five stages filled by TMA; two accumulators of 256 TMEM columns, so
+// that a tile's epilogue runs under the next tile's products.  Results leave
+// through shared memory by TMA; what an epilogue reads besides (residual, dy,
+// g and u) comes in by TMA to the very places its results leave from, issued
+// when the tile before has left and so long before the accumulator is ready.
+// kGate takes 128 rows of the gate's weights and 128 of the up projection's as
+// one B tile (one of each per CTA), so a thread's accumulator row holds g and u
+// of the same channels.
+// The tensor core adds to its fp32 accumulator with truncation: 1e-7 of the
+// running sum per step of 16 elements of K.  The sums over rows (kDw) and over
+// the wide side (kDx) stop every 8,192 elements and are added up in registers
+// with rounding to nearest: at most 5e-5 is left, a fortieth of the results'
+// bf16 rounding; sums over at most kMostK channels need no stop.
+// Warps of a CTA: 0 TMA producer, 1 MMA issuer (of the pair's first CTA), 2
+// TMEM owner, 4-11 epilogue (two warpgroups).  CTAs are persistent and walk the
+// tiles in panels of 8 columns of tiles, so that the pairs running together
+// share rows of A and of B in L2.
+#pragma once
+#include <type_traits>
+
+#include "activation.cuh"
+#include "pair.cuh"
+#include "rowwise.cuh"
+
+namespace tpk {
+namespace product {
+
+constexpr int kTile = 256;             // rows (and, but for kGate, columns) of a pair's tile
+constexpr int kHalf = 128;             // rows of A / of B a CTA holds
+constexpr int kBoxBytes = kHalf * 128; // 128 rows of 64 bf16
+constexpr int kThreads = 384;
+constexpr int kEpiThreads = 256;
+constexpr int kPanel = 8;
+constexpr int kStages = 5;
+constexpr int kChunk = 128;            // stages per accumulation of kDx, kDw
+constexpr int kMostK = 32768;          // channels of a sum that never stops
+constexpr int kPairs = 76;             // pairs a split over K aims to fill
+// The chunked epilogue holds 128 columns of a row per thread: the other warps
+// give registers to its two warpgroups.
+constexpr uint32_t kRegsCtl = 56;
+constexpr uint32_t kRegsEpi = 216;
+constexpr int kRegsNeeded = 128 * kRegsCtl + 256 * kRegsEpi;
+
+enum Mode { kLin = 0, kDz = 1, kDx = 2, kDw = 3, kGate = 4, kGateBwd = 5 };
+
+struct Maps {
+  CUtensorMap a, b, b2;      // b2: kGate's up rows
+  CUtensorMap in, in2;       // kLin residual, kDz dy; kGateBwd g, u
+  CUtensorMap out, out2, out3;   // kGate: a, g, u; kGateBwd: dg, du
+};
+
+struct Params {
+  int32_t M, N, K;           // extents of the product (kGate, kGateBwd: N = channels of one of the two)
+  int32_t splits;
+  int32_t act;
+  int32_t has_in;            // kLin: a residual
+  int32_t save;              // kGate: g and u go out too
+  const float* bias;         // [N] or nullptr
+  float* colsum;             // kDz: [ceil(M / 32)][N] sums of 32 rows of dz; nullptr: none
+  float* acc;                // splits > 1: [splits * tiles][256 * 256]
+  int32_t* err;
+};
+
+struct Smem {
+  uint8_t a[kStages][kBoxBytes];
+  uint8_t b[kStages][kBoxBytes];
+  uint8_t out[2][2][kBoxBytes];        // per warpgroup
+  uint64_t full[kStages], empty[kStages];
+  uint64_t tm_full[2], tm_empty[2];
+  uint64_t in_full[2][2];
+  uint64_t drain;
+  uint32_t tmem_base;
+  int abort_flag;
+  uint32_t issued;   // stages the producer has filled
+};
+constexpr size_t kSmemBytes = sizeof(Smem) + 1024;
+static_assert(kSmemBytes <= 227 * 1024, "shared memory");
+
+// Splits over K where the tiles alone do not fill the GPU: one round of units
+// for a few tiles; otherwise, below four rounds, the split into up to 8 that
+// makes the rounds shortest, where it saves a tenth or more.  A split has 8
+// stages of K or more.
+constexpr int kSplitRounds = 4, kSplitMost = 8;
+inline int splits_for(int64_t tiles, int64_t k_iters) {
+  const int64_t most = k_iters / 8;
+  if (tiles <= 0 || tiles > kSplitRounds * kPairs || most <= 1) return 1;
+  if (tiles * kSplitMost <= kPairs) {
+    const int64_t s = kPairs / tiles;
+    return static_cast<int>(s < most ? s : most);
+  }
+  int64_t best = 1, rounds = (tiles + kPairs - 1) / kPairs;
+  for (int64_t s = 2; s <= kSplitMost && s <= most; ++s) {
+    const int64_t r = (tiles * s + kPairs - 1) / kPairs;
+    if (r * best * 10 <= rounds * s * 9) {
+      best = s;
+      rounds = r;
+    }
+  }
+  return static_cast<int>(best);
+}
+
+// Unit u covers tile (m, n) and the stages [k0, k0 + nk) of K.
+struct Shape {
+  int mt, nt, units, k_iters;
+};
+struct Unit {
+  int m, n, k0, nk, split;
+};
+template <int kMode>
+constexpr int kTileN = kMode == kGate ? kHalf : kTile;
+
+template <int kMode>
+__host__ __device__ inline Shape shape_of(const Params& p) {
+  Shape s;
+  s.mt = (p.M + kTile - 1) / kTile;
+  s.nt = (p.N + kTileN<kMode> - 1) / kTileN<kMode>;
+  s.k_iters = (p.K + 63) / 64;
+  s.units = s.mt * s.nt * p.splits;
+  return s;
+}
+__device__ __forceinline__ Unit unit_of(const Params& p, const Shape& s, int u) {
+  Unit w;
+  const int tiles = s.mt * s.nt;
+  w.split = u / tiles;
+  int t = u - w.split * tiles;
+  const int panel = t / (kPanel * s.mt);
+  t -= panel * kPanel * s.mt;
+  const int width = min(kPanel, s.nt - panel * kPanel);
+  w.m = t / width;
+  w.n = panel * kPanel + t % width;
+  w.k0 = static_cast<int>(static_cast<int64_t>(s.k_iters) * w.split / p.splits);
+  w.nk = static_cast<int>(static_cast<int64_t>(s.k_iters) * (w.split + 1) / p.splits) - w.k0;
+  return w;
+}
+
+__device__ __forceinline__ uint64_t pair_at(const uint32_t (&x)[32], int e) {
+  return ptx::f2(__uint_as_float(x[2 * e]), __uint_as_float(x[2 * e + 1]));
+}
+
+// 32 columns of a row into half `half` of a box of 64, in the TMA's 128-byte
+// swizzle (16-byte piece i of row r at piece i ^ (r % 8)).
+__device__ __forceinline__ void put64(uint8_t* box, int r, int half, const uint32_t (&o)[16]) {
+#pragma unroll
+  for (int q = 0; q < 4; ++q)
+    *reinterpret_cast<uint4*>(box + r * 128 + (((half * 4 + q) ^ (r & 7)) * 16)) =
+        make_uint4(o[4 * q], o[4 * q + 1], o[4 * q + 2], o[4 * q + 3]);
+}
+__device__ __forceinline__ void get64(const uint8_t* box, int r, int half, uint32_t (&o)[16]) {
+#pragma unroll
+  for (int q = 0; q < 4; ++q) {
+    const int4 v = ptx::lds128i(box + r * 128 + (((half * 4 + q) ^ (r & 7)) * 16));
+    o[4 * q] = v.x; o[4 * q + 1] = v.y; o[4 * q + 2] = v.z; o[4 * q + 3] = v.w;
+  }
+}
+// The same for boxes of 32 columns in the 64-byte swizzle (piece i of row r at
+// piece i ^ (r / 2 % 4)).
+__device__ __forceinline__ uint8_t* at32(uint8_t* box, int r, int q) {
+  return box + r * 64 + ((q ^ ((r >> 1) & 3)) * 16);
+}
+
+// Sums over the warp's 32 rows of x[0..31] (a row per lane): lane l returns
+// the sum of column l.  Each step halves the columns a lane holds.
+__device__ __forceinline__ float column_sums(float (&x)[32], int lane) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) {
+    const bool up = lane & o;
+#pragma unroll
+    for (int j = 0; j < o; ++j) {
+      const float send = up ? x[j] : x[j + o], keep = up ? x[j + o] : x[j];
+      x[j] = keep + __shfl_xor_sync(0xffffffffu, send, o);
+    }
+  }
+  return x[0];
+}
+
+// kOne: every tile is a single accumulation, which goes out while it is read
+// from TMEM and need not be held whole.
+template <int kMode, bool kOne>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
+    product_kernel(const __grid_constant__ Maps maps, const Params p) {
+  extern __shared__ uint8_t smem_raw[];
+  Smem& S = *reinterpret_cast<Smem*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  constexpr bool kAmn = kMode == kDw;                                          // A stored with M contiguous
+  constexpr bool kBmn = kMode == kDx || kMode == kDw || kMode == kGateBwd;     // B stored with N contiguous
+  constexpr bool kPlain = kMode == kLin || kMode == kDx || kMode == kDw;
+  static_assert(kOne || kMode == kDx || kMode == kDw, "sums over channels do not stop");
+  const int warp = threadIdx.x >> 5;
+  const uint32_t rank = ptx::cluster_rank();
+  const int pair = blockIdx.x >> 1, n_pairs = gridDim.x >> 1;
+  volatile int* abort_flag = &S.abort_flag;
+  const Shape sh = shape_of<kMode>(p);
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < kStages; ++s) {
+      ptx::mbar_init(&S.full[s], 1);
+      ptx::mbar_init(&S.empty[s], 1);
+    }
+    for (int b = 0; b < 2; ++b) {
+      ptx::mbar_init(&S.tm_full[b], 1);
+      ptx::mbar_init(&S.tm_empty[b], 2 * kEpiThreads / 32);   // every epilogue warp of the pair
+      ptx::mbar_init(&S.in_full[0][b], 1);
+      ptx::mbar_init(&S.in_full[1][b], 1);
+    }
+    ptx::mbar_init(&S.drain, 1);
+    S.abort_flag = 0;
+    S.issued = 0;
+    ptx::fence_mbar_init();
+  }
+  if (warp == 2) {
+    ptx::tmem_alloc_pair(&S.tmem_base, 512);
+    ptx::tmem_relinquish_pair();
+  }
+  ptx::tc_fence_before();
+  __syncthreads();
+  ptx::cluster_sync();   // the other CTA's barriers exist
+  ptx::tc_fence_after();
+  const uint32_t tmem = S.tmem_base;
+  if (warp < 4) {
+    if constexpr (!kOne) ptx::regs_dec<kRegsCtl>();
+    if (warp == 0) {
+      // ---------------------------------------------------------- producer
+      if (ptx::elect_one()) {
+        ptx::prefetch_tensormap(&maps.a);
+        ptx::prefetch_tensormap(&maps.b);
+        const CUtensorMap* mb = kMode == kGate && rank == 1 ? &maps.b2 : &maps.b;
+        uint32_t it = 0;
+        bool ok = true;
+        for (int u = pair; ok && u < sh.units; u += n_pairs) {
+          const Unit w = unit_of(p, sh, u);
+          const int m0 = w.m * kTile + static_cast<int>(rank) * kHalf;
+          const int n0 = w.n * kTileN<kMode> + (kMode == kGate ? 0 : static_cast<int>(rank) * kHalf);
+          for (int k = 0; k < w.nk; ++k, ++it) {
+            const int st = it % kStages;
+            if (it >= kStages && !ptx::mbar_wait(&S.empty[st], (it / kStages - 1) & 1, abort_flag, kWaitLimitNs)) {
+              ok = false;
+              break;
+            }
+            if (rank == 0) ptx::mbar_arrive_expect_tx(&S.full[st], 4 * kBoxBytes);
+            const uint32_t bar = ptx::cluster_addr(&S.full[st], 0);
+            const int kk = (w.k0 + k) * 64;
+            if constexpr (kAmn) {
+              ptx::tma_load_2d_pair(S.a[st], &maps.a, bar, m0, kk);
+              ptx::tma_load_2d_pair(S.a[st] + kBoxBytes / 2, &maps.a, bar, m0 + 64, kk);
+            } else {
+              ptx::tma_load_2d_pair(S.a[st], &maps.a, bar, kk, m0);
+            }
+            if constexpr (kBmn) {
+              ptx::tma_load_2d_pair(S.b[st], mb, bar, n0, kk);
+              ptx::tma_load_2d_pair(S.b[st] + kBoxBytes / 2, mb, bar, n0 + 64, kk);
+            } else {
+              ptx::tma_load_2d_pair(S.b[st], mb, bar, kk, n0);
+            }
+          }
+        }
+        S.issued = it;
+      }
+    } else if (warp == 1 && rank == 0) {
+      // ---------------------------------------------------------- MMA issuer
+      if (ptx::elect_one()) {
+        constexpr uint32_t idesc = ptx::idesc_bf16_f32(kTile, kTile, kAmn, kBmn);
+        // K step of 16 elements: 32 bytes along a K-major row, 16 rows of 128
+        // bytes of an MN-major box (its two 64-column boxes half a stage apart)
+        constexpr uint32_t kStepA = kAmn ? 2048 : 32, kStepB = kBmn ? 2048 : 32;
+        uint32_t it = 0, tile = 0;
+        bool ok = true;
+        for (int u = pair; ok && u < sh.units; u += n_pairs) {
+          const Unit w = unit_of(p, sh, u);
+          const int per = kOne ? w.nk : kChunk;
+          for (int k0 = 0; ok && k0 < w.nk; k0 += per, ++tile) {
+            const uint32_t buf = tile & 1;
+            if (tile >= 2 && !ptx::mbar_wait(&S.tm_empty[buf], (tile / 2 - 1) & 1, abort_flag, kWaitLimitNs)) {
+              ok = false;
+              break;
+            }
+            ptx::tc_fence_after();
+            const int nk = min(per, w.nk - k0);
+            for (int k = 0; k < nk; ++k, ++it) {
+              const int st = it % kStages;
+              if (!ptx::mbar_wait(&S.full[st], (it / kStages) & 1, abort_flag, kWaitLimitNs)) {
+                ok = false;
+                break;
+              }
+              ptx::tc_fence_after();
+              const uint64_t ad = ptx::sw128_desc(ptx::smem_addr(S.a[st]), kAmn ? kBoxBytes / 2 : 16, 1024);
+              const uint64_t bd = ptx::sw128_desc(ptx::smem_addr(S.b[st]), kBmn ? kBoxBytes / 2 : 16, 1024);
+#pragma unroll
+              for (int q = 0; q < 4; ++q)
+                ptx::mma_ss_pair(tmem + buf * kTile, ptx::desc_add(ad, q * kStepA), ptx::desc_add(bd, q * kStepB),
+                                 idesc, (k > 0 || q > 0) ? 1u : 0u);
+              ptx::mma_commit_pair(&S.empty[st]);
+            }
+            if (ok) ptx::mma_commit_pair(&S.tm_full[buf]);
+          }
+        }
+        // every product issued above has completed before TMEM is released
+        ptx::mma_commit_pair(&S.drain);
+        ptx::mbar_drain(&S.drain, 0);
+      }
+    }
+  } else {
+    // ------------------------------------------------------------ epilogue
+    if constexpr (!kOne) ptx::regs_inc<kRegsEpi>();
+    const int wg = (warp - 4) >> 2;
+    const int lane = threadIdx.x & 31;
+    const int rc = (warp & 3) * 32 + lane;   // row of this CTA's half tile
+    const bool leader = (threadIdx.x & 127) == 0;
+    const uint32_t lane_off = static_cast<uint32_t>((warp & 3) * 32) << 16;
+    const uint32_t bar_empty[2] = {ptx::cluster_addr(&S.tm_empty[0], 0), ptx::cluster_addr(&S.tm_empty[1], 0)};
+    uint8_t* const box[2] = {S.out[wg][0], S.out[wg][1]};
+    auto meet = [&] { asm volatile("bar.sync %0, 128;" ::"r"(wg + 1) : "memory"); };
+    // loads into box s so far (each thread's count), of which the last may be under way
+    uint32_t loads[2] = {0, 0};
+    const bool takes = kMode == kDz || kMode == kGateBwd || (kMode == kLin && p.has_in && p.splits == 1);
+    uint32_t tile = 0, sent = 0;
+    bool ok = true;
+    for (int u = pair; ok && u < sh.units; u += n_pairs) {
+      const Unit w = unit_of(p, sh, u);
+      const int row0 = w.m * kTile + static_cast<int>(rank) * kHalf;   // first row of this CTA
+      const int n0 = w.n * kTileN<kMode> + wg * (kTileN<kMode> / 2);   // first column of this warpgroup
+      // what the epilogue reads, into the boxes that it will leave from
+      auto fetch = [&](int s, int col) {
+        if constexpr (kMode == kGateBwd) {
+          ptx::mbar_arrive_expect_tx(&S.in_full[wg][s], kBoxBytes);
+          ptx::tma_load_2d(box[s], &maps.in, &S.in_full[wg][s], col, row0);
+          ptx::tma_load_2d(box[s] + kBoxBytes / 2, &maps.in2, &S.in_full[wg][s], col, row0);
+        } else {
+          ptx::mbar_arrive_expect_tx(&S.in_full[wg][s], kBoxBytes);
+          ptx::tma_load_2d(box[s], &maps.in, &S.in_full[wg][s], col, row0);
+        }
+      };
+      auto fetched = [&](int s) {
+        return ptx::mbar_wait(&S.in_full[wg][s], (loads[s] - 1) & 1, abort_flag, kWaitLimitNs);
+      };
+      if (takes) {
+        if (leader) {
+          ptx::bulk_wait_read<0>();   // the boxes' last results have left
+          fetch(0, n0);
+          fetch(1, n0 + (kMode == kGateBwd ? 32 : 64));
+        }
+        ++loads[0];
+        ++loads[1];
+      }
+      // the accumulator: 128 columns as packed pairs where chunks are added up
+      uint64_t z[kOne ? 1 : kHalf / 2];
+      if constexpr (!kOne) {
+#pragma unroll 1
+        for (int k = 0; ok && k < w.nk; k += kChunk) {
+          const uint32_t buf = tile & 1;
+          if (!__all_sync(0xffffffffu, ptx::mbar_wait(&S.tm_full[buf], (tile / 2) & 1, abort_flag, kWaitLimitNs))) {
+            ok = false;
+            break;
+          }
+          ptx::tc_fence_after();
+          ++tile;
+          const uint32_t tm = tmem + lane_off + buf * kTile + wg * kHalf;
+#pragma unroll
+          for (int c = 0; c < 4; ++c) {
+            uint32_t x[32];
+            ptx::tmem_ld32(tm + c * 32, x);
+            ptx::tmem_wait_ld_of(x);
+#pragma unroll
+            for (int e = 0; e < 16; ++e)
+              z[c * 16 + e] = k == 0 ? pair_at(x, e) : ptx::add2(z[c * 16 + e], pair_at(x, e));
+          }
+          ptx::tc_fence_before();
+          __syncwarp();
+          if (lane == 0) ptx::mbar_arrive_cluster(bar_empty[buf]);
+        }
+      } else {
+        ok = ptx::mbar_wait(&S.tm_full[tile & 1], (tile / 2) & 1, abort_flag, kWaitLimitNs);
+      }
+      // a warpgroup has barriers of its own and gives up as a whole
+      ok = ptx::all_of_128(wg + 1, ok);
+      if (!ok) break;
+      const uint32_t buf = tile & 1;
+      const uint32_t tm = tmem + lane_off + buf * kTile + (kMode == kGate ? wg * 64 : wg * kHalf);
+      if constexpr (kOne) {
+        ptx::tc_fence_after();
+        ++tile;
+      }
+      auto release = [&] {   // the whole accumulator has been read
+        ptx::tc_fence_before();
+        __syncwarp();
+        if (lane == 0) ptx::mbar_arrive_cluster(bar_empty[buf]);
+      };
+
+      if constexpr (kPlain || kMode == kDz) {
+        // 32 columns at a time, read from TMEM while those before go out
+        uint32_t raw[kOne ? 2 : 1][32];
+        if constexpr (kOne) {
+          ptx::tmem_ld32(tm, raw[0]);
+          ptx::tmem_wait_ld_of(raw[0]);
+        }
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          uint64_t x[16];
+          if constexpr (kOne) {
+            if (c < 3) ptx::tmem_ld32(tm + (c + 1) * 32, raw[(c + 1) & 1]);
+#pragma unroll
+            for (int e = 0; e < 16; ++e) x[e] = pair_at(raw[c & 1], e);
+          } else {
+#pragma unroll
+            for (int e = 0; e < 16; ++e) x[e] = z[c * 16 + e];
+          }
+          const int c0 = n0 + c * 32, b = c >> 1, half = c & 1;
+          if (kPlain && p.splits > 1) {
+            const int64_t tile_id = static_cast<int64_t>(w.split) * sh.mt * sh.nt + w.m * sh.nt + w.n;
+            float* blk = p.acc + tile_id * (kTile * kTile) + (static_cast<int>(rank) * kHalf + rc) * kTile + wg * kHalf;
+            ulonglong2* ap = reinterpret_cast<ulonglong2*>(blk + c * 32);
+#pragma unroll
+            for (int q = 0; q < 8; ++q) ap[q] = make_ulonglong2(x[2 * q], x[2 * q + 1]);
+          } else {
+            uint32_t o[16];
+            if (half == 0) {
+              if (takes) {
+                ok = fetched(b);
+              } else {
+                if (leader) ptx::bulk_wait_read<1>();   // this box's last store
+                meet();
+              }
+            }
+            if constexpr (kMode == kLin) {
+              // the plain projection stores what it has summed
+              uint32_t in[16];
+              if (takes) get64(box[b], rc, half, in);
+              float v[32];
+#pragma unroll
+              for (int e = 0; e < 16; ++e) ptx::unf2(x[e], v[2 * e], v[2 * e + 1]);
+              if (p.bias) {
+#pragma unroll
+                for (int e = 0; e < 32; e += 4)
+                  if (c0 + e < p.N) {
+                    const float4 bv = __ldg(reinterpret_cast<const float4*>(p.bias + c0 + e));
+                    v[e] += bv.x; v[e + 1] += bv.y; v[e + 2] += bv.z; v[e + 3] += bv.w;
+                  }
+              }
+              if (p.act != TPK_ACT_NONE)
+                with_act(p.act, [&](auto t) {
+#pragma unroll
+                  for (int e = 0; e < 32; ++e) v[e] = act_of<decltype(t)::value>(v[e]);
+                });
+#pragma unroll
+              for (int e = 0; e < 16; ++e) {
+                if (takes) {
+                  v[2 * e] += lo16(in[e]);
+                  v[2 * e + 1] += hi16(in[e]);
+                }
+                o[e] = ptx::pack_bf16x2(v[2 * e], v[2 * e + 1]);
+              }
+            } else if constexpr (kMode == kDz) {
+              uint32_t in[16];
+              get64(box[b], rc, half, in);
+              float v[32];
+#pragma unroll
+              for (int e = 0; e < 16; ++e) ptx::unf2(x[e], v[2 * e], v[2 * e + 1]);
+              if (p.bias) {
+#pragma unroll
+                for (int e = 0; e < 32; e += 4)
+                  if (c0 + e < p.N) {
+                    const float4 bv = __ldg(reinterpret_cast<const float4*>(p.bias + c0 + e));
+                    v[e] += bv.x; v[e + 1] += bv.y; v[e + 2] += bv.z; v[e + 3] += bv.w;
+                  }
+              }
+              const bool inside = row0 + rc < p.M;
+              with_act(p.act, [&](auto t) {
+#pragma unroll
+                for (int e = 0; e < 32; ++e) {
+                  float slope;
+                  act_slope<decltype(t)::value>(v[e], slope);
+                  v[e] = (e & 1 ? hi16(in[e / 2]) : lo16(in[e / 2])) * slope;
+                }
+              });
+#pragma unroll
+              for (int e = 0; e < 16; ++e) o[e] = ptx::pack_bf16x2(v[2 * e], v[2 * e + 1]);
+              if (p.colsum) {
+                if (!inside)
+#pragma unroll
+                  for (int e = 0; e < 32; ++e) v[e] = 0.f;
+                const float sum = column_sums(v, lane);
+                if (row0 + (warp & 3) * 32 < p.M && c0 + lane < p.N)
+                  p.colsum[static_cast<int64_t>(row0 / 32 + (warp & 3)) * p.N + c0 + lane] = sum;
+              }
+            } else {
+#pragma unroll
+              for (int e = 0; e < 16; ++e) {
+                float lo, hi;
+                ptx::unf2(x[e], lo, hi);
+                o[e] = ptx::pack_bf16x2(lo, hi);
+              }
+            }
+            put64(box[b], rc, half, o);
+            if (half == 1) {
+              ptx::fence_async_shared();
+              meet();
+              if (leader) {
+                if (c0 - 32 < p.N && row0 < p.M) ptx::tma_store_2d(&maps.out, box[b], c0 - 32, row0);
+                ptx::bulk_commit();
+              }
+            }
+          }
+          if constexpr (kOne) {
+            if (c < 3) ptx::tmem_wait_ld_of(raw[(c + 1) & 1]);
+            if (c == 2) release();
+          }
+        }
+      } else if constexpr (kMode == kGate) {
+        // columns [0, 64) of this warpgroup: g at 0, u at 128 of the accumulator
+        uint32_t a[2][16];
+        if (p.save) {
+          if (leader) ptx::bulk_wait_read<0>();
+          meet();
+        }
+#pragma unroll
+        for (int half = 0; half < 2; ++half) {
+          uint32_t g[32], up[32];
+          ptx::tmem_ld32(tm + half * 32, g);
+          ptx::tmem_ld32(tm + kHalf + half * 32, up);
+          ptx::tmem_wait_ld_of(g);
+          ptx::tmem_wait_ld_of(up);
+          if (half == 1) release();
+          if (p.save) {
+            uint32_t o[16];
+#pragma unroll
+            for (int e = 0; e < 16; ++e) o[e] = ptx::pack_bf16x2(__uint_as_float(g[2 * e]), __uint_as_float(g[2 * e + 1]));
+            put64(box[0], rc, half, o);
+#pragma unroll
+            for (int e = 0; e < 16; ++e)
+              o[e] = ptx::pack_bf16x2(__uint_as_float(up[2 * e]), __uint_as_float(up[2 * e + 1]));
+            put64(box[1], rc, half, o);
+          }
+          with_act(p.act, [&](auto t) {
+#pragma unroll
+            for (int e = 0; e < 16; ++e)
+              a[half][e] =
+                  ptx::pack_bf16x2(act_of<decltype(t)::value>(__uint_as_float(g[2 * e])) * __uint_as_float(up[2 * e]),
+                                   act_of<decltype(t)::value>(__uint_as_float(g[2 * e + 1])) *
+                                       __uint_as_float(up[2 * e + 1]));
+          });
+        }
+        const bool inside = n0 < p.N && row0 < p.M;
+        int s = 0;
+        if (p.save) {
+          ptx::fence_async_shared();
+          meet();
+          if (leader) {
+            if (inside) ptx::tma_store_2d(&maps.out2, box[0], n0, row0);
+            ptx::bulk_commit();
+            if (inside) ptx::tma_store_2d(&maps.out3, box[1], n0, row0);
+            ptx::bulk_commit();
+            ptx::bulk_wait_read<1>();   // g has left
+          }
+        } else {
+          s = static_cast<int>(sent++ & 1);
+          if (leader) ptx::bulk_wait_read<1>();
+        }
+        meet();
+        put64(box[s], rc, 0, a[0]);
+        put64(box[s], rc, 1, a[1]);
+        ptx::fence_async_shared();
+        meet();
+        if (leader) {
+          if (inside) ptx::tma_store_2d(&maps.out, box[s], n0, row0);
+          ptx::bulk_commit();
+        }
+      } else {
+        // kGateBwd: 32 columns at a time, g and u in the two halves of a box
+        uint32_t raw[2][32];
+        ptx::tmem_ld32(tm, raw[0]);
+        ptx::tmem_wait_ld_of(raw[0]);
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          if (c < 3) ptx::tmem_ld32(tm + (c + 1) * 32, raw[(c + 1) & 1]);
+          const int s = c & 1, c0 = n0 + c * 32;
+          ok = fetched(s) && ok;
+          with_act(p.act, [&](auto t) {
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+              uint8_t* gp = at32(box[s], rc, q);
+              uint8_t* up = gp + kBoxBytes / 2;
+              const int4 gv = ptx::lds128i(gp), uv = ptx::lds128i(up);
+              const uint32_t gw[4] = {static_cast<uint32_t>(gv.x), static_cast<uint32_t>(gv.y),
+                                      static_cast<uint32_t>(gv.z), static_cast<uint32_t>(gv.w)};
+              const uint32_t uw[4] = {static_cast<uint32_t>(uv.x), static_cast<uint32_t>(uv.y),
+                                      static_cast<uint32_t>(uv.z), static_cast<uint32_t>(uv.w)};
+              uint32_t og[4], ou[4];
+#pragma unroll
+              for (int e = 0; e < 4; ++e) {
+                const float d0 = __uint_as_float(raw[c & 1][q * 8 + 2 * e]);
+                const float d1 = __uint_as_float(raw[c & 1][q * 8 + 2 * e + 1]);
+                float s0, s1;
+                const float a0 = act_slope<decltype(t)::value>(lo16(gw[e]), s0);
+                const float a1 = act_slope<decltype(t)::value>(hi16(gw[e]), s1);
+                og[e] = ptx::pack_bf16x2(d0 * lo16(uw[e]) * s0, d1 * hi16(uw[e]) * s1);
+                ou[e] = ptx::pack_bf16x2(d0 * a0, d1 * a1);
+              }
+              *reinterpret_cast<uint4*>(gp) = make_uint4(og[0], og[1], og[2], og[3]);
+              *reinterpret_cast<uint4*>(up) = make_uint4(ou[0], ou[1], ou[2], ou[3]);
+            }
+          });
+          ptx::fence_async_shared();
+          meet();
+          if (leader) {
+            if (c0 < p.N && row0 < p.M) {
+              ptx::tma_store_2d(&maps.out, box[s], c0, row0);
+              ptx::tma_store_2d(&maps.out2, box[s] + kBoxBytes / 2, c0, row0);
+            }
+            ptx::bulk_commit();
+            if (c < 2) {
+              ptx::bulk_wait_read<0>();
+              fetch(s, c0 + 64);
+            }
+          }
+          if (c < 2) ++loads[s];
+          if (c < 3) ptx::tmem_wait_ld_of(raw[(c + 1) & 1]);
+          if (c == 2) release();
+        }
+      }
+      if (takes) ok = ptx::all_of_128(wg + 1, ok);   // a load that gave up
+    }
+    if (leader) {
+      // loads that nobody waited for (after a timeout) have arrived before the CTA leaves
+      for (int s = 0; s < 2; ++s)
+        if (loads[s]) ptx::mbar_drain(&S.in_full[wg][s], (loads[s] - 1) & 1);
+      ptx::bulk_wait_all();
+    }
+  }
+  // Both CTAs leave together: nothing of the pair signals or reads a CTA that
+  // has gone.  After a timeout the stages' copies are waited for first.
+  __syncwarp();
+  __syncthreads();
+  ptx::cluster_sync();
+  if (S.abort_flag) {
+    if (threadIdx.x == 0) {
+      if (p.err) *p.err = TPK_E_TIMEOUT;
+      if (rank == 0)
+        for (uint32_t i = S.issued > kStages ? S.issued - kStages : 0; i < S.issued; ++i)
+          ptx::mbar_drain(&S.full[i % kStages], (i / kStages) & 1);
+    }
+  }
+  __syncwarp();
+  __syncthreads();
+  ptx::cluster_sync();
+  ptx::tc_fence_after();
+  if (warp == 2) ptx::tmem_dealloc_pair(tmem, 512);
+}
+
+// ---- host -------------------------------------------------------------------------
+// A row-major bf16 matrix whose rows lie ld elements apart.
+struct Mat {
+  const void* p;
+  int64_t rows, cols, ld;
+};
+inline int map_of(CUtensorMap* m, const Mat& a, int box_rows, int box_cols = 64) {
+  return make_map_2d(m, a.p, a.rows, a.cols, a.ld, box_rows, box_cols);
+}
+
+inline int64_t tiles_of(int64_t M, int64_t N) { return (M + kTile - 1) / kTile * ((N + kTile - 1) / kTile); }
+// Workspace of a product that may be split over K.
+inline size_t acc_bytes(int64_t M, int64_t N, int64_t K) {
+  const int64_t tiles = tiles_of(M, N);
+  const int s = splits_for(tiles, (K + 63) / 64);
+  return s > 1 ? static_cast<size_t>(tiles) * s * kTile * kTile * 4 : 0;
+}
+
+template <int kMode, bool kOne>
+int launch(const Maps& maps, const Params& p, cudaStream_t s) {
+  constexpr auto kern = product_kernel<kMode, kOne>;
+  static PerContext<int> rec;
+  int unused = 0;
+  const int st = guarded([&] { return rec.get(&unused, [](int*) {
+    cudaFuncAttributes fa;
+    if (cudaFuncGetAttributes(&fa, kern) != cudaSuccess) return TPK_E_CUDA;
+    // setmaxnreg waits for registers the CTA was not launched with
+    if (!kOne && fa.numRegs * kThreads < kRegsNeeded) return TPK_E_UNSUPPORTED;
+    return cuda_status(
+        cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(kSmemBytes)));
+  }); });
+  if (st != TPK_OK) return st;
+  const int units = shape_of<kMode>(p).units;
+  int pairs = num_sms() / 2;
+  pairs = pairs < 1 ? 1 : pairs;
+  pairs = pairs < units ? pairs : units;
+  kern<<<static_cast<unsigned>(2 * pairs), kThreads, kSmemBytes, s>>>(maps, p);
+  return cuda_status(cudaGetLastError());
+}
+
+// Products of linear.cu that the feed-forward block uses too.  acc: acc_bytes.
+// y = act(x w^T + bias) + residual (residual.p may be nullptr)
+int linear_product(const Mat& x, const Mat& w, const float* bias, int act, const Mat& residual, const Mat& y,
+                   float* acc, int32_t* err, cudaStream_t s);
+// dx = dz w
+int input_product(const Mat& dz, const Mat& w, const Mat& dx, float* acc, int32_t* err, cudaStream_t s);
+// dw = dz^T x
+int weight_product(const Mat& dz, const Mat& x, const Mat& dw, float* acc, int32_t* err, cudaStream_t s);
+
+}  // namespace product
+}  // namespace tpk

@@ -8,9 +8,14 @@
 // 16-byte accesses: a thread rotates 8 pairs (x_i, x_{i+d/2}).
 // The angle depth * base^(-2i/d) is reduced to a fraction of a turn in fp64
 // (exact for depths < 2^31), then evaluated with sincospif in fp32.
+//
+// rope_rows_kernel is the general form (tpk_rope_by_depth_ex): either pairing,
+// a part of the head, any angle per position and pair, strided rows.
 #include <cuda_bf16.h>
 
-#include "common.cuh"
+#include <cmath>
+
+#include "rowwise.cuh"
 
 namespace tpk {
 namespace {
@@ -79,6 +84,109 @@ __global__ void __launch_bounds__(kThreads) rope_kernel(const __nv_bfloat16* q_i
   }
 }
 
+// ---- the general form ---------------------------------------------------------
+// Turns per position of each pair as a 64-bit fraction: the angle's place in its
+// turn is the low 64 bits of an integer product, off by depth * 2^-65 at most,
+// for any int32 depth.  (In fp64 the products and roundings alone would take a
+// third of the kernel's time on this part.)
+constexpr int kMostPairs = 128;      // rot <= 256
+constexpr int kRowsMost = 16;        // positions per block
+constexpr int kRowItems = 4;         // pieces per thread whose loads are in flight together
+
+struct Fractions {
+  uint64_t v[kMostPairs];
+};
+
+struct RopeRows {
+  const __nv_bfloat16 *q_in, *k_in;
+  __nv_bfloat16 *q_out, *k_out;
+  int64_t ld_q, ld_k, ld_qo, ld_ko;
+  const int32_t* depth;
+  int64_t F;
+  int32_t Hq, Hkv, D, rot;
+  int32_t per;                       // positions per block
+  float factor, sign;
+};
+
+// A piece is 16 bytes of a head, or, for a rotated piece of the half layout,
+// the two whose channels make pairs.
+template <bool kInter>
+__global__ void __launch_bounds__(kThreads) rope_rows_kernel(const RopeRows p, const Fractions fr) {
+  __shared__ __align__(16) float2 cs[kRowsMost * kMostPairs];
+  const int pairs = p.rot / 2;
+  const int64_t f0 = static_cast<int64_t>(blockIdx.x) * p.per;
+  const int n = p.F - f0 < p.per ? static_cast<int>(p.F - f0) : p.per;
+  const int turned = kInter ? p.rot / 8 : p.rot / 16;          // rotated pieces of a head
+  const int per_head = turned + (p.D - p.rot) / 8;
+  const int heads = p.Hq + p.Hkv, per_pos = heads * per_head;
+  const int items = n * per_pos;
+  for (int i0 = threadIdx.x; i0 - static_cast<int>(threadIdx.x) < items; i0 += kThreads * kRowItems) {
+    uint4 a[kRowItems], b[kRowItems];
+    int at[kRowItems];               // position * 256 + piece; -1: none
+    __nv_bfloat16* dst[kRowItems];
+#pragma unroll
+    for (int j = 0; j < kRowItems; ++j) {
+      const int it = i0 + j * kThreads;
+      at[j] = -1;
+      if (it >= items) continue;
+      const int pos = it / per_pos, rem = it - pos * per_pos;
+      const int h = rem / per_head, c = rem - h * per_head;
+      const int64_t f = f0 + pos;
+      const __nv_bfloat16* src;
+      if (h < p.Hq) {
+        src = p.q_in + f * p.ld_q + h * p.D;
+        dst[j] = p.q_out + f * p.ld_qo + h * p.D;
+      } else {
+        src = p.k_in + f * p.ld_k + (h - p.Hq) * p.D;
+        dst[j] = p.k_out + f * p.ld_ko + (h - p.Hq) * p.D;
+      }
+      at[j] = pos * 256 + c;
+      const int ch = c < turned ? c * 8 : p.rot + (c - turned) * 8;
+      a[j] = *reinterpret_cast<const uint4*>(src + ch);
+      if (!kInter && c < turned) b[j] = *reinterpret_cast<const uint4*>(src + pairs + ch);
+      dst[j] += ch;
+    }
+    if (i0 == static_cast<int>(threadIdx.x)) {   // the angles, while the first pieces are on their way
+      for (int t = threadIdx.x; t < n * pairs; t += kThreads) {
+        const int pos = t / pairs, i = t - pos * pairs;
+        const uint64_t turn = static_cast<uint64_t>(static_cast<int64_t>(__ldg(p.depth + f0 + pos))) * fr.v[i];
+        float s, c;
+        sincospif(static_cast<float>(static_cast<int64_t>(turn)) * 0x1p-63f, &s, &c);
+        cs[t] = make_float2(c * p.factor, s * p.factor * p.sign);
+      }
+      __syncthreads();
+    }
+#pragma unroll
+    for (int j = 0; j < kRowItems; ++j) {
+      if (at[j] < 0) continue;
+      const int pos = at[j] >> 8, c = at[j] & 255;
+      if (c < turned) {
+        uint32_t x[4] = {a[j].x, a[j].y, a[j].z, a[j].w};
+        if constexpr (kInter) {
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const float2 w = cs[pos * pairs + c * 4 + e];
+            const float u = lo16(x[e]), v = hi16(x[e]);
+            x[e] = pack2(u * w.x - v * w.y, u * w.y + v * w.x);
+          }
+        } else {
+          uint32_t y[4] = {b[j].x, b[j].y, b[j].z, b[j].w};
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const float4 w = *reinterpret_cast<const float4*>(&cs[pos * pairs + c * 8 + 2 * e]);
+            const float u0 = lo16(x[e]), u1 = hi16(x[e]), v0 = lo16(y[e]), v1 = hi16(y[e]);
+            x[e] = pack2(u0 * w.x - v0 * w.y, u1 * w.z - v1 * w.w);
+            y[e] = pack2(u0 * w.y + v0 * w.x, u1 * w.w + v1 * w.z);
+          }
+          *reinterpret_cast<uint4*>(dst[j] + pairs) = make_uint4(y[0], y[1], y[2], y[3]);
+        }
+        a[j] = make_uint4(x[0], x[1], x[2], x[3]);
+      }
+      *reinterpret_cast<uint4*>(dst[j]) = a[j];
+    }
+  }
+}
+
 }  // namespace
 }  // namespace tpk
 
@@ -104,5 +212,69 @@ extern "C" int tpk_rope_by_depth(const void* q_in, const void* k_in, void* q_out
       static_cast<const __nv_bfloat16*>(q_in), static_cast<const __nv_bfloat16*>(k_in),
       static_cast<__nv_bfloat16*>(q_out), static_cast<__nv_bfloat16*>(k_out), depth, F, q_in ? Hq : 0,
       k_in ? Hkv : 0, d, turns, inverse);
+  return cuda_status(cudaGetLastError());
+}
+
+extern "C" int tpk_rope_by_depth_ex(const void* q_in, int64_t ld_q, const void* k_in, int64_t ld_k, void* q_out,
+                                    int64_t ld_qo, void* k_out, int64_t ld_ko, const int32_t* depth, int64_t F,
+                                    int32_t Hq, int32_t Hkv, int32_t d, const tpk_rope_opts* opts, int32_t inverse,
+                                    void* stream) {
+  using namespace tpk;
+  if (F < 0 || Hq < 0 || Hkv < 0 || !opts || d < 16 || d > 512 || d % 8) return TPK_E_ARG;
+  const int rot = opts->rot;
+  if (rot < 16 || rot % 16 || rot > d || rot > 2 * kMostPairs || !opts->freqs || !std::isfinite(opts->factor) ||
+      (opts->interleaved & ~1))
+    return TPK_E_ARG;
+  if ((q_in == nullptr) != (q_out == nullptr) || (k_in == nullptr) != (k_out == nullptr)) return TPK_E_ARG;
+  if ((q_in && Hq <= 0) || (k_in && Hkv <= 0)) return TPK_E_ARG;
+  if (!aligned16(q_in) || !aligned16(k_in) || !aligned16(q_out) || !aligned16(k_out)) return TPK_E_ARG;
+  const int64_t wq = int64_t{Hq} * d, wk = int64_t{Hkv} * d;
+  if (q_in && (ld_q < wq || ld_qo < wq || ld_q % 8 || ld_qo % 8)) return TPK_E_ARG;
+  if (k_in && (ld_k < wk || ld_ko < wk || ld_k % 8 || ld_ko % 8)) return TPK_E_ARG;
+  if ((q_in && q_in == q_out && ld_q != ld_qo) || (k_in && k_in == k_out && ld_k != ld_ko)) return TPK_E_ARG;
+  Fractions fr{};
+  for (int i = 0; i < rot / 2; ++i) {
+    if (!std::isfinite(opts->freqs[i])) return TPK_E_ARG;
+    const double turns = opts->freqs[i] / 6.283185307179586476925286766559;
+    double frac = turns - std::floor(turns);          // whole turns per position turn nothing
+    if (frac >= 1.0) frac = 0.0;
+    // 64 bits of the fraction, 32 at a time (each step exact)
+    const double hi = std::floor(frac * 4294967296.0), lo = (frac * 4294967296.0 - hi) * 4294967296.0;
+    fr.v[i] = (static_cast<uint64_t>(hi) << 32) + static_cast<uint64_t>(lo + 0.5);
+  }
+  if (F == 0 || (!q_in && !k_in)) return TPK_OK;
+  if (!depth) return TPK_E_ARG;
+  if ((q_in ? Hq : 0) + int64_t{k_in ? Hkv : 0} > 65536) return TPK_E_UNSUPPORTED;
+  const int st = check_device();
+  if (st != TPK_OK) return st;
+  RopeRows p{};
+  p.q_in = static_cast<const __nv_bfloat16*>(q_in);
+  p.k_in = static_cast<const __nv_bfloat16*>(k_in);
+  p.q_out = static_cast<__nv_bfloat16*>(q_out);
+  p.k_out = static_cast<__nv_bfloat16*>(k_out);
+  p.ld_q = ld_q;
+  p.ld_k = ld_k;
+  p.ld_qo = ld_qo;
+  p.ld_ko = ld_ko;
+  p.depth = depth;
+  p.F = F;
+  p.Hq = q_in ? Hq : 0;
+  p.Hkv = k_in ? Hkv : 0;
+  p.D = d;
+  p.rot = rot;
+  p.factor = static_cast<float>(opts->factor);
+  p.sign = inverse ? -1.f : 1.f;
+  // as many positions as give every thread its pieces once
+  const bool inter = opts->interleaved != 0;
+  const int64_t per_pos = int64_t{p.Hq + p.Hkv} * ((inter ? rot / 8 : rot / 16) + (d - rot) / 8);
+  int64_t per = kThreads * kRowItems / per_pos;
+  p.per = static_cast<int32_t>(per < 1 ? 1 : per > kRowsMost ? kRowsMost : per);
+  const int64_t blocks = (F + p.per - 1) / p.per;
+  if (blocks > 0x7fffffff) return TPK_E_OVERFLOW;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  if (inter)
+    rope_rows_kernel<true><<<static_cast<unsigned>(blocks), kThreads, 0, s>>>(p, fr);
+  else
+    rope_rows_kernel<false><<<static_cast<unsigned>(blocks), kThreads, 0, s>>>(p, fr);
   return cuda_status(cudaGetLastError());
 }

@@ -882,3 +882,269 @@ def lm_loss_bwd(h, w, target, lse, dloss, scale=1.0, dh=None, dw=None, workspace
     _launch(dev, lib.tpk_lm_loss_bwd, *args, p_lse, p_dloss, p_dh, p_dw, N, V, C, float(scale), ws.data_ptr(),
             ws.nbytes, p_err)
     return dh, dw
+
+
+# ---- projections, feed-forward block, rotary positions, policy objective --------
+
+ACTIVATIONS = {"none": B.ACT_NONE, None: B.ACT_NONE, "silu": B.ACT_SILU, "gelu": B.ACT_GELU,
+               "gelu_tanh": B.ACT_GELU_TANH}
+
+
+def _activation(name):
+    if name not in ACTIVATIONS:
+        raise ValueError("act must be one of none, silu, gelu, gelu_tanh, got %r" % (name,))
+    return ACTIVATIONS[name]
+
+
+def _out_rows(t, shape, name, ref):
+    """(tensor, address, row stride) of a bf16 output whose rows may lie apart."""
+    if t is None:
+        t = torch.empty(shape, dtype=torch.bfloat16, device=ref.device)
+        return t, t.data_ptr(), shape[1]
+    return (t,) + _rows2(t, name, shape)
+
+
+def _linear_args(x, w, bias):
+    """(N, C, O, addresses and stride of x, w, bias), checked."""
+    N, C = _matrix(x, (torch.bfloat16,), "x")
+    O = _matrix(w, (torch.bfloat16,), "w")[0]
+    if O < 8 or O % 8:
+        raise ValueError("w must have a multiple of 8 rows, got %d" % O)
+    p_w = _arg(w, torch.bfloat16, (O, C), "w")
+    return (N, C, O) + _rows2(x, "x", (N, C)) + (p_w, None if bias is None else _arg(bias, torch.float32, (O,), "bias"))
+
+
+def linear(x, w, bias=None, act="none", residual=None, out=None, workspace=None, dev_err=None):
+    """Matrix product with bias, activation and residual (``tpk_linear``):
+    y = act(x @ w.T + bias) + residual.
+
+    x [N, C], w [O, C], residual [N, O] bf16, bias [O] fp32; rows of x, residual
+    and ``out`` may be strided (column slices).  act: none, silu, gelu or
+    gelu_tanh.  ``out`` may be ``residual``.  Returns y [N, O] bf16."""
+    lib = B.load()
+    N, C, O, p_x, ld_x, p_w, p_b = _linear_args(x, w, bias)
+    a = _activation(act)
+    p_r, ld_r = (None, O) if residual is None else _rows2(residual, "residual", (N, O))
+    given = out, workspace, dev_err
+    out, p_y, ld_y = _out_rows(out, (N, O), "out", x)
+    p_err = _dev_err(dev_err)
+    need = lib.tpk_linear_workspace_bytes(N, C, O, a, 0)
+    ws = _workspace(workspace, need, x, "the projection") if need or workspace is not None else None
+    dev = _device("x w bias residual out workspace dev_err", x, w, bias, residual, *given)
+    _launch(dev, lib.tpk_linear, p_x, ld_x, p_w, p_b, a, p_r, ld_r, p_y, ld_y, N, C, O,
+            None if ws is None else ws.data_ptr(), 0 if ws is None else ws.nbytes, p_err)
+    return out
+
+
+def linear_bwd(x, w, dy, bias=None, act="none", dx=None, dw=None, db=None, workspace=None, dev_err=None):
+    """Gradients of ``linear`` for the gradient dy of its result
+    (``tpk_linear_bwd``); x, w, bias, act as given to it.  The residual's
+    gradient is dy.  With an activation x @ w.T + bias is formed again.  dy and
+    ``dx`` may be column slices.  Returns (dx [N, C] bf16, dw [O, C] bf16,
+    db [O] fp32, None without a bias)."""
+    lib = B.load()
+    N, C, O, p_x, ld_x, p_w, p_b = _linear_args(x, w, bias)
+    a = _activation(act)
+    p_dy, ld_dy = _rows2(dy, "dy", (N, O))
+    if db is not None and bias is None:
+        raise ValueError("db is given, but not the bias it is the gradient of")
+    given = dx, dw, db, workspace, dev_err
+    dx, p_dx, ld_dx = _out_rows(dx, (N, C), "dx", x)
+    dw, p_dw = _out(dw, torch.bfloat16, (O, C), "dw", x)
+    db, p_db = (None, None) if bias is None else _out(db, torch.float32, (O,), "db", x)
+    p_err = _dev_err(dev_err)
+    ws = _workspace(workspace, lib.tpk_linear_workspace_bytes(N, C, O, a, 1), x, "the projection's backward")
+    dev = _device("x w dy bias dx dw db workspace dev_err", x, w, dy, bias, *given)
+    _launch(dev, lib.tpk_linear_bwd, p_x, ld_x, p_w, p_b, a, p_dy, ld_dy, p_dx, ld_dx, p_dw, p_db, N, C, O,
+            ws.data_ptr(), ws.nbytes, p_err)
+    return dx, dw, db
+
+
+def _ffn_args(x, w_in, w_out):
+    """(N, C, I, O, address and stride of x, addresses of the weights), checked."""
+    N, C = _matrix(x, (torch.bfloat16,), "x")
+    O, I = _matrix(w_out, (torch.bfloat16,), "w_out")
+    if O < 8 or O % 8:
+        raise ValueError("w_out must have a multiple of 8 rows, got %d" % O)
+    return (N, C, I, O) + _rows2(x, "x", (N, C)) + (_arg(w_in, torch.bfloat16, (2 * I, C), "w_in"),
+                                                     _arg(w_out, torch.bfloat16, (O, I), "w_out"))
+
+
+def gated_ffn(x, w_in, w_out, act="silu", residual=None, save=False, out=None, pre=None, a=None, workspace=None,
+              dev_err=None):
+    """Gated feed-forward block (``tpk_gated_ffn``):
+    y = (act(x @ w_in[:I].T) * (x @ w_in[I:].T)) @ w_out.T + residual.
+
+    x [N, C], w_in [2 I, C] (the gate's rows first), w_out [O, I], residual
+    [N, O] bf16; rows of x, residual and ``out`` may be strided; ``out`` may be
+    ``residual``.  Returns y [N, O]; with ``save`` (y, pre [N, 2 I], a [N, I]),
+    what ``gated_ffn_bwd`` needs."""
+    lib = B.load()
+    N, C, I, O, p_x, ld_x, p_in, p_out = _ffn_args(x, w_in, w_out)
+    k = _activation(act)
+    if not save and (pre is not None or a is not None):
+        raise ValueError("pre and a are written with save=True alone")
+    p_r, ld_r = (None, O) if residual is None else _rows2(residual, "residual", (N, O))
+    given = out, pre, a, workspace, dev_err
+    out, p_y, ld_y = _out_rows(out, (N, O), "out", x)
+    p_pre = p_a = None
+    if save:
+        pre, p_pre = _out(pre, torch.bfloat16, (N, 2 * I), "pre", x)
+        a, p_a = _out(a, torch.bfloat16, (N, I), "a", x)
+    p_err = _dev_err(dev_err)
+    ws = _workspace(workspace, lib.tpk_gated_ffn_workspace_bytes(N, C, I, O, 0), x, "the block")
+    dev = _device("x w_in w_out residual out pre a workspace dev_err", x, w_in, w_out, residual, *given)
+    _launch(dev, lib.tpk_gated_ffn, p_x, ld_x, p_in, p_out, k, p_r, ld_r, p_pre, p_a, p_y, ld_y, N, C, I, O,
+            ws.data_ptr(), ws.nbytes, p_err)
+    return (out, pre, a) if save else out
+
+
+def gated_ffn_bwd(x, w_in, w_out, dy, pre, a, act="silu", dx=None, dw_in=None, dw_out=None, workspace=None,
+                  dev_err=None):
+    """Gradients of ``gated_ffn`` for the gradient dy of its result
+    (``tpk_gated_ffn_bwd``); x, the weights and act as given to it, pre and a
+    as it saved them.  The residual's gradient is dy.  dy and ``dx`` may be
+    column slices.  Returns (dx [N, C], dw_in [2 I, C], dw_out [O, I]) bf16."""
+    lib = B.load()
+    N, C, I, O, p_x, ld_x, p_in, p_out = _ffn_args(x, w_in, w_out)
+    k = _activation(act)
+    p_dy, ld_dy = _rows2(dy, "dy", (N, O))
+    p_pre, p_a = _arg(pre, torch.bfloat16, (N, 2 * I), "pre"), _arg(a, torch.bfloat16, (N, I), "a")
+    given = dx, dw_in, dw_out, workspace, dev_err
+    dx, p_dx, ld_dx = _out_rows(dx, (N, C), "dx", x)
+    dw_in, p_din = _out(dw_in, torch.bfloat16, (2 * I, C), "dw_in", x)
+    dw_out, p_dout = _out(dw_out, torch.bfloat16, (O, I), "dw_out", x)
+    p_err = _dev_err(dev_err)
+    ws = _workspace(workspace, lib.tpk_gated_ffn_workspace_bytes(N, C, I, O, 1), x, "the block's backward")
+    dev = _device("x w_in w_out dy pre a dx dw_in dw_out workspace dev_err", x, w_in, w_out, dy, pre, a, *given)
+    _launch(dev, lib.tpk_gated_ffn_bwd, p_x, ld_x, p_in, p_out, k, p_dy, ld_dy, p_pre, p_a, p_dx, ld_dx, p_din, p_dout,
+            N, C, I, O, ws.data_ptr(), ws.nbytes, p_err)
+    return dx, dw_in, dw_out
+
+
+def rope_freqs(rot, base=1e4, stretch=1.0, trained=None, fast=32.0, slow=1.0):
+    """Radians per position of each of the rot / 2 pairs (float64), for
+    ``rope_by_depth_ex``: base^(-2i / rot), stretched for contexts ``stretch``
+    times as long as the model was trained on.  Without ``trained`` every
+    frequency is divided by stretch (positions interpolated); with ``trained``
+    (that context's length) pairs that turn ``fast`` times or more in it keep
+    theirs, those that turn ``slow`` times or less are divided, with a linear
+    ramp between."""
+    f = float(base) ** (-np.arange(0, rot, 2, dtype=np.float64) / rot)
+    if trained is None:
+        return f / stretch
+    if not fast > slow:
+        raise ValueError("fast must be above slow")
+    keep = np.clip((trained * f / (2.0 * np.pi) - slow) / (fast - slow), 0.0, 1.0)
+    return f * (keep + (1.0 - keep) / stretch)
+
+
+def _heads(t, name, shape=None):
+    """(address, row stride) of a 3-d bf16 tensor whose rows may lie apart."""
+    _rows3(t, name, shape)
+    n, h, d = t.shape
+    ld = t.stride(0) if n > 1 else h * d
+    if ld < h * d or ld % 8:
+        raise ValueError("%s: rows must not overlap and must lie a multiple of 8 elements apart" % name)
+    return t.data_ptr(), ld
+
+
+def rope_by_depth_ex(q, k, depth, freqs, interleaved=False, factor=1.0, inverse=False, q_out=None, k_out=None):
+    """RoPE at ``depth`` in its other forms (``tpk_rope_by_depth_ex``): either
+    pairing of channels (halves, or ``interleaved`` neighbours), in the first
+    ``2 * len(freqs)`` channels of a head, by ``depth * freqs`` radians
+    (``rope_freqs``), times ``factor``; the other channels are copied.
+    ``inverse``: the transpose, for gradients.
+
+    q [F, Hq, d], k [F, Hkv, d] bf16 (either may be None), rows may be strided
+    (column slices of a fused projection); depth int32 [F].  Returns
+    (q_out, k_out), new contiguous tensors unless given; ``q_out=q`` rotates in
+    place."""
+    lib = B.load()
+    if q is None and k is None:
+        return None, None
+    ref = q if q is not None else k
+    if not isinstance(ref, torch.Tensor) or ref.dim() != 3:
+        raise TypeError("q and k must be 3-d bf16 tensors")
+    F, _, d = ref.shape
+    fr = np.ascontiguousarray(freqs, dtype=np.float64)
+    if fr.ndim != 1 or not 8 <= len(fr) <= min(d // 2, 128) or len(fr) % 8:
+        raise ValueError("freqs must hold a multiple of 8 pairs, no more than half the head (or 128)")
+    if not np.isfinite(fr).all() or not math.isfinite(factor):
+        raise ValueError("freqs and factor must be finite")
+    if d % 8 or d > 512:
+        raise ValueError("heads must have a multiple of 8 channels, 512 at most, got %d" % d)
+    p_depth = _arg(depth, torch.int32, (F,), "depth")
+    given, at, heads = (q_out, k_out), [], []
+    outs = []
+    for t, o, name in ((q, q_out, "q"), (k, k_out, "k")):
+        if t is None:
+            if o is not None:
+                raise ValueError("%s_out is given, but not %s" % (name, name))
+            at.append((None, 0, None, 0))
+            heads.append(0)
+            outs.append(None)
+            continue
+        p_in, ld_in = _heads(t, name, (F, t.shape[1], d) if isinstance(t, torch.Tensor) and t.dim() == 3 else None)
+        if o is None:
+            o = torch.empty(t.shape, dtype=torch.bfloat16, device=t.device)
+        p_o, ld_o = _heads(o, name + "_out", tuple(t.shape))
+        if p_o == p_in and ld_o != ld_in:
+            raise ValueError("%s_out starts where %s does, with other rows" % (name, name))
+        at.append((p_in, ld_in, p_o, ld_o))
+        heads.append(t.shape[1])
+        outs.append(o)
+    dev = _device("depth q k q_out k_out", depth, q, k, *given)
+    opts = B.RopeOpts(2 * len(fr), 1 if interleaved else 0, float(factor), fr.ctypes.data)
+    _launch(dev, lib.tpk_rope_by_depth_ex, at[0][0], at[0][1], at[1][0], at[1][1], at[0][2], at[0][3], at[1][2], at[1][3],
+            p_depth, F, heads[0], heads[1], d, ctypes.byref(opts), 1 if inverse else 0)
+    return outs[0], outs[1]
+
+
+def policy_loss(loss, old_logp, advantage, weight, token_index, fwd_raw_begin, fwd_raw, ref_logp=None, clip_low=0.2,
+                clip_high=0.2, dual_clip=0.0, kl_coef=0.0, seq_offsets=None, stats=None, dloss=None, workspace=None):
+    """Clipped policy objective with a KL term over a packed batch, and its
+    gradient with respect to ``lm_loss``'s loss (``tpk_policy_loss``).
+
+    loss [F] fp32 (``lm_loss``: minus the log-probabilities); per raw token
+    old_logp, advantage, weight and optionally ref_logp [R] fp32 (a weight of 0:
+    no loss, nothing else of the token is read); token_index, fwd_raw_begin,
+    fwd_raw: a device plan's.  The ratio is a token's, or with ``seq_offsets``
+    (int32 [sequences + 1]) the geometric mean over its sequence.  clip_low,
+    clip_high: the ratio's band around 1; dual_clip > 1: the ratio's limit where
+    the advantage is negative; kl_coef: weight of exp(t) - t - 1, t = ref - logp.
+    Returns (stats, dloss): stats [5] fp32 = the objective, weighted sums of the
+    KL term, of the clipped tokens and of the ratio, the sum of weights; dloss
+    [F] fp32, for ``lm_loss_bwd``."""
+    lib = B.load()
+    f32, i32 = torch.float32, torch.int32
+    if not isinstance(loss, torch.Tensor) or not isinstance(old_logp, torch.Tensor):
+        raise TypeError("loss and old_logp must be tensors")
+    F, R = loss.numel(), old_logp.numel()
+    args = (_arg(loss, f32, (F,), "loss"), _arg(old_logp, f32, (R,), "old_logp"),
+            None if ref_logp is None else _arg(ref_logp, f32, (R,), "ref_logp"),
+            _arg(advantage, f32, (R,), "advantage"), _arg(weight, f32, (R,), "weight"),
+            _arg(token_index, i32, (R,), "token_index"), _arg(fwd_raw_begin, i32, (F + 1,), "fwd_raw_begin"),
+            _arg(fwd_raw, i32, (R,), "fwd_raw"))
+    if F > R:
+        raise ValueError("loss has %d positions, more than the %d raw tokens" % (F, R))
+    if not 0.0 <= clip_low <= 1.0 or not clip_high >= 0.0 or not (dual_clip == 0.0 or dual_clip > 1.0) or \
+            not 0.0 <= kl_coef < math.inf:
+        raise ValueError("clip_low must be in [0, 1], clip_high >= 0, dual_clip 0 or above 1, kl_coef >= 0")
+    seqs, p_seq = 0, None
+    if seq_offsets is not None:
+        seqs = seq_offsets.numel() - 1 if isinstance(seq_offsets, torch.Tensor) else 0
+        p_seq = _arg(seq_offsets, i32, (seqs + 1,), "seq_offsets")
+        if seqs < 1:
+            raise ValueError("seq_offsets must hold at least one sequence")
+    given = stats, dloss, workspace
+    stats, p_stats = _out(stats, f32, (5,), "stats", loss)
+    dloss, p_dloss = _out(dloss, f32, (F,), "dloss", loss)
+    ws = _workspace(workspace, lib.tpk_policy_loss_workspace_bytes(R, seqs), loss, "the objective")
+    dev = _device("loss old_logp advantage weight token_index fwd_raw_begin fwd_raw ref_logp seq_offsets stats dloss "
+                  "workspace", loss, old_logp, advantage, weight, token_index, fwd_raw_begin, fwd_raw, ref_logp,
+                  seq_offsets, *given)
+    opts = B.PolicyOpts(float(clip_low), float(clip_high), float(dual_clip), float(kl_coef))
+    _launch(dev, lib.tpk_policy_loss, *args, p_seq, seqs, ctypes.byref(opts), p_stats, p_dloss, R, F, ws.data_ptr(),
+            ws.nbytes)
+    return stats, dloss
