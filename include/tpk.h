@@ -710,25 +710,28 @@ int tpk_linear_bwd(const void* x, int64_t ld_x, const void* w, const float* bias
 /* Gated feed-forward block:
  *   g = x w_in[0:I]^T,  u = x w_in[I:2I]^T,  a = act(g) * u,  y = a w_out^T + residual
  *   x [N, C], w_in [2 I, C], w_out [O, I], residual, y [N, O] bf16
- *   pre [N, 2 I] (g | u) and a [N, I] bf16, contiguous: kept for the backward;
- *   pre NULL: not written; a NULL: in the workspace.
+ *   saved: tpk_gated_ffn_saved_bytes(N, I) bytes for the backward (g and u as
+ *   fp16, scaled by a power of two for every 32 channels of a row: 2^-11 of their
+ *   value); a [N, I] bf16, contiguous, for the backward too.  saved NULL: not
+ *   written; a NULL: in the workspace.
  * residual may be NULL; y may be residual itself.  C, I, O <= 32,768.
  *   workspace: tpk_gated_ffn_workspace_bytes(N, C, I, O, 0) bytes (less is
  *   needed where a is given). */
 size_t tpk_gated_ffn_workspace_bytes(int64_t N, int32_t C, int32_t I, int32_t O, int32_t backward);
+size_t tpk_gated_ffn_saved_bytes(int64_t N, int32_t I);
 int tpk_gated_ffn(const void* x, int64_t ld_x, const void* w_in, const void* w_out, int32_t act, const void* residual,
-                  int64_t ld_res, void* pre, void* a, void* y, int64_t ld_y, int64_t N, int32_t C, int32_t I,
+                  int64_t ld_res, void* saved, void* a, void* y, int64_t ld_y, int64_t N, int32_t C, int32_t I,
                   int32_t O, void* workspace, size_t ws_bytes, int32_t* dev_err, void* stream);
 
 /* Gradients of tpk_gated_ffn for the gradient dy of y (the residual's is dy):
  *   da = dy w_out,  dg = da u act'(g),  du = da act(g)
  *   dx = dg w_in[0:I] + du w_in[I:2I],  dw_in = (dg | du)^T x,  dw_out = dy^T a
- *   pre and a: the forward's, read only.  dx [N, C], dw_in [2 I, C], dw_out
+ *   saved and a: the forward's, read only.  dx [N, C], dw_in [2 I, C], dw_out
  *   [O, I] bf16, every row of the weights' gradients written (zeros for N = 0).
  *   workspace: tpk_gated_ffn_workspace_bytes(N, C, I, O, 1) bytes (dg | du,
  *   partial tiles). */
 int tpk_gated_ffn_bwd(const void* x, int64_t ld_x, const void* w_in, const void* w_out, int32_t act, const void* dy,
-                      int64_t ld_dy, const void* pre, const void* a, void* dx, int64_t ld_dx, void* dw_in,
+                      int64_t ld_dy, const void* saved, const void* a, void* dx, int64_t ld_dx, void* dw_in,
                       void* dw_out, int64_t N, int32_t C, int32_t I, int32_t O, void* workspace, size_t ws_bytes,
                       int32_t* dev_err, void* stream);
 

@@ -40,7 +40,7 @@ EXPORTS = [
     "tpk_block_norm", "tpk_block_norm_bwd_workspace_bytes", "tpk_block_norm_bwd",
     "tpk_lm_loss_workspace_bytes", "tpk_lm_loss", "tpk_lm_loss_bwd",
     "tpk_rope_by_depth_ex", "tpk_linear_workspace_bytes", "tpk_linear", "tpk_linear_bwd",
-    "tpk_gated_ffn_workspace_bytes", "tpk_gated_ffn", "tpk_gated_ffn_bwd",
+    "tpk_gated_ffn_workspace_bytes", "tpk_gated_ffn_saved_bytes", "tpk_gated_ffn", "tpk_gated_ffn_bwd",
     "tpk_policy_loss_workspace_bytes", "tpk_policy_loss",
     "tpk_status_string",
     "tpk_version",
@@ -154,6 +154,8 @@ def _sig(lib):
     lib.tpk_linear_bwd.argtypes = [P, I64, P, P, I32, P, I64, P, I64, P, P, I64, I32, I32, P, SZ, P, P]
     lib.tpk_gated_ffn_workspace_bytes.argtypes = [I64, I32, I32, I32, I32]
     lib.tpk_gated_ffn_workspace_bytes.restype = SZ
+    lib.tpk_gated_ffn_saved_bytes.argtypes = [I64, I32]
+    lib.tpk_gated_ffn_saved_bytes.restype = SZ
     lib.tpk_gated_ffn.argtypes = [P, I64, P, P, I32, P, I64, P, P, P, I64, I64, I32, I32, I32, P, SZ, P, P]
     lib.tpk_gated_ffn_bwd.argtypes = [P, I64, P, P, I32, P, I64, P, P, P, I64, P, P, I64, I32, I32, I32, P, SZ, P, P]
     lib.tpk_policy_loss_workspace_bytes.argtypes = [I64, I32]

@@ -1,6 +1,6 @@
 // Activations of the projections and the feed-forward block, and their
-// derivatives, in fp32 (include/tpk.h, TPK_ACT_*).
-//   silu       z s,  s = 1 / (1 + e^-z)            s (1 + z (1 - s))
+// derivatives, in fp32 on packed pairs (include/tpk.h, TPK_ACT_*).
+//   silu       z s,  s = 1 / (1 + e^-z)            s + z s (1 - s)
 //   gelu       z Phi(z)                            Phi(z) + z phi(z)
 //   gelu_tanh  z s(k (z + c z^3)), k = 2 sqrt(2 / pi), c = 0.044715
 //              (0.5 (1 + tanh t) = s(2 t): no difference of close numbers)
@@ -8,7 +8,9 @@
 // x >= 0 (Abramowitz and Stegun, Handbook of Mathematical Functions, 7.1.26):
 // within 1.5e-7, far inside the results' bf16 rounding, at a third of the
 // instructions of the full-precision function, and the derivative shares the
-// exponential.
+// exponential.  An epilogue does 32,768 of these per tile and CTA while the
+// tensor pipe needs 256 cycles per 64 elements of K, so instructions count: two
+// values per instruction wherever there is a packed form.
 #pragma once
 #include "ptx.cuh"
 #include "tpk.h"
@@ -16,65 +18,85 @@
 namespace tpk {
 
 constexpr float kActLog2e = 1.4426950408889634f;
+constexpr float kTanhK = 1.5957691216057308f;   // 2 sqrt(2 / pi)
 
-__device__ __forceinline__ float sigmoid_of(float z) { return __fdividef(1.f, 1.f + ptx::ex2(-z * kActLog2e)); }
-
-// (erfc(|z| / sqrt 2), e^{-z^2 / 2})
-__device__ __forceinline__ void tail_of(float z, float& q, float& e) {
-  const float x = fabsf(z) * 0.70710678118654752f;
-  const float t = __fdividef(1.f, fmaf(0.3275911f, x, 1.f));
-  e = ptx::ex2(z * z * (-0.5f * kActLog2e));
-  float p = fmaf(t, 1.061405429f, -1.453152027f);
-  p = fmaf(t, p, 1.421413741f);
-  p = fmaf(t, p, -0.284496736f);
-  p = fmaf(t, p, 0.254829592f);
-  q = p * t * e;
+__device__ __forceinline__ uint64_t both(float v) { return ptx::f2(v, v); }
+__device__ __forceinline__ uint64_t ex2_2(uint64_t v) {
+  float a, b;
+  ptx::unf2(v, a, b);
+  return ptx::f2(ptx::ex2(a), ptx::ex2(b));
 }
-
-__device__ __forceinline__ float tanh_arg(float z) {
-  constexpr float k = 1.5957691216057308f;   // 2 sqrt(2 / pi)
-  return z * fmaf(0.044715f * k, z * z, k);
+__device__ __forceinline__ uint64_t rcp_2(uint64_t v) {
+  float a, b;
+  ptx::unf2(v, a, b);
+  return ptx::f2(ptx::rcp(a), ptx::rcp(b));
+}
+__device__ __forceinline__ uint64_t sigmoid_2(uint64_t z) {
+  return rcp_2(ptx::add2(ex2_2(ptx::mul2(z, both(-kActLog2e))), both(1.f)));
+}
+// k (z + c z^3)
+__device__ __forceinline__ uint64_t tanh_arg_2(uint64_t z, uint64_t zz) {
+  return ptx::mul2(z, ptx::fma2(zz, both(0.044715f * kTanhK), both(kTanhK)));
+}
+// Phi(z); e^{-z^2 / 2} in e
+__device__ __forceinline__ uint64_t phi_2(uint64_t z, uint64_t& e) {
+  constexpr uint64_t kSign = 0x8000000080000000ull;
+  const uint64_t x = z & ~kSign;
+  const uint64_t t = rcp_2(ptx::fma2(x, both(0.3275911f * 0.70710678118654752f), both(1.f)));
+  e = ex2_2(ptx::mul2(ptx::mul2(z, z), both(-0.5f * kActLog2e)));
+  uint64_t p = ptx::fma2(t, both(1.061405429f), both(-1.453152027f));
+  p = ptx::fma2(t, p, both(1.421413741f));
+  p = ptx::fma2(t, p, both(-0.284496736f));
+  p = ptx::fma2(t, p, both(0.254829592f));
+  const uint64_t q = ptx::mul2(ptx::mul2(p, t), e);               // erfc(|z| / sqrt 2)
+  const uint64_t w = ptx::fma2(q, both(-0.5f), both(0.5f));       // |Phi - 1/2|
+  return ptx::add2(w | (z & kSign), both(0.5f));
+}
+// A square that a factor of zero may meet: finite.
+__device__ __forceinline__ uint64_t square_2(uint64_t z) {
+  float a, b;
+  ptx::unf2(ptx::mul2(z, z), a, b);
+  return ptx::f2(fminf(a, 1e36f), fminf(b, 1e36f));
 }
 
 template <int kAct>
-__device__ __forceinline__ float act_of(float z) {
-  if constexpr (kAct == TPK_ACT_SILU) return z * sigmoid_of(z);
+__device__ __forceinline__ uint64_t act_2(uint64_t z) {
+  if constexpr (kAct == TPK_ACT_SILU) return ptx::mul2(z, sigmoid_2(z));
   if constexpr (kAct == TPK_ACT_GELU) {
-    float q, e;
-    tail_of(z, q, e);
-    const float h = q == 0.f ? 0.f : 0.5f * z * q;   // (an infinite z has no product with 0)
-    return z > 0.f ? z - h : h;
+    uint64_t e;
+    return ptx::mul2(z, phi_2(z, e));
   }
-  if constexpr (kAct == TPK_ACT_GELU_TANH) return z * sigmoid_of(tanh_arg(z));
+  if constexpr (kAct == TPK_ACT_GELU_TANH) return ptx::mul2(z, sigmoid_2(tanh_arg_2(z, ptx::mul2(z, z))));
   return z;
 }
 
 // act(z), and its derivative in `slope`.
 template <int kAct>
-__device__ __forceinline__ float act_slope(float z, float& slope) {
+__device__ __forceinline__ uint64_t act_slope_2(uint64_t z, uint64_t& slope) {
+  const uint64_t one = both(1.f), minus = both(-1.f);
   if constexpr (kAct == TPK_ACT_SILU) {
-    const float s = sigmoid_of(z);
-    slope = s * fmaf(z, 1.f - s, 1.f);
-    return z * s;
+    const uint64_t s = sigmoid_2(z), v = ptx::mul2(z, s);
+    slope = ptx::fma2(v, ptx::fma2(s, minus, one), s);
+    return v;
   }
   if constexpr (kAct == TPK_ACT_GELU) {
-    float q, e;
-    tail_of(z, q, e);
-    const float h = 0.5f * q, phi = z > 0.f ? 1.f - h : h;
-    slope = fmaf(z * e, 0.39894228040143268f, phi);   // 1 / sqrt(2 pi)
-    return z * phi;
+    uint64_t e;
+    const uint64_t phi = phi_2(z, e);
+    slope = ptx::fma2(ptx::mul2(z, e), both(0.39894228040143268f), phi);   // 1 / sqrt(2 pi)
+    return ptx::mul2(z, phi);
   }
   if constexpr (kAct == TPK_ACT_GELU_TANH) {
-    const float s = sigmoid_of(tanh_arg(z)), t = s * (1.f - s);
-    constexpr float k = 1.5957691216057308f;
-    slope = t == 0.f ? s : fmaf(z * t, fmaf(3.f * 0.044715f * k, z * z, k), s);   // far out z^2 has no value
-    return z * s;
+    const uint64_t zz = square_2(z);
+    const uint64_t s = sigmoid_2(tanh_arg_2(z, zz)), v = ptx::mul2(z, s);
+    const uint64_t d = ptx::fma2(zz, both(3.f * 0.044715f * kTanhK), both(kTanhK));
+    slope = ptx::fma2(ptx::mul2(v, ptx::fma2(s, minus, one)), d, s);
+    return v;
   }
-  slope = 1.f;
+  slope = one;
   return z;
 }
 
-// body(integral_constant<act>): one copy of an epilogue's arithmetic per activation.
+// body(tag of the activation): one copy of an epilogue's arithmetic per activation.
 template <int kAct>
 struct ActTag {
   static constexpr int value = kAct;

@@ -36,7 +36,6 @@ struct FewParams {
   int64_t ld_res;
   __nv_bfloat16* y;
   int64_t ld_y;
-  __nv_bfloat16* pre;        // gated: nullptr, or [N, 2 O]
   int32_t* err;
 };
 
@@ -164,19 +163,14 @@ __global__ void __launch_bounds__(kFewThreads) few_kernel(const __grid_constant_
         u.x += e.x; u.y += e.y; u.z += e.z; u.w += e.w;
       }
     }
-    if (kGated) {
-      if (p.pre) {
-        __nv_bfloat16* g = p.pre + static_cast<int64_t>(t) * 2 * p.O + o;
-        *reinterpret_cast<uint2*>(g) = make_uint2(pack2(v.x, v.y), pack2(v.z, v.w));
-        *reinterpret_cast<uint2*>(g + p.O) = make_uint2(pack2(u.x, u.y), pack2(u.z, u.w));
-      }
-    } else if (p.bias) {
+    if (!kGated && p.bias) {
       const float4 b = __ldg(reinterpret_cast<const float4*>(p.bias + o));
       v.x += b.x; v.y += b.y; v.z += b.z; v.w += b.w;
     }
     with_act(p.act, [&](auto k) {
       constexpr int kAct = decltype(k)::value;
-      v = make_float4(act_of<kAct>(v.x), act_of<kAct>(v.y), act_of<kAct>(v.z), act_of<kAct>(v.w));
+      ptx::unf2(act_2<kAct>(ptx::f2(v.x, v.y)), v.x, v.y);
+      ptx::unf2(act_2<kAct>(ptx::f2(v.z, v.w)), v.z, v.w);
     });
     if (kGated) {
       v.x *= u.x; v.y *= u.y; v.z *= u.z; v.w *= u.w;
@@ -253,8 +247,7 @@ int few_linear(const Mat& x, const Mat& w, const float* bias, int act, const Mat
   return few_dispatch<false>(x, m, p, after, s);
 }
 
-int few_gate(const Mat& x, const Mat& w_gate, const Mat& w_up, int act, const Mat& a, __nv_bfloat16* pre, int32_t* err,
-             cudaStream_t s) {
+int few_gate(const Mat& x, const Mat& w_gate, const Mat& w_up, int act, const Mat& a, int32_t* err, cudaStream_t s) {
   FewMaps m;
   int st = map_of(&m.w, w_gate, 64);
   if (st == TPK_OK) st = map_of(&m.w2, w_up, 64);
@@ -266,7 +259,6 @@ int few_gate(const Mat& x, const Mat& w_gate, const Mat& w_up, int act, const Ma
   p.act = act;
   p.y = static_cast<__nv_bfloat16*>(const_cast<void*>(a.p));
   p.ld_y = a.ld;
-  p.pre = pre;
   p.err = err;
   return few_dispatch<true>(x, m, p, false, s);
 }

@@ -12,9 +12,8 @@ constexpr int kFewRows = 64;   // rows; see few.cu
 // stream's last kernel, which lets this one start early.
 int few_linear(const Mat& x, const Mat& w, const float* bias, int act, const Mat& residual, const Mat& y, bool after,
                int32_t* err, cudaStream_t s);
-// a = act(g) u, g = x w_gate^T, u = x w_up^T; g and u kept in pre (its columns [0, I), [I, 2 I)) unless nullptr
-int few_gate(const Mat& x, const Mat& w_gate, const Mat& w_up, int act, const Mat& a, __nv_bfloat16* pre, int32_t* err,
-             cudaStream_t s);
+// a = act(g) u, g = x w_gate^T, u = x w_up^T
+int few_gate(const Mat& x, const Mat& w_gate, const Mat& w_up, int act, const Mat& a, int32_t* err, cudaStream_t s);
 
 }  // namespace product
 }  // namespace tpk

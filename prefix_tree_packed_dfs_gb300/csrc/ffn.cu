@@ -6,8 +6,8 @@
 // tile of the accumulator holds g and u of the same channels, and only a (and,
 // for training, g and u) leaves it.  The backward's first kernel forms da and
 // takes it straight to dg and du; da is never stored.
-// g, u, a, dg and du are kept in bf16, as the operands of their products are:
-// a rounding of 2^-9 each, on sums that round to bf16 themselves.
+// a, dg and du are rounded to bf16, as operands of their products; g and u are
+// kept for the backward as scaled fp16 (product.cuh).
 #include "few.cuh"
 
 namespace tpk {
@@ -57,12 +57,22 @@ Params params(int64_t M, int64_t N, int64_t K, int act, int32_t* err) {
   p.N = static_cast<int32_t>(N);
   p.K = static_cast<int32_t>(K);
   p.splits = 1;
+  p.whole = INT32_MAX;   // nothing is split
   p.act = act;
   p.err = err;
   return p;
 }
 
 const __nv_bfloat16* bf(const void* p) { return static_cast<const __nv_bfloat16*>(p); }
+
+// What the forward keeps: g and u side by side, 16 bits each, [N, 2 I], then the exponents.
+struct Saved {
+  Mat g, u;
+  uint8_t* exps;
+};
+Saved saved_of(void* p, int64_t N, int64_t I) {
+  return Saved{Mat{p, N, I, 2 * I}, Mat{bf(p) + I, N, I, 2 * I}, static_cast<uint8_t*>(p) + N * 4 * I};
+}
 
 }  // namespace
 }  // namespace product
@@ -74,8 +84,14 @@ extern "C" size_t tpk_gated_ffn_workspace_bytes(int64_t N, int32_t C, int32_t I,
   return carve(nullptr, N, C, I, O, backward != 0, false, nullptr);
 }
 
+extern "C" size_t tpk_gated_ffn_saved_bytes(int64_t N, int32_t I) {
+  using namespace tpk::product;
+  if (!sizes_ok(N, 8, I, 8) || I > kMostK) return 0;
+  return static_cast<size_t>(N) * 4 * I + exp_bytes(N, I);
+}
+
 extern "C" int tpk_gated_ffn(const void* x, int64_t ld_x, const void* w_in, const void* w_out, int32_t act,
-                             const void* residual, int64_t ld_res, void* pre, void* a, void* y, int64_t ld_y, int64_t N,
+                             const void* residual, int64_t ld_res, void* saved, void* a, void* y, int64_t ld_y, int64_t N,
                              int32_t C, int32_t I, int32_t O, void* workspace, size_t ws_bytes, int32_t* dev_err,
                              void* stream) {
   using namespace tpk;
@@ -86,7 +102,7 @@ extern "C" int tpk_gated_ffn(const void* x, int64_t ld_x, const void* w_in, cons
   if (!tiles_ok(N, C, I, O)) return TPK_E_OVERFLOW;
   if (N == 0) return TPK_OK;
   if (!x || !w_in || !w_out || !y || !aligned16(x) || !aligned16(w_in) || !aligned16(w_out) || !aligned16(y) ||
-      !aligned16(residual) || !aligned16(pre) || !aligned16(a))
+      !aligned16(residual) || !aligned16(saved) || !aligned16(a))
     return TPK_E_ARG;
   FfnWork k;
   const size_t need = carve(static_cast<uint8_t*>(workspace), N, C, I, O, false, a != nullptr, &k);
@@ -96,8 +112,8 @@ extern "C" int tpk_gated_ffn(const void* x, int64_t ld_x, const void* w_in, cons
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   const Mat mx{x, N, C, ld_x}, gate{w_in, I, C, C}, up{bf(w_in) + int64_t{I} * C, I, C, C}, down{w_out, O, I, I};
   const Mat ma{a ? a : k.a, N, I, I}, res{residual, N, O, ld_res}, my{y, N, O, ld_y};
-  if (N <= kFewRows) {
-    st = few_gate(mx, gate, up, act, ma, static_cast<__nv_bfloat16*>(pre), dev_err, s);
+  if (N <= kFewRows && !saved) {
+    st = few_gate(mx, gate, up, act, ma, dev_err, s);
     return st == TPK_OK ? few_linear(ma, down, nullptr, TPK_ACT_NONE, res, my, true, dev_err, s) : st;
   }
   Maps m;
@@ -105,17 +121,20 @@ extern "C" int tpk_gated_ffn(const void* x, int64_t ld_x, const void* w_in, cons
   if (st == TPK_OK) st = map_of(&m.b, gate, kHalf);
   if (st == TPK_OK) st = map_of(&m.b2, up, kHalf);
   if (st == TPK_OK) st = map_of(&m.out, ma, kHalf);
-  if (st == TPK_OK && pre) st = map_of(&m.out2, Mat{pre, N, I, 2 * int64_t{I}}, kHalf);
-  if (st == TPK_OK && pre) st = map_of(&m.out3, Mat{bf(pre) + I, N, I, 2 * int64_t{I}}, kHalf);
+  const Saved k16 = saved_of(saved, N, I);
+  if (st == TPK_OK && saved) st = map_of(&m.out2, k16.g, kHalf);
+  if (st == TPK_OK && saved) st = map_of(&m.out3, k16.u, kHalf);
   if (st != TPK_OK) return st;
   Params p = params(N, I, C, act, dev_err);
-  p.save = pre != nullptr;
-  st = launch<kGate, true>(m, p, s);
-  return st == TPK_OK ? linear_product(ma, down, nullptr, TPK_ACT_NONE, res, my, k.acc, dev_err, s) : st;
+  p.save = saved != nullptr;
+  p.exps = k16.exps;
+  p.exp_rows = exp_rows(N);
+  st = launch<kGate, true>(m, p, false, s);
+  return st == TPK_OK ? linear_product(ma, down, nullptr, TPK_ACT_NONE, res, my, k.acc, true, dev_err, s) : st;
 }
 
 extern "C" int tpk_gated_ffn_bwd(const void* x, int64_t ld_x, const void* w_in, const void* w_out, int32_t act,
-                                 const void* dy, int64_t ld_dy, const void* pre, const void* a, void* dx, int64_t ld_dx,
+                                 const void* dy, int64_t ld_dy, const void* saved, const void* a, void* dx, int64_t ld_dx,
                                  void* dw_in, void* dw_out, int64_t N, int32_t C, int32_t I, int32_t O, void* workspace,
                                  size_t ws_bytes, int32_t* dev_err, void* stream) {
   using namespace tpk;
@@ -133,8 +152,8 @@ extern "C" int tpk_gated_ffn_bwd(const void* x, int64_t ld_x, const void* w_in, 
     if (st == TPK_OK) st = cuda_status(cudaMemsetAsync(dw_out, 0, static_cast<size_t>(2) * O * I, s));
     return st;
   }
-  if (!x || !w_in || !w_out || !dy || !pre || !a || !dx || !aligned16(x) || !aligned16(w_in) || !aligned16(w_out) ||
-      !aligned16(dy) || !aligned16(pre) || !aligned16(a) || !aligned16(dx))
+  if (!x || !w_in || !w_out || !dy || !saved || !a || !dx || !aligned16(x) || !aligned16(w_in) || !aligned16(w_out) ||
+      !aligned16(dy) || !aligned16(saved) || !aligned16(a) || !aligned16(dx))
     return TPK_E_ARG;
   FfnWork k;
   if (!workspace || reinterpret_cast<uintptr_t>(workspace) % 256 ||
@@ -147,14 +166,18 @@ extern "C" int tpk_gated_ffn_bwd(const void* x, int64_t ld_x, const void* w_in, 
   Maps m;
   st = map_of(&m.a, mdy, kHalf);
   if (st == TPK_OK) st = map_of(&m.b, Mat{w_out, O, I, I}, 64);
-  if (st == TPK_OK) st = map_of(&m.in, Mat{pre, N, I, wide}, kHalf, 32);
-  if (st == TPK_OK) st = map_of(&m.in2, Mat{bf(pre) + I, N, I, wide}, kHalf, 32);
+  const Saved k16 = saved_of(const_cast<void*>(saved), N, I);
+  if (st == TPK_OK) st = map_of(&m.in, k16.g, kHalf, 32);
+  if (st == TPK_OK) st = map_of(&m.in2, k16.u, kHalf, 32);
   if (st == TPK_OK) st = map_of(&m.out, Mat{k.dgu, N, I, wide}, kHalf, 32);
   if (st == TPK_OK) st = map_of(&m.out2, Mat{k.dgu + I, N, I, wide}, kHalf, 32);
-  if (st == TPK_OK) st = launch<kGateBwd, true>(m, params(N, I, O, act, dev_err), s);
+  Params p = params(N, I, O, act, dev_err);
+  p.exps = k16.exps;
+  p.exp_rows = exp_rows(N);
+  if (st == TPK_OK) st = launch<kGateBwd, true>(m, p, false, s);
   const Mat dgu{k.dgu, N, wide, wide};
-  if (st == TPK_OK) st = input_product(dgu, Mat{w_in, wide, C, C}, Mat{dx, N, C, ld_dx}, k.acc, dev_err, s);
-  if (st == TPK_OK) st = weight_product(dgu, mx, Mat{dw_in, wide, C, C}, k.acc, dev_err, s);
-  if (st == TPK_OK) st = weight_product(mdy, Mat{a, N, I, I}, Mat{dw_out, O, I, I}, k.acc, dev_err, s);
+  if (st == TPK_OK) st = input_product(dgu, Mat{w_in, wide, C, C}, Mat{dx, N, C, ld_dx}, k.acc, true, dev_err, s);
+  if (st == TPK_OK) st = weight_product(dgu, mx, Mat{dw_in, wide, C, C}, k.acc, true, dev_err, s);
+  if (st == TPK_OK) st = weight_product(mdy, Mat{a, N, I, I}, Mat{dw_out, O, I, I}, k.acc, true, dev_err, s);
   return st;
 }

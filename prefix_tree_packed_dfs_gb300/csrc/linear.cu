@@ -39,6 +39,8 @@ template <typename T>
 __global__ void __launch_bounds__(kSumThreads) column_sum_kernel(const T* __restrict__ m, int64_t rows, int cols,
                                                                  int64_t ld, int64_t per, float* __restrict__ out) {
   __shared__ float4 part[8][32][2];
+  ptx::dependents_launch();
+  ptx::dependency_wait();
   const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
   const int c = blockIdx.x * kSumCols + lane * 8;
   const int64_t lo = static_cast<int64_t>(blockIdx.y) * per, hi = lo + per < rows ? lo + per : rows;
@@ -74,70 +76,82 @@ int64_t sum_blocks(int64_t rows, int64_t cols) {
 }
 
 template <typename T>
-int column_sums(const T* m, int64_t rows, int64_t cols, int64_t ld, float* part, float* out, cudaStream_t s) {
+int column_sums(const T* m, int64_t rows, int64_t cols, int64_t ld, float* part, float* out, bool after,
+                cudaStream_t s) {
   const unsigned across = static_cast<unsigned>((cols + kSumCols - 1) / kSumCols);
   const int64_t per = sum_rows(rows, cols), blocks = sum_blocks(rows, cols);
-  float* to = blocks == 1 ? out : part;
-  column_sum_kernel<T><<<dim3(across, static_cast<unsigned>(blocks)), kSumThreads, 0, s>>>(
-      m, rows, static_cast<int>(cols), ld, per, to);
-  if (blocks > 1)
-    column_sum_kernel<float><<<dim3(across, 1), kSumThreads, 0, s>>>(part, blocks, static_cast<int>(cols), cols, blocks,
-                                                                     out);
-  return cuda_status(cudaGetLastError());
+  const int n = static_cast<int>(cols);
+  const int st = launch_kernel(column_sum_kernel<T>, dim3(across, static_cast<unsigned>(blocks)), kSumThreads, 0, after,
+                               s, m, rows, n, ld, per, blocks == 1 ? out : part);
+  if (st != TPK_OK || blocks == 1) return st;
+  return launch_kernel(column_sum_kernel<float>, dim3(across), kSumThreads, 0, true, s, static_cast<const float*>(part),
+                       blocks, n, cols, blocks, out);
 }
 
 // The sum of a split product's partial tiles, 8 columns per thread, and kLin's
-// epilogue.
-__global__ void __launch_bounds__(256) join_kernel(const float* __restrict__ acc, int M, int N, int splits,
+// epilogue.  residual may be out.
+__global__ void __launch_bounds__(256) join_kernel(const float* __restrict__ acc, int M, int N, int whole, int splits,
                                                    const float* __restrict__ bias, int act,
-                                                   const __nv_bfloat16* residual, int64_t ld_res,
-                                                   __nv_bfloat16* out, int64_t ld_out) {
-  const int nt = (N + kTile - 1) / kTile;
-  const int64_t step = static_cast<int64_t>((M + kTile - 1) / kTile) * nt * (kTile * kTile);
-  const int vecs = N / 8;
-  const int64_t items = static_cast<int64_t>(M) * vecs;
+                                                   const __nv_bfloat16* residual, int64_t ld_res, __nv_bfloat16* out,
+                                                   int64_t ld_out) {
+  ptx::dependents_launch();
+  ptx::dependency_wait();
+  const int mt = (M + kTile - 1) / kTile, nt = (N + kTile - 1) / kTile, tail = mt * nt - whole;
+  const int64_t step = static_cast<int64_t>(tail) * (kTile * kTile);
+  const int64_t items = static_cast<int64_t>(tail) * (kTile * kTile / 8);
   for (int64_t it = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x; it < items;
        it += static_cast<int64_t>(gridDim.x) * 256) {
-    const int64_t r = it / vecs;
-    const int col = static_cast<int>(it - r * vecs) * 8;
-    const float* from = acc + ((r / kTile) * nt + col / kTile) * (kTile * kTile) + (r % kTile) * kTile + col % kTile;
-    float v[8] = {};
+    int m, n;
+    place_of(mt, nt, whole + static_cast<int>(it / (kTile * kTile / 8)), m, n);
+    const int64_t r = static_cast<int64_t>(m) * kTile + it / (kTile / 8) % kTile;
+    const int col = n * kTile + static_cast<int>(it % (kTile / 8)) * 8;
+    if (r >= M || col >= N) continue;
+    const float* from = acc + it * 8;
+    float4 x = make_float4(0.f, 0.f, 0.f, 0.f), y = x;
 #pragma unroll 4
     for (int s = 0; s < splits; ++s) {
-      const float4 x = __ldcg(reinterpret_cast<const float4*>(from + s * step));
-      const float4 y = __ldcg(reinterpret_cast<const float4*>(from + s * step) + 1);
-      v[0] += x.x; v[1] += x.y; v[2] += x.z; v[3] += x.w;
-      v[4] += y.x; v[5] += y.y; v[6] += y.z; v[7] += y.w;
+      const float4 a = __ldcg(reinterpret_cast<const float4*>(from + s * step));
+      const float4 b = __ldcg(reinterpret_cast<const float4*>(from + s * step) + 1);
+      x.x += a.x; x.y += a.y; x.z += a.z; x.w += a.w;
+      y.x += b.x; y.y += b.y; y.z += b.z; y.w += b.w;
     }
+    uint64_t v[4] = {ptx::f2(x.x, x.y), ptx::f2(x.z, x.w), ptx::f2(y.x, y.y), ptx::f2(y.z, y.w)};
     if (bias) {
-      const float4 x = __ldg(reinterpret_cast<const float4*>(bias + col));
-      const float4 y = __ldg(reinterpret_cast<const float4*>(bias + col) + 1);
-      v[0] += x.x; v[1] += x.y; v[2] += x.z; v[3] += x.w;
-      v[4] += y.x; v[5] += y.y; v[6] += y.z; v[7] += y.w;
+      const ulonglong2 a = __ldg(reinterpret_cast<const ulonglong2*>(bias + col));
+      const ulonglong2 b = __ldg(reinterpret_cast<const ulonglong2*>(bias + col) + 1);
+      v[0] = ptx::add2(v[0], a.x);
+      v[1] = ptx::add2(v[1], a.y);
+      v[2] = ptx::add2(v[2], b.x);
+      v[3] = ptx::add2(v[3], b.y);
     }
     if (act != TPK_ACT_NONE)
       with_act(act, [&](auto t) {
 #pragma unroll
-        for (int e = 0; e < 8; ++e) v[e] = act_of<decltype(t)::value>(v[e]);
+        for (int e = 0; e < 4; ++e) v[e] = act_2<decltype(t)::value>(v[e]);
       });
     if (residual) {
       const uint4 q = *reinterpret_cast<const uint4*>(residual + r * ld_res + col);
-      v[0] += lo16(q.x); v[1] += hi16(q.x); v[2] += lo16(q.y); v[3] += hi16(q.y);
-      v[4] += lo16(q.z); v[5] += hi16(q.z); v[6] += lo16(q.w); v[7] += hi16(q.w);
+      const uint32_t w[4] = {q.x, q.y, q.z, q.w};
+#pragma unroll
+      for (int e = 0; e < 4; ++e) v[e] = ptx::add2(v[e], ptx::f2(lo16(w[e]), hi16(w[e])));
     }
-    *reinterpret_cast<uint4*>(out + r * ld_out + col) =
-        make_uint4(pack2(v[0], v[1]), pack2(v[2], v[3]), pack2(v[4], v[5]), pack2(v[6], v[7]));
+    uint32_t o[4];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      float lo, hi;
+      ptx::unf2(v[e], lo, hi);
+      o[e] = ptx::pack_bf16x2(lo, hi);
+    }
+    *reinterpret_cast<uint4*>(out + r * ld_out + col) = make_uint4(o[0], o[1], o[2], o[3]);
   }
 }
 
-int join(const float* acc, int64_t M, int64_t N, int splits, const float* bias, int act, const Mat& residual,
-         const Mat& out, cudaStream_t s) {
-  const int64_t blocks = (M * (N / 8) + 255) / 256, most = int64_t{num_sms()} * 16;
-  join_kernel<<<static_cast<unsigned>(blocks < most ? blocks : most), 256, 0, s>>>(
-      acc, static_cast<int>(M), static_cast<int>(N), splits, bias, act,
-      static_cast<const __nv_bfloat16*>(residual.p), residual.ld, static_cast<__nv_bfloat16*>(const_cast<void*>(out.p)),
-      out.ld);
-  return cuda_status(cudaGetLastError());
+int join(const Params& p, const float* bias, int act, const Mat& residual, const Mat& out, cudaStream_t s) {
+  const int64_t blocks = (tiles_of(p.M, p.N) - p.whole) * (kTile / 8), most = int64_t{num_sms()} * 16;
+  return launch_kernel(join_kernel, dim3(static_cast<unsigned>(blocks < most ? blocks : most)), 256, 0, true, s,
+                       static_cast<const float*>(p.acc), p.M, p.N, p.whole, p.splits, bias, act,
+                       static_cast<const __nv_bfloat16*>(residual.p), residual.ld,
+                       static_cast<__nv_bfloat16*>(const_cast<void*>(out.p)), out.ld);
 }
 
 Params params(int64_t M, int64_t N, int64_t K, bool split, float* acc, int32_t* err) {
@@ -145,10 +159,17 @@ Params params(int64_t M, int64_t N, int64_t K, bool split, float* acc, int32_t* 
   p.M = static_cast<int32_t>(M);
   p.N = static_cast<int32_t>(N);
   p.K = static_cast<int32_t>(K);
-  p.splits = split ? splits_for(tiles_of(M, N), (K + 63) / 64) : 1;
+  const Split s = split ? split_of(tiles_of(M, N), (K + 63) / 64) : Split{tiles_of(M, N), 0, 1};
+  p.whole = static_cast<int32_t>(s.whole);
+  p.splits = s.splits;
   p.acc = acc;
   p.err = err;
   return p;
+}
+// Stages of K of the longest unit.
+int longest(const Params& p) {
+  const int k = (p.K + 63) / 64;
+  return p.whole > 0 || p.splits == 1 ? k : k / p.splits + 1;
 }
 
 struct LinearWork {
@@ -189,8 +210,8 @@ bool ld_ok(int64_t ld, int64_t cols) { return ld >= cols && ld % 8 == 0; }
 }  // namespace
 
 int linear_product(const Mat& x, const Mat& w, const float* bias, int act, const Mat& residual, const Mat& y,
-                   float* acc, int32_t* err, cudaStream_t s) {
-  if (x.rows <= kFewRows) return few_linear(x, w, bias, act, residual, y, false, err, s);
+                   float* acc, bool after, int32_t* err, cudaStream_t s) {
+  if (x.rows <= kFewRows) return few_linear(x, w, bias, act, residual, y, after, err, s);
   Maps m;
   int st = map_of(&m.a, x, kHalf);
   if (st == TPK_OK) st = map_of(&m.b, w, kHalf);
@@ -201,35 +222,30 @@ int linear_product(const Mat& x, const Mat& w, const float* bias, int act, const
   p.bias = bias;
   p.act = act;
   p.has_in = residual.p != nullptr;
-  st = launch<kLin, true>(m, p, s);
-  if (st == TPK_OK && p.splits > 1) st = join(acc, p.M, p.N, p.splits, bias, act, residual, y, s);
-  return st;
+  st = launch<kLin, true>(m, p, after, s);
+  return st == TPK_OK && p.splits > 1 ? join(p, bias, act, residual, y, s) : st;
 }
 
-int input_product(const Mat& dz, const Mat& w, const Mat& dx, float* acc, int32_t* err, cudaStream_t s) {
+int input_product(const Mat& dz, const Mat& w, const Mat& dx, float* acc, bool after, int32_t* err, cudaStream_t s) {
   Maps m;
   int st = map_of(&m.a, dz, kHalf);
   if (st == TPK_OK) st = map_of(&m.b, w, 64);
   if (st == TPK_OK) st = map_of(&m.out, dx, kHalf);
   if (st != TPK_OK) return st;
   const Params p = params(dz.rows, w.cols, dz.cols, true, acc, err);
-  const int64_t each = (dz.cols + 63) / 64 / p.splits + 1;   // stages of a unit, at most
-  st = each <= kChunk ? launch<kDx, true>(m, p, s) : launch<kDx, false>(m, p, s);
-  if (st == TPK_OK && p.splits > 1) st = join(acc, p.M, p.N, p.splits, nullptr, TPK_ACT_NONE, Mat{}, dx, s);
-  return st;
+  st = longest(p) <= kChunk ? launch<kDx, true>(m, p, after, s) : launch<kDx, false>(m, p, after, s);
+  return st == TPK_OK && p.splits > 1 ? join(p, nullptr, TPK_ACT_NONE, Mat{}, dx, s) : st;
 }
 
-int weight_product(const Mat& dz, const Mat& x, const Mat& dw, float* acc, int32_t* err, cudaStream_t s) {
+int weight_product(const Mat& dz, const Mat& x, const Mat& dw, float* acc, bool after, int32_t* err, cudaStream_t s) {
   Maps m;
   int st = map_of(&m.a, dz, 64);
   if (st == TPK_OK) st = map_of(&m.b, x, 64);
   if (st == TPK_OK) st = map_of(&m.out, dw, kHalf);
   if (st != TPK_OK) return st;
   const Params p = params(dz.cols, x.cols, dz.rows, true, acc, err);
-  const int64_t each = (dz.rows + 63) / 64 / p.splits + 1;
-  st = each <= kChunk ? launch<kDw, true>(m, p, s) : launch<kDw, false>(m, p, s);
-  if (st == TPK_OK && p.splits > 1) st = join(acc, p.M, p.N, p.splits, nullptr, TPK_ACT_NONE, Mat{}, dw, s);
-  return st;
+  st = longest(p) <= kChunk ? launch<kDw, true>(m, p, after, s) : launch<kDw, false>(m, p, after, s);
+  return st == TPK_OK && p.splits > 1 ? join(p, nullptr, TPK_ACT_NONE, Mat{}, dw, s) : st;
 }
 
 }  // namespace product
@@ -259,7 +275,7 @@ extern "C" int tpk_linear(const void* x, int64_t ld_x, const void* w, const floa
   const int st = check_device();
   if (st != TPK_OK) return st;
   return linear_product(Mat{x, N, C, ld_x}, Mat{w, O, C, C}, bias, act, Mat{residual, N, O, ld_res}, Mat{y, N, O, ld_y},
-                        k.acc, dev_err, static_cast<cudaStream_t>(stream));
+                        k.acc, false, dev_err, static_cast<cudaStream_t>(stream));
 }
 
 extern "C" int tpk_linear_bwd(const void* x, int64_t ld_x, const void* w, const float* bias, int32_t act,
@@ -300,12 +316,13 @@ extern "C" int tpk_linear_bwd(const void* x, int64_t ld_x, const void* w, const 
     p.bias = bias;
     p.act = act;
     p.colsum = db ? k.sums : nullptr;
-    if (st == TPK_OK) st = launch<kDz, true>(m, p, s);
-    if (st == TPK_OK && db) st = column_sums(k.sums, (N + 31) / 32, O, O, k.part, db, s);
+    if (st == TPK_OK) st = launch<kDz, true>(m, p, false, s);
+    if (st == TPK_OK && db) st = column_sums(k.sums, (N + 31) / 32, O, O, k.part, db, true, s);
   } else if (db) {
-    st = column_sums(static_cast<const __nv_bfloat16*>(dy), N, O, ld_dy, k.part, db, s);
+    st = column_sums(static_cast<const __nv_bfloat16*>(dy), N, O, ld_dy, k.part, db, false, s);
   }
-  if (st == TPK_OK) st = input_product(dz, mw, Mat{dx, N, C, ld_dx}, k.acc, dev_err, s);
-  if (st == TPK_OK) st = weight_product(dz, mx, Mat{dw, O, C, C}, k.acc, dev_err, s);
+  if (st == TPK_OK)
+    st = input_product(dz, mw, Mat{dx, N, C, ld_dx}, k.acc, act != TPK_ACT_NONE || db, dev_err, s);
+  if (st == TPK_OK) st = weight_product(dz, mx, Mat{dw, O, C, C}, k.acc, true, dev_err, s);
   return st;
 }

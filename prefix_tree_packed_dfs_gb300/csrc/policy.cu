@@ -7,11 +7,16 @@
 // weighted ones up, and leaves the token's share of the gradient.  The second
 // adds the shares of the raw tokens of each position, in their order, and joins
 // the sums; it starts under the first (programmatic dependent launch).
-// Where a weight is zero nothing else of the token is read.
-// Log-ratios are differences of two fp32 numbers, formed and compared with the
-// clip's borders in fp64, so that a token is never on the wrong side; a
-// sequence's mean is an fp64 sum.  exp(t) - t - 1 near t = 0 is its series.
-// What bounds it: the launches; the batch of 64 rollouts below moves 4 MB.
+// Log-ratios are differences of two fp32 numbers and are kept as the exact sum
+// of two, for their comparison with the clip's borders (a token is never on the
+// wrong side) and for a sequence's mean; fp64 instructions, of which this part
+// has few, are left to single threads (a sequence pass with fp64 block sums took
+// 83 us where this one takes the figure below).  exp(t) - t - 1 near t = 0 is its
+// series.
+// What bounds it: latency, of the launches and of the chain offset -> token ->
+// share.
+#include <cmath>
+
 #include "pair.cuh"
 #include "rowwise.cuh"
 
@@ -22,6 +27,21 @@ constexpr int kPolThreads = 256;
 constexpr int kPolBlocks = 1216;   // of the token pass, at most
 constexpr int kStats = 5;          // objective, KL, clipped, ratio, weight
 
+// The unevaluated sum of two fp32 numbers, the second below half a step of the first.
+struct Pair {
+  float hi, lo;
+};
+__device__ __forceinline__ Pair two_sum(float a, float b) {
+  const float s = a + b, t = s - a;
+  return Pair{s, (a - (s - t)) + (b - t)};
+}
+__device__ __forceinline__ Pair add(Pair a, Pair b) {
+  const Pair s = two_sum(a.hi, b.hi);
+  return two_sum(s.hi, s.lo + (a.lo + b.lo));
+}
+// a - b, of which the sign is right next to 0 too
+__device__ __forceinline__ float less(Pair a, Pair b) { return (a.hi - b.hi) + (a.lo - b.lo); }
+
 struct Policy {
   const float *loss, *old_logp, *ref_logp, *advantage, *weight;
   const int32_t* token_index;
@@ -29,31 +49,42 @@ struct Policy {
   const int32_t* offsets;
   int32_t n_seqs;
   int64_t R, F;
-  double log_lo, log_hi, log_dual;   // borders of the log-ratio; log_dual = inf: none
+  Pair log_lo, log_hi, log_dual;     // borders of the log-ratio; log_dual = inf: none
   float lo, hi, dual, kl;
   float* share;                      // [R] gradient of each raw token
-  double* sums;                      // [blocks][kStats]
+  double* sums;                      // [rows][kStats]
   int32_t sum_rows;
   float* stats;
   float* dloss;
 };
 
+// For a log-ratio: the ratio to use, and whether a border holds it, where the
+// advantage is positive (0) and negative (1).
+struct Clip {
+  float ratio, used[2];
+  bool held[2];
+};
+__device__ __forceinline__ Clip clip_of(const Policy& p, Pair d) {
+  Clip c;
+  c.ratio = expf(d.hi + d.lo);
+  c.held[0] = less(d, p.log_hi) > 0.f;
+  c.used[0] = c.held[0] ? p.hi : c.ratio;
+  const bool below = less(d, p.log_lo) < 0.f, above = less(d, p.log_dual) > 0.f;
+  c.held[1] = below || above;
+  c.used[1] = above ? p.dual : below ? p.lo : c.ratio;
+  return c;
+}
+
 struct Term {
-  float grad;     // of advantage * ratio, times the ratio; 0 where held by a border
+  float grad;     // of the ratio's part, by the log-ratio; 0 where held by a border
   float objective, held;
 };
-__device__ __forceinline__ Term clipped(const Policy& p, double d, float ratio, float adv) {
+__device__ __forceinline__ Term term_of(const Clip& c, float adv) {
+  const bool neg = adv < 0.f, zero = adv == 0.f;
+  const bool held = !zero && (neg ? c.held[1] : c.held[0]);
   Term t;
-  float used = ratio;
-  bool held = false;
-  if (adv > 0.f) {
-    if (d > p.log_hi) held = true, used = p.hi;
-  } else if (adv < 0.f) {
-    if (d < p.log_lo) held = true, used = p.lo;
-    if (d > p.log_dual) held = true, used = p.dual;
-  }
-  t.objective = -adv * used;
-  t.grad = held ? 0.f : adv * ratio;
+  t.objective = -adv * (zero ? c.ratio : neg ? c.used[1] : c.used[0]);
+  t.grad = held ? 0.f : adv * c.ratio;
   t.held = held ? 1.f : 0.f;
   return t;
 }
@@ -70,22 +101,35 @@ __device__ __forceinline__ float k3(float t) {
   return t * t * s;
 }
 
-// Position of raw token r, or -1 where r carries no loss.
-__device__ __forceinline__ int64_t position(const Policy& p, int64_t r, float& w) {
-  w = __ldg(p.weight + r);
-  if (w == 0.f) return -1;
+// A raw token: its weight and its position, -1 where it carries no loss.
+struct Token {
+  float w;
+  int64_t f;
+};
+__device__ __forceinline__ Token token_at(const Policy& p, int64_t r) {
+  Token t;
+  t.w = __ldg(p.weight + r);
   const int64_t f = __ldg(p.token_index + r);
-  return f >= 0 && f < p.F ? f : -1;
+  t.f = t.w != 0.f && f >= 0 && f < p.F ? f : -1;
+  return t;
+}
+
+// The KL term of a token; its share of the gradient is added to grad.
+__device__ __forceinline__ float kl_of(const Policy& p, float ref, float loss, float& grad) {
+  const Pair d = two_sum(ref, loss);   // ref - logp
+  const float t = d.hi + d.lo;
+  if (p.kl != 0.f) grad += p.kl * expm1f(t);
+  return k3(t);
 }
 
 // The block's sums of s into row `row` of p.sums.
 template <int kThreadsOf>
 __device__ __forceinline__ void put_sums(const Policy& p, const float (&s)[kStats], int row) {
-  __shared__ double part[kThreadsOf / 32][kStats];
+  __shared__ float part[kThreadsOf / 32][kStats];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
 #pragma unroll
   for (int i = 0; i < kStats; ++i) {
-    double v = s[i];
+    float v = s[i];
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
     if (lane == 0) part[warp][i] = v;
@@ -98,62 +142,64 @@ __device__ __forceinline__ void put_sums(const Policy& p, const float (&s)[kStat
   }
 }
 
-// The KL term of a token: its value (weighted sums), its share of the gradient.
-__device__ __forceinline__ float kl_of(const Policy& p, int64_t r, float logp, float& grad) {
-  const float t = static_cast<float>(static_cast<double>(__ldg(p.ref_logp + r)) - static_cast<double>(logp));
-  if (p.kl != 0.f) grad += p.kl * expm1f(t);
-  return k3(t);
-}
-
 __global__ void __launch_bounds__(kPolThreads) policy_token_kernel(const Policy p) {
   ptx::dependents_launch();
   float s[kStats] = {};
   const int64_t step = static_cast<int64_t>(gridDim.x) * kPolThreads;
 #pragma unroll 2
   for (int64_t r = static_cast<int64_t>(blockIdx.x) * kPolThreads + threadIdx.x; r < p.R; r += step) {
-    float w, g = 0.f;
-    const int64_t f = position(p, r, w);
-    if (f >= 0) {
-      const float logp = -__ldg(p.loss + f), adv = __ldg(p.advantage + r);
-      const double d = static_cast<double>(logp) - static_cast<double>(__ldg(p.old_logp + r));
-      const float ratio = expf(static_cast<float>(d));
-      const Term t = clipped(p, d, ratio, adv);
+    const Token k = token_at(p, r);
+    const float old = __ldg(p.old_logp + r), adv = __ldg(p.advantage + r);
+    const float ref = p.ref_logp ? __ldg(p.ref_logp + r) : 0.f;
+    float g = 0.f;
+    if (k.f >= 0) {
+      const float loss = __ldg(p.loss + k.f);
+      const Clip c = clip_of(p, two_sum(-loss, -old));
+      const Term t = term_of(c, adv);
       float objective = t.objective, kl = 0.f;
       g = t.grad;
       if (p.ref_logp) {
-        kl = kl_of(p, r, logp, g);
+        kl = kl_of(p, ref, loss, g);
         if (p.kl != 0.f) objective = fmaf(p.kl, kl, objective);
       }
-      g *= w;
-      s[0] = fmaf(w, objective, s[0]);
-      s[1] = fmaf(w, kl, s[1]);
-      s[2] = fmaf(w, t.held, s[2]);
-      s[3] = fmaf(w, ratio, s[3]);
-      s[4] += w;
+      g *= k.w;
+      s[0] = fmaf(k.w, objective, s[0]);
+      s[1] = fmaf(k.w, kl, s[1]);
+      s[2] = fmaf(k.w, t.held, s[2]);
+      s[3] = fmaf(k.w, c.ratio, s[3]);
+      s[4] += k.w;
     }
     p.share[r] = g;
   }
   put_sums<kPolThreads>(p, s, blockIdx.x);
 }
 
-template <typename T>
-__device__ __forceinline__ T block_sum(T v, T* room) {
+// The block's sum of v and of n.
+template <int kThreadsOf>
+__device__ __forceinline__ Pair block_sum(Pair v, int& n) {
+  __shared__ Pair room[kThreadsOf / 32];
+  __shared__ int many[kThreadsOf / 32];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-  __syncthreads();   // room has been read
-  if (lane == 0) room[warp] = v;
+  for (int o = 16; o > 0; o >>= 1) {
+    v = add(v, Pair{__shfl_xor_sync(0xffffffffu, v.hi, o), __shfl_xor_sync(0xffffffffu, v.lo, o)});
+    n += __shfl_xor_sync(0xffffffffu, n, o);
+  }
+  __syncthreads();   // the room has been read
+  if (lane == 0) room[warp] = v, many[warp] = n;
   __syncthreads();
-  T s = 0;
-  for (int i = 0; i < static_cast<int>(blockDim.x) / 32; ++i) s += room[i];
-  return s;
+  v = room[0];
+  n = many[0];
+#pragma unroll
+  for (int i = 1; i < kThreadsOf / 32; ++i) v = add(v, room[i]), n += many[i];
+  return v;
 }
 
 // A CTA per sequence: ratio = exp(mean log-ratio of its tokens that carry loss).
 constexpr int kSeqThreads = 512;
 __global__ void __launch_bounds__(kSeqThreads) policy_sequence_kernel(const Policy p) {
   ptx::dependents_launch();
-  __shared__ double room[kSeqThreads / 32];
+  __shared__ Clip clip;
   auto inside = [&](int64_t x) { return x < 0 ? 0 : x > p.R ? p.R : x; };
   const int i = blockIdx.x;
   const int64_t lo = inside(__ldg(p.offsets + i)), hi = inside(__ldg(p.offsets + i + 1));
@@ -162,95 +208,168 @@ __global__ void __launch_bounds__(kSeqThreads) policy_sequence_kernel(const Poli
     for (int64_t r = threadIdx.x; r < lo; r += kSeqThreads) p.share[r] = 0.f;
   if (i + 1 == p.n_seqs)
     for (int64_t r = hi + threadIdx.x; r < p.R; r += kSeqThreads) p.share[r] = 0.f;
-  double sum = 0.0, many = 0.0;
-#pragma unroll 4
-  for (int64_t r = lo + threadIdx.x; r < hi; r += kSeqThreads) {
-    float w;
-    const int64_t f = position(p, r, w);
-    if (f >= 0) {
-      sum -= static_cast<double>(__ldg(p.loss + f)) + static_cast<double>(__ldg(p.old_logp + r));
-      many += 1.0;
+  // A sequence of up to kKeep tokens per thread is read once; what is longer is
+  // read again by each step.
+  constexpr int kKeep = 4;
+  const int64_t first = lo + threadIdx.x, later = first + int64_t{kKeep} * kSeqThreads;
+  Token kept[kKeep];
+  float old[kKeep], adv[kKeep], ref[kKeep], loss[kKeep];
+#pragma unroll
+  for (int j = 0; j < kKeep; ++j) {
+    const int64_t r = first + j * kSeqThreads;
+    kept[j] = Token{0.f, -1};
+    old[j] = adv[j] = ref[j] = 0.f;
+    if (r < hi) {
+      kept[j] = token_at(p, r);
+      old[j] = __ldg(p.old_logp + r);
+      adv[j] = __ldg(p.advantage + r);
+      if (p.ref_logp) ref[j] = __ldg(p.ref_logp + r);
     }
   }
-  sum = block_sum(sum, room);
-  many = block_sum(many, room);
-  const double d = many > 0.0 ? sum / many : 0.0;
-  const float ratio = expf(static_cast<float>(d));
+#pragma unroll
+  for (int j = 0; j < kKeep; ++j) loss[j] = kept[j].f >= 0 ? __ldg(p.loss + kept[j].f) : 0.f;
+  Pair sum{0.f, 0.f};
+  int many = 0;
+#pragma unroll
+  for (int j = 0; j < kKeep; ++j)
+    if (kept[j].f >= 0) {
+      sum = add(sum, two_sum(-loss[j], -old[j]));
+      ++many;
+    }
+#pragma unroll 4
+  for (int64_t r = later; r < hi; r += kSeqThreads) {
+    const Token k = token_at(p, r);
+    const float o = __ldg(p.old_logp + r);
+    if (k.f >= 0) {
+      sum = add(sum, two_sum(-__ldg(p.loss + k.f), -o));
+      ++many;
+    }
+  }
+  sum = block_sum<kSeqThreads>(sum, many);
+  if (threadIdx.x == 0) {
+    const double d = many ? (static_cast<double>(sum.hi) + static_cast<double>(sum.lo)) / many : 0.0;
+    const float top = static_cast<float>(d);
+    clip = clip_of(p, Pair{top, static_cast<float>(d - static_cast<double>(top))});
+  }
+  __syncthreads();
+  const Clip c = clip;
   // the ratio's gradient, which every token shares
-  double pull = 0.0;
+  Pair pull{0.f, 0.f};
   float s[kStats] = {};
+  auto gather = [&](const Token& k, float a) {
+    const Term t = term_of(c, a);
+    pull = add(pull, Pair{k.w * t.grad, 0.f});
+    s[0] = fmaf(k.w, t.objective, s[0]);
+    s[2] = fmaf(k.w, t.held, s[2]);
+    s[3] = fmaf(k.w, c.ratio, s[3]);
+    s[4] += k.w;
+  };
+#pragma unroll
+  for (int j = 0; j < kKeep; ++j)
+    if (kept[j].f >= 0) gather(kept[j], adv[j]);
 #pragma unroll 4
-  for (int64_t r = lo + threadIdx.x; r < hi; r += kSeqThreads) {
-    float w;
-    if (position(p, r, w) < 0) continue;
-    const Term t = clipped(p, d, ratio, __ldg(p.advantage + r));
-    pull += static_cast<double>(w * t.grad);
-    s[0] = fmaf(w, t.objective, s[0]);
-    s[2] = fmaf(w, t.held, s[2]);
-    s[3] = fmaf(w, ratio, s[3]);
-    s[4] += w;
+  for (int64_t r = later; r < hi; r += kSeqThreads) {
+    const Token k = token_at(p, r);
+    const float a = __ldg(p.advantage + r);
+    if (k.f >= 0) gather(k, a);
   }
-  pull = block_sum(pull, room);
-  const float each = many > 0.0 ? static_cast<float>(pull / many) : 0.f;
+  int unused = 0;
+  pull = block_sum<kSeqThreads>(pull, unused);
+  const float each = many ? (pull.hi + pull.lo) / static_cast<float>(many) : 0.f;
+  auto share = [&](const Token& k, float token_ref, float token_loss) {
+    if (k.f < 0) return 0.f;
+    if (!p.ref_logp) return each;
+    float pull_kl = 0.f;
+    const float kl = kl_of(p, token_ref, token_loss, pull_kl);
+    if (p.kl != 0.f) s[0] = fmaf(k.w, p.kl * kl, s[0]);
+    s[1] = fmaf(k.w, kl, s[1]);
+    return fmaf(k.w, pull_kl, each);
+  };
+#pragma unroll
+  for (int j = 0; j < kKeep; ++j)
+    if (first + j * kSeqThreads < hi) p.share[first + j * kSeqThreads] = share(kept[j], ref[j], loss[j]);
 #pragma unroll 4
-  for (int64_t r = lo + threadIdx.x; r < hi; r += kSeqThreads) {
-    float w, g = 0.f;
-    const int64_t f = position(p, r, w);
-    if (f >= 0) {
-      g = each;
-      if (p.ref_logp) {
-        float k = 0.f;
-        const float kl = kl_of(p, r, -__ldg(p.loss + f), k);
-        g = fmaf(w, k, g);
-        if (p.kl != 0.f) s[0] = fmaf(w, p.kl * kl, s[0]);
-        s[1] = fmaf(w, kl, s[1]);
-      }
-    }
-    p.share[r] = g;
+  for (int64_t r = later; r < hi; r += kSeqThreads) {
+    const Token k = token_at(p, r);
+    p.share[r] = share(k, p.ref_logp && k.f >= 0 ? __ldg(p.ref_logp + r) : 0.f, k.f >= 0 ? __ldg(p.loss + k.f) : 0.f);
   }
   put_sums<kSeqThreads>(p, s, i);
 }
 
-// dloss[f] = sum of the shares of f's raw tokens.  A CTA takes 32 positions,
-// one per lane (neighbouring positions' tokens are neighbours in raw order), and
-// its eight warps every eighth token of each: a prompt under hundreds of
-// sequences is no long walk.  The last CTA joins the first pass's sums.
+// dloss[f] = sum of the shares of f's raw tokens.  A warp takes 32 neighbouring
+// positions, one per lane (their tokens are neighbours in raw order too).  Where
+// one of the 32 has many tokens (a prompt under hundreds of sequences) the
+// CTA's eight warps take every eighth token each.  A CTA's warps take groups
+// from all over the batch, so that a prompt's groups meet different CTAs.  The
+// last CTA joins the first pass's sums.
+constexpr int kLong = 32;   // tokens of a position that a lane adds up alone
+template <int kAhead>
+__device__ __forceinline__ float shares(const Policy& p, int64_t lo, int64_t hi, int step) {
+  float s = 0.f;
+  for (int64_t e0 = lo; e0 < hi; e0 += kAhead * step) {
+    int r[kAhead];
+#pragma unroll
+    for (int j = 0; j < kAhead; ++j) {
+      const int64_t e = e0 + j * step;
+      r[j] = e < hi ? __ldg(p.raw + e) : -1;
+    }
+#pragma unroll
+    for (int j = 0; j < kAhead; ++j)
+      if (r[j] >= 0 && r[j] < p.R) s += __ldcg(p.share + r[j]);
+  }
+  return s;
+}
+
 __global__ void __launch_bounds__(kPolThreads) policy_position_kernel(const Policy p) {
   constexpr int kWarps = kPolThreads / 32;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  if (blockIdx.x + 1 == gridDim.x) {
+  const int blocks = static_cast<int>(gridDim.x) - 1;
+  if (static_cast<int>(blockIdx.x) == blocks) {
     ptx::dependency_wait();
-    __shared__ double room[kPolThreads / 32];
-    for (int i = 0; i < kStats; ++i) {
+    __shared__ double room[kStats][32];
+    const int i = threadIdx.x / 32;
+    if (i < kStats) {
       double v = 0.0;
-      for (int r = threadIdx.x; r < p.sum_rows; r += kPolThreads) v += p.sums[static_cast<int64_t>(r) * kStats + i];
-      v = block_sum(v, room);
-      if (threadIdx.x == 0) p.stats[i] = static_cast<float>(v);
+#pragma unroll 4
+      for (int r = lane; r < p.sum_rows; r += 32) v += __ldcg(p.sums + static_cast<int64_t>(r) * kStats + i);
+      room[i][lane] = v;
+      __syncwarp();
+      if (lane == 0) {
+        for (int l = 1; l < 32; ++l) v += room[i][l];
+        p.stats[i] = static_cast<float>(v);
+      }
     }
     return;
   }
-  const int64_t f = static_cast<int64_t>(blockIdx.x) * 32 + lane;
-  int64_t lo = 0, hi = 0;
+  const int64_t f = (static_cast<int64_t>(warp) * blocks + blockIdx.x) * 32 + lane;
+  int lo = 0, hi = 0;
   if (f < p.F) {
     lo = __ldg(p.raw_begin + f);
     hi = __ldg(p.raw_begin + f + 1);
     lo = lo < 0 ? 0 : lo;
-    hi = hi > p.R ? p.R : hi;
+    hi = hi > p.R ? static_cast<int>(p.R) : hi;
   }
-  ptx::dependency_wait();
-  float s = 0.f;
-#pragma unroll 4
-  for (int64_t e = lo + warp; e < hi; e += kWarps) {
-    const int64_t r = __ldg(p.raw + e);
-    if (r >= 0 && r < p.R) s += __ldcg(p.share + r);
-  }
+  __shared__ int from[kWarps][32], to[kWarps][32], is_long[kWarps];
   __shared__ float part[kWarps][32];
-  part[warp][lane] = s;
+  from[warp][lane] = lo;
+  to[warp][lane] = hi;
+  const bool any = __any_sync(0xffffffffu, hi - lo > kLong);
+  if (lane == 0) is_long[warp] = any;
+  ptx::dependency_wait();
+  if (!any && f < p.F) p.dloss[f] = shares<4>(p, lo, hi, 1);
   __syncthreads();
-  if (warp != 0 || f >= p.F) return;
+  for (int g = 0; g < kWarps; ++g) {
+    if (!is_long[g]) continue;
+    part[warp][lane] = shares<16>(p, int64_t{from[g][lane]} + warp, to[g][lane], kWarps);
+    __syncthreads();
+    if (warp == g && f < p.F) {
+      float s = 0.f;
 #pragma unroll
-  for (int i = 1; i < kWarps; ++i) s += part[i][lane];
-  p.dloss[f] = s;
+      for (int i = 0; i < kWarps; ++i) s += part[i][lane];
+      p.dloss[f] = s;
+    }
+    __syncthreads();
+  }
 }
 
 int token_blocks(int64_t R) {
@@ -306,9 +425,13 @@ extern "C" int tpk_policy_loss(const float* loss, const float* old_logp, const f
   p.n_seqs = n_seqs;
   p.R = R;
   p.F = F;
-  p.log_lo = log1p(-opts->clip_low);
-  p.log_hi = log1p(opts->clip_high);
-  p.log_dual = opts->dual_clip > 0.0 ? log(opts->dual_clip) : INFINITY;
+  auto pair = [](double x) {
+    const float top = static_cast<float>(x);
+    return Pair{top, std::isfinite(top) ? static_cast<float>(x - static_cast<double>(top)) : 0.f};
+  };
+  p.log_lo = pair(log1p(-opts->clip_low));
+  p.log_hi = pair(log1p(opts->clip_high));
+  p.log_dual = pair(opts->dual_clip > 0.0 ? log(opts->dual_clip) : INFINITY);
   p.lo = static_cast<float>(1.0 - opts->clip_low);
   p.hi = static_cast<float>(1.0 + opts->clip_high);
   p.dual = static_cast<float>(opts->dual_clip);
@@ -325,7 +448,7 @@ extern "C" int tpk_policy_loss(const float* loss, const float* old_logp, const f
   st = cuda_status(cudaGetLastError());
   if (st != TPK_OK) return st;
   cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3(static_cast<unsigned>((F + 31) / 32 + 1));
+  cfg.gridDim = dim3(static_cast<unsigned>((F + kPolThreads - 1) / kPolThreads + 1));
   cfg.blockDim = dim3(kPolThreads);
   cfg.stream = s;
   cudaLaunchAttribute at[1];

@@ -7,9 +7,9 @@
 //   kDw       dz^T x             stored
 //   kGate     x (w_gate | w_up)^T   a = act(g) u (and g, u kept)
 //   kGateBwd  dy w_out              dg = da u act'(g), du = da act(g)
-// kLin, kDx and kDw may be split over K where their tiles alone do not fill
-// the GPU: fp32 partial tiles, summed in a fixed order by linear.cu's
-// join_kernel, which then does the epilogue.
+// The tiles that are left over from whole rounds of kLin, kDx and kDw may be
+// split over K (split_of): fp32 partial tiles, summed in a fixed order by
+// linear.cu's join_kernel, which then does the epilogue.
 //
 // 256 x 256 tiles on a pair of CTAs (tcgen05 cta_group::2): each CTA holds 128
 // rows of A, 128 of B and its 128 rows of the result.  64 elements of K per
@@ -26,6 +26,14 @@
 // the wide side (kDx) stop every 8,192 elements and are added up in registers
 // with rounding to nearest: at most 5e-5 is left, a fortieth of the results'
 // bf16 rounding; sums over at most kMostK channels need no stop.
+// g and u are kept for the backward in 16 bits: as fp16 scaled by a power of two
+// for every 32 channels of a row, so that the largest lies in [2^14, 2^15).  That
+// is eight times as precise as bf16 for the same bytes, at any scale (a value
+// 2^-29 of its group's largest still has its 11 bits); with g and u in bf16 the
+// gradients' error over fp64 was 3.0e-3 of their norm against 2.4e-3 with them
+// unrounded, of which 1.7e-3 is the results' own rounding.
+// Kernels of one call overlap at their ends (programmatic dependent launch):
+// each sets itself up and then waits for the one before.
 // Warps of a CTA: 0 TMA producer, 1 MMA issuer (of the pair's first CTA), 2
 // TMEM owner, 4-11 epilogue (two warpgroups).  CTAs are persistent and walk the
 // tiles in panels of 8 columns of tiles, so that the pairs running together
@@ -50,6 +58,7 @@ constexpr int kStages = 5;
 constexpr int kChunk = 128;            // stages per accumulation of kDx, kDw
 constexpr int kMostK = 32768;          // channels of a sum that never stops
 constexpr int kPairs = 76;             // pairs a split over K aims to fill
+constexpr int kGroup = 32;             // channels that share a power of two in what kGate keeps
 // The chunked epilogue holds 128 columns of a row per thread: the other warps
 // give registers to its two warpgroups.
 constexpr uint32_t kRegsCtl = 56;
@@ -66,13 +75,15 @@ struct Maps {
 
 struct Params {
   int32_t M, N, K;           // extents of the product (kGate, kGateBwd: N = channels of one of the two)
-  int32_t splits;
+  int32_t whole, splits;     // tiles before the split ones; splits of each of those (split_of)
   int32_t act;
   int32_t has_in;            // kLin: a residual
   int32_t save;              // kGate: g and u go out too
   const float* bias;         // [N] or nullptr
   float* colsum;             // kDz: [ceil(M / 32)][N] sums of 32 rows of dz; nullptr: none
-  float* acc;                // splits > 1: [splits * tiles][256 * 256]
+  float* acc;                // splits > 1: [splits][tiles - whole][256 * 256]
+  uint8_t* exps;             // kGate, kGateBwd: [2][groups][exp_rows] biased exponents of g's and u's largest
+  int64_t exp_rows;
   int32_t* err;
 };
 
@@ -91,27 +102,30 @@ struct Smem {
 constexpr size_t kSmemBytes = sizeof(Smem) + 1024;
 static_assert(kSmemBytes <= 227 * 1024, "shared memory");
 
-// Splits over K where the tiles alone do not fill the GPU: one round of units
-// for a few tiles; otherwise, below four rounds, the split into up to 8 that
-// makes the rounds shortest, where it saves a tenth or more.  A split has 8
-// stages of K or more.
-constexpr int kSplitRounds = 4, kSplitMost = 8;
-inline int splits_for(int64_t tiles, int64_t k_iters) {
-  const int64_t most = k_iters / 8;
-  if (tiles <= 0 || tiles > kSplitRounds * kPairs || most <= 1) return 1;
-  if (tiles * kSplitMost <= kPairs) {
-    const int64_t s = kPairs / tiles;
-    return static_cast<int>(s < most ? s : most);
-  }
-  int64_t best = 1, rounds = (tiles + kPairs - 1) / kPairs;
-  for (int64_t s = 2; s <= kSplitMost && s <= most; ++s) {
-    const int64_t r = (tiles * s + kPairs - 1) / kPairs;
-    if (r * best * 10 <= rounds * s * 9) {
-      best = s;
-      rounds = r;
+// The split over K.  Pairs take tiles in rounds; the `tail` tiles left over from
+// whole rounds (all of them, if they are few) take a round of their own, which
+// `splits` units for each of them make shorter.  It has to pay for the partial
+// tiles (written and read once, at about 5 TB/s) and for the joining kernel.
+struct Split {
+  int64_t whole, tail;
+  int splits;
+};
+inline Split split_of(int64_t tiles, int64_t k_iters) {
+  Split s{tiles, 0, 1};
+  const int64_t tail = tiles % kPairs;
+  if (tail == 0) return s;
+  const double tile_us = 0.135 * static_cast<double>(k_iters);   // 64 elements of K: 256 cycles
+  double best = tile_us;
+  for (int64_t n = 2; n <= k_iters / 4 && n <= (tail * 8 < kPairs ? kPairs / tail : 8); ++n) {
+    const int64_t rounds = (tail * n + kPairs - 1) / kPairs;
+    const double us = tile_us * static_cast<double>(rounds) / static_cast<double>(n) + 3.0 +
+                      0.105 * static_cast<double>(tail * n);
+    if (us < best) {
+      best = us;
+      s = Split{tiles - tail, tail, static_cast<int>(n)};
     }
   }
-  return static_cast<int>(best);
+  return s;
 }
 
 // Unit u covers tile (m, n) and the stages [k0, k0 + nk) of K.
@@ -119,7 +133,9 @@ struct Shape {
   int mt, nt, units, k_iters;
 };
 struct Unit {
-  int m, n, k0, nk, split;
+  int m, n, k0, nk;
+  int split;                 // -1: the whole of K
+  int tile;
 };
 template <int kMode>
 constexpr int kTileN = kMode == kGate ? kHalf : kTile;
@@ -130,21 +146,28 @@ __host__ __device__ inline Shape shape_of(const Params& p) {
   s.mt = (p.M + kTile - 1) / kTile;
   s.nt = (p.N + kTileN<kMode> - 1) / kTileN<kMode>;
   s.k_iters = (p.K + 63) / 64;
-  s.units = s.mt * s.nt * p.splits;
+  s.units = p.whole + (s.mt * s.nt - p.whole) * p.splits;
   return s;
 }
+// Tile t of the walk, in panels of kPanel columns of tiles.
+__device__ __forceinline__ void place_of(int mt, int nt, int t, int& m, int& n) {
+  const int panel = t / (kPanel * mt);
+  t -= panel * kPanel * mt;
+  const int width = min(kPanel, nt - panel * kPanel);
+  m = t / width;
+  n = panel * kPanel + t % width;
+}
 __device__ __forceinline__ Unit unit_of(const Params& p, const Shape& s, int u) {
-  Unit w;
-  const int tiles = s.mt * s.nt;
-  w.split = u / tiles;
-  int t = u - w.split * tiles;
-  const int panel = t / (kPanel * s.mt);
-  t -= panel * kPanel * s.mt;
-  const int width = min(kPanel, s.nt - panel * kPanel);
-  w.m = t / width;
-  w.n = panel * kPanel + t % width;
-  w.k0 = static_cast<int>(static_cast<int64_t>(s.k_iters) * w.split / p.splits);
-  w.nk = static_cast<int>(static_cast<int64_t>(s.k_iters) * (w.split + 1) / p.splits) - w.k0;
+  Unit w{0, 0, 0, s.k_iters, -1};
+  if (u >= p.whole && p.splits > 1) {
+    const int tail = s.mt * s.nt - p.whole;
+    w.split = (u - p.whole) / tail;
+    u = p.whole + (u - p.whole) % tail;
+    w.k0 = static_cast<int>(static_cast<int64_t>(s.k_iters) * w.split / p.splits);
+    w.nk = static_cast<int>(static_cast<int64_t>(s.k_iters) * (w.split + 1) / p.splits) - w.k0;
+  }
+  w.tile = u;
+  place_of(s.mt, s.nt, u, w.m, w.n);
   return w;
 }
 
@@ -172,6 +195,28 @@ __device__ __forceinline__ void get64(const uint8_t* box, int r, int half, uint3
 __device__ __forceinline__ uint8_t* at32(uint8_t* box, int r, int q) {
   return box + r * 64 + ((q ^ ((r >> 1) & 3)) * 16);
 }
+
+// The biased exponent of the largest finite magnitude of x, within [15, 254].
+__device__ __forceinline__ uint32_t largest_exponent(const uint32_t (&x)[32]) {
+  float top[4] = {};
+#pragma unroll
+  for (int e = 0; e < 32; e += 2)
+    top[(e / 2) & 3] = ptx::max3(top[(e / 2) & 3], fabsf(__uint_as_float(x[e])), fabsf(__uint_as_float(x[e + 1])));
+  uint32_t m = __float_as_uint(fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])));
+  if (m >= 0x7f800000u) {   // an infinity has no say
+    m = 0;
+#pragma unroll
+    for (int e = 0; e < 32; ++e) {
+      const uint32_t v = x[e] & 0x7fffffffu;
+      m = v < 0x7f800000u && v > m ? v : m;
+    }
+  }
+  m >>= 23;
+  return m < 15 ? 15 : m;
+}
+// The power of two that takes such a group to [2^14, 2^15), and its inverse.
+__device__ __forceinline__ float group_scale(uint32_t e) { return __uint_as_float((268 - e) << 23); }
+__device__ __forceinline__ float group_unscale(uint32_t e) { return __uint_as_float((e - 14) << 23); }
 
 // Sums over the warp's 32 rows of x[0..31] (a row per lane): lane l returns
 // the sum of column l.  Each step halves the columns a lane holds.
@@ -230,6 +275,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   ptx::cluster_sync();   // the other CTA's barriers exist
   ptx::tc_fence_after();
   const uint32_t tmem = S.tmem_base;
+  ptx::dependents_launch();
+  ptx::dependency_wait();   // what the kernel before wrote is there
   if (warp < 4) {
     if constexpr (!kOne) ptx::regs_dec<kRegsCtl>();
     if (warp == 0) {
@@ -325,11 +372,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     auto meet = [&] { asm volatile("bar.sync %0, 128;" ::"r"(wg + 1) : "memory"); };
     // loads into box s so far (each thread's count), of which the last may be under way
     uint32_t loads[2] = {0, 0};
-    const bool takes = kMode == kDz || kMode == kGateBwd || (kMode == kLin && p.has_in && p.splits == 1);
     uint32_t tile = 0, sent = 0;
     bool ok = true;
     for (int u = pair; ok && u < sh.units; u += n_pairs) {
       const Unit w = unit_of(p, sh, u);
+      const bool takes = kMode == kDz || kMode == kGateBwd || (kMode == kLin && p.has_in && w.split < 0);
       const int row0 = w.m * kTile + static_cast<int>(rank) * kHalf;   // first row of this CTA
       const int n0 = w.n * kTileN<kMode> + wg * (kTileN<kMode> / 2);   // first column of this warpgroup
       // what the epilogue reads, into the boxes that it will leave from
@@ -346,6 +393,18 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       auto fetched = [&](int s) {
         return ptx::mbar_wait(&S.in_full[wg][s], (loads[s] - 1) & 1, abort_flag, kWaitLimitNs);
       };
+      uint32_t exps[4] = {};   // kGateBwd: the exponents of this row's groups, u's above g's
+      if constexpr (kMode == kGateBwd) {
+        const int64_t groups = (p.N + kGroup - 1) / kGroup;
+#pragma unroll
+        for (int c = 0; c < 4; ++c)
+          if (n0 + c * kGroup < p.N && row0 + rc < p.M) {
+            const uint8_t* e = p.exps + (n0 / kGroup + c) * p.exp_rows + row0 + rc;
+            exps[c] = __ldg(e) | static_cast<uint32_t>(__ldg(e + groups * p.exp_rows)) << 16;
+          } else {
+            exps[c] = 0x7f007fu;
+          }
+      }
       if (takes) {
         if (leader) {
           ptx::bulk_wait_read<0>();   // the boxes' last results have left
@@ -418,8 +477,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             for (int e = 0; e < 16; ++e) x[e] = z[c * 16 + e];
           }
           const int c0 = n0 + c * 32, b = c >> 1, half = c & 1;
-          if (kPlain && p.splits > 1) {
-            const int64_t tile_id = static_cast<int64_t>(w.split) * sh.mt * sh.nt + w.m * sh.nt + w.n;
+          if (kPlain && w.split >= 0) {
+            const int64_t tile_id = static_cast<int64_t>(w.split) * (sh.mt * sh.nt - p.whole) + w.tile - p.whole;
             float* blk = p.acc + tile_id * (kTile * kTile) + (static_cast<int>(rank) * kHalf + rc) * kTile + wg * kHalf;
             ulonglong2* ap = reinterpret_cast<ulonglong2*>(blk + c * 32);
 #pragma unroll
@@ -434,74 +493,55 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                 meet();
               }
             }
-            if constexpr (kMode == kLin) {
-              // the plain projection stores what it has summed
+            if constexpr (kMode == kLin || kMode == kDz) {
               uint32_t in[16];
               if (takes) get64(box[b], rc, half, in);
-              float v[32];
-#pragma unroll
-              for (int e = 0; e < 16; ++e) ptx::unf2(x[e], v[2 * e], v[2 * e + 1]);
               if (p.bias) {
 #pragma unroll
-                for (int e = 0; e < 32; e += 4)
-                  if (c0 + e < p.N) {
-                    const float4 bv = __ldg(reinterpret_cast<const float4*>(p.bias + c0 + e));
-                    v[e] += bv.x; v[e + 1] += bv.y; v[e + 2] += bv.z; v[e + 3] += bv.w;
+                for (int e = 0; e < 16; e += 2)
+                  if (c0 + 2 * e < p.N) {
+                    const ulonglong2 bv = __ldg(reinterpret_cast<const ulonglong2*>(p.bias + c0 + 2 * e));
+                    x[e] = ptx::add2(x[e], bv.x);
+                    x[e + 1] = ptx::add2(x[e + 1], bv.y);
                   }
               }
-              if (p.act != TPK_ACT_NONE)
+              if constexpr (kMode == kLin) {
+                if (p.act != TPK_ACT_NONE)
+                  with_act(p.act, [&](auto t) {
+#pragma unroll
+                    for (int e = 0; e < 16; ++e) x[e] = act_2<decltype(t)::value>(x[e]);
+                  });
+                if (takes)
+#pragma unroll
+                  for (int e = 0; e < 16; ++e) x[e] = ptx::add2(x[e], ptx::f2(lo16(in[e]), hi16(in[e])));
+              } else {
                 with_act(p.act, [&](auto t) {
 #pragma unroll
-                  for (int e = 0; e < 32; ++e) v[e] = act_of<decltype(t)::value>(v[e]);
-                });
-#pragma unroll
-              for (int e = 0; e < 16; ++e) {
-                if (takes) {
-                  v[2 * e] += lo16(in[e]);
-                  v[2 * e + 1] += hi16(in[e]);
-                }
-                o[e] = ptx::pack_bf16x2(v[2 * e], v[2 * e + 1]);
-              }
-            } else if constexpr (kMode == kDz) {
-              uint32_t in[16];
-              get64(box[b], rc, half, in);
-              float v[32];
-#pragma unroll
-              for (int e = 0; e < 16; ++e) ptx::unf2(x[e], v[2 * e], v[2 * e + 1]);
-              if (p.bias) {
-#pragma unroll
-                for (int e = 0; e < 32; e += 4)
-                  if (c0 + e < p.N) {
-                    const float4 bv = __ldg(reinterpret_cast<const float4*>(p.bias + c0 + e));
-                    v[e] += bv.x; v[e + 1] += bv.y; v[e + 2] += bv.z; v[e + 3] += bv.w;
+                  for (int e = 0; e < 16; ++e) {
+                    uint64_t slope;
+                    act_slope_2<decltype(t)::value>(x[e], slope);
+                    x[e] = ptx::mul2(ptx::f2(lo16(in[e]), hi16(in[e])), slope);
                   }
+                });
               }
+            }
+#pragma unroll
+            for (int e = 0; e < 16; ++e) {
+              float lo, hi;
+              ptx::unf2(x[e], lo, hi);
+              o[e] = ptx::pack_bf16x2(lo, hi);
+            }
+            if (kMode == kDz && p.colsum) {
+              float v[32];
               const bool inside = row0 + rc < p.M;
-              with_act(p.act, [&](auto t) {
-#pragma unroll
-                for (int e = 0; e < 32; ++e) {
-                  float slope;
-                  act_slope<decltype(t)::value>(v[e], slope);
-                  v[e] = (e & 1 ? hi16(in[e / 2]) : lo16(in[e / 2])) * slope;
-                }
-              });
-#pragma unroll
-              for (int e = 0; e < 16; ++e) o[e] = ptx::pack_bf16x2(v[2 * e], v[2 * e + 1]);
-              if (p.colsum) {
-                if (!inside)
-#pragma unroll
-                  for (int e = 0; e < 32; ++e) v[e] = 0.f;
-                const float sum = column_sums(v, lane);
-                if (row0 + (warp & 3) * 32 < p.M && c0 + lane < p.N)
-                  p.colsum[static_cast<int64_t>(row0 / 32 + (warp & 3)) * p.N + c0 + lane] = sum;
-              }
-            } else {
 #pragma unroll
               for (int e = 0; e < 16; ++e) {
-                float lo, hi;
-                ptx::unf2(x[e], lo, hi);
-                o[e] = ptx::pack_bf16x2(lo, hi);
+                ptx::unf2(x[e], v[2 * e], v[2 * e + 1]);
+                if (!inside) v[2 * e] = v[2 * e + 1] = 0.f;
               }
+              const float sum = column_sums(v, lane);
+              if (row0 + (warp & 3) * 32 < p.M && c0 + lane < p.N)
+                p.colsum[static_cast<int64_t>(row0 / 32 + (warp & 3)) * p.N + c0 + lane] = sum;
             }
             put64(box[b], rc, half, o);
             if (half == 1) {
@@ -534,22 +574,37 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           ptx::tmem_wait_ld_of(up);
           if (half == 1) release();
           if (p.save) {
+            const uint32_t eg = largest_exponent(g), eu = largest_exponent(up);
+            if (n0 + half * kGroup < p.N && row0 + rc < p.M) {
+              const int64_t groups = (p.N + kGroup - 1) / kGroup;
+              uint8_t* e = p.exps + (n0 / kGroup + half) * p.exp_rows + row0 + rc;
+              e[0] = static_cast<uint8_t>(eg);
+              e[groups * p.exp_rows] = static_cast<uint8_t>(eu);
+            }
+            const uint64_t sg = both(group_scale(eg)), su = both(group_scale(eu));
             uint32_t o[16];
 #pragma unroll
-            for (int e = 0; e < 16; ++e) o[e] = ptx::pack_bf16x2(__uint_as_float(g[2 * e]), __uint_as_float(g[2 * e + 1]));
+            for (int e = 0; e < 16; ++e) {
+              float lo, hi;
+              ptx::unf2(ptx::mul2(pair_at(g, e), sg), lo, hi);
+              o[e] = ptx::pack_f16x2(lo, hi);
+            }
             put64(box[0], rc, half, o);
 #pragma unroll
-            for (int e = 0; e < 16; ++e)
-              o[e] = ptx::pack_bf16x2(__uint_as_float(up[2 * e]), __uint_as_float(up[2 * e + 1]));
+            for (int e = 0; e < 16; ++e) {
+              float lo, hi;
+              ptx::unf2(ptx::mul2(pair_at(up, e), su), lo, hi);
+              o[e] = ptx::pack_f16x2(lo, hi);
+            }
             put64(box[1], rc, half, o);
           }
           with_act(p.act, [&](auto t) {
 #pragma unroll
-            for (int e = 0; e < 16; ++e)
-              a[half][e] =
-                  ptx::pack_bf16x2(act_of<decltype(t)::value>(__uint_as_float(g[2 * e])) * __uint_as_float(up[2 * e]),
-                                   act_of<decltype(t)::value>(__uint_as_float(g[2 * e + 1])) *
-                                       __uint_as_float(up[2 * e + 1]));
+            for (int e = 0; e < 16; ++e) {
+              float lo, hi;
+              ptx::unf2(ptx::mul2(act_2<decltype(t)::value>(pair_at(g, e)), pair_at(up, e)), lo, hi);
+              a[half][e] = ptx::pack_bf16x2(lo, hi);
+            }
           });
         }
         const bool inside = n0 < p.N && row0 < p.M;
@@ -587,26 +642,27 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           if (c < 3) ptx::tmem_ld32(tm + (c + 1) * 32, raw[(c + 1) & 1]);
           const int s = c & 1, c0 = n0 + c * 32;
           ok = fetched(s) && ok;
+          const uint64_t sg = both(group_unscale(exps[c] & 0xff)), su = both(group_unscale(exps[c] >> 16));
           with_act(p.act, [&](auto t) {
 #pragma unroll
             for (int q = 0; q < 4; ++q) {
               uint8_t* gp = at32(box[s], rc, q);
               uint8_t* up = gp + kBoxBytes / 2;
               const int4 gv = ptx::lds128i(gp), uv = ptx::lds128i(up);
-              const uint32_t gw[4] = {static_cast<uint32_t>(gv.x), static_cast<uint32_t>(gv.y),
-                                      static_cast<uint32_t>(gv.z), static_cast<uint32_t>(gv.w)};
-              const uint32_t uw[4] = {static_cast<uint32_t>(uv.x), static_cast<uint32_t>(uv.y),
-                                      static_cast<uint32_t>(uv.z), static_cast<uint32_t>(uv.w)};
+              const int gw[4] = {gv.x, gv.y, gv.z, gv.w}, uw[4] = {uv.x, uv.y, uv.z, uv.w};
               uint32_t og[4], ou[4];
 #pragma unroll
               for (int e = 0; e < 4; ++e) {
-                const float d0 = __uint_as_float(raw[c & 1][q * 8 + 2 * e]);
-                const float d1 = __uint_as_float(raw[c & 1][q * 8 + 2 * e + 1]);
-                float s0, s1;
-                const float a0 = act_slope<decltype(t)::value>(lo16(gw[e]), s0);
-                const float a1 = act_slope<decltype(t)::value>(hi16(gw[e]), s1);
-                og[e] = ptx::pack_bf16x2(d0 * lo16(uw[e]) * s0, d1 * hi16(uw[e]) * s1);
-                ou[e] = ptx::pack_bf16x2(d0 * a0, d1 * a1);
+                const uint64_t g = ptx::mul2(ptx::unpack_f16x2(static_cast<uint32_t>(gw[e])), sg);
+                const uint64_t u = ptx::mul2(ptx::unpack_f16x2(static_cast<uint32_t>(uw[e])), su);
+                const uint64_t da = pair_at(raw[c & 1], q * 4 + e);
+                uint64_t slope;
+                const uint64_t v = act_slope_2<decltype(t)::value>(g, slope);
+                float lo, hi;
+                ptx::unf2(ptx::mul2(ptx::mul2(da, u), slope), lo, hi);
+                og[e] = ptx::pack_bf16x2(lo, hi);
+                ptx::unf2(ptx::mul2(da, v), lo, hi);
+                ou[e] = ptx::pack_bf16x2(lo, hi);
               }
               *reinterpret_cast<uint4*>(gp) = make_uint4(og[0], og[1], og[2], og[3]);
               *reinterpret_cast<uint4*>(up) = make_uint4(ou[0], ou[1], ou[2], ou[3]);
@@ -672,13 +728,32 @@ inline int map_of(CUtensorMap* m, const Mat& a, int box_rows, int box_cols = 64)
 inline int64_t tiles_of(int64_t M, int64_t N) { return (M + kTile - 1) / kTile * ((N + kTile - 1) / kTile); }
 // Workspace of a product that may be split over K.
 inline size_t acc_bytes(int64_t M, int64_t N, int64_t K) {
-  const int64_t tiles = tiles_of(M, N);
-  const int s = splits_for(tiles, (K + 63) / 64);
-  return s > 1 ? static_cast<size_t>(tiles) * s * kTile * kTile * 4 : 0;
+  const Split s = split_of(tiles_of(M, N), (K + 63) / 64);
+  return static_cast<size_t>(s.tail) * s.splits * kTile * kTile * 4;
+}
+// Rows of the exponents that kGate keeps, and their bytes.
+inline int64_t exp_rows(int64_t N) { return (N + 127) / 128 * 128; }
+inline size_t exp_bytes(int64_t N, int64_t I) { return static_cast<size_t>((I + kGroup - 1) / kGroup * 2 * exp_rows(N)); }
+
+// Kernel launch; after: the stream's last kernel is this library's, of the same
+// call, and this one may start under its end (it waits for it itself).
+template <typename... Args, typename... Given>
+int launch_kernel(void (*kern)(Args...), dim3 grid, int threads, size_t smem, bool after, cudaStream_t s, Given... given) {
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(static_cast<unsigned>(threads));
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = s;
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = after ? 1 : 0;
+  return cuda_status(cudaLaunchKernelEx(&cfg, kern, static_cast<Args>(given)...));
 }
 
 template <int kMode, bool kOne>
-int launch(const Maps& maps, const Params& p, cudaStream_t s) {
+int launch(const Maps& maps, const Params& p, bool after, cudaStream_t s) {
   constexpr auto kern = product_kernel<kMode, kOne>;
   static PerContext<int> rec;
   int unused = 0;
@@ -695,18 +770,18 @@ int launch(const Maps& maps, const Params& p, cudaStream_t s) {
   int pairs = num_sms() / 2;
   pairs = pairs < 1 ? 1 : pairs;
   pairs = pairs < units ? pairs : units;
-  kern<<<static_cast<unsigned>(2 * pairs), kThreads, kSmemBytes, s>>>(maps, p);
-  return cuda_status(cudaGetLastError());
+  return launch_kernel(kern, dim3(static_cast<unsigned>(2 * pairs)), kThreads, kSmemBytes, after, s, maps, p);
 }
 
-// Products of linear.cu that the feed-forward block uses too.  acc: acc_bytes.
+// Products of linear.cu that the feed-forward block uses too.  acc: acc_bytes;
+// after: as in launch_kernel.
 // y = act(x w^T + bias) + residual (residual.p may be nullptr)
 int linear_product(const Mat& x, const Mat& w, const float* bias, int act, const Mat& residual, const Mat& y,
-                   float* acc, int32_t* err, cudaStream_t s);
+                   float* acc, bool after, int32_t* err, cudaStream_t s);
 // dx = dz w
-int input_product(const Mat& dz, const Mat& w, const Mat& dx, float* acc, int32_t* err, cudaStream_t s);
+int input_product(const Mat& dz, const Mat& w, const Mat& dx, float* acc, bool after, int32_t* err, cudaStream_t s);
 // dw = dz^T x
-int weight_product(const Mat& dz, const Mat& x, const Mat& dw, float* acc, int32_t* err, cudaStream_t s);
+int weight_product(const Mat& dz, const Mat& x, const Mat& dw, float* acc, bool after, int32_t* err, cudaStream_t s);
 
 }  // namespace product
 }  // namespace tpk

@@ -105,13 +105,21 @@ struct RopeRows {
   int64_t F;
   int32_t Hq, Hkv, D, rot;
   int32_t per;                       // positions per block
+  uint32_t inv_pos, inv_head;        // 2^32 / pieces of a position, of a head, rounded up
   float factor, sign;
 };
+
+// a / b by the reciprocal inv = 2^32 / b, rounded up: exact while a * b < 2^32
+// (a block's several positions are few pieces; a position has 2^16 heads of 64
+// pieces at most).
+__device__ __forceinline__ int quotient(int a, int b, uint32_t inv) {
+  return b == 1 ? a : static_cast<int>(__umulhi(static_cast<uint32_t>(a), inv));
+}
 
 // A piece is 16 bytes of a head, or, for a rotated piece of the half layout,
 // the two whose channels make pairs.
 template <bool kInter>
-__global__ void __launch_bounds__(kThreads) rope_rows_kernel(const RopeRows p, const Fractions fr) {
+__global__ void __launch_bounds__(kThreads, 4) rope_rows_kernel(const RopeRows p, const Fractions fr) {
   __shared__ __align__(16) float2 cs[kRowsMost * kMostPairs];
   const int pairs = p.rot / 2;
   const int64_t f0 = static_cast<int64_t>(blockIdx.x) * p.per;
@@ -129,8 +137,8 @@ __global__ void __launch_bounds__(kThreads) rope_rows_kernel(const RopeRows p, c
       const int it = i0 + j * kThreads;
       at[j] = -1;
       if (it >= items) continue;
-      const int pos = it / per_pos, rem = it - pos * per_pos;
-      const int h = rem / per_head, c = rem - h * per_head;
+      const int pos = p.per == 1 ? 0 : quotient(it, per_pos, p.inv_pos), rem = it - pos * per_pos;
+      const int h = quotient(rem, per_head, p.inv_head), c = rem - h * per_head;
       const int64_t f = f0 + pos;
       const __nv_bfloat16* src;
       if (h < p.Hq) {
@@ -269,6 +277,9 @@ extern "C" int tpk_rope_by_depth_ex(const void* q_in, int64_t ld_q, const void* 
   const int64_t per_pos = int64_t{p.Hq + p.Hkv} * ((inter ? rot / 8 : rot / 16) + (d - rot) / 8);
   int64_t per = kThreads * kRowItems / per_pos;
   p.per = static_cast<int32_t>(per < 1 ? 1 : per > kRowsMost ? kRowsMost : per);
+  const int64_t per_head = (inter ? rot / 8 : rot / 16) + (d - rot) / 8;
+  p.inv_pos = static_cast<uint32_t>(((int64_t{1} << 32) + per_pos - 1) / per_pos);
+  p.inv_head = static_cast<uint32_t>(((int64_t{1} << 32) + per_head - 1) / per_head);
   const int64_t blocks = (F + p.per - 1) / p.per;
   if (blocks > 0x7fffffff) return TPK_E_OVERFLOW;
   cudaStream_t s = static_cast<cudaStream_t>(stream);

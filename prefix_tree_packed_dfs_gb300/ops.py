@@ -977,8 +977,9 @@ def gated_ffn(x, w_in, w_out, act="silu", residual=None, save=False, out=None, p
 
     x [N, C], w_in [2 I, C] (the gate's rows first), w_out [O, I], residual
     [N, O] bf16; rows of x, residual and ``out`` may be strided; ``out`` may be
-    ``residual``.  Returns y [N, O]; with ``save`` (y, pre [N, 2 I], a [N, I]),
-    what ``gated_ffn_bwd`` needs."""
+    ``residual``.  Returns y [N, O]; with ``save`` (y, pre, a), what
+    ``gated_ffn_bwd`` needs: pre uint8, g and u in a form of the library's own,
+    a [N, I] bf16."""
     lib = B.load()
     N, C, I, O, p_x, ld_x, p_in, p_out = _ffn_args(x, w_in, w_out)
     k = _activation(act)
@@ -989,7 +990,7 @@ def gated_ffn(x, w_in, w_out, act="silu", residual=None, save=False, out=None, p
     out, p_y, ld_y = _out_rows(out, (N, O), "out", x)
     p_pre = p_a = None
     if save:
-        pre, p_pre = _out(pre, torch.bfloat16, (N, 2 * I), "pre", x)
+        pre, p_pre = _out(pre, torch.uint8, (lib.tpk_gated_ffn_saved_bytes(N, I),), "pre", x)
         a, p_a = _out(a, torch.bfloat16, (N, I), "a", x)
     p_err = _dev_err(dev_err)
     ws = _workspace(workspace, lib.tpk_gated_ffn_workspace_bytes(N, C, I, O, 0), x, "the block")
@@ -1009,7 +1010,8 @@ def gated_ffn_bwd(x, w_in, w_out, dy, pre, a, act="silu", dx=None, dw_in=None, d
     N, C, I, O, p_x, ld_x, p_in, p_out = _ffn_args(x, w_in, w_out)
     k = _activation(act)
     p_dy, ld_dy = _rows2(dy, "dy", (N, O))
-    p_pre, p_a = _arg(pre, torch.bfloat16, (N, 2 * I), "pre"), _arg(a, torch.bfloat16, (N, I), "a")
+    p_pre = _arg(pre, torch.uint8, (lib.tpk_gated_ffn_saved_bytes(N, I),), "pre")
+    p_a = _arg(a, torch.bfloat16, (N, I), "a")
     given = dx, dw_in, dw_out, workspace, dev_err
     dx, p_dx, ld_dx = _out_rows(dx, (N, C), "dx", x)
     dw_in, p_din = _out(dw_in, torch.bfloat16, (2 * I, C), "dw_in", x)
@@ -1070,8 +1072,6 @@ def rope_by_depth_ex(q, k, depth, freqs, interleaved=False, factor=1.0, inverse=
     fr = np.ascontiguousarray(freqs, dtype=np.float64)
     if fr.ndim != 1 or not 8 <= len(fr) <= min(d // 2, 128) or len(fr) % 8:
         raise ValueError("freqs must hold a multiple of 8 pairs, no more than half the head (or 128)")
-    if not np.isfinite(fr).all() or not math.isfinite(factor):
-        raise ValueError("freqs and factor must be finite")
     if d % 8 or d > 512:
         raise ValueError("heads must have a multiple of 8 channels, 512 at most, got %d" % d)
     p_depth = _arg(depth, torch.int32, (F,), "depth")
@@ -1095,7 +1095,7 @@ def rope_by_depth_ex(q, k, depth, freqs, interleaved=False, factor=1.0, inverse=
         heads.append(t.shape[1])
         outs.append(o)
     dev = _device("depth q k q_out k_out", depth, q, k, *given)
-    opts = B.RopeOpts(2 * len(fr), 1 if interleaved else 0, float(factor), fr.ctypes.data)
+    opts = B.RopeOpts(2 * len(fr), 1 if interleaved else 0, float(factor), fr.__array_interface__["data"][0])
     _launch(dev, lib.tpk_rope_by_depth_ex, at[0][0], at[0][1], at[1][0], at[1][1], at[0][2], at[0][3], at[1][2], at[1][3],
             p_depth, F, heads[0], heads[1], d, ctypes.byref(opts), 1 if inverse else 0)
     return outs[0], outs[1]

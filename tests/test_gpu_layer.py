@@ -12,8 +12,9 @@ the power of two below a value; 2^-9 of most).
    b |dz| more; dx, dw: the sums of those times the other factor's magnitude,
    the products' own e, and b of the result.  db: sum e_d + N u sum |dz|.
  * gated_ffn: a off by e_a = 1.13 e_g |u| + |act| e_u + 2^-19 (|g| + 1) |u| + b |a|;
-   its backward works on g, u and a rounded to bf16, which adds b |g|, b |u| to
-   e_g, e_u.
+   its backward works on a rounded to bf16 and on g and u kept as scaled fp16,
+   which adds 2^-11 of their value (and 2^-38 of the largest of 32 neighbours: half
+   the step of fp16's smallest numbers, 2^-25, against 2^14) to e_g, e_u.
  * rope: fp32 products of sin and cos within 2^-21: 2^-20 factor (|a| + |b|), and b.
  * policy: a share is a product of few fp32 factors and one exponential of
    |argument| < 8 (relative error below 8u + 2^-22): 2^-19 of the terms'
@@ -159,16 +160,25 @@ def test_gated_ffn(ops, n, c, i, o, act, res):
     R = None if r is None else _f64(r)
     ry, rgu, ra = ol.gated_ffn(X, WI, WO, act, R)
     g, u, e_g, e_u, v, _, e_a = _ffn_parts(X, WI, WO, act)
-    _within(pre, rgu, BF * np.abs(rgu) + 1.01 * np.concatenate([e_g, e_u], 1), "pre")
+    keep = lambda t, e: 2.0 ** -11 * (np.abs(t) + e) + 2.0 ** -38 * (np.abs(t) + e).max(1, keepdims=True)
+    k_g, k_u = keep(g, e_g), keep(u, e_u)
+    half = pre[:4 * n * i].view(torch.float16).view(n, 2, i).double().cpu().numpy()
+    groups, rows = -(-i // 32), -(-n // 128) * 128
+    exps = pre[4 * n * i:].view(2, groups, rows)[:, :, :n].cpu().numpy().astype(np.int64)
+    unscale = np.repeat(2.0 ** (exps - 141), 32, 1)[:, :i].transpose(2, 0, 1)
+    got = (half * unscale).reshape(n, 2 * i)
+    err_pre = np.abs(got - rgu)
+    assert (err_pre <= np.concatenate([k_g + e_g, k_u + e_u], 1)).all(), "pre: off by %.3g" % err_pre.max()
     _within(a, ra, e_a, "a")
     tol = BF * np.abs(ry) + e_a @ np.abs(WO).T + (i + 2) * 2.0 ** -23 * (np.abs(ra) @ np.abs(WO).T) * 1.01
     tol = tol + 2 * U * (0 if R is None else np.abs(R) + np.abs(ry))
     _within(y, ry, tol, "y")
-    assert torch.equal(y, ops.gated_ffn(x, w_in, w_out, act=act, residual=r))   # nothing kept: the same result
+    y2 = ops.gated_ffn(x, w_in, w_out, act=act, residual=r)   # nothing kept
+    _within(y2, ry, tol, "y with nothing kept")
     if res:
         r2 = r.clone()
         ops.gated_ffn(x, w_in, w_out, act=act, residual=r2, out=r2)
-        assert torch.equal(r2, y)
+        assert torch.equal(r2, y2)
     dy = _rnd(6, n, 2 * o)[:, :o]
     dx, dwi, dwo = ops.gated_ffn_bwd(x, w_in, w_out, dy, pre, a, act=act, dev_err=err)
     assert int(err) == 0
@@ -176,7 +186,7 @@ def test_gated_ffn(ops, n, c, i, o, act, res):
     rx, rwi, rwo = ol.gated_ffn_bwd(X, WI, WO, D, act)
     slope = ol.act(g, act)[1]
     da, e_da = D @ WO, (o + 2) * 2.0 ** -23 * (np.abs(D) @ np.abs(WO))
-    q_g, q_u = e_g + BF * (np.abs(g) + e_g), e_u + BF * (np.abs(u) + e_u)     # of g, u as kept
+    q_g, q_u = e_g + k_g, e_u + k_u     # of g, u as kept
     top = np.abs(da) + e_da
     curve = 0.0 if act == "none" else 1.2
     e_dg = e_da * (np.abs(u) + q_u) * 1.13 + np.abs(da) * (q_u * 1.13 + (np.abs(u) + q_u) * (curve * q_g + 2.0 ** -19))
