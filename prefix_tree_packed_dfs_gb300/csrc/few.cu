@@ -1,6 +1,6 @@
 // A few rows times a weight matrix: one read of the weights is all the time
 // there is.  The operands change places: 128 rows of the weights are the MMA's
-// M, the tokens (16, 32 or 64, padded by the TMA with zeros) its N.  A tile's K
+// M, the tokens (16, 32, 48 or 64, padded by the TMA with zeros) its N.  A tile's K
 // is shared out over a cluster of up to 8 CTAs, so that a few dozen tiles keep
 // every SM loading; each CTA streams its share through a ring of TMA stages,
 // and the partial sums meet through distributed shared memory, added in the
@@ -51,7 +51,7 @@ __global__ void __launch_bounds__(kFewThreads) few_kernel(const __grid_constant_
   Sm& S = *reinterpret_cast<Sm*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   float* red = reinterpret_cast<float*>(S.a[0]);   // [kTok][128], once the stages have been read
   static_assert(kTok * 512 <= kS * kBoxBytes, "partial sums");
-  constexpr int kCols = kTok < 32 ? 32 : kTok;     // TMEM columns
+  constexpr int kCols = kTok <= 32 ? 32 : 64;     // TMEM columns
   const int warp = threadIdx.x >> 5;
   uint32_t rank, ranks;
   asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(rank));
@@ -61,6 +61,17 @@ __global__ void __launch_bounds__(kFewThreads) few_kernel(const __grid_constant_
   const int nk = static_cast<int>(static_cast<int64_t>(p.k_iters) * (rank + 1) / ranks) - k0;
   volatile int* abort_flag = &S.abort_flag;
 
+  if (kGated) ptx::dependents_launch();
+  auto weights = [&](int st, int k) {
+    ptx::mbar_arrive_expect_tx(&S.full[st], kBoxBytes + kTok * 128);
+    if (kGated) {
+      ptx::tma_load_2d(S.a[st], &maps.w, &S.full[st], (k0 + k) * 64, tile * 64);
+      ptx::tma_load_2d(S.a[st] + kBoxBytes / 2, &maps.w2, &S.full[st], (k0 + k) * 64, tile * 64);
+    } else {
+      ptx::tma_load_2d(S.a[st], &maps.w, &S.full[st], (k0 + k) * 64, tile * 128);
+    }
+  };
+  const int first = nk < kS ? nk : kS;
   if (threadIdx.x == 0) {
     for (int s = 0; s < kS; ++s) {
       ptx::mbar_init(&S.full[s], 1);
@@ -69,6 +80,9 @@ __global__ void __launch_bounds__(kFewThreads) few_kernel(const __grid_constant_
     ptx::mbar_init(&S.done, 1);
     S.abort_flag = 0;
     ptx::fence_mbar_init();
+    // the first weights are on their way while the CTA sets itself up; they wait
+    // for no earlier kernel
+    for (int k = 0; k < first; ++k) weights(k, k);
   }
   if (warp == 2) {
     ptx::tmem_alloc(&S.tmem_base, kCols);
@@ -78,21 +92,8 @@ __global__ void __launch_bounds__(kFewThreads) few_kernel(const __grid_constant_
   __syncthreads();
   ptx::tc_fence_after();
   const uint32_t tmem = S.tmem_base;
-  if (kGated) ptx::dependents_launch();
   if (warp == 0) {
-    if (ptx::elect_one()) {
-      auto weights = [&](int st, int k) {
-        ptx::mbar_arrive_expect_tx(&S.full[st], kBoxBytes + kTok * 128);
-        if (kGated) {
-          ptx::tma_load_2d(S.a[st], &maps.w, &S.full[st], (k0 + k) * 64, tile * 64);
-          ptx::tma_load_2d(S.a[st] + kBoxBytes / 2, &maps.w2, &S.full[st], (k0 + k) * 64, tile * 64);
-        } else {
-          ptx::tma_load_2d(S.a[st], &maps.w, &S.full[st], (k0 + k) * 64, tile * 128);
-        }
-      };
-      // the weights wait for no earlier kernel
-      const int first = nk < kS ? nk : kS;
-      for (int k = 0; k < first; ++k) weights(k, k);
+    if (threadIdx.x == 0) {
       ptx::dependency_wait();
       for (int k = 0; k < first; ++k) ptx::tma_load_2d(S.b[k], &maps.x, &S.full[k], (k0 + k) * 64, 0);
       int issued = first;
@@ -183,8 +184,9 @@ __global__ void __launch_bounds__(kFewThreads) few_kernel(const __grid_constant_
   ptx::cluster_sync();   // nobody reads a CTA that has gone
 }
 
-// CTAs that share a tile's K: as many as keep two CTAs per SM busy, each with
-// two stages or more.
+// CTAs that share a tile's K: as many as run together, two per SM, each with two
+// stages or more.  (One token, width 8,192 to 2,048, 16 tiles: 8 CTAs each 8.4 us, 4
+// 10.3, 1 27; 40 tokens, 192 gated tiles of width 4,096: 1 CTA each 36 us, 4 43.)
 int few_ranks(int64_t tiles, int k_iters) {
   int s = kFewCluster;
   while (s > 1 && (tiles * s > 2 * num_sms() || k_iters < 2 * s)) s /= 2;
@@ -217,11 +219,12 @@ int few_launch(const FewMaps& m, const FewParams& p, bool after, cudaStream_t s)
 
 template <bool kGated>
 int few_dispatch(const Mat& x, FewMaps& m, const FewParams& p, bool after, cudaStream_t s) {
-  const int tok = p.N <= 16 ? 16 : p.N <= 32 ? 32 : 64;
+  const int tok = (p.N + 15) / 16 * 16;
   const int st = map_of(&m.x, x, tok);
   if (st != TPK_OK) return st;
   return tok == 16   ? few_launch<16, kGated>(m, p, after, s)
          : tok == 32 ? few_launch<32, kGated>(m, p, after, s)
+         : tok == 48 ? few_launch<48, kGated>(m, p, after, s)
                      : few_launch<64, kGated>(m, p, after, s);
 }
 

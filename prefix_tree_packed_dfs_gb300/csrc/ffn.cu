@@ -16,7 +16,7 @@ namespace {
 
 struct FfnWork {
   __nv_bfloat16 *a = nullptr, *dgu = nullptr;
-  float* acc = nullptr;
+  float *acc = nullptr, *acc_in = nullptr, *acc_out = nullptr;
 };
 size_t carve(uint8_t* base, int64_t N, int64_t C, int64_t I, int64_t O, bool backward, bool own_a, FfnWork* w) {
   FfnWork o;
@@ -31,9 +31,9 @@ size_t carve(uint8_t* base, int64_t N, int64_t C, int64_t I, int64_t O, bool bac
     if (N > kFewRows) o.acc = reinterpret_cast<float*>(take(acc_bytes(N, O, I)));
   } else {
     o.dgu = reinterpret_cast<__nv_bfloat16*>(take(static_cast<size_t>(N) * 2 * I * 2));
-    size_t most = acc_bytes(N, C, 2 * I);
-    for (size_t b : {acc_bytes(2 * I, C, N), acc_bytes(O, I, N)}) most = b > most ? b : most;
-    o.acc = reinterpret_cast<float*>(take(most));
+    o.acc = reinterpret_cast<float*>(take(acc_bytes(N, C, 2 * I)));
+    o.acc_in = reinterpret_cast<float*>(take(acc_bytes(2 * I, C, N)));
+    o.acc_out = reinterpret_cast<float*>(take(acc_bytes(O, I, N)));
   }
   if (w) *w = o;
   return at;
@@ -167,17 +167,22 @@ extern "C" int tpk_gated_ffn_bwd(const void* x, int64_t ld_x, const void* w_in, 
   st = map_of(&m.a, mdy, kHalf);
   if (st == TPK_OK) st = map_of(&m.b, Mat{w_out, O, I, I}, 64);
   const Saved k16 = saved_of(const_cast<void*>(saved), N, I);
-  if (st == TPK_OK) st = map_of(&m.in, k16.g, kHalf, 32);
-  if (st == TPK_OK) st = map_of(&m.in2, k16.u, kHalf, 32);
-  if (st == TPK_OK) st = map_of(&m.out, Mat{k.dgu, N, I, wide}, kHalf, 32);
-  if (st == TPK_OK) st = map_of(&m.out2, Mat{k.dgu + I, N, I, wide}, kHalf, 32);
+  if (st == TPK_OK) st = map_of(&m.in, k16.g, kHalf);
+  if (st == TPK_OK) st = map_of(&m.in2, k16.u, kHalf);
+  if (st == TPK_OK) st = map_of(&m.out, Mat{k.dgu, N, I, wide}, kHalf);
+  if (st == TPK_OK) st = map_of(&m.out2, Mat{k.dgu + I, N, I, wide}, kHalf);
   Params p = params(N, I, O, act, dev_err);
   p.exps = k16.exps;
   p.exp_rows = exp_rows(N);
   if (st == TPK_OK) st = launch<kGateBwd, true>(m, p, false, s);
   const Mat dgu{k.dgu, N, wide, wide};
-  if (st == TPK_OK) st = input_product(dgu, Mat{w_in, wide, C, C}, Mat{dx, N, C, ld_dx}, k.acc, true, dev_err, s);
-  if (st == TPK_OK) st = weight_product(dgu, mx, Mat{dw_in, wide, C, C}, k.acc, true, dev_err, s);
-  if (st == TPK_OK) st = weight_product(mdy, Mat{a, N, I, I}, Mat{dw_out, O, I, I}, k.acc, true, dev_err, s);
+  const Mat mdx{dx, N, C, ld_dx}, mdin{dw_in, wide, C, C}, mdout{dw_out, O, I, I};
+  Params px, pin, pout;
+  if (st == TPK_OK) st = input_product(dgu, Mat{w_in, wide, C, C}, mdx, k.acc, true, dev_err, s, &px);
+  if (st == TPK_OK) st = weight_product(dgu, mx, mdin, k.acc_in, px, dev_err, s, &pin);
+  if (st == TPK_OK) st = weight_product(mdy, Mat{a, N, I, I}, mdout, k.acc_out, pin, dev_err, s, &pout);
+  if (st == TPK_OK) st = join_left(px, mdx, s);
+  if (st == TPK_OK) st = join_left(pin, mdin, s);
+  if (st == TPK_OK) st = join_left(pout, mdout, s);
   return st;
 }

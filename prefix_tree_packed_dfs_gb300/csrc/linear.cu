@@ -37,10 +37,11 @@ struct Eight<float> {
 // out[b][c] = sum of the rows b * per .. of m: a CTA takes 256 columns of `per` rows.
 template <typename T>
 __global__ void __launch_bounds__(kSumThreads) column_sum_kernel(const T* __restrict__ m, int64_t rows, int cols,
-                                                                 int64_t ld, int64_t per, float* __restrict__ out) {
+                                                                 int64_t ld, int64_t per, float* __restrict__ out,
+                                                                 int early) {
   __shared__ float4 part[8][32][2];
   ptx::dependents_launch();
-  ptx::dependency_wait();
+  if (!early) ptx::dependency_wait();
   const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
   const int c = blockIdx.x * kSumCols + lane * 8;
   const int64_t lo = static_cast<int64_t>(blockIdx.y) * per, hi = lo + per < rows ? lo + per : rows;
@@ -52,14 +53,16 @@ __global__ void __launch_bounds__(kSumThreads) column_sum_kernel(const T* __rest
   part[w][lane][0] = make_float4(v[0], v[1], v[2], v[3]);
   part[w][lane][1] = make_float4(v[4], v[5], v[6], v[7]);
   __syncthreads();
-  if (w >= 2 || c >= cols) return;
-  float4 s = part[0][lane][w];
+  if (w < 2 && c < cols) {
+    float4 s = part[0][lane][w];
 #pragma unroll
-  for (int i = 1; i < 8; ++i) {
-    const float4 x = part[i][lane][w];
-    s.x += x.x; s.y += x.y; s.z += x.z; s.w += x.w;
+    for (int i = 1; i < 8; ++i) {
+      const float4 x = part[i][lane][w];
+      s.x += x.x; s.y += x.y; s.z += x.z; s.w += x.w;
+    }
+    *reinterpret_cast<float4*>(out + static_cast<int64_t>(blockIdx.y) * cols + c + w * 4) = s;
   }
-  *reinterpret_cast<float4*>(out + static_cast<int64_t>(blockIdx.y) * cols + c + w * 4) = s;
+  if (early) ptx::dependency_wait();
 }
 
 // Row blocks of the first pass: enough CTAs for two per SM, 32 rows each or more.
@@ -75,17 +78,17 @@ int64_t sum_blocks(int64_t rows, int64_t cols) {
   return (rows + per - 1) / per;
 }
 
+// Needs nothing of the stream's last kernel (as a product's `early`).
 template <typename T>
-int column_sums(const T* m, int64_t rows, int64_t cols, int64_t ld, float* part, float* out, bool after,
-                cudaStream_t s) {
+int column_sums(const T* m, int64_t rows, int64_t cols, int64_t ld, float* part, float* out, cudaStream_t s) {
   const unsigned across = static_cast<unsigned>((cols + kSumCols - 1) / kSumCols);
   const int64_t per = sum_rows(rows, cols), blocks = sum_blocks(rows, cols);
   const int n = static_cast<int>(cols);
-  const int st = launch_kernel(column_sum_kernel<T>, dim3(across, static_cast<unsigned>(blocks)), kSumThreads, 0, after,
-                               s, m, rows, n, ld, per, blocks == 1 ? out : part);
+  const int st = launch_kernel(column_sum_kernel<T>, dim3(across, static_cast<unsigned>(blocks)), kSumThreads, 0, true,
+                               s, m, rows, n, ld, per, blocks == 1 ? out : part, 1);
   if (st != TPK_OK || blocks == 1) return st;
   return launch_kernel(column_sum_kernel<float>, dim3(across), kSumThreads, 0, true, s, static_cast<const float*>(part),
-                       blocks, n, cols, blocks, out);
+                       blocks, n, cols, blocks, out, 0);
 }
 
 // The sum of a split product's partial tiles, 8 columns per thread, and kLin's
@@ -174,7 +177,7 @@ int longest(const Params& p) {
 
 struct LinearWork {
   __nv_bfloat16* dz = nullptr;
-  float *sums = nullptr, *part = nullptr, *acc = nullptr;
+  float *sums = nullptr, *part = nullptr, *acc = nullptr, *acc_w = nullptr;
 };
 size_t carve(uint8_t* base, int64_t N, int64_t C, int64_t O, int32_t act, bool backward, LinearWork* w) {
   LinearWork o;
@@ -192,8 +195,8 @@ size_t carve(uint8_t* base, int64_t N, int64_t C, int64_t O, int32_t act, bool b
       o.sums = reinterpret_cast<float*>(take(static_cast<size_t>((N + 31) / 32) * O * 4));
     }
     o.part = reinterpret_cast<float*>(take(static_cast<size_t>(kSumMost) * O * 4));
-    const size_t x = acc_bytes(N, C, O), y = acc_bytes(O, C, N);
-    o.acc = reinterpret_cast<float*>(take(x > y ? x : y));
+    o.acc = reinterpret_cast<float*>(take(acc_bytes(N, C, O)));
+    o.acc_w = reinterpret_cast<float*>(take(acc_bytes(O, C, N)));
   }
   if (w) *w = o;
   return at;
@@ -226,26 +229,34 @@ int linear_product(const Mat& x, const Mat& w, const float* bias, int act, const
   return st == TPK_OK && p.splits > 1 ? join(p, bias, act, residual, y, s) : st;
 }
 
-int input_product(const Mat& dz, const Mat& w, const Mat& dx, float* acc, bool after, int32_t* err, cudaStream_t s) {
+int input_product(const Mat& dz, const Mat& w, const Mat& dx, float* acc, bool after, int32_t* err, cudaStream_t s,
+                  Params* left) {
   Maps m;
   int st = map_of(&m.a, dz, kHalf);
   if (st == TPK_OK) st = map_of(&m.b, w, 64);
   if (st == TPK_OK) st = map_of(&m.out, dx, kHalf);
   if (st != TPK_OK) return st;
-  const Params p = params(dz.rows, w.cols, dz.cols, true, acc, err);
-  st = longest(p) <= kChunk ? launch<kDx, true>(m, p, after, s) : launch<kDx, false>(m, p, after, s);
-  return st == TPK_OK && p.splits > 1 ? join(p, nullptr, TPK_ACT_NONE, Mat{}, dx, s) : st;
+  Params p = params(dz.rows, w.cols, dz.cols, true, acc, err);
+  p.late = 1;
+  *left = p;
+  return longest(p) <= kChunk ? launch<kDx, true>(m, p, after, s) : launch<kDx, false>(m, p, after, s);
 }
 
-int weight_product(const Mat& dz, const Mat& x, const Mat& dw, float* acc, bool after, int32_t* err, cudaStream_t s) {
+int weight_product(const Mat& dz, const Mat& x, const Mat& dw, float* acc, const Params& before, int32_t* err,
+                   cudaStream_t s, Params* left) {
   Maps m;
   int st = map_of(&m.a, dz, 64);
   if (st == TPK_OK) st = map_of(&m.b, x, 64);
   if (st == TPK_OK) st = map_of(&m.out, dw, kHalf);
   if (st != TPK_OK) return st;
-  const Params p = params(dz.cols, x.cols, dz.rows, true, acc, err);
-  st = longest(p) <= kChunk ? launch<kDw, true>(m, p, after, s) : launch<kDw, false>(m, p, after, s);
-  return st == TPK_OK && p.splits > 1 ? join(p, nullptr, TPK_ACT_NONE, Mat{}, dw, s) : st;
+  Params p = params(dz.cols, x.cols, dz.rows, true, acc, err);
+  p.early = shape_of<kDx>(before).units < kPairs;
+  *left = p;
+  return longest(p) <= kChunk ? launch<kDw, true>(m, p, true, s) : launch<kDw, false>(m, p, true, s);
+}
+
+int join_left(const Params& left, const Mat& out, cudaStream_t s) {
+  return left.splits > 1 ? join(left, nullptr, TPK_ACT_NONE, Mat{}, out, s) : TPK_OK;
 }
 
 }  // namespace product
@@ -317,12 +328,16 @@ extern "C" int tpk_linear_bwd(const void* x, int64_t ld_x, const void* w, const 
     p.act = act;
     p.colsum = db ? k.sums : nullptr;
     if (st == TPK_OK) st = launch<kDz, true>(m, p, false, s);
-    if (st == TPK_OK && db) st = column_sums(k.sums, (N + 31) / 32, O, O, k.part, db, true, s);
-  } else if (db) {
-    st = column_sums(static_cast<const __nv_bfloat16*>(dy), N, O, ld_dy, k.part, db, false, s);
   }
-  if (st == TPK_OK)
-    st = input_product(dz, mw, Mat{dx, N, C, ld_dx}, k.acc, act != TPK_ACT_NONE || db, dev_err, s);
-  if (st == TPK_OK) st = weight_product(dz, mx, Mat{dw, O, C, C}, k.acc, true, dev_err, s);
+  const Mat mdx{dx, N, C, ld_dx}, mdw{dw, O, C, C};
+  Params px, pw;
+  if (st == TPK_OK) st = input_product(dz, mw, mdx, k.acc, act != TPK_ACT_NONE, dev_err, s, &px);
+  if (st == TPK_OK) st = weight_product(dz, mx, mdw, k.acc_w, px, dev_err, s, &pw);
+  if (st == TPK_OK && db)
+    st = act != TPK_ACT_NONE
+             ? column_sums(k.sums, (N + 31) / 32, O, O, k.part, db, s)
+             : column_sums(static_cast<const __nv_bfloat16*>(dy), N, O, ld_dy, k.part, db, s);
+  if (st == TPK_OK) st = join_left(px, mdx, s);
+  if (st == TPK_OK) st = join_left(pw, mdw, s);
   return st;
 }

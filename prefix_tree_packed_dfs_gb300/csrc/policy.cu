@@ -196,8 +196,8 @@ __device__ __forceinline__ Pair block_sum(Pair v, int& n) {
 }
 
 // A CTA per sequence: ratio = exp(mean log-ratio of its tokens that carry loss).
-constexpr int kSeqThreads = 512;
-__global__ void __launch_bounds__(kSeqThreads) policy_sequence_kernel(const Policy p) {
+constexpr int kSeqThreads = 256;
+__global__ void __launch_bounds__(kSeqThreads, 4) policy_sequence_kernel(const Policy p) {
   ptx::dependents_launch();
   __shared__ Clip clip;
   auto inside = [&](int64_t x) { return x < 0 ? 0 : x > p.R ? p.R : x; };

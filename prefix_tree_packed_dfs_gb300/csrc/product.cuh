@@ -32,10 +32,20 @@
 // 2^-29 of its group's largest still has its 11 bits); with g and u in bf16 the
 // gradients' error over fp64 was 3.0e-3 of their norm against 2.4e-3 with them
 // unrounded, of which 1.7e-3 is the results' own rounding.
-// Kernels of one call overlap at their ends (programmatic dependent launch):
-// each sets itself up and then waits for the one before.
+// Kernels of one call overlap (programmatic dependent launch): each sets itself
+// up under the one before and then waits for it.  A product that needs nothing of
+// the one before, where that one leaves SMs free (early), takes them at once and
+// waits at its end, so that a kernel that is done means that those before it are
+// (1,001 rows, widths 1,000 and 552, forward and backward: 50 us against 56; beside
+// a product that fills the GPU it costs 1%).
 // Warps of a CTA: 0 TMA producer, 1 MMA issuer (of the pair's first CTA), 2
-// TMEM owner, 4-11 epilogue (two warpgroups).  CTAs are persistent and walk the
+// TMEM owner, 4-11 epilogue (two warpgroups).  kGateBwd moves 64 columns of g and
+// u in and of dg and du out at a time, through two places; warp 3 carries them, so
+// that a place is filled again, for the next tile too, as soon as its results have
+// left.  Its g and u come in beside operands that take 64 bytes per cycle and SM
+// alone, which is what bounds it: 32,768 rows, widths 2,048 and 8,192, 711 us (1.55
+// PFLOP/s; the same product without them 545).  With four stages and three places
+// it took 790, with boxes of 32 columns 740, with g and u sent ahead to L2 776.  CTAs are persistent and walk the
 // tiles in panels of 8 columns of tiles, so that the pairs running together
 // share rows of A and of B in L2.
 #pragma once
@@ -79,6 +89,8 @@ struct Params {
   int32_t act;
   int32_t has_in;            // kLin: a residual
   int32_t save;              // kGate: g and u go out too
+  int32_t early;             // needs nothing of the kernel before, only of those that it waited for
+  int32_t late;              // lets the next kernel start only after its own wait (that one may be early)
   const float* bias;         // [N] or nullptr
   float* colsum;             // kDz: [ceil(M / 32)][N] sums of 32 rows of dz; nullptr: none
   float* acc;                // splits > 1: [splits][tiles - whole][256 * 256]
@@ -90,10 +102,10 @@ struct Params {
 struct Smem {
   uint8_t a[kStages][kBoxBytes];
   uint8_t b[kStages][kBoxBytes];
-  uint8_t out[2][2][kBoxBytes];        // per warpgroup
+  uint8_t out[2][2][kBoxBytes];        // two boxes per warpgroup; kGateBwd: two places of g and u
   uint64_t full[kStages], empty[kStages];
   uint64_t tm_full[2], tm_empty[2];
-  uint64_t in_full[2][2];
+  uint64_t in_full[2][2], written[2];
   uint64_t drain;
   uint32_t tmem_base;
   int abort_flag;
@@ -114,7 +126,7 @@ inline Split split_of(int64_t tiles, int64_t k_iters) {
   Split s{tiles, 0, 1};
   const int64_t tail = tiles % kPairs;
   if (tail == 0) return s;
-  const double tile_us = 0.135 * static_cast<double>(k_iters);   // 64 elements of K: 256 cycles
+  const double tile_us = 0.27 * static_cast<double>(k_iters);   // 64 elements of K: 512 cycles
   double best = tile_us;
   for (int64_t n = 2; n <= k_iters / 4 && n <= (tail * 8 < kPairs ? kPairs / tail : 8); ++n) {
     const int64_t rounds = (tail * n + kPairs - 1) / kPairs;
@@ -190,12 +202,6 @@ __device__ __forceinline__ void get64(const uint8_t* box, int r, int half, uint3
     o[4 * q] = v.x; o[4 * q + 1] = v.y; o[4 * q + 2] = v.z; o[4 * q + 3] = v.w;
   }
 }
-// The same for boxes of 32 columns in the 64-byte swizzle (piece i of row r at
-// piece i ^ (r / 2 % 4)).
-__device__ __forceinline__ uint8_t* at32(uint8_t* box, int r, int q) {
-  return box + r * 64 + ((q ^ ((r >> 1) & 3)) * 16);
-}
-
 // The biased exponent of the largest finite magnitude of x, within [15, 254].
 __device__ __forceinline__ uint32_t largest_exponent(const uint32_t (&x)[32]) {
   float top[4] = {};
@@ -260,6 +266,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       ptx::mbar_init(&S.tm_empty[b], 2 * kEpiThreads / 32);   // every epilogue warp of the pair
       ptx::mbar_init(&S.in_full[0][b], 1);
       ptx::mbar_init(&S.in_full[1][b], 1);
+      ptx::mbar_init(&S.written[b], kEpiThreads / 32);
     }
     ptx::mbar_init(&S.drain, 1);
     S.abort_flag = 0;
@@ -275,8 +282,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   ptx::cluster_sync();   // the other CTA's barriers exist
   ptx::tc_fence_after();
   const uint32_t tmem = S.tmem_base;
-  ptx::dependents_launch();
-  ptx::dependency_wait();   // what the kernel before wrote is there
+  if (!p.late) ptx::dependents_launch();
+  if (!p.early) ptx::dependency_wait();   // what the kernel before wrote is there
+  if (p.late) ptx::dependents_launch();
   if (warp < 4) {
     if constexpr (!kOne) ptx::regs_dec<kRegsCtl>();
     if (warp == 0) {
@@ -359,6 +367,46 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         ptx::mbar_drain(&S.drain, 0);
       }
     }
+    if constexpr (kMode == kGateBwd) {
+      if (warp == 3 && ptx::elect_one()) {
+        // ---------------------------------------------------------- carrier
+        const int mine = pair < sh.units ? (sh.units - 1 - pair) / n_pairs + 1 : 0;   // tiles of this pair
+        auto place = [&](int q, int& col, int& row) {   // of the q-th 64 columns
+          const Unit w = unit_of(p, sh, pair + (q >> 2) * n_pairs);
+          col = w.n * kTile + (q & 3) * 64;
+          row = w.m * kTile + static_cast<int>(rank) * kHalf;
+        };
+        auto fetch = [&](int q) {
+          int col, row;
+          place(q, col, row);
+          uint64_t* bar = &S.in_full[0][q & 1];
+          ptx::mbar_arrive_expect_tx(bar, 2 * kBoxBytes);
+          ptx::tma_load_2d(S.out[q & 1][0], &maps.in, bar, col, row);
+          ptx::tma_load_2d(S.out[q & 1][1], &maps.in2, bar, col, row);
+        };
+        const int n = 4 * mine;
+        int issued = n < 2 ? n : 2;
+        for (int q = 0; q < issued; ++q) fetch(q);
+        for (int q = 0; q < n; ++q) {
+          if (!ptx::mbar_wait(&S.written[q & 1], (q >> 1) & 1, abort_flag, kWaitLimitNs)) break;
+          int col, row;
+          place(q, col, row);
+          if (col < p.N && row < p.M) {
+            ptx::tma_store_2d(&maps.out, S.out[q & 1][0], col, row);
+            ptx::tma_store_2d(&maps.out2, S.out[q & 1][1], col, row);
+          }
+          ptx::bulk_commit();
+          if (issued < n) {
+            ptx::bulk_wait_read<0>();
+            fetch(issued++);
+          }
+        }
+        // after a timeout: no copy is left under way
+        for (int q = issued > 2 ? issued - 2 : 0; q < issued; ++q)
+          ptx::mbar_drain(&S.in_full[0][q & 1], (q >> 1) & 1);
+        ptx::bulk_wait_all();
+      }
+    }
   } else {
     // ------------------------------------------------------------ epilogue
     if constexpr (!kOne) ptx::regs_inc<kRegsEpi>();
@@ -378,17 +426,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       const Unit w = unit_of(p, sh, u);
       const bool takes = kMode == kDz || kMode == kGateBwd || (kMode == kLin && p.has_in && w.split < 0);
       const int row0 = w.m * kTile + static_cast<int>(rank) * kHalf;   // first row of this CTA
-      const int n0 = w.n * kTileN<kMode> + wg * (kTileN<kMode> / 2);   // first column of this warpgroup
+      // first column of this warpgroup; kGateBwd: of its 32 in every 64
+      const int n0 = w.n * kTileN<kMode> + wg * (kMode == kGateBwd ? 32 : kTileN<kMode> / 2);
       // what the epilogue reads, into the boxes that it will leave from
       auto fetch = [&](int s, int col) {
-        if constexpr (kMode == kGateBwd) {
-          ptx::mbar_arrive_expect_tx(&S.in_full[wg][s], kBoxBytes);
-          ptx::tma_load_2d(box[s], &maps.in, &S.in_full[wg][s], col, row0);
-          ptx::tma_load_2d(box[s] + kBoxBytes / 2, &maps.in2, &S.in_full[wg][s], col, row0);
-        } else {
-          ptx::mbar_arrive_expect_tx(&S.in_full[wg][s], kBoxBytes);
-          ptx::tma_load_2d(box[s], &maps.in, &S.in_full[wg][s], col, row0);
-        }
+        ptx::mbar_arrive_expect_tx(&S.in_full[wg][s], kBoxBytes);
+        ptx::tma_load_2d(box[s], &maps.in, &S.in_full[wg][s], col, row0);
       };
       auto fetched = [&](int s) {
         return ptx::mbar_wait(&S.in_full[wg][s], (loads[s] - 1) & 1, abort_flag, kWaitLimitNs);
@@ -398,18 +441,18 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         const int64_t groups = (p.N + kGroup - 1) / kGroup;
 #pragma unroll
         for (int c = 0; c < 4; ++c)
-          if (n0 + c * kGroup < p.N && row0 + rc < p.M) {
-            const uint8_t* e = p.exps + (n0 / kGroup + c) * p.exp_rows + row0 + rc;
+          if (n0 + c * 64 < p.N && row0 + rc < p.M) {
+            const uint8_t* e = p.exps + (n0 / kGroup + c * 2) * p.exp_rows + row0 + rc;
             exps[c] = __ldg(e) | static_cast<uint32_t>(__ldg(e + groups * p.exp_rows)) << 16;
           } else {
             exps[c] = 0x7f007fu;
           }
       }
-      if (takes) {
+      if (kMode != kGateBwd && takes) {
         if (leader) {
           ptx::bulk_wait_read<0>();   // the boxes' last results have left
           fetch(0, n0);
-          fetch(1, n0 + (kMode == kGateBwd ? 32 : 64));
+          fetch(1, n0 + 64);
         }
         ++loads[0];
         ++loads[1];
@@ -447,7 +490,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       ok = ptx::all_of_128(wg + 1, ok);
       if (!ok) break;
       const uint32_t buf = tile & 1;
-      const uint32_t tm = tmem + lane_off + buf * kTile + (kMode == kGate ? wg * 64 : wg * kHalf);
+      const uint32_t tm = tmem + lane_off + buf * kTile + wg * (kMode == kGate ? 64 : kMode == kGateBwd ? 32 : kHalf);
       if constexpr (kOne) {
         ptx::tc_fence_after();
         ++tile;
@@ -633,62 +676,47 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           ptx::bulk_commit();
         }
       } else {
-        // kGateBwd: 32 columns at a time, g and u in the two halves of a box
+        // kGateBwd: 32 of 64 columns at a time, g and u in the two boxes of a place
         uint32_t raw[2][32];
         ptx::tmem_ld32(tm, raw[0]);
         ptx::tmem_wait_ld_of(raw[0]);
 #pragma unroll
         for (int c = 0; c < 4; ++c) {
-          if (c < 3) ptx::tmem_ld32(tm + (c + 1) * 32, raw[(c + 1) & 1]);
-          const int s = c & 1, c0 = n0 + c * 32;
-          ok = fetched(s) && ok;
+          if (c < 3) ptx::tmem_ld32(tm + (c + 1) * 64, raw[(c + 1) & 1]);
+          const int s = c & 1;
+          ++loads[s];
+          ok = ptx::mbar_wait(&S.in_full[0][s], (loads[s] - 1) & 1, abort_flag, kWaitLimitNs) && ok;
           const uint64_t sg = both(group_unscale(exps[c] & 0xff)), su = both(group_unscale(exps[c] >> 16));
+          uint32_t g16[16], u16[16];
+          get64(S.out[s][0], rc, wg, g16);
+          get64(S.out[s][1], rc, wg, u16);
           with_act(p.act, [&](auto t) {
 #pragma unroll
-            for (int q = 0; q < 4; ++q) {
-              uint8_t* gp = at32(box[s], rc, q);
-              uint8_t* up = gp + kBoxBytes / 2;
-              const int4 gv = ptx::lds128i(gp), uv = ptx::lds128i(up);
-              const int gw[4] = {gv.x, gv.y, gv.z, gv.w}, uw[4] = {uv.x, uv.y, uv.z, uv.w};
-              uint32_t og[4], ou[4];
-#pragma unroll
-              for (int e = 0; e < 4; ++e) {
-                const uint64_t g = ptx::mul2(ptx::unpack_f16x2(static_cast<uint32_t>(gw[e])), sg);
-                const uint64_t u = ptx::mul2(ptx::unpack_f16x2(static_cast<uint32_t>(uw[e])), su);
-                const uint64_t da = pair_at(raw[c & 1], q * 4 + e);
-                uint64_t slope;
-                const uint64_t v = act_slope_2<decltype(t)::value>(g, slope);
-                float lo, hi;
-                ptx::unf2(ptx::mul2(ptx::mul2(da, u), slope), lo, hi);
-                og[e] = ptx::pack_bf16x2(lo, hi);
-                ptx::unf2(ptx::mul2(da, v), lo, hi);
-                ou[e] = ptx::pack_bf16x2(lo, hi);
-              }
-              *reinterpret_cast<uint4*>(gp) = make_uint4(og[0], og[1], og[2], og[3]);
-              *reinterpret_cast<uint4*>(up) = make_uint4(ou[0], ou[1], ou[2], ou[3]);
+            for (int e = 0; e < 16; ++e) {
+              const uint64_t g = ptx::mul2(ptx::unpack_f16x2(g16[e]), sg);
+              const uint64_t u = ptx::mul2(ptx::unpack_f16x2(u16[e]), su);
+              const uint64_t da = pair_at(raw[c & 1], e);
+              uint64_t slope;
+              const uint64_t v = act_slope_2<decltype(t)::value>(g, slope);
+              float lo, hi;
+              ptx::unf2(ptx::mul2(ptx::mul2(da, u), slope), lo, hi);
+              g16[e] = ptx::pack_bf16x2(lo, hi);
+              ptx::unf2(ptx::mul2(da, v), lo, hi);
+              u16[e] = ptx::pack_bf16x2(lo, hi);
             }
           });
+          put64(S.out[s][0], rc, wg, g16);
+          put64(S.out[s][1], rc, wg, u16);
           ptx::fence_async_shared();
-          meet();
-          if (leader) {
-            if (c0 < p.N && row0 < p.M) {
-              ptx::tma_store_2d(&maps.out, box[s], c0, row0);
-              ptx::tma_store_2d(&maps.out2, box[s] + kBoxBytes / 2, c0, row0);
-            }
-            ptx::bulk_commit();
-            if (c < 2) {
-              ptx::bulk_wait_read<0>();
-              fetch(s, c0 + 64);
-            }
-          }
-          if (c < 2) ++loads[s];
+          __syncwarp();
+          if (lane == 0) ptx::mbar_arrive(&S.written[s]);
           if (c < 3) ptx::tmem_wait_ld_of(raw[(c + 1) & 1]);
           if (c == 2) release();
         }
       }
       if (takes) ok = ptx::all_of_128(wg + 1, ok);   // a load that gave up
     }
-    if (leader) {
+    if (kMode != kGateBwd && leader) {
       // loads that nobody waited for (after a timeout) have arrived before the CTA leaves
       for (int s = 0; s < 2; ++s)
         if (loads[s]) ptx::mbar_drain(&S.in_full[wg][s], (loads[s] - 1) & 1);
@@ -713,6 +741,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   ptx::cluster_sync();
   ptx::tc_fence_after();
   if (warp == 2) ptx::tmem_dealloc_pair(tmem, 512);
+  if (p.early) ptx::dependency_wait();
 }
 
 // ---- host -------------------------------------------------------------------------
@@ -721,9 +750,7 @@ struct Mat {
   const void* p;
   int64_t rows, cols, ld;
 };
-inline int map_of(CUtensorMap* m, const Mat& a, int box_rows, int box_cols = 64) {
-  return make_map_2d(m, a.p, a.rows, a.cols, a.ld, box_rows, box_cols);
-}
+inline int map_of(CUtensorMap* m, const Mat& a, int box_rows) { return make_map_2d(m, a.p, a.rows, a.cols, a.ld, box_rows); }
 
 inline int64_t tiles_of(int64_t M, int64_t N) { return (M + kTile - 1) / kTile * ((N + kTile - 1) / kTile); }
 // Workspace of a product that may be split over K.
@@ -778,10 +805,14 @@ int launch(const Maps& maps, const Params& p, bool after, cudaStream_t s) {
 // y = act(x w^T + bias) + residual (residual.p may be nullptr)
 int linear_product(const Mat& x, const Mat& w, const float* bias, int act, const Mat& residual, const Mat& y,
                    float* acc, bool after, int32_t* err, cudaStream_t s);
-// dx = dz w
-int input_product(const Mat& dz, const Mat& w, const Mat& dx, float* acc, bool after, int32_t* err, cudaStream_t s);
-// dw = dz^T x
-int weight_product(const Mat& dz, const Mat& x, const Mat& dw, float* acc, bool after, int32_t* err, cudaStream_t s);
+// dx = dz w, up to join_left of *left
+int input_product(const Mat& dz, const Mat& w, const Mat& dx, float* acc, bool after, int32_t* err, cudaStream_t s,
+                  Params* left);
+// dw = dz^T x, up to join_left of *left; `before`: the stream's last kernel, a product of which it needs nothing
+int weight_product(const Mat& dz, const Mat& x, const Mat& dw, float* acc, const Params& before, int32_t* err,
+                   cudaStream_t s, Params* left);
+// The sums of a product's split tiles, where it has any.
+int join_left(const Params& left, const Mat& out, cudaStream_t s);
 
 }  // namespace product
 }  // namespace tpk
