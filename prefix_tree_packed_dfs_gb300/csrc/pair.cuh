@@ -77,6 +77,11 @@ __device__ __forceinline__ float4 lds128_cluster(const void* p, uint32_t rank) {
   return v;
 }
 
+// v into the same shared-memory object in CTA `rank` of the cluster.
+__device__ __forceinline__ void st_cluster(int* p, uint32_t rank, int v) {
+  asm volatile("st.shared::cluster.s32 [%0], %1;" ::"r"(cluster_addr(p, rank)), "r"(v) : "memory");
+}
+
 // Programmatic dependent launch: the next kernel of the stream, where it asked
 // for it, may start (launch); everything of the kernel before is done (wait).
 __device__ __forceinline__ void dependents_launch() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }

@@ -103,6 +103,7 @@ struct Smem {
   uint8_t a[kStages][kBoxBytes];
   uint8_t b[kStages][kBoxBytes];
   uint8_t out[2][2][kBoxBytes];        // two boxes per warpgroup; kGateBwd: two places of g and u
+  float bias[2][kHalf];                // of the tile at hand, per warpgroup
   uint64_t full[kStages], empty[kStages];
   uint64_t tm_full[2], tm_empty[2];
   uint64_t in_full[2][2], written[2];
@@ -273,18 +274,23 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     S.issued = 0;
     ptx::fence_mbar_init();
   }
-  if (warp == 2) {
-    ptx::tmem_alloc_pair(&S.tmem_base, 512);
-    ptx::tmem_relinquish_pair();
-  }
-  ptx::tc_fence_before();
-  __syncthreads();
-  ptx::cluster_sync();   // the other CTA's barriers exist
-  ptx::tc_fence_after();
-  const uint32_t tmem = S.tmem_base;
+  __syncwarp();
+  ptx::cluster_sync();   // both CTAs' barriers exist
   if (!p.late) ptx::dependents_launch();
   if (!p.early) ptx::dependency_wait();   // what the kernel before wrote is there
   if (p.late) ptx::dependents_launch();
+  // the producer needs no accumulator and is off
+  uint32_t tmem = 0;
+  if (warp == 2) {
+    ptx::tmem_alloc_pair(&S.tmem_base, 512);
+    ptx::tmem_relinquish_pair();
+    ptx::tc_fence_before();
+  }
+  if (warp > 0) {
+    asm volatile("bar.sync 3, %0;" ::"n"(kThreads - 32) : "memory");
+    ptx::tc_fence_after();
+    tmem = S.tmem_base;
+  }
   if (warp < 4) {
     if constexpr (!kOne) ptx::regs_dec<kRegsCtl>();
     if (warp == 0) {
@@ -404,7 +410,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         // after a timeout: no copy is left under way
         for (int q = issued > 2 ? issued - 2 : 0; q < issued; ++q)
           ptx::mbar_drain(&S.in_full[0][q & 1], (q >> 1) & 1);
-        ptx::bulk_wait_all();
+        ptx::bulk_wait_read<0>();
       }
     }
   } else {
@@ -418,8 +424,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     const uint32_t bar_empty[2] = {ptx::cluster_addr(&S.tm_empty[0], 0), ptx::cluster_addr(&S.tm_empty[1], 0)};
     uint8_t* const box[2] = {S.out[wg][0], S.out[wg][1]};
     auto meet = [&] { asm volatile("bar.sync %0, 128;" ::"r"(wg + 1) : "memory"); };
-    // loads into box s so far (each thread's count), of which the last may be under way
-    uint32_t loads[2] = {0, 0};
+    uint32_t taken = 0;   // tiles that took something in; of the last, both boxes' loads may be under way
     uint32_t tile = 0, sent = 0;
     bool ok = true;
     for (int u = pair; ok && u < sh.units; u += n_pairs) {
@@ -434,28 +439,31 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         ptx::tma_load_2d(box[s], &maps.in, &S.in_full[wg][s], col, row0);
       };
       auto fetched = [&](int s) {
-        return ptx::mbar_wait(&S.in_full[wg][s], (loads[s] - 1) & 1, abort_flag, kWaitLimitNs);
+        return ptx::mbar_wait(&S.in_full[wg][s], (taken - 1) & 1, abort_flag, kWaitLimitNs);
       };
-      uint32_t exps[4] = {};   // kGateBwd: the exponents of this row's groups, u's above g's
-      if constexpr (kMode == kGateBwd) {
-        const int64_t groups = (p.N + kGroup - 1) / kGroup;
-#pragma unroll
-        for (int c = 0; c < 4; ++c)
-          if (n0 + c * 64 < p.N && row0 + rc < p.M) {
-            const uint8_t* e = p.exps + (n0 / kGroup + c * 2) * p.exp_rows + row0 + rc;
-            exps[c] = __ldg(e) | static_cast<uint32_t>(__ldg(e + groups * p.exp_rows)) << 16;
-          } else {
-            exps[c] = 0x7f007fu;
-          }
-      }
+      // kGateBwd: the exponents of this row's groups of the c-th 64 columns, u's above g's
+      auto exponents = [&](int c) {
+        if (n0 + c * 64 >= p.N || row0 + rc >= p.M) return 0x7f007fu;
+        const uint8_t* e = p.exps + (n0 / kGroup + c * 2) * p.exp_rows + row0 + rc;
+        return __ldg(e) | static_cast<uint32_t>(__ldg(e + static_cast<int64_t>((p.N + kGroup - 1) / kGroup) * p.exp_rows)) << 16;
+      };
+      uint32_t exps = 0;
+      if constexpr (kMode == kGateBwd) exps = exponents(0);
       if (kMode != kGateBwd && takes) {
         if (leader) {
           ptx::bulk_wait_read<0>();   // the boxes' last results have left
           fetch(0, n0);
           fetch(1, n0 + 64);
         }
-        ++loads[0];
-        ++loads[1];
+        ++taken;
+      }
+      // the tile's bias, read by all rows from shared memory (a load per 32 columns on
+      // its way from DRAM to every thread cost a lone tile 2.5 us)
+      if constexpr (kMode == kLin || kMode == kDz) {
+        if (p.bias) {
+          const int at = n0 + static_cast<int>(threadIdx.x & 127);
+          S.bias[wg][threadIdx.x & 127] = at < p.N ? __ldg(p.bias + at) : 0.f;
+        }
       }
       // the accumulator: 128 columns as packed pairs where chunks are added up
       uint64_t z[kOne ? 1 : kHalf / 2];
@@ -502,19 +510,21 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       };
 
       if constexpr (kPlain || kMode == kDz) {
-        // 32 columns at a time, read from TMEM while those before go out
-        uint32_t raw[kOne ? 2 : 1][32];
+        // 32 columns at a time, read from TMEM while those before go out.  (One copy of
+        // the code: a kernel of one tile per CTA pays for every instruction's way here.)
+        uint32_t raw[32];
         if constexpr (kOne) {
-          ptx::tmem_ld32(tm, raw[0]);
-          ptx::tmem_wait_ld_of(raw[0]);
+          ptx::tmem_ld32(tm, raw);
+          ptx::tmem_wait_ld_of(raw);
         }
-#pragma unroll
+        constexpr int kUnroll = kOne ? 1 : 4;
+#pragma unroll kUnroll
         for (int c = 0; c < 4; ++c) {
           uint64_t x[16];
           if constexpr (kOne) {
-            if (c < 3) ptx::tmem_ld32(tm + (c + 1) * 32, raw[(c + 1) & 1]);
 #pragma unroll
-            for (int e = 0; e < 16; ++e) x[e] = pair_at(raw[c & 1], e);
+            for (int e = 0; e < 16; ++e) x[e] = pair_at(raw, e);
+            if (c < 3) ptx::tmem_ld32(tm + (c + 1) * 32, raw);
           } else {
 #pragma unroll
             for (int e = 0; e < 16; ++e) x[e] = z[c * 16 + e];
@@ -541,12 +551,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
               if (takes) get64(box[b], rc, half, in);
               if (p.bias) {
 #pragma unroll
-                for (int e = 0; e < 16; e += 2)
-                  if (c0 + 2 * e < p.N) {
-                    const ulonglong2 bv = __ldg(reinterpret_cast<const ulonglong2*>(p.bias + c0 + 2 * e));
-                    x[e] = ptx::add2(x[e], bv.x);
-                    x[e + 1] = ptx::add2(x[e + 1], bv.y);
-                  }
+                for (int e = 0; e < 16; e += 2) {
+                  const ulonglong2 bv = ptx::lds128u(&S.bias[wg][c * 32 + 2 * e]);
+                  x[e] = ptx::add2(x[e], bv.x);
+                  x[e + 1] = ptx::add2(x[e + 1], bv.y);
+                }
               }
               if constexpr (kMode == kLin) {
                 if (p.act != TPK_ACT_NONE)
@@ -597,7 +606,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             }
           }
           if constexpr (kOne) {
-            if (c < 3) ptx::tmem_wait_ld_of(raw[(c + 1) & 1]);
+            if (c < 3) ptx::tmem_wait_ld_of(raw);
             if (c == 2) release();
           }
         }
@@ -677,16 +686,21 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         }
       } else {
         // kGateBwd: 32 of 64 columns at a time, g and u in the two boxes of a place
-        uint32_t raw[2][32];
-        ptx::tmem_ld32(tm, raw[0]);
-        ptx::tmem_wait_ld_of(raw[0]);
+        uint32_t raw[32];
+        ptx::tmem_ld32(tm, raw);
+        ptx::tmem_wait_ld_of(raw);
+#pragma unroll 1
+        for (int c = 0; c < 4; ++c, ++sent) {
+          uint64_t x[16];
 #pragma unroll
-        for (int c = 0; c < 4; ++c) {
-          if (c < 3) ptx::tmem_ld32(tm + (c + 1) * 64, raw[(c + 1) & 1]);
-          const int s = c & 1;
-          ++loads[s];
-          ok = ptx::mbar_wait(&S.in_full[0][s], (loads[s] - 1) & 1, abort_flag, kWaitLimitNs) && ok;
-          const uint64_t sg = both(group_unscale(exps[c] & 0xff)), su = both(group_unscale(exps[c] >> 16));
+          for (int e = 0; e < 16; ++e) x[e] = pair_at(raw, e);
+          const uint64_t sg = both(group_unscale(exps & 0xff)), su = both(group_unscale(exps >> 16));
+          if (c < 3) {
+            ptx::tmem_ld32(tm + (c + 1) * 64, raw);
+            exps = exponents(c + 1);
+          }
+          const int s = static_cast<int>(sent & 1);
+          ok = ptx::mbar_wait(&S.in_full[0][s], (sent >> 1) & 1, abort_flag, kWaitLimitNs) && ok;
           uint32_t g16[16], u16[16];
           get64(S.out[s][0], rc, wg, g16);
           get64(S.out[s][1], rc, wg, u16);
@@ -695,7 +709,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             for (int e = 0; e < 16; ++e) {
               const uint64_t g = ptx::mul2(ptx::unpack_f16x2(g16[e]), sg);
               const uint64_t u = ptx::mul2(ptx::unpack_f16x2(u16[e]), su);
-              const uint64_t da = pair_at(raw[c & 1], e);
+              const uint64_t da = x[e];
               uint64_t slope;
               const uint64_t v = act_slope_2<decltype(t)::value>(g, slope);
               float lo, hi;
@@ -710,7 +724,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           ptx::fence_async_shared();
           __syncwarp();
           if (lane == 0) ptx::mbar_arrive(&S.written[s]);
-          if (c < 3) ptx::tmem_wait_ld_of(raw[(c + 1) & 1]);
+          if (c < 3) ptx::tmem_wait_ld_of(raw);
           if (c == 2) release();
         }
       }
@@ -719,14 +733,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     if (kMode != kGateBwd && leader) {
       // loads that nobody waited for (after a timeout) have arrived before the CTA leaves
       for (int s = 0; s < 2; ++s)
-        if (loads[s]) ptx::mbar_drain(&S.in_full[wg][s], (loads[s] - 1) & 1);
-      ptx::bulk_wait_all();
+        if (taken) ptx::mbar_drain(&S.in_full[wg][s], (taken - 1) & 1);
+      ptx::bulk_wait_read<0>();   // (what is still on its way out is out when the kernel is done)
     }
   }
   // Both CTAs leave together: nothing of the pair signals or reads a CTA that
-  // has gone.  After a timeout the stages' copies are waited for first.
+  // has gone.  After a timeout in either the stages' copies are waited for first.
   __syncwarp();
   __syncthreads();
+  if (threadIdx.x == 0 && S.abort_flag) ptx::st_cluster(&S.abort_flag, rank ^ 1, 1);
   ptx::cluster_sync();
   if (S.abort_flag) {
     if (threadIdx.x == 0) {
@@ -735,10 +750,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         for (uint32_t i = S.issued > kStages ? S.issued - kStages : 0; i < S.issued; ++i)
           ptx::mbar_drain(&S.full[i % kStages], (i / kStages) & 1);
     }
+    __syncwarp();
+    ptx::cluster_sync();
   }
-  __syncwarp();
-  __syncthreads();
-  ptx::cluster_sync();
   ptx::tc_fence_after();
   if (warp == 2) ptx::tmem_dealloc_pair(tmem, 512);
   if (p.early) ptx::dependency_wait();
