@@ -157,22 +157,28 @@ int join(const Params& p, const float* bias, int act, const Mat& residual, const
                        static_cast<__nv_bfloat16*>(const_cast<void*>(out.p)), out.ld);
 }
 
-Params params(int64_t M, int64_t N, int64_t K, bool split, float* acc, int32_t* err) {
+Params params(int64_t M, int64_t N, int64_t K, float* acc, int32_t* err) {
   Params p{};
   p.M = static_cast<int32_t>(M);
   p.N = static_cast<int32_t>(N);
   p.K = static_cast<int32_t>(K);
-  const Split s = split ? split_of(tiles_of(M, N), (K + 63) / 64) : Split{tiles_of(M, N), 0, 1};
-  p.whole = static_cast<int32_t>(s.whole);
-  p.splits = s.splits;
+  const Plan plan = plan_of(M, N, K);
+  p.narrow = plan.narrow;
+  p.whole = static_cast<int32_t>(plan.split.whole);
+  p.splits = plan.split.splits;
   p.acc = acc;
   p.err = err;
   return p;
 }
-// Stages of K of the longest unit.
-int longest(const Params& p) {
-  const int k = (p.K + 63) / 64;
-  return p.whole > 0 || p.splits == 1 ? k : k / p.splits + 1;
+// The product as planned, in single accumulations where they are short enough.
+template <int kMode>
+int launch_plan(const Maps& m, const Params& p, bool after, cudaStream_t s) {
+  if (p.narrow) return launch<kMode, true, true>(m, p, after, s);
+  if constexpr (kMode == kDx || kMode == kDw) {
+    const int k = (p.K + 63) / 64, longest = p.whole > 0 || p.splits == 1 ? k : k / p.splits + 1;
+    if (longest > kChunk) return launch<kMode, false>(m, p, after, s);
+  }
+  return launch<kMode, true>(m, p, after, s);
 }
 
 struct LinearWork {
@@ -217,15 +223,15 @@ int linear_product(const Mat& x, const Mat& w, const float* bias, int act, const
   if (x.rows <= kFewRows) return few_linear(x, w, bias, act, residual, y, after, err, s);
   Maps m;
   int st = map_of(&m.a, x, kHalf);
-  if (st == TPK_OK) st = map_of(&m.b, w, kHalf);
+  if (st == TPK_OK) st = map_of(&m.b, w, plan_of(x.rows, w.rows, x.cols).narrow ? kHalf / 2 : kHalf);
   if (st == TPK_OK) st = map_of(&m.out, y, kHalf);
   if (st == TPK_OK && residual.p) st = map_of(&m.in, residual, kHalf);
   if (st != TPK_OK) return st;
-  Params p = params(x.rows, w.rows, x.cols, true, acc, err);
+  Params p = params(x.rows, w.rows, x.cols, acc, err);
   p.bias = bias;
   p.act = act;
   p.has_in = residual.p != nullptr;
-  st = launch<kLin, true>(m, p, after, s);
+  st = launch_plan<kLin>(m, p, after, s);
   return st == TPK_OK && p.splits > 1 ? join(p, bias, act, residual, y, s) : st;
 }
 
@@ -236,10 +242,10 @@ int input_product(const Mat& dz, const Mat& w, const Mat& dx, float* acc, bool a
   if (st == TPK_OK) st = map_of(&m.b, w, 64);
   if (st == TPK_OK) st = map_of(&m.out, dx, kHalf);
   if (st != TPK_OK) return st;
-  Params p = params(dz.rows, w.cols, dz.cols, true, acc, err);
+  Params p = params(dz.rows, w.cols, dz.cols, acc, err);
   p.late = 1;
   *left = p;
-  return longest(p) <= kChunk ? launch<kDx, true>(m, p, after, s) : launch<kDx, false>(m, p, after, s);
+  return launch_plan<kDx>(m, p, after, s);
 }
 
 int weight_product(const Mat& dz, const Mat& x, const Mat& dw, float* acc, const Params& before, int32_t* err,
@@ -249,10 +255,10 @@ int weight_product(const Mat& dz, const Mat& x, const Mat& dw, float* acc, const
   if (st == TPK_OK) st = map_of(&m.b, x, 64);
   if (st == TPK_OK) st = map_of(&m.out, dw, kHalf);
   if (st != TPK_OK) return st;
-  Params p = params(dz.cols, x.cols, dz.rows, true, acc, err);
-  p.early = shape_of<kDx>(before).units < kPairs;
+  Params p = params(dz.cols, x.cols, dz.rows, acc, err);
+  p.early = (before.narrow ? shape_of<kDx, true>(before) : shape_of<kDx>(before)).units < kPairs;
   *left = p;
-  return longest(p) <= kChunk ? launch<kDw, true>(m, p, true, s) : launch<kDw, false>(m, p, true, s);
+  return launch_plan<kDw>(m, p, true, s);
 }
 
 int join_left(const Params& left, const Mat& out, cudaStream_t s) {
@@ -319,15 +325,19 @@ extern "C" int tpk_linear_bwd(const void* x, int64_t ld_x, const void* w, const 
   if (act != TPK_ACT_NONE) {
     Maps m;
     st = map_of(&m.a, mx, kHalf);
-    if (st == TPK_OK) st = map_of(&m.b, mw, kHalf);
+    Params p = params(N, O, C, nullptr, dev_err);
+    if (!p.narrow) {   // its epilogue has no joined form
+      p.whole = static_cast<int32_t>(tiles_of(N, O));
+      p.splits = 1;
+    }
+    if (st == TPK_OK) st = map_of(&m.b, mw, p.narrow ? kHalf / 2 : kHalf);
     if (st == TPK_OK) st = map_of(&m.in, dz, kHalf);
     dz = Mat{k.dz, N, O, O};
     if (st == TPK_OK) st = map_of(&m.out, dz, kHalf);
-    Params p = params(N, O, C, false, nullptr, dev_err);
     p.bias = bias;
     p.act = act;
     p.colsum = db ? k.sums : nullptr;
-    if (st == TPK_OK) st = launch<kDz, true>(m, p, false, s);
+    if (st == TPK_OK) st = launch_plan<kDz>(m, p, false, s);
   }
   const Mat mdx{dx, N, C, ld_dx}, mdw{dw, O, C, C};
   Params px, pw;

@@ -38,6 +38,8 @@
 // waits at its end, so that a kernel that is done means that those before it are
 // (1,001 rows, widths 1,000 and 552, forward and backward: 50 us against 56; beside
 // a product that fills the GPU it costs 1%).
+// A few tiles leave most SMs idle and wait for their epilogue at the end: kLin, kDz,
+// kDx and kDw then take tiles half as wide (256 x 128, plan_of).
 // Warps of a CTA: 0 TMA producer, 1 MMA issuer (of the pair's first CTA), 2
 // TMEM owner, 4-11 epilogue (two warpgroups).  kGateBwd moves 64 columns of g and
 // u in and of dg and du out at a time, through two places; warp 3 carries them, so
@@ -90,6 +92,7 @@ struct Params {
   int32_t has_in;            // kLin: a residual
   int32_t save;              // kGate: g and u go out too
   int32_t early;             // needs nothing of the kernel before, only of those that it waited for
+  int32_t narrow;            // tiles of 128 columns (the kernel knows by its type)
   int32_t late;              // lets the next kernel start only after its own wait (that one may be early)
   const float* bias;         // [N] or nullptr
   float* colsum;             // kDz: [ceil(M / 32)][N] sums of 32 rows of dz; nullptr: none
@@ -123,22 +126,46 @@ struct Split {
   int64_t whole, tail;
   int splits;
 };
-inline Split split_of(int64_t tiles, int64_t k_iters) {
+// us: of the last round.
+inline Split split_of(int64_t tiles, int64_t k_iters, double* us_out = nullptr) {
   Split s{tiles, 0, 1};
   const int64_t tail = tiles % kPairs;
-  if (tail == 0) return s;
   const double tile_us = 0.27 * static_cast<double>(k_iters);   // 64 elements of K: 512 cycles
   double best = tile_us;
+  if (us_out) *us_out = best;
+  if (tail == 0) return s;
   for (int64_t n = 2; n <= k_iters / 4 && n <= (tail * 8 < kPairs ? kPairs / tail : 8); ++n) {
     const int64_t rounds = (tail * n + kPairs - 1) / kPairs;
-    const double us = tile_us * static_cast<double>(rounds) / static_cast<double>(n) + 3.0 +
-                      0.105 * static_cast<double>(tail * n);
+    const double us = tile_us * static_cast<double>(rounds) / static_cast<double>(n) + 6.0 +
+                      0.105 * static_cast<double>(tail * n) + 0.1 * static_cast<double>(n);
     if (us < best) {
       best = us;
       s = Split{tiles - tail, tail, static_cast<int>(n)};
     }
   }
+  if (us_out) *us_out = best;
   return s;
+}
+
+// How a product is done: in wide tiles, some of them split, or in narrow ones.
+// Those need 256 cycles for 64 elements of K where few pairs run, about 384 where
+// the operands' way into the SMs is full, and half of the 2.2 us that a lone wide
+// tile's epilogue takes.  (1,000 rows, widths 1,000 and 552, gelu: 10.7 us in narrow
+// tiles, 14.5 in wide ones; 200 rows, widths 1,024 and 256: 7.2 against 10.5.)
+struct Plan {
+  bool narrow;
+  Split split;
+};
+inline Plan plan_of(int64_t M, int64_t N, int64_t K) {
+  const int64_t mt = (M + kTile - 1) / kTile, wide = mt * ((N + kTile - 1) / kTile);
+  const int64_t narrow = mt * ((N + kHalf - 1) / kHalf), k_iters = (K + 63) / 64;
+  double us;
+  Plan p{false, split_of(wide, k_iters, &us)};
+  if (wide > kPairs || k_iters > kChunk) return p;
+  const int64_t rounds = (narrow + kPairs - 1) / kPairs;
+  const double stage_us = narrow <= kPairs / 2 ? 0.14 : 0.2;
+  if (stage_us * static_cast<double>(rounds * k_iters) + 1.1 < us + 2.2) p = Plan{true, Split{narrow, 0, 1}};
+  return p;
 }
 
 // Unit u covers tile (m, n) and the stages [k0, k0 + nk) of K.
@@ -150,14 +177,15 @@ struct Unit {
   int split;                 // -1: the whole of K
   int tile;
 };
-template <int kMode>
-constexpr int kTileN = kMode == kGate ? kHalf : kTile;
+// Columns of a tile.
+template <int kMode, bool kNarrow = false>
+constexpr int kTileN = kMode == kGate || kNarrow ? kHalf : kTile;
 
-template <int kMode>
+template <int kMode, bool kNarrow = false>
 __host__ __device__ inline Shape shape_of(const Params& p) {
   Shape s;
   s.mt = (p.M + kTile - 1) / kTile;
-  s.nt = (p.N + kTileN<kMode> - 1) / kTileN<kMode>;
+  s.nt = (p.N + kTileN<kMode, kNarrow> - 1) / kTileN<kMode, kNarrow>;
   s.k_iters = (p.K + 63) / 64;
   s.units = p.whole + (s.mt * s.nt - p.whole) * p.splits;
   return s;
@@ -242,7 +270,7 @@ __device__ __forceinline__ float column_sums(float (&x)[32], int lane) {
 
 // kOne: every tile is a single accumulation, which goes out while it is read
 // from TMEM and need not be held whole.
-template <int kMode, bool kOne>
+template <int kMode, bool kOne, bool kNarrow>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     product_kernel(const __grid_constant__ Maps maps, const Params p) {
   extern __shared__ uint8_t smem_raw[];
@@ -251,11 +279,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   constexpr bool kBmn = kMode == kDx || kMode == kDw || kMode == kGateBwd;     // B stored with N contiguous
   constexpr bool kPlain = kMode == kLin || kMode == kDx || kMode == kDw;
   static_assert(kOne || kMode == kDx || kMode == kDw, "sums over channels do not stop");
+  static_assert(!kNarrow || (kOne && kMode < kGate), "narrow tiles are whole sums");
+  constexpr int kCols = kNarrow ? kHalf : kTile;   // columns of the accumulator
+  constexpr int kBRows = kCols / 2;                // rows of B a CTA holds
   const int warp = threadIdx.x >> 5;
   const uint32_t rank = ptx::cluster_rank();
   const int pair = blockIdx.x >> 1, n_pairs = gridDim.x >> 1;
   volatile int* abort_flag = &S.abort_flag;
-  const Shape sh = shape_of<kMode>(p);
+  const Shape sh = shape_of<kMode, kNarrow>(p);
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < kStages; ++s) {
@@ -282,7 +313,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   // the producer needs no accumulator and is off
   uint32_t tmem = 0;
   if (warp == 2) {
-    ptx::tmem_alloc_pair(&S.tmem_base, 512);
+    ptx::tmem_alloc_pair(&S.tmem_base, 2 * kCols);
     ptx::tmem_relinquish_pair();
     ptx::tc_fence_before();
   }
@@ -304,14 +335,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         for (int u = pair; ok && u < sh.units; u += n_pairs) {
           const Unit w = unit_of(p, sh, u);
           const int m0 = w.m * kTile + static_cast<int>(rank) * kHalf;
-          const int n0 = w.n * kTileN<kMode> + (kMode == kGate ? 0 : static_cast<int>(rank) * kHalf);
+          const int n0 = w.n * kTileN<kMode, kNarrow> + (kMode == kGate ? 0 : static_cast<int>(rank) * kBRows);
           for (int k = 0; k < w.nk; ++k, ++it) {
             const int st = it % kStages;
             if (it >= kStages && !ptx::mbar_wait(&S.empty[st], (it / kStages - 1) & 1, abort_flag, kWaitLimitNs)) {
               ok = false;
               break;
             }
-            if (rank == 0) ptx::mbar_arrive_expect_tx(&S.full[st], 4 * kBoxBytes);
+            if (rank == 0) ptx::mbar_arrive_expect_tx(&S.full[st], 2 * (kBoxBytes + kBRows * 128));
             const uint32_t bar = ptx::cluster_addr(&S.full[st], 0);
             const int kk = (w.k0 + k) * 64;
             if constexpr (kAmn) {
@@ -322,7 +353,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             }
             if constexpr (kBmn) {
               ptx::tma_load_2d_pair(S.b[st], mb, bar, n0, kk);
-              ptx::tma_load_2d_pair(S.b[st] + kBoxBytes / 2, mb, bar, n0 + 64, kk);
+              if (kBRows > 64) ptx::tma_load_2d_pair(S.b[st] + kBoxBytes / 2, mb, bar, n0 + 64, kk);
             } else {
               ptx::tma_load_2d_pair(S.b[st], mb, bar, kk, n0);
             }
@@ -333,7 +364,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     } else if (warp == 1 && rank == 0) {
       // ---------------------------------------------------------- MMA issuer
       if (ptx::elect_one()) {
-        constexpr uint32_t idesc = ptx::idesc_bf16_f32(kTile, kTile, kAmn, kBmn);
+        constexpr uint32_t idesc = ptx::idesc_bf16_f32(kTile, kCols, kAmn, kBmn);
         // K step of 16 elements: 32 bytes along a K-major row, 16 rows of 128
         // bytes of an MN-major box (its two 64-column boxes half a stage apart)
         constexpr uint32_t kStepA = kAmn ? 2048 : 32, kStepB = kBmn ? 2048 : 32;
@@ -361,7 +392,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
               const uint64_t bd = ptx::sw128_desc(ptx::smem_addr(S.b[st]), kBmn ? kBoxBytes / 2 : 16, 1024);
 #pragma unroll
               for (int q = 0; q < 4; ++q)
-                ptx::mma_ss_pair(tmem + buf * kTile, ptx::desc_add(ad, q * kStepA), ptx::desc_add(bd, q * kStepB),
+                ptx::mma_ss_pair(tmem + buf * kCols, ptx::desc_add(ad, q * kStepA), ptx::desc_add(bd, q * kStepB),
                                  idesc, (k > 0 || q > 0) ? 1u : 0u);
               ptx::mma_commit_pair(&S.empty[st]);
             }
@@ -432,7 +463,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       const bool takes = kMode == kDz || kMode == kGateBwd || (kMode == kLin && p.has_in && w.split < 0);
       const int row0 = w.m * kTile + static_cast<int>(rank) * kHalf;   // first row of this CTA
       // first column of this warpgroup; kGateBwd: of its 32 in every 64
-      const int n0 = w.n * kTileN<kMode> + wg * (kMode == kGateBwd ? 32 : kTileN<kMode> / 2);
+      const int n0 = w.n * kTileN<kMode, kNarrow> + wg * (kMode == kGateBwd ? 32 : kTileN<kMode, kNarrow> / 2);
       // what the epilogue reads, into the boxes that it will leave from
       auto fetch = [&](int s, int col) {
         ptx::mbar_arrive_expect_tx(&S.in_full[wg][s], kBoxBytes);
@@ -453,7 +484,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         if (leader) {
           ptx::bulk_wait_read<0>();   // the boxes' last results have left
           fetch(0, n0);
-          fetch(1, n0 + 64);
+          if (!kNarrow) fetch(1, n0 + 64);
         }
         ++taken;
       }
@@ -461,8 +492,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       // its way from DRAM to every thread cost a lone tile 2.5 us)
       if constexpr (kMode == kLin || kMode == kDz) {
         if (p.bias) {
-          const int at = n0 + static_cast<int>(threadIdx.x & 127);
-          S.bias[wg][threadIdx.x & 127] = at < p.N ? __ldg(p.bias + at) : 0.f;
+          const int i = threadIdx.x & 127;
+          if (!kNarrow || i < 64) S.bias[wg][i] = n0 + i < p.N ? __ldg(p.bias + n0 + i) : 0.f;
         }
       }
       // the accumulator: 128 columns as packed pairs where chunks are added up
@@ -477,7 +508,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           }
           ptx::tc_fence_after();
           ++tile;
-          const uint32_t tm = tmem + lane_off + buf * kTile + wg * kHalf;
+          const uint32_t tm = tmem + lane_off + buf * kCols + wg * kHalf;
 #pragma unroll
           for (int c = 0; c < 4; ++c) {
             uint32_t x[32];
@@ -498,7 +529,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       ok = ptx::all_of_128(wg + 1, ok);
       if (!ok) break;
       const uint32_t buf = tile & 1;
-      const uint32_t tm = tmem + lane_off + buf * kTile + wg * (kMode == kGate ? 64 : kMode == kGateBwd ? 32 : kHalf);
+      const uint32_t tm =
+          tmem + lane_off + buf * kCols + wg * (kMode == kGate || kNarrow ? 64 : kMode == kGateBwd ? 32 : kHalf);
       if constexpr (kOne) {
         ptx::tc_fence_after();
         ++tile;
@@ -517,14 +549,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           ptx::tmem_ld32(tm, raw);
           ptx::tmem_wait_ld_of(raw);
         }
-        constexpr int kUnroll = kOne ? 1 : 4;
+        constexpr int kUnroll = kOne ? 1 : 4, kLast = kNarrow ? 1 : 3;
 #pragma unroll kUnroll
-        for (int c = 0; c < 4; ++c) {
+        for (int c = 0; c <= kLast; ++c) {
           uint64_t x[16];
           if constexpr (kOne) {
 #pragma unroll
             for (int e = 0; e < 16; ++e) x[e] = pair_at(raw, e);
-            if (c < 3) ptx::tmem_ld32(tm + (c + 1) * 32, raw);
+            if (c < kLast) ptx::tmem_ld32(tm + (c + 1) * 32, raw);
           } else {
 #pragma unroll
             for (int e = 0; e < 16; ++e) x[e] = z[c * 16 + e];
@@ -542,7 +574,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
               if (takes) {
                 ok = fetched(b);
               } else {
-                if (leader) ptx::bulk_wait_read<1>();   // this box's last store
+                if (leader) ptx::bulk_wait_read<kNarrow ? 0 : 1>();   // this box's last store
                 meet();
               }
             }
@@ -606,8 +638,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             }
           }
           if constexpr (kOne) {
-            if (c < 3) ptx::tmem_wait_ld_of(raw);
-            if (c == 2) release();
+            if (c < kLast) ptx::tmem_wait_ld_of(raw);
+            if (c == kLast - 1) release();
           }
         }
       } else if constexpr (kMode == kGate) {
@@ -732,7 +764,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     }
     if (kMode != kGateBwd && leader) {
       // loads that nobody waited for (after a timeout) have arrived before the CTA leaves
-      for (int s = 0; s < 2; ++s)
+      for (int s = 0; s < (kNarrow ? 1 : 2); ++s)
         if (taken) ptx::mbar_drain(&S.in_full[wg][s], (taken - 1) & 1);
       ptx::bulk_wait_read<0>();   // (what is still on its way out is out when the kernel is done)
     }
@@ -754,7 +786,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     ptx::cluster_sync();
   }
   ptx::tc_fence_after();
-  if (warp == 2) ptx::tmem_dealloc_pair(tmem, 512);
+  if (warp == 2) ptx::tmem_dealloc_pair(tmem, 2 * kCols);
   if (p.early) ptx::dependency_wait();
 }
 
@@ -769,7 +801,7 @@ inline int map_of(CUtensorMap* m, const Mat& a, int box_rows) { return make_map_
 inline int64_t tiles_of(int64_t M, int64_t N) { return (M + kTile - 1) / kTile * ((N + kTile - 1) / kTile); }
 // Workspace of a product that may be split over K.
 inline size_t acc_bytes(int64_t M, int64_t N, int64_t K) {
-  const Split s = split_of(tiles_of(M, N), (K + 63) / 64);
+  const Split s = plan_of(M, N, K).split;
   return static_cast<size_t>(s.tail) * s.splits * kTile * kTile * 4;
 }
 // Rows of the exponents that kGate keeps, and their bytes.
@@ -793,9 +825,9 @@ int launch_kernel(void (*kern)(Args...), dim3 grid, int threads, size_t smem, bo
   return cuda_status(cudaLaunchKernelEx(&cfg, kern, static_cast<Args>(given)...));
 }
 
-template <int kMode, bool kOne>
+template <int kMode, bool kOne, bool kNarrow = false>
 int launch(const Maps& maps, const Params& p, bool after, cudaStream_t s) {
-  constexpr auto kern = product_kernel<kMode, kOne>;
+  constexpr auto kern = product_kernel<kMode, kOne, kNarrow>;
   static PerContext<int> rec;
   int unused = 0;
   const int st = guarded([&] { return rec.get(&unused, [](int*) {
@@ -807,7 +839,7 @@ int launch(const Maps& maps, const Params& p, bool after, cudaStream_t s) {
         cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(kSmemBytes)));
   }); });
   if (st != TPK_OK) return st;
-  const int units = shape_of<kMode>(p).units;
+  const int units = shape_of<kMode, kNarrow>(p).units;
   int pairs = num_sms() / 2;
   pairs = pairs < 1 ? 1 : pairs;
   pairs = pairs < units ? pairs : units;
