@@ -27,10 +27,10 @@ size_t carve(uint8_t* base, int64_t N, int64_t C, int64_t I, int64_t O, bool bac
     return p;
   };
   if (!backward) {
-    if (!own_a) o.a = reinterpret_cast<__nv_bfloat16*>(take(static_cast<size_t>(N) * I * 2));
+    if (!own_a) o.a = reinterpret_cast<__nv_bfloat16*>(take(static_cast<size_t>(N * own_stride(I)) * 2));
     if (N > kFewRows) o.acc = reinterpret_cast<float*>(take(acc_bytes(N, O, I)));
   } else {
-    o.dgu = reinterpret_cast<__nv_bfloat16*>(take(static_cast<size_t>(N) * 2 * I * 2));
+    o.dgu = reinterpret_cast<__nv_bfloat16*>(take(static_cast<size_t>(N * own_stride(2 * I)) * 2));
     o.acc = reinterpret_cast<float*>(take(acc_bytes(N, C, 2 * I)));
     o.acc_in = reinterpret_cast<float*>(take(acc_bytes(2 * I, C, N)));
     o.acc_out = reinterpret_cast<float*>(take(acc_bytes(O, I, N)));
@@ -65,13 +65,14 @@ Params params(int64_t M, int64_t N, int64_t K, int act, int32_t* err) {
 
 const __nv_bfloat16* bf(const void* p) { return static_cast<const __nv_bfloat16*>(p); }
 
-// What the forward keeps: g and u side by side, 16 bits each, [N, 2 I], then the exponents.
+// What the forward keeps: rows of g and u, 16 bits each, own_stride(I) apart, then the exponents.
 struct Saved {
   Mat g, u;
   uint8_t* exps;
 };
 Saved saved_of(void* p, int64_t N, int64_t I) {
-  return Saved{Mat{p, N, I, 2 * I}, Mat{bf(p) + I, N, I, 2 * I}, static_cast<uint8_t*>(p) + N * 4 * I};
+  const int64_t to_u = own_stride(I);
+  return Saved{Mat{p, N, I, 2 * to_u}, Mat{bf(p) + to_u, N, I, 2 * to_u}, static_cast<uint8_t*>(p) + N * 4 * to_u};
 }
 
 }  // namespace
@@ -87,7 +88,7 @@ extern "C" size_t tpk_gated_ffn_workspace_bytes(int64_t N, int32_t C, int32_t I,
 extern "C" size_t tpk_gated_ffn_saved_bytes(int64_t N, int32_t I) {
   using namespace tpk::product;
   if (!sizes_ok(N, 8, I, 8) || I > kMostK) return 0;
-  return static_cast<size_t>(N) * 4 * I + exp_bytes(N, I);
+  return static_cast<size_t>(N * 4 * own_stride(I)) + exp_bytes(N, I);
 }
 
 extern "C" int tpk_gated_ffn(const void* x, int64_t ld_x, const void* w_in, const void* w_out, int32_t act,
@@ -111,7 +112,7 @@ extern "C" int tpk_gated_ffn(const void* x, int64_t ld_x, const void* w_in, cons
   if (st != TPK_OK) return st;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   const Mat mx{x, N, C, ld_x}, gate{w_in, I, C, C}, up{bf(w_in) + int64_t{I} * C, I, C, C}, down{w_out, O, I, I};
-  const Mat ma{a ? a : k.a, N, I, I}, res{residual, N, O, ld_res}, my{y, N, O, ld_y};
+  const Mat ma{a ? a : k.a, N, I, a ? I : own_stride(I)}, res{residual, N, O, ld_res}, my{y, N, O, ld_y};
   if (N <= kFewRows && !saved) {
     st = few_gate(mx, gate, up, act, ma, dev_err, s);
     return st == TPK_OK ? few_linear(ma, down, nullptr, TPK_ACT_NONE, res, my, true, dev_err, s) : st;
@@ -169,13 +170,14 @@ extern "C" int tpk_gated_ffn_bwd(const void* x, int64_t ld_x, const void* w_in, 
   const Saved k16 = saved_of(const_cast<void*>(saved), N, I);
   if (st == TPK_OK) st = map_of(&m.in, k16.g, kHalf);
   if (st == TPK_OK) st = map_of(&m.in2, k16.u, kHalf);
-  if (st == TPK_OK) st = map_of(&m.out, Mat{k.dgu, N, I, wide}, kHalf);
-  if (st == TPK_OK) st = map_of(&m.out2, Mat{k.dgu + I, N, I, wide}, kHalf);
+  const int64_t ld = own_stride(wide);
+  if (st == TPK_OK) st = map_of(&m.out, Mat{k.dgu, N, I, ld}, kHalf);
+  if (st == TPK_OK) st = map_of(&m.out2, Mat{k.dgu + I, N, I, ld}, kHalf);
   Params p = params(N, I, O, act, dev_err);
   p.exps = k16.exps;
   p.exp_rows = exp_rows(N);
   if (st == TPK_OK) st = launch<kGateBwd, true>(m, p, false, s);
-  const Mat dgu{k.dgu, N, wide, wide};
+  const Mat dgu{k.dgu, N, wide, ld};
   const Mat mdx{dx, N, C, ld_dx}, mdin{dw_in, wide, C, C}, mdout{dw_out, O, I, I};
   Params px, pin, pout;
   if (st == TPK_OK) st = input_product(dgu, Mat{w_in, wide, C, C}, mdx, k.acc, true, dev_err, s, &px);

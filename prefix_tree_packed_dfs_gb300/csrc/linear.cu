@@ -197,7 +197,7 @@ size_t carve(uint8_t* base, int64_t N, int64_t C, int64_t O, int32_t act, bool b
     if (N > kFewRows) o.acc = reinterpret_cast<float*>(take(acc_bytes(N, O, C)));
   } else {
     if (act != TPK_ACT_NONE) {
-      o.dz = reinterpret_cast<__nv_bfloat16*>(take(static_cast<size_t>(N) * O * 2));
+      o.dz = reinterpret_cast<__nv_bfloat16*>(take(static_cast<size_t>(N * own_stride(O)) * 2));
       o.sums = reinterpret_cast<float*>(take(static_cast<size_t>((N + 31) / 32) * O * 4));
     }
     o.part = reinterpret_cast<float*>(take(static_cast<size_t>(kSumMost) * O * 4));
@@ -332,7 +332,7 @@ extern "C" int tpk_linear_bwd(const void* x, int64_t ld_x, const void* w, const 
     }
     if (st == TPK_OK) st = map_of(&m.b, mw, p.narrow ? kHalf / 2 : kHalf);
     if (st == TPK_OK) st = map_of(&m.in, dz, kHalf);
-    dz = Mat{k.dz, N, O, O};
+    dz = Mat{k.dz, N, O, own_stride(O)};
     if (st == TPK_OK) st = map_of(&m.out, dz, kHalf);
     p.bias = bias;
     p.act = act;

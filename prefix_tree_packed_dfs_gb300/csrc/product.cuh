@@ -798,6 +798,10 @@ struct Mat {
 };
 inline int map_of(CUtensorMap* m, const Mat& a, int box_rows) { return make_map_2d(m, a.p, a.rows, a.cols, a.ld, box_rows); }
 
+// Row stride of the library's own buffers: rows that start on 128 bytes take the
+// TMA one line per box and row, others two.
+inline int64_t own_stride(int64_t cols) { return (cols + 63) / 64 * 64; }
+
 inline int64_t tiles_of(int64_t M, int64_t N) { return (M + kTile - 1) / kTile * ((N + kTile - 1) / kTile); }
 // Workspace of a product that may be split over K.
 inline size_t acc_bytes(int64_t M, int64_t N, int64_t K) {

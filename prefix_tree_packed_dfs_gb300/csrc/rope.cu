@@ -116,11 +116,15 @@ __device__ __forceinline__ int quotient(int a, int b, uint32_t inv) {
   return b == 1 ? a : static_cast<int>(__umulhi(static_cast<uint32_t>(a), inv));
 }
 
+// The pairs' (cos, sin) of a position lie by twos, two of every piece side by
+// side: neighbouring lanes, which hold neighbouring pieces, read neighbouring 16
+// bytes.  (In the pairs' own order every read took four turns: rope_batch 196 us.)
 // A piece is 16 bytes of a head, or, for a rotated piece of the half layout,
 // the two whose channels make pairs.
 template <bool kInter>
 __global__ void __launch_bounds__(kThreads, 4) rope_rows_kernel(const RopeRows p, const Fractions fr) {
-  __shared__ __align__(16) float2 cs[kRowsMost * kMostPairs];
+  __shared__ float4 cs[kRowsMost * kMostPairs / 2];
+  constexpr int kPer = kInter ? 4 : 8;                         // pairs of a piece
   const int pairs = p.rot / 2;
   const int64_t f0 = static_cast<int64_t>(blockIdx.x) * p.per;
   const int n = p.F - f0 < p.per ? static_cast<int>(p.F - f0) : p.per;
@@ -160,7 +164,9 @@ __global__ void __launch_bounds__(kThreads, 4) rope_rows_kernel(const RopeRows p
         const uint64_t turn = static_cast<uint64_t>(static_cast<int64_t>(__ldg(p.depth + f0 + pos))) * fr.v[i];
         float s, c;
         sincospif(static_cast<float>(static_cast<int64_t>(turn)) * 0x1p-63f, &s, &c);
-        cs[t] = make_float2(c * p.factor, s * p.factor * p.sign);
+        const int j = i % kPer;
+        reinterpret_cast<float2*>(cs)[2 * (pos * (pairs / 2) + j / 2 * turned + i / kPer) + j % 2] =
+            make_float2(c * p.factor, s * p.factor * p.sign);
       }
       __syncthreads();
     }
@@ -170,18 +176,20 @@ __global__ void __launch_bounds__(kThreads, 4) rope_rows_kernel(const RopeRows p
       const int pos = at[j] >> 8, c = at[j] & 255;
       if (c < turned) {
         uint32_t x[4] = {a[j].x, a[j].y, a[j].z, a[j].w};
+        const float4* at_c = cs + pos * (pairs / 2) + c;
         if constexpr (kInter) {
 #pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const float2 w = cs[pos * pairs + c * 4 + e];
-            const float u = lo16(x[e]), v = hi16(x[e]);
-            x[e] = pack2(u * w.x - v * w.y, u * w.y + v * w.x);
+          for (int e = 0; e < 4; e += 2) {
+            const float4 w = at_c[e / 2 * turned];
+            const float u0 = lo16(x[e]), v0 = hi16(x[e]), u1 = lo16(x[e + 1]), v1 = hi16(x[e + 1]);
+            x[e] = pack2(u0 * w.x - v0 * w.y, u0 * w.y + v0 * w.x);
+            x[e + 1] = pack2(u1 * w.z - v1 * w.w, u1 * w.w + v1 * w.z);
           }
         } else {
           uint32_t y[4] = {b[j].x, b[j].y, b[j].z, b[j].w};
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
-            const float4 w = *reinterpret_cast<const float4*>(&cs[pos * pairs + c * 8 + 2 * e]);
+            const float4 w = at_c[e * turned];
             const float u0 = lo16(x[e]), u1 = hi16(x[e]), v0 = lo16(y[e]), v1 = hi16(y[e]);
             x[e] = pack2(u0 * w.x - v0 * w.y, u1 * w.z - v1 * w.w);
             y[e] = pack2(u0 * w.y + v0 * w.x, u1 * w.w + v1 * w.z);

@@ -162,9 +162,10 @@ def test_gated_ffn(ops, n, c, i, o, act, res):
     g, u, e_g, e_u, v, _, e_a = _ffn_parts(X, WI, WO, act)
     keep = lambda t, e: 2.0 ** -11 * (np.abs(t) + e) + 2.0 ** -38 * (np.abs(t) + e).max(1, keepdims=True)
     k_g, k_u = keep(g, e_g), keep(u, e_u)
-    half = pre[:4 * n * i].view(torch.float16).view(n, 2, i).double().cpu().numpy()
+    ip = -(-i // 64) * 64
+    half = pre[:4 * n * ip].view(torch.float16).view(n, 2, ip)[:, :, :i].double().cpu().numpy()
     groups, rows = -(-i // 32), -(-n // 128) * 128
-    exps = pre[4 * n * i:].view(2, groups, rows)[:, :, :n].cpu().numpy().astype(np.int64)
+    exps = pre[4 * n * ip:].view(2, groups, rows)[:, :, :n].cpu().numpy().astype(np.int64)
     unscale = np.repeat(2.0 ** (exps - 141), 32, 1)[:, :i].transpose(2, 0, 1)
     got = (half * unscale).reshape(n, 2 * i)
     err_pre = np.abs(got - rgu)
