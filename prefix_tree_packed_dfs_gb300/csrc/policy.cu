@@ -10,8 +10,8 @@
 // Log-ratios are differences of two fp32 numbers and are kept as the exact sum
 // of two, for their comparison with the clip's borders (a token is never on the
 // wrong side) and for a sequence's mean; fp64 instructions, of which this part
-// has few, are left to single threads (a sequence pass with fp64 block sums took
-// 83 us where this one takes the figure below).  exp(t) - t - 1 near t = 0 is its
+// has few, are left to single threads (512 sequences, 548,000 tokens: a sequence
+// pass with fp64 block sums took 83 us, this one 13).  exp(t) - t - 1 near t = 0 is its
 // series.
 // What bounds it: latency, of the launches and of the chain offset -> token ->
 // share.
@@ -104,12 +104,12 @@ __device__ __forceinline__ float k3(float t) {
 // A raw token: its weight and its position, -1 where it carries no loss.
 struct Token {
   float w;
-  int64_t f;
+  int32_t f;
 };
 __device__ __forceinline__ Token token_at(const Policy& p, int64_t r) {
   Token t;
   t.w = __ldg(p.weight + r);
-  const int64_t f = __ldg(p.token_index + r);
+  const int32_t f = __ldg(p.token_index + r);
   t.f = t.w != 0.f && f >= 0 && f < p.F ? f : -1;
   return t;
 }
@@ -210,7 +210,7 @@ __global__ void __launch_bounds__(kSeqThreads, 4) policy_sequence_kernel(const P
     for (int64_t r = hi + threadIdx.x; r < p.R; r += kSeqThreads) p.share[r] = 0.f;
   // A sequence of up to kKeep tokens per thread is read once; what is longer is
   // read again by each step.
-  constexpr int kKeep = 4;
+  constexpr int kKeep = 6;
   const int64_t first = lo + threadIdx.x, later = first + int64_t{kKeep} * kSeqThreads;
   Token kept[kKeep];
   float old[kKeep], adv[kKeep], ref[kKeep], loss[kKeep];
@@ -299,24 +299,46 @@ __global__ void __launch_bounds__(kSeqThreads, 4) policy_sequence_kernel(const P
 // dloss[f] = sum of the shares of f's raw tokens.  A warp takes 32 neighbouring
 // positions, one per lane (their tokens are neighbours in raw order too).  Where
 // one of the 32 has many tokens (a prompt under hundreds of sequences) the
-// CTA's eight warps take every eighth token each.  A CTA's warps take groups
-// from all over the batch, so that a prompt's groups meet different CTAs.  The
-// last CTA joins the first pass's sums.
-constexpr int kLong = 32;   // tokens of a position that a lane adds up alone
-template <int kAhead>
-__device__ __forceinline__ float shares(const Policy& p, int64_t lo, int64_t hi, int step) {
-  float s = 0.f;
-  for (int64_t e0 = lo; e0 < hi; e0 += kAhead * step) {
-    int r[kAhead];
+// CTA's eight warps share each list out.  A CTA's warps take groups from all over
+// the batch, so that a prompt's groups meet different CTAs.  The last CTA joins
+// the first pass's sums.
+constexpr int kLong = 8;   // tokens of a position that a lane adds up alone
+constexpr int kQuads = 8;  // 16-byte pieces of a long list in flight
+
+// The shares of up to kMost tokens from e on, short of hi.
+template <int kMost>
+__device__ __forceinline__ float some_shares(const Policy& p, int e, int hi) {
+  int r[kMost];
 #pragma unroll
-    for (int j = 0; j < kAhead; ++j) {
-      const int64_t e = e0 + j * step;
-      r[j] = e < hi ? __ldg(p.raw + e) : -1;
+  for (int j = 0; j < kMost; ++j) r[j] = e + j < hi ? __ldg(p.raw + e + j) : -1;
+  float s = 0.f;
+#pragma unroll
+  for (int j = 0; j < kMost; ++j)
+    if (r[j] >= 0 && r[j] < p.R) s += __ldcg(p.share + r[j]);
+  return s;
+}
+// The lists of neighbouring positions lie far apart: a lane reads its own in
+// 16-byte pieces.
+__device__ __forceinline__ float many_shares(const Policy& p, int lo, int hi) {
+  const int to_line = static_cast<int>(-(reinterpret_cast<intptr_t>(p.raw + lo) >> 2)) & 3;
+  const int first = lo + to_line < hi ? lo + to_line : hi;
+  float s = some_shares<3>(p, lo, first);
+  int e = first;
+  for (; e + 4 * kQuads <= hi; e += 4 * kQuads) {
+    int4 r[kQuads];
+#pragma unroll
+    for (int j = 0; j < kQuads; ++j) r[j] = __ldg(reinterpret_cast<const int4*>(p.raw + e) + j);
+    float v[4 * kQuads];
+#pragma unroll
+    for (int j = 0; j < kQuads; ++j) {
+      const int at[4] = {r[j].x, r[j].y, r[j].z, r[j].w};
+#pragma unroll
+      for (int i = 0; i < 4; ++i) v[4 * j + i] = at[i] >= 0 && at[i] < p.R ? __ldcg(p.share + at[i]) : 0.f;
     }
 #pragma unroll
-    for (int j = 0; j < kAhead; ++j)
-      if (r[j] >= 0 && r[j] < p.R) s += __ldcg(p.share + r[j]);
+    for (int j = 0; j < 4 * kQuads; ++j) s += v[j];
   }
+  for (; e < hi; e += 16) s += some_shares<16>(p, e, hi);
   return s;
 }
 
@@ -356,11 +378,13 @@ __global__ void __launch_bounds__(kPolThreads) policy_position_kernel(const Poli
   const bool any = __any_sync(0xffffffffu, hi - lo > kLong);
   if (lane == 0) is_long[warp] = any;
   ptx::dependency_wait();
-  if (!any && f < p.F) p.dloss[f] = shares<4>(p, lo, hi, 1);
+  if (!any && f < p.F) p.dloss[f] = some_shares<kLong>(p, lo, hi);
   __syncthreads();
   for (int g = 0; g < kWarps; ++g) {
     if (!is_long[g]) continue;
-    part[warp][lane] = shares<16>(p, int64_t{from[g][lane]} + warp, to[g][lane], kWarps);
+    const int first = from[g][lane], n = to[g][lane] - first;
+    auto cut = [&](int w) { return first + static_cast<int>(static_cast<int64_t>(n) * w / kWarps); };
+    part[warp][lane] = many_shares(p, cut(warp), cut(warp + 1));
     __syncthreads();
     if (warp == g && f < p.F) {
       float s = 0.f;

@@ -1044,7 +1044,7 @@ def rope_freqs(rot, base=1e4, stretch=1.0, trained=None, fast=32.0, slow=1.0):
 def _heads(t, name, shape=None):
     """(address, row stride) of a 3-d bf16 tensor whose rows may lie apart."""
     _rows3(t, name, shape)
-    n, h, d = t.shape
+    n, h, d = t.shape if shape is None else shape
     ld = t.stride(0) if n > 1 else h * d
     if ld < h * d or ld % 8:
         raise ValueError("%s: rows must not overlap and must lie a multiple of 8 elements apart" % name)
@@ -1088,7 +1088,9 @@ def rope_by_depth_ex(q, k, depth, freqs, interleaved=False, factor=1.0, inverse=
         p_in, ld_in = _heads(t, name, (F, t.shape[1], d) if isinstance(t, torch.Tensor) and t.dim() == 3 else None)
         if o is None:
             o = torch.empty(t.shape, dtype=torch.bfloat16, device=t.device)
-        p_o, ld_o = _heads(o, name + "_out", tuple(t.shape))
+            p_o, ld_o = o.data_ptr(), t.shape[1] * d
+        else:
+            p_o, ld_o = _heads(o, name + "_out", tuple(t.shape))
         if p_o == p_in and ld_o != ld_in:
             raise ValueError("%s_out starts where %s does, with other rows" % (name, name))
         at.append((p_in, ld_in, p_o, ld_o))
