@@ -66,7 +66,6 @@ constexpr int kBoxBytes = kHalf * 128; // 128 rows of 64 bf16
 constexpr int kThreads = 384;
 constexpr int kEpiThreads = 256;
 constexpr int kPanel = 8;
-constexpr int kStages = 5;
 constexpr int kChunk = 128;            // stages per accumulation of kDx, kDw
 constexpr int kMostK = 32768;          // channels of a sum that never stops
 constexpr int kPairs = 76;             // pairs a split over K aims to fill
@@ -102,10 +101,14 @@ struct Params {
   int32_t* err;
 };
 
+template <int kMode>
 struct Smem {
+  static constexpr bool kSix = kMode == kDx || kMode == kDw;
+  static constexpr int kStages = kSix ? 6 : 5;
+  static constexpr int kBoxes = kSix ? 1 : 2;
   uint8_t a[kStages][kBoxBytes];
   uint8_t b[kStages][kBoxBytes];
-  uint8_t out[2][2][kBoxBytes];        // two boxes per warpgroup; kGateBwd: two places of g and u
+  uint8_t out[2][kBoxes][kBoxBytes];        // two boxes per warpgroup; kGateBwd: two places of g and u
   float bias[2][kHalf];                // of the tile at hand, per warpgroup
   uint64_t full[kStages], empty[kStages];
   uint64_t tm_full[2], tm_empty[2];
@@ -115,8 +118,9 @@ struct Smem {
   int abort_flag;
   uint32_t issued;   // stages the producer has filled
 };
-constexpr size_t kSmemBytes = sizeof(Smem) + 1024;
-static_assert(kSmemBytes <= 227 * 1024, "shared memory");
+template <int kMode>
+constexpr size_t kSmemBytes = sizeof(Smem<kMode>) + 1024;
+static_assert(kSmemBytes<kLin> <= 227 * 1024 && kSmemBytes<kDx> <= 227 * 1024, "shared memory");
 
 // The split over K.  Pairs take tiles in rounds; the `tail` tiles left over from
 // whole rounds (all of them, if they are few) take a round of their own, which
@@ -274,7 +278,9 @@ template <int kMode, bool kOne, bool kNarrow>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     product_kernel(const __grid_constant__ Maps maps, const Params p) {
   extern __shared__ uint8_t smem_raw[];
-  Smem& S = *reinterpret_cast<Smem*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  using Sm = Smem<kMode>;
+  constexpr int kStages = Sm::kStages;
+  Sm& S = *reinterpret_cast<Sm*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   constexpr bool kAmn = kMode == kDw;                                          // A stored with M contiguous
   constexpr bool kBmn = kMode == kDx || kMode == kDw || kMode == kGateBwd;     // B stored with N contiguous
   constexpr bool kPlain = kMode == kLin || kMode == kDx || kMode == kDw;
@@ -453,7 +459,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     const bool leader = (threadIdx.x & 127) == 0;
     const uint32_t lane_off = static_cast<uint32_t>((warp & 3) * 32) << 16;
     const uint32_t bar_empty[2] = {ptx::cluster_addr(&S.tm_empty[0], 0), ptx::cluster_addr(&S.tm_empty[1], 0)};
-    uint8_t* const box[2] = {S.out[wg][0], S.out[wg][1]};
+    uint8_t* const box[2] = {S.out[wg][0], S.out[wg][Sm::kBoxes - 1]};
     auto meet = [&] { asm volatile("bar.sync %0, 128;" ::"r"(wg + 1) : "memory"); };
     uint32_t taken = 0;   // tiles that took something in; of the last, both boxes' loads may be under way
     uint32_t tile = 0, sent = 0;
@@ -574,7 +580,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
               if (takes) {
                 ok = fetched(b);
               } else {
-                if (leader) ptx::bulk_wait_read<kNarrow ? 0 : 1>();   // this box's last store
+                if (leader) ptx::bulk_wait_read<kNarrow || Sm::kBoxes == 1 ? 0 : 1>();   // this box's last store
                 meet();
               }
             }
@@ -840,14 +846,14 @@ int launch(const Maps& maps, const Params& p, bool after, cudaStream_t s) {
     // setmaxnreg waits for registers the CTA was not launched with
     if (!kOne && fa.numRegs * kThreads < kRegsNeeded) return TPK_E_UNSUPPORTED;
     return cuda_status(
-        cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(kSmemBytes)));
+        cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(kSmemBytes<kMode>)));
   }); });
   if (st != TPK_OK) return st;
   const int units = shape_of<kMode, kNarrow>(p).units;
   int pairs = num_sms() / 2;
   pairs = pairs < 1 ? 1 : pairs;
   pairs = pairs < units ? pairs : units;
-  return launch_kernel(kern, dim3(static_cast<unsigned>(2 * pairs)), kThreads, kSmemBytes, after, s, maps, p);
+  return launch_kernel(kern, dim3(static_cast<unsigned>(2 * pairs)), kThreads, kSmemBytes<kMode>, after, s, maps, p);
 }
 
 // Products of linear.cu that the feed-forward block uses too.  acc: acc_bytes;
