@@ -103,7 +103,7 @@ struct Params {
 
 template <int kMode>
 struct Smem {
-  static constexpr bool kSix = kMode == kDx || kMode == kDw;
+  static constexpr bool kSix = kMode == kDx || kMode == kDw || kMode == kGate;
   static constexpr int kStages = kSix ? 6 : 5;
   static constexpr int kBoxes = kSix ? 1 : 2;
   uint8_t a[kStages][kBoxBytes];
@@ -650,11 +650,20 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         }
       } else if constexpr (kMode == kGate) {
         // columns [0, 64) of this warpgroup: g at 0, u at 128 of the accumulator
-        uint32_t a[2][16];
-        if (p.save) {
+        uint32_t a[2][16], u16[2][16];
+        auto take_box = [&] {   // its last store has left
           if (leader) ptx::bulk_wait_read<0>();
           meet();
-        }
+        };
+        auto send = [&](const CUtensorMap* to) {
+          ptx::fence_async_shared();
+          meet();
+          if (leader) {
+            if (n0 < p.N && row0 < p.M) ptx::tma_store_2d(to, box[0], n0, row0);
+            ptx::bulk_commit();
+          }
+        };
+        if (p.save) take_box();
 #pragma unroll
         for (int half = 0; half < 2; ++half) {
           uint32_t g[32], up[32];
@@ -678,15 +687,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
               float lo, hi;
               ptx::unf2(ptx::mul2(pair_at(g, e), sg), lo, hi);
               o[e] = ptx::pack_f16x2(lo, hi);
+              ptx::unf2(ptx::mul2(pair_at(up, e), su), lo, hi);
+              u16[half][e] = ptx::pack_f16x2(lo, hi);
             }
             put64(box[0], rc, half, o);
-#pragma unroll
-            for (int e = 0; e < 16; ++e) {
-              float lo, hi;
-              ptx::unf2(ptx::mul2(pair_at(up, e), su), lo, hi);
-              o[e] = ptx::pack_f16x2(lo, hi);
-            }
-            put64(box[1], rc, half, o);
+            if (half == 1) send(&maps.out2);
           }
           with_act(p.act, [&](auto t) {
 #pragma unroll
@@ -697,31 +702,16 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             }
           });
         }
-        const bool inside = n0 < p.N && row0 < p.M;
-        int s = 0;
         if (p.save) {
-          ptx::fence_async_shared();
-          meet();
-          if (leader) {
-            if (inside) ptx::tma_store_2d(&maps.out2, box[0], n0, row0);
-            ptx::bulk_commit();
-            if (inside) ptx::tma_store_2d(&maps.out3, box[1], n0, row0);
-            ptx::bulk_commit();
-            ptx::bulk_wait_read<1>();   // g has left
-          }
-        } else {
-          s = static_cast<int>(sent++ & 1);
-          if (leader) ptx::bulk_wait_read<1>();
+          take_box();
+          put64(box[0], rc, 0, u16[0]);
+          put64(box[0], rc, 1, u16[1]);
+          send(&maps.out3);
         }
-        meet();
-        put64(box[s], rc, 0, a[0]);
-        put64(box[s], rc, 1, a[1]);
-        ptx::fence_async_shared();
-        meet();
-        if (leader) {
-          if (inside) ptx::tma_store_2d(&maps.out, box[s], n0, row0);
-          ptx::bulk_commit();
-        }
+        take_box();
+        put64(box[0], rc, 0, a[0]);
+        put64(box[0], rc, 1, a[1]);
+        send(&maps.out);
       } else {
         // kGateBwd: 32 of 64 columns at a time, g and u in the two boxes of a place
         uint32_t raw[32];
