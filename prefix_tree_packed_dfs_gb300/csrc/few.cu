@@ -4,8 +4,10 @@
 // is shared out over a cluster of up to 8 CTAs, so that a few dozen tiles keep
 // every SM loading; each CTA streams its share through a ring of TMA stages,
 // and the partial sums meet through distributed shared memory, added in the
-// order of the ranks.  For the gated form a tile holds 64 rows of the gate's
-// weights and the 64 of the up projection's for the same channels.
+// order of the ranks.  For the gated form a tile holds rows of the gate's weights
+// and as many of the up projection's for the same channels.  A tile may have fewer
+// than 128 rows (a multiple of 8: what the MMA reads beyond them reaches no result),
+// so that the tiles come out even over the SMs (few_shape).
 #include "few.cuh"
 
 namespace tpk {
@@ -13,7 +15,6 @@ namespace product {
 namespace {
 
 constexpr int kFewThreads = 128;
-constexpr int kFewCluster = 8;
 
 template <int kTok>
 struct FewSmem {
@@ -30,6 +31,7 @@ constexpr size_t kFewBytes = sizeof(FewSmem<kTok>) + 1024;
 
 struct FewParams {
   int32_t N, O, k_iters;     // tokens, results per token (of one of the two, gated), stages of K
+  int32_t rows;              // channels of a tile
   int32_t act;
   const float* bias;
   const __nv_bfloat16* residual;
@@ -63,13 +65,9 @@ __global__ void __launch_bounds__(kFewThreads) few_kernel(const __grid_constant_
 
   if (kGated) ptx::dependents_launch();
   auto weights = [&](int st, int k) {
-    ptx::mbar_arrive_expect_tx(&S.full[st], kBoxBytes + kTok * 128);
-    if (kGated) {
-      ptx::tma_load_2d(S.a[st], &maps.w, &S.full[st], (k0 + k) * 64, tile * 64);
-      ptx::tma_load_2d(S.a[st] + kBoxBytes / 2, &maps.w2, &S.full[st], (k0 + k) * 64, tile * 64);
-    } else {
-      ptx::tma_load_2d(S.a[st], &maps.w, &S.full[st], (k0 + k) * 64, tile * 128);
-    }
+    ptx::mbar_arrive_expect_tx(&S.full[st], (kGated ? 2 : 1) * p.rows * 128 + kTok * 128);
+    ptx::tma_load_2d(S.a[st], &maps.w, &S.full[st], (k0 + k) * 64, tile * p.rows);
+    if (kGated) ptx::tma_load_2d(S.a[st] + p.rows * 128, &maps.w2, &S.full[st], (k0 + k) * 64, tile * p.rows);
   };
   const int first = nk < kS ? nk : kS;
   if (threadIdx.x == 0) {
@@ -149,18 +147,17 @@ __global__ void __launch_bounds__(kFewThreads) few_kernel(const __grid_constant_
   if ((!ok || S.abort_flag) && threadIdx.x == 0 && p.err) *p.err = TPK_E_TIMEOUT;
 
   // this CTA's share of the channels, four at a time
-  constexpr int kWide = kGated ? 64 : 128;
-  const int quads = kWide / 4 / static_cast<int>(ranks);
+  const int quads = (p.rows / 4 + static_cast<int>(ranks) - 1) / static_cast<int>(ranks);
   for (int i = threadIdx.x; i < p.N * quads; i += kFewThreads) {
     const int t = i / quads, at = (static_cast<int>(rank) * quads + i % quads) * 4;
-    const int o = tile * kWide + at;
-    if (o >= p.O) continue;
+    const int o = tile * p.rows + at;
+    if (at >= p.rows || o >= p.O) continue;
     float4 v = make_float4(0.f, 0.f, 0.f, 0.f), u = v;
     for (uint32_t k = 0; k < ranks; ++k) {
       const float4 d = ptx::lds128_cluster(red + t * 128 + at, k);
       v.x += d.x; v.y += d.y; v.z += d.z; v.w += d.w;
       if (kGated) {
-        const float4 e = ptx::lds128_cluster(red + t * 128 + 64 + at, k);
+        const float4 e = ptx::lds128_cluster(red + t * 128 + p.rows + at, k);
         u.x += e.x; u.y += e.y; u.z += e.z; u.w += e.w;
       }
     }
@@ -184,62 +181,90 @@ __global__ void __launch_bounds__(kFewThreads) few_kernel(const __grid_constant_
   ptx::cluster_sync();   // nobody reads a CTA that has gone
 }
 
-// CTAs that share a tile's K: as many as run together, two per SM, each with two
-// stages or more.  (One token, width 8,192 to 2,048, 16 tiles: 8 CTAs each 8.4 us, 4
-// 10.3, 1 27; 40 tokens, 192 gated tiles of width 4,096: 1 CTA each 36 us, 4 43.)
-int few_ranks(int64_t tiles, int k_iters) {
-  int s = kFewCluster;
-  while (s > 1 && (tiles * s > 2 * num_sms() || k_iters < 2 * s)) s /= 2;
-  return s;
+// Channels per tile and CTAs that share a tile's K (each with two stages or more):
+// the pair that leaves the busiest SM the least to read, weights and tokens, of
+// those whose clusters all run together (a second round of clusters cost one token,
+// 2,048 to 4,096, 11.0 us against 8.5); among equals the one with most CTAs.  More
+// channels than that: full tiles, one CTA each.  Two CTAs run per SM; of the clusters
+// of 4 and 8 all but two are at home at once (74 and 36 on 152 SMs; the runtime's
+// occupancy query counts one CTA per SM for kernels that use tensor memory).  (40
+// tokens, width 4,096, 12,288 gated channels: 48 channels a tile 36 us, 64 39; one
+// token, width 8,192 to 2,048, 128 channels: 8 CTAs 12 us, 4 about 14, 1 27.)
+struct FewShape {
+  int rows, ranks;
+  int64_t tiles;
+};
+FewShape few_shape(int64_t O, bool gated, int tok, int k_iters) {
+  const int most_rows = gated ? 64 : 128, sms = num_sms();
+  FewShape best{most_rows, 1, (O + most_rows - 1) / most_rows};
+  double least = 0.0;
+  for (int ranks = 1; ranks <= 8 && (ranks == 1 || k_iters >= 2 * ranks); ranks *= 2)
+    for (int rows = most_rows; rows >= most_rows / 2; rows -= 8) {
+      const int64_t tiles = (O + rows - 1) / rows, ctas = tiles * ranks;
+      if (tiles > 2 * sms / ranks - (ranks > 2 ? 2 : 0)) continue;
+      // (one CTA alone on its SM leaves it idle at its ends)
+      const double read = static_cast<double>((ctas + sms - 1) / sms * ((gated ? 2 : 1) * rows + tok)) / ranks *
+                          (ctas > sms ? 1.0 : 1.15);
+      if (least == 0.0 || read < least || (read == least && ctas > best.tiles * best.ranks)) {
+        least = read;
+        best = FewShape{rows, ranks, tiles};
+      }
+    }
+  return best;
 }
 
+struct FewConfig {   // a launch of clusters of `ranks` CTAs
+  cudaLaunchConfig_t cfg{};
+  cudaLaunchAttribute at[2];
+  FewConfig(int64_t tiles, int ranks, size_t smem, bool after, cudaStream_t s) {
+    cfg.gridDim = dim3(static_cast<unsigned>(tiles * ranks));
+    cfg.blockDim = dim3(kFewThreads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = s;
+    at[0].id = cudaLaunchAttributeClusterDimension;
+    at[0].val.clusterDim.x = static_cast<unsigned>(ranks);
+    at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
+    at[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[1].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = at;
+    cfg.numAttrs = after ? 2 : 1;
+  }
+};
+
 template <int kTok, bool kGated>
-int few_launch(const FewMaps& m, const FewParams& p, bool after, cudaStream_t s) {
+int few_launch(const Mat& x, const Mat& w, const Mat& w2, FewParams& p, bool after, cudaStream_t s) {
   constexpr auto kern = few_kernel<kTok, kGated>;
   static PerContext<int> rec;
-  const int st = guarded([&] { return set_smem_once(rec, kern, kFewBytes<kTok>); });
+  int st = guarded([&] { return set_smem_once(rec, kern, kFewBytes<kTok>); });
   if (st != TPK_OK) return st;
-  const int64_t tiles = (p.O + (kGated ? 63 : 127)) / (kGated ? 64 : 128);
-  const int ranks = few_ranks(tiles, p.k_iters);
-  cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3(static_cast<unsigned>(tiles * ranks));
-  cfg.blockDim = dim3(kFewThreads);
-  cfg.dynamicSmemBytes = kFewBytes<kTok>;
-  cfg.stream = s;
-  cudaLaunchAttribute at[2];
-  at[0].id = cudaLaunchAttributeClusterDimension;
-  at[0].val.clusterDim.x = static_cast<unsigned>(ranks);
-  at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
-  at[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  at[1].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = at;
-  cfg.numAttrs = after ? 2 : 1;
-  return cuda_status(cudaLaunchKernelEx(&cfg, kern, m, p));
+  const FewShape shape = few_shape(p.O, kGated, kTok, p.k_iters);
+  p.rows = shape.rows;
+  FewMaps m;
+  st = map_of(&m.w, w, shape.rows);
+  if (st == TPK_OK) st = map_of(&m.x, x, kTok);
+  if (st == TPK_OK && kGated) st = map_of(&m.w2, w2, shape.rows);
+  if (st != TPK_OK) return st;
+  FewConfig c(shape.tiles, shape.ranks, kFewBytes<kTok>, after, s);
+  return cuda_status(cudaLaunchKernelEx(&c.cfg, kern, m, p));
 }
 
 template <bool kGated>
-int few_dispatch(const Mat& x, FewMaps& m, const FewParams& p, bool after, cudaStream_t s) {
+int few_dispatch(const Mat& x, const Mat& w, const Mat& w2, FewParams& p, bool after, cudaStream_t s) {
+  p.N = static_cast<int32_t>(x.rows);
+  p.O = static_cast<int32_t>(w.rows);
+  p.k_iters = static_cast<int32_t>((w.cols + 63) / 64);
   const int tok = (p.N + 15) / 16 * 16;
-  const int st = map_of(&m.x, x, tok);
-  if (st != TPK_OK) return st;
-  return tok == 16   ? few_launch<16, kGated>(m, p, after, s)
-         : tok == 32 ? few_launch<32, kGated>(m, p, after, s)
-         : tok == 48 ? few_launch<48, kGated>(m, p, after, s)
-                     : few_launch<64, kGated>(m, p, after, s);
+  return tok == 16   ? few_launch<16, kGated>(x, w, w2, p, after, s)
+         : tok == 32 ? few_launch<32, kGated>(x, w, w2, p, after, s)
+         : tok == 48 ? few_launch<48, kGated>(x, w, w2, p, after, s)
+                     : few_launch<64, kGated>(x, w, w2, p, after, s);
 }
 
 }  // namespace
 
 int few_linear(const Mat& x, const Mat& w, const float* bias, int act, const Mat& residual, const Mat& y, bool after,
                int32_t* err, cudaStream_t s) {
-  FewMaps m;
-  int st = map_of(&m.w, w, 128);
-  if (st != TPK_OK) return st;
-  m.w2 = m.w;
   FewParams p{};
-  p.N = static_cast<int32_t>(x.rows);
-  p.O = static_cast<int32_t>(w.rows);
-  p.k_iters = static_cast<int32_t>((w.cols + 63) / 64);
   p.act = act;
   p.bias = bias;
   p.residual = static_cast<const __nv_bfloat16*>(residual.p);
@@ -247,23 +272,16 @@ int few_linear(const Mat& x, const Mat& w, const float* bias, int act, const Mat
   p.y = static_cast<__nv_bfloat16*>(const_cast<void*>(y.p));
   p.ld_y = y.ld;
   p.err = err;
-  return few_dispatch<false>(x, m, p, after, s);
+  return few_dispatch<false>(x, w, w, p, after, s);
 }
 
 int few_gate(const Mat& x, const Mat& w_gate, const Mat& w_up, int act, const Mat& a, int32_t* err, cudaStream_t s) {
-  FewMaps m;
-  int st = map_of(&m.w, w_gate, 64);
-  if (st == TPK_OK) st = map_of(&m.w2, w_up, 64);
-  if (st != TPK_OK) return st;
   FewParams p{};
-  p.N = static_cast<int32_t>(x.rows);
-  p.O = static_cast<int32_t>(w_gate.rows);
-  p.k_iters = static_cast<int32_t>((w_gate.cols + 63) / 64);
   p.act = act;
   p.y = static_cast<__nv_bfloat16*>(const_cast<void*>(a.p));
   p.ld_y = a.ld;
   p.err = err;
-  return few_dispatch<true>(x, m, p, false, s);
+  return few_dispatch<true>(x, w_gate, w_up, p, false, s);
 }
 
 }  // namespace product
