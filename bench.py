@@ -925,7 +925,10 @@ def run_layout(a):
 def run_operators(a):
     """The operators around the token mixers on one workload's packed
     positions: width Hq * head_dim, the workloads' 32,000 token ids, targets
-    the next packed token of every position that has one.  L2 flushed before
+    the next packed token of every position that has one; the projections
+    (fused q, k, v, and the output onto the residual stream), a gated
+    feed-forward block of four times the width, rotary positions stretched for
+    a long context, and the policy objective over every raw token.  L2 flushed before
     every timed call; one JSON line."""
     import torch
     import workloads
@@ -950,6 +953,17 @@ def run_operators(a):
     h = rows[0]
     loss, lse = ops.lm_loss(h, table, target, scale=C ** -0.5)
     n_on = int((target >= 0).sum())
+    Hq, Hkv, d, I, R = w.n_heads_q, w.n_heads_kv, w.head_dim, 4 * C, plan.info["n_raw"]
+    qkv_w, out_w = wrng.normal_bf16(seed + 6, ((Hq + 2 * Hkv) * d, C), "cuda"), wrng.normal_bf16(seed + 7, (C, C), "cuda")
+    w_in, w_out = wrng.normal_bf16(seed + 8, (2 * I, C), "cuda"), wrng.normal_bf16(seed + 9, (C, I), "cuda")
+    qkv = ops.linear(h, qkv_w)
+    O = qkv.shape[1]
+    q, k = qkv[:, :Hq * d].unflatten(1, (Hq, d)), qkv[:, Hq * d:(Hq + Hkv) * d].unflatten(1, (Hkv, d))
+    freqs = ops.rope_freqs(d, w.rope_base, stretch=8.0, trained=8192)
+    _, pre, a_kept = ops.gated_ffn(h, w_in, w_out, save=True)
+    weight = torch.from_numpy((nxt >= 0).astype(np.float32) / len(nxt)).cuda()
+    old = -ops.scatter_token_index(dp.token_index, lse_src=loss[None])[1][0]
+    adv = torch.ones(R, device="cuda")
 
     def timed(fn):
         for _ in range(a.warmup):
@@ -974,7 +988,17 @@ def run_operators(a):
              16 * F * C, 0),
             ("lm_loss", lambda: ops.lm_loss(h, table, target, scale=C ** -0.5), (F + V) * C * 2, 2 * n_on * V * C),
             ("lm_loss_bwd", lambda: ops.lm_loss_bwd(h, table, target, lse, dloss, scale=C ** -0.5),
-             2 * (F + V) * C * 2, 6 * n_on * V * C)):
+             2 * (F + V) * C * 2, 6 * n_on * V * C),
+            ("linear_qkv", lambda: ops.linear(h, qkv_w), 2 * (F * C + O * C + F * O), 2 * F * C * O),
+            ("linear_out", lambda: ops.linear(h, out_w, residual=res), 2 * (3 * F * C + C * C), 2 * F * C * C),
+            ("linear_bwd_qkv", lambda: ops.linear_bwd(h, qkv_w, qkv), 4 * (F * C + O * C) + 2 * F * O, 4 * F * C * O),
+            ("gated_ffn", lambda: ops.gated_ffn(h, w_in, w_out, residual=res), 2 * (3 * F * C + 3 * C * I),
+             6 * F * C * I),
+            ("gated_ffn_bwd", lambda: ops.gated_ffn_bwd(h, w_in, w_out, dx, pre, a_kept),
+             2 * (3 * F * C + 6 * C * I + 3 * F * I), 12 * F * C * I),
+            ("rope_by_depth_ex", lambda: ops.rope_by_depth_ex(q, k, dp.depth, freqs), 4 * F * (Hq + Hkv) * d + 4 * F, 0),
+            ("policy_loss", lambda: ops.policy_loss(loss, old, adv, weight, dp.token_index, dp.fwd_raw_begin,
+                                                    dp.fwd_raw, ref_logp=old, kl_coef=0.04), 24 * R + 12 * F, 0)):
         ms = timed(fn)
         out[name] = {"ms": ms, "algorithmic_bytes": nbytes, "gbs": nbytes / ms / 1e6,
                      "frac_of_copy_peak": nbytes / ms / 1e6 / peaks["hbm_gbs"]}
