@@ -13,14 +13,26 @@
 //
 // 256 x 256 tiles on a pair of CTAs (tcgen05 cta_group::2): each CTA holds 128
 // rows of A, 128 of B and its 128 rows of the result.  64 elements of K per
-// stage, five stages filled by TMA; two accumulators of 256 TMEM columns, so
-// that a tile's epilogue runs under the next tile's products.  Results leave
-// through shared memory by TMA; what an epilogue reads besides (residual, dy,
-// g and u) comes in by TMA to the very places its results leave from, issued
-// when the tile before has left and so long before the accumulator is ready.
+// stage, the stages filled by TMA; two accumulators of 256 TMEM columns, so that
+// a tile's epilogue runs under the next tile's products.  Results leave through
+// shared memory by TMA; what an epilogue reads besides (residual, dy, g and u)
+// comes in by TMA to the very places its results leave from, issued when the tile
+// before has left and so long before the accumulator is ready.  kDx, kDw and kGate
+// read nothing, let a warpgroup's results leave through one box and have six
+// stages (tensor pipe 88-90% of the cycles); the others have five and two boxes.
+// (Residual, dy, g and u by plain loads of 64 bytes per row and thread, one chunk
+// ahead and with L2 prefetches, six stages for all: kDz 188 us against 169,
+// kGateBwd 250 against 189 at 8,192 rows.)
 // kGate takes 128 rows of the gate's weights and 128 of the up projection's as
 // one B tile (one of each per CTA), so a thread's accumulator row holds g and u
 // of the same channels.
+// kGateBwd moves 64 columns of g and u in and of dg and du out at a time, through
+// two places; warp 3 carries them, so that a place is filled again, for the next
+// tile too, as soon as its results have left.  Its g and u come in beside operands
+// that take 64 bytes per cycle and SM alone: 32,768 rows, widths 2,048 and 8,192,
+// 711 us (1.55 PFLOP/s) against 545 for the same product without them.  (Four
+// stages and three places 790 us, boxes of 32 columns 740, g and u sent ahead to
+// L2 776.)
 // The tensor core adds to its fp32 accumulator with truncation: 1e-7 of the
 // running sum per step of 16 elements of K.  The sums over rows (kDw) and over
 // the wide side (kDx) stop every 8,192 elements and are added up in registers
@@ -32,24 +44,21 @@
 // 2^-29 of its group's largest still has its 11 bits); with g and u in bf16 the
 // gradients' error over fp64 was 3.0e-3 of their norm against 2.4e-3 with them
 // unrounded, of which 1.7e-3 is the results' own rounding.
+// A few tiles leave most SMs idle and wait for their epilogue at the end: kLin, kDz,
+// kDx and kDw then take tiles half as wide (256 x 128, plan_of).
 // Kernels of one call overlap (programmatic dependent launch): each sets itself
 // up under the one before and then waits for it.  A product that needs nothing of
 // the one before, where that one leaves SMs free (early), takes them at once and
 // waits at its end, so that a kernel that is done means that those before it are
 // (1,001 rows, widths 1,000 and 552, forward and backward: 50 us against 56; beside
 // a product that fills the GPU it costs 1%).
-// A few tiles leave most SMs idle and wait for their epilogue at the end: kLin, kDz,
-// kDx and kDw then take tiles half as wide (256 x 128, plan_of).
 // Warps of a CTA: 0 TMA producer, 1 MMA issuer (of the pair's first CTA), 2
-// TMEM owner, 4-11 epilogue (two warpgroups).  kGateBwd moves 64 columns of g and
-// u in and of dg and du out at a time, through two places; warp 3 carries them, so
-// that a place is filled again, for the next tile too, as soon as its results have
-// left.  Its g and u come in beside operands that take 64 bytes per cycle and SM
-// alone, which is what bounds it: 32,768 rows, widths 2,048 and 8,192, 711 us (1.55
-// PFLOP/s; the same product without them 545).  With four stages and three places
-// it took 790, with boxes of 32 columns 740, with g and u sent ahead to L2 776.  CTAs are persistent and walk the
-// tiles in panels of 8 columns of tiles, so that the pairs running together
-// share rows of A and of B in L2.
+// TMEM owner, 3 kGateBwd's carrier, 4-11 epilogue (two warpgroups).  CTAs are
+// persistent and walk the tiles in panels of 8 columns of tiles, so that the pairs
+// running together share rows of A and of B in L2.
+// What bounds it: the tensor pipe, then the power limit (8,192 rows: gate 2 x
+// 2,048 x 8,192 294 us, 1.87 PFLOP/s; dx 285, dw 275; 96,888 rows of 2,048 onto the
+// residual stream 442 us, 1.84 PFLOP/s; long runs settle at 1.6-1.7).
 #pragma once
 #include <type_traits>
 
