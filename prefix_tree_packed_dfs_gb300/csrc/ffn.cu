@@ -57,6 +57,7 @@ Params params(int64_t M, int64_t N, int64_t K, int act, int32_t* err) {
   p.N = static_cast<int32_t>(N);
   p.K = static_cast<int32_t>(K);
   p.splits = 1;
+  p.teams = 1;
   p.whole = INT32_MAX;   // nothing is split
   p.act = act;
   p.err = err;

@@ -84,10 +84,10 @@ int column_sums(const T* m, int64_t rows, int64_t cols, int64_t ld, float* part,
   const unsigned across = static_cast<unsigned>((cols + kSumCols - 1) / kSumCols);
   const int64_t per = sum_rows(rows, cols), blocks = sum_blocks(rows, cols);
   const int n = static_cast<int>(cols);
-  const int st = launch_kernel(column_sum_kernel<T>, dim3(across, static_cast<unsigned>(blocks)), kSumThreads, 0, true,
+  const int st = launch_kernel(column_sum_kernel<T>, dim3(across, static_cast<unsigned>(blocks)), kSumThreads, 0, 1, true,
                                s, m, rows, n, ld, per, blocks == 1 ? out : part, 1);
   if (st != TPK_OK || blocks == 1) return st;
-  return launch_kernel(column_sum_kernel<float>, dim3(across), kSumThreads, 0, true, s, static_cast<const float*>(part),
+  return launch_kernel(column_sum_kernel<float>, dim3(across), kSumThreads, 0, 1, true, s, static_cast<const float*>(part),
                        blocks, n, cols, blocks, out, 0);
 }
 
@@ -151,7 +151,7 @@ __global__ void __launch_bounds__(256) join_kernel(const float* __restrict__ acc
 
 int join(const Params& p, const float* bias, int act, const Mat& residual, const Mat& out, cudaStream_t s) {
   const int64_t blocks = (tiles_of(p.M, p.N) - p.whole) * (kTile / 8), most = int64_t{num_sms()} * 16;
-  return launch_kernel(join_kernel, dim3(static_cast<unsigned>(blocks < most ? blocks : most)), 256, 0, true, s,
+  return launch_kernel(join_kernel, dim3(static_cast<unsigned>(blocks < most ? blocks : most)), 256, 0, 1, true, s,
                        static_cast<const float*>(p.acc), p.M, p.N, p.whole, p.splits, bias, act,
                        static_cast<const __nv_bfloat16*>(residual.p), residual.ld,
                        static_cast<__nv_bfloat16*>(const_cast<void*>(out.p)), out.ld);
@@ -164,6 +164,7 @@ Params params(int64_t M, int64_t N, int64_t K, float* acc, int32_t* err) {
   p.K = static_cast<int32_t>(K);
   const Plan plan = plan_of(M, N, K);
   p.narrow = plan.narrow;
+  p.teams = plan.teams;
   p.whole = static_cast<int32_t>(plan.split.whole);
   p.splits = plan.split.splits;
   p.acc = acc;
@@ -231,6 +232,10 @@ int linear_product(const Mat& x, const Mat& w, const float* bias, int act, const
   p.bias = bias;
   p.act = act;
   p.has_in = residual.p != nullptr;
+  p.in = static_cast<const uint16_t*>(residual.p);
+  p.ld_in = residual.ld;
+  p.out = static_cast<uint16_t*>(const_cast<void*>(y.p));
+  p.ld_out = y.ld;
   st = launch_plan<kLin>(m, p, after, s);
   return st == TPK_OK && p.splits > 1 ? join(p, bias, act, residual, y, s) : st;
 }
@@ -244,6 +249,8 @@ int input_product(const Mat& dz, const Mat& w, const Mat& dx, float* acc, bool a
   if (st != TPK_OK) return st;
   Params p = params(dz.rows, w.cols, dz.cols, acc, err);
   p.late = 1;
+  p.out = static_cast<uint16_t*>(const_cast<void*>(dx.p));
+  p.ld_out = dx.ld;
   *left = p;
   return launch_plan<kDx>(m, p, after, s);
 }
@@ -256,7 +263,9 @@ int weight_product(const Mat& dz, const Mat& x, const Mat& dw, float* acc, const
   if (st == TPK_OK) st = map_of(&m.out, dw, kHalf);
   if (st != TPK_OK) return st;
   Params p = params(dz.cols, x.cols, dz.rows, acc, err);
-  p.early = (before.narrow ? shape_of<kDx, true>(before) : shape_of<kDx>(before)).units < kPairs;
+  p.early = (before.narrow ? shape_of<kDx, true>(before) : shape_of<kDx>(before)).units * before.teams < kPairs;
+  p.out = static_cast<uint16_t*>(const_cast<void*>(dw.p));
+  p.ld_out = dw.ld;
   *left = p;
   return launch_plan<kDw>(m, p, true, s);
 }
@@ -332,6 +341,10 @@ extern "C" int tpk_linear_bwd(const void* x, int64_t ld_x, const void* w, const 
     }
     if (st == TPK_OK) st = map_of(&m.b, mw, p.narrow ? kHalf / 2 : kHalf);
     if (st == TPK_OK) st = map_of(&m.in, dz, kHalf);
+    p.in = static_cast<const uint16_t*>(dy);
+    p.ld_in = ld_dy;
+    p.out = reinterpret_cast<uint16_t*>(k.dz);
+    p.ld_out = own_stride(O);
     dz = Mat{k.dz, N, O, own_stride(O)};
     if (st == TPK_OK) st = map_of(&m.out, dz, kHalf);
     p.bias = bias;

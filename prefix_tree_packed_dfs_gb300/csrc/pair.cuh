@@ -82,6 +82,18 @@ __device__ __forceinline__ void st_cluster(int* p, uint32_t rank, int v) {
   asm volatile("st.shared::cluster.s32 [%0], %1;" ::"r"(cluster_addr(p, rank)), "r"(v) : "memory");
 }
 
+// 16 bytes at a cluster address, as two packed fp32 pairs.
+__device__ __forceinline__ ulonglong2 lds128u_cluster(uint32_t addr) {
+  ulonglong2 v;
+  asm volatile("ld.shared::cluster.v2.b64 {%0, %1}, [%2];" : "=l"(v.x), "=l"(v.y) : "r"(addr) : "memory");
+  return v;
+}
+__device__ __forceinline__ uint32_t cluster_size() {
+  uint32_t r;
+  asm volatile("mov.u32 %0, %%cluster_nctarank;" : "=r"(r));
+  return r;
+}
+
 // Programmatic dependent launch: the next kernel of the stream, where it asked
 // for it, may start (launch); everything of the kernel before is done (wait).
 __device__ __forceinline__ void dependents_launch() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
@@ -110,12 +122,12 @@ __device__ __forceinline__ void mma_ss_pair(uint32_t d_tmem, uint64_t a_desc, ui
       : "memory");
 }
 // Arrive (once) on `bar` in both CTAs when all previously issued tcgen05
-// async operations of this thread have completed.
-__device__ __forceinline__ void mma_commit_pair(uint64_t* bar) {
+// async operations of this thread have completed; lead: the pair's first CTA.
+__device__ __forceinline__ void mma_commit_pair(uint64_t* bar, uint32_t lead = 0) {
   asm volatile(
       "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(
           smem_addr(bar)),
-      "h"(static_cast<uint16_t>(3))
+      "h"(static_cast<uint16_t>(3u << lead))
       : "memory");
 }
 

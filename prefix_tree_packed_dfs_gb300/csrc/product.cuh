@@ -45,7 +45,12 @@
 // gradients' error over fp64 was 3.0e-3 of their norm against 2.4e-3 with them
 // unrounded, of which 1.7e-3 is the results' own rounding.
 // A few tiles leave most SMs idle and wait for their epilogue at the end: kLin, kDz,
-// kDx and kDw then take tiles half as wide (256 x 128, plan_of).
+// kDx and kDw then take tiles half as wide (256 x 128, plan_of), and up to four pairs
+// of a cluster share a tile's K: each leaves its sums in shared memory, where the
+// stages were, and takes a part of the rows out, adding the pairs' sums up in their
+// order through distributed shared memory (a warp reads whole rows: 16 bytes of 32
+// rows each took 4 us longer).  (1,003 rows, widths 5,456 to 1,000:
+// 17 us against 28 in narrow tiles alone; 256 rows, 8,192 to 256: 12 against 16.)
 // Kernels of one call overlap (programmatic dependent launch): each sets itself
 // up under the one before and then waits for it.  A product that needs nothing of
 // the one before, where that one leaves SMs free (early), takes them at once and
@@ -78,6 +83,8 @@ constexpr int kPanel = 8;
 constexpr int kChunk = 128;            // stages per accumulation of kDx, kDw
 constexpr int kMostK = 32768;          // channels of a sum that never stops
 constexpr int kPairs = 76;             // pairs a split over K aims to fill
+constexpr int kTeams = 4;              // pairs of a cluster at most
+constexpr int kClusters4 = 36, kClusters8 = 15;   // clusters of 4 and 8 CTAs that 152 SMs hold at once, one CTA each
 constexpr int kGroup = 32;             // channels that share a power of two in what kGate keeps
 // The chunked epilogue holds 128 columns of a row per thread: the other warps
 // give registers to its two warpgroups.
@@ -98,9 +105,13 @@ struct Params {
   int32_t whole, splits;     // tiles before the split ones; splits of each of those (split_of)
   int32_t act;
   int32_t has_in;            // kLin: a residual
+  const uint16_t* in;        // teams: residual or dy, and the result, which leave their rows' maps unused
+  uint16_t* out;
+  int64_t ld_in, ld_out;
   int32_t save;              // kGate: g and u go out too
   int32_t early;             // needs nothing of the kernel before, only of those that it waited for
   int32_t narrow;            // tiles of 128 columns (the kernel knows by its type)
+  int32_t teams;             // pairs that share a tile's K (the kernel knows by its cluster); > 1: one tile each
   int32_t late;              // lets the next kernel start only after its own wait (that one may be early)
   const float* bias;         // [N] or nullptr
   float* colsum;             // kDz: [ceil(M / 32)][N] sums of 32 rows of dz; nullptr: none
@@ -164,20 +175,36 @@ inline Split split_of(int64_t tiles, int64_t k_iters, double* us_out = nullptr) 
 // Those need 256 cycles for 64 elements of K where few pairs run, about 384 where
 // the operands' way into the SMs is full, and half of the 2.2 us that a lone wide
 // tile's epilogue takes.  (1,000 rows, widths 1,000 and 552, gelu: 10.7 us in narrow
-// tiles, 14.5 in wide ones; 200 rows, widths 1,024 and 256: 7.2 against 10.5.)
+// tiles, 14.5 in wide ones; 200 rows, widths 1,024 and 256: 7.2 against 10.5.)  A team
+// of pairs divides the stages and pays about 2.2 us to meet.
 struct Plan {
   bool narrow;
+  int teams;
   Split split;
 };
 inline Plan plan_of(int64_t M, int64_t N, int64_t K) {
   const int64_t mt = (M + kTile - 1) / kTile, wide = mt * ((N + kTile - 1) / kTile);
   const int64_t narrow = mt * ((N + kHalf - 1) / kHalf), k_iters = (K + 63) / 64;
   double us;
-  Plan p{false, split_of(wide, k_iters, &us)};
-  if (wide > kPairs || k_iters > kChunk) return p;
+  Plan p{false, 1, split_of(wide, k_iters, &us)};
+  us += 2.2;
+  if (wide > kPairs) return p;
   const int64_t rounds = (narrow + kPairs - 1) / kPairs;
   const double stage_us = narrow <= kPairs / 2 ? 0.14 : 0.2;
-  if (stage_us * static_cast<double>(rounds * k_iters) + 1.1 < us + 2.2) p = Plan{true, Split{narrow, 0, 1}};
+  const double alone = stage_us * static_cast<double>(rounds * k_iters) + 1.1;
+  if (alone < us && k_iters <= kChunk) {
+    us = alone;
+    p = Plan{true, 1, Split{narrow, 0, 1}};
+  }
+  for (int teams = 2; teams <= kTeams; teams *= 2) {
+    const int64_t each = (k_iters + teams - 1) / teams;
+    if (narrow > (teams == 2 ? kClusters4 : kClusters8) || k_iters < 2 * teams || each > kChunk) continue;
+    const double together = stage_us * static_cast<double>(each) + 1.1 + 2.2;
+    if (together < us) {
+      us = together;
+      p = Plan{true, teams, Split{narrow, 0, 1}};
+    }
+  }
   return p;
 }
 
@@ -211,9 +238,13 @@ __device__ __forceinline__ void place_of(int mt, int nt, int t, int& m, int& n) 
   m = t / width;
   n = panel * kPanel + t % width;
 }
-__device__ __forceinline__ Unit unit_of(const Params& p, const Shape& s, int u) {
-  Unit w{0, 0, 0, s.k_iters, -1};
-  if (u >= p.whole && p.splits > 1) {
+template <bool kNarrow>
+__device__ __forceinline__ Unit unit_of(const Params& p, const Shape& s, int u, int team, int teams) {
+  Unit w{0, 0, 0, s.k_iters, -1, 0};
+  if (kNarrow) {   // never split over units, but over the pairs of a cluster
+    w.k0 = s.k_iters * team / teams;
+    w.nk = s.k_iters * (team + 1) / teams - w.k0;
+  } else if (u >= p.whole && p.splits > 1) {
     const int tail = s.mt * s.nt - p.whole;
     w.split = (u - p.whole) / tail;
     u = p.whole + (u - p.whole) % tail;
@@ -266,6 +297,11 @@ __device__ __forceinline__ uint32_t largest_exponent(const uint32_t (&x)[32]) {
 __device__ __forceinline__ float group_scale(uint32_t e) { return __uint_as_float((268 - e) << 23); }
 __device__ __forceinline__ float group_unscale(uint32_t e) { return __uint_as_float((e - 14) << 23); }
 
+// Where the 16 bytes q of a row of 128 fp32 sums lie in a pair's shared memory.
+__device__ __forceinline__ uint32_t team_place(int r, int q) {
+  return static_cast<uint32_t>(r * 512 + ((q ^ (r & 31)) * 16));
+}
+
 // Sums over the warp's 32 rows of x[0..31] (a row per lane): lane l returns
 // the sum of column l.  Each step halves the columns a lane holds.
 __device__ __forceinline__ float column_sums(float (&x)[32], int lane) {
@@ -284,7 +320,7 @@ __device__ __forceinline__ float column_sums(float (&x)[32], int lane) {
 // kOne: every tile is a single accumulation, which goes out while it is read
 // from TMEM and need not be held whole.
 template <int kMode, bool kOne, bool kNarrow>
-__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
+__global__ void __launch_bounds__(kThreads, 1)
     product_kernel(const __grid_constant__ Maps maps, const Params p) {
   extern __shared__ uint8_t smem_raw[];
   using Sm = Smem<kMode>;
@@ -298,8 +334,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   constexpr int kCols = kNarrow ? kHalf : kTile;   // columns of the accumulator
   constexpr int kBRows = kCols / 2;                // rows of B a CTA holds
   const int warp = threadIdx.x >> 5;
-  const uint32_t rank = ptx::cluster_rank();
-  const int pair = blockIdx.x >> 1, n_pairs = gridDim.x >> 1;
+  const uint32_t place = ptx::cluster_rank(), size = ptx::cluster_size();
+  const uint32_t rank = place & 1, lead = place & ~1u;         // of the pair, its first CTA
+  const int team = static_cast<int>(place >> 1), teams = static_cast<int>(size >> 1);
+  const int pair = static_cast<int>(blockIdx.x / size), n_pairs = static_cast<int>(gridDim.x / size);
   volatile int* abort_flag = &S.abort_flag;
   const Shape sh = shape_of<kMode, kNarrow>(p);
 
@@ -321,7 +359,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     ptx::fence_mbar_init();
   }
   __syncwarp();
-  ptx::cluster_sync();   // both CTAs' barriers exist
+  ptx::cluster_sync();   // the cluster's barriers exist
   if (!p.late) ptx::dependents_launch();
   if (!p.early) ptx::dependency_wait();   // what the kernel before wrote is there
   if (p.late) ptx::dependents_launch();
@@ -348,7 +386,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         uint32_t it = 0;
         bool ok = true;
         for (int u = pair; ok && u < sh.units; u += n_pairs) {
-          const Unit w = unit_of(p, sh, u);
+          const Unit w = unit_of<kNarrow>(p, sh, u, team, teams);
           const int m0 = w.m * kTile + static_cast<int>(rank) * kHalf;
           const int n0 = w.n * kTileN<kMode, kNarrow> + (kMode == kGate ? 0 : static_cast<int>(rank) * kBRows);
           for (int k = 0; k < w.nk; ++k, ++it) {
@@ -358,7 +396,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
               break;
             }
             if (rank == 0) ptx::mbar_arrive_expect_tx(&S.full[st], 2 * (kBoxBytes + kBRows * 128));
-            const uint32_t bar = ptx::cluster_addr(&S.full[st], 0);
+            const uint32_t bar = ptx::cluster_addr(&S.full[st], lead);
             const int kk = (w.k0 + k) * 64;
             if constexpr (kAmn) {
               ptx::tma_load_2d_pair(S.a[st], &maps.a, bar, m0, kk);
@@ -386,7 +424,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         uint32_t it = 0, tile = 0;
         bool ok = true;
         for (int u = pair; ok && u < sh.units; u += n_pairs) {
-          const Unit w = unit_of(p, sh, u);
+          const Unit w = unit_of<kNarrow>(p, sh, u, team, teams);
           const int per = kOne ? w.nk : kChunk;
           for (int k0 = 0; ok && k0 < w.nk; k0 += per, ++tile) {
             const uint32_t buf = tile & 1;
@@ -409,13 +447,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
               for (int q = 0; q < 4; ++q)
                 ptx::mma_ss_pair(tmem + buf * kCols, ptx::desc_add(ad, q * kStepA), ptx::desc_add(bd, q * kStepB),
                                  idesc, (k > 0 || q > 0) ? 1u : 0u);
-              ptx::mma_commit_pair(&S.empty[st]);
+              ptx::mma_commit_pair(&S.empty[st], lead);
             }
-            if (ok) ptx::mma_commit_pair(&S.tm_full[buf]);
+            if (ok) ptx::mma_commit_pair(&S.tm_full[buf], lead);
           }
         }
         // every product issued above has completed before TMEM is released
-        ptx::mma_commit_pair(&S.drain);
+        ptx::mma_commit_pair(&S.drain, lead);
         ptx::mbar_drain(&S.drain, 0);
       }
     }
@@ -424,7 +462,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         // ---------------------------------------------------------- carrier
         const int mine = pair < sh.units ? (sh.units - 1 - pair) / n_pairs + 1 : 0;   // tiles of this pair
         auto place = [&](int q, int& col, int& row) {   // of the q-th 64 columns
-          const Unit w = unit_of(p, sh, pair + (q >> 2) * n_pairs);
+          const Unit w = unit_of<kNarrow>(p, sh, pair + (q >> 2) * n_pairs, team, teams);
           col = w.n * kTile + (q & 3) * 64;
           row = w.m * kTile + static_cast<int>(rank) * kHalf;
         };
@@ -459,6 +497,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         ptx::bulk_wait_read<0>();
       }
     }
+    if (kNarrow && teams > 1) {
+      __syncwarp();
+      ptx::cluster_sync();   // the other pairs' sums are there
+    }
   } else {
     // ------------------------------------------------------------ epilogue
     if constexpr (!kOne) ptx::regs_inc<kRegsEpi>();
@@ -467,15 +509,17 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     const int rc = (warp & 3) * 32 + lane;   // row of this CTA's half tile
     const bool leader = (threadIdx.x & 127) == 0;
     const uint32_t lane_off = static_cast<uint32_t>((warp & 3) * 32) << 16;
-    const uint32_t bar_empty[2] = {ptx::cluster_addr(&S.tm_empty[0], 0), ptx::cluster_addr(&S.tm_empty[1], 0)};
+    const uint32_t bar_empty[2] = {ptx::cluster_addr(&S.tm_empty[0], lead), ptx::cluster_addr(&S.tm_empty[1], lead)};
     uint8_t* const box[2] = {S.out[wg][0], S.out[wg][Sm::kBoxes - 1]};
     auto meet = [&] { asm volatile("bar.sync %0, 128;" ::"r"(wg + 1) : "memory"); };
+    bool met = false;     // teams: the barrier behind the other pairs' sums has been passed
     uint32_t taken = 0;   // tiles that took something in; of the last, both boxes' loads may be under way
     uint32_t tile = 0, sent = 0;
     bool ok = true;
     for (int u = pair; ok && u < sh.units; u += n_pairs) {
-      const Unit w = unit_of(p, sh, u);
-      const bool takes = kMode == kDz || kMode == kGateBwd || (kMode == kLin && p.has_in && w.split < 0);
+      const Unit w = unit_of<kNarrow>(p, sh, u, team, teams);
+      const bool takes =
+          (kMode == kDz || kMode == kGateBwd || (kMode == kLin && p.has_in && w.split < 0)) && teams == 1;
       const int row0 = w.m * kTile + static_cast<int>(rank) * kHalf;   // first row of this CTA
       // first column of this warpgroup; kGateBwd: of its 32 in every 64
       const int n0 = w.n * kTileN<kMode, kNarrow> + wg * (kMode == kGateBwd ? 32 : kTileN<kMode, kNarrow> / 2);
@@ -506,7 +550,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       // the tile's bias, read by all rows from shared memory (a load per 32 columns on
       // its way from DRAM to every thread cost a lone tile 2.5 us)
       if constexpr (kMode == kLin || kMode == kDz) {
-        if (p.bias) {
+        if (p.bias && teams == 1) {
           const int i = threadIdx.x & 127;
           if (!kNarrow || i < 64) S.bias[wg][i] = n0 + i < p.N ? __ldg(p.bias + n0 + i) : 0.f;
         }
@@ -556,6 +600,100 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         if (lane == 0) ptx::mbar_arrive_cluster(bar_empty[buf]);
       };
 
+      if constexpr (kNarrow) {
+        if (teams > 1) {
+          // this row's sums, 16 bytes at a time, to where the stages were
+#pragma unroll 1
+          for (int c = 0; c < 2; ++c) {
+            uint32_t y[32];
+            ptx::tmem_ld32(tm + c * 32, y);
+            ptx::tmem_wait_ld_of(y);
+#pragma unroll
+            for (int q = 0; q < 8; ++q)
+              *reinterpret_cast<uint4*>(S.a[0] + team_place(rc, wg * 16 + c * 8 + q)) =
+                  make_uint4(y[4 * q], y[4 * q + 1], y[4 * q + 2], y[4 * q + 3]);
+          }
+          __syncwarp();
+          ptx::cluster_sync();
+          met = true;
+          // this pair's part of the rows, four at a time per warp, four columns per lane
+          const int rows = kHalf / teams, c0 = w.n * kHalf + lane * 4;
+          const bool in_n = c0 < p.N;
+          uint64_t b0 = 0, b1 = 0;
+          if ((kMode == kLin || kMode == kDz) && p.bias && in_n) {
+            const ulonglong2 v = __ldg(reinterpret_cast<const ulonglong2*>(p.bias + c0));
+            b0 = v.x;
+            b1 = v.y;
+          }
+          float4 sums = make_float4(0.f, 0.f, 0.f, 0.f);   // kDz: of the rows of a group of 32
+#pragma unroll 1
+          for (int i0 = (warp - 4) * 4; i0 < rows; i0 += 32) {
+            uint64_t x[4][2] = {};
+#pragma unroll 2
+            for (int k = 0; k < teams; ++k) {
+              const uint32_t from = ptx::cluster_addr(S.a[0], static_cast<uint32_t>(2 * k) + rank);
+              ulonglong2 y[4];
+#pragma unroll
+              for (int j = 0; j < 4; ++j) y[j] = ptx::lds128u_cluster(from + team_place(team * rows + i0 + j, lane));
+#pragma unroll
+              for (int j = 0; j < 4; ++j) {
+                x[j][0] = ptx::add2(x[j][0], y[j].x);
+                x[j][1] = ptx::add2(x[j][1], y[j].y);
+              }
+            }
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+              const int row = row0 + team * rows + i0 + j;
+              const bool inside = row < p.M && in_n;
+              if constexpr (kMode == kLin || kMode == kDz) {
+                uint2 q = make_uint2(0, 0);
+                if (p.in && inside) q = *reinterpret_cast<const uint2*>(p.in + row * p.ld_in + c0);
+                const uint64_t y[2] = {ptx::f2(lo16(q.x), hi16(q.x)), ptx::f2(lo16(q.y), hi16(q.y))};
+                x[j][0] = ptx::add2(x[j][0], b0);
+                x[j][1] = ptx::add2(x[j][1], b1);
+                with_act(p.act, [&](auto t) {
+#pragma unroll
+                  for (int e = 0; e < 2; ++e) {
+                    if constexpr (kMode == kLin) {
+                      x[j][e] = ptx::add2(act_2<decltype(t)::value>(x[j][e]), y[e]);
+                    } else {
+                      uint64_t slope;
+                      act_slope_2<decltype(t)::value>(x[j][e], slope);
+                      x[j][e] = ptx::mul2(y[e], slope);
+                    }
+                  }
+                });
+              }
+              float v[4];
+              ptx::unf2(x[j][0], v[0], v[1]);
+              ptx::unf2(x[j][1], v[2], v[3]);
+              if (inside) {
+                *reinterpret_cast<uint2*>(p.out + row * p.ld_out + c0) =
+                    make_uint2(ptx::pack_bf16x2(v[0], v[1]), ptx::pack_bf16x2(v[2], v[3]));
+                sums.x += v[0]; sums.y += v[1]; sums.z += v[2]; sums.w += v[3];
+              }
+            }
+            if (kMode == kDz && p.colsum) {   // the eight warps have done 32 rows
+              float4* part = reinterpret_cast<float4*>(S.out[0][0]);   // [8][32]
+              part[(warp - 4) * 32 + lane] = sums;
+              sums = make_float4(0.f, 0.f, 0.f, 0.f);
+              asm volatile("bar.sync 4, %0;" ::"n"(kEpiThreads) : "memory");
+              const int group = (row0 + team * rows + i0) / 32;
+              if (warp == 4 && in_n && group * 32 < p.M) {
+                float4 s = part[lane];
+#pragma unroll
+                for (int k = 1; k < 8; ++k) {
+                  const float4 y = part[k * 32 + lane];
+                  s.x += y.x; s.y += y.y; s.z += y.z; s.w += y.w;
+                }
+                *reinterpret_cast<float4*>(p.colsum + static_cast<int64_t>(group) * p.N + c0) = s;
+              }
+              asm volatile("bar.sync 4, %0;" ::"n"(kEpiThreads) : "memory");
+            }
+          }
+          break;   // the one tile there is
+        }
+      }
       if constexpr (kPlain || kMode == kDz) {
         // 32 columns at a time, read from TMEM while those before go out.  (One copy of
         // the code: a kernel of one tile per CTA pays for every instruction's way here.)
@@ -767,6 +905,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       }
       if (takes) ok = ptx::all_of_128(wg + 1, ok);   // a load that gave up
     }
+    if (kNarrow && teams > 1 && !met) {   // gave up before
+      __syncwarp();
+      ptx::cluster_sync();
+    }
     if (kMode != kGateBwd && leader) {
       // loads that nobody waited for (after a timeout) have arrived before the CTA leaves
       for (int s = 0; s < (kNarrow ? 1 : 2); ++s)
@@ -774,11 +916,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       ptx::bulk_wait_read<0>();   // (what is still on its way out is out when the kernel is done)
     }
   }
-  // Both CTAs leave together: nothing of the pair signals or reads a CTA that
-  // has gone.  After a timeout in either the stages' copies are waited for first.
+  // The cluster's CTAs leave together: nothing signals or reads a CTA that has
+  // gone.  After a timeout in any the stages' copies are waited for first.
   __syncwarp();
   __syncthreads();
-  if (threadIdx.x == 0 && S.abort_flag) ptx::st_cluster(&S.abort_flag, rank ^ 1, 1);
+  if (threadIdx.x == 0 && S.abort_flag)
+    for (uint32_t i = 0; i < size; ++i) ptx::st_cluster(&S.abort_flag, i, 1);
   ptx::cluster_sync();
   if (S.abort_flag) {
     if (threadIdx.x == 0) {
@@ -817,20 +960,31 @@ inline size_t acc_bytes(int64_t M, int64_t N, int64_t K) {
 inline int64_t exp_rows(int64_t N) { return (N + 127) / 128 * 128; }
 inline size_t exp_bytes(int64_t N, int64_t I) { return static_cast<size_t>((I + kGroup - 1) / kGroup * 2 * exp_rows(N)); }
 
-// Kernel launch; after: the stream's last kernel is this library's, of the same
-// call, and this one may start under its end (it waits for it itself).
+// Kernel launch in clusters; after: the stream's last kernel is this library's, of
+// the same call, and this one may start under its end (it waits for it itself).
 template <typename... Args, typename... Given>
-int launch_kernel(void (*kern)(Args...), dim3 grid, int threads, size_t smem, bool after, cudaStream_t s, Given... given) {
+int launch_kernel(void (*kern)(Args...), dim3 grid, int threads, size_t smem, int cluster, bool after, cudaStream_t s,
+                  Given... given) {
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = grid;
   cfg.blockDim = dim3(static_cast<unsigned>(threads));
   cfg.dynamicSmemBytes = smem;
   cfg.stream = s;
-  cudaLaunchAttribute at[1];
-  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  at[0].val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchAttribute at[2];
+  unsigned n = 0;
+  if (cluster > 1) {
+    at[n].id = cudaLaunchAttributeClusterDimension;
+    at[n].val.clusterDim.x = static_cast<unsigned>(cluster);
+    at[n].val.clusterDim.y = at[n].val.clusterDim.z = 1;
+    ++n;
+  }
+  if (after) {
+    at[n].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[n].val.programmaticStreamSerializationAllowed = 1;
+    ++n;
+  }
   cfg.attrs = at;
-  cfg.numAttrs = after ? 1 : 0;
+  cfg.numAttrs = n;
   return cuda_status(cudaLaunchKernelEx(&cfg, kern, static_cast<Args>(given)...));
 }
 
@@ -849,10 +1003,12 @@ int launch(const Maps& maps, const Params& p, bool after, cudaStream_t s) {
   }); });
   if (st != TPK_OK) return st;
   const int units = shape_of<kMode, kNarrow>(p).units;
-  int pairs = num_sms() / 2;
-  pairs = pairs < 1 ? 1 : pairs;
-  pairs = pairs < units ? pairs : units;
-  return launch_kernel(kern, dim3(static_cast<unsigned>(2 * pairs)), kThreads, kSmemBytes<kMode>, after, s, maps, p);
+  int clusters = num_sms() / 2;
+  clusters = clusters < 1 ? 1 : clusters;
+  clusters = clusters < units || p.teams > 1 ? (p.teams > 1 ? units : clusters) : units;
+  const int size = 2 * p.teams;
+  return launch_kernel(kern, dim3(static_cast<unsigned>(size * clusters)), kThreads, kSmemBytes<kMode>, size, after, s,
+                       maps, p);
 }
 
 // Products of linear.cu that the feed-forward block uses too.  acc: acc_bytes;
