@@ -245,7 +245,7 @@ int few_launch(const Mat& x, const Mat& w, const Mat& w2, FewParams& p, bool aft
   if (st == TPK_OK && kGated) st = map_of(&m.w2, w2, shape.rows);
   if (st != TPK_OK) return st;
   FewConfig c(shape.tiles, shape.ranks, kFewBytes<kTok>, after, s);
-  return cuda_status(cudaLaunchKernelEx(&c.cfg, kern, m, p));
+  return launched(cudaLaunchKernelEx(&c.cfg, kern, m, p));
 }
 
 template <bool kGated>

@@ -103,7 +103,7 @@ extern "C" int tpk_gated_ffn(const void* x, int64_t ld_x, const void* w_in, cons
   if (!widths_ok(C, I, O)) return TPK_E_UNSUPPORTED;
   if (!tiles_ok(N, C, I, O)) return TPK_E_OVERFLOW;
   if (N == 0) return TPK_OK;
-  if (!x || !w_in || !w_out || !y || !aligned16(x) || !aligned16(w_in) || !aligned16(w_out) || !aligned16(y) ||
+  if (!x || !w_in || !w_out || !y || y == x || !aligned16(x) || !aligned16(w_in) || !aligned16(w_out) || !aligned16(y) ||
       !aligned16(residual) || !aligned16(saved) || !aligned16(a))
     return TPK_E_ARG;
   FfnWork k;
@@ -154,7 +154,7 @@ extern "C" int tpk_gated_ffn_bwd(const void* x, int64_t ld_x, const void* w_in, 
     if (st == TPK_OK) st = cuda_status(cudaMemsetAsync(dw_out, 0, static_cast<size_t>(2) * O * I, s));
     return st;
   }
-  if (!x || !w_in || !w_out || !dy || !saved || !a || !dx || !aligned16(x) || !aligned16(w_in) || !aligned16(w_out) ||
+  if (!x || !w_in || !w_out || !dy || !saved || !a || !dx || dx == x || dx == dy || !aligned16(x) || !aligned16(w_in) || !aligned16(w_out) ||
       !aligned16(dy) || !aligned16(saved) || !aligned16(a) || !aligned16(dx))
     return TPK_E_ARG;
   FfnWork k;

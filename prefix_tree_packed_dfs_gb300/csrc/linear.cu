@@ -293,7 +293,7 @@ extern "C" int tpk_linear(const void* x, int64_t ld_x, const void* w, const floa
   if (C > kMostK) return TPK_E_UNSUPPORTED;
   if (!tiles_ok(N, C, O)) return TPK_E_OVERFLOW;
   if (N == 0) return TPK_OK;
-  if (!x || !w || !y || !aligned16(x) || !aligned16(w) || !aligned16(y) || !aligned16(residual) || !aligned16(bias))
+  if (!x || !w || !y || y == x || y == w || !aligned16(x) || !aligned16(w) || !aligned16(y) || !aligned16(residual) || !aligned16(bias))
     return TPK_E_ARG;
   LinearWork k;
   const size_t need = carve(static_cast<uint8_t*>(workspace), N, C, O, act, false, &k);
@@ -321,7 +321,7 @@ extern "C" int tpk_linear_bwd(const void* x, int64_t ld_x, const void* w, const 
     if (st == TPK_OK && db) st = cuda_status(cudaMemsetAsync(db, 0, static_cast<size_t>(O) * 4, s));
     return st;
   }
-  if (!x || !w || !dy || !dx || !aligned16(x) || !aligned16(w) || !aligned16(dy) || !aligned16(dx) || !aligned16(bias))
+  if (!x || !w || !dy || !dx || dx == x || dx == dy || dx == w || !aligned16(x) || !aligned16(w) || !aligned16(dy) || !aligned16(dx) || !aligned16(bias))
     return TPK_E_ARG;
   LinearWork k;
   if (!workspace || reinterpret_cast<uintptr_t>(workspace) % 256 ||

@@ -480,5 +480,5 @@ extern "C" int tpk_policy_loss(const float* loss, const float* old_logp, const f
   at[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = at;
   cfg.numAttrs = 1;
-  return cuda_status(cudaLaunchKernelEx(&cfg, policy_position_kernel, p));
+  return launched(cudaLaunchKernelEx(&cfg, policy_position_kernel, p));
 }

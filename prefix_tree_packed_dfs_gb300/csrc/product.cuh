@@ -985,7 +985,7 @@ int launch_kernel(void (*kern)(Args...), dim3 grid, int threads, size_t smem, in
   }
   cfg.attrs = at;
   cfg.numAttrs = n;
-  return cuda_status(cudaLaunchKernelEx(&cfg, kern, static_cast<Args>(given)...));
+  return launched(cudaLaunchKernelEx(&cfg, kern, static_cast<Args>(given)...));
 }
 
 template <int kMode, bool kOne, bool kNarrow = false>

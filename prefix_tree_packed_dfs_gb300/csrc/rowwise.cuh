@@ -15,6 +15,12 @@ constexpr int kMaxSms = 256;
 
 inline bool aligned16(const void* p) { return reinterpret_cast<uintptr_t>(p) % 16 == 0; }
 
+// Status of a launch; its error does not stay behind for the caller's own checks.
+inline int launched(cudaError_t e) {
+  if (e != cudaSuccess) cudaGetLastError();
+  return cuda_status(e);
+}
+
 // body() -> status, for the C entry points: nothing thrown on the host (out of
 // memory, a mutex) leaves the library.
 template <typename Body>

@@ -63,7 +63,7 @@ def _err():
 # rows: one, few (all three token widths, both ends), below and above a tile, ragged; odd widths
 LINEAR = [(1, 64, 64), (1, 2048, 4096), (3, 8, 8), (16, 1000, 552), (17, 136, 1032), (32, 4096, 264), (33, 72, 2048),
           (64, 520, 776), (65, 64, 128), (128, 256, 256), (200, 2048, 512), (257, 1000, 520), (1001, 552, 1000),
-          (700, 4096, 136), (3000, 64, 2056)]
+          (700, 4096, 136), (3000, 64, 2056), (1000, 4096, 1000)]
 
 
 def _linear_ref(x, w, bias, act, residual):

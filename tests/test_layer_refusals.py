@@ -29,7 +29,7 @@ def test_linear_refuses_on_the_host(lib):
     for kw in (dict(x=None), dict(w=None), dict(y=None), dict(x=P(8)), dict(w=P(24)), dict(y=P(1032)), dict(b=P(4)),
                dict(r=P(8), ld_r=128), dict(r=P(16), ld_r=120), dict(ld_x=56), dict(ld_x=68), dict(ld_y=120),
                dict(ld_y=132), dict(n=-1), dict(c=0), dict(c=60), dict(o=4), dict(o=130), dict(act=-1), dict(act=4),
-               dict(o=(1 << 20) + 8, ld_y=1 << 21), dict(n=(1 << 31) - 8192)):
+               dict(o=(1 << 20) + 8, ld_y=1 << 21), dict(n=(1 << 31) - 8192), dict(y=P(256)), dict(y=P(512))):
         assert call(**kw) == ARG, kw
     assert call(c=32776, ld_x=32776) == UNSUPPORTED
     assert call(n=(1 << 31) - 8200, o=1 << 20, ld_y=1 << 20) == OVERFLOW
@@ -52,7 +52,7 @@ def test_linear_bwd_refuses_on_the_host(lib):
         return lib.tpk_linear_bwd(a["x"], a["ld_x"], a["w"], a["b"], a["act"], a["dy"], a["ld_dy"], a["dx"], a["ld_dx"],
                                   a["dw"], a["db"], a["n"], a["c"], a["o"], a["ws"], a["ws_bytes"], None, None)
     for kw in (dict(x=None), dict(w=None), dict(dy=None), dict(dx=None), dict(dw=None), dict(db=P(4)), dict(ld_dy=120),
-               dict(ld_dx=60), dict(ld_dx=56), dict(dw=P(8)), dict(dx=P(8)), dict(c=12, ld_x=16, ld_dx=16)):
+               dict(ld_dx=60), dict(ld_dx=56), dict(dw=P(8)), dict(dx=P(8)), dict(dx=P(256)), dict(dx=P(768)), dict(c=12, ld_x=16, ld_dx=16)):
         assert call(**kw) == ARG, kw
     assert call(ws=None) == WORKSPACE and call(ws=P(4100)) == WORKSPACE
     assert call(ws_bytes=lib.tpk_linear_workspace_bytes(70, 64, 128, 1, 1) - 1) == WORKSPACE
@@ -67,7 +67,7 @@ def test_gated_ffn_refuses_on_the_host(lib):
         return lib.tpk_gated_ffn(q["x"], q["ld_x"], q["wi"], q["wo"], q["act"], q["r"], q["ld_r"], q["saved"], q["a"],
                                  q["y"], q["ld_y"], q["n"], q["c"], q["i"], q["o"], q["ws"], q["ws_bytes"], None, None)
     for kw in (dict(x=None), dict(wi=None), dict(wo=None), dict(y=None), dict(saved=P(8)), dict(a=P(8)), dict(i=100),
-               dict(i=0), dict(o=12, ld_y=16), dict(act=7), dict(ld_x=60), dict(r=P(16), ld_r=8)):
+               dict(i=0), dict(o=12, ld_y=16), dict(act=7), dict(ld_x=60), dict(r=P(16), ld_r=8), dict(y=P(256))):
         assert call(**kw) == ARG, kw
     for kw in (dict(c=32776, ld_x=32776), dict(i=32776), dict(o=32776, ld_y=32776)):
         assert call(**kw) == UNSUPPORTED, kw
@@ -79,7 +79,7 @@ def test_gated_ffn_refuses_on_the_host(lib):
         **{})[k] if k not in kw else kw[k] for k in ("x", "ld_x", "wi", "wo", "act", "dy", "ld_dy", "saved", "a", "dx",
                                                      "ld_dx", "dwi", "dwo", "n", "c", "i", "o", "ws", "ws_bytes")],
         None, None)
-    for kw in (dict(saved=None), dict(a=None), dict(dwi=None), dict(dwo=P(8)), dict(dx=None), dict(ld_dy=56)):
+    for kw in (dict(saved=None), dict(a=None), dict(dwi=None), dict(dwo=P(8)), dict(dx=None), dict(ld_dy=56), dict(dx=P(256)), dict(dx=P(1024))):
         assert bwd(**kw) == ARG, kw
     assert bwd(ws=None) == WORKSPACE and bwd(ws_bytes=64) == WORKSPACE
     assert lib.tpk_gated_ffn_saved_bytes(70, 100) == 0 and lib.tpk_gated_ffn_saved_bytes(70, 128) > 70 * 128 * 4
