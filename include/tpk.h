@@ -688,7 +688,8 @@ int tpk_lm_loss_bwd(const void* h, const void* w, const int32_t* target, const f
  *   y[n, o] = act( sum_c x[n, c] w[o, c] + bias[o] ) + residual[n, o]
  *   x [N, C], w [O, C], residual, y [N, O] bf16;  bias [O] fp32
  * bias and residual may be NULL; y may be residual itself (same stride), else
- * outputs overlap no input (y = x is refused, dx = x and dx = dy too).  C <= 32,768, O <= 2^20.  N = 0 does nothing.
+ * outputs overlap no input (y = x is refused, dx = x and dx = dy too).
+ * C <= 32,768, O <= 2^20.  N = 0 does nothing.
  * workspace: tpk_linear_workspace_bytes(N, C, O, act, 0) bytes, may be 0. */
 size_t tpk_linear_workspace_bytes(int64_t N, int32_t C, int32_t O, int32_t act, int32_t backward);
 int tpk_linear(const void* x, int64_t ld_x, const void* w, const float* bias, int32_t act, const void* residual,
