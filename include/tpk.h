@@ -679,6 +679,7 @@ int tpk_lm_loss_bwd(const void* h, const void* w, const int32_t* target, const f
  * TPK_E_UNSUPPORTED for a width of a sum above 32,768, TPK_E_OVERFLOW for more
  * than 2^27 tiles of 256 x 256, TPK_E_WORKSPACE; dev_err (device int32, may be
  * NULL) becomes TPK_E_TIMEOUT if a device wait gave up. */
+#define TPK_FEW_ROWS 64      /* up to so many rows of x tpk_linear reads the weights once and needs no workspace */
 #define TPK_ACT_NONE      0
 #define TPK_ACT_SILU      1  /* z / (1 + exp(-z)) */
 #define TPK_ACT_GELU      2  /* z Phi(z), Phi within 1.5e-7 */

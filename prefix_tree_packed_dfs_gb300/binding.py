@@ -22,6 +22,7 @@ PLACE_NEXT_FIT = 1
 PLACE_GROUPS = 2
 BF16, F32 = 0, 1
 ACT_NONE, ACT_SILU, ACT_GELU, ACT_GELU_TANH = 0, 1, 2, 3
+FEW_ROWS = 64
 FIELD_DEPTH, FIELD_TOKEN_INDEX, FIELD_SUBTREE_END, FIELD_PARENT = 0, 1, 2, 3
 FIELD_FWD_RAW_BEGIN, FIELD_FWD_RAW = 4, 5
 FIELD_SEG_START, FIELD_SEG_LEN, FIELD_SEG_PARENT, FIELD_SEG_OFF = 6, 7, 8, 9

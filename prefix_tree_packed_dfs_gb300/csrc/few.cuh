@@ -6,7 +6,7 @@
 namespace tpk {
 namespace product {
 
-constexpr int kFewRows = 64;   // rows; see few.cu
+constexpr int kFewRows = TPK_FEW_ROWS;   // see few.cu
 
 // y = act(x w^T + bias) + residual.  after: x (and residual) come from the
 // stream's last kernel, which lets this one start early.

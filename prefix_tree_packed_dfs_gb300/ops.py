@@ -904,14 +904,43 @@ def _out_rows(t, shape, name, ref):
     return (t,) + _rows2(t, name, shape)
 
 
+def _rows_of(t, name):
+    """(rows, channels, address, row stride) of a 2-d bf16 tensor whose rows may
+    lie apart, of a multiple of 8 channels."""
+    if not isinstance(t, torch.Tensor) or t.dtype is not torch.bfloat16 or t.dim() != 2:
+        raise TypeError("%s must be a 2-d bf16 tensor" % name)
+    n, c = t.shape
+    if c < 8 or c % 8:
+        raise ValueError("%s must have a multiple of 8 channels, got %d" % (name, c))
+    ld, unit = t.stride()
+    if unit != 1:
+        raise ValueError("%s: channels must be contiguous inside a row" % name)
+    if n <= 1:
+        ld = c
+    elif ld < c or ld % 8:
+        raise ValueError("%s: rows must not overlap and must lie a multiple of 8 elements apart" % name)
+    return n, c, t.data_ptr(), ld
+
+
+def _weights(t, cols, name):
+    """(rows, address) of a contiguous bf16 matrix of `cols` columns and a multiple of 8 rows."""
+    if not isinstance(t, torch.Tensor) or t.dtype is not torch.bfloat16 or t.dim() != 2:
+        raise TypeError("%s must be a 2-d bf16 tensor" % name)
+    rows, c = t.shape
+    if c != cols:
+        raise ValueError("%s must have shape (rows, %d), got %s" % (name, cols, tuple(t.shape)))
+    if rows < 8 or rows % 8:
+        raise ValueError("%s must have a multiple of 8 rows, got %d" % (name, rows))
+    if not t.is_contiguous():
+        raise ValueError("%s must be contiguous" % name)
+    return rows, t.data_ptr()
+
+
 def _linear_args(x, w, bias):
     """(N, C, O, addresses and stride of x, w, bias), checked."""
-    N, C = _matrix(x, (torch.bfloat16,), "x")
-    O = _matrix(w, (torch.bfloat16,), "w")[0]
-    if O < 8 or O % 8:
-        raise ValueError("w must have a multiple of 8 rows, got %d" % O)
-    p_w = _arg(w, torch.bfloat16, (O, C), "w")
-    return (N, C, O) + _rows2(x, "x", (N, C)) + (p_w, None if bias is None else _arg(bias, torch.float32, (O,), "bias"))
+    N, C, p_x, ld_x = _rows_of(x, "x")
+    O, p_w = _weights(w, C, "w")
+    return N, C, O, p_x, ld_x, p_w, None if bias is None else _arg(bias, torch.float32, (O,), "bias")
 
 
 def linear(x, w, bias=None, act="none", residual=None, out=None, workspace=None, dev_err=None):
@@ -928,7 +957,8 @@ def linear(x, w, bias=None, act="none", residual=None, out=None, workspace=None,
     given = out, workspace, dev_err
     out, p_y, ld_y = _out_rows(out, (N, O), "out", x)
     p_err = _dev_err(dev_err)
-    need = lib.tpk_linear_workspace_bytes(N, C, O, a, 0)
+    # (a few rows, one or so, are a matter of microseconds: no question about a workspace they do not need)
+    need = 0 if N <= B.FEW_ROWS else lib.tpk_linear_workspace_bytes(N, C, O, a, 0)
     ws = _workspace(workspace, need, x, "the projection") if need or workspace is not None else None
     dev = _device("x w bias residual out workspace dev_err", x, w, bias, residual, *given)
     _launch(dev, lib.tpk_linear, p_x, ld_x, p_w, p_b, a, p_r, ld_r, p_y, ld_y, N, C, O,
@@ -962,12 +992,12 @@ def linear_bwd(x, w, dy, bias=None, act="none", dx=None, dw=None, db=None, works
 
 def _ffn_args(x, w_in, w_out):
     """(N, C, I, O, address and stride of x, addresses of the weights), checked."""
-    N, C = _matrix(x, (torch.bfloat16,), "x")
-    O, I = _matrix(w_out, (torch.bfloat16,), "w_out")
-    if O < 8 or O % 8:
-        raise ValueError("w_out must have a multiple of 8 rows, got %d" % O)
-    return (N, C, I, O) + _rows2(x, "x", (N, C)) + (_arg(w_in, torch.bfloat16, (2 * I, C), "w_in"),
-                                                     _arg(w_out, torch.bfloat16, (O, I), "w_out"))
+    N, C, p_x, ld_x = _rows_of(x, "x")
+    I2, p_in = _weights(w_in, C, "w_in")
+    if I2 % 16:
+        raise ValueError("w_in must have twice a multiple of 8 rows, got %d" % I2)
+    O, p_out = _weights(w_out, I2 // 2, "w_out")
+    return N, C, I2 // 2, O, p_x, ld_x, p_in, p_out
 
 
 def gated_ffn(x, w_in, w_out, act="silu", residual=None, save=False, out=None, pre=None, a=None, workspace=None,

@@ -40,7 +40,7 @@ def test_linear_refuses_on_the_host(lib):
         assert call(n=100, c=8192, ld_x=8192, o=256, ld_y=256, ws_bytes=need - 1) == WORKSPACE
     assert lib.tpk_linear_workspace_bytes(0, 64, 64, 0, 1) == 0
     assert lib.tpk_linear_workspace_bytes(10, 60, 64, 0, 1) == 0
-    assert lib.tpk_linear_workspace_bytes(64, 4096, 4096, 0, 0) == 0       # a few rows need none
+    assert lib.tpk_linear_workspace_bytes(B.FEW_ROWS, 8192, 256, 0, 0) == 0       # a few rows need none
 
 
 def test_linear_bwd_refuses_on_the_host(lib):
@@ -124,6 +124,7 @@ def test_wrappers_name_what_is_wrong(lib):
             (TypeError, "x", lambda: ops.linear(x.float(), w)),
             (TypeError, "w", lambda: ops.linear(x, w.half())),
             (ValueError, "w must have shape", lambda: ops.linear(x, _bf(16, 72))),
+            (ValueError, "w must be contiguous", lambda: ops.linear(x, _bf(64, 16).T)),
             (ValueError, "multiple of 8 channels", lambda: ops.linear(_bf(3, 60), _bf(16, 60))),
             (ValueError, "multiple of 8 rows", lambda: ops.linear(x, _bf(12, 64))),
             (ValueError, "act", lambda: ops.linear(x, w, act="relu")),
@@ -136,7 +137,9 @@ def test_wrappers_name_what_is_wrong(lib):
             (ValueError, "db is given", lambda: ops.linear_bwd(x, w, _bf(3, 16), db=torch.zeros(16))),
             (ValueError, "dy", lambda: ops.linear_bwd(x, w, _bf(3, 24))),
             (ValueError, "no CPU path", lambda: ops.linear_bwd(x, w, _bf(3, 16))),
-            (ValueError, "w_in must have shape", lambda: ops.gated_ffn(x, _bf(16, 64), _bf(64, 16))),
+            (ValueError, "w_out must have shape", lambda: ops.gated_ffn(x, _bf(16, 64), _bf(64, 16))),
+            (ValueError, "w_in must have shape", lambda: ops.gated_ffn(x, _bf(16, 72), _bf(64, 8))),
+            (ValueError, "twice a multiple", lambda: ops.gated_ffn(x, _bf(24, 64), _bf(64, 12))),
             (ValueError, "save=True", lambda: ops.gated_ffn(x, _bf(32, 64), _bf(64, 16), a=_bf(3, 16))),
             (ValueError, "no CPU path", lambda: ops.gated_ffn(x, _bf(32, 64), _bf(64, 16))),
             (TypeError, "pre", lambda: ops.gated_ffn_bwd(x, _bf(32, 64), _bf(64, 16), x, _bf(3, 32), _bf(3, 16))),
