@@ -180,10 +180,14 @@ extern "C" int tpk_gated_ffn_bwd(const void* x, int64_t ld_x, const void* w_in, 
   if (st == TPK_OK) st = launch<kGateBwd, true>(m, p, false, s);
   const Mat dgu{k.dgu, N, wide, ld};
   const Mat mdx{dx, N, C, ld_dx}, mdin{dw_in, wide, C, C}, mdout{dw_out, O, I, I};
+  const Mat win{w_in, wide, C, C}, ma{a, N, I, I};
+  const Grad grads[3] = {{dgu, false, win, mdx}, {dgu, true, mx, mdin}, {mdy, true, ma, mdout}};
+  Params all{};
+  if (grads_plan(grads, 3, &all)) return st == TPK_OK ? grads_product(grads, 3, all, true, dev_err, s) : st;
   Params px, pin, pout;
-  if (st == TPK_OK) st = input_product(dgu, Mat{w_in, wide, C, C}, mdx, k.acc, true, dev_err, s, &px);
+  if (st == TPK_OK) st = input_product(dgu, win, mdx, k.acc, true, dev_err, s, &px);
   if (st == TPK_OK) st = weight_product(dgu, mx, mdin, k.acc_in, px, dev_err, s, &pin);
-  if (st == TPK_OK) st = weight_product(mdy, Mat{a, N, I, I}, mdout, k.acc_out, pin, dev_err, s, &pout);
+  if (st == TPK_OK) st = weight_product(mdy, ma, mdout, k.acc_out, pin, dev_err, s, &pout);
   if (st == TPK_OK) st = join_left(px, mdx, s);
   if (st == TPK_OK) st = join_left(pin, mdin, s);
   if (st == TPK_OK) st = join_left(pout, mdout, s);

@@ -270,6 +270,30 @@ int weight_product(const Mat& dz, const Mat& x, const Mat& dw, float* acc, const
   return launch_plan<kDw>(m, p, true, s);
 }
 
+int grads_product(const Grad* g, int n, Params& p, bool after, int32_t* err, cudaStream_t s) {
+  Maps m;
+  CUtensorMap* const a[3] = {&m.a, &m.in, &m.more};
+  CUtensorMap* const b[3] = {&m.b, &m.b2, &m.in2};
+  CUtensorMap* const out[3] = {&m.out, &m.out2, &m.out3};
+  int st = TPK_OK;
+  bool taken[3] = {};
+  for (int i = 0; i < n; ++i) {   // the product that p.sub[i] describes
+    int j = 0;
+    while (taken[j] || g[j].out.rows != p.sub[i].M || g[j].out.cols != p.sub[i].N || g[j].amn != (p.sub[i].amn != 0)) ++j;
+    taken[j] = true;
+    if (st == TPK_OK) st = map_of(a[i], g[j].a, g[j].amn ? 64 : kHalf);
+    if (st == TPK_OK) st = map_of(b[i], g[j].b, 64);
+    if (st == TPK_OK) st = map_of(out[i], g[j].out, kHalf);
+  }
+  if (st != TPK_OK) return st;
+  p.teams = 1;
+  p.narrow = 1;
+  p.splits = 1;
+  p.late = 1;
+  p.err = err;
+  return launch<kGrads, true, true>(m, p, after, s);
+}
+
 int join_left(const Params& left, const Mat& out, cudaStream_t s) {
   return left.splits > 1 ? join(left, nullptr, TPK_ACT_NONE, Mat{}, out, s) : TPK_OK;
 }
@@ -353,9 +377,15 @@ extern "C" int tpk_linear_bwd(const void* x, int64_t ld_x, const void* w, const 
     if (st == TPK_OK) st = launch_plan<kDz>(m, p, false, s);
   }
   const Mat mdx{dx, N, C, ld_dx}, mdw{dw, O, C, C};
-  Params px, pw;
-  if (st == TPK_OK) st = input_product(dz, mw, mdx, k.acc, act != TPK_ACT_NONE, dev_err, s, &px);
-  if (st == TPK_OK) st = weight_product(dz, mx, mdw, k.acc_w, px, dev_err, s, &pw);
+  Params px{}, pw{}, both{};
+  px.splits = pw.splits = 1;
+  const Grad grads[2] = {{dz, false, mw, mdx}, {dz, true, mx, mdw}};
+  if (grads_plan(grads, 2, &both)) {
+    if (st == TPK_OK) st = grads_product(grads, 2, both, act != TPK_ACT_NONE, dev_err, s);
+  } else {
+    if (st == TPK_OK) st = input_product(dz, mw, mdx, k.acc, act != TPK_ACT_NONE, dev_err, s, &px);
+    if (st == TPK_OK) st = weight_product(dz, mx, mdw, k.acc_w, px, dev_err, s, &pw);
+  }
   if (st == TPK_OK && db)
     st = act != TPK_ACT_NONE
              ? column_sums(k.sums, (N + 31) / 32, O, O, k.part, db, s)

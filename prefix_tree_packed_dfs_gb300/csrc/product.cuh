@@ -7,6 +7,7 @@
 //   kDw       dz^T x             stored
 //   kGate     x (w_gate | w_up)^T   a = act(g) u (and g, u kept)
 //   kGateBwd  dy w_out              dg = da u act'(g), du = da act(g)
+//   kGrads    the kDx and kDw products of a small backward in one launch
 // The tiles that are left over from whole rounds of kLin, kDx and kDw may be
 // split over K (split_of): fp32 partial tiles, summed in a fixed order by
 // linear.cu's join_kernel, which then does the epilogue.
@@ -51,6 +52,10 @@
 // order through distributed shared memory (a warp reads whole rows: 16 bytes of 32
 // rows each took 4 us longer).  (1,003 rows, widths 5,456 to 1,000:
 // 17 us against 28 in narrow tiles alone; 256 rows, 8,192 to 256: 12 against 16.)
+// A small backward's products that do not wait for one another (dx, dw; the block's
+// dx, dw_in, dw_out) are one launch of narrow tiles, the longest sums first (kGrads,
+// grads_plan); a pair that has one of those takes fewer of the others.  (1,003 rows
+// back through 1,000 -> 2,728 -> 1,000: 34 us against 51 in three.)
 // Kernels of one call overlap (programmatic dependent launch): each sets itself
 // up under the one before and then waits for it.  A product that needs nothing of
 // the one before, where that one leaves SMs free (early), takes them at once and
@@ -92,12 +97,24 @@ constexpr uint32_t kRegsCtl = 56;
 constexpr uint32_t kRegsEpi = 216;
 constexpr int kRegsNeeded = 128 * kRegsCtl + 256 * kRegsEpi;
 
-enum Mode { kLin = 0, kDz = 1, kDx = 2, kDw = 3, kGate = 4, kGateBwd = 5 };
+enum Mode { kLin = 0, kDz = 1, kDx = 2, kDw = 3, kGate = 4, kGateBwd = 5, kGrads = 6 };
 
 struct Maps {
   CUtensorMap a, b, b2;      // b2: kGate's up rows
   CUtensorMap in, in2;       // kLin residual, kDz dy; kGateBwd g, u
   CUtensorMap out, out2, out3;   // kGate: a, g, u; kGateBwd: dg, du
+  CUtensorMap more;
+  // kGrads: of the s-th product
+  __host__ __device__ const CUtensorMap& grad_a(int s) const { return s == 0 ? a : s == 1 ? in : more; }
+  __host__ __device__ const CUtensorMap& grad_b(int s) const { return s == 0 ? b : s == 1 ? b2 : in2; }
+  __host__ __device__ const CUtensorMap& grad_out(int s) const { return s == 0 ? out : s == 1 ? out2 : out3; }
+};
+
+// One of kGrads' products.
+struct Sub {
+  int32_t M, N, k_iters;
+  int32_t amn;               // A stored with M contiguous (dw)
+  int32_t mt, nt;
 };
 
 struct Params {
@@ -118,12 +135,13 @@ struct Params {
   float* acc;                // splits > 1: [splits][tiles - whole][256 * 256]
   uint8_t* exps;             // kGate, kGateBwd: [2][groups][exp_rows] biased exponents of g's and u's largest
   int64_t exp_rows;
+  Sub sub[3];                // kGrads, by falling k_iters
   int32_t* err;
 };
 
 template <int kMode>
 struct Smem {
-  static constexpr bool kSix = kMode == kDx || kMode == kDw || kMode == kGate;
+  static constexpr bool kSix = kMode == kDx || kMode == kDw || kMode == kGate || kMode == kGrads;
   static constexpr int kStages = kSix ? 6 : 5;
   static constexpr int kBoxes = kSix ? 1 : 2;
   uint8_t a[kStages][kBoxBytes];
@@ -181,20 +199,22 @@ struct Plan {
   bool narrow;
   int teams;
   Split split;
+  double us;     // estimate, without the kernel's start and end
 };
 inline Plan plan_of(int64_t M, int64_t N, int64_t K) {
   const int64_t mt = (M + kTile - 1) / kTile, wide = mt * ((N + kTile - 1) / kTile);
   const int64_t narrow = mt * ((N + kHalf - 1) / kHalf), k_iters = (K + 63) / 64;
   double us;
-  Plan p{false, 1, split_of(wide, k_iters, &us)};
+  Plan p{false, 1, split_of(wide, k_iters, &us), 0.0};
   us += 2.2;
+  p.us = us + 0.27 * static_cast<double>((p.split.tail ? p.split.whole : wide - wide % kPairs) / kPairs * k_iters);
   if (wide > kPairs) return p;
   const int64_t rounds = (narrow + kPairs - 1) / kPairs;
   const double stage_us = narrow <= kPairs / 2 ? 0.14 : 0.2;
   const double alone = stage_us * static_cast<double>(rounds * k_iters) + 1.1;
   if (alone < us && k_iters <= kChunk) {
     us = alone;
-    p = Plan{true, 1, Split{narrow, 0, 1}};
+    p = Plan{true, 1, Split{narrow, 0, 1}, us};
   }
   for (int teams = 2; teams <= kTeams; teams *= 2) {
     const int64_t each = (k_iters + teams - 1) / teams;
@@ -202,7 +222,7 @@ inline Plan plan_of(int64_t M, int64_t N, int64_t K) {
     const double together = stage_us * static_cast<double>(each) + 1.1 + 2.2;
     if (together < us) {
       us = together;
-      p = Plan{true, teams, Split{narrow, 0, 1}};
+      p = Plan{true, teams, Split{narrow, 0, 1}, us};
     }
   }
   return p;
@@ -216,6 +236,7 @@ struct Unit {
   int m, n, k0, nk;
   int split;                 // -1: the whole of K
   int tile;
+  int sub;                   // kGrads
 };
 // Columns of a tile.
 template <int kMode, bool kNarrow = false>
@@ -240,7 +261,7 @@ __device__ __forceinline__ void place_of(int mt, int nt, int t, int& m, int& n) 
 }
 template <bool kNarrow>
 __device__ __forceinline__ Unit unit_of(const Params& p, const Shape& s, int u, int team, int teams) {
-  Unit w{0, 0, 0, s.k_iters, -1, 0};
+  Unit w{0, 0, 0, s.k_iters, -1, 0, 0};
   if (kNarrow) {   // never split over units, but over the pairs of a cluster
     w.k0 = s.k_iters * team / teams;
     w.nk = s.k_iters * (team + 1) / teams - w.k0;
@@ -254,6 +275,41 @@ __device__ __forceinline__ Unit unit_of(const Params& p, const Shape& s, int u, 
   w.tile = u;
   place_of(s.mt, s.nt, u, w.m, w.n);
   return w;
+}
+
+// kGrads: the i-th tile of pair `pair` of `pairs`, if it has so many.  The first
+// product's tiles go round; while some pairs do one more of those, the others do
+// `e` of the shorter ones; the rest goes round.
+__device__ __forceinline__ bool grad_unit(const Params& p, int pair, int pairs, int i, Unit& w) {
+  const int n0 = p.sub[0].mt * p.sub[0].nt, n1 = p.sub[1].mt * p.sub[1].nt, n2 = p.sub[2].mt * p.sub[2].nt;
+  const int extra = n0 % pairs, mine = n0 / pairs + (pair < extra ? 1 : 0);
+  if (i < mine) {
+    w.sub = 0;
+    w.tile = pair + pairs * i;
+  } else {
+    i -= mine;
+    const int rest = n1 + n2, idle = pairs - extra;
+    const int e = extra > 0 ? p.sub[0].k_iters / p.sub[1].k_iters : 0;
+    const int ahead = min(rest, idle * e);
+    int v = -1;
+    if (pair >= extra) {
+      const int at = pair - extra, has = at < ahead ? (ahead - at - 1) / idle + 1 : 0;
+      if (i < has) v = at + idle * i;
+      i -= has;
+    }
+    if (v < 0) {
+      v = ahead + pair + pairs * i;
+      if (v >= rest) return false;
+    }
+    w.sub = v < n1 ? 1 : 2;
+    w.tile = v < n1 ? v : v - n1;
+  }
+  const Sub& s = p.sub[w.sub];
+  w.k0 = 0;
+  w.nk = s.k_iters;
+  w.split = -1;
+  place_of(s.mt, s.nt, w.tile, w.m, w.n);
+  return true;
 }
 
 __device__ __forceinline__ uint64_t pair_at(const uint32_t (&x)[32], int e) {
@@ -327,10 +383,10 @@ __global__ void __launch_bounds__(kThreads, 1)
   constexpr int kStages = Sm::kStages;
   Sm& S = *reinterpret_cast<Sm*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   constexpr bool kAmn = kMode == kDw;                                          // A stored with M contiguous
-  constexpr bool kBmn = kMode == kDx || kMode == kDw || kMode == kGateBwd;     // B stored with N contiguous
-  constexpr bool kPlain = kMode == kLin || kMode == kDx || kMode == kDw;
+  constexpr bool kBmn = kMode == kDx || kMode == kDw || kMode == kGateBwd || kMode == kGrads;   // B with N contiguous
+  constexpr bool kPlain = kMode == kLin || kMode == kDx || kMode == kDw || kMode == kGrads;
   static_assert(kOne || kMode == kDx || kMode == kDw, "sums over channels do not stop");
-  static_assert(!kNarrow || (kOne && kMode < kGate), "narrow tiles are whole sums");
+  static_assert(!kNarrow || (kOne && (kMode < kGate || kMode == kGrads)), "narrow tiles are whole sums");
   constexpr int kCols = kNarrow ? kHalf : kTile;   // columns of the accumulator
   constexpr int kBRows = kCols / 2;                // rows of B a CTA holds
   const int warp = threadIdx.x >> 5;
@@ -340,6 +396,16 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int pair = static_cast<int>(blockIdx.x / size), n_pairs = static_cast<int>(gridDim.x / size);
   volatile int* abort_flag = &S.abort_flag;
   const Shape sh = shape_of<kMode, kNarrow>(p);
+  auto next = [&](int i, Unit& w) {   // the pair's i-th unit
+    if constexpr (kMode == kGrads) {
+      return grad_unit(p, pair, n_pairs, i, w);
+    } else {
+      const int u = pair + i * n_pairs;
+      if (u >= sh.units) return false;
+      w = unit_of<kNarrow>(p, sh, u, team, teams);
+      return true;
+    }
+  };
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < kStages; ++s) {
@@ -385,8 +451,11 @@ __global__ void __launch_bounds__(kThreads, 1)
         const CUtensorMap* mb = kMode == kGate && rank == 1 ? &maps.b2 : &maps.b;
         uint32_t it = 0;
         bool ok = true;
-        for (int u = pair; ok && u < sh.units; u += n_pairs) {
-          const Unit w = unit_of<kNarrow>(p, sh, u, team, teams);
+        Unit w;
+        for (int i = 0; ok && next(i, w); ++i) {
+          const CUtensorMap* ma = kMode == kGrads ? &maps.grad_a(w.sub) : &maps.a;
+          if (kMode == kGrads) mb = &maps.grad_b(w.sub);
+          const bool amn = kMode == kGrads ? p.sub[w.sub].amn != 0 : kAmn;
           const int m0 = w.m * kTile + static_cast<int>(rank) * kHalf;
           const int n0 = w.n * kTileN<kMode, kNarrow> + (kMode == kGate ? 0 : static_cast<int>(rank) * kBRows);
           for (int k = 0; k < w.nk; ++k, ++it) {
@@ -398,11 +467,11 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (rank == 0) ptx::mbar_arrive_expect_tx(&S.full[st], 2 * (kBoxBytes + kBRows * 128));
             const uint32_t bar = ptx::cluster_addr(&S.full[st], lead);
             const int kk = (w.k0 + k) * 64;
-            if constexpr (kAmn) {
-              ptx::tma_load_2d_pair(S.a[st], &maps.a, bar, m0, kk);
-              ptx::tma_load_2d_pair(S.a[st] + kBoxBytes / 2, &maps.a, bar, m0 + 64, kk);
+            if (amn) {
+              ptx::tma_load_2d_pair(S.a[st], ma, bar, m0, kk);
+              ptx::tma_load_2d_pair(S.a[st] + kBoxBytes / 2, ma, bar, m0 + 64, kk);
             } else {
-              ptx::tma_load_2d_pair(S.a[st], &maps.a, bar, kk, m0);
+              ptx::tma_load_2d_pair(S.a[st], ma, bar, kk, m0);
             }
             if constexpr (kBmn) {
               ptx::tma_load_2d_pair(S.b[st], mb, bar, n0, kk);
@@ -417,14 +486,17 @@ __global__ void __launch_bounds__(kThreads, 1)
     } else if (warp == 1 && rank == 0) {
       // ---------------------------------------------------------- MMA issuer
       if (ptx::elect_one()) {
-        constexpr uint32_t idesc = ptx::idesc_bf16_f32(kTile, kCols, kAmn, kBmn);
         // K step of 16 elements: 32 bytes along a K-major row, 16 rows of 128
         // bytes of an MN-major box (its two 64-column boxes half a stage apart)
-        constexpr uint32_t kStepA = kAmn ? 2048 : 32, kStepB = kBmn ? 2048 : 32;
+        constexpr uint32_t kStepB = kBmn ? 2048 : 32;
         uint32_t it = 0, tile = 0;
         bool ok = true;
-        for (int u = pair; ok && u < sh.units; u += n_pairs) {
-          const Unit w = unit_of<kNarrow>(p, sh, u, team, teams);
+        Unit w;
+        for (int i = 0; ok && next(i, w); ++i) {
+          const bool amn = kMode == kGrads ? p.sub[w.sub].amn != 0 : kAmn;
+          const uint32_t step_a = amn ? 2048 : 32, lbo_a = amn ? kBoxBytes / 2 : 16;
+          const uint32_t idesc =
+              amn ? ptx::idesc_bf16_f32(kTile, kCols, true, kBmn) : ptx::idesc_bf16_f32(kTile, kCols, false, kBmn);
           const int per = kOne ? w.nk : kChunk;
           for (int k0 = 0; ok && k0 < w.nk; k0 += per, ++tile) {
             const uint32_t buf = tile & 1;
@@ -441,11 +513,11 @@ __global__ void __launch_bounds__(kThreads, 1)
                 break;
               }
               ptx::tc_fence_after();
-              const uint64_t ad = ptx::sw128_desc(ptx::smem_addr(S.a[st]), kAmn ? kBoxBytes / 2 : 16, 1024);
+              const uint64_t ad = ptx::sw128_desc(ptx::smem_addr(S.a[st]), lbo_a, 1024);
               const uint64_t bd = ptx::sw128_desc(ptx::smem_addr(S.b[st]), kBmn ? kBoxBytes / 2 : 16, 1024);
 #pragma unroll
               for (int q = 0; q < 4; ++q)
-                ptx::mma_ss_pair(tmem + buf * kCols, ptx::desc_add(ad, q * kStepA), ptx::desc_add(bd, q * kStepB),
+                ptx::mma_ss_pair(tmem + buf * kCols, ptx::desc_add(ad, q * step_a), ptx::desc_add(bd, q * kStepB),
                                  idesc, (k > 0 || q > 0) ? 1u : 0u);
               ptx::mma_commit_pair(&S.empty[st], lead);
             }
@@ -516,8 +588,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     uint32_t taken = 0;   // tiles that took something in; of the last, both boxes' loads may be under way
     uint32_t tile = 0, sent = 0;
     bool ok = true;
-    for (int u = pair; ok && u < sh.units; u += n_pairs) {
-      const Unit w = unit_of<kNarrow>(p, sh, u, team, teams);
+    Unit w;
+    for (int i = 0; ok && next(i, w); ++i) {
+      const int M = kMode == kGrads ? p.sub[w.sub].M : p.M, N = kMode == kGrads ? p.sub[w.sub].N : p.N;
+      const CUtensorMap* to = kMode == kGrads ? &maps.grad_out(w.sub) : &maps.out;
       const bool takes =
           (kMode == kDz || kMode == kGateBwd || (kMode == kLin && p.has_in && w.split < 0)) && teams == 1;
       const int row0 = w.m * kTile + static_cast<int>(rank) * kHalf;   // first row of this CTA
@@ -785,7 +859,7 @@ __global__ void __launch_bounds__(kThreads, 1)
               ptx::fence_async_shared();
               meet();
               if (leader) {
-                if (c0 - 32 < p.N && row0 < p.M) ptx::tma_store_2d(&maps.out, box[b], c0 - 32, row0);
+                if (c0 - 32 < N && row0 < M) ptx::tma_store_2d(to, box[b], c0 - 32, row0);
                 ptx::bulk_commit();
               }
             }
@@ -988,6 +1062,47 @@ int launch_kernel(void (*kern)(Args...), dim3 grid, int threads, size_t smem, in
   return launched(cudaLaunchKernelEx(&cfg, kern, static_cast<Args>(given)...));
 }
 
+// One of a backward's products: out[M, N] = A B over K.
+struct Grad {
+  Mat a;          // dz: [M, K], or [K, M] for a weight's gradient (amn)
+  bool amn;
+  Mat b;          // [K, N]
+  Mat out;
+};
+// Plans up to three of them as one launch; false if one after the other is quicker
+// (each pays about 4 us for its start and end), or a sum is too long for one piece.
+inline bool grads_plan(const Grad* g, int n, Params* p) {
+  int64_t units = 0, work = 0, longest = 0, last = 0;
+  double apart = 0.0;
+  int order[3] = {0, 1, 2};
+  auto k_of = [&](int i) { return ((g[i].amn ? g[i].a.rows : g[i].a.cols) + 63) / 64; };
+  for (int i = 1; i < n; ++i)
+    for (int j = i; j > 0 && k_of(order[j]) > k_of(order[j - 1]); --j) {
+      const int x = order[j];
+      order[j] = order[j - 1];
+      order[j - 1] = x;
+    }
+  for (int i = 0; i < 3; ++i) p->sub[i] = Sub{0, 0, 1, 0, 0, 0};
+  for (int i = 0; i < n; ++i) {
+    const Grad& x = g[order[i]];
+    const int64_t k = k_of(order[i]), mt = (x.out.rows + kTile - 1) / kTile, nt = (x.out.cols + kHalf - 1) / kHalf;
+    if (k > kChunk || mt * nt > 16 * kPairs) return false;
+    p->sub[i] = Sub{static_cast<int32_t>(x.out.rows), static_cast<int32_t>(x.out.cols), static_cast<int32_t>(k),
+                    x.amn, static_cast<int32_t>(mt), static_cast<int32_t>(nt)};
+    units += mt * nt;
+    work += mt * nt * k;
+    longest = k > longest ? k : longest;
+    last = k;
+    apart += plan_of(x.out.rows, x.out.cols, k * 64).us + 4.0;
+  }
+  // the busiest pair: its share and one tile more, or one of the longest sums
+  const int64_t share = (work + kPairs - 1) / kPairs + last;
+  const int64_t stages = units <= kPairs ? longest : longest + last > share ? longest + last : share;
+  return (units <= kPairs / 2 ? 0.14 : 0.2) * static_cast<double>(stages) + 1.1 + 4.0 < apart;
+}
+// They, as planned (order of p.sub).
+int grads_product(const Grad* g, int n, Params& p, bool after, int32_t* err, cudaStream_t s);
+
 template <int kMode, bool kOne, bool kNarrow = false>
 int launch(const Maps& maps, const Params& p, bool after, cudaStream_t s) {
   constexpr auto kern = product_kernel<kMode, kOne, kNarrow>;
@@ -1002,7 +1117,11 @@ int launch(const Maps& maps, const Params& p, bool after, cudaStream_t s) {
         cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(kSmemBytes<kMode>)));
   }); });
   if (st != TPK_OK) return st;
-  const int units = shape_of<kMode, kNarrow>(p).units;
+  int units = shape_of<kMode, kNarrow>(p).units;
+  if (kMode == kGrads) {
+    units = 0;
+    for (const Sub& x : p.sub) units += x.mt * x.nt;
+  }
   int clusters = num_sms() / 2;
   clusters = clusters < 1 ? 1 : clusters;
   clusters = clusters < units || p.teams > 1 ? (p.teams > 1 ? units : clusters) : units;
