@@ -673,7 +673,7 @@ int tpk_lm_loss_bwd(const void* h, const void* w, const int32_t* target, const f
  * strides ld_*, in elements: multiples of 8, not below the width; column slices
  * of a fused projection), weights are contiguous.  Widths are multiples of 8,
  * pointers 16-byte aligned.  Sums run in a fixed order: results do not depend on
- * timing.  Workspaces need not be cleared, are 256-byte aligned, and belong to
+ * timing (the order, and with it the last bits, goes by the sizes).  Workspaces need not be cleared, are 256-byte aligned, and belong to
  * one call (or captured graph) at a time.
  * Errors: TPK_E_ARG for a bad pointer, size, stride or activation,
  * TPK_E_UNSUPPORTED for a width of a sum above 32,768, TPK_E_OVERFLOW for more

@@ -38,7 +38,7 @@
 // running sum per step of 16 elements of K.  The sums over rows (kDw) and over
 // the wide side (kDx) stop every 8,192 elements and are added up in registers
 // with rounding to nearest: at most 5e-5 is left, a fortieth of the results'
-// bf16 rounding; sums over at most kMostK channels need no stop.
+// bf16 rounding; sums over at most kMostK channels (2e-4 at most) need no stop.
 // g and u are kept for the backward in 16 bits: as fp16 scaled by a power of two
 // for every 32 channels of a row, so that the largest lies in [2^14, 2^15).  That
 // is eight times as precise as bf16 for the same bytes, at any scale (a value
@@ -174,7 +174,7 @@ inline Split split_of(int64_t tiles, int64_t k_iters, double* us_out = nullptr) 
   const int64_t tail = tiles % kPairs;
   const double tile_us = 0.27 * static_cast<double>(k_iters);   // 64 elements of K: 512 cycles
   double best = tile_us;
-  if (us_out) *us_out = best;
+  if (us_out) *us_out = tail == 0 ? 0.0 : best;
   if (tail == 0) return s;
   for (int64_t n = 2; n <= k_iters / 4 && n <= (tail * 8 < kPairs ? kPairs / tail : 8); ++n) {
     const int64_t rounds = (tail * n + kPairs - 1) / kPairs;
@@ -192,7 +192,8 @@ inline Split split_of(int64_t tiles, int64_t k_iters, double* us_out = nullptr) 
 // How a product is done: in wide tiles, some of them split, or in narrow ones.
 // Those need 256 cycles for 64 elements of K where few pairs run, about 384 where
 // the operands' way into the SMs is full, and half of the 2.2 us that a lone wide
-// tile's epilogue takes.  (1,000 rows, widths 1,000 and 552, gelu: 10.7 us in narrow
+// tile's epilogue takes; where few columns are left of the last wide tile they are
+// quicker in any number.  (1,000 rows, widths 1,000 and 552, gelu: 10.7 us in narrow
 // tiles, 14.5 in wide ones; 200 rows, widths 1,024 and 256: 7.2 against 10.5.)  A team
 // of pairs divides the stages and pays about 2.2 us to meet.
 struct Plan {
@@ -206,24 +207,16 @@ inline Plan plan_of(int64_t M, int64_t N, int64_t K) {
   const int64_t narrow = mt * ((N + kHalf - 1) / kHalf), k_iters = (K + 63) / 64;
   double us;
   Plan p{false, 1, split_of(wide, k_iters, &us), 0.0};
-  us += 2.2;
-  p.us = us + 0.27 * static_cast<double>((p.split.tail ? p.split.whole : wide - wide % kPairs) / kPairs * k_iters);
-  if (wide > kPairs) return p;
+  p.us = us + 2.2 + 0.27 * static_cast<double>((p.split.tail ? p.split.whole : wide - wide % kPairs) / kPairs * k_iters);
   const int64_t rounds = (narrow + kPairs - 1) / kPairs;
   const double stage_us = narrow <= kPairs / 2 ? 0.14 : 0.2;
   const double alone = stage_us * static_cast<double>(rounds * k_iters) + 1.1;
-  if (alone < us && k_iters <= kChunk) {
-    us = alone;
-    p = Plan{true, 1, Split{narrow, 0, 1}, us};
-  }
+  if (alone < p.us && k_iters <= kChunk) p = Plan{true, 1, Split{narrow, 0, 1}, alone};
   for (int teams = 2; teams <= kTeams; teams *= 2) {
     const int64_t each = (k_iters + teams - 1) / teams;
     if (narrow > (teams == 2 ? kClusters4 : kClusters8) || k_iters < 2 * teams || each > kChunk) continue;
     const double together = stage_us * static_cast<double>(each) + 1.1 + 2.2;
-    if (together < us) {
-      us = together;
-      p = Plan{true, teams, Split{narrow, 0, 1}, us};
-    }
+    if (together < p.us) p = Plan{true, teams, Split{narrow, 0, 1}, together};
   }
   return p;
 }
