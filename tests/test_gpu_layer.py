@@ -63,7 +63,8 @@ def _err():
 # rows: one, few (all three token widths, both ends), below and above a tile, ragged; odd widths
 LINEAR = [(1, 64, 64), (1, 2048, 4096), (3, 8, 8), (16, 1000, 552), (17, 136, 1032), (32, 4096, 264), (33, 72, 2048),
           (64, 520, 776), (65, 64, 128), (128, 256, 256), (200, 2048, 512), (257, 1000, 520), (1001, 552, 1000),
-          (700, 4096, 136), (3000, 64, 2056), (1000, 4096, 1000)]
+          (700, 4096, 136), (3000, 64, 2056), (1000, 4096, 1000), (130, 8, 8),
+          (66, 24, 4104), (2600, 328, 1032)]
 
 
 def _linear_ref(x, w, bias, act, residual):
@@ -135,7 +136,7 @@ def test_linear_bwd(ops, n, c, o, act, bias):
 
 FFN = [(1, 64, 64, 64), (1, 2048, 1024, 2048), (5, 8, 8, 8), (16, 136, 200, 136), (32, 1000, 328, 1000),
        (40, 256, 1032, 512), (64, 520, 136, 520), (65, 64, 128, 64), (129, 128, 264, 72), (257, 1000, 520, 1000),
-       (1003, 264, 1096, 264), (300, 2048, 256, 2048)]
+       (1003, 264, 1096, 264), (300, 2048, 256, 2048), (130, 8, 8, 8), (70, 24, 2056, 8)]
 
 
 def _ffn_parts(X, WI, WO, act):
