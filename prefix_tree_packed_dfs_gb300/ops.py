@@ -1071,14 +1071,39 @@ def rope_freqs(rot, base=1e4, stretch=1.0, trained=None, fast=32.0, slow=1.0):
     return f * (keep + (1.0 - keep) / stretch)
 
 
-def _heads(t, name, shape=None):
-    """(address, row stride) of a 3-d bf16 tensor whose rows may lie apart."""
-    _rows3(t, name, shape)
-    n, h, d = t.shape if shape is None else shape
-    ld = t.stride(0) if n > 1 else h * d
-    if ld < h * d or ld % 8:
+def _heads(t, name):
+    """(positions, heads, channels, address, row stride) of a 3-d bf16 tensor whose rows may lie apart."""
+    if not isinstance(t, torch.Tensor) or t.dtype is not torch.bfloat16 or t.dim() != 3:
+        raise TypeError("%s must be a 3-d bf16 tensor" % name)
+    n, h, d = t.shape
+    ld, head, unit = t.stride()
+    if unit != 1 or head != d:
+        raise ValueError("%s: heads and elements must be contiguous inside a row" % name)
+    if n <= 1:
+        ld = h * d
+    elif ld < h * d or ld % 8:
         raise ValueError("%s: rows must not overlap and must lie a multiple of 8 elements apart" % name)
-    return t.data_ptr(), ld
+    return n, h, d, t.data_ptr(), ld
+
+
+def _rotated(t, out, name, F, d):
+    """(heads, address, row stride, output, its address, its row stride) of q or k and what it turns into."""
+    if t is None:
+        if out is not None:
+            raise ValueError("%s_out is given, but not %s" % (name, name))
+        return 0, None, 0, None, None, 0
+    n, h, c, p_in, ld_in = _heads(t, name)
+    if n != F or c != d:
+        raise ValueError("%s must have shape %s, got %s" % (name, (F, h, d), (n, h, c)))
+    if out is None:
+        out = torch.empty((n, h, c), dtype=torch.bfloat16, device=t.device)
+        return h, p_in, ld_in, out, out.data_ptr(), h * c
+    n, ho, c, p_out, ld_out = _heads(out, name + "_out")
+    if n != F or ho != h or c != d:
+        raise ValueError("%s_out must have shape %s, got %s" % (name, (F, h, d), (n, ho, c)))
+    if p_out == p_in and ld_out != ld_in:
+        raise ValueError("%s_out starts where %s does, with other rows" % (name, name))
+    return h, p_in, ld_in, out, p_out, ld_out
 
 
 def rope_by_depth_ex(q, k, depth, freqs, interleaved=False, factor=1.0, inverse=False, q_out=None, k_out=None):
@@ -1100,37 +1125,19 @@ def rope_by_depth_ex(q, k, depth, freqs, interleaved=False, factor=1.0, inverse=
         raise TypeError("q and k must be 3-d bf16 tensors")
     F, _, d = ref.shape
     fr = np.ascontiguousarray(freqs, dtype=np.float64)
-    if fr.ndim != 1 or not 8 <= len(fr) <= min(d // 2, 128) or len(fr) % 8:
+    pairs = len(fr) if fr.ndim == 1 else 0
+    if pairs % 8 or not 8 <= pairs <= 128 or 2 * pairs > d:
         raise ValueError("freqs must hold a multiple of 8 pairs, no more than half the head (or 128)")
     if d % 8 or d > 512:
         raise ValueError("heads must have a multiple of 8 channels, 512 at most, got %d" % d)
     p_depth = _arg(depth, torch.int32, (F,), "depth")
-    given, at, heads = (q_out, k_out), [], []
-    outs = []
-    for t, o, name in ((q, q_out, "q"), (k, k_out, "k")):
-        if t is None:
-            if o is not None:
-                raise ValueError("%s_out is given, but not %s" % (name, name))
-            at.append((None, 0, None, 0))
-            heads.append(0)
-            outs.append(None)
-            continue
-        p_in, ld_in = _heads(t, name, (F, t.shape[1], d) if isinstance(t, torch.Tensor) and t.dim() == 3 else None)
-        if o is None:
-            o = torch.empty(t.shape, dtype=torch.bfloat16, device=t.device)
-            p_o, ld_o = o.data_ptr(), t.shape[1] * d
-        else:
-            p_o, ld_o = _heads(o, name + "_out", tuple(t.shape))
-        if p_o == p_in and ld_o != ld_in:
-            raise ValueError("%s_out starts where %s does, with other rows" % (name, name))
-        at.append((p_in, ld_in, p_o, ld_o))
-        heads.append(t.shape[1])
-        outs.append(o)
-    dev = _device("depth q k q_out k_out", depth, q, k, *given)
-    opts = B.RopeOpts(2 * len(fr), 1 if interleaved else 0, float(factor), fr.__array_interface__["data"][0])
-    _launch(dev, lib.tpk_rope_by_depth_ex, at[0][0], at[0][1], at[1][0], at[1][1], at[0][2], at[0][3], at[1][2], at[1][3],
-            p_depth, F, heads[0], heads[1], d, ctypes.byref(opts), 1 if inverse else 0)
-    return outs[0], outs[1]
+    hq, p_q, ld_q, q_new, p_qo, ld_qo = _rotated(q, q_out, "q", F, d)
+    hk, p_k, ld_k, k_new, p_ko, ld_ko = _rotated(k, k_out, "k", F, d)
+    dev = _device("depth q k q_out k_out", depth, q, k, q_out, k_out)
+    opts = B.RopeOpts(2 * pairs, 1 if interleaved else 0, float(factor), fr.__array_interface__["data"][0])
+    _launch(dev, lib.tpk_rope_by_depth_ex, p_q, ld_q, p_k, ld_k, p_qo, ld_qo, p_ko, ld_ko, p_depth, F, hq, hk, d,
+            ctypes.byref(opts), 1 if inverse else 0)
+    return q_new, k_new
 
 
 def policy_loss(loss, old_logp, advantage, weight, token_index, fwd_raw_begin, fwd_raw, ref_logp=None, clip_low=0.2,
