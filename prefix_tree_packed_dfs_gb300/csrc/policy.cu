@@ -27,19 +27,21 @@ constexpr int kPolThreads = 256;
 constexpr int kPolBlocks = 1216;   // of the token pass, at most
 constexpr int kStats = 5;          // objective, KL, clipped, ratio, weight
 
-// The unevaluated sum of two fp32 numbers, the second below half a step of the first.
+// The unevaluated sum of two fp32 numbers, the second below half a step of the first
+// (0 beside an infinity, whose error would come out as NaN).
 struct Pair {
   float hi, lo;
 };
 __device__ __forceinline__ Pair two_sum(float a, float b) {
-  const float s = a + b, t = s - a;
-  return Pair{s, (a - (s - t)) + (b - t)};
+  const float s = a + b, t = s - a, e = (a - (s - t)) + (b - t);
+  return Pair{s, e == e ? e : 0.f};
 }
 __device__ __forceinline__ Pair add(Pair a, Pair b) {
   const Pair s = two_sum(a.hi, b.hi);
   return two_sum(s.hi, s.lo + (a.lo + b.lo));
 }
-// a - b, of which the sign is right next to 0 too
+// a - b, of which the sign is right next to 0 too; NaN, which is on neither side,
+// for equal infinities
 __device__ __forceinline__ float less(Pair a, Pair b) { return (a.hi - b.hi) + (a.lo - b.lo); }
 
 struct Policy {
@@ -89,8 +91,9 @@ __device__ __forceinline__ Term term_of(const Clip& c, float adv) {
   return t;
 }
 
-// exp(t) - t - 1
+// exp(t) - t - 1; infinite at both infinities
 __device__ __forceinline__ float k3(float t) {
+  if (isinf(t)) return INFINITY;
   if (fabsf(t) >= 0.3f) return expm1f(t) - t;
   // t^2 (1/2! + t/3! + .. + t^5/7!): the next term is 4e-8 of it
   float s = fmaf(t, 1.f / 5040.f, 1.f / 720.f);
@@ -249,7 +252,7 @@ __global__ void __launch_bounds__(kSeqThreads, 4) policy_sequence_kernel(const P
   if (threadIdx.x == 0) {
     const double d = many ? (static_cast<double>(sum.hi) + static_cast<double>(sum.lo)) / many : 0.0;
     const float top = static_cast<float>(d);
-    clip = clip_of(p, Pair{top, static_cast<float>(d - static_cast<double>(top))});
+    clip = clip_of(p, Pair{top, isinf(top) ? 0.f : static_cast<float>(d - static_cast<double>(top))});
   }
   __syncthreads();
   const Clip c = clip;

@@ -1,0 +1,143 @@
+"""The policy objective where its numbers end: infinite log-probabilities, ratios
+past fp32's range, long sums.
+
+The reference is the objective's formula in fp64, with s by the advantage's sign
+(A > 0: A min(ratio, 1 + clip_high); A < 0: A max(ratio, 1 - clip_low), at most
+the dual clip; A = 0: 0), so that infinities go through it.  Finite results:
+2^-19 of the terms' magnitudes, as in test_gpu_layer.py.
+"""
+import numpy as np
+import pytest
+import torch
+
+pytestmark = pytest.mark.gpu
+
+INF, LARGEST = np.inf, float(np.finfo(np.float32).max)
+
+
+@pytest.fixture(scope="module")
+def ops():
+    assert torch.cuda.is_available()
+    from prefix_tree_packed_dfs_gb300 import ops as o
+    return o
+
+
+def _formula(loss, old, adv, weight, index, offsets, ref, lo, hi, dual, kl_coef):
+    """(stats, dloss, magnitudes of the terms of both)."""
+    stats, smag, grad, mag = np.zeros(5), np.zeros(5), np.zeros(len(loss)), np.zeros(len(loss))
+    bounds = [(r, r + 1) for r in range(len(old))] if offsets is None else list(zip(offsets[:-1], offsets[1:]))
+    with np.errstate(all="ignore"):
+        for b, e in bounds:
+            on = [r for r in range(b, e) if weight[r] != 0]
+            if not on:
+                continue
+            ratio = np.exp(np.mean([-loss[index[r]] - old[r] for r in on]))
+            pull, pull_mag = 0.0, 0.0
+            for r in on:
+                A, w = adv[r], weight[r]
+                if A > 0:
+                    used, held = min(ratio, 1 + hi), ratio > 1 + hi
+                else:
+                    used, held = max(ratio, 1 - lo), ratio < 1 - lo
+                    if dual and used > dual:
+                        used, held = dual, True
+                held = held and A != 0
+                s, g = (0.0, 0.0) if A == 0 else (A * used, 0.0 if held else A * ratio)
+                t = 0.0 if ref is None else ref[r] + loss[index[r]]
+                kl = INF if np.isinf(t) else np.expm1(t) - t
+                k = kl_coef * kl if kl_coef else 0.0
+                terms = np.array([k - s, kl, float(held), ratio, 1.0])
+                stats += w * terms
+                smag += w * np.abs([k + abs(s), kl, float(held), ratio, 1.0])
+                pull, pull_mag = pull + w * g, pull_mag + abs(w * g)
+                if kl_coef and ref is not None:
+                    grad[index[r]] += w * kl_coef * np.expm1(t)
+                    mag[index[r]] += w * kl_coef * (np.exp(t) + 1)
+            for r in on:
+                grad[index[r]] += pull / len(on)
+                mag[index[r]] += pull_mag / len(on)
+    return stats, grad, smag, mag
+
+
+def _matches(got, want, mag, what, rel=2.0 ** -19):
+    got = got.double().cpu().numpy()
+    want = np.where(np.abs(want) > LARGEST, np.sign(want) * INF, want)
+    ends = ~np.isfinite(want)
+    assert np.array_equal(got[ends], want[ends], equal_nan=True), (what, got, want)
+    assert (np.abs(got - want)[~ends] <= rel * mag[~ends] + 1e-30).all(), (what, got, want)
+
+
+def _batch(level):
+    """Two positions under three sequences of five own tokens each, the second sequence's third token for the tests."""
+    index = np.concatenate([np.concatenate([[0, 1], np.arange(5) + 2 + 5 * k]) for k in range(3)]).astype(np.int32)
+    g = np.random.default_rng(3)
+    s = dict(loss=(0.1 + 2 * g.random(17)), index=index, at=7 + 4)
+    s["old"] = -s["loss"][index] + 0.2 * g.normal(size=21)
+    s["ref"] = -s["loss"][index] + 0.3 * g.normal(size=21)
+    s["adv"], s["weight"] = 0.5 + g.random(21), 0.1 + g.random(21)
+    s["offsets"] = np.arange(0, 22, 7, dtype=np.int32) if level == "sequence" else None
+    return {k: v.astype(np.float32).astype(np.float64) if isinstance(v, np.ndarray) and v.dtype == np.float64 else v
+            for k, v in s.items()}
+
+
+def _run(ops, s, **kw):
+    index = s["index"]
+    begin = np.zeros(len(s["loss"]) + 1, np.int32)
+    begin[1:] = np.cumsum(np.bincount(index, minlength=len(s["loss"])))
+    t = lambda a: torch.from_numpy(np.ascontiguousarray(a)).cuda()
+    f = lambda a: t(np.asarray(a).astype(np.float32))
+    return ops.policy_loss(f(s["loss"]), f(s["old"]), f(s["adv"]), f(s["weight"]), t(index), t(begin),
+                           t(np.argsort(index, kind="stable").astype(np.int32)),
+                           ref_logp=None if s["ref"] is None else f(s["ref"]),
+                           seq_offsets=None if s["offsets"] is None else t(s["offsets"]), **kw)
+
+
+def _check(ops, s, lo=0.2, hi=0.28, dual=0.0, kl=0.0):
+    want = _formula(s["loss"], s["old"], s["adv"], s["weight"], s["index"], s["offsets"], s["ref"], lo, hi, dual, kl)
+    stats, dloss = _run(ops, s, clip_low=lo, clip_high=hi, dual_clip=dual, kl_coef=kl)
+    _matches(stats, want[0], want[2], "stats")
+    _matches(dloss, want[1], want[3], "dloss")
+    return dloss
+
+
+@pytest.mark.parametrize("level", ["token", "sequence"])
+@pytest.mark.parametrize("dual", [0.0, 3.0])
+@pytest.mark.parametrize("which,value,kl,ref", [
+    (which, value, kl, ref) for kl, ref in ((0.0, False), (0.0, True), (0.05, True))
+    for which, value in (("old", -INF), ("old", INF), ("loss", INF)) + ((("ref", -INF), ("ref", INF)) if ref else ())])
+@pytest.mark.parametrize("sign", [1.0, -1.0])
+def test_infinite_log_probabilities(ops, level, dual, kl, ref, which, value, sign):
+    s = _batch(level)
+    if not ref:
+        s["ref"] = None
+    s["adv"] = s["adv"] * sign
+    plain = _check(ops, s, dual=dual, kl=kl)
+    at = s["at"]
+    s[which][s["index"][at] if which == "loss" else at] = value
+    got = _check(ops, s, dual=dual, kl=kl)
+    # what does not share the token's position or its sequence's ratio stays as it was
+    lo, hi = (7, 14) if level == "sequence" else (at, at + 1)
+    apart = np.ones(len(s["loss"]), bool)
+    apart[s["index"][lo:hi]] = False
+    assert torch.equal(got[torch.from_numpy(apart)], plain[torch.from_numpy(apart)])
+
+
+@pytest.mark.parametrize("level", ["token", "sequence"])
+@pytest.mark.parametrize("border", [dict(lo=1.0), dict(hi=INF), dict(lo=1.0, hi=INF), dict(dual=INF)])
+@pytest.mark.parametrize("value", [-INF, INF])
+@pytest.mark.parametrize("sign", [1.0, -1.0])
+def test_infinite_log_probabilities_at_borders_without_end(ops, level, border, value, sign):
+    s = _batch(level)
+    s["adv"] = s["adv"] * sign
+    s["old"][s["at"]] = value
+    _check(ops, s, kl=0.05, **border)
+
+
+@pytest.mark.parametrize("level", ["token", "sequence"])
+@pytest.mark.parametrize("value", [-INF, INF])
+def test_an_infinite_log_probability_among_others_that_cancel_it_not(ops, level, value):
+    """Two of a kind in a sequence, and advantages of both signs."""
+    s = _batch(level)
+    s["adv"][::2] *= -1
+    s["old"][s["at"]] = s["old"][s["at"] + 1] = value
+    _check(ops, s, dual=3.0)
