@@ -749,7 +749,8 @@ int tpk_gated_ffn_bwd(const void* x, int64_t ld_x, const void* w_in, const void*
  *   kl = exp(t) - t - 1,  t = ref_logp[r] - logp     (ref_logp NULL: 0)
  *   objective = sum_r weight[r] (kl_coef kl - s)
  *   dloss[f]  = d objective / d loss[f], summed over the raw tokens of f
- * A token whose s is held by a border passes no gradient of its ratio.
+ * A token whose s is held by a border passes no gradient of its ratio; one
+ * with A = 0 has s = 0 and passes none either, whatever its ratio.
  * Infinite log-probabilities count by the formulas' limits: a ratio of 0 or
  * infinity, which the borders hold as any other, and an infinite kl.  Of a
  * token of weight 0 nothing else is read.  Shared positions take the shares of

@@ -82,11 +82,12 @@ struct Term {
   float objective, held;
 };
 __device__ __forceinline__ Term term_of(const Clip& c, float adv) {
+  // without an advantage nothing, however large the ratio
   const bool neg = adv < 0.f, zero = adv == 0.f;
   const bool held = !zero && (neg ? c.held[1] : c.held[0]);
   Term t;
-  t.objective = -adv * (zero ? c.ratio : neg ? c.used[1] : c.used[0]);
-  t.grad = held ? 0.f : adv * c.ratio;
+  t.objective = zero ? 0.f : -adv * (neg ? c.used[1] : c.used[0]);
+  t.grad = held || zero ? 0.f : adv * c.ratio;
   t.held = held ? 1.f : 0.f;
   return t;
 }

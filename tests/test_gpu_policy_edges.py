@@ -61,10 +61,10 @@ def _formula(loss, old, adv, weight, index, offsets, ref, lo, hi, dual, kl_coef)
 
 def _matches(got, want, mag, what, rel=2.0 ** -19):
     got = got.double().cpu().numpy()
-    want = np.where(np.abs(want) > LARGEST, np.sign(want) * INF, want)
+    want = np.where(np.abs(want) > LARGEST, np.copysign(INF, want), want)
     ends = ~np.isfinite(want)
     assert np.array_equal(got[ends], want[ends], equal_nan=True), (what, got, want)
-    assert (np.abs(got - want)[~ends] <= rel * mag[~ends] + 1e-30).all(), (what, got, want)
+    assert (np.abs(got[~ends] - want[~ends]) <= rel * mag[~ends] + 1e-30).all(), (what, got, want)
 
 
 def _batch(level):
@@ -141,3 +141,17 @@ def test_an_infinite_log_probability_among_others_that_cancel_it_not(ops, level,
     s["adv"][::2] *= -1
     s["old"][s["at"]] = s["old"][s["at"] + 1] = value
     _check(ops, s, dual=3.0)
+
+
+@pytest.mark.parametrize("level", ["token", "sequence"])
+@pytest.mark.parametrize("gap", [100.0, 1e30, INF])
+@pytest.mark.parametrize("dual", [0.0, 3.0])
+def test_no_advantage_beside_a_ratio_past_the_range(ops, level, gap, dual):
+    """A group of equal rewards has advantages of 0: they add nothing, at a ratio that fp32 cannot hold too."""
+    s = _batch(level)
+    s["adv"][7:14] = 0.0
+    s["old"][7:14] = np.float32(-gap)
+    dloss = _check(ops, s, dual=dual)
+    assert not dloss[torch.from_numpy(s["index"][9:14]).long().cuda()].any()
+    s["adv"][8] = 0.5            # held at the border beside them
+    _check(ops, s, dual=dual)
