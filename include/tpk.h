@@ -763,7 +763,8 @@ int tpk_gated_ffn_bwd(const void* x, int64_t ld_x, const void* w_in, const void*
  *   held by a border, times ratio; the sum of weights (fp64 sums, fixed order).
  *   workspace: tpk_policy_loss_workspace_bytes bytes, 256-byte aligned, need not
  *   be cleared (a share per raw token, partial sums); one call at a time.
- * R = 0 writes zero stats.  Errors: TPK_E_ARG, TPK_E_WORKSPACE. */
+ * R = 0 writes zero stats.  R, n_seqs < 2^31 - 8192.  Errors: TPK_E_ARG,
+ * TPK_E_WORKSPACE. */
 typedef struct {
     double clip_low, clip_high;   /* 0 <= clip_low <= 1, clip_high >= 0 */
     double dual_clip;             /* 0, or > 1 */

@@ -369,11 +369,10 @@ __global__ void __launch_bounds__(kPolThreads) policy_position_kernel(const Poli
   }
   const int64_t f = (static_cast<int64_t>(warp) * blocks + blockIdx.x) * 32 + lane;
   int lo = 0, hi = 0;
-  if (f < p.F) {
-    lo = __ldg(p.raw_begin + f);
-    hi = __ldg(p.raw_begin + f + 1);
-    lo = lo < 0 ? 0 : lo;
-    hi = hi > p.R ? static_cast<int>(p.R) : hi;
+  if (f < p.F) {   // (whatever the list's ends are, it stays within [0, R))
+    const int most = static_cast<int>(p.R);
+    lo = min(max(__ldg(p.raw_begin + f), 0), most);
+    hi = min(max(__ldg(p.raw_begin + f + 1), lo), most);
   }
   __shared__ int from[kWarps][32], to[kWarps][32], is_long[kWarps];
   __shared__ float part[kWarps][32];
@@ -405,13 +404,15 @@ int token_blocks(int64_t R) {
   return static_cast<int>(b < 1 ? 1 : b > kPolBlocks ? kPolBlocks : b);
 }
 size_t share_bytes(int64_t R) { return (static_cast<size_t>(R) * 4 + 255) / 256 * 256; }
+// Lists and partial sums are walked in strides that run past their ends by less than 8,192, in 32 bits.
+bool count_ok(int64_t n) { return n >= 0 && n < (int64_t{1} << 31) - 8192; }
 
 }  // namespace
 }  // namespace tpk
 
 extern "C" size_t tpk_policy_loss_workspace_bytes(int64_t R, int32_t n_seqs) {
   using namespace tpk;
-  if (R < 0 || R >= (int64_t{1} << 31) || n_seqs < 0) return 0;
+  if (!count_ok(R) || !count_ok(n_seqs)) return 0;
   const size_t rows = n_seqs > 0 ? static_cast<size_t>(n_seqs) : token_blocks(R);
   return share_bytes(R) + rows * kStats * sizeof(double);
 }
@@ -422,8 +423,8 @@ extern "C" int tpk_policy_loss(const float* loss, const float* old_logp, const f
                                const tpk_policy_opts* opts, float* stats, float* dloss, int64_t R, int64_t F,
                                void* workspace, size_t ws_bytes, void* stream) {
   using namespace tpk;
-  if (!opts || R < 0 || F < 0 || F > R || R >= (int64_t{1} << 31) || !stats) return TPK_E_ARG;
-  if (seq_offsets ? n_seqs < 1 : n_seqs != 0) return TPK_E_ARG;
+  if (!opts || !count_ok(R) || F < 0 || F > R || !stats) return TPK_E_ARG;
+  if (seq_offsets ? n_seqs < 1 || !count_ok(n_seqs) : n_seqs != 0) return TPK_E_ARG;
   if (!(opts->clip_low >= 0.0 && opts->clip_low <= 1.0) || !(opts->clip_high >= 0.0) ||
       !(opts->dual_clip == 0.0 || opts->dual_clip > 1.0) || !(opts->kl_coef >= 0.0 && opts->kl_coef < INFINITY))
     return TPK_E_ARG;

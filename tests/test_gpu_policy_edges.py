@@ -155,3 +155,32 @@ def test_no_advantage_beside_a_ratio_past_the_range(ops, level, gap, dual):
     assert not dloss[torch.from_numpy(s["index"][9:14]).long().cuda()].any()
     s["adv"][8] = 0.5            # held at the border beside them
     _check(ops, s, dual=dual)
+
+
+def test_ends_of_lists_that_lie_outside_the_batch(ops):
+    """An end below 0 or above R counts as 0 or R, one below its list's start as that start; other positions are as they were."""
+    index = np.repeat(np.arange(40), np.where(np.arange(40) % 5 == 0, 60, 3)).astype(np.int32)
+    g = np.random.default_rng(4)
+    R, F = len(index), 40
+    begin = np.zeros(F + 1, np.int32)
+    begin[1:] = np.cumsum(np.bincount(index))
+    raw = np.arange(R, dtype=np.int32)
+    t = lambda a: torch.from_numpy(a).cuda()
+    f = lambda *s: g.normal(size=s).astype(np.float32)
+    loss, adv, weight = np.abs(f(F)), f(R), np.abs(f(R))
+    old = -loss[index] + 0.1 * f(R)
+    run = lambda b: ops.policy_loss(t(loss), t(old), t(adv), t(weight), t(index), t(b), t(raw))[1].cpu().numpy()
+    want = run(begin)
+    share = lambda lo, hi: float(ops.policy_loss(t(loss), t(old), t(adv), t(weight), t(index),
+                                                 t(np.array([lo] + [hi] * F, np.int32)), t(raw))[1][0])
+    for at, value in ((0, -2 ** 31), (0, -1), (F, R + 1), (F, 2 ** 31 - 1), (17, 2 ** 31 - 1), (17, -2 ** 31), (20, -5)):
+        b = begin.copy()
+        b[at] = value
+        got = run(b)
+        touched = [k for k in (at - 1, at) if 0 <= k < F]
+        rest = np.setdiff1d(np.arange(F), touched)
+        assert np.array_equal(got[rest], want[rest])
+        for k in touched:
+            lo = min(max(int(b[k]), 0), R)
+            hi = min(max(int(b[k + 1]), lo), R)
+            assert abs(got[k] - share(lo, hi)) <= 2.0 ** -19 * np.abs(adv * weight).sum() * 2
