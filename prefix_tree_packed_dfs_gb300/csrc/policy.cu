@@ -68,7 +68,7 @@ struct Clip {
 };
 __device__ __forceinline__ Clip clip_of(const Policy& p, Pair d) {
   Clip c;
-  c.ratio = expf(d.hi + d.lo);
+  c.ratio = expf(d.hi);
   c.held[0] = less(d, p.log_hi) > 0.f;
   c.used[0] = c.held[0] ? p.hi : c.ratio;
   const bool below = less(d, p.log_lo) < 0.f, above = less(d, p.log_dual) > 0.f;
@@ -94,8 +94,10 @@ __device__ __forceinline__ Term term_of(const Clip& c, float adv) {
 
 // exp(t) - t - 1; infinite at both infinities
 __device__ __forceinline__ float k3(float t) {
-  if (isinf(t)) return INFINITY;
-  if (fabsf(t) >= 0.3f) return expm1f(t) - t;
+  if (fabsf(t) >= 0.3f) {
+    const float e = expm1f(t);
+    return e == INFINITY ? e : e - t;
+  }
   // t^2 (1/2! + t/3! + .. + t^5/7!): the next term is 4e-8 of it
   float s = fmaf(t, 1.f / 5040.f, 1.f / 720.f);
   s = fmaf(t, s, 1.f / 120.f);
@@ -120,8 +122,7 @@ __device__ __forceinline__ Token token_at(const Policy& p, int64_t r) {
 
 // The KL term of a token; its share of the gradient is added to grad.
 __device__ __forceinline__ float kl_of(const Policy& p, float ref, float loss, float& grad) {
-  const Pair d = two_sum(ref, loss);   // ref - logp
-  const float t = d.hi + d.lo;
+  const float t = ref + loss;   // ref - logp
   if (p.kl != 0.f) grad += p.kl * expm1f(t);
   return k3(t);
 }
@@ -178,32 +179,36 @@ __global__ void __launch_bounds__(kPolThreads) policy_token_kernel(const Policy 
   put_sums<kPolThreads>(p, s, blockIdx.x);
 }
 
-// The block's sum of v and of n.
+// The warps' sums of v and of n, for the first of them to add up.
 template <int kThreadsOf>
-__device__ __forceinline__ Pair block_sum(Pair v, int& n) {
-  __shared__ Pair room[kThreadsOf / 32];
-  __shared__ int many[kThreadsOf / 32];
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+struct Parts {
+  Pair sum[kThreadsOf / 32];
+  int many[kThreadsOf / 32];
+
+  __device__ __forceinline__ void put(Pair v, int n) {
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) {
-    v = add(v, Pair{__shfl_xor_sync(0xffffffffu, v.hi, o), __shfl_xor_sync(0xffffffffu, v.lo, o)});
-    n += __shfl_xor_sync(0xffffffffu, n, o);
+    for (int o = 16; o > 0; o >>= 1) {
+      v = add(v, Pair{__shfl_xor_sync(0xffffffffu, v.hi, o), __shfl_xor_sync(0xffffffffu, v.lo, o)});
+      n += __shfl_xor_sync(0xffffffffu, n, o);
+    }
+    if ((threadIdx.x & 31) == 0) sum[threadIdx.x >> 5] = v, many[threadIdx.x >> 5] = n;
   }
-  __syncthreads();   // the room has been read
-  if (lane == 0) room[warp] = v, many[warp] = n;
-  __syncthreads();
-  v = room[0];
-  n = many[0];
+  __device__ __forceinline__ Pair total(int& n) const {
+    Pair v = sum[0];
+    n = many[0];
 #pragma unroll
-  for (int i = 1; i < kThreadsOf / 32; ++i) v = add(v, room[i]), n += many[i];
-  return v;
-}
+    for (int i = 1; i < kThreadsOf / 32; ++i) v = add(v, sum[i]), n += many[i];
+    return v;
+  }
+};
 
 // A CTA per sequence: ratio = exp(mean log-ratio of its tokens that carry loss).
 constexpr int kSeqThreads = 256;
 __global__ void __launch_bounds__(kSeqThreads, 4) policy_sequence_kernel(const Policy p) {
   ptx::dependents_launch();
   __shared__ Clip clip;
+  __shared__ Parts<kSeqThreads> log_ratios, pulls;
+  __shared__ float share_of_pull;
   auto inside = [&](int64_t x) { return x < 0 ? 0 : x > p.R ? p.R : x; };
   const int i = blockIdx.x;
   const int64_t lo = inside(__ldg(p.offsets + i)), hi = inside(__ldg(p.offsets + i + 1));
@@ -249,8 +254,10 @@ __global__ void __launch_bounds__(kSeqThreads, 4) policy_sequence_kernel(const P
       ++many;
     }
   }
-  sum = block_sum<kSeqThreads>(sum, many);
+  log_ratios.put(sum, many);
+  __syncthreads();
   if (threadIdx.x == 0) {
+    sum = log_ratios.total(many);
     const double d = many ? (static_cast<double>(sum.hi) + static_cast<double>(sum.lo)) / many : 0.0;
     const float top = static_cast<float>(d);
     clip = clip_of(p, Pair{top, isinf(top) ? 0.f : static_cast<float>(d - static_cast<double>(top))});
@@ -277,9 +284,15 @@ __global__ void __launch_bounds__(kSeqThreads, 4) policy_sequence_kernel(const P
     const float a = __ldg(p.advantage + r);
     if (k.f >= 0) gather(k, a);
   }
-  int unused = 0;
-  pull = block_sum<kSeqThreads>(pull, unused);
-  const float each = many ? (pull.hi + pull.lo) / static_cast<float>(many) : 0.f;
+  pulls.put(pull, 0);
+  __syncthreads();
+  if (threadIdx.x == 0) {
+    int unused;
+    pull = pulls.total(unused);
+    share_of_pull = many ? (pull.hi + pull.lo) / static_cast<float>(many) : 0.f;
+  }
+  __syncthreads();
+  const float each = share_of_pull;
   auto share = [&](const Token& k, float token_ref, float token_loss) {
     if (k.f < 0) return 0.f;
     if (!p.ref_logp) return each;
