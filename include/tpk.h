@@ -760,7 +760,11 @@ int tpk_gated_ffn_bwd(const void* x, int64_t ld_x, const void* w_in, const void*
  *   seq_offsets: device int32 [n_seqs + 1], ascending, 0 first and R last, or
  *   NULL with n_seqs = 0.
  *   stats [5] fp32: the objective; sums of weight times kl, times 1 where s is
- *   held by a border, times ratio; the sum of weights (fp64 sums, fixed order).
+ *   held by a border, times ratio; the sum of weights.  Added in a fixed order,
+ *   up to six of a thread's terms at a time in fp32 and these sums in pairs of fp32
+ *   numbers, a warp's threads in fp32, the warps in fp64: within 2^-20 of the
+ *   terms' magnitudes, however many there are.
+ *   dloss: fp32 sums in a fixed order.
  *   workspace: tpk_policy_loss_workspace_bytes bytes, 256-byte aligned, need not
  *   be cleared (a share per raw token, partial sums); one call at a time.
  * R = 0 writes zero stats.  R, n_seqs < 2^31 - 8192.  Errors: TPK_E_ARG,

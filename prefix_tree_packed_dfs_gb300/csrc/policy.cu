@@ -9,10 +9,10 @@
 // the sums; it starts under the first (programmatic dependent launch).
 // Log-ratios are differences of two fp32 numbers and are kept as the exact sum
 // of two, for their comparison with the clip's borders (a token is never on the
-// wrong side) and for a sequence's mean; fp64 instructions, of which this part
-// has few, are left to single threads (512 sequences, 548,000 tokens: a sequence
-// pass with fp64 block sums took 83 us, this one 13).  exp(t) - t - 1 near t = 0 is its
-// series.
+// wrong side) and for a sequence's mean, as are the sums of a thread's batches of
+// tokens; fp64 instructions, of which this part has few, are left to single threads
+// (512 sequences, 548,000 tokens: a sequence pass with fp64 block sums took 83 us,
+// this one 13).  exp(t) - t - 1 near t = 0 is its series.
 // What bounds it: latency, of the launches and of the chain offset -> token ->
 // share.
 #include <cmath>
@@ -39,6 +39,12 @@ __device__ __forceinline__ Pair two_sum(float a, float b) {
 __device__ __forceinline__ Pair add(Pair a, Pair b) {
   const Pair s = two_sum(a.hi, b.hi);
   return two_sum(s.hi, s.lo + (a.lo + b.lo));
+}
+// Adds x to s, as exactly as two fp32 numbers can hold it.
+__device__ __forceinline__ void into(Pair& s, float x) {
+  const Pair t = two_sum(s.hi, x);
+  s.hi = t.hi;
+  s.lo += t.lo;
 }
 // a - b, of which the sign is right next to 0 too; NaN, which is on neither side,
 // for equal infinities
@@ -127,14 +133,15 @@ __device__ __forceinline__ float kl_of(const Policy& p, float ref, float loss, f
   return k3(t);
 }
 
-// The block's sums of s into row `row` of p.sums.
+// The block's sums of s into row `row` of p.sums: a thread's is off by the roundings of
+// one batch of tokens and one more, however many it had, a warp's by five more.
 template <int kThreadsOf>
-__device__ __forceinline__ void put_sums(const Policy& p, const float (&s)[kStats], int row) {
+__device__ __forceinline__ void put_sums(const Policy& p, const Pair (&s)[kStats], int row) {
   __shared__ float part[kThreadsOf / 32][kStats];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
 #pragma unroll
   for (int i = 0; i < kStats; ++i) {
-    float v = s[i];
+    float v = s[i].hi + s[i].lo;
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
     if (lane == 0) part[warp][i] = v;
@@ -149,32 +156,48 @@ __device__ __forceinline__ void put_sums(const Policy& p, const float (&s)[kStat
 
 __global__ void __launch_bounds__(kPolThreads) policy_token_kernel(const Policy p) {
   ptx::dependents_launch();
-  float s[kStats] = {};
+  constexpr int kBatch = 2;
+  Pair s[kStats] = {};
   const int64_t step = static_cast<int64_t>(gridDim.x) * kPolThreads;
-#pragma unroll 2
-  for (int64_t r = static_cast<int64_t>(blockIdx.x) * kPolThreads + threadIdx.x; r < p.R; r += step) {
-    const Token k = token_at(p, r);
-    const float old = __ldg(p.old_logp + r), adv = __ldg(p.advantage + r);
-    const float ref = p.ref_logp ? __ldg(p.ref_logp + r) : 0.f;
-    float g = 0.f;
-    if (k.f >= 0) {
-      const float loss = __ldg(p.loss + k.f);
-      const Clip c = clip_of(p, two_sum(-loss, -old));
-      const Term t = term_of(c, adv);
-      float objective = t.objective, kl = 0.f;
-      g = t.grad;
-      if (p.ref_logp) {
-        kl = kl_of(p, ref, loss, g);
-        if (p.kl != 0.f) objective = fmaf(p.kl, kl, objective);
-      }
-      g *= k.w;
-      s[0] = fmaf(k.w, objective, s[0]);
-      s[1] = fmaf(k.w, kl, s[1]);
-      s[2] = fmaf(k.w, t.held, s[2]);
-      s[3] = fmaf(k.w, c.ratio, s[3]);
-      s[4] += k.w;
+#pragma unroll 1
+  for (int64_t r0 = static_cast<int64_t>(blockIdx.x) * kPolThreads + threadIdx.x; r0 < p.R; r0 += kBatch * step) {
+    Token k[kBatch];
+    float old[kBatch], adv[kBatch], ref[kBatch], loss[kBatch], some[kStats] = {};
+#pragma unroll
+    for (int j = 0; j < kBatch; ++j) {
+      const int64_t r = r0 + j * step;
+      const bool in = r < p.R;
+      k[j] = in ? token_at(p, r) : Token{0.f, -1};
+      old[j] = in ? __ldg(p.old_logp + r) : 0.f;
+      adv[j] = in ? __ldg(p.advantage + r) : 0.f;
+      ref[j] = in && p.ref_logp ? __ldg(p.ref_logp + r) : 0.f;
     }
-    p.share[r] = g;
+#pragma unroll
+    for (int j = 0; j < kBatch; ++j) loss[j] = k[j].f >= 0 ? __ldg(p.loss + k[j].f) : 0.f;
+#pragma unroll
+    for (int j = 0; j < kBatch; ++j) {
+      float g = 0.f;
+      if (k[j].f >= 0) {
+        const Clip c = clip_of(p, two_sum(-loss[j], -old[j]));
+        const Term t = term_of(c, adv[j]);
+        float objective = t.objective, kl = 0.f;
+        g = t.grad;
+        if (p.ref_logp) {
+          kl = kl_of(p, ref[j], loss[j], g);
+          if (p.kl != 0.f) objective = fmaf(p.kl, kl, objective);
+        }
+        const float w = k[j].w;
+        g *= w;
+        some[0] = fmaf(w, objective, some[0]);
+        some[1] = fmaf(w, kl, some[1]);
+        some[2] = fmaf(w, t.held, some[2]);
+        some[3] = fmaf(w, c.ratio, some[3]);
+        some[4] += w;
+      }
+      if (r0 + j * step < p.R) p.share[r0 + j * step] = g;
+    }
+#pragma unroll
+    for (int i = 0; i < kStats; ++i) into(s[i], some[i]);
   }
   put_sums<kPolThreads>(p, s, blockIdx.x);
 }
@@ -219,7 +242,7 @@ __global__ void __launch_bounds__(kSeqThreads, 4) policy_sequence_kernel(const P
     for (int64_t r = hi + threadIdx.x; r < p.R; r += kSeqThreads) p.share[r] = 0.f;
   // A sequence of up to kKeep tokens per thread is read once; what is longer is
   // read again by each step.
-  constexpr int kKeep = 6;
+  constexpr int kKeep = 6, kBatch = 4;
   const int64_t first = lo + threadIdx.x, later = first + int64_t{kKeep} * kSeqThreads;
   Token kept[kKeep];
   float old[kKeep], adv[kKeep], ref[kKeep], loss[kKeep];
@@ -266,23 +289,37 @@ __global__ void __launch_bounds__(kSeqThreads, 4) policy_sequence_kernel(const P
   const Clip c = clip;
   // the ratio's gradient, which every token shares
   Pair pull{0.f, 0.f};
-  float s[kStats] = {};
-  auto gather = [&](const Token& k, float a) {
+  // sums of the kept tokens; those of the others are added to them as pairs
+  float near[kStats] = {};
+  auto gather = [&](const Token& k, float a, float (&to)[kStats]) {
     const Term t = term_of(c, a);
     pull = add(pull, Pair{k.w * t.grad, 0.f});
-    s[0] = fmaf(k.w, t.objective, s[0]);
-    s[2] = fmaf(k.w, t.held, s[2]);
-    s[3] = fmaf(k.w, c.ratio, s[3]);
-    s[4] += k.w;
+    to[0] = fmaf(k.w, t.objective, to[0]);
+    to[2] = fmaf(k.w, t.held, to[2]);
+    to[3] = fmaf(k.w, c.ratio, to[3]);
+    to[4] += k.w;
   };
 #pragma unroll
   for (int j = 0; j < kKeep; ++j)
-    if (kept[j].f >= 0) gather(kept[j], adv[j]);
-#pragma unroll 4
-  for (int64_t r = later; r < hi; r += kSeqThreads) {
-    const Token k = token_at(p, r);
-    const float a = __ldg(p.advantage + r);
-    if (k.f >= 0) gather(k, a);
+    if (kept[j].f >= 0) gather(kept[j], adv[j], near);
+  Pair s[kStats];
+#pragma unroll
+  for (int i = 0; i < kStats; ++i) s[i] = Pair{near[i], 0.f};
+#pragma unroll 1
+  for (int64_t r0 = later; r0 < hi; r0 += kBatch * kSeqThreads) {
+    Token k[kBatch];
+    float a[kBatch], some[kStats] = {};
+#pragma unroll
+    for (int j = 0; j < kBatch; ++j) {
+      const int64_t r = r0 + j * kSeqThreads;
+      k[j] = r < hi ? token_at(p, r) : Token{0.f, -1};
+      a[j] = r < hi ? __ldg(p.advantage + r) : 0.f;
+    }
+#pragma unroll
+    for (int j = 0; j < kBatch; ++j)
+      if (k[j].f >= 0) gather(k[j], a[j], some);
+#pragma unroll
+    for (int i = 0; i < kStats; ++i) into(s[i], some[i]);
   }
   pulls.put(pull, 0);
   __syncthreads();
@@ -293,22 +330,39 @@ __global__ void __launch_bounds__(kSeqThreads, 4) policy_sequence_kernel(const P
   }
   __syncthreads();
   const float each = share_of_pull;
+  float kls = 0.f, parts = 0.f;   // sums of w kl, and of its part of the objective
   auto share = [&](const Token& k, float token_ref, float token_loss) {
     if (k.f < 0) return 0.f;
     if (!p.ref_logp) return each;
     float pull_kl = 0.f;
     const float kl = kl_of(p, token_ref, token_loss, pull_kl);
-    if (p.kl != 0.f) s[0] = fmaf(k.w, p.kl * kl, s[0]);
-    s[1] = fmaf(k.w, kl, s[1]);
+    if (p.kl != 0.f) parts = fmaf(k.w, p.kl * kl, parts);
+    kls = fmaf(k.w, kl, kls);
     return fmaf(k.w, pull_kl, each);
   };
 #pragma unroll
   for (int j = 0; j < kKeep; ++j)
     if (first + j * kSeqThreads < hi) p.share[first + j * kSeqThreads] = share(kept[j], ref[j], loss[j]);
-#pragma unroll 4
-  for (int64_t r = later; r < hi; r += kSeqThreads) {
-    const Token k = token_at(p, r);
-    p.share[r] = share(k, p.ref_logp && k.f >= 0 ? __ldg(p.ref_logp + r) : 0.f, k.f >= 0 ? __ldg(p.loss + k.f) : 0.f);
+  into(s[0], parts);
+  into(s[1], kls);
+#pragma unroll 1
+  for (int64_t r0 = later; r0 < hi; r0 += kBatch * kSeqThreads) {
+    kls = parts = 0.f;
+    Token k[kBatch];
+    float of_ref[kBatch], of_loss[kBatch];
+#pragma unroll
+    for (int j = 0; j < kBatch; ++j) {
+      const int64_t r = r0 + j * kSeqThreads;
+      k[j] = r < hi ? token_at(p, r) : Token{0.f, -1};
+      of_ref[j] = p.ref_logp && r < hi ? __ldg(p.ref_logp + r) : 0.f;
+    }
+#pragma unroll
+    for (int j = 0; j < kBatch; ++j) of_loss[j] = p.ref_logp && k[j].f >= 0 ? __ldg(p.loss + k[j].f) : 0.f;
+#pragma unroll
+    for (int j = 0; j < kBatch; ++j)
+      if (r0 + j * kSeqThreads < hi) p.share[r0 + j * kSeqThreads] = share(k[j], of_ref[j], of_loss[j]);
+    into(s[0], parts);
+    into(s[1], kls);
   }
   put_sums<kSeqThreads>(p, s, i);
 }

@@ -184,3 +184,34 @@ def test_ends_of_lists_that_lie_outside_the_batch(ops):
             lo = min(max(int(b[k]), 0), R)
             hi = min(max(int(b[k + 1]), lo), R)
             assert abs(got[k] - share(lo, hi)) <= 2.0 ** -19 * np.abs(adv * weight).sum() * 2
+
+
+@pytest.mark.parametrize("level", ["token", "sequence"])
+@pytest.mark.parametrize("lengths", [(2000003,), (3, 1000000, 1, 999999), (8000000,)])
+def test_statistics_of_many_tokens(ops, level, lengths):
+    """Sums of thousands of terms per thread.  The sums of weights and of clipped tokens: up to six of a thread's
+    terms at a time in fp32, 6 roundings, and these sums in pairs; a warp's 5, and one each for the pair and the result:
+    13 x 2^-24 of the magnitudes.
+    The others have the exponential's 2^-19 besides (here |d| < 2)."""
+    R = sum(lengths)
+    g = torch.Generator(device="cuda").manual_seed(R)
+    rnd = lambda: torch.rand(R, generator=g, device="cuda")
+    index = torch.arange(R, dtype=torch.int32, device="cuda")
+    begin = torch.arange(R + 1, dtype=torch.int32, device="cuda")
+    off = torch.tensor(np.concatenate([[0], np.cumsum(lengths)]), dtype=torch.int32, device="cuda")
+    loss, weight = 0.1 + rnd(), torch.full((R,), 0.1, device="cuda")
+    old, ref, adv = -loss + 0.8 * (rnd() - 0.4), -loss + rnd() - 0.5, 0.5 + rnd()
+    stats, dloss = ops.policy_loss(loss, old, adv, weight, index, begin, index, ref_logp=ref, kl_coef=0.1,
+                                   seq_offsets=off if level == "sequence" else None)
+    d, t, w, A = -loss.double() - old.double(), ref.double() + loss.double(), weight.double(), adv.double()
+    n = torch.tensor(lengths, device="cuda")
+    if level == "sequence":
+        seq = torch.repeat_interleave(torch.arange(len(lengths), device="cuda"), n)
+        d = (torch.zeros(len(lengths), dtype=torch.float64, device="cuda").index_add_(0, seq, d) / n)[seq]
+    ratio, kl = torch.exp(d), torch.expm1(t) - t
+    terms = torch.stack([w * (0.1 * kl - A * ratio.clamp(max=1.2)), w * kl, w * (ratio > 1.2), w * ratio, w])
+    mag = terms.abs().sum(1)
+    mag[0] = (w * (0.1 * kl + A * ratio.clamp(max=1.2))).sum()
+    rel = torch.tensor([2.0 ** -19] * 2 + [13 * 2.0 ** -24, 2.0 ** -19, 13 * 2.0 ** -24], dtype=torch.float64, device="cuda")
+    off_by = (stats.double() - terms.sum(1)).abs() / mag.clamp(min=1e-30)
+    assert (off_by <= rel).all(), off_by
