@@ -144,17 +144,19 @@ __device__ __forceinline__ void tmem_wait_ld_of(uint32_t (&r)[32]) {
                : "memory");
 }
 
-// Whether ok holds for all 128 threads of barrier `id`; every one of them calls it.
-__device__ __forceinline__ bool all_of_128(int id, bool ok) {
+// Whether ok holds for all kCount threads of barrier `id`; every one of them calls it.
+template <int kCount>
+__device__ __forceinline__ bool all_of(int id, bool ok) {
   uint32_t r;
   asm volatile(
-      "{\n .reg .pred p, q;\n setp.ne.u32 p, %2, 0;\n barrier.cta.red.and.aligned.pred q, %1, 128, p;\n"
+      "{\n .reg .pred p, q;\n setp.ne.u32 p, %2, 0;\n barrier.cta.red.and.aligned.pred q, %1, %3, p;\n"
       " selp.u32 %0, 1, 0, q;\n}\n"
       : "=r"(r)
-      : "r"(id), "r"(ok ? 1u : 0u)
+      : "r"(id), "r"(ok ? 1u : 0u), "n"(kCount)
       : "memory");
   return r != 0;
 }
+__device__ __forceinline__ bool all_of_128(int id, bool ok) { return all_of<128>(id, ok); }
 
 }  // namespace ptx
 }  // namespace tpk

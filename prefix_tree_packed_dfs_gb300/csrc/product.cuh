@@ -651,8 +651,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       } else {
         ok = ptx::mbar_wait(&S.tm_full[tile & 1], (tile / 2) & 1, abort_flag, kWaitLimitNs);
       }
-      // a warpgroup has barriers of its own and gives up as a whole
-      ok = ptx::all_of_128(wg + 1, ok);
+      // a warpgroup has barriers of its own and gives up as a whole; where pairs share a
+      // tile the two meet on their way (the cluster's barrier, kDz's sums) and do so together
+      ok = kNarrow && teams > 1 ? ptx::all_of<kEpiThreads>(4, ok) : ptx::all_of_128(wg + 1, ok);
       if (!ok) break;
       const uint32_t buf = tile & 1;
       const uint32_t tm =
