@@ -123,10 +123,11 @@ __global__ void __launch_bounds__(kFewThreads) few_kernel(const __grid_constant_
   }
   __syncwarp();
   ptx::dependency_wait();
-  const bool ok = ptx::mbar_drain(&S.done, 0);   // every product issued has been done
+  // Every product issued has been done, and the producer's last loads have landed: the
+  // stages are free.  One answer for all threads: a warp reads TMEM as a whole.
+  const bool ok = __syncthreads_and(ptx::mbar_drain(&S.done, 0));
   ptx::tc_fence_after();
   // every thread's row of the accumulator (a result's channel) to shared memory, channels side by side
-  __syncthreads();   // the producer's last loads have landed: the stages are free
   if (ok) {
 #pragma unroll
     for (int c = 0; c < kTok; c += 16) {
