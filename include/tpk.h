@@ -709,6 +709,28 @@ int tpk_linear_bwd(const void* x, int64_t ld_x, const void* w, const float* bias
                    int64_t ld_dy, void* dx, int64_t ld_dx, void* dw, float* db, int64_t N, int32_t C, int32_t O,
                    void* workspace, size_t ws_bytes, int32_t* dev_err, void* stream);
 
+/* How tpk_linear (backward = 0) or tpk_linear_bwd does a call's products, for
+ * profiles and tests: writes out[0..3) and returns how many, or an error (as the
+ * call's own).  Needs no GPU.  The choice goes by the sizes alone and may differ
+ * between versions. */
+#define TPK_PRODUCT_Y  0
+#define TPK_PRODUCT_DZ 1
+#define TPK_PRODUCT_DX 2
+#define TPK_PRODUCT_DW 3
+#define TPK_FORM_FEW      0  /* TPK_FEW_ROWS rows at most: the weights read once */
+#define TPK_FORM_WIDE     1  /* 256 x 256 tiles */
+#define TPK_FORM_NARROW   2  /* 256 x 128 tiles */
+#define TPK_FORM_TOGETHER 3  /* 256 x 128 tiles, dx and dw in one launch */
+typedef struct {
+    int32_t product, form;
+    int32_t teams;          /* pairs of CTAs that share a tile's K */
+    int32_t tiles;          /* of the result (few rows: 0) */
+    int32_t split_tiles;    /* of those, split over K, in */
+    int32_t splits;         /* parts, which a second kernel joins */
+    int32_t pieces;         /* accumulations of the longest sum */
+} tpk_product_plan;
+int tpk_linear_plan(int64_t N, int32_t C, int32_t O, int32_t act, int32_t backward, tpk_product_plan* out);
+
 /* Gated feed-forward block:
  *   g = x w_in[0:I]^T,  u = x w_in[I:2I]^T,  a = act(g) * u,  y = a w_out^T + residual
  *   x [N, C], w_in [2 I, C], w_out [O, I], residual, y [N, O] bf16

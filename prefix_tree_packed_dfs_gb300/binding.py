@@ -23,6 +23,8 @@ PLACE_GROUPS = 2
 BF16, F32 = 0, 1
 ACT_NONE, ACT_SILU, ACT_GELU, ACT_GELU_TANH = 0, 1, 2, 3
 FEW_ROWS = 64
+PRODUCTS = ("y", "dz", "dx", "dw")
+FORMS = ("few", "wide", "narrow", "together")
 FIELD_DEPTH, FIELD_TOKEN_INDEX, FIELD_SUBTREE_END, FIELD_PARENT = 0, 1, 2, 3
 FIELD_FWD_RAW_BEGIN, FIELD_FWD_RAW = 4, 5
 FIELD_SEG_START, FIELD_SEG_LEN, FIELD_SEG_PARENT, FIELD_SEG_OFF = 6, 7, 8, 9
@@ -40,7 +42,7 @@ EXPORTS = [
     "tpk_embed", "tpk_embed_bwd_workspace_bytes", "tpk_embed_bwd",
     "tpk_block_norm", "tpk_block_norm_bwd_workspace_bytes", "tpk_block_norm_bwd",
     "tpk_lm_loss_workspace_bytes", "tpk_lm_loss", "tpk_lm_loss_bwd",
-    "tpk_rope_by_depth_ex", "tpk_linear_workspace_bytes", "tpk_linear", "tpk_linear_bwd",
+    "tpk_rope_by_depth_ex", "tpk_linear_workspace_bytes", "tpk_linear_plan", "tpk_linear", "tpk_linear_bwd",
     "tpk_gated_ffn_workspace_bytes", "tpk_gated_ffn_saved_bytes", "tpk_gated_ffn", "tpk_gated_ffn_bwd",
     "tpk_policy_loss_workspace_bytes", "tpk_policy_loss",
     "tpk_status_string",
@@ -68,6 +70,11 @@ class RopeOpts(ctypes.Structure):
     """tpk_rope_opts: rotated channels, pairing, factor, host array of radians per position."""
     _fields_ = [("rot", ctypes.c_int32), ("interleaved", ctypes.c_int32), ("factor", ctypes.c_double),
                 ("freqs", ctypes.c_void_p)]
+
+
+class ProductPlan(ctypes.Structure):
+    """tpk_product_plan: how one product of a projection is done."""
+    _fields_ = [(n, ctypes.c_int32) for n in ("product", "form", "teams", "tiles", "split_tiles", "splits", "pieces")]
 
 
 class PolicyOpts(ctypes.Structure):
@@ -151,6 +158,7 @@ def _sig(lib):
                                          ctypes.POINTER(RopeOpts), I32, P]
     lib.tpk_linear_workspace_bytes.argtypes = [I64, I32, I32, I32, I32]
     lib.tpk_linear_workspace_bytes.restype = SZ
+    lib.tpk_linear_plan.argtypes = [I64, I32, I32, I32, I32, ctypes.POINTER(ProductPlan)]
     lib.tpk_linear.argtypes = [P, I64, P, P, I32, P, I64, P, I64, I64, I32, I32, P, SZ, P, P]
     lib.tpk_linear_bwd.argtypes = [P, I64, P, P, I32, P, I64, P, I64, P, P, I64, I32, I32, P, SZ, P, P]
     lib.tpk_gated_ffn_workspace_bytes.argtypes = [I64, I32, I32, I32, I32]

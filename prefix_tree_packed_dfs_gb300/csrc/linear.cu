@@ -157,12 +157,22 @@ int join(const Params& p, const float* bias, int act, const Mat& residual, const
                        static_cast<__nv_bfloat16*>(const_cast<void*>(out.p)), out.ld);
 }
 
-Params params(int64_t M, int64_t N, int64_t K, float* acc, int32_t* err) {
+// The plans of tpk_linear's products: y and dz [N, O] over C, dx [N, C] over O, dw [O, C] over N.
+Plan forward_plan(int64_t N, int64_t C, int64_t O) { return plan_of(N, O, C); }
+Plan input_plan(int64_t N, int64_t C, int64_t O) { return plan_of(N, C, O); }
+Plan weight_plan(int64_t N, int64_t C, int64_t O) { return plan_of(O, C, N); }
+// dz's epilogue has no joined form: a wide plan stays whole
+Plan dz_plan(int64_t N, int64_t C, int64_t O) {
+  Plan p = plan_of(N, O, C);
+  if (!p.narrow) p.split = Split{tiles_of(N, O), 0, 1};
+  return p;
+}
+
+Params params(int64_t M, int64_t N, int64_t K, const Plan& plan, float* acc, int32_t* err) {
   Params p{};
   p.M = static_cast<int32_t>(M);
   p.N = static_cast<int32_t>(N);
   p.K = static_cast<int32_t>(K);
-  const Plan plan = plan_of(M, N, K);
   p.narrow = plan.narrow;
   p.teams = plan.teams;
   p.whole = static_cast<int32_t>(plan.split.whole);
@@ -171,14 +181,17 @@ Params params(int64_t M, int64_t N, int64_t K, float* acc, int32_t* err) {
   p.err = err;
   return p;
 }
+// Stages of the longest sum that a pair adds up.
+int64_t longest_of(const Plan& p, int64_t K) {
+  const int64_t k = (K + 63) / 64;
+  return p.narrow ? (k + p.teams - 1) / p.teams : p.split.whole > 0 || p.split.splits == 1 ? k : k / p.split.splits + 1;
+}
 // The product as planned, in single accumulations where they are short enough.
 template <int kMode>
-int launch_plan(const Maps& m, const Params& p, bool after, cudaStream_t s) {
+int launch_plan(const Maps& m, const Params& p, const Plan& plan, bool after, cudaStream_t s) {
   if (p.narrow) return launch<kMode, true, true>(m, p, after, s);
-  if constexpr (kMode == kDx || kMode == kDw) {
-    const int k = (p.K + 63) / 64, longest = p.whole > 0 || p.splits == 1 ? k : k / p.splits + 1;
-    if (longest > kChunk) return launch<kMode, false>(m, p, after, s);
-  }
+  if constexpr (kMode == kDx || kMode == kDw)
+    if (longest_of(plan, p.K) > kChunk) return launch<kMode, false>(m, p, after, s);
   return launch<kMode, true>(m, p, after, s);
 }
 
@@ -195,15 +208,15 @@ size_t carve(uint8_t* base, int64_t N, int64_t C, int64_t O, int32_t act, bool b
     return p;
   };
   if (!backward) {
-    if (N > kFewRows) o.acc = reinterpret_cast<float*>(take(acc_bytes(N, O, C)));
+    if (N > kFewRows) o.acc = reinterpret_cast<float*>(take(acc_bytes(forward_plan(N, C, O))));
   } else {
     if (act != TPK_ACT_NONE) {
       o.dz = reinterpret_cast<__nv_bfloat16*>(take(static_cast<size_t>(N * own_stride(O)) * 2));
       o.sums = reinterpret_cast<float*>(take(static_cast<size_t>((N + 31) / 32) * O * 4));
     }
     o.part = reinterpret_cast<float*>(take(static_cast<size_t>(kSumMost) * O * 4));
-    o.acc = reinterpret_cast<float*>(take(acc_bytes(N, C, O)));
-    o.acc_w = reinterpret_cast<float*>(take(acc_bytes(O, C, N)));
+    o.acc = reinterpret_cast<float*>(take(acc_bytes(input_plan(N, C, O))));
+    o.acc_w = reinterpret_cast<float*>(take(acc_bytes(weight_plan(N, C, O))));
   }
   if (w) *w = o;
   return at;
@@ -224,11 +237,12 @@ int linear_product(const Mat& x, const Mat& w, const float* bias, int act, const
   if (x.rows <= kFewRows) return few_linear(x, w, bias, act, residual, y, after, err, s);
   Maps m;
   int st = map_of(&m.a, x, kHalf);
-  if (st == TPK_OK) st = map_of(&m.b, w, plan_of(x.rows, w.rows, x.cols).narrow ? kHalf / 2 : kHalf);
+  const Plan plan = forward_plan(x.rows, x.cols, w.rows);
+  if (st == TPK_OK) st = map_of(&m.b, w, plan.narrow ? kHalf / 2 : kHalf);
   if (st == TPK_OK) st = map_of(&m.out, y, kHalf);
   if (st == TPK_OK && residual.p) st = map_of(&m.in, residual, kHalf);
   if (st != TPK_OK) return st;
-  Params p = params(x.rows, w.rows, x.cols, acc, err);
+  Params p = params(x.rows, w.rows, x.cols, plan, acc, err);
   p.bias = bias;
   p.act = act;
   p.has_in = residual.p != nullptr;
@@ -236,7 +250,7 @@ int linear_product(const Mat& x, const Mat& w, const float* bias, int act, const
   p.ld_in = residual.ld;
   p.out = static_cast<uint16_t*>(const_cast<void*>(y.p));
   p.ld_out = y.ld;
-  st = launch_plan<kLin>(m, p, after, s);
+  st = launch_plan<kLin>(m, p, plan, after, s);
   return st == TPK_OK && p.splits > 1 ? join(p, bias, act, residual, y, s) : st;
 }
 
@@ -247,12 +261,13 @@ int input_product(const Mat& dz, const Mat& w, const Mat& dx, float* acc, bool a
   if (st == TPK_OK) st = map_of(&m.b, w, 64);
   if (st == TPK_OK) st = map_of(&m.out, dx, kHalf);
   if (st != TPK_OK) return st;
-  Params p = params(dz.rows, w.cols, dz.cols, acc, err);
+  const Plan plan = input_plan(dz.rows, w.cols, dz.cols);
+  Params p = params(dz.rows, w.cols, dz.cols, plan, acc, err);
   p.late = 1;
   p.out = static_cast<uint16_t*>(const_cast<void*>(dx.p));
   p.ld_out = dx.ld;
   *left = p;
-  return launch_plan<kDx>(m, p, after, s);
+  return launch_plan<kDx>(m, p, plan, after, s);
 }
 
 int weight_product(const Mat& dz, const Mat& x, const Mat& dw, float* acc, const Params& before, int32_t* err,
@@ -262,12 +277,13 @@ int weight_product(const Mat& dz, const Mat& x, const Mat& dw, float* acc, const
   if (st == TPK_OK) st = map_of(&m.b, x, 64);
   if (st == TPK_OK) st = map_of(&m.out, dw, kHalf);
   if (st != TPK_OK) return st;
-  Params p = params(dz.cols, x.cols, dz.rows, acc, err);
+  const Plan plan = weight_plan(dz.rows, x.cols, dz.cols);
+  Params p = params(dz.cols, x.cols, dz.rows, plan, acc, err);
   p.early = (before.narrow ? shape_of<kDx, true>(before) : shape_of<kDx>(before)).units * before.teams < kPairs;
   p.out = static_cast<uint16_t*>(const_cast<void*>(dw.p));
   p.ld_out = dw.ld;
   *left = p;
-  return launch_plan<kDw>(m, p, true, s);
+  return launch_plan<kDw>(m, p, plan, true, s);
 }
 
 int grads_product(const Grad* g, int n, Params& p, bool after, int32_t* err, cudaStream_t s) {
@@ -305,6 +321,43 @@ extern "C" size_t tpk_linear_workspace_bytes(int64_t N, int32_t C, int32_t O, in
   using namespace tpk::product;
   if (!sizes_ok(N, C, O) || !tiles_ok(N, C, O) || N == 0) return 0;
   return carve(nullptr, N, C, O, act, backward != 0, nullptr);
+}
+
+extern "C" int tpk_linear_plan(int64_t N, int32_t C, int32_t O, int32_t act, int32_t backward, tpk_product_plan* out) {
+  using namespace tpk::product;
+  if (!out || !sizes_ok(N, C, O) || !act_ok(act)) return TPK_E_ARG;
+  if (C > kMostK) return TPK_E_UNSUPPORTED;
+  if (!tiles_ok(N, C, O)) return TPK_E_OVERFLOW;
+  if (N == 0) return 0;
+  int n = 0;
+  auto put = [&](int32_t product, const Plan& p, int64_t M, int64_t width, int64_t K, bool may_stop) {
+    const int64_t longest = longest_of(p, K);
+    out[n++] = tpk_product_plan{product, p.narrow ? TPK_FORM_NARROW : TPK_FORM_WIDE, p.teams,
+                                static_cast<int32_t>(p.narrow ? p.split.whole : tiles_of(M, width)),
+                                static_cast<int32_t>(p.split.tail), p.split.splits,
+                                static_cast<int32_t>(may_stop ? (longest + kChunk - 1) / kChunk : 1)};
+  };
+  if (!backward) {
+    if (N <= kFewRows)
+      out[n++] = tpk_product_plan{TPK_PRODUCT_Y, TPK_FORM_FEW, 1, 0, 0, 1, 1};
+    else
+      put(TPK_PRODUCT_Y, forward_plan(N, C, O), N, O, C, false);
+    return n;
+  }
+  if (act != TPK_ACT_NONE) put(TPK_PRODUCT_DZ, dz_plan(N, C, O), N, O, C, false);
+  const Mat dz{nullptr, N, O, O}, w{nullptr, O, C, C}, x{nullptr, N, C, C};
+  const Grad grads[2] = {{dz, false, w, x}, {dz, true, x, w}};
+  Params both{};
+  if (grads_plan(grads, 2, &both)) {
+    for (int32_t product : {TPK_PRODUCT_DX, TPK_PRODUCT_DW}) {
+      const Sub& s = both.sub[(both.sub[0].amn != 0) == (product == TPK_PRODUCT_DW) ? 0 : 1];
+      out[n++] = tpk_product_plan{product, TPK_FORM_TOGETHER, 1, s.mt * s.nt, 0, 1, 1};
+    }
+    return n;
+  }
+  put(TPK_PRODUCT_DX, input_plan(N, C, O), N, C, O, true);
+  put(TPK_PRODUCT_DW, weight_plan(N, C, O), O, C, N, true);
+  return n;
 }
 
 extern "C" int tpk_linear(const void* x, int64_t ld_x, const void* w, const float* bias, int32_t act,
@@ -358,11 +411,8 @@ extern "C" int tpk_linear_bwd(const void* x, int64_t ld_x, const void* w, const 
   if (act != TPK_ACT_NONE) {
     Maps m;
     st = map_of(&m.a, mx, kHalf);
-    Params p = params(N, O, C, nullptr, dev_err);
-    if (!p.narrow) {   // its epilogue has no joined form
-      p.whole = static_cast<int32_t>(tiles_of(N, O));
-      p.splits = 1;
-    }
+    const Plan plan = dz_plan(N, C, O);
+    Params p = params(N, O, C, plan, nullptr, dev_err);
     if (st == TPK_OK) st = map_of(&m.b, mw, p.narrow ? kHalf / 2 : kHalf);
     if (st == TPK_OK) st = map_of(&m.in, dz, kHalf);
     p.in = static_cast<const uint16_t*>(dy);
@@ -374,7 +424,7 @@ extern "C" int tpk_linear_bwd(const void* x, int64_t ld_x, const void* w, const 
     p.bias = bias;
     p.act = act;
     p.colsum = db ? k.sums : nullptr;
-    if (st == TPK_OK) st = launch_plan<kDz>(m, p, false, s);
+    if (st == TPK_OK) st = launch_plan<kDz>(m, p, plan, false, s);
   }
   const Mat mdx{dx, N, C, ld_dx}, mdw{dw, O, C, C};
   Params px{}, pw{}, both{};

@@ -1020,10 +1020,10 @@ inline int64_t own_stride(int64_t cols) { return (cols + 63) / 64 * 64; }
 
 inline int64_t tiles_of(int64_t M, int64_t N) { return (M + kTile - 1) / kTile * ((N + kTile - 1) / kTile); }
 // Workspace of a product that may be split over K.
-inline size_t acc_bytes(int64_t M, int64_t N, int64_t K) {
-  const Split s = plan_of(M, N, K).split;
-  return static_cast<size_t>(s.tail) * s.splits * kTile * kTile * 4;
+inline size_t acc_bytes(const Plan& p) {
+  return static_cast<size_t>(p.split.tail) * p.split.splits * kTile * kTile * 4;
 }
+inline size_t acc_bytes(int64_t M, int64_t N, int64_t K) { return acc_bytes(plan_of(M, N, K)); }
 // Rows of the exponents that kGate keeps, and their bytes.
 inline int64_t exp_rows(int64_t N) { return (N + 127) / 128 * 128; }
 inline size_t exp_bytes(int64_t N, int64_t I) { return static_cast<size_t>((I + kGroup - 1) / kGroup * 2 * exp_rows(N)); }

@@ -990,6 +990,22 @@ def linear_bwd(x, w, dy, bias=None, act="none", dx=None, dw=None, db=None, works
     return dx, dw, db
 
 
+def linear_plan(n, c, o, act="none", backward=False):
+    """How ``linear`` (or ``linear_bwd``) does the products of n rows, c channels
+    and o results (``tpk_linear_plan``): {"y" / "dz", "dx", "dw": {"form": few,
+    wide, narrow or together, "teams", "tiles", "split_tiles", "splits",
+    "pieces"}}.  For profiles and tests; needs no GPU."""
+    out = (B.ProductPlan * 3)()
+    got = B.load().tpk_linear_plan(n, c, o, _activation(act), 1 if backward else 0, out)
+    if got < 0:
+        B.check(got, "tpk_linear_plan")
+    plans = {}
+    for p in out[:got]:
+        d = {k: getattr(p, k) for k, _ in p._fields_[2:]}
+        plans[B.PRODUCTS[p.product]] = dict(form=B.FORMS[p.form], **d)
+    return plans
+
+
 def _ffn_args(x, w_in, w_out):
     """(N, C, I, O, address and stride of x, addresses of the weights), checked."""
     N, C, p_x, ld_x = _rows_of(x, "x")
