@@ -161,12 +161,8 @@ int join(const Params& p, const float* bias, int act, const Mat& residual, const
 Plan forward_plan(int64_t N, int64_t C, int64_t O) { return plan_of(N, O, C); }
 Plan input_plan(int64_t N, int64_t C, int64_t O) { return plan_of(N, C, O); }
 Plan weight_plan(int64_t N, int64_t C, int64_t O) { return plan_of(O, C, N); }
-// dz's epilogue has no joined form: a wide plan stays whole
-Plan dz_plan(int64_t N, int64_t C, int64_t O) {
-  Plan p = plan_of(N, O, C);
-  if (!p.narrow) p.split = Split{tiles_of(N, O), 0, 1};
-  return p;
-}
+// (dz's epilogue has no joined form)
+Plan dz_plan(int64_t N, int64_t C, int64_t O) { return plan_of(N, O, C, false); }
 
 Params params(int64_t M, int64_t N, int64_t K, const Plan& plan, float* acc, int32_t* err) {
   Params p{};

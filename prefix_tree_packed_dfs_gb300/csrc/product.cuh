@@ -169,13 +169,13 @@ struct Split {
   int splits;
 };
 // us: of the last round.
-inline Split split_of(int64_t tiles, int64_t k_iters, double* us_out = nullptr) {
+inline Split split_of(int64_t tiles, int64_t k_iters, double* us_out = nullptr, bool may_split = true) {
   Split s{tiles, 0, 1};
   const int64_t tail = tiles % kPairs;
   const double tile_us = 0.27 * static_cast<double>(k_iters);   // 64 elements of K: 512 cycles
   double best = tile_us;
   if (us_out) *us_out = tail == 0 ? 0.0 : best;
-  if (tail == 0) return s;
+  if (tail == 0 || !may_split) return s;
   for (int64_t n = 2; n <= k_iters / 4 && n <= (tail * 8 < kPairs ? kPairs / tail : 8); ++n) {
     const int64_t rounds = (tail * n + kPairs - 1) / kPairs;
     const double us = tile_us * static_cast<double>(rounds) / static_cast<double>(n) + 6.0 +
@@ -202,11 +202,11 @@ struct Plan {
   Split split;
   double us;     // estimate, without the kernel's start and end
 };
-inline Plan plan_of(int64_t M, int64_t N, int64_t K) {
+inline Plan plan_of(int64_t M, int64_t N, int64_t K, bool may_split = true) {
   const int64_t mt = (M + kTile - 1) / kTile, wide = mt * ((N + kTile - 1) / kTile);
   const int64_t narrow = mt * ((N + kHalf - 1) / kHalf), k_iters = (K + 63) / 64;
   double us;
-  Plan p{false, 1, split_of(wide, k_iters, &us), 0.0};
+  Plan p{false, 1, split_of(wide, k_iters, &us, may_split), 0.0};
   p.us = us + 2.2 + 0.27 * static_cast<double>((p.split.tail ? p.split.whole : wide - wide % kPairs) / kPairs * k_iters);
   const int64_t rounds = (narrow + kPairs - 1) / kPairs;
   const double stage_us = narrow <= kPairs / 2 ? 0.14 : 0.2;

@@ -33,6 +33,7 @@ BACKWARD = {
     (2048, 4096, 12288): (("wide", 0, 0, 1), ("wide", 0, 0, 2), ("wide", 0, 0, 1)),
     (16384, 2048, 2560): (("wide", 0, 0, 1), ("wide", 0, 0, 1), ("wide", 76, 4, 2)),
     (2500, 2056, 20000): (("wide", 0, 0, 1), ("wide", 76, 14, 3), ("wide", 0, 0, 1)),
+    (1208, 8192, 1024): (("narrow", 0, 0, 1), ("together", 0, 0, 1), ("together", 0, 0, 1)),
     (300, 520, 1032): (("narrow", 0, 0, 1), ("together", 0, 0, 1), ("together", 0, 0, 1)),
 }
 
@@ -97,6 +98,18 @@ def test_split_forward_refuses_without_its_workspace(lib):
             return lib.tpk_linear(P(256), c, P(512), None, 0, None, 0, P(1024), o, n, c, o, ws, ws_bytes, None, None)
         assert call(None, 0) == -7 and call(None, need) == -7
         assert call(P(4096), need - 1) == -7 and call(P(4100), need) == -7
+
+
+def test_dz_is_planned_without_the_split_that_it_does_not_have(lib):
+    """Where the forward's best is wide tiles split over K, dz takes the best of what it can do: here narrow
+    tiles, not wide ones on half as many pairs or in one more round."""
+    from prefix_tree_packed_dfs_gb300 import ops
+    for n, c, o in ((1208, 8192, 1024), (4922, 8016, 200), (2564, 5680, 1624), (78, 8152, 5248)):
+        assert ops.linear_plan(n, c, o)["y"]["splits"] > 1
+        dz = ops.linear_plan(n, c, o, act="silu", backward=True)["dz"]
+        assert dz["form"] == "narrow" and dz["splits"] == 1, dz
+    # where wide tiles are best without a split they stay
+    assert ops.linear_plan(819, 3272, 5344, act="silu", backward=True)["dz"]["form"] == "wide"
 
 
 @pytest.fixture(scope="module")
