@@ -5,12 +5,15 @@
 //   gelu_tanh  z s(k (z + c z^3)), k = 2 sqrt(2 / pi), c = 0.044715
 //              (0.5 (1 + tanh t) = s(2 t): no difference of close numbers)
 // Phi through erfc(x) ~ (a1 t + .. + a5 t^5) e^{-x^2}, t = 1 / (1 + p x), for
-// x >= 0 (Abramowitz and Stegun, Handbook of Mathematical Functions, 7.1.26):
-// within 1.5e-7, far inside the results' bf16 rounding, at a third of the
-// instructions of the full-precision function, and the derivative shares the
-// exponential.  An epilogue does 32,768 of these per tile and CTA while the
-// tensor pipe needs 256 cycles per 64 elements of K, so instructions count: two
-// values per instruction wherever there is a packed form.
+// x >= 0 (Abramowitz and Stegun, Handbook of Mathematical Functions, 7.1.26), at a
+// third of the instructions of the full-precision function, and the derivative
+// shares the exponential.  Its error is absolute, 1.5e-7.  Below 0 Phi is half of
+// that value itself, not 1 less the other half, so that gelu's tail keeps the fit's
+// relative error: 5e-4 at z = -4, 1.6e-3 at -5 (a bf16 rounding is 2e-3 to 4e-3),
+// 6.5e-3 at -7, where gelu is -9e-12.  (As 0.5 - w it was 4% off at -5.)
+// An epilogue does 32,768 of these per tile and CTA while the tensor pipe needs
+// 256 cycles per 64 elements of K, so instructions count: two values per
+// instruction wherever there is a packed form.
 #pragma once
 #include "ptx.cuh"
 #include "tpk.h"
@@ -38,19 +41,25 @@ __device__ __forceinline__ uint64_t sigmoid_2(uint64_t z) {
 __device__ __forceinline__ uint64_t tanh_arg_2(uint64_t z, uint64_t zz) {
   return ptx::mul2(z, ptx::fma2(zz, both(0.044715f * kTanhK), both(kTanhK)));
 }
+// h below 0, 1 - h from there on.
+__device__ __forceinline__ float side(float z, float h) {
+  asm("{\n .reg .pred p;\n setp.ge.f32 p, %1, 0f00000000;\n @p sub.f32 %0, 0f3F800000, %0;\n}\n" : "+f"(h) : "f"(z));
+  return h;
+}
 // Phi(z); e^{-z^2 / 2} in e
 __device__ __forceinline__ uint64_t phi_2(uint64_t z, uint64_t& e) {
   constexpr uint64_t kSign = 0x8000000080000000ull;
   const uint64_t x = z & ~kSign;
   const uint64_t t = rcp_2(ptx::fma2(x, both(0.3275911f * 0.70710678118654752f), both(1.f)));
   e = ex2_2(ptx::mul2(ptx::mul2(z, z), both(-0.5f * kActLog2e)));
-  uint64_t p = ptx::fma2(t, both(1.061405429f), both(-1.453152027f));
-  p = ptx::fma2(t, p, both(1.421413741f));
-  p = ptx::fma2(t, p, both(-0.284496736f));
-  p = ptx::fma2(t, p, both(0.254829592f));
-  const uint64_t q = ptx::mul2(ptx::mul2(p, t), e);               // erfc(|z| / sqrt 2)
-  const uint64_t w = ptx::fma2(q, both(-0.5f), both(0.5f));       // |Phi - 1/2|
-  return ptx::add2(w | (z & kSign), both(0.5f));
+  uint64_t p = ptx::fma2(t, both(0.5f * 1.061405429f), both(0.5f * -1.453152027f));
+  p = ptx::fma2(t, p, both(0.5f * 1.421413741f));
+  p = ptx::fma2(t, p, both(0.5f * -0.284496736f));
+  p = ptx::fma2(t, p, both(0.5f * 0.254829592f));
+  float zl, zh, lo, hi;
+  ptx::unf2(z, zl, zh);
+  ptx::unf2(ptx::mul2(ptx::mul2(p, t), e), lo, hi);               // erfc(|z| / sqrt 2) / 2
+  return ptx::f2(side(zl, lo), side(zh, hi));
 }
 // A square that a factor of zero may meet: finite.
 __device__ __forceinline__ uint64_t square_2(uint64_t z) {
