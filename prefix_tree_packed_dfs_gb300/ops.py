@@ -738,6 +738,16 @@ def embed_bwd(tokens, dout, vocab, scale=1.0, dtype=torch.float32, dtable=None, 
     return dtable
 
 
+def _row_stride(ld, rows, width, name):
+    """The stride of rows of ``width`` elements that may lie apart (column slices),
+    given as ld elements: 16-byte aligned, without overlap; of no account for one row."""
+    if rows <= 1:
+        return width
+    if ld < width or ld % 8:
+        raise ValueError("%s: rows must not overlap and must lie a multiple of 8 elements apart" % name)
+    return ld
+
+
 def _rows2(t, name, shape):
     """(address, row stride in elements) of a 2-d bf16 tensor whose rows may
     lie apart (column slices), 16-byte aligned."""
@@ -748,11 +758,7 @@ def _rows2(t, name, shape):
     ld, unit = t.stride()
     if unit != 1:
         raise ValueError("%s: channels must be contiguous inside a row" % name)
-    if shape[0] <= 1:
-        ld = shape[1]
-    elif ld < shape[1] or ld % 8:
-        raise ValueError("%s: rows must not overlap and must lie a multiple of 8 elements apart" % name)
-    return t.data_ptr(), ld
+    return t.data_ptr(), _row_stride(ld, shape[0], shape[1], name)
 
 
 def _norm_args(res, w_pre, y, w_post, gate):
@@ -915,11 +921,7 @@ def _rows_of(t, name):
     ld, unit = t.stride()
     if unit != 1:
         raise ValueError("%s: channels must be contiguous inside a row" % name)
-    if n <= 1:
-        ld = c
-    elif ld < c or ld % 8:
-        raise ValueError("%s: rows must not overlap and must lie a multiple of 8 elements apart" % name)
-    return n, c, t.data_ptr(), ld
+    return n, c, t.data_ptr(), _row_stride(ld, n, c, name)
 
 
 def _weights(t, cols, name):
@@ -1095,11 +1097,7 @@ def _heads(t, name):
     ld, head, unit = t.stride()
     if unit != 1 or head != d:
         raise ValueError("%s: heads and elements must be contiguous inside a row" % name)
-    if n <= 1:
-        ld = h * d
-    elif ld < h * d or ld % 8:
-        raise ValueError("%s: rows must not overlap and must lie a multiple of 8 elements apart" % name)
-    return n, h, d, t.data_ptr(), ld
+    return n, h, d, t.data_ptr(), _row_stride(ld, n, h * d, name)
 
 
 def _rotated(t, out, name, F, d):
