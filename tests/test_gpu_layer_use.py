@@ -37,11 +37,11 @@ def _near(got, ref, tol, what):
 
 
 @pytest.mark.parametrize("n,c,o", [
-    (70, 64, 9000), (300, 64, 20000),            # dx: a sum of two and three chunks
+    (70, 64, 9000), (300, 64, 20000),            # dx: a long sum shared by four pairs
     (8200, 64, 72), (20000, 136, 264),           # dw: the same
-    (130, 9000, 256), (300, 20000, 64),          # forward: a sum that never stops, split over K
-    (4096, 256, 5000), (19457, 512, 256),        # tiles left over from whole rounds, split
-    (100000, 64, 64), (30000, 200, 72),          # a tile's long column split many ways; many narrow tiles
+    (130, 9000, 256), (300, 20000, 64),          # forward: a sum that never stops, shared by four pairs
+    (4096, 256, 5000), (19457, 512, 256),        # wide tiles in rounds; narrow ones, dw by four pairs
+    (100000, 64, 64), (30000, 200, 72),          # dw: a tile's long column split many ways
 ])
 def test_linear_long_sums(ops, n, c, o):
     x, w, dy = _rnd(1, n, c), _rnd(2, o, c, std=c ** -0.5), _rnd(3, n, o)
