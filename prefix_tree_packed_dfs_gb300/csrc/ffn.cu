@@ -106,6 +106,7 @@ extern "C" int tpk_gated_ffn(const void* x, int64_t ld_x, const void* w_in, cons
   if (!x || !w_in || !w_out || !y || y == x || !aligned16(x) || !aligned16(w_in) || !aligned16(w_out) || !aligned16(y) ||
       !aligned16(residual) || !aligned16(saved) || !aligned16(a))
     return TPK_E_ARG;
+  if (residual == y && ld_res != ld_y && N > 1) return TPK_E_ARG;
   FfnWork k;
   const size_t need = carve(static_cast<uint8_t*>(workspace), N, C, I, O, false, a != nullptr, &k);
   if (need && (!workspace || reinterpret_cast<uintptr_t>(workspace) % 256 || ws_bytes < need)) return TPK_E_WORKSPACE;

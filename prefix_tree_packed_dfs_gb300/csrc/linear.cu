@@ -368,6 +368,7 @@ extern "C" int tpk_linear(const void* x, int64_t ld_x, const void* w, const floa
   if (N == 0) return TPK_OK;
   if (!x || !w || !y || y == x || y == w || !aligned16(x) || !aligned16(w) || !aligned16(y) || !aligned16(residual) || !aligned16(bias))
     return TPK_E_ARG;
+  if (residual == y && ld_res != ld_y && N > 1) return TPK_E_ARG;
   LinearWork k;
   const size_t need = carve(static_cast<uint8_t*>(workspace), N, C, O, act, false, &k);
   if (need && (!workspace || reinterpret_cast<uintptr_t>(workspace) % 256 || ws_bytes < need)) return TPK_E_WORKSPACE;

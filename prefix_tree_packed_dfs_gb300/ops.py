@@ -738,6 +738,12 @@ def embed_bwd(tokens, dout, vocab, scale=1.0, dtype=torch.float32, dtable=None, 
     return dtable
 
 
+def _onto(p_res, ld_res, p_out, ld_out):
+    """``out`` may be the residual, row for row."""
+    if p_res == p_out and p_res is not None and ld_res != ld_out:
+        raise ValueError("out starts where residual does, with other rows")
+
+
 def _row_stride(ld, rows, width, name):
     """The stride of rows of ``width`` elements that may lie apart (column slices),
     given as ld elements: 16-byte aligned, without overlap; of no account for one row."""
@@ -958,6 +964,7 @@ def linear(x, w, bias=None, act="none", residual=None, out=None, workspace=None,
     p_r, ld_r = (None, O) if residual is None else _rows2(residual, "residual", (N, O))
     given = out, workspace, dev_err
     out, p_y, ld_y = _out_rows(out, (N, O), "out", x)
+    _onto(p_r, ld_r, p_y, ld_y)
     p_err = _dev_err(dev_err)
     # (a few rows, one or so, are a matter of microseconds: no question about a workspace they do not need)
     need = 0 if N <= B.FEW_ROWS else lib.tpk_linear_workspace_bytes(N, C, O, a, 0)
@@ -1036,6 +1043,7 @@ def gated_ffn(x, w_in, w_out, act="silu", residual=None, save=False, out=None, p
     p_r, ld_r = (None, O) if residual is None else _rows2(residual, "residual", (N, O))
     given = out, pre, a, workspace, dev_err
     out, p_y, ld_y = _out_rows(out, (N, O), "out", x)
+    _onto(p_r, ld_r, p_y, ld_y)
     p_pre = p_a = None
     if save:
         pre, p_pre = _out(pre, torch.uint8, (lib.tpk_gated_ffn_saved_bytes(N, I),), "pre", x)

@@ -37,3 +37,27 @@ def test_the_stride_of_one_row_is_of_no_account(lib, ld):
     with pytest.raises(ValueError, match="no CPU path"):
         ops.rope_by_depth_ex(one.as_strided((1, 1, 64), (ld, 64, 1)), None, torch.zeros(1, dtype=torch.int32),
                              ops.rope_freqs(64))
+
+
+def test_a_result_that_starts_where_the_residual_does_has_its_rows(lib):
+    """In place on the residual means row for row: with another stride a row would be written before it was read."""
+    import ctypes
+    P = ctypes.c_void_p
+    buf, w = torch.zeros(3 * 128, dtype=BF), torch.zeros(64, 64, dtype=BF)
+    wi = torch.zeros(128, 64, dtype=BF)
+    dense, apart = buf[:192].view(3, 64), buf.view(3, 128)[:, :64]
+    x = torch.zeros(3, 64, dtype=BF)
+    for r, o in ((dense, apart), (apart, dense)):
+        with pytest.raises(ValueError, match="out starts where residual does"):
+            ops.linear(x, w, residual=r, out=o)
+        with pytest.raises(ValueError, match="out starts where residual does"):
+            ops.gated_ffn(x, wi, w, residual=r, out=o)
+    with pytest.raises(ValueError, match="no CPU path"):
+        ops.linear(x, w, residual=apart, out=apart)
+    with pytest.raises(ValueError, match="no CPU path"):      # one row has no stride
+        ops.linear(x[:1], w, residual=apart[:1], out=dense[:1])
+    for n in (3, 70):
+        assert lib.tpk_linear(P(256), 64, P(512), None, 0, P(1024), 128, P(1024), 64, n, 64, 64, P(4096), 1 << 30, None,
+                              None) == -1
+        assert lib.tpk_gated_ffn(P(256), 64, P(512), P(768), 1, P(1024), 128, None, None, P(1024), 64, n, 64, 64, 64,
+                                 P(4096), 1 << 30, None, None) == -1
