@@ -40,11 +40,12 @@ __device__ __forceinline__ Pair add(Pair a, Pair b) {
   const Pair s = two_sum(a.hi, b.hi);
   return two_sum(s.hi, s.lo + (a.lo + b.lo));
 }
-// Adds x to s, as exactly as two fp32 numbers can hold it.
+// Adds x to s, as exactly as two fp32 numbers can hold it; the second stays below half
+// a step of the first, or it would round itself after a million terms alike.
 __device__ __forceinline__ void into(Pair& s, float x) {
   const Pair t = two_sum(s.hi, x);
-  s.hi = t.hi;
-  s.lo += t.lo;
+  const float l = s.lo + t.lo, h = t.hi + l, e = l - (h - t.hi);
+  s = Pair{h, e == e ? e : 0.f};
 }
 // a - b, of which the sign is right next to 0 too; NaN, which is on neither side,
 // for equal infinities

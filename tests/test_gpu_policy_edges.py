@@ -215,3 +215,20 @@ def test_statistics_of_many_tokens(ops, level, lengths):
     rel = torch.tensor([2.0 ** -19] * 2 + [13 * 2.0 ** -24, 2.0 ** -19, 13 * 2.0 ** -24], dtype=torch.float64, device="cuda")
     off_by = (stats.double() - terms.sum(1)).abs() / mag.clamp(min=1e-30)
     assert (off_by <= rel).all(), off_by
+
+
+@pytest.mark.parametrize("cut", [None, 1.0, 0.75])
+def test_statistics_of_hundreds_of_millions_of_tokens(ops, cut):
+    """Millions of terms per thread, all alike, so that their roundings do not cancel: 13 x 2^-24 as above (the ratio is
+    exactly 1, and nothing else is rounded).  Token by token, as one sequence, and as two."""
+    R = 600000000
+    index = torch.arange(R + 1, dtype=torch.int32, device="cuda")
+    full = lambda v: torch.full((R,), v, device="cuda")
+    offsets = None if cut is None else torch.tensor([0, int(R * cut), R], dtype=torch.int32, device="cuda")
+    w = np.float32(1e-3)
+    stats, dloss = ops.policy_loss(full(0.5), full(-0.5), full(1.0), full(float(w)), index[:R], index, index[:R],
+                                   seq_offsets=offsets)
+    want = float(w) * R * np.array([-1.0, 0.0, 0.0, 1.0, 1.0])
+    off = np.abs(stats.double().cpu().numpy() - want)
+    assert (off <= 13 * 2.0 ** -24 * np.abs(want)).all(), off / want[-1]
+    assert torch.equal(dloss[::1000003], full(float(w))[::1000003])
